@@ -405,6 +405,108 @@ int indexer_page_indices(indexer_plan_t plan, const int32_t* raw_idx, const int3
 int indexer_chunk_rows(int64_t prefix_len, double budget_token2, int32_t chunk_min,
                        int32_t chunk_max, int32_t page, int32_t pow2);
 
+/* ---------------------------------------------------------- rotary positions
+ * The operators below are what a layer needs around the indexer: its bf16
+ * projections turned into the indexer's operands, a quantised cache of them, and
+ * attention over the keys the indexer selected.
+ *
+ * A rotation turns pairs of a head vector's elements: pair i of row t becomes
+ *     a' = m (a cos u - b sin u),   b' = m (a sin u + b cos u),   u = position[t] * f_i
+ * in fp32 with one rounding; the other elements are copied.
+ *   D            elements of a head vector, 2..256
+ *   rot_dim      rotated elements, even, 2..D; rot_offset the first of them
+ *   layout       IDX_ROPE_HALF: pairs (i, i + rot_dim/2) of the rotated part;
+ *                IDX_ROPE_INTERLEAVED: pairs (2i, 2i+1)
+ *   base         f_i = base^(-2i/rot_dim)
+ *   factor       context scaling, >= 1 (1: none).  With original_len <= 0 every f_i is
+ *                divided by it.  With original_len > 0 pairs that make at most beta_slow
+ *                turns over original_len positions are divided by it, those that make at
+ *                least beta_fast are kept, and those between are mixed linearly in i
+ *                (bounds rounded outwards to whole pairs)
+ *   amplitude    m (1: none), applied to the rotated elements only
+ * The angle is reduced exactly for every int32 position (a 64-bit phase per position), so
+ * its error is below 3e-7 rad at any context length.
+ */
+#define IDX_BF16 0
+#define IDX_FP16 1
+#define IDX_FP32 2
+#define IDX_CODES 3                /* indexer_cache_read: codes and scales as stored */
+#define IDX_ROPE_HALF 0
+#define IDX_ROPE_INTERLEAVED 1
+#define IDX_MAX_HEADS 1024         /* heads of one call of the operators below */
+
+typedef struct indexer_rope_spec {
+    int32_t D;
+    int32_t rot_dim;
+    int32_t rot_offset;
+    int32_t layout;
+    double base;
+    double factor;
+    double original_len;
+    double beta_fast;
+    double beta_slow;
+    double amplitude;
+} indexer_rope_spec;
+
+typedef struct indexer_rope_s* indexer_rope_t;
+
+/* Validate a rotation and keep its frequencies (host only, needs no GPU; built once per
+ * model and used by every call). */
+int indexer_rope_create(const indexer_rope_spec* spec, indexer_rope_t* out_rope);
+void indexer_rope_destroy(indexer_rope_t rope);
+
+/* Rotate x [rows, heads, D] of dtype IDX_BF16, IDX_FP16 or IDX_FP32 into out (same type).
+ * Strides are in elements (last axis contiguous, none negative; output rows and heads at
+ * least D apart).  out may be x itself with the same strides, else the two must not
+ * overlap.  positions: device int32 [rows], any value.  inverse = 1 turns back (the
+ * rotation's transpose: also its gradient).  16-byte aligned rows, rot_dim a multiple of 16 and
+ * rot_offset of 8 take the vector kernel. */
+int indexer_rope(indexer_rope_t rope, const void* x, int32_t dtype, int32_t rows, int32_t heads,
+                 int64_t row_stride, int64_t head_stride, const int32_t* positions,
+                 int32_t inverse, void* out, int64_t out_row_stride, int64_t out_head_stride,
+                 void* stream);
+
+/* ------------------------------------------------- quantised operands and caches
+ * A cache holds num_slots x heads vectors of D elements (D a multiple of 32, 32..256) in
+ * one of the key formats:
+ *   IDX_K_FP8_E4M3         codes e4m3 [num_slots, heads, D], scales float [num_slots, heads]:
+ *                          scale = largest magnitude / 448 (at least 2^-126; 1 for a zero
+ *                          vector), code = e4m3(x / scale), ties to even, saturating
+ *   IDX_K_FP4_E2M1_UE8M0   codes [num_slots, heads, D/2] (element 2i in the low nibble),
+ *                          scales ue8m0 [num_slots, heads, D/32]: 2^e with e =
+ *                          floor(log2(largest magnitude)) - 2 of the 32 elements (1 for a
+ *                          zero block), code = e2m1(x / 2^e), ties to even, saturating
+ * With heads = 1 these are the indexer's keys, with slots = NULL its queries (T rows of H
+ * heads: codes [T, H, D], s_q [T, H]).
+ *
+ * indexer_cache_write: x [rows, heads, D] (dtype and strides as above) is rotated (rope not
+ *   NULL: positions int32 [rows], rope's D = D; the rotated values stay in fp32) and
+ *   quantised into slot slots[i] (int32 [rows]; NULL: slot i).  Rows whose slot is negative
+ *   or not below num_slots are skipped.  No two rows of a call may name the same slot.  NaN
+ *   is stored as 0 and an infinity as the largest code of the largest scale, so codes and
+ *   scales are always finite, as the indexer needs them.
+ * indexer_cache_read: rows slots[i] (NULL: row i) of the cache into out [rows, heads, D] of
+ *   out_dtype IDX_BF16, IDX_FP16 or IDX_FP32 as code * scale in fp32, rounded to the type; or with
+ *   out_dtype IDX_CODES as codes (out) and scales (out_scales) packed in the cache's own
+ *   format, which is how a paged cache becomes the packed keys of the indexer's calls.  A
+ *   slot outside the cache reads as zeros (scale 1).
+ * codes and out are 16-byte aligned, scales 4-byte aligned.
+ */
+int indexer_cache_write(indexer_rope_t rope, const void* x, int32_t dtype, int32_t rows,
+                        int32_t heads, int32_t D, int64_t row_stride, int64_t head_stride,
+                        const int32_t* positions, const int32_t* slots, int32_t num_slots,
+                        int32_t format, void* codes, void* scales, void* stream);
+int indexer_cache_read(const void* codes, const void* scales, int32_t format, int32_t num_slots,
+                       int32_t heads, int32_t D, const int32_t* slots, int32_t rows,
+                       int32_t out_dtype, void* out, void* out_scales, void* stream);
+
+/* Cache slots of the batch's packed keys: slots [total_keys] = page_table[r, j / page_size] *
+ * page_size + j % page_size for key j of request r, -1 where the entry is negative or the slot
+ * does not fit an int32.  page_table as in indexer_page_indices.  Built once per batch, for
+ * indexer_cache_read of whole prefixes. */
+int indexer_page_slots(indexer_plan_t plan, const int32_t* page_table, int64_t ld_page_table,
+                       int32_t page_size, int32_t* slots, void* stream);
+
 const char* indexer_error_string(int status);
 int indexer_version(void);
 

@@ -11,5 +11,8 @@ from ._lib import (  # noqa: F401
     indexer_launch_count, indexer_profile_main_kernel, indexer_set_wait_budget, indexer_status, indexer_topk, indexer_version,
     indexer_chunk_rows, indexer_page_indices, indexer_candidate_blocks_tail,
     indexer_fused_topk_mapped, indexer_convert_fp4, indexer_fallback_rows,
+    IDX_BF16, IDX_CODES, IDX_FP16, IDX_FP32, IDX_ROPE_HALF, IDX_ROPE_INTERLEAVED, Rope,
+    indexer_cache_read, indexer_cache_write, indexer_page_slots, indexer_rope,
+    indexer_rope_create,
     lib,
 )

@@ -32,6 +32,12 @@ IDX_Q_FP8_E4M3 = 0
 IDX_Q_FP4_E2M1_UE8M0 = 1
 IDX_SELECT_AUTO = 0
 IDX_SELECT_STREAM = 1
+IDX_BF16 = 0
+IDX_FP16 = 1
+IDX_FP32 = 2
+IDX_CODES = 3
+IDX_ROPE_HALF = 0
+IDX_ROPE_INTERLEAVED = 1
 
 EXPORTED = ("indexer_plan", "indexer_plan_destroy", "indexer_plan_info", "indexer_logits",
             "indexer_topk", "indexer_fused_topk", "indexer_candidate_blocks",
@@ -40,7 +46,8 @@ EXPORTED = ("indexer_plan", "indexer_plan_destroy", "indexer_plan_info", "indexe
             "indexer_version", "indexer_fused_topk_noalloc", "indexer_profile_main_kernel",
             "indexer_chunk_rows", "indexer_page_indices", "indexer_candidate_blocks_tail",
             "indexer_fused_topk_mapped", "indexer_convert_fp4", "indexer_fallback_rows",
-            "indexer_noalloc_status")
+            "indexer_noalloc_status", "indexer_rope_create", "indexer_rope_destroy",
+            "indexer_rope", "indexer_cache_write", "indexer_cache_read", "indexer_page_slots")
 IDX_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -62,6 +69,15 @@ class _Problem(ctypes.Structure):
         ("cand_topk", ctypes.c_int32), ("key_block", ctypes.c_int32),
         ("transient_budget_bytes", ctypes.c_uint64),
         ("select_mode", ctypes.c_int32), ("qdtype", ctypes.c_int32),
+    ]
+
+
+class _RopeSpec(ctypes.Structure):
+    _fields_ = [
+        ("D", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("rot_offset", ctypes.c_int32),
+        ("layout", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+        ("original_len", ctypes.c_double), ("beta_fast", ctypes.c_double),
+        ("beta_slow", ctypes.c_double), ("amplitude", ctypes.c_double),
     ]
 
 
@@ -104,10 +120,19 @@ def lib():
         L.indexer_candidate_blocks_tail.argtypes = [P, P, P, P, P, P, P, P, P, i64, P, sz, P]
         L.indexer_fused_topk_mapped.argtypes = [P, P, P, P, P, P, P, P, i64, P, i64, P, P, P,
                                                 sz, P]
+        L.indexer_rope_create.argtypes = [ctypes.POINTER(_RopeSpec), ctypes.POINTER(P)]
+        L.indexer_rope_destroy.argtypes = [P]
+        L.indexer_rope_destroy.restype = None
+        L.indexer_rope.argtypes = [P, P, i32, i32, i32, i64, i64, P, i32, P, i64, i64, P]
+        L.indexer_cache_write.argtypes = [P, P, i32, i32, i32, i32, i64, i64, P, P, i32, i32, P,
+                                          P, P]
+        L.indexer_cache_read.argtypes = [P, P, i32, i32, i32, i32, P, i32, i32, P, P, P]
+        L.indexer_page_slots.argtypes = [P, P, i64, i32, P, P]
         L.indexer_error_string.argtypes = [i32]
         L.indexer_error_string.restype = ctypes.c_char_p
         for name in EXPORTED:
-            if name not in ("indexer_plan_destroy", "indexer_error_string"):
+            if name not in ("indexer_plan_destroy", "indexer_error_string",
+                            "indexer_rope_destroy"):
                 getattr(L, name).restype = ctypes.c_int
         L.indexer_launch_count.restype = ctypes.c_longlong
         L.indexer_fallback_rows.argtypes = [P, P, P]
@@ -329,3 +354,127 @@ def indexer_chunk_rows(prefix_len: int, budget_token2: float = 2.0e8, chunk_min:
     if r < 0:
         raise IndexerError("indexer_chunk_rows", r)
     return r
+
+
+# ------------------------------------------------------- operators around the indexer
+
+_DTYPES = {torch.bfloat16: IDX_BF16, torch.float16: IDX_FP16, torch.float32: IDX_FP32}
+
+
+def _dense(name: str, t, dims: int) -> int:
+    """The library's type code of a strided CUDA tensor whose last axis is contiguous."""
+    code = _DTYPES.get(t.dtype)
+    if code is None or not t.is_cuda or t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name}: {dims}-d bf16, fp16 or fp32 CUDA tensor with a contiguous "
+                         "last axis expected")
+    return code
+
+
+def _i32(name: str, t, shape):
+    """A contiguous int32 CUDA tensor of that shape, or None."""
+    if t is not None and (t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous()
+                          or tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name}: contiguous int32 CUDA tensor of shape {tuple(shape)} expected")
+    return _ptr(t)
+
+
+class Rope:
+    """Owns an ``indexer_rope_t``; destroyed with the object."""
+
+    def __init__(self, handle, spec: _RopeSpec):
+        self.handle = handle
+        self.spec = spec
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h is not None and _lib is not None:
+            _lib.indexer_rope_destroy(h)
+
+
+def indexer_rope_create(D: int, rot_dim: int, rot_offset: int = 0, layout: int = IDX_ROPE_HALF,
+                        base: float = 10000.0, factor: float = 1.0, original_len: float = 0.0,
+                        beta_fast: float = 32.0, beta_slow: float = 1.0,
+                        amplitude: float = 1.0) -> Rope:
+    """A rotation of ``rot_dim`` of a head vector's ``D`` elements (host only; see the header
+    for the scaling of long contexts)."""
+    spec = _RopeSpec(D, rot_dim, rot_offset, layout, base, factor, original_len, beta_fast,
+                     beta_slow, amplitude)
+    handle = ctypes.c_void_p()
+    _check("indexer_rope_create", lib().indexer_rope_create(ctypes.byref(spec),
+                                                            ctypes.byref(handle)))
+    return Rope(handle, spec)
+
+
+def indexer_rope(rope: Rope, x, positions, out=None, inverse: bool = False, stream=None):
+    """Rotate ``x`` [rows, heads, D] at ``positions`` (int32 [rows]) into ``out`` (default: a
+    new tensor; may be ``x``) and return it; ``inverse`` turns back."""
+    if out is None:
+        out = torch.empty_like(x)
+    code = _dense("x", x, 3)
+    if _dense("out", out, 3) != code or out.shape != x.shape or x.shape[2] != rope.spec.D:
+        raise ValueError("out: a tensor of x's shape and type, D elements a head, expected")
+    rows, heads, _ = x.shape
+    _check("indexer_rope", lib().indexer_rope(
+        rope.handle, _ptr(x), code, rows, heads, x.stride(0), x.stride(1),
+        _i32("positions", positions, (rows,)), 1 if inverse else 0, _ptr(out), out.stride(0),
+        out.stride(1), _stream(stream)))
+    return out
+
+
+def _cache_shape(codes, scales, fmt: int):
+    """(slots, heads, D) of a cache's codes and scales."""
+    slots, heads, n = codes.shape
+    D = 2 * n if fmt == IDX_K_FP4_E2M1_UE8M0 else n
+    want = (slots, heads, D // 32) if fmt == IDX_K_FP4_E2M1_UE8M0 else (slots, heads)
+    kind = torch.uint8 if fmt == IDX_K_FP4_E2M1_UE8M0 else torch.float32
+    if (codes.element_size() != 1 or not codes.is_cuda or not codes.is_contiguous()
+            or scales.dtype != kind or not scales.is_cuda or not scales.is_contiguous()
+            or tuple(scales.shape) != want):
+        raise ValueError(f"cache: contiguous CUDA codes of one byte and {kind} scales of shape "
+                         f"{want} expected")
+    return slots, heads, D
+
+
+def indexer_cache_write(x, codes, scales, fmt: int = IDX_K_FP8_E4M3, rope: Optional[Rope] = None,
+                        positions=None, slots=None, stream=None):
+    """Rotate (``rope``) and quantise ``x`` [rows, heads, D] into rows ``slots`` (int32 [rows];
+    default: row i) of a cache: ``codes`` [num_slots, heads, D] (e2m1: D/2) and ``scales``."""
+    n, heads, D = _cache_shape(codes, scales, fmt)
+    code = _dense("x", x, 3)
+    rows = x.shape[0]
+    if tuple(x.shape[1:]) != (heads, D):
+        raise ValueError(f"x: [rows, {heads}, {D}] expected")
+    _check("indexer_cache_write", lib().indexer_cache_write(
+        None if rope is None else rope.handle, _ptr(x), code, rows, heads, D, x.stride(0),
+        x.stride(1), _i32("positions", positions, (rows,)), _i32("slots", slots, (rows,)), n,
+        fmt, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def indexer_cache_read(codes, scales, fmt: int, slots, out, out_scales=None, stream=None):
+    """Rows ``slots`` (int32 [rows]; None: row i) of a cache into ``out``: as bf16, fp16 or fp32
+    values [rows, heads, D], or, with ``out_scales``, as packed codes and scales."""
+    n, heads, D = _cache_shape(codes, scales, fmt)
+    rows = out.shape[0]
+    if out_scales is not None:
+        code = IDX_CODES
+        if _cache_shape(out, out_scales, fmt) != (rows, heads, D):
+            raise ValueError("out: codes of the cache's heads and size expected")
+    else:
+        code = _dense("out", out, 3)
+        if tuple(out.shape[1:]) != (heads, D) or not out.is_contiguous():
+            raise ValueError(f"out: contiguous [rows, {heads}, {D}] expected")
+    _check("indexer_cache_read", lib().indexer_cache_read(
+        _ptr(codes), _ptr(scales), fmt, n, heads, D, _i32("slots", slots, (rows,)), rows, code,
+        _ptr(out), _ptr(out_scales), _stream(stream)))
+    return out
+
+
+def indexer_page_slots(plan: Plan, page_table, page_size: int, slots=None, stream=None):
+    """Cache slots of the batch's packed keys (int32 [total_keys]) from a page table."""
+    if slots is None:
+        slots = torch.empty(plan.problem.total_keys, dtype=torch.int32, device=page_table.device)
+    table = _i32("page_table", page_table, (plan.problem.num_requests, page_table.shape[-1]))
+    _check("indexer_page_slots", lib().indexer_page_slots(
+        plan.handle, table, page_table.stride(0), int(page_size),
+        _i32("slots", slots, (plan.problem.total_keys,)), _stream(stream)))
+    return slots

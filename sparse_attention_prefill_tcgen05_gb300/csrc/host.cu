@@ -708,6 +708,22 @@ int prepare(Ctx& c, const void* q, const float* s_q, const float* w, const void*
 
 }  // namespace
 
+namespace idx {
+
+PlanView plan_view(const indexer_plan_s* p)
+{
+    return PlanView{p->R, p->T, p->Lk, p->max_L, p->row_begin.data(), p->key_begin.data(),
+                    p->L.data()};
+}
+
+void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+
+bool device_supported() { return device_info().ok; }
+
+int device_sms() { return device_info().sms; }
+
+}  // namespace idx
+
 extern "C" {
 
 int indexer_version(void) { return 2; }

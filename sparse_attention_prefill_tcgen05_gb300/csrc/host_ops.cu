@@ -1,0 +1,224 @@
+// Host side of the operators around the indexer: rotary positions, quantised caches and
+// attention over the selected keys.  Argument checks, launches; no device memory is
+// allocated and nothing synchronizes.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "indexer.h"
+#include "internal.h"
+
+using namespace idx;
+
+struct indexer_rope_s {
+    int32_t D = 0;
+    RopeParams p;
+};
+
+namespace {
+
+bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+bool dense_type(int dtype) { return dtype == IDX_BF16 || dtype == IDX_FP16 || dtype == IDX_FP32; }
+
+size_t type_bytes(int dtype) { return dtype == IDX_FP32 ? 4 : 2; }
+
+int finish(cudaError_t e) { return e == cudaSuccess ? IDX_OK : IDX_ERR_CUDA; }
+
+// 2^64 turns per 2 pi radians: a frequency in radians per position as the phase a
+// position adds, modulo one turn.
+uint64_t phase_increment(double radians)
+{
+    double turns = radians / 6.283185307179586476925286766559;
+    turns -= std::floor(turns);
+    return static_cast<uint64_t>(std::ldexp(turns, 53)) << 11;
+}
+
+}  // namespace
+
+extern "C" {
+
+int indexer_rope_create(const indexer_rope_spec* s, indexer_rope_t* out)
+{
+    if (!out)
+        return IDX_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (!s || s->D < 2 || s->D > kMaxHeadDim || s->rot_dim < 2 || s->rot_dim % 2 != 0 ||
+        s->rot_dim > s->D || s->rot_offset < 0 || s->rot_offset > s->D - s->rot_dim ||
+        (s->layout != IDX_ROPE_HALF && s->layout != IDX_ROPE_INTERLEAVED) || !(s->base > 0.0) ||
+        !std::isfinite(s->base) || !(s->factor >= 1.0) || !std::isfinite(s->factor) ||
+        !std::isfinite(s->amplitude))
+        return IDX_ERR_INVALID_ARG;
+    if (s->factor > 1.0 && s->original_len > 0.0 &&
+        (!std::isfinite(s->original_len) || !(s->beta_fast > 0.0) || !(s->beta_slow > 0.0) ||
+         !(s->beta_fast >= s->beta_slow) || !std::isfinite(s->beta_fast) || !(s->base > 1.0)))
+        return IDX_ERR_INVALID_ARG;
+    indexer_rope_s* r = new (std::nothrow) indexer_rope_s();
+    if (!r)
+        return IDX_ERR_INVALID_ARG;
+    std::memset(&r->p, 0, sizeof(r->p));
+    r->D = s->D;
+    r->p.rot = s->rot_dim;
+    r->p.offset = s->rot_offset;
+    r->p.interleaved = s->layout == IDX_ROPE_INTERLEAVED;
+    r->p.amplitude = static_cast<float>(s->amplitude);
+    double lo = 0.0, hi = 0.0;
+    const bool parts = s->factor > 1.0 && s->original_len > 0.0;
+    if (parts) {
+        // the pair that makes n turns over the original length
+        const auto pair_of = [&](double n) {
+            return s->rot_dim * std::log(s->original_len / (n * 6.283185307179586)) /
+                   (2.0 * std::log(s->base));
+        };
+        lo = std::max(std::floor(pair_of(s->beta_fast)), 0.0);
+        hi = std::min(std::ceil(pair_of(s->beta_slow)), s->rot_dim - 1.0);
+    }
+    for (int i = 0; i < s->rot_dim / 2; ++i) {
+        double f = std::pow(s->base, -2.0 * i / s->rot_dim);
+        if (parts) {
+            const double ramp = std::min(std::max((i - lo) / std::max(hi - lo, 0.001), 0.0), 1.0);
+            f = f / s->factor * ramp + f * (1.0 - ramp);
+        } else {
+            f /= s->factor;
+        }
+        r->p.inc[i] = phase_increment(f);
+    }
+    *out = r;
+    return IDX_OK;
+}
+
+void indexer_rope_destroy(indexer_rope_t rope) { delete rope; }
+
+int indexer_rope(indexer_rope_t rope, const void* x, int32_t dtype, int32_t rows, int32_t heads,
+                 int64_t row_stride, int64_t head_stride, const int32_t* positions,
+                 int32_t inverse, void* out, int64_t out_row_stride, int64_t out_head_stride,
+                 void* stream)
+{
+    if (!rope || !dense_type(dtype) || rows < 0 || heads < 1 || heads > IDX_MAX_HEADS ||
+        row_stride < 0 || head_stride < 0 || out_row_stride < 0 || out_head_stride < 0 ||
+        (inverse != 0 && inverse != 1))
+        return IDX_ERR_INVALID_ARG;
+    if (rows > 0 &&
+        (!x || !out || !positions || !is_aligned(x, type_bytes(dtype)) ||
+         !is_aligned(out, type_bytes(dtype)) || !is_aligned(positions, 4) ||
+         (heads > 1 && out_head_stride < rope->D) || (rows > 1 && out_row_stride < rope->D) ||
+         (x == out && ((rows > 1 && row_stride != out_row_stride) ||
+                       (heads > 1 && head_stride != out_head_stride)))))
+        return IDX_ERR_INVALID_ARG;
+    if (!device_supported())
+        return IDX_ERR_UNSUPPORTED;
+    if (rows == 0)
+        return IDX_OK;
+    RopeParams rp = rope->p;
+    rp.inverse = inverse;
+    const RopeCall c{x,    out,  positions,   row_stride, head_stride, out_row_stride,
+                     out_head_stride, rows, heads,       rope->D,    dtype};
+    count_launch();
+    return finish(launch_rope(rp, c, static_cast<cudaStream_t>(stream)));
+}
+
+static bool cache_format(int format, int heads, int D, int num_slots)
+{
+    return (format == IDX_K_FP8_E4M3 || format == IDX_K_FP4_E2M1_UE8M0) && heads >= 1 &&
+           heads <= IDX_MAX_HEADS && D >= 32 && D <= kMaxHeadDim && D % 32 == 0 && num_slots >= 0;
+}
+
+int indexer_cache_write(indexer_rope_t rope, const void* x, int32_t dtype, int32_t rows,
+                        int32_t heads, int32_t D, int64_t row_stride, int64_t head_stride,
+                        const int32_t* positions, const int32_t* slots, int32_t num_slots,
+                        int32_t format, void* codes, void* scales, void* stream)
+{
+    if (!dense_type(dtype) || !cache_format(format, heads, D, num_slots) || rows < 0 ||
+        row_stride < 0 || head_stride < 0 || (rope && rope->D != D))
+        return IDX_ERR_INVALID_ARG;
+    if (rows > 0 && (!x || !codes || !scales || (rope && !positions) ||
+                     !is_aligned(x, type_bytes(dtype)) || !is_aligned(codes, 16) ||
+                     !is_aligned(scales, 4) || !is_aligned(positions, 4) ||
+                     !is_aligned(slots, 4) || (!slots && rows > num_slots)))
+        return IDX_ERR_INVALID_ARG;
+    if (!device_supported())
+        return IDX_ERR_UNSUPPORTED;
+    if (rows == 0)
+        return IDX_OK;
+    RopeParams rp;
+    if (rope)
+        rp = rope->p;
+    else
+        std::memset(&rp, 0, sizeof(rp));
+    const CacheWriteCall c{x,
+                           positions,
+                           slots,
+                           static_cast<uint8_t*>(codes),
+                           scales,
+                           row_stride,
+                           head_stride,
+                           rows,
+                           heads,
+                           D,
+                           dtype,
+                           num_slots,
+                           format == IDX_K_FP4_E2M1_UE8M0};
+    count_launch();
+    return finish(launch_cache_write(rp, c, static_cast<cudaStream_t>(stream)));
+}
+
+int indexer_cache_read(const void* codes, const void* scales, int32_t format, int32_t num_slots,
+                       int32_t heads, int32_t D, const int32_t* slots, int32_t rows,
+                       int32_t out_dtype, void* out, void* out_scales, void* stream)
+{
+    if (!cache_format(format, heads, D, num_slots) || rows < 0 ||
+        !(dense_type(out_dtype) || out_dtype == IDX_CODES))
+        return IDX_ERR_INVALID_ARG;
+    if (rows > 0 && (!codes || !scales || !out || !is_aligned(codes, 16) ||
+                     !is_aligned(scales, 4) || !is_aligned(out, 16) || !is_aligned(slots, 4) ||
+                     (!slots && rows > num_slots) ||
+                     (out_dtype == IDX_CODES && (!out_scales || !is_aligned(out_scales, 4)))))
+        return IDX_ERR_INVALID_ARG;
+    if (!device_supported())
+        return IDX_ERR_UNSUPPORTED;
+    if (rows == 0)
+        return IDX_OK;
+    const CacheReadCall c{static_cast<const uint8_t*>(codes),
+                          scales,
+                          slots,
+                          out,
+                          out_scales,
+                          rows,
+                          heads,
+                          D,
+                          num_slots,
+                          format == IDX_K_FP4_E2M1_UE8M0,
+                          out_dtype};
+    count_launch();
+    return finish(launch_cache_read(c, static_cast<cudaStream_t>(stream)));
+}
+
+int indexer_page_slots(indexer_plan_t p, const int32_t* page_table, int64_t ld_page_table,
+                       int32_t page_size, int32_t* slots, void* stream)
+{
+    if (!p || page_size < 1)
+        return IDX_ERR_INVALID_ARG;
+    const PlanView v = plan_view(p);
+    if (ld_page_table < (v.max_L + (int64_t)page_size - 1) / page_size)
+        return IDX_ERR_INVALID_ARG;
+    if (v.Lk > 0 && (!page_table || !slots || !is_aligned(page_table, 4) || !is_aligned(slots, 4)))
+        return IDX_ERR_INVALID_ARG;
+    if (!device_supported())
+        return IDX_ERR_UNSUPPORTED;
+    if (v.Lk == 0)
+        return IDX_OK;
+    PageSlotParams pp;
+    std::memset(&pp, 0, sizeof(pp));
+    pp.table = page_table;
+    pp.ld_table = ld_page_table;
+    pp.slots = slots;
+    pp.page = page_size;
+    pp.num_requests = v.R;
+    std::copy(v.key_begin, v.key_begin + v.R + 1, pp.key_begin);
+    count_launch();
+    return finish(launch_page_slots(pp, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

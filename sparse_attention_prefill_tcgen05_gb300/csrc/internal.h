@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+struct indexer_plan_s;
+
 namespace idx {
 
 // Launch with programmatic stream serialization: the kernel may begin before the
@@ -299,5 +301,81 @@ cudaError_t launch_fp4_to_fp8(const uint8_t* k4, const uint8_t* sf, int keys, in
 cudaError_t launch_pad_heads(const void* q, const float* s_q, const float* w, void* q_out,
                              float* s_q_out, float* w_out, int rows, int h_in, int h_out, int D,
                              cudaStream_t st);
+
+// ------------------------------------------------- operators around the indexer
+// What the operators' entry points read of a plan, and the library's launch counter.
+struct PlanView {
+    int R, T, Lk, max_L;
+    const int32_t* row_begin;    // [R+1]
+    const int32_t* key_begin;    // [R+1]
+    const int32_t* L;            // [R]
+};
+PlanView plan_view(const struct ::indexer_plan_s* p);
+void count_launch();             // adds one to indexer_launch_count
+bool device_supported();         // the current device is one the kernels are built for
+int device_sms();                // its SMs
+
+constexpr int kMaxRotPairs = 128;
+constexpr int kMaxHeadDim = 256;
+
+// Rotation of pairs of a vector's elements.  Pair i turns by position * inc[i] / 2^64
+// turns: the product is taken modulo 2^64, so the angle is exact at every position.
+struct RopeParams {
+    int32_t rot;                 // rotated elements (even); 0: no rotation
+    int32_t offset;              // first rotated element
+    int32_t interleaved;         // pairs (2i, 2i+1) instead of (i, i + rot/2)
+    int32_t inverse;             // turn back
+    float amplitude;             // factor of the rotated elements
+    uint64_t inc[kMaxRotPairs];
+};
+
+// x [rows, heads, D] (element strides, last axis contiguous) rotated into out.
+struct RopeCall {
+    const void* x;
+    void* out;
+    const int32_t* positions;    // [rows]
+    int64_t x_row, x_head, out_row, out_head;   // strides in elements
+    int32_t rows, heads, D, dtype;
+};
+cudaError_t launch_rope(const RopeParams& rp, const RopeCall& c, cudaStream_t st);
+
+// x [rows, heads, D] rotated (rp.rot > 0) and quantised into rows of a cache
+// [num_slots, heads]: row i goes to slot slots[i] (nullptr: i); slots outside
+// [0, num_slots) are skipped.
+struct CacheWriteCall {
+    const void* x;
+    const int32_t* positions;
+    const int32_t* slots;
+    uint8_t* codes;
+    void* scales;
+    int64_t x_row, x_head;
+    int32_t rows, heads, D, dtype, num_slots, fp4;
+};
+cudaError_t launch_cache_write(const RopeParams& rp, const CacheWriteCall& c, cudaStream_t st);
+
+// Cache rows slots[i] (nullptr: i), i < rows: as values of out_dtype, or (out_dtype
+// IDX_CODES) as codes and scales.  Rows of slots outside the cache read as zeros.
+struct CacheReadCall {
+    const uint8_t* codes;
+    const void* scales;
+    const int32_t* slots;
+    void* out;
+    void* out_scales;
+    int32_t rows, heads, D, num_slots, fp4, out_dtype;
+};
+cudaError_t launch_cache_read(const CacheReadCall& c, cudaStream_t st);
+
+// Cache slot of every packed key of the batch: key j of request r is at
+// table[r, j / page] * page + j % page, -1 where the entry is negative or the slot
+// does not fit an int32.
+struct PageSlotParams {
+    const int32_t* table;
+    int64_t ld_table;
+    int32_t* slots;              // [total keys]
+    int32_t page;
+    int32_t num_requests;
+    int32_t key_begin[kMaxRequests + 1];
+};
+cudaError_t launch_page_slots(const PageSlotParams& p, cudaStream_t st);
 
 }  // namespace idx
