@@ -507,6 +507,102 @@ int indexer_cache_read(const void* codes, const void* scales, int32_t format, in
 int indexer_page_slots(indexer_plan_t plan, const int32_t* page_table, int64_t ld_page_table,
                        int32_t page_size, int32_t* slots, void* stream);
 
+/* ------------------------------------------- attention over the selected keys
+ * For row t of request r, query head h and its key/value head g = h / (Hq / Hkv):
+ *     a_j = scale * <q[t,h,:], k[slot(j),g,:]>,   lse[t,h] = log sum_j exp(a_j),
+ *     out[t,h,:] = sum_j exp(a_j - lse[t,h]) v[slot(j),g,:]
+ * over the row's selected keys j.  Entry sel[t,i] selects the keys
+ * [sel * block, sel * block + block) of the row's request (block = 1: the indexer's key
+ * indices); those below compress_len[t] and the request's key count take part.  Negative
+ * entries, entries past the row's keys and entries at or past sel_count[t] select nothing, in any
+ * place of the row; a key selected twice counts twice.  A row that selects nothing gives out = 0 and
+ * lse = -inf.
+ *   slot(j) = page_table[r, j / page_size] * page_size + j % page_size with page_size > 0,
+ *   else the packed key cu_seqlens_k[r] + j.  Keys on negative table entries, or whose
+ *   slot is not below num_slots, are left out.
+ * Formats: q and out are dtype (IDX_BF16, IDX_FP16); k and v are of that type
+ * (IDX_KV_DENSE) or caches of format IDX_K_FP8_E4M3 with their scales [num_slots, Hkv]
+ * (IDX_KV_FP8_E4M3).  Scores, softmax and sums are fp32; the softmax weights enter the product with
+ * v with 8 bits of mantissa or more, relative to the row's largest.
+ *
+ * indexer_attention_spec:
+ *   Hq, Hkv      query and key/value heads, Hkv divides Hq, Hq <= IDX_MAX_HEADS
+ *   D            64 or 128 (others IDX_ERR_UNSUPPORTED)
+ *   block        keys per entry: 1, 2, 4, ... 128
+ *   num_sel      entries per row, 1..65,536
+ *   num_slots    rows of k and v
+ *   scale        finite
+ * indexer_attention_create: host only, needs no GPU, once per batch (plan: its requests, rows
+ *   and key counts); *workspace_bytes receives what a call needs (0 where rows alone fill
+ *   the GPU; else partial results of rows whose keys are split over several blocks).  The plan
+ *   may be destroyed afterwards.
+ */
+#define IDX_KV_DENSE 0
+#define IDX_KV_FP8_E4M3 1
+
+typedef struct indexer_attention_spec {
+    int32_t Hq;
+    int32_t Hkv;
+    int32_t D;
+    int32_t block;
+    int32_t num_sel;
+    int32_t dtype;
+    int32_t kv_format;
+    int32_t num_slots;
+    int32_t page_size;
+    float scale;
+} indexer_attention_spec;
+
+typedef struct indexer_attention_s* indexer_attention_t;
+
+int indexer_attention_create(indexer_plan_t plan, const indexer_attention_spec* spec,
+                             indexer_attention_t* out_attention, size_t* workspace_bytes);
+void indexer_attention_destroy(indexer_attention_t attention);
+
+/* Operands of one call.  Strides in elements, none negative; rows and heads of q, k and v
+ * are 16-byte aligned (base and strides), the last axis contiguous; out's rows and heads
+ * are at least D apart.
+ *   q [rows, Hq, D], k and v [num_slots, Hkv, D], out [rows, Hq, D]
+ *   k_scale, v_scale  float [num_slots, Hkv] packed (IDX_KV_FP8_E4M3), else NULL
+ *   sel               int32 [rows, num_sel], rows ld_sel apart
+ *   sel_count         int32 [rows] or NULL (num_sel for every row)
+ *   compress_len      int32 [rows]
+ *   page_table        int32 [requests, ld_page_table] (page_size > 0), else NULL
+ *   lse               float [rows, Hq] packed, or NULL
+ */
+typedef struct indexer_attention_io {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* out;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* sel;
+    const int32_t* sel_count;
+    const int32_t* compress_len;
+    const int32_t* page_table;
+    float* lse;
+    int64_t q_row, q_head;
+    int64_t k_slot, k_head;
+    int64_t v_slot, v_head;
+    int64_t out_row, out_head;
+    int64_t ld_sel;
+    int64_t ld_page_table;
+} indexer_attention_io;
+
+/* ws: 256-byte aligned, at least what indexer_attention_create asked for (may be NULL where
+ * that is 0).  Two calls that overlap on the GPU need a workspace each. */
+int indexer_sparse_attention(indexer_attention_t attention, const indexer_attention_io* io,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/* Block lists of a candidate mask (indexer_candidate_blocks' output, or any mask of
+ * `block` keys per byte): blocks int32 [rows, num_sel] = the row's first num_sel non-zero
+ * blocks below ceil(min(compress_len[t], L_r) / block) in ascending order, then -1; count
+ * int32 [rows] (or NULL) how many those are.  ld_mask >= ceil(max L_r / block). */
+int indexer_mask_blocks(indexer_plan_t plan, const uint8_t* cand_mask, int64_t ld_mask,
+                        const int32_t* compress_len, int32_t block, int32_t* blocks,
+                        int32_t num_sel, int32_t* count, void* stream);
+
 const char* indexer_error_string(int status);
 int indexer_version(void);
 

@@ -13,6 +13,7 @@ from ._lib import (  # noqa: F401
     indexer_fused_topk_mapped, indexer_convert_fp4, indexer_fallback_rows,
     IDX_BF16, IDX_CODES, IDX_FP16, IDX_FP32, IDX_ROPE_HALF, IDX_ROPE_INTERLEAVED, Rope,
     indexer_cache_read, indexer_cache_write, indexer_page_slots, indexer_rope,
-    indexer_rope_create,
+    indexer_rope_create, Attention, IDX_KV_DENSE, IDX_KV_FP8_E4M3, indexer_attention_create,
+    indexer_mask_blocks, indexer_sparse_attention,
     lib,
 )

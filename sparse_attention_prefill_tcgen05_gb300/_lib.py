@@ -38,6 +38,8 @@ IDX_FP32 = 2
 IDX_CODES = 3
 IDX_ROPE_HALF = 0
 IDX_ROPE_INTERLEAVED = 1
+IDX_KV_DENSE = 0
+IDX_KV_FP8_E4M3 = 1
 
 EXPORTED = ("indexer_plan", "indexer_plan_destroy", "indexer_plan_info", "indexer_logits",
             "indexer_topk", "indexer_fused_topk", "indexer_candidate_blocks",
@@ -47,7 +49,9 @@ EXPORTED = ("indexer_plan", "indexer_plan_destroy", "indexer_plan_info", "indexe
             "indexer_chunk_rows", "indexer_page_indices", "indexer_candidate_blocks_tail",
             "indexer_fused_topk_mapped", "indexer_convert_fp4", "indexer_fallback_rows",
             "indexer_noalloc_status", "indexer_rope_create", "indexer_rope_destroy",
-            "indexer_rope", "indexer_cache_write", "indexer_cache_read", "indexer_page_slots")
+            "indexer_rope", "indexer_cache_write", "indexer_cache_read", "indexer_page_slots",
+            "indexer_attention_create", "indexer_attention_destroy", "indexer_sparse_attention",
+            "indexer_mask_blocks")
 IDX_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -79,6 +83,21 @@ class _RopeSpec(ctypes.Structure):
         ("original_len", ctypes.c_double), ("beta_fast", ctypes.c_double),
         ("beta_slow", ctypes.c_double), ("amplitude", ctypes.c_double),
     ]
+
+
+class _AttentionSpec(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "Hq", "Hkv", "D", "block", "num_sel", "dtype", "kv_format", "num_slots", "page_size")]
+    _fields_ += [("scale", ctypes.c_float)]
+
+
+class _AttentionIo(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "q", "k", "v", "out", "k_scale", "v_scale", "sel", "sel_count", "compress_len",
+        "page_table", "lse")]
+    _fields_ += [(n, ctypes.c_int64) for n in (
+        "q_row", "q_head", "k_slot", "k_head", "v_slot", "v_head", "out_row", "out_head",
+        "ld_sel", "ld_page_table")]
 
 
 _lib = None
@@ -128,11 +147,17 @@ def lib():
                                           P, P]
         L.indexer_cache_read.argtypes = [P, P, i32, i32, i32, i32, P, i32, i32, P, P, P]
         L.indexer_page_slots.argtypes = [P, P, i64, i32, P, P]
+        L.indexer_attention_create.argtypes = [P, ctypes.POINTER(_AttentionSpec),
+                                               ctypes.POINTER(P), ctypes.POINTER(sz)]
+        L.indexer_attention_destroy.argtypes = [P]
+        L.indexer_attention_destroy.restype = None
+        L.indexer_sparse_attention.argtypes = [P, ctypes.POINTER(_AttentionIo), P, sz, P]
+        L.indexer_mask_blocks.argtypes = [P, P, i64, P, i32, P, i32, P, P]
         L.indexer_error_string.argtypes = [i32]
         L.indexer_error_string.restype = ctypes.c_char_p
         for name in EXPORTED:
             if name not in ("indexer_plan_destroy", "indexer_error_string",
-                            "indexer_rope_destroy"):
+                            "indexer_rope_destroy", "indexer_attention_destroy"):
                 getattr(L, name).restype = ctypes.c_int
         L.indexer_launch_count.restype = ctypes.c_longlong
         L.indexer_fallback_rows.argtypes = [P, P, P]
@@ -478,3 +503,99 @@ def indexer_page_slots(plan: Plan, page_table, page_size: int, slots=None, strea
         plan.handle, table, page_table.stride(0), int(page_size),
         _i32("slots", slots, (plan.problem.total_keys,)), _stream(stream)))
     return slots
+
+
+class Attention:
+    """Owns an ``indexer_attention_t``; destroyed with the object."""
+
+    def __init__(self, handle, workspace_bytes: int, spec: _AttentionSpec, rows: int,
+                 requests: int):
+        self.handle = handle
+        self.workspace_bytes = workspace_bytes
+        self.spec = spec
+        self.rows = rows
+        self.requests = requests
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h is not None and _lib is not None:
+            _lib.indexer_attention_destroy(h)
+
+
+def indexer_attention_create(plan: Plan, Hq: int, Hkv: int, D: int, num_sel: int, block: int = 1,
+                             dtype: int = IDX_BF16, kv_format: int = IDX_KV_DENSE,
+                             num_slots: Optional[int] = None, page_size: int = 0,
+                             scale: Optional[float] = None) -> Attention:
+    """Attention over ``num_sel`` selected keys (or blocks of ``block`` keys) a row for the
+    plan's batch (host only).  ``num_slots`` rows of k and v (default: the packed keys),
+    ``scale`` 1/sqrt(D) by default."""
+    spec = _AttentionSpec(Hq, Hkv, D, block, num_sel, dtype, kv_format,
+                          plan.problem.total_keys if num_slots is None else num_slots, page_size,
+                          max(D, 1) ** -0.5 if scale is None else scale)
+    handle, ws = ctypes.c_void_p(), ctypes.c_size_t()
+    _check("indexer_attention_create", lib().indexer_attention_create(
+        plan.handle, ctypes.byref(spec), ctypes.byref(handle), ctypes.byref(ws)))
+    return Attention(handle, ws.value, spec, plan.problem.total_rows, plan.problem.num_requests)
+
+
+def indexer_sparse_attention(attn: Attention, q, k, v, sel, compress_len, out, ws=None,
+                             k_scale=None, v_scale=None, sel_count=None, page_table=None,
+                             lse=None, stream=None):
+    """Attention of ``q`` [rows, Hq, D] over the keys ``sel`` (int32 [rows, num_sel]) of ``k`` and
+    ``v`` [num_slots, Hkv, D] into ``out`` (and ``lse`` fp32 [rows, Hq]); see the header."""
+    s = attn.spec
+    dense = s.kv_format == IDX_KV_DENSE
+    for name, t, shape in (("q", q, (attn.rows, s.Hq, s.D)), ("out", out, (attn.rows, s.Hq, s.D)),
+                           ("k", k, (s.num_slots, s.Hkv, s.D)), ("v", v, (s.num_slots, s.Hkv, s.D))):
+        if t.shape != shape or t.stride(2) != 1 or not t.is_cuda:
+            raise ValueError(f"{name}: CUDA tensor {shape} with a contiguous last axis expected")
+        if name in "kv" and not dense:
+            if t.element_size() != 1:
+                raise ValueError(f"{name}: e4m3 codes of one byte expected")
+        elif _DTYPES.get(t.dtype) != s.dtype:
+            raise ValueError(f"{name}: tensor of the attention's type expected")
+    if sel.dtype != torch.int32 or sel.shape != (attn.rows, s.num_sel) or not sel.is_cuda or \
+            sel.stride(1) != 1:
+        raise ValueError(f"sel: int32 CUDA tensor {(attn.rows, s.num_sel)} expected")
+    for name, t, shape in (("k_scale", k_scale, (s.num_slots, s.Hkv)),
+                           ("v_scale", v_scale, (s.num_slots, s.Hkv)),
+                           ("lse", lse, (attn.rows, s.Hq))):
+        if t is not None and (t.dtype != torch.float32 or t.shape != shape or not t.is_cuda
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name}: contiguous fp32 CUDA tensor {shape} expected")
+    ld_table = 0
+    if page_table is not None:
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_cuda or \
+                page_table.shape[0] != attn.requests or page_table.stride(1) != 1:
+            raise ValueError("page_table: int32 CUDA tensor [requests, pages] expected")
+        ld_table = page_table.stride(0) if attn.requests > 1 else page_table.shape[1]
+    io = _AttentionIo(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+        None if k_scale is None else k_scale.data_ptr(),
+        None if v_scale is None else v_scale.data_ptr(), sel.data_ptr(),
+        None if sel_count is None else _i32("sel_count", sel_count, (attn.rows,)).value,
+        _i32("compress_len", compress_len, (attn.rows,)).value,
+        None if page_table is None else page_table.data_ptr(),
+        None if lse is None else lse.data_ptr(), q.stride(0), q.stride(1), k.stride(0),
+        k.stride(1), v.stride(0), v.stride(1), out.stride(0), out.stride(1),
+        sel.stride(0) if attn.rows > 1 else s.num_sel, ld_table)
+    _check("indexer_sparse_attention", lib().indexer_sparse_attention(
+        attn.handle, ctypes.byref(io), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+        _stream(stream)))
+    return out
+
+
+def indexer_mask_blocks(plan: Plan, cand_mask, compress_len, block: int, blocks, count=None,
+                        stream=None):
+    """The candidate blocks of every mask row as a list: ``blocks`` int32 [rows, num_sel]
+    (ascending, then -1) and ``count`` int32 [rows]."""
+    rows = plan.problem.total_rows
+    if cand_mask.element_size() != 1 or not cand_mask.is_cuda or cand_mask.dim() != 2 or \
+            cand_mask.shape[0] != rows or cand_mask.stride(1) != 1:
+        raise ValueError("cand_mask: CUDA tensor [rows, blocks] of one byte expected")
+    _check("indexer_mask_blocks", lib().indexer_mask_blocks(
+        plan.handle, _ptr(cand_mask), cand_mask.stride(0) if rows > 1 else cand_mask.shape[1],
+        _i32("compress_len", compress_len, (rows,)), int(block),
+        _i32("blocks", blocks, (rows, blocks.shape[-1])), blocks.shape[-1],
+        _i32("count", count, (rows,)), _stream(stream)))
+    return blocks

@@ -19,7 +19,7 @@ ROOT = os.path.dirname(HERE)
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libindexer.so")
 SOURCES = ["logits_tc.cu", "select.cu", "rowtopk.cu", "misc.cu", "host.cu",
-           "operands.cu", "host_ops.cu"]
+           "operands.cu", "attention.cu", "host_ops.cu"]
 HEADERS = ["internal.h", "ptx.cuh", "groupsel.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -17,6 +17,12 @@ struct indexer_rope_s {
     RopeParams p;
 };
 
+struct indexer_attention_s {
+    indexer_attention_spec spec;
+    AttnParams p;                // everything but the operands of a call
+    size_t ws_bytes = 0;
+};
+
 namespace {
 
 bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -219,6 +225,154 @@ int indexer_page_slots(indexer_plan_t p, const int32_t* page_table, int64_t ld_p
     std::copy(v.key_begin, v.key_begin + v.R + 1, pp.key_begin);
     count_launch();
     return finish(launch_page_slots(pp, static_cast<cudaStream_t>(stream)));
+}
+
+int indexer_attention_create(indexer_plan_t plan, const indexer_attention_spec* s,
+                             indexer_attention_t* out, size_t* ws_bytes)
+{
+    if (!out)
+        return IDX_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (!plan || !s || s->Hkv < 1 || s->Hq < 1 || s->Hq > IDX_MAX_HEADS ||
+        s->Hq % s->Hkv != 0 || s->block < 1 || s->block > 128 ||
+        (s->block & (s->block - 1)) != 0 || s->num_sel < 1 || s->num_sel > 65536 ||
+        (s->dtype != IDX_BF16 && s->dtype != IDX_FP16) ||
+        (s->kv_format != IDX_KV_DENSE && s->kv_format != IDX_KV_FP8_E4M3) || s->num_slots < 0 ||
+        s->page_size < 0 || !std::isfinite(s->scale) || s->D < 1)
+        return IDX_ERR_INVALID_ARG;
+    if (s->D != 64 && s->D != 128)
+        return IDX_ERR_UNSUPPORTED;
+    const PlanView v = plan_view(plan);
+    if ((int64_t)v.T * s->Hq > INT32_MAX)
+        return IDX_ERR_INVALID_ARG;
+    indexer_attention_s* a = new (std::nothrow) indexer_attention_s();
+    if (!a)
+        return IDX_ERR_INVALID_ARG;
+    a->spec = *s;
+    AttnParams& p = a->p;
+    std::memset(&p, 0, sizeof(p));
+    p.scale_log2 = static_cast<float>(s->scale * 1.4426950408889634);
+    p.rows = v.T;
+    p.Hq = s->Hq;
+    p.Hkv = s->Hkv;
+    p.group = s->Hq / s->Hkv;
+    while ((1 << p.block_shift) < s->block)
+        ++p.block_shift;
+    p.num_sel = s->num_sel;
+    p.num_slots = s->num_slots;
+    p.page = s->page_size;
+    p.num_requests = v.R;
+    std::copy(v.row_begin, v.row_begin + v.R + 1, p.row_begin);
+    std::copy(v.key_begin, v.key_begin + v.R + 1, p.key_begin);
+    p.splits = 1;
+    *out = a;
+    if (ws_bytes)
+        *ws_bytes = a->ws_bytes;
+    return IDX_OK;
+}
+
+void indexer_attention_destroy(indexer_attention_t a) { delete a; }
+
+int indexer_sparse_attention(indexer_attention_t a, const indexer_attention_io* io, void* ws,
+                             size_t ws_bytes, void* stream)
+{
+    if (!a || !io)
+        return IDX_ERR_INVALID_ARG;
+    const indexer_attention_spec& s = a->spec;
+    const bool fp8 = s.kv_format == IDX_KV_FP8_E4M3;
+    const int64_t kb = fp8 ? 1 : 2;       // bytes of a cached element
+    if (a->p.rows > 0) {
+        const bool strides_ok =
+            io->q_row >= 0 && io->q_head >= 0 && io->k_slot >= 0 && io->k_head >= 0 &&
+            io->v_slot >= 0 && io->v_head >= 0 && io->out_row >= 0 && io->out_head >= 0 &&
+            (io->q_row * 2) % 16 == 0 && (io->q_head * 2) % 16 == 0 &&
+            (io->k_slot * kb) % 16 == 0 && (io->k_head * kb) % 16 == 0 &&
+            (io->v_slot * kb) % 16 == 0 && (io->v_head * kb) % 16 == 0 &&
+            (s.Hq == 1 || io->out_head >= s.D) && (a->p.rows == 1 || io->out_row >= s.D);
+        if (!strides_ok || !io->q || !io->out || !io->sel || !io->compress_len ||
+            (s.num_slots > 0 && (!io->k || !io->v)) || !is_aligned(io->q, 16) ||
+            !is_aligned(io->k, 16) || !is_aligned(io->v, 16) || !is_aligned(io->out, 2) ||
+            !is_aligned(io->sel, 4) || !is_aligned(io->sel_count, 4) ||
+            !is_aligned(io->compress_len, 4) || !is_aligned(io->page_table, 4) ||
+            !is_aligned(io->lse, 4) || !is_aligned(io->k_scale, 4) || !is_aligned(io->v_scale, 4) ||
+            io->ld_sel < s.num_sel ||
+            (fp8 && s.num_slots > 0 && (!io->k_scale || !io->v_scale)))
+            return IDX_ERR_INVALID_ARG;
+        if (s.page_size > 0) {
+            int max_L = 0;
+            for (int r = 0; r < a->p.num_requests; ++r)
+                max_L = std::max(max_L, a->p.key_begin[r + 1] - a->p.key_begin[r]);
+            if (!io->page_table ||
+                io->ld_page_table < (max_L + (int64_t)s.page_size - 1) / s.page_size)
+                return IDX_ERR_INVALID_ARG;
+        }
+    }
+    if (a->ws_bytes > 0) {
+        if (!ws || !is_aligned(ws, 256))
+            return IDX_ERR_INVALID_ARG;
+        if (ws_bytes < a->ws_bytes)
+            return IDX_ERR_WORKSPACE;
+    }
+    if (!device_supported())
+        return IDX_ERR_UNSUPPORTED;
+    if (a->p.rows == 0)
+        return IDX_OK;
+    AttnParams p = a->p;
+    p.q = static_cast<const uint8_t*>(io->q);
+    p.k = static_cast<const uint8_t*>(io->k);
+    p.v = static_cast<const uint8_t*>(io->v);
+    p.out = static_cast<uint8_t*>(io->out);
+    p.k_scale = io->k_scale;
+    p.v_scale = io->v_scale;
+    p.sel = io->sel;
+    p.sel_count = io->sel_count;
+    p.clen = io->compress_len;
+    p.table = io->page_table;
+    p.lse = io->lse;
+    p.q_row = 2 * io->q_row;
+    p.q_head = 2 * io->q_head;
+    p.k_slot = kb * io->k_slot;
+    p.k_head = kb * io->k_head;
+    p.v_slot = kb * io->v_slot;
+    p.v_head = kb * io->v_head;
+    p.out_row = 2 * io->out_row;
+    p.out_head = 2 * io->out_head;
+    p.ld_sel = io->ld_sel;
+    p.ld_table = io->ld_page_table;
+    count_launch();
+    return finish(launch_attention(p, s.D, s.dtype, fp8, static_cast<cudaStream_t>(stream)));
+}
+
+int indexer_mask_blocks(indexer_plan_t plan, const uint8_t* cand_mask, int64_t ld_mask,
+                        const int32_t* compress_len, int32_t block, int32_t* blocks,
+                        int32_t num_sel, int32_t* count, void* stream)
+{
+    if (!plan || block < 1 || num_sel < 1)
+        return IDX_ERR_INVALID_ARG;
+    const PlanView v = plan_view(plan);
+    if (ld_mask < (v.max_L + (int64_t)block - 1) / block ||
+        (v.T > 0 && (!cand_mask || !compress_len || !blocks || !is_aligned(compress_len, 4) ||
+                     !is_aligned(blocks, 4) || !is_aligned(count, 4))))
+        return IDX_ERR_INVALID_ARG;
+    if (!device_supported())
+        return IDX_ERR_UNSUPPORTED;
+    if (v.T == 0)
+        return IDX_OK;
+    MaskBlocksParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.mask = cand_mask;
+    p.ld_mask = ld_mask;
+    p.clen = compress_len;
+    p.blocks = blocks;
+    p.count = count;
+    p.block = block;
+    p.num_sel = num_sel;
+    p.rows = v.T;
+    p.num_requests = v.R;
+    std::copy(v.row_begin, v.row_begin + v.R + 1, p.row_begin);
+    std::copy(v.L, v.L + v.R, p.key_count);
+    count_launch();
+    return finish(launch_mask_blocks(p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

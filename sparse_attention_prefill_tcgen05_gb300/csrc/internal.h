@@ -378,4 +378,50 @@ struct PageSlotParams {
 };
 cudaError_t launch_page_slots(const PageSlotParams& p, cudaStream_t st);
 
+// Attention over the selected keys.  A work item is (row, key/value head, tile of query
+// heads, split of the row's key tiles of kAttnTile keys).
+constexpr int kAttnTile = 128;
+struct AttnParams {
+    const uint8_t* q;            // byte strides
+    const uint8_t* k;
+    const uint8_t* v;
+    uint8_t* out;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* sel;
+    const int32_t* sel_count;
+    const int32_t* clen;
+    const int32_t* table;
+    float* lse;
+    int64_t q_row, q_head, k_slot, k_head, v_slot, v_head, out_row, out_head;
+    int64_t ld_sel, ld_table;
+    float* part_o;               // [items, heads of a tile, D] of split rows
+    float* part_ml;              // [items, heads of a tile, 2]: running maximum (base 2), sum
+    float scale_log2;            // scale * log2(e)
+    int32_t rows, Hq, Hkv, group;    // group = Hq / Hkv
+    int32_t head_tiles;          // tiles of query heads per key/value head
+    int32_t block_shift;         // log2(keys per entry)
+    int32_t num_sel;
+    int32_t num_slots;
+    int32_t page;                // 0: packed keys
+    int32_t splits;              // splits per row
+    int32_t split_tiles;         // key tiles per split
+    int32_t num_requests;
+    int32_t row_begin[kMaxRequests + 1];
+    int32_t key_begin[kMaxRequests + 1];
+};
+cudaError_t launch_attention(const AttnParams& p, int D, int dtype, bool fp8, cudaStream_t st);
+
+struct MaskBlocksParams {
+    const uint8_t* mask;
+    int64_t ld_mask;
+    const int32_t* clen;
+    int32_t* blocks;
+    int32_t* count;              // nullable
+    int32_t block, num_sel, rows, num_requests;
+    int32_t row_begin[kMaxRequests + 1];
+    int32_t key_count[kMaxRequests];
+};
+cudaError_t launch_mask_blocks(const MaskBlocksParams& p, cudaStream_t st);
+
 }  // namespace idx
