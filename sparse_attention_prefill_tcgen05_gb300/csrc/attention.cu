@@ -1,5 +1,6 @@
 // Attention over the selected keys, and the block lists of candidate masks.
 #include <algorithm>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -110,6 +111,680 @@ attention_kernel(const __grid_constant__ AttnParams p)
         p.lse[item] = any ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
 }
 
+// ---------------------------------------------------------------- tensor-core kernel
+
+// Modes: k and v of q's type (bf16 or fp16), or e4m3 caches under bf16 or fp16 queries.
+constexpr int kModeBf16 = 0, kModeFp16 = 1, kModeFp8Bf16 = 2, kModeFp8Fp16 = 3;
+
+constexpr int kProducers = 8;       // warps that gather keys and values, 16 rows of a tile each
+constexpr int kMetaDepth = 8;       // tiles whose validity (and scales) are held
+constexpr long long kWaitCycles = 4000000000LL;   // about two seconds
+constexpr int kSmemLimit = 232448;
+
+template <int D, int NH, int MODE>
+struct AttnCfg {
+    static constexpr bool kFp8 = MODE >= kModeFp8Bf16;
+    static constexpr int kQTerms = MODE == kModeFp8Bf16 ? 2 : MODE == kModeFp8Fp16 ? 3 : 1;
+    static constexpr int kPTerms = kFp8 ? 2 : 1;
+    static constexpr int kEb = kFp8 ? 1 : 2;            // bytes of an operand element
+    static constexpr int kRow = D * kEb;                // bytes of a cached vector
+    static constexpr int kAtom = kRow < 128 ? kRow : 128;
+    static constexpr int kAtoms = kRow / kAtom;
+    static constexpr int kStage = kAttnTile * kRow;
+    static constexpr int kQRows = NH * kQTerms;
+    static constexpr int kQBytes = kQRows * kRow;
+    static constexpr int kPRow = NH * kPTerms * kEb;    // 2 NH
+    static constexpr int kPBytes = kAttnTile * kPRow;
+    static constexpr int kGroups = NH / 16;             // softmax warpgroups, 16 heads each
+    static constexpr int kSoftmaxWarps = 4 * kGroups;
+    static constexpr int kThreads = 32 * (kSoftmaxWarps + kProducers + 1);
+    static constexpr int kMeta = kMetaDepth * kAttnTile * (kFp8 ? 9 : 1);
+    static constexpr int kMisc = kMeta + 2 * kGroups * 4 * 16 * 4 + 2 * NH * 4 + 512;
+    static constexpr int kFit = (kSmemLimit - kMisc - 2 * kPBytes - 2 * kQBytes) / kStage;
+    static constexpr int kStages = kFit < 12 ? kFit : 12;
+    static constexpr int kLag = kStages - 2;            // stages in flight behind the signalled
+    static constexpr int kSmem = kStages * kStage + 2 * kPBytes + 2 * kQBytes + kMisc;
+    static constexpr int kSCols = kQRows;               // TMEM columns of a score tile
+    static constexpr int kOCols = NH * kPTerms;
+    static constexpr int kCols = 2 * (kSCols + kOCols);
+    static constexpr int kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+    static_assert(kCols <= 512 && kStages >= 4 && kSmem <= kSmemLimit, "tile does not fit");
+};
+
+// Byte offset in a tile of `W`-byte rows as the W-byte swizzle places it.
+template <int W>
+__device__ __forceinline__ uint32_t swizzled(uint32_t off)
+{
+    return off ^ (((off >> 7) & (W / 16 - 1)) << 4);
+}
+
+struct AttnItem {
+    int t, g, ht, split;
+    int n_sel;          // entries of the row
+    int tile, tiles;    // key tiles [tile, tiles) of this item
+};
+
+__device__ __forceinline__ AttnItem attn_item(const AttnParams& p, int item)
+{
+    AttnItem w;
+    w.split = item % p.splits;
+    item /= p.splits;
+    w.ht = item % p.head_tiles;
+    item /= p.head_tiles;
+    w.g = item % p.Hkv;
+    w.t = item / p.Hkv;
+    w.n_sel = p.sel_count ? max(0, min(p.num_sel, p.sel_count[w.t])) : p.num_sel;
+    const int all = ((w.n_sel << p.block_shift) + kAttnTile - 1) / kAttnTile;
+    w.tile = w.split * p.split_tiles;
+    w.tiles = min(all, w.tile + p.split_tiles);
+    return w;
+}
+
+// 16 values of every lane, combined over the warp: lane i ends with value i / 2.
+template <bool kMax>
+__device__ __forceinline__ float reduce16(const float (&v)[16])
+{
+    const int lane = threadIdx.x & 31;
+    float a[8], b[4], c[2];
+    auto op = [](float x, float y) { return kMax ? fmaxf(x, y) : x + y; };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const bool up = lane & 16;
+        const float r = __shfl_xor_sync(0xFFFFFFFFu, up ? v[i] : v[i + 8], 16);
+        a[i] = op(up ? v[i + 8] : v[i], r);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool up = lane & 8;
+        const float r = __shfl_xor_sync(0xFFFFFFFFu, up ? a[i] : a[i + 4], 8);
+        b[i] = op(up ? a[i + 4] : a[i], r);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool up = lane & 4;
+        const float r = __shfl_xor_sync(0xFFFFFFFFu, up ? b[i] : b[i + 2], 4);
+        c[i] = op(up ? b[i + 2] : b[i], r);
+    }
+    const bool up = lane & 2;
+    const float r = __shfl_xor_sync(0xFFFFFFFFu, up ? c[0] : c[1], 2);
+    const float d = op(up ? c[1] : c[0], r);
+    return op(d, __shfl_xor_sync(0xFFFFFFFFu, d, 1));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int D, int NH, int MODE>
+__global__ void __launch_bounds__(AttnCfg<D, NH, MODE>::kThreads, 1)
+attention_tc_kernel(const __grid_constant__ AttnParams p)
+{
+    using C = AttnCfg<D, NH, MODE>;
+    using T = typename std::conditional<MODE == kModeBf16 || MODE == kModeFp8Bf16, __nv_bfloat16,
+                                        __half>::type;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    uint8_t* stages = sm;
+    uint8_t* pbuf = stages + C::kStages * C::kStage;
+    uint8_t* qbuf = pbuf + 2 * C::kPBytes;
+    uint8_t* valid = qbuf + 2 * C::kQBytes;                    // [kMetaDepth][128]
+    float* exch_max = reinterpret_cast<float*>(valid + C::kMeta);
+    float* exch_sum = exch_max + C::kGroups * 64;
+    float* qscale = exch_sum + C::kGroups * 64;                // [2][NH]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(qscale + 2 * NH);
+    uint64_t* kv_full = bars;
+    uint64_t* kv_empty = kv_full + C::kStages;
+    uint64_t* meta_full = kv_empty + C::kStages;
+    uint64_t* meta_empty = meta_full + kMetaDepth;
+    uint64_t* q_empty = meta_empty + kMetaDepth;
+    uint64_t* s_full = q_empty + 2;
+    uint64_t* s_empty = s_full + 2;
+    uint64_t* p_full = s_empty + 2;
+    uint64_t* p_empty = p_full + 2;
+    uint64_t* o_full = p_empty + 2;
+    uint64_t* o_empty = o_full + 2;
+    uint64_t* drained = o_empty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x / 32), 0);
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(kv_full + i, kProducers);
+            mbar_init(kv_empty + i, 1);
+        }
+        for (int i = 0; i < kMetaDepth; ++i) {
+            mbar_init(meta_full + i, kProducers);
+            mbar_init(meta_empty + i, C::kSoftmaxWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_empty + i, 1);
+            mbar_init(s_full + i, 1);
+            mbar_init(s_empty + i, C::kSoftmaxWarps);
+            mbar_init(p_full + i, C::kSoftmaxWarps);
+            mbar_init(p_empty + i, 1);
+            mbar_init(o_full + i, 1);
+            mbar_init(o_empty + i, C::kSoftmaxWarps);
+        }
+        mbar_init(drained, 1);
+        // the swizzled tiles need their 1024-byte boundaries
+        *abort_flag = (smem_u32(sm) & 1023u) != 0;
+        fence_mbar_init();
+    }
+    constexpr int kMmaWarp = C::kSoftmaxWarps + kProducers;
+    if (warp == kMmaWarp) {
+        tmem_alloc(tmem_slot, C::kTmem);
+        tmem_relinquish();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem_s = tmem, tmem_o = tmem + 2 * C::kSCols;
+    pdl_wait_then_release();
+    // The status word is cleared by the call itself; a wait that gives up sets it a whole
+    // wait budget later.
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        *p.status = *abort_flag ? kStatusBadArg : 0u;
+
+    const int total = p.rows * p.Hkv * p.head_tiles * p.splits;
+    volatile int* ab = abort_flag;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (mbar_wait(bar, parity, kWaitCycles, ab))
+            return true;
+        if (!*ab) {
+            *ab = 1;
+            atomicOr(p.status, kStatusTimeout);
+        }
+        return false;
+    };
+
+    if (warp < C::kSoftmaxWarps) {
+        // ---------------------------------------------------------------- softmax
+        // Thread = one key of the tile (a TMEM lane) x 16 heads.
+        const int wg = warp / 4, quad = warp & 3, key = 32 * quad + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+        const int bar_id = 1 + wg;
+        float* xmax = exch_max + wg * 64;
+        float* xsum = exch_sum + wg * 64;
+        bool bad = false, out_of_here = false;
+        int n = 0, iq = 0;
+        for (int item = blockIdx.x; item < total && !out_of_here; item += gridDim.x) {
+            const AttnItem w = attn_item(p, item);
+            const int head0 = w.ht * NH + 16 * wg;      // first head of the group for this thread
+            float m[16], l[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                m[i] = -3.0e38f;
+                l[i] = 0.0f;
+            }
+            for (int j = w.tile; j < w.tiles; ++j, ++n) {
+                const int b = n & 1;
+                bad |= !wait(s_full + b, (n >> 1) & 1);
+                tc_fence_after();
+                float x[16];
+                tmem_ld_32x32b_x16(tmem_s + lanes + b * C::kSCols + 16 * wg, x);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(s_empty + b);
+                bad |= !wait(meta_full + n % kMetaDepth, (n / kMetaDepth) & 1);
+                const bool ok = valid[(n % kMetaDepth) * kAttnTile + key] != 0;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(meta_empty + n % kMetaDepth);
+                float over = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    x[i] *= p.scale_log2;
+                    over = fmaxf(over, x[i] - m[i]);
+                }
+                // The running maximum is replaced only where a score passes it by more than
+                // 2^8: weights then stay below 2^8, and most tiles need no rescaling of the
+                // accumulated output (and no exchange over the keys).
+                const bool first = j == w.tile;
+                if (first || bar_any((ok && over > 8.0f) || bad, bar_id, 128)) {
+                    float v[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        v[i] = ok ? x[i] : -INFINITY;
+                    const float mine = reduce16<true>(v);
+                    if ((lane & 1) == 0)
+                        xmax[quad * 16 + lane / 2] = mine;
+                    if (!bar_all(!bad, bar_id, 128)) {
+                        out_of_here = true;
+                        break;
+                    }
+                    float f[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float mn =
+                            fmaxf(fmaxf(fmaxf(m[i], xmax[i]), fmaxf(xmax[16 + i], xmax[32 + i])),
+                                  xmax[48 + i]);
+                        f[i] = ex2(m[i] - mn);
+                        m[i] = mn;
+                        l[i] *= f[i];
+                    }
+                    if (!first) {
+                        // the products of the tiles before are complete
+                        bad |= !wait(p_empty + ((n - 1) & 1), ((n - 1) >> 1) & 1);
+                        tc_fence_after();
+                        const uint32_t at = tmem_o + lanes + (iq & 1) * C::kOCols + 16 * wg;
+                        tmem_ld_32x32b_x16(at, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            v[i] *= f[i];
+                        tmem_st_32x32b_x16(at, v);
+                        tmem_wait_st();
+                        tc_fence_before();
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    x[i] = ok ? ex2(x[i] - m[i]) : 0.0f;
+                    l[i] += x[i];
+                }
+                bad |= !wait(p_empty + b, ((n >> 1) & 1) ^ 1);
+                uint8_t* prow = pbuf + b * C::kPBytes;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint4 v4 = make_uint4(
+                        pack2<T>(x[8 * c], x[8 * c + 1]), pack2<T>(x[8 * c + 2], x[8 * c + 3]),
+                        pack2<T>(x[8 * c + 4], x[8 * c + 5]), pack2<T>(x[8 * c + 6], x[8 * c + 7]));
+                    *reinterpret_cast<uint4*>(
+                        prow + swizzled<C::kPRow>(key * C::kPRow + 32 * wg + 16 * c)) = v4;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(p_full + b);
+            }
+            if (out_of_here)
+                break;
+            const bool some = w.tiles > w.tile;
+            float o[16];
+            float total_l[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                o[i] = 0.0f;
+                total_l[i] = 0.0f;
+            }
+            if (some) {
+                const float mine = reduce16<false>(l);
+                if ((lane & 1) == 0)
+                    xsum[quad * 16 + lane / 2] = mine;
+                bad |= !wait(o_full + (iq & 1), (iq >> 1) & 1);
+                if (!bar_all(!bad, bar_id, 128))
+                    break;
+                tc_fence_after();
+                tmem_ld_32x32b_x16(tmem_o + lanes + (iq & 1) * C::kOCols + 16 * wg, o);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(o_empty + (iq & 1));
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    total_l[i] = (xsum[i] + xsum[16 + i]) + (xsum[32 + i] + xsum[48 + i]);
+                ++iq;
+            }
+            // thread = one element (of D) x 16 heads
+            if (p.splits == 1) {
+                uint8_t* out = p.out + w.t * p.out_row + (int64_t)w.g * p.group * p.out_head;
+                float* lse = p.lse ? p.lse + (int64_t)w.t * p.Hq + w.g * p.group : nullptr;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int h = head0 + i;
+                    if (h < p.group) {
+                        if (D == 128 || key < D)
+                            reinterpret_cast<T*>(out + h * p.out_head)[key] =
+                                static_cast<T>(total_l[i] == 0.0f ? 0.0f : o[i] / total_l[i]);
+                        if (lse && key == i)
+                            lse[h] = (m[i] + log2f(total_l[i])) * 0.693147180559945309f;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int64_t at = (int64_t)item * NH + 16 * wg + i;
+                    if (D == 128 || key < D)
+                        p.part_o[at * D + key] = o[i];
+                    if (key == i)
+                        reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(m[i], total_l[i]);
+                }
+            }
+        }
+    } else if (warp < kMmaWarp) {
+        // --------------------------------------------------------------- producers
+        // A warp gathers 16 keys of every tile.  The index of a key is read two tiles ahead
+        // and its page one tile ahead, over the items' ends.
+        const int pw = warp - C::kSoftmaxWarps, row = lane & 15;
+        struct Cursor {
+            AttnItem w;
+            int item, r, len, base;
+        };
+        auto load_item = [&](Cursor& c) {
+            c.w = attn_item(p, c.item);
+            c.r = request_of(p.row_begin, p.num_requests, c.w.t);
+            c.base = p.key_begin[c.r];
+            c.len = min(p.clen[c.w.t], p.key_begin[c.r + 1] - c.base);
+        };
+        // to the first tile of the next item that has any
+        auto settle = [&](Cursor& c) {
+            while (c.item < total) {
+                load_item(c);
+                if (c.w.tile < c.w.tiles)
+                    return;
+                c.item += gridDim.x;
+            }
+        };
+        auto next = [&](Cursor c) {
+            if (c.item < total && ++c.w.tile >= c.w.tiles) {
+                c.item += gridDim.x;
+                settle(c);
+            }
+            return c;
+        };
+        auto entry = [&](const Cursor& c) {      // the list entry of this lane's key
+            if (c.item >= total)
+                return -1;
+            const int pos = c.w.tile * kAttnTile + pw * 16 + row;
+            const int e = pos >> p.block_shift;
+            return e < c.w.n_sel ? p.sel[c.w.t * p.ld_sel + e] : -1;
+        };
+        struct Where {
+            int32_t page, off;                   // slot = page * page size + off; page < 0: none
+        };
+        auto locate = [&](const Cursor& c, int32_t e) {
+            Where a{-1, 0};
+            if (e < 0 || c.item >= total)
+                return a;
+            const int pos = c.w.tile * kAttnTile + pw * 16 + row;
+            const int64_t j = ((int64_t)e << p.block_shift) + (pos & ((1 << p.block_shift) - 1));
+            if (j >= c.len)
+                return a;
+            if (p.page == 0) {
+                a.page = 0;
+                a.off = c.base + static_cast<int32_t>(j);
+            } else {
+                const int32_t pg = static_cast<int32_t>(j) / p.page;
+                a.page = p.table[c.r * p.ld_table + pg];
+                a.off = static_cast<int32_t>(j) - pg * p.page;
+            }
+            return a;
+        };
+        int issued = 0, signalled = 0;           // stages, alternately k and v
+        auto signal = [&] {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(kv_full + signalled % C::kStages);
+                if ((signalled & 1) == 0)
+                    mbar_arrive(meta_full + (signalled >> 1) % kMetaDepth);
+            }
+            ++signalled;
+        };
+        // Wait for a buffer; what is in flight is signalled first if the wait is not over at
+        // once, since the consumer may need it to free the buffer.
+        auto acquire = [&](uint64_t* bar, uint32_t parity) {
+            if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)))
+                return true;
+            cp_async_wait<0>();
+            while (signalled < issued)
+                signal();
+            return static_cast<bool>(__all_sync(0xFFFFFFFFu, wait(bar, parity)));
+        };
+
+        Cursor c0;
+        c0.item = blockIdx.x;
+        settle(c0);
+        int32_t e0 = entry(c0);
+        Cursor c1 = next(c0);
+        int32_t e1 = entry(c1);
+        Where a0 = locate(c0, e0);
+        int n = 0, iq = 0, last_item = -1;
+        bool ok = true;
+        while (c0.item < total && ok) {
+            const Cursor c2 = next(c1);
+            const int32_t e2 = entry(c2);
+            const Where a1 = locate(c1, e1);
+            const int64_t slot64 = (int64_t)a0.page * max(p.page, 1) + a0.off;
+            const int32_t slot =
+                a0.page >= 0 && slot64 < p.num_slots ? static_cast<int32_t>(slot64) : -1;
+            const AttnItem& w = c0.w;
+            if (c0.item != last_item) {
+                // the item's queries join the copies of its first keys
+                ok = acquire(q_empty + (iq & 1), ((iq >> 1) & 1) ^ 1);
+                if (!ok)
+                    break;
+                constexpr int kChunks = C::kQBytes / 16, kPerRow = C::kRow / 16;
+                const uint8_t* q = p.q + w.t * p.q_row + (int64_t)w.g * p.group * p.q_head;
+                const uint32_t dst = smem_u32(qbuf + (iq & 1) * C::kQBytes);
+                for (int i = pw * 32 + lane; i < kChunks; i += 32 * kProducers) {
+                    const int h = i / kPerRow, c = i % kPerRow;
+                    const bool in = w.ht * NH + h < p.group;
+                    const uint32_t off = (c / 8) * (NH * 128) + h * 128 + (c % 8) * 16;
+                    cp_async16(dst + swizzled<128>(off),
+                               in ? q + (int64_t)(w.ht * NH + h) * p.q_head + c * 16 : q, in);
+                }
+                last_item = c0.item;
+                ++iq;
+            }
+            ok = acquire(meta_empty + n % kMetaDepth, ((n / kMetaDepth) & 1) ^ 1);
+            if (!ok)
+                break;
+            if (lane < 16)
+                valid[(n % kMetaDepth) * kAttnTile + pw * 16 + row] = slot >= 0;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const int st = issued % C::kStages;
+                ok = acquire(kv_empty + st, ((issued / C::kStages) & 1) ^ 1);
+                if (!ok)
+                    break;
+                const uint8_t* src = kv == 0 ? p.k + w.g * p.k_head : p.v + w.g * p.v_head;
+                const int64_t stride = kv == 0 ? p.k_slot : p.v_slot;
+                const uint32_t dst = smem_u32(stages + st * C::kStage);
+                constexpr int kPerRow = C::kRow / 16, kRows = 32 / kPerRow;   // rows a copy takes
+                const int c = lane % kPerRow;
+#pragma unroll
+                for (int i = 0; i < 16 / kRows; ++i) {
+                    const int rr = i * kRows + lane / kPerRow;
+                    const int32_t s = __shfl_sync(0xFFFFFFFFu, slot, rr);
+                    const uint32_t off = (c * 16 / C::kAtom) * (kAttnTile * C::kAtom) +
+                                         (pw * 16 + rr) * C::kAtom + (c * 16) % C::kAtom;
+                    cp_async16(dst + swizzled<C::kAtom>(off),
+                               src + (s >= 0 ? s * stride + c * 16 : 0), s >= 0);
+                }
+                cp_async_commit();
+                ++issued;
+                if (issued - signalled > C::kLag) {
+                    cp_async_wait<C::kLag>();
+                    signal();
+                }
+            }
+            ++n;
+            c0 = c1;
+            a0 = a1;
+            c1 = c2;
+            e1 = e2;
+        }
+        cp_async_wait<0>();
+        while (signalled < issued)
+            signal();
+    } else {
+        // --------------------------------------------------------------------- MMA
+        constexpr int kK = 32 / C::kEb;                 // contraction elements of one MMA
+        constexpr uint32_t idesc_s =
+            idesc_dense(128, C::kQRows, MODE == kModeBf16 ? 1 : 0, false, false);
+        constexpr uint32_t idesc_o =
+            idesc_dense(128, C::kOCols, MODE == kModeBf16 ? 1 : 0, true, true);
+        struct Pending {
+            bool any, first, last;
+            int n, iq;
+        } pv{false, false, false, 0, 0};
+        auto product = [&]() {                          // O += P V of a tile
+            const int st = (2 * pv.n + 1) % C::kStages, b = pv.n & 1;
+            bool ok = wait(kv_full + st, ((2 * pv.n + 1) / C::kStages) & 1) &&
+                      wait(p_full + b, (pv.n >> 1) & 1) &&
+                      (!pv.first || wait(o_empty + (pv.iq & 1), ((pv.iq >> 1) & 1) ^ 1));
+            if (!__all_sync(0xFFFFFFFFu, ok))
+                return false;
+            tc_fence_after();
+            if (elect_one()) {
+                // v rows are keys: both operands are read along their rows.  D = 64 takes the
+                // same 64 elements for both halves of the 128 output rows.
+                constexpr uint32_t lbo = D * C::kEb > C::kAtom ? kAttnTile * C::kAtom : 0;
+                const uint64_t a0 = smem_desc(smem_u32(stages + st * C::kStage), C::kAtom, lbo,
+                                              8 * C::kAtom);
+                const uint64_t b0 = smem_desc(smem_u32(pbuf + b * C::kPBytes), C::kPRow, 0,
+                                              8 * C::kPRow);
+                const uint32_t d = tmem_o + (pv.iq & 1) * C::kOCols;
+#pragma unroll
+                for (int k = 0; k < kAttnTile / kK; ++k)
+                    mma_f16(d, a0 + k * (kK * C::kAtom / 16), b0 + k * (kK * C::kPRow / 16),
+                            idesc_o, !pv.first || k > 0);
+                mma_commit(kv_empty + st);
+                mma_commit(p_empty + b);
+                if (pv.last)
+                    mma_commit(o_full + (pv.iq & 1));
+            }
+            __syncwarp();
+            return true;
+        };
+        int n = 0, iq = 0;
+        bool ok = true;
+        for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+            const AttnItem w = attn_item(p, item);
+            for (int j = w.tile; j < w.tiles; ++j, ++n) {
+                const int st = (2 * n) % C::kStages, b = n & 1;
+                ok = wait(kv_full + st, ((2 * n) / C::kStages) & 1) &&
+                     wait(s_empty + b, ((n >> 1) & 1) ^ 1);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t a = smem_u32(stages + st * C::kStage);
+                    const uint32_t q = smem_u32(qbuf + (iq & 1) * C::kQBytes);
+#pragma unroll
+                    for (int k = 0; k < D / kK; ++k) {
+                        const int atom = k * 32 / C::kAtom, in = (k * 32) % C::kAtom;
+                        mma_f16(tmem_s + b * C::kSCols,
+                                smem_desc(a + atom * (kAttnTile * C::kAtom) + in, C::kAtom, 16,
+                                          8 * C::kAtom),
+                                smem_desc(q + atom * (C::kQRows * C::kAtom) + in, C::kAtom, 16,
+                                          8 * C::kAtom),
+                                idesc_s, k > 0);
+                    }
+                    mma_commit(kv_empty + st);
+                    mma_commit(s_full + b);
+                    if (j + 1 == w.tiles)
+                        mma_commit(q_empty + (iq & 1));
+                }
+                __syncwarp();
+                if (pv.any && !product()) {
+                    ok = false;
+                    break;
+                }
+                pv = Pending{true, j == w.tile, j + 1 == w.tiles, n, iq};
+            }
+            iq += w.tiles > w.tile;
+        }
+        if (ok && pv.any)
+            product();
+        // what was issued, and its arrivals, end before the memory goes
+        if (elect_one())
+            mma_commit(drained);
+        __syncwarp();
+        volatile int never = 0;
+        mbar_wait(drained, 0, kWaitCycles, &never);
+    }
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmem);
+    }
+}
+
+// Split rows: the partial outputs of a row and head, weighted by their running maxima.  One
+// warp per (row, query head).
+template <typename T, int D>
+__global__ void __launch_bounds__(128)
+attention_join_kernel(const __grid_constant__ AttnParams p, int nh)
+{
+    pdl_wait_then_release();
+    const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+    if (i >= (int64_t)p.rows * p.Hq)
+        return;
+    const int lane = threadIdx.x & 31;
+    const int64_t t = i / p.Hq;
+    const int h = static_cast<int>(i % p.Hq), g = h / p.group, hg = h % p.group;
+    const int64_t item0 = ((t * p.Hkv + g) * p.head_tiles + hg / nh) * p.splits;
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+    float m = -3.0e38f;
+    for (int s = 0; s < p.splits; ++s)
+        m = fmaxf(m, ml[(item0 + s) * nh + hg % nh].x);
+    constexpr int N = D / 32;
+    float o[N] = {}, l = 0.0f;
+    for (int s = 0; s < p.splits; ++s) {
+        const int64_t at = (item0 + s) * nh + hg % nh;
+        const float2 v = ml[at];
+        const float f = ex2(v.x - m);
+        l = fmaf(v.y, f, l);
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            o[k] = fmaf(p.part_o[at * D + lane + 32 * k], f, o[k]);
+    }
+    T* out = reinterpret_cast<T*>(p.out + t * p.out_row + h * p.out_head);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        out[lane + 32 * k] = static_cast<T>(l == 0.0f ? 0.0f : o[k] / l);
+    if (p.lse && lane == 0)
+        p.lse[i] = (m + log2f(l)) * 0.693147180559945309f;
+}
+
+template <int D, int NH, int MODE>
+cudaError_t attention_tc(const AttnParams& p, cudaStream_t st)
+{
+    using C = AttnCfg<D, NH, MODE>;
+    static const cudaError_t attr =
+        cudaFuncSetAttribute(attention_tc_kernel<D, NH, MODE>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (attr != cudaSuccess)
+        return attr;
+    const int items = p.rows * p.Hkv * p.head_tiles * p.splits;
+    return launch_pdl(attention_tc_kernel<D, NH, MODE>, dim3(std::min(items, device_sms())),
+                      dim3(C::kThreads), C::kSmem, st, p);
+}
+
+template <int D, int MODE>
+cudaError_t attention_heads(const AttnParams& p, int nh, cudaStream_t st)
+{
+    cudaError_t e = nh == 16   ? attention_tc<D, 16, MODE>(p, st)
+                    : nh == 32 ? attention_tc<D, 32, MODE>(p, st)
+                               : attention_tc<D, 64, MODE>(p, st);
+    if (e != cudaSuccess || p.splits == 1)
+        return e;
+    using T = typename std::conditional<MODE == kModeBf16, __nv_bfloat16, __half>::type;
+    count_launch();
+    const unsigned blocks = static_cast<unsigned>(((int64_t)p.rows * p.Hq + 3) / 4);
+    return launch_pdl(attention_join_kernel<T, D>, dim3(blocks), dim3(128), 0, st, p, nh);
+}
+
 // One warp per row: 32 mask bytes at a time, each set byte's place by a ballot.
 __global__ void __launch_bounds__(128)
 mask_blocks_kernel(const __grid_constant__ MaskBlocksParams p)
@@ -150,8 +825,23 @@ cudaError_t attention_of(const AttnParams& p, int D, cudaStream_t st)
 
 }  // namespace
 
+int attention_heads_per_tile(int group, int dtype, bool fp8)
+{
+    (void)dtype;
+    (void)fp8;
+    return group <= 16 ? 16 : group <= 32 ? 32 : 64;
+}
+
 cudaError_t launch_attention(const AttnParams& p, int D, int dtype, bool fp8, cudaStream_t st)
 {
+    if (!fp8) {
+        const int nh = attention_heads_per_tile(p.group, dtype, fp8);
+        if (dtype == IDX_BF16)
+            return D == 64 ? attention_heads<64, kModeBf16>(p, nh, st)
+                           : attention_heads<128, kModeBf16>(p, nh, st);
+        return D == 64 ? attention_heads<64, kModeFp16>(p, nh, st)
+                       : attention_heads<128, kModeFp16>(p, nh, st);
+    }
     if (dtype == IDX_BF16)
         return fp8 ? attention_of<__nv_bfloat16, __nv_fp8_e4m3>(p, D, st)
                    : attention_of<__nv_bfloat16, __nv_bfloat16>(p, D, st);

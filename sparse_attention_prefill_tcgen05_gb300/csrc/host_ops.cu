@@ -20,10 +20,13 @@ struct indexer_rope_s {
 struct indexer_attention_s {
     indexer_attention_spec spec;
     AttnParams p;                // everything but the operands of a call
+    size_t part_floats = 0;      // partial vectors
     size_t ws_bytes = 0;
 };
 
 namespace {
+
+constexpr int kPlanSms = 152;    // SMs the splits are planned for
 
 bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -264,7 +267,33 @@ int indexer_attention_create(indexer_plan_t plan, const indexer_attention_spec* 
     p.num_requests = v.R;
     std::copy(v.row_begin, v.row_begin + v.R + 1, p.row_begin);
     std::copy(v.key_begin, v.key_begin + v.R + 1, p.key_begin);
-    p.splits = 1;
+    // Work items: rows x key/value heads x tiles of query heads, each over the row's key
+    // tiles.  Where they do not fill the SMs, the tiles of a row are split: the number of
+    // splits that ends first, in tiles' times, with one per item for its start and four for
+    // the kernel that joins the parts.
+    const int nh = attention_heads_per_tile(p.group, s->dtype, s->kv_format != IDX_KV_DENSE);
+    p.head_tiles = (p.group + nh - 1) / nh;
+    const int64_t tiles = (((int64_t)s->num_sel << p.block_shift) + kAttnTile - 1) / kAttnTile;
+    const int64_t items = (int64_t)v.T * s->Hkv * p.head_tiles;
+    if (items > (1 << 30)) {
+        delete a;
+        return IDX_ERR_INVALID_ARG;
+    }
+    int64_t best = INT64_MAX;
+    for (int64_t n = 1; n <= std::min<int64_t>(tiles, 64) && items * n <= (1 << 30); ++n) {
+        const int64_t per = (tiles + n - 1) / n;
+        if ((tiles + per - 1) / per != n)
+            continue;
+        const int64_t cost = (items * n + kPlanSms - 1) / kPlanSms * (per + 1) + (n > 1 ? 4 : 0);
+        if (cost < best) {
+            best = cost;
+            p.splits = static_cast<int32_t>(n);
+            p.split_tiles = static_cast<int32_t>(per);
+        }
+    }
+    // status word, then the parts of split rows
+    a->part_floats = p.splits > 1 ? (size_t)(items * p.splits) * nh : 0;
+    a->ws_bytes = 256 + a->part_floats * (s->D + 2) * sizeof(float);
     *out = a;
     if (ws_bytes)
         *ws_bytes = a->ws_bytes;
@@ -307,7 +336,7 @@ int indexer_sparse_attention(indexer_attention_t a, const indexer_attention_io* 
                 return IDX_ERR_INVALID_ARG;
         }
     }
-    if (a->ws_bytes > 0) {
+    if (a->p.rows > 0) {
         if (!ws || !is_aligned(ws, 256))
             return IDX_ERR_INVALID_ARG;
         if (ws_bytes < a->ws_bytes)
@@ -339,6 +368,9 @@ int indexer_sparse_attention(indexer_attention_t a, const indexer_attention_io* 
     p.out_head = 2 * io->out_head;
     p.ld_sel = io->ld_sel;
     p.ld_table = io->ld_page_table;
+    p.status = static_cast<uint32_t*>(ws);
+    p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
+    p.part_o = p.part_ml + 2 * a->part_floats;
     count_launch();
     return finish(launch_attention(p, s.D, s.dtype, fp8, static_cast<cudaStream_t>(stream)));
 }

@@ -397,6 +397,7 @@ struct AttnParams {
     int64_t ld_sel, ld_table;
     float* part_o;               // [items, heads of a tile, D] of split rows
     float* part_ml;              // [items, heads of a tile, 2]: running maximum (base 2), sum
+    uint32_t* status;
     float scale_log2;            // scale * log2(e)
     int32_t rows, Hq, Hkv, group;    // group = Hq / Hkv
     int32_t head_tiles;          // tiles of query heads per key/value head
@@ -410,6 +411,8 @@ struct AttnParams {
     int32_t row_begin[kMaxRequests + 1];
     int32_t key_begin[kMaxRequests + 1];
 };
+// Query heads of one key/value head that a work item takes together.
+int attention_heads_per_tile(int group, int dtype, bool fp8);
 cudaError_t launch_attention(const AttnParams& p, int D, int dtype, bool fp8, cudaStream_t st);
 
 struct MaskBlocksParams {
