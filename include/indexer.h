@@ -560,8 +560,8 @@ int indexer_attention_create(indexer_plan_t plan, const indexer_attention_spec* 
 void indexer_attention_destroy(indexer_attention_t attention);
 
 /* Operands of one call.  Strides in elements, none negative; rows and heads of q, k and v
- * are 16-byte aligned (base and strides), the last axis contiguous; out's rows and heads
- * are at least D apart.
+ * are 16-byte aligned (base and strides), the last axis contiguous, rows of k and v less than
+ * 4 GiB apart; out's rows and heads are at least D apart.
  *   q [rows, Hq, D], k and v [num_slots, Hkv, D], out [rows, Hq, D]
  *   k_scale, v_scale  float [num_slots, Hkv] packed (IDX_KV_FP8_E4M3), else NULL
  *   sel               int32 [rows, num_sel], rows ld_sel apart

@@ -116,8 +116,11 @@ attention_kernel(const __grid_constant__ AttnParams p)
 // Modes: k and v of q's type (bf16 or fp16), or e4m3 caches under bf16 or fp16 queries.
 constexpr int kModeBf16 = 0, kModeFp16 = 1, kModeFp8Bf16 = 2, kModeFp8Fp16 = 3;
 
-constexpr int kProducers = 8;       // warps that gather keys and values, 16 rows of a tile each
-constexpr int kMetaDepth = 8;       // tiles whose validity (and scales) are held
+// Tiles whose validity bits (and scales) are held for the softmax.  No barrier guards them:
+// with d tiles in the ring of stages (d <= 4) the bits of tile n + 8 are written after the slots
+// of tile n + 8 - d were read, thus after a v stage came free of tile n + 8 - 2 d >= n, whose
+// weights were complete.
+constexpr int kMaskDepth = 8;
 constexpr long long kWaitCycles = 4000000000LL;   // about two seconds
 constexpr int kSmemLimit = 232448;
 
@@ -137,18 +140,27 @@ struct AttnCfg {
     static constexpr int kPBytes = kAttnTile * kPRow;
     static constexpr int kGroups = NH / 16;             // softmax warpgroups, 16 heads each
     static constexpr int kSoftmaxWarps = 4 * kGroups;
-    static constexpr int kThreads = 32 * (kSoftmaxWarps + kProducers + 1);
-    static constexpr int kMeta = kMetaDepth * kAttnTile * (kFp8 ? 9 : 1);
-    static constexpr int kMisc = kMeta + 2 * kGroups * 4 * 16 * 4 + 2 * NH * 4 + 512;
-    static constexpr int kFit = (kSmemLimit - kMisc - 2 * kPBytes - 2 * kQBytes) / kStage;
-    static constexpr int kStages = kFit < 12 ? kFit : 12;
-    static constexpr int kLag = kStages - 2;            // stages in flight behind the signalled
-    static constexpr int kSmem = kStages * kStage + 2 * kPBytes + 2 * kQBytes + kMisc;
+    
+    // at most four tiles of stages, and the slots of as many tiles
+    static constexpr int kSlotTile = kAttnTile * 4;
+    static constexpr int kMaskBytes = kMaskDepth * (16 + (kFp8 ? kAttnTile * 8 : 0));
+    static constexpr int kMisc =
+        kMaskBytes + 2 * kGroups * 4 * 16 * 4 + (kFp8 ? 2 * NH * 4 : 0) + 8 * (3 * 8 + 2 * 8 + 2);
+    static constexpr int kFit = (kSmemLimit - kMisc - 2 * kPBytes - 2 * kQBytes) /
+                                (2 * kStage + kSlotTile);
+    // Tiles held.  A warp fills the same stage of the ring every time and reads the same
+    // slot buffer, so it sees every phase of the barriers it waits on (a parity wait two
+    // phases early would pass at once).
+    static constexpr int kTiles = kFit < 4 ? kFit : 4;
+    static constexpr int kStages = 2 * kTiles;
+    static constexpr int kThreads = 32 * (kSoftmaxWarps + kStages + 2);
+    static constexpr int kSmem =
+        kStages * kStage + 2 * kPBytes + 2 * kQBytes + kTiles * kSlotTile + kMisc;
     static constexpr int kSCols = kQRows;               // TMEM columns of a score tile
     static constexpr int kOCols = NH * kPTerms;
     static constexpr int kCols = 2 * (kSCols + kOCols);
     static constexpr int kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-    static_assert(kCols <= 512 && kStages >= 4 && kSmem <= kSmemLimit, "tile does not fit");
+    static_assert(kCols <= 512 && kTiles >= 2 && kSmem <= kSmemLimit, "tile does not fit");
 };
 
 // Byte offset in a tile of `W`-byte rows as the W-byte swizzle places it.
@@ -156,6 +168,15 @@ template <int W>
 __device__ __forceinline__ uint32_t swizzled(uint32_t off)
 {
     return off ^ (((off >> 7) & (W / 16 - 1)) << 4);
+}
+
+// Row `off` / W of such a tile (W-byte rows, off below 8 W) as what its chunks' addresses
+// are combined with: for an address a whose bits from 16 up to the row are a chunk of row 0
+// of an aligned group of 8 rows, a ^ swizzle_of(off) is that chunk of the row.
+template <int W>
+__device__ __forceinline__ constexpr uint32_t swizzle_of(uint32_t off)
+{
+    return off | (((off >> 7) & (W / 16 - 1)) << 4);
 }
 
 struct AttnItem {
@@ -173,7 +194,10 @@ __device__ __forceinline__ AttnItem attn_item(const AttnParams& p, int item)
     item /= p.head_tiles;
     w.g = item % p.Hkv;
     w.t = item / p.Hkv;
-    w.n_sel = p.sel_count ? max(0, min(p.num_sel, p.sel_count[w.t])) : p.num_sel;
+    // the shuffle tells the compiler that the count, and the loops over it, are uniform
+    w.n_sel = p.sel_count ? __shfl_sync(0xFFFFFFFFu,
+                                        max(0, min(p.num_sel, p.sel_count[w.t])), 0)
+                          : p.num_sel;
     const int all = ((w.n_sel << p.block_shift) + kAttnTile - 1) / kAttnTile;
     w.tile = w.split * p.split_tiles;
     w.tiles = min(all, w.tile + p.split_tiles);
@@ -239,16 +263,18 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
     uint8_t* stages = sm;
     uint8_t* pbuf = stages + C::kStages * C::kStage;
     uint8_t* qbuf = pbuf + 2 * C::kPBytes;
-    uint8_t* valid = qbuf + 2 * C::kQBytes;                    // [kMetaDepth][128]
-    float* exch_max = reinterpret_cast<float*>(valid + C::kMeta);
+    int32_t* slots = reinterpret_cast<int32_t*>(qbuf + 2 * C::kQBytes);   // [kTiles][128]
+    uint32_t* mask = reinterpret_cast<uint32_t*>(slots + C::kTiles * kAttnTile);   // [kMaskDepth][4]
+    float* exch_max = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(mask) + C::kMaskBytes);
     float* exch_sum = exch_max + C::kGroups * 64;
     float* qscale = exch_sum + C::kGroups * 64;                // [2][NH]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(qscale + 2 * NH);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(qscale + (C::kFp8 ? 2 * NH : 0));
     uint64_t* kv_full = bars;
     uint64_t* kv_empty = kv_full + C::kStages;
-    uint64_t* meta_full = kv_empty + C::kStages;
-    uint64_t* meta_empty = meta_full + kMetaDepth;
-    uint64_t* q_empty = meta_empty + kMetaDepth;
+    uint64_t* slot_full = kv_empty + C::kStages;
+    uint64_t* slot_empty = slot_full + C::kTiles;
+    uint64_t* q_full = slot_empty + C::kTiles;
+    uint64_t* q_empty = q_full + 2;
     uint64_t* s_full = q_empty + 2;
     uint64_t* s_empty = s_full + 2;
     uint64_t* p_full = s_empty + 2;
@@ -263,14 +289,15 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(kv_full + i, kProducers);
+            mbar_init(kv_full + i, 1);
             mbar_init(kv_empty + i, 1);
         }
-        for (int i = 0; i < kMetaDepth; ++i) {
-            mbar_init(meta_full + i, kProducers);
-            mbar_init(meta_empty + i, C::kSoftmaxWarps);
+        for (int i = 0; i < C::kTiles; ++i) {
+            mbar_init(slot_full + i, 1);
+            mbar_init(slot_empty + i, 2);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + i, 1);
             mbar_init(q_empty + i, 1);
             mbar_init(s_full + i, 1);
             mbar_init(s_empty + i, C::kSoftmaxWarps);
@@ -284,7 +311,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         *abort_flag = (smem_u32(sm) & 1023u) != 0;
         fence_mbar_init();
     }
-    constexpr int kMmaWarp = C::kSoftmaxWarps + kProducers;
+    constexpr int kSlotWarp = C::kSoftmaxWarps + C::kStages, kMmaWarp = kSlotWarp + 1;
     if (warp == kMmaWarp) {
         tmem_alloc(tmem_slot, C::kTmem);
         tmem_relinquish();
@@ -338,30 +365,31 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 tmem_ld_32x32b_x16(tmem_s + lanes + b * C::kSCols + 16 * wg, x);
                 tmem_wait_ld();
                 tc_fence_before();
+                // (the scores' arrival implies the mask's)
+                const uint32_t ok = mask[(n % kMaskDepth) * 4 + quad];
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(s_empty + b);
-                bad |= !wait(meta_full + n % kMetaDepth, (n / kMetaDepth) & 1);
-                const bool ok = valid[(n % kMetaDepth) * kAttnTile + key] != 0;
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(meta_empty + n % kMetaDepth);
-                float over = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < 16; ++i)
                     x[i] *= p.scale_log2;
-                    over = fmaxf(over, x[i] - m[i]);
+                if (ok != 0xFFFFFFFFu) {
+                    const bool mine = (ok >> lane) & 1u;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        x[i] = mine ? x[i] : -INFINITY;
                 }
+                float over = x[0] - m[0];
+#pragma unroll
+                for (int i = 1; i < 16; ++i)
+                    over = fmaxf(over, x[i] - m[i]);
                 // The running maximum is replaced only where a score passes it by more than
                 // 2^8: weights then stay below 2^8, and most tiles need no rescaling of the
                 // accumulated output (and no exchange over the keys).
                 const bool first = j == w.tile;
-                if (first || bar_any((ok && over > 8.0f) || bad, bar_id, 128)) {
+                if (first || bar_any(over > 8.0f || bad, bar_id, 128)) {
                     float v[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        v[i] = ok ? x[i] : -INFINITY;
-                    const float mine = reduce16<true>(v);
+                    const float mine = reduce16<true>(x);
                     if ((lane & 1) == 0)
                         xmax[quad * 16 + lane / 2] = mine;
                     if (!bar_all(!bad, bar_id, 128)) {
@@ -395,7 +423,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    x[i] = ok ? ex2(x[i] - m[i]) : 0.0f;
+                    x[i] = ex2(x[i] - m[i]);   // a key that is none: 0
                     l[i] += x[i];
                 }
                 bad |= !wait(p_empty + b, ((n >> 1) & 1) ^ 1);
@@ -468,163 +496,172 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 }
             }
         }
-    } else if (warp < kMmaWarp) {
-        // --------------------------------------------------------------- producers
-        // A warp gathers 16 keys of every tile.  The index of a key is read two tiles ahead
-        // and its page one tile ahead, over the items' ends.
-        const int pw = warp - C::kSoftmaxWarps, row = lane & 15;
-        struct Cursor {
-            AttnItem w;
-            int item, r, len, base;
-        };
-        auto load_item = [&](Cursor& c) {
-            c.w = attn_item(p, c.item);
-            c.r = request_of(p.row_begin, p.num_requests, c.w.t);
-            c.base = p.key_begin[c.r];
-            c.len = min(p.clen[c.w.t], p.key_begin[c.r + 1] - c.base);
-        };
-        // to the first tile of the next item that has any
-        auto settle = [&](Cursor& c) {
-            while (c.item < total) {
-                load_item(c);
-                if (c.w.tile < c.w.tiles)
-                    return;
-                c.item += gridDim.x;
-            }
-        };
-        auto next = [&](Cursor c) {
-            if (c.item < total && ++c.w.tile >= c.w.tiles) {
-                c.item += gridDim.x;
-                settle(c);
-            }
-            return c;
-        };
-        auto entry = [&](const Cursor& c) {      // the list entry of this lane's key
-            if (c.item >= total)
-                return -1;
-            const int pos = c.w.tile * kAttnTile + pw * 16 + row;
-            const int e = pos >> p.block_shift;
-            return e < c.w.n_sel ? p.sel[c.w.t * p.ld_sel + e] : -1;
-        };
-        struct Where {
-            int32_t page, off;                   // slot = page * page size + off; page < 0: none
-        };
-        auto locate = [&](const Cursor& c, int32_t e) {
-            Where a{-1, 0};
-            if (e < 0 || c.item >= total)
-                return a;
-            const int pos = c.w.tile * kAttnTile + pw * 16 + row;
-            const int64_t j = ((int64_t)e << p.block_shift) + (pos & ((1 << p.block_shift) - 1));
-            if (j >= c.len)
-                return a;
-            if (p.page == 0) {
-                a.page = 0;
-                a.off = c.base + static_cast<int32_t>(j);
-            } else {
-                const int32_t pg = static_cast<int32_t>(j) / p.page;
-                a.page = p.table[c.r * p.ld_table + pg];
-                a.off = static_cast<int32_t>(j) - pg * p.page;
-            }
-            return a;
-        };
-        int issued = 0, signalled = 0;           // stages, alternately k and v
-        auto signal = [&] {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(kv_full + signalled % C::kStages);
-                if ((signalled & 1) == 0)
-                    mbar_arrive(meta_full + (signalled >> 1) % kMetaDepth);
-            }
-            ++signalled;
-        };
-        // Wait for a buffer; what is in flight is signalled first if the wait is not over at
-        // once, since the consumer may need it to free the buffer.
-        auto acquire = [&](uint64_t* bar, uint32_t parity) {
-            if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)))
-                return true;
-            cp_async_wait<0>();
-            while (signalled < issued)
-                signal();
-            return static_cast<bool>(__all_sync(0xFFFFFFFFu, wait(bar, parity)));
-        };
-
-        Cursor c0;
-        c0.item = blockIdx.x;
-        settle(c0);
-        int32_t e0 = entry(c0);
-        Cursor c1 = next(c0);
-        int32_t e1 = entry(c1);
-        Where a0 = locate(c0, e0);
-        int n = 0, iq = 0, last_item = -1;
+    } else if (warp < kSlotWarp) {
+        // ---------------------------------------------------------------- gather
+        // Warp i fills stage i of the ring: it waits for the stage, copies the 128 vectors
+        // (zeros for keys that are none), waits for its own copies and signals.  The other
+        // stages' warps keep the memory system busy meanwhile.
+        const int pw = warp - C::kSoftmaxWarps;
+        constexpr int kPerRow = C::kRow / 16;            // copies of 16 bytes a vector takes
+        constexpr int kSpans = 32 / kPerRow;             // vectors copied at a time,
+        constexpr int kSpan = kAttnTile / kSpans;        // kSpan keys apart
+        const int chunk = lane % kPerRow, row0 = lane / kPerRow * kSpan;
+        const uint32_t stage = smem_u32(stages + pw * C::kStage) + row0 * C::kAtom +
+                               (chunk * 16 / C::kAtom) * (kAttnTile * C::kAtom) +
+                               (chunk * 16) % C::kAtom;
+        const uint32_t k_slot = static_cast<uint32_t>(p.k_slot);
+        const uint32_t v_slot = static_cast<uint32_t>(p.v_slot);
+        int n = 0, st = 0, uses = 0;             // st: the tile's place in the ring
         bool ok = true;
-        while (c0.item < total && ok) {
-            const Cursor c2 = next(c1);
-            const int32_t e2 = entry(c2);
-            const Where a1 = locate(c1, e1);
-            const int64_t slot64 = (int64_t)a0.page * max(p.page, 1) + a0.off;
-            const int32_t slot =
-                a0.page >= 0 && slot64 < p.num_slots ? static_cast<int32_t>(slot64) : -1;
-            const AttnItem& w = c0.w;
-            if (c0.item != last_item) {
-                // the item's queries join the copies of its first keys
-                ok = acquire(q_empty + (iq & 1), ((iq >> 1) & 1) ^ 1);
-                if (!ok)
-                    break;
-                constexpr int kChunks = C::kQBytes / 16, kPerRow = C::kRow / 16;
+        for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+            const AttnItem w = attn_item(p, item);
+            for (int j = w.tile; j < w.tiles && ok; ++j, ++n) {
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (2 * st + kv == pw && ok) {
+                        ok = wait(kv_empty + pw, (uses & 1) ^ 1);
+                        const int sl = pw / 2;
+                        ok = ok && wait(slot_full + sl, uses & 1);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (ok) {
+                            const uint8_t* src = (kv == 0 ? p.k + w.g * p.k_head
+                                                          : p.v + w.g * p.v_head) + chunk * 16;
+                            const uint32_t stride = kv == 0 ? k_slot : v_slot;
+                            const int32_t* rows = slots + sl * kAttnTile + row0;
+                            const uint4 bits =
+                                *reinterpret_cast<const uint4*>(mask + (n % kMaskDepth) * 4);
+                            if ((bits.x & bits.y & bits.z & bits.w) == 0xFFFFFFFFu) {
+#pragma unroll 4
+                                for (int i = 0; i < kSpan; i += 8) {
+                                    const int4 s0 = *reinterpret_cast<const int4*>(rows + i);
+                                    const int4 s1 = *reinterpret_cast<const int4*>(rows + i + 4);
+                                    const int32_t s[8] = {s0.x, s0.y, s0.z, s0.w,
+                                                          s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k)
+                                        cp_async16((stage + i * C::kAtom) ^
+                                                       swizzle_of<C::kAtom>(k * C::kAtom),
+                                                   src + (uint64_t)(uint32_t)s[k] * stride);
+                                }
+                            } else {
+                                for (int i = 0; i < kSpan; ++i) {
+                                    const int32_t s = rows[i];
+                                    cp_async16((stage + i / 8 * 8 * C::kAtom) ^
+                                                   swizzle_of<C::kAtom>(i % 8 * C::kAtom),
+                                               src + (uint64_t)(uint32_t)max(s, 0) * stride, s >= 0);
+                                }
+                            }
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(slot_empty + sl);
+                        }
+                        cp_async_commit();
+                        cp_async_wait<0>();
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (ok && lane == 0)
+                            mbar_arrive(kv_full + pw);
+                        ++uses;
+                    }
+                }
+                st = st + 1 == C::kTiles ? 0 : st + 1;
+            }
+        }
+    } else if (warp == kSlotWarp) {
+        // ----------------------------------------------------------------- slots
+        // Cache slots of the selected keys, four tiles at a time so that the reads of the
+        // lists, and then of the page table, are in flight together.
+        int n = 0, iq = 0;
+        bool ok = true;
+        for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+            const AttnItem w = attn_item(p, item);
+            const int r = request_of(p.row_begin, p.num_requests, w.t);
+            const int base = p.key_begin[r];
+            const int len = min(p.clen[w.t], p.key_begin[r + 1] - base);
+            const int32_t* sel = p.sel + w.t * p.ld_sel;
+            const int32_t* table = p.table + r * p.ld_table;
+            if (w.tile >= w.tiles)
+                continue;
+            ok = wait(q_empty + (iq & 1), ((iq >> 1) & 1) ^ 1);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok)
+                break;
+            {
+                constexpr int kPerRow = C::kRow / 16;
                 const uint8_t* q = p.q + w.t * p.q_row + (int64_t)w.g * p.group * p.q_head;
                 const uint32_t dst = smem_u32(qbuf + (iq & 1) * C::kQBytes);
-                for (int i = pw * 32 + lane; i < kChunks; i += 32 * kProducers) {
+#pragma unroll 4
+                for (int i = lane; i < C::kQBytes / 16; i += 32) {
                     const int h = i / kPerRow, c = i % kPerRow;
                     const bool in = w.ht * NH + h < p.group;
                     const uint32_t off = (c / 8) * (NH * 128) + h * 128 + (c % 8) * 16;
                     cp_async16(dst + swizzled<128>(off),
                                in ? q + (int64_t)(w.ht * NH + h) * p.q_head + c * 16 : q, in);
                 }
-                last_item = c0.item;
-                ++iq;
-            }
-            ok = acquire(meta_empty + n % kMetaDepth, ((n / kMetaDepth) & 1) ^ 1);
-            if (!ok)
-                break;
-            if (lane < 16)
-                valid[(n % kMetaDepth) * kAttnTile + pw * 16 + row] = slot >= 0;
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                const int st = issued % C::kStages;
-                ok = acquire(kv_empty + st, ((issued / C::kStages) & 1) ^ 1);
-                if (!ok)
-                    break;
-                const uint8_t* src = kv == 0 ? p.k + w.g * p.k_head : p.v + w.g * p.v_head;
-                const int64_t stride = kv == 0 ? p.k_slot : p.v_slot;
-                const uint32_t dst = smem_u32(stages + st * C::kStage);
-                constexpr int kPerRow = C::kRow / 16, kRows = 32 / kPerRow;   // rows a copy takes
-                const int c = lane % kPerRow;
-#pragma unroll
-                for (int i = 0; i < 16 / kRows; ++i) {
-                    const int rr = i * kRows + lane / kPerRow;
-                    const int32_t s = __shfl_sync(0xFFFFFFFFu, slot, rr);
-                    const uint32_t off = (c * 16 / C::kAtom) * (kAttnTile * C::kAtom) +
-                                         (pw * 16 + rr) * C::kAtom + (c * 16) % C::kAtom;
-                    cp_async16(dst + swizzled<C::kAtom>(off),
-                               src + (s >= 0 ? s * stride + c * 16 : 0), s >= 0);
-                }
                 cp_async_commit();
-                ++issued;
-                if (issued - signalled > C::kLag) {
-                    cp_async_wait<C::kLag>();
-                    signal();
+            }
+            for (int j0 = w.tile; j0 < w.tiles && ok; j0 += 4) {
+                int32_t at[16];                  // list entry, then key, then slot
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int pos = j0 * kAttnTile + 32 * i + lane;
+                    const int e = pos >> p.block_shift;
+                    at[i] = j0 + i / 4 < w.tiles && e < w.n_sel ? sel[e] : -1;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int pos = j0 * kAttnTile + 32 * i + lane;
+                    const int64_t key = ((int64_t)at[i] << p.block_shift) +
+                                        (pos & ((1 << p.block_shift) - 1));
+                    at[i] = at[i] >= 0 && key < len ? static_cast<int32_t>(key) : -1;
+                }
+                if (p.page == 0) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        at[i] = at[i] >= 0 && base + (int64_t)at[i] < p.num_slots ? base + at[i] : -1;
+                } else {
+                    int32_t page[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        page[i] = at[i] >= 0 ? table[at[i] / p.page] : -1;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int64_t slot = (int64_t)page[i] * p.page + at[i] % p.page;
+                        at[i] = page[i] >= 0 && slot < p.num_slots ? static_cast<int32_t>(slot) : -1;
+                    }
+                }
+                if (j0 == w.tile) {
+                    cp_async_wait<0>();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(q_full + (iq & 1));
+                    ++iq;
+                }
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    if (j0 + b >= w.tiles)
+                        break;
+                    ok = wait(slot_empty + n % C::kTiles, ((n / C::kTiles) & 1) ^ 1);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok)
+                        break;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        slots[(n % C::kTiles) * kAttnTile + 32 * i + lane] = at[4 * b + i];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, at[4 * b + i] >= 0);
+                        if (lane == i)
+                            mask[(n % kMaskDepth) * 4 + i] = bits;
+                    }
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(slot_full + n % C::kTiles);
+                    ++n;
                 }
             }
-            ++n;
-            c0 = c1;
-            a0 = a1;
-            c1 = c2;
-            e1 = e2;
         }
-        cp_async_wait<0>();
-        while (signalled < issued)
-            signal();
     } else {
         // --------------------------------------------------------------------- MMA
         constexpr int kK = 32 / C::kEb;                 // contraction elements of one MMA
@@ -671,7 +708,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             const AttnItem w = attn_item(p, item);
             for (int j = w.tile; j < w.tiles; ++j, ++n) {
                 const int st = (2 * n) % C::kStages, b = n & 1;
-                ok = wait(kv_full + st, ((2 * n) / C::kStages) & 1) &&
+                ok = (j != w.tile || wait(q_full + (iq & 1), (iq >> 1) & 1)) &&
+                     wait(kv_full + st, ((2 * n) / C::kStages) & 1) &&
                      wait(s_empty + b, ((n >> 1) & 1) ^ 1);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok)

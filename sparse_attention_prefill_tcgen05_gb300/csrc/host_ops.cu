@@ -317,6 +317,7 @@ int indexer_sparse_attention(indexer_attention_t a, const indexer_attention_io* 
             (io->q_row * 2) % 16 == 0 && (io->q_head * 2) % 16 == 0 &&
             (io->k_slot * kb) % 16 == 0 && (io->k_head * kb) % 16 == 0 &&
             (io->v_slot * kb) % 16 == 0 && (io->v_head * kb) % 16 == 0 &&
+            kb * io->k_slot <= UINT32_MAX && kb * io->v_slot <= UINT32_MAX &&
             (s.Hq == 1 || io->out_head >= s.D) && (a->p.rows == 1 || io->out_row >= s.D);
         if (!strides_ok || !io->q || !io->out || !io->sel || !io->compress_len ||
             (s.num_slots > 0 && (!io->k || !io->v)) || !is_aligned(io->q, 16) ||

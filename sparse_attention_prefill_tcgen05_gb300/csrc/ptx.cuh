@@ -62,6 +62,20 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity)
     return ok != 0;
 }
 
+// The same test without the wait: try_wait may suspend the thread for a while first.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // try_wait that lets the hardware suspend the thread until the phase completes
 // or `hint_ns` nanoseconds pass, instead of returning at once (a waiting warp
 // then takes no issue slots from the warps doing work).
@@ -497,7 +511,7 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const float (
         : "memory");
 }
 
-// Copy 16 (or 4) bytes from global to shared memory, or zeros where `ok` is false (the
+// Copy 16 bytes from global to shared memory, or zeros where `ok` is false (the
 // address is then not read).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok)
 {
@@ -506,10 +520,10 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool o
                  : "memory");
 }
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ok)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(ok ? 4 : 0)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src))
                  : "memory");
 }
 
