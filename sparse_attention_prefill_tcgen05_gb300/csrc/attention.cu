@@ -145,7 +145,7 @@ struct AttnCfg {
     static constexpr int kSlotTile = kAttnTile * 4;
     static constexpr int kMaskBytes = kMaskDepth * (16 + (kFp8 ? kAttnTile * 8 : 0));
     static constexpr int kMisc =
-        kMaskBytes + 2 * kGroups * 4 * 16 * 4 + (kFp8 ? 2 * NH * 4 : 0) + 8 * (3 * 8 + 2 * 8 + 2);
+        kMaskBytes + NH * 4 * 4 + 2 * NH * 4 + (kFp8 ? 2 * NH * 4 : 0) + 8 * (3 * 8 + 2 * 10 + 2);
     static constexpr int kFit = (kSmemLimit - kMisc - 2 * kPBytes - 2 * kQBytes) /
                                 (2 * kStage + kSlotTile);
     // Tiles held.  A warp fills the same stage of the ring every time and reads the same
@@ -153,7 +153,7 @@ struct AttnCfg {
     // phases early would pass at once).
     static constexpr int kTiles = kFit < 4 ? kFit : 4;
     static constexpr int kStages = 2 * kTiles;
-    static constexpr int kThreads = 32 * (kSoftmaxWarps + kStages + 2);
+    static constexpr int kThreads = 32 * (kSoftmaxWarps + 4 + kStages + 2);
     static constexpr int kSmem =
         kStages * kStage + 2 * kPBytes + 2 * kQBytes + kTiles * kSlotTile + kMisc;
     static constexpr int kSCols = kQRows;               // TMEM columns of a score tile
@@ -185,19 +185,32 @@ struct AttnItem {
     int tile, tiles;    // key tiles [tile, tiles) of this item
 };
 
+__device__ __forceinline__ int quotient(int n, const Divisor& d)
+{
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * d.mul) >> d.shift);
+}
+
+template <bool kOneLane = false>
 __device__ __forceinline__ AttnItem attn_item(const AttnParams& p, int item)
 {
     AttnItem w;
-    w.split = item % p.splits;
-    item /= p.splits;
-    w.ht = item % p.head_tiles;
-    item /= p.head_tiles;
-    w.g = item % p.Hkv;
-    w.t = item / p.Hkv;
-    // the shuffle tells the compiler that the count, and the loops over it, are uniform
-    w.n_sel = p.sel_count ? __shfl_sync(0xFFFFFFFFu,
-                                        max(0, min(p.num_sel, p.sel_count[w.t])), 0)
-                          : p.num_sel;
+    int q = quotient(item, p.by_splits);
+    w.split = item - q * p.splits;
+    item = q;
+    q = quotient(item, p.by_head_tiles);
+    w.ht = item - q * p.head_tiles;
+    item = q;
+    q = quotient(item, p.by_hkv);
+    w.g = item - q * p.Hkv;
+    item = q;
+    w.t = item;
+    w.n_sel = p.num_sel;
+    if (p.sel_count) {
+        w.n_sel = max(0, min(p.num_sel, p.sel_count[w.t]));
+        // (the shuffle tells the compiler that the count, and the loops over it, are uniform)
+        if (!kOneLane)
+            w.n_sel = __shfl_sync(0xFFFFFFFFu, w.n_sel, 0);
+    }
     const int all = ((w.n_sel << p.block_shift) + kAttnTile - 1) / kAttnTile;
     w.tile = w.split * p.split_tiles;
     w.tiles = min(all, w.tile + p.split_tiles);
@@ -252,6 +265,20 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi)
     return r;
 }
 
+// The rest of a wait that is not over at once.  Out of line: the roles' loops together have to
+// stay in the instruction cache (with every wait inlined a third of the fetches missed it).
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* ab,
+                                     uint32_t* status)
+{
+    if (mbar_wait(bar, parity, kWaitCycles, ab))
+        return true;
+    if (!*ab) {
+        *ab = 1;
+        atomicOr(status, kStatusTimeout);
+    }
+    return false;
+}
+
 template <int D, int NH, int MODE>
 __global__ void __launch_bounds__(AttnCfg<D, NH, MODE>::kThreads, 1)
 attention_tc_kernel(const __grid_constant__ AttnParams p)
@@ -265,9 +292,9 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
     uint8_t* qbuf = pbuf + 2 * C::kPBytes;
     int32_t* slots = reinterpret_cast<int32_t*>(qbuf + 2 * C::kQBytes);   // [kTiles][128]
     uint32_t* mask = reinterpret_cast<uint32_t*>(slots + C::kTiles * kAttnTile);   // [kMaskDepth][4]
-    float* exch_max = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(mask) + C::kMaskBytes);
-    float* exch_sum = exch_max + C::kGroups * 64;
-    float* qscale = exch_sum + C::kGroups * 64;                // [2][NH]
+    float* exch = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(mask) + C::kMaskBytes);
+    float* factor = exch + C::kGroups * 64;                    // [2][NH]: of an item's output
+    float* qscale = factor + 2 * NH;                           // [2][NH]
     uint64_t* bars = reinterpret_cast<uint64_t*>(qscale + (C::kFp8 ? 2 * NH : 0));
     uint64_t* kv_full = bars;
     uint64_t* kv_empty = kv_full + C::kStages;
@@ -281,7 +308,9 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
     uint64_t* p_empty = p_full + 2;
     uint64_t* o_full = p_empty + 2;
     uint64_t* o_empty = o_full + 2;
-    uint64_t* drained = o_empty + 2;
+    uint64_t* f_full = o_empty + 2;
+    uint64_t* f_empty = f_full + 2;
+    uint64_t* drained = f_empty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -304,14 +333,17 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             mbar_init(p_full + i, C::kSoftmaxWarps);
             mbar_init(p_empty + i, 1);
             mbar_init(o_full + i, 1);
-            mbar_init(o_empty + i, C::kSoftmaxWarps);
+            mbar_init(o_empty + i, 4);
+            mbar_init(f_full + i, C::kSoftmaxWarps);
+            mbar_init(f_empty + i, 4);
         }
         mbar_init(drained, 1);
         // the swizzled tiles need their 1024-byte boundaries
         *abort_flag = (smem_u32(sm) & 1023u) != 0;
         fence_mbar_init();
     }
-    constexpr int kSlotWarp = C::kSoftmaxWarps + C::kStages, kMmaWarp = kSlotWarp + 1;
+    constexpr int kGatherWarp = C::kSoftmaxWarps + 4;
+    constexpr int kSlotWarp = kGatherWarp + C::kStages, kMmaWarp = kSlotWarp + 1;
     if (warp == kMmaWarp) {
         tmem_alloc(tmem_slot, C::kTmem);
         tmem_relinquish();
@@ -329,13 +361,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
     const int total = p.rows * p.Hkv * p.head_tiles * p.splits;
     volatile int* ab = abort_flag;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (mbar_wait(bar, parity, kWaitCycles, ab))
-            return true;
-        if (!*ab) {
-            *ab = 1;
-            atomicOr(p.status, kStatusTimeout);
-        }
-        return false;
+        return mbar_try_wait(bar, parity) || wait_on(bar, parity, ab, p.status);
     };
 
     if (warp < C::kSoftmaxWarps) {
@@ -344,13 +370,11 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         const int wg = warp / 4, quad = warp & 3, key = 32 * quad + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
         const int bar_id = 1 + wg;
-        float* xmax = exch_max + wg * 64;
-        float* xsum = exch_sum + wg * 64;
+        float* x4 = exch + wg * 64;                  // [4 quadrants][16 heads]
         bool bad = false, out_of_here = false;
         int n = 0, iq = 0;
         for (int item = blockIdx.x; item < total && !out_of_here; item += gridDim.x) {
             const AttnItem w = attn_item(p, item);
-            const int head0 = w.ht * NH + 16 * wg;      // first head of the group for this thread
             float m[16], l[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -390,8 +414,10 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 if (first || bar_any(over > 8.0f || bad, bar_id, 128)) {
                     float v[16];
                     const float mine = reduce16<true>(x);
+                    if (first)
+                        bar_all(true, bar_id, 128);  // the last item's sums have been read
                     if ((lane & 1) == 0)
-                        xmax[quad * 16 + lane / 2] = mine;
+                        x4[quad * 16 + lane / 2] = mine;
                     if (!bar_all(!bad, bar_id, 128)) {
                         out_of_here = true;
                         break;
@@ -400,8 +426,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float mn =
-                            fmaxf(fmaxf(fmaxf(m[i], xmax[i]), fmaxf(xmax[16 + i], xmax[32 + i])),
-                                  xmax[48 + i]);
+                            fmaxf(fmaxf(fmaxf(m[i], x4[i]), fmaxf(x4[16 + i], x4[32 + i])),
+                                  x4[48 + i]);
                         f[i] = ex2(m[i] - mn);
                         m[i] = mn;
                         l[i] *= f[i];
@@ -443,57 +469,106 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             }
             if (out_of_here)
                 break;
-            const bool some = w.tiles > w.tile;
-            float o[16];
-            float total_l[16];
+            if (w.tiles == w.tile)
+                continue;
+            // The item's sums; the epilogue's warps get 1 / sum (the output waits for the last
+            // product, the next item's first scores do not).
+            const float mine = reduce16<false>(l);
+            if (!bar_all(!bad, bar_id, 128))             // the last maxima have been read
+                break;
+            if ((lane & 1) == 0)
+                x4[quad * 16 + lane / 2] = mine;
+            bad |= !wait(f_empty + (iq & 1), ((iq >> 1) & 1) ^ 1);
+            if (!bar_all(!bad, bar_id, 128))
+                break;
+            if (quad == 0) {
+                const int i = lane & 15;
+                float mi = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                o[i] = 0.0f;
-                total_l[i] = 0.0f;
+                for (int k = 0; k < 16; ++k)
+                    mi = i == k ? m[k] : mi;
+                const float li = (x4[i] + x4[16 + i]) + (x4[32 + i] + x4[48 + i]);
+                if (lane < 16) {
+                    const int h = w.ht * NH + 16 * wg + i;
+                    factor[(iq & 1) * NH + 16 * wg + i] =
+                        p.splits > 1 ? 1.0f : li == 0.0f ? 0.0f : 1.0f / li;
+                    if (p.splits > 1)
+                        reinterpret_cast<float2*>(p.part_ml)[(int64_t)item * NH + 16 * wg + i] =
+                            make_float2(mi, li);
+                    else if (p.lse && h < p.group)
+                        p.lse[(int64_t)w.t * p.Hq + w.g * p.group + h] =
+                            (mi + log2f(li)) * 0.693147180559945309f;
+                }
             }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(f_full + (iq & 1));
+            ++iq;
+        }
+    } else if (warp < kGatherWarp) {
+        // --------------------------------------------------------------- epilogue
+        // Thread = one element (of D) of NH heads.
+        const int quad = warp & 3, dim = 32 * quad + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+        int iq = 0;
+        bool ok = true;
+        for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+            const AttnItem w = attn_item(p, item);
+            const bool some = w.tiles > w.tile;
+            uint8_t* out = p.out + w.t * p.out_row + (int64_t)(w.g * p.group + w.ht * NH) * p.out_head;
+            const int heads = min(NH, p.group - w.ht * NH);
             if (some) {
-                const float mine = reduce16<false>(l);
-                if ((lane & 1) == 0)
-                    xsum[quad * 16 + lane / 2] = mine;
-                bad |= !wait(o_full + (iq & 1), (iq >> 1) & 1);
-                if (!bar_all(!bad, bar_id, 128))
+                ok = wait(f_full + (iq & 1), (iq >> 1) & 1) && wait(o_full + (iq & 1), (iq >> 1) & 1);
+                if (!__all_sync(0xFFFFFFFFu, ok))
                     break;
                 tc_fence_after();
-                tmem_ld_32x32b_x16(tmem_o + lanes + (iq & 1) * C::kOCols + 16 * wg, o);
-                tmem_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(o_empty + (iq & 1));
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    total_l[i] = (xsum[i] + xsum[16 + i]) + (xsum[32 + i] + xsum[48 + i]);
-                ++iq;
             }
-            // thread = one element (of D) x 16 heads
-            if (p.splits == 1) {
-                uint8_t* out = p.out + w.t * p.out_row + (int64_t)w.g * p.group * p.out_head;
-                float* lse = p.lse ? p.lse + (int64_t)w.t * p.Hq + w.g * p.group : nullptr;
+            const bool parts = p.splits > 1, write = D == 128 || dim < D;
+            const int count = parts ? NH : heads;
+            float* part = p.part_o + (int64_t)item * NH * D + dim;
+#pragma unroll 1
+            for (int h0 = 0; h0 < count; h0 += 16) {
+                float o[16] = {};
+                if (some) {
+                    tmem_ld_32x32b_x16(tmem_o + lanes + (iq & 1) * C::kOCols + h0, o);
+                    tmem_wait_ld();
+                }
+                if (parts) {
+                    float* to = part + h0 * D;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int h = head0 + i;
-                    if (h < p.group) {
-                        if (D == 128 || key < D)
-                            reinterpret_cast<T*>(out + h * p.out_head)[key] =
-                                static_cast<T>(total_l[i] == 0.0f ? 0.0f : o[i] / total_l[i]);
-                        if (lse && key == i)
-                            lse[h] = (m[i] + log2f(total_l[i])) * 0.693147180559945309f;
+                    for (int i = 0; i < 16; ++i)
+                        if (write)
+                            to[i * D] = o[i];
+                } else {
+                    const float* f = factor + (iq & 1) * NH + h0;
+                    uint8_t* to = out + h0 * p.out_head + 2 * dim;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float v = f[i] != 0.0f ? o[i] * f[i] : 0.0f;
+                        if (write && h0 + i < heads)
+                            *reinterpret_cast<T*>(to) = static_cast<T>(some ? v : 0.0f);
+                        to += p.out_head;
                     }
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int64_t at = (int64_t)item * NH + 16 * wg + i;
-                    if (D == 128 || key < D)
-                        p.part_o[at * D + key] = o[i];
-                    if (key == i)
-                        reinterpret_cast<float2*>(p.part_ml)[at] = make_float2(m[i], total_l[i]);
+            }
+            if (!some) {
+#pragma unroll 1
+                for (int h = dim; h < count; h += kAttnTile) {
+                    if (parts)
+                        reinterpret_cast<float2*>(p.part_ml)[(int64_t)item * NH + h] =
+                            make_float2(-3.0e38f, 0.0f);
+                    else if (p.lse)
+                        p.lse[(int64_t)w.t * p.Hq + w.g * p.group + w.ht * NH + h] = -INFINITY;
                 }
+            }
+            if (some) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(o_empty + (iq & 1));
+                    mbar_arrive(f_empty + (iq & 1));
+                }
+                ++iq;
             }
         }
     } else if (warp < kSlotWarp) {
@@ -501,7 +576,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         // Warp i fills stage i of the ring: it waits for the stage, copies the 128 vectors
         // (zeros for keys that are none), waits for its own copies and signals.  The other
         // stages' warps keep the memory system busy meanwhile.
-        const int pw = warp - C::kSoftmaxWarps;
+        const int pw = warp - kGatherWarp;
         constexpr int kPerRow = C::kRow / 16;            // copies of 16 bytes a vector takes
         constexpr int kSpans = 32 / kPerRow;             // vectors copied at a time,
         constexpr int kSpan = kAttnTile / kSpans;        // kSpan keys apart
@@ -509,158 +584,168 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         const uint32_t stage = smem_u32(stages + pw * C::kStage) + row0 * C::kAtom +
                                (chunk * 16 / C::kAtom) * (kAttnTile * C::kAtom) +
                                (chunk * 16) % C::kAtom;
-        const uint32_t k_slot = static_cast<uint32_t>(p.k_slot);
-        const uint32_t v_slot = static_cast<uint32_t>(p.v_slot);
-        int n = 0, st = 0, uses = 0;             // st: the tile's place in the ring
+        const bool is_v = pw & 1;
+        const uint8_t* kv = (is_v ? p.v : p.k) + chunk * 16;
+        const int64_t kv_head = is_v ? p.v_head : p.k_head;
+        const uint32_t kv_slot = static_cast<uint32_t>(is_v ? p.v_slot : p.k_slot);
+        const int sl = pw / 2;                   // the pair's place in the ring of tiles
+        int n = 0, uses = 0;
         bool ok = true;
         for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
             const AttnItem w = attn_item(p, item);
-            for (int j = w.tile; j < w.tiles && ok; ++j, ++n) {
+            const int end = n + max(0, w.tiles - w.tile);
+            const uint8_t* src = kv + w.g * kv_head;
+            // the pair's tiles of the item
+            for (int m = uses * C::kTiles + sl; m < end; m += C::kTiles) {
+                ok = wait(kv_empty + pw, (uses & 1) ^ 1) && wait(slot_full + sl, uses & 1);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok)
+                    break;
+                const int32_t* rows = slots + sl * kAttnTile + row0;
+                const uint4 bits = *reinterpret_cast<const uint4*>(mask + (m % kMaskDepth) * 4);
+                if ((bits.x & bits.y & bits.z & bits.w) == 0xFFFFFFFFu) {
+#pragma unroll 1
+                    for (int i = 0; i < kSpan; i += 8) {
+                        const int4 s0 = *reinterpret_cast<const int4*>(rows + i);
+                        const int4 s1 = *reinterpret_cast<const int4*>(rows + i + 4);
+                        const int32_t s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (2 * st + kv == pw && ok) {
-                        ok = wait(kv_empty + pw, (uses & 1) ^ 1);
-                        const int sl = pw / 2;
-                        ok = ok && wait(slot_full + sl, uses & 1);
-                        ok = __all_sync(0xFFFFFFFFu, ok);
-                        if (ok) {
-                            const uint8_t* src = (kv == 0 ? p.k + w.g * p.k_head
-                                                          : p.v + w.g * p.v_head) + chunk * 16;
-                            const uint32_t stride = kv == 0 ? k_slot : v_slot;
-                            const int32_t* rows = slots + sl * kAttnTile + row0;
-                            const uint4 bits =
-                                *reinterpret_cast<const uint4*>(mask + (n % kMaskDepth) * 4);
-                            if ((bits.x & bits.y & bits.z & bits.w) == 0xFFFFFFFFu) {
-#pragma unroll 4
-                                for (int i = 0; i < kSpan; i += 8) {
-                                    const int4 s0 = *reinterpret_cast<const int4*>(rows + i);
-                                    const int4 s1 = *reinterpret_cast<const int4*>(rows + i + 4);
-                                    const int32_t s[8] = {s0.x, s0.y, s0.z, s0.w,
-                                                          s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-                                    for (int k = 0; k < 8; ++k)
-                                        cp_async16((stage + i * C::kAtom) ^
-                                                       swizzle_of<C::kAtom>(k * C::kAtom),
-                                                   src + (uint64_t)(uint32_t)s[k] * stride);
-                                }
-                            } else {
-                                for (int i = 0; i < kSpan; ++i) {
-                                    const int32_t s = rows[i];
-                                    cp_async16((stage + i / 8 * 8 * C::kAtom) ^
-                                                   swizzle_of<C::kAtom>(i % 8 * C::kAtom),
-                                               src + (uint64_t)(uint32_t)max(s, 0) * stride, s >= 0);
-                                }
-                            }
-                            __syncwarp();
-                            if (lane == 0)
-                                mbar_arrive(slot_empty + sl);
-                        }
-                        cp_async_commit();
-                        cp_async_wait<0>();
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (ok && lane == 0)
-                            mbar_arrive(kv_full + pw);
-                        ++uses;
+                        for (int k = 0; k < 8; ++k)
+                            cp_async16((stage + i * C::kAtom) ^ swizzle_of<C::kAtom>(k * C::kAtom),
+                                       src + (uint64_t)(uint32_t)s[k] * kv_slot);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < kSpan; ++i) {
+                        const int32_t s = rows[i];
+                        cp_async16((stage + i / 8 * 8 * C::kAtom) ^
+                                       swizzle_of<C::kAtom>(i % 8 * C::kAtom),
+                                   src + (uint64_t)(uint32_t)max(s, 0) * kv_slot, s >= 0);
                     }
                 }
-                st = st + 1 == C::kTiles ? 0 : st + 1;
+                cp_async_commit();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(slot_empty + sl);
+                cp_async_wait<0>();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(kv_full + pw);
+                ++uses;
             }
+            n = end;
         }
     } else if (warp == kSlotWarp) {
         // ----------------------------------------------------------------- slots
-        // Cache slots of the selected keys, four tiles at a time so that the reads of the
-        // lists, and then of the page table, are in flight together.
-        int n = 0, iq = 0;
+        // Cache slots of the selected keys, four keys of a tile per lane.  The list entries are
+        // read two tiles ahead and their pages one tile ahead, over the items' ends.
+        struct Tile {
+            int item, t, g, ht, base, r, len, tile;      // item < 0: no tile
+        };
+        Tile d1{-1}, d2{-1};                             // whose pages, whose entries are read
+        int32_t entry[4] = {}, key[4] = {}, page[4] = {};
+        AttnItem w;
+        w.tile = w.tiles = w.n_sel = 0;
+        int next_item = blockIdx.x, r = 0, base = 0, len = 0;
+        int n = 0, iq = 0, last_item = -1, drain = 0;
         bool ok = true;
-        for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-            const AttnItem w = attn_item(p, item);
-            const int r = request_of(p.row_begin, p.num_requests, w.t);
-            const int base = p.key_begin[r];
-            const int len = min(p.clen[w.t], p.key_begin[r + 1] - base);
-            const int32_t* sel = p.sel + w.t * p.ld_sel;
-            const int32_t* table = p.table + r * p.ld_table;
-            if (w.tile >= w.tiles)
+        while (ok && drain < 3) {
+            // tile n: slots from its pages
+            int32_t slot[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t at = (int64_t)page[i] * p.page + key[i];
+                slot[i] = page[i] >= 0 && at < p.num_slots ? static_cast<int32_t>(at) : -1;
+            }
+            const Tile d0 = d1;
+            // tile n + 1: keys and pages from its entries
+            d1 = d2;
+            if (d1.item >= 0) {
+                const int32_t* table = p.table + d1.r * p.ld_table;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int pos = d1.tile * kAttnTile + 32 * i + lane;
+                    const int64_t k = ((int64_t)entry[i] << p.block_shift) +
+                                      (pos & ((1 << p.block_shift) - 1));
+                    const bool in = entry[i] >= 0 && k < d1.len;
+                    key[i] = static_cast<int32_t>(k);
+                    page[i] = in ? 0 : -1;
+                    if (p.page == 0) {
+                        key[i] += d1.base;
+                    } else if (in) {
+                        const int pg = quotient(key[i], p.by_page);
+                        page[i] = table[pg];
+                        key[i] -= pg * p.page;
+                    }
+                }
+            }
+            // tile n + 2: entries
+            while (w.tile >= w.tiles && next_item < total) {
+                w = attn_item(p, next_item);
+                r = request_of(p.row_begin, p.num_requests, w.t);
+                base = p.key_begin[r];
+                len = min(p.clen[w.t], p.key_begin[r + 1] - base);
+                next_item += gridDim.x;
+            }
+            d2 = Tile{-1};
+            if (w.tile < w.tiles) {
+                d2 = Tile{next_item, w.t, w.g, w.ht, base, r, len, w.tile};
+                const int32_t* sel = p.sel + w.t * p.ld_sel;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = (w.tile * kAttnTile + 32 * i + lane) >> p.block_shift;
+                    entry[i] = at < w.n_sel ? sel[at] : -1;
+                }
+                ++w.tile;
+            }
+            drain = d2.item < 0 ? drain + 1 : 0;
+            if (d0.item < 0)
                 continue;
-            ok = wait(q_empty + (iq & 1), ((iq >> 1) & 1) ^ 1);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok)
-                break;
-            {
+            const bool new_item = d0.item != last_item;
+            if (new_item) {
+                // the item's queries, before its first tile
+                ok = wait(q_empty + (iq & 1), ((iq >> 1) & 1) ^ 1);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok)
+                    break;
                 constexpr int kPerRow = C::kRow / 16;
-                const uint8_t* q = p.q + w.t * p.q_row + (int64_t)w.g * p.group * p.q_head;
+                const uint8_t* q = p.q + d0.t * p.q_row + (int64_t)d0.g * p.group * p.q_head;
                 const uint32_t dst = smem_u32(qbuf + (iq & 1) * C::kQBytes);
-#pragma unroll 4
+#pragma unroll 1
                 for (int i = lane; i < C::kQBytes / 16; i += 32) {
-                    const int h = i / kPerRow, c = i % kPerRow;
-                    const bool in = w.ht * NH + h < p.group;
-                    const uint32_t off = (c / 8) * (NH * 128) + h * 128 + (c % 8) * 16;
+                    const int h = i / kPerRow, c16 = i % kPerRow;
+                    const bool in = d0.ht * NH + h < p.group;
+                    const uint32_t off = (c16 / 8) * (NH * 128) + h * 128 + (c16 % 8) * 16;
                     cp_async16(dst + swizzled<128>(off),
-                               in ? q + (int64_t)(w.ht * NH + h) * p.q_head + c * 16 : q, in);
+                               in ? q + (int64_t)(d0.ht * NH + h) * p.q_head + c16 * 16 : q, in);
                 }
                 cp_async_commit();
             }
-            for (int j0 = w.tile; j0 < w.tiles && ok; j0 += 4) {
-                int32_t at[16];                  // list entry, then key, then slot
+            ok = wait(slot_empty + n % C::kTiles, ((n / C::kTiles) & 1) ^ 1);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok)
+                break;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int pos = j0 * kAttnTile + 32 * i + lane;
-                    const int e = pos >> p.block_shift;
-                    at[i] = j0 + i / 4 < w.tiles && e < w.n_sel ? sel[e] : -1;
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int pos = j0 * kAttnTile + 32 * i + lane;
-                    const int64_t key = ((int64_t)at[i] << p.block_shift) +
-                                        (pos & ((1 << p.block_shift) - 1));
-                    at[i] = at[i] >= 0 && key < len ? static_cast<int32_t>(key) : -1;
-                }
-                if (p.page == 0) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        at[i] = at[i] >= 0 && base + (int64_t)at[i] < p.num_slots ? base + at[i] : -1;
-                } else {
-                    int32_t page[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        page[i] = at[i] >= 0 ? table[at[i] / p.page] : -1;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int64_t slot = (int64_t)page[i] * p.page + at[i] % p.page;
-                        at[i] = page[i] >= 0 && slot < p.num_slots ? static_cast<int32_t>(slot) : -1;
-                    }
-                }
-                if (j0 == w.tile) {
-                    cp_async_wait<0>();
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(q_full + (iq & 1));
-                    ++iq;
-                }
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if (j0 + b >= w.tiles)
-                        break;
-                    ok = wait(slot_empty + n % C::kTiles, ((n / C::kTiles) & 1) ^ 1);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (!ok)
-                        break;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        slots[(n % C::kTiles) * kAttnTile + 32 * i + lane] = at[4 * b + i];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, at[4 * b + i] >= 0);
-                        if (lane == i)
-                            mask[(n % kMaskDepth) * 4 + i] = bits;
-                    }
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(slot_full + n % C::kTiles);
-                    ++n;
-                }
+            for (int i = 0; i < 4; ++i) {
+                slots[(n % C::kTiles) * kAttnTile + 32 * i + lane] = slot[i];
+                const uint32_t bits = __ballot_sync(0xFFFFFFFFu, slot[i] >= 0);
+                if (lane == i)
+                    mask[(n % kMaskDepth) * 4 + i] = bits;
             }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(slot_full + n % C::kTiles);
+            if (new_item) {
+                cp_async_wait<0>();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(q_full + (iq & 1));
+                ++iq;
+                last_item = d0.item;
+            }
+            ++n;
         }
     } else {
         // --------------------------------------------------------------------- MMA
@@ -669,87 +754,94 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             idesc_dense(128, C::kQRows, MODE == kModeBf16 ? 1 : 0, false, false);
         constexpr uint32_t idesc_o =
             idesc_dense(128, C::kOCols, MODE == kModeBf16 ? 1 : 0, true, true);
-        struct Pending {
-            bool any, first, last;
-            int n, iq;
-        } pv{false, false, false, 0, 0};
-        auto product = [&]() {                          // O += P V of a tile
-            const int st = (2 * pv.n + 1) % C::kStages, b = pv.n & 1;
-            bool ok = wait(kv_full + st, ((2 * pv.n + 1) / C::kStages) & 1) &&
-                      wait(p_full + b, (pv.n >> 1) & 1) &&
-                      (!pv.first || wait(o_empty + (pv.iq & 1), ((pv.iq >> 1) & 1) ^ 1));
-            if (!__all_sync(0xFFFFFFFFu, ok))
-                return false;
-            tc_fence_after();
-            if (elect_one()) {
-                // v rows are keys: both operands are read along their rows.  D = 64 takes the
-                // same 64 elements for both halves of the 128 output rows.
-                constexpr uint32_t lbo = D * C::kEb > C::kAtom ? kAttnTile * C::kAtom : 0;
-                const uint64_t a0 = smem_desc(smem_u32(stages + st * C::kStage), C::kAtom, lbo,
-                                              8 * C::kAtom);
-                const uint64_t b0 = smem_desc(smem_u32(pbuf + b * C::kPBytes), C::kPRow, 0,
-                                              8 * C::kPRow);
+        // One elected lane waits and issues.
+        if (elect_one()) {
+            struct Pending {
+                bool any, first, last;
+                int n, iq;
+            } pv{false, false, false, 0, 0};
+            const uint64_t k_desc = smem_desc(smem_u32(stages), C::kAtom, 16, 8 * C::kAtom);
+            // v rows are keys: both operands of the second product are read along their rows.
+            // D = 64 takes the same 64 elements for both halves of the 128 output rows.
+            constexpr uint32_t lbo = C::kAtoms > 1 ? kAttnTile * C::kAtom : 0;
+            const uint64_t v_desc = smem_desc(smem_u32(stages), C::kAtom, lbo, 8 * C::kAtom);
+            const uint64_t q_desc = smem_desc(smem_u32(qbuf), C::kAtom, 16, 8 * C::kAtom);
+            const uint64_t p_desc = smem_desc(smem_u32(pbuf), C::kPRow, 0, 8 * C::kPRow);
+            int vst = 0;                                // the pending product's stage
+            auto product = [&]() {                      // O += P V of a tile
+                const int b = pv.n & 1;
+                if (!(wait(kv_full + vst, (pv.n / C::kTiles) & 1) &&
+                      (!pv.first || wait(o_empty + (pv.iq & 1), ((pv.iq >> 1) & 1) ^ 1)) &&
+                      wait(p_full + b, (pv.n >> 1) & 1)))
+                    return false;
+                tc_fence_after();
+                const uint64_t a0 = v_desc + vst * (C::kStage / 16);
+                const uint64_t b0 = p_desc + b * (C::kPBytes / 16);
                 const uint32_t d = tmem_o + (pv.iq & 1) * C::kOCols;
 #pragma unroll
                 for (int k = 0; k < kAttnTile / kK; ++k)
                     mma_f16(d, a0 + k * (kK * C::kAtom / 16), b0 + k * (kK * C::kPRow / 16),
                             idesc_o, !pv.first || k > 0);
-                mma_commit(kv_empty + st);
+                mma_commit(kv_empty + vst);
                 mma_commit(p_empty + b);
                 if (pv.last)
                     mma_commit(o_full + (pv.iq & 1));
+                return true;
+            };
+            int n = 0, iq = 0, st = 0;                  // st: the k stage of tile n
+            int item = blockIdx.x, j = 0, first = 0, end = 0;
+            if (item < total) {
+                const AttnItem w = attn_item<true>(p, item);
+                first = j = w.tile;
+                end = w.tiles;
             }
-            __syncwarp();
-            return true;
-        };
-        int n = 0, iq = 0;
-        bool ok = true;
-        for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-            const AttnItem w = attn_item(p, item);
-            for (int j = w.tile; j < w.tiles; ++j, ++n) {
-                const int st = (2 * n) % C::kStages, b = n & 1;
-                ok = (j != w.tile || wait(q_full + (iq & 1), (iq >> 1) & 1)) &&
-                     wait(kv_full + st, ((2 * n) / C::kStages) & 1) &&
-                     wait(s_empty + b, ((n >> 1) & 1) ^ 1);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok)
-                    break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t a = smem_u32(stages + st * C::kStage);
-                    const uint32_t q = smem_u32(qbuf + (iq & 1) * C::kQBytes);
+            while (true) {
+                while (j >= end && (item += gridDim.x) < total) {
+                    const AttnItem w = attn_item<true>(p, item);
+                    first = j = w.tile;
+                    end = w.tiles;
+                }
+                const bool more = j < end;
+                const Pending next{more, j == first, j + 1 == end, n, iq};
+                const int next_st = st + 1;
+                if (more) {                             // S = Q K of tile n
+                    const int b = n & 1;
+                    if (!((!next.first || wait(q_full + (iq & 1), (iq >> 1) & 1)) &&
+                          wait(kv_full + st, (n / C::kTiles) & 1) &&
+                          wait(s_empty + b, ((n >> 1) & 1) ^ 1)))
+                        break;
+                    tc_fence_after();
+                    const uint64_t a0 = k_desc + st * (C::kStage / 16);
+                    const uint64_t b0 = q_desc + (iq & 1) * (C::kQBytes / 16);
 #pragma unroll
                     for (int k = 0; k < D / kK; ++k) {
                         const int atom = k * 32 / C::kAtom, in = (k * 32) % C::kAtom;
                         mma_f16(tmem_s + b * C::kSCols,
-                                smem_desc(a + atom * (kAttnTile * C::kAtom) + in, C::kAtom, 16,
-                                          8 * C::kAtom),
-                                smem_desc(q + atom * (C::kQRows * C::kAtom) + in, C::kAtom, 16,
-                                          8 * C::kAtom),
-                                idesc_s, k > 0);
+                                a0 + (atom * (kAttnTile * C::kAtom) + in) / 16,
+                                b0 + (atom * (C::kQRows * C::kAtom) + in) / 16, idesc_s, k > 0);
                     }
-                    mma_commit(kv_empty + st);
                     mma_commit(s_full + b);
-                    if (j + 1 == w.tiles)
+                    mma_commit(kv_empty + st);
+                    if (next.last)
                         mma_commit(q_empty + (iq & 1));
+                    iq += next.last;
+                    ++j;
+                    ++n;
+                    st = st + 2 == C::kStages ? 0 : st + 2;
                 }
-                __syncwarp();
-                if (pv.any && !product()) {
-                    ok = false;
+                if (pv.any && !product())
                     break;
-                }
-                pv = Pending{true, j == w.tile, j + 1 == w.tiles, n, iq};
+                if (!more)
+                    break;
+                pv = next;
+                vst = next_st;
             }
-            iq += w.tiles > w.tile;
-        }
-        if (ok && pv.any)
-            product();
-        // what was issued, and its arrivals, end before the memory goes
-        if (elect_one())
+            // what was issued, and its arrivals, end before the memory goes
             mma_commit(drained);
+            volatile int never = 0;
+            mbar_wait(drained, 0, kWaitCycles, &never);
+        }
         __syncwarp();
-        volatile int never = 0;
-        mbar_wait(drained, 0, kWaitCycles, &never);
     }
     __syncthreads();
     if (warp == kMmaWarp) {

@@ -264,6 +264,7 @@ int indexer_attention_create(indexer_plan_t plan, const indexer_attention_spec* 
     p.num_sel = s->num_sel;
     p.num_slots = s->num_slots;
     p.page = s->page_size;
+    p.by_page = divisor(std::max(1, s->page_size));
     p.num_requests = v.R;
     std::copy(v.row_begin, v.row_begin + v.R + 1, p.row_begin);
     std::copy(v.key_begin, v.key_begin + v.R + 1, p.key_begin);
@@ -291,6 +292,9 @@ int indexer_attention_create(indexer_plan_t plan, const indexer_attention_spec* 
             p.split_tiles = static_cast<int32_t>(per);
         }
     }
+    p.by_splits = divisor(p.splits);
+    p.by_head_tiles = divisor(p.head_tiles);
+    p.by_hkv = divisor(p.Hkv);
     // status word, then the parts of split rows
     a->part_floats = p.splits > 1 ? (size_t)(items * p.splits) * nh : 0;
     a->ws_bytes = 256 + a->part_floats * (s->D + 2) * sizeof(float);

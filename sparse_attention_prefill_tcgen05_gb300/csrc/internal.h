@@ -381,6 +381,20 @@ cudaError_t launch_page_slots(const PageSlotParams& p, cudaStream_t st);
 // Attention over the selected keys.  A work item is (row, key/value head, tile of query
 // heads, split of the row's key tiles of kAttnTile keys).
 constexpr int kAttnTile = 128;
+// Division of numbers below 2^31 by a constant of the call: n / d = (n * mul) >> shift with
+// mul = ceil(2^shift / d), shift = 31 + ceil(log2 d).
+struct Divisor {
+    uint32_t mul;
+    int32_t shift;
+    int32_t d;
+};
+inline Divisor divisor(int32_t d)
+{
+    int l = 0;
+    while ((1ll << l) < d)
+        ++l;
+    return Divisor{static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), 31 + l, d};
+}
 struct AttnParams {
     const uint8_t* q;            // byte strides
     const uint8_t* k;
@@ -406,6 +420,7 @@ struct AttnParams {
     int32_t num_slots;
     int32_t page;                // 0: packed keys
     int32_t splits;              // splits per row
+    Divisor by_page, by_splits, by_head_tiles, by_hkv;
     int32_t split_tiles;         // key tiles per split
     int32_t num_requests;
     int32_t row_begin[kMaxRequests + 1];
