@@ -116,11 +116,6 @@ attention_kernel(const __grid_constant__ AttnParams p)
 // Modes: k and v of q's type (bf16 or fp16), or e4m3 caches under bf16 or fp16 queries.
 constexpr int kModeBf16 = 0, kModeFp16 = 1, kModeFp8Bf16 = 2, kModeFp8Fp16 = 3;
 
-// Tiles whose validity bits (and scales) are held for the softmax.  No barrier guards them:
-// with d tiles in the ring of stages (d <= 4) the bits of tile n + 8 are written after the slots
-// of tile n + 8 - d were read, thus after a v stage came free of tile n + 8 - 2 d >= n, whose
-// weights were complete.
-constexpr int kMaskDepth = 8;
 constexpr long long kWaitCycles = 4000000000LL;   // about two seconds
 constexpr int kSmemLimit = 232448;
 
@@ -138,34 +133,37 @@ struct AttnCfg {
     static constexpr int kQBytes = kQRows * kRow;
     static constexpr int kPRow = NH * kPTerms * kEb;    // 2 NH
     static constexpr int kPBytes = kAttnTile * kPRow;
-    static constexpr int kGroups = NH / 16;             // softmax warpgroups, 16 heads each
-    static constexpr int kSoftmaxWarps = 4 * kGroups;
-    
-    // at most four tiles of stages, and the slots of as many tiles
-    static constexpr int kSlotTile = kAttnTile * 4;
-    static constexpr int kMaskBytes = kMaskDepth * (16 + (kFp8 ? kAttnTile * 8 : 0));
-    static constexpr int kMisc =
-        kMaskBytes + NH * 4 * 4 + 2 * NH * 4 + (kFp8 ? 2 * NH * 4 : 0) + 8 * (3 * 8 + 2 * 10 + 2);
-    static constexpr int kFit = (kSmemLimit - kMisc - 2 * kPBytes - 2 * kQBytes) /
-                                (2 * kStage + kSlotTile);
-    // Tiles held.  A warp fills the same stage of the ring every time and reads the same
-    // slot buffer, so it sees every phase of the barriers it waits on (a parity wait two
-    // phases early would pass at once).
-    static constexpr int kTiles = kFit < 4 ? kFit : 4;
-    static constexpr int kStages = 2 * kTiles;
-    static constexpr int kThreads = 32 * (kSoftmaxWarps + 4 + kStages + 2);
-    static constexpr int kSmem =
-        kStages * kStage + 2 * kPBytes + 2 * kQBytes + kTiles * kSlotTile + kMisc;
+    // Two softmax warpgroups.  Up to 32 heads they take alternate tiles of an item, each with
+    // an output accumulator, running maximum and sum of its own (joined by the epilogue): a
+    // tile's chain of waits, exponentials and stores then overlaps the next tile's.  64 heads
+    // are shared between them, 32 each.
+    static constexpr bool kAlternate = NH <= 32;
+    static constexpr int kHeads = NH < 32 ? NH : 32;    // heads of a softmax thread
+    static constexpr int kTileWarps = kAlternate ? 4 : 8;   // softmax warps that take a tile
+    static constexpr int kAccs = kAlternate ? 2 : 1;    // accumulators of an item
     static constexpr int kSCols = kQRows;               // TMEM columns of a score tile
-    static constexpr int kOCols = NH * kPTerms;
-    static constexpr int kCols = 2 * (kSCols + kOCols);
-    static constexpr int kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+    static constexpr int kOCols = NH * kPTerms;         // of an accumulator
+    static constexpr int kCols = 2 * kSCols + 2 * kAccs * kOCols;
+    static constexpr int kTmem = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+    // Shared memory after the stages, the weights and the queries.
+    static constexpr int kStats = 2 * 4 * kHeads * 4;   // sums by warpgroup and quadrant
+    static constexpr int kMax = 2 * kHeads * 4;         // maxima by warpgroup
+    static constexpr int kQScale = kFp8 ? 2 * NH * 4 : 0;
+    static constexpr int kKeyInfo = kAttnTile * (kFp8 ? 9 : 1);   // of a tile, 2 kTiles of them
+    static constexpr int kFixed = kStats + kMax + kQScale + 2 * kPBytes + 2 * kQBytes + 8 * 20;
+    static constexpr int kFit =
+        (kSmemLimit - kFixed) / (2 * kStage + 2 * kKeyInfo + 8 * 4);
+    static constexpr int kTiles = kFit < 4 ? kFit : 4;  // tiles in the ring
+    static constexpr int kStages = 2 * kTiles;          // and as many warps that fill them
+    static constexpr int kSmem = kFixed + kTiles * (2 * kStage + 2 * kKeyInfo + 8 * 4);
+    static constexpr int kGatherWarp = 8 + 4, kQueryWarp = kGatherWarp + kStages;
+    static constexpr int kMmaWarp = kQueryWarp + 1, kThreads = 32 * (kMmaWarp + 1);
     static_assert(kCols <= 512 && kTiles >= 2 && kSmem <= kSmemLimit, "tile does not fit");
 };
 
 // Byte offset in a tile of `W`-byte rows as the W-byte swizzle places it.
 template <int W>
-__device__ __forceinline__ uint32_t swizzled(uint32_t off)
+__device__ __forceinline__ constexpr uint32_t swizzled(uint32_t off)
 {
     return off ^ (((off >> 7) & (W / 16 - 1)) << 4);
 }
@@ -202,8 +200,7 @@ __device__ __forceinline__ AttnItem attn_item(const AttnParams& p, int item)
     item = q;
     q = quotient(item, p.by_hkv);
     w.g = item - q * p.Hkv;
-    item = q;
-    w.t = item;
+    w.t = q;
     w.n_sel = p.num_sel;
     if (p.sel_count) {
         w.n_sel = max(0, min(p.num_sel, p.sel_count[w.t]));
@@ -213,13 +210,13 @@ __device__ __forceinline__ AttnItem attn_item(const AttnParams& p, int item)
     }
     const int all = ((w.n_sel << p.block_shift) + kAttnTile - 1) / kAttnTile;
     w.tile = w.split * p.split_tiles;
-    w.tiles = min(all, w.tile + p.split_tiles);
+    w.tiles = max(w.tile, min(all, w.tile + p.split_tiles));
     return w;
 }
 
 // 16 values of every lane, combined over the warp: lane i ends with value i / 2.
 template <bool kMax>
-__device__ __forceinline__ float reduce16(const float (&v)[16])
+__device__ __forceinline__ float reduce16(const float* v)
 {
     const int lane = threadIdx.x & 31;
     float a[8], b[4], c[2];
@@ -265,6 +262,57 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi)
     return r;
 }
 
+// Pairs of fp32 values on the packed FMA pipe: a = a * s + c, a = a * s, a += b, a += b * s.
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ void fma2(float& a0, float& a1, float s0, float s1, float c0, float c1)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(pair(a0, a1)), "l"(pair(s0, s1)), "l"(pair(c0, c1)));
+    unpair(r, a0, a1);
+}
+__device__ __forceinline__ void mul2(float& a0, float& a1, float s0, float s1)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a0, a1)), "l"(pair(s0, s1)));
+    unpair(r, a0, a1);
+}
+__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a0, a1)), "l"(pair(b0, b1)));
+    unpair(r, a0, a1);
+}
+__device__ __forceinline__ void add2_scaled(float& a0, float& a1, float b0, float b1, float s)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(r)
+        : "l"(pair(b0, b1)), "l"(pair(s, s)), "l"(pair(a0, a1)));
+    unpair(r, a0, a1);
+}
+
+// Two values as e4m3 (low byte: the first), and what is left of them, 16 times.
+__device__ __forceinline__ uint32_t e4m3_split(float& a, float& b)
+{
+    const __nv_fp8x2_storage_t r =
+        __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(r, __NV_E4M3)));
+    a = 16.0f * (a - f.x);
+    b = 16.0f * (b - f.y);
+    return r;
+}
+
 // The rest of a wait that is not over at once.  Out of line: the roles' loops together have to
 // stay in the instruction cache (with every wait inlined a third of the fetches missed it).
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* ab,
@@ -286,21 +334,21 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
     using C = AttnCfg<D, NH, MODE>;
     using T = typename std::conditional<MODE == kModeBf16 || MODE == kModeFp8Bf16, __nv_bfloat16,
                                         __half>::type;
+    constexpr int HN = C::kHeads;
     extern __shared__ __align__(1024) uint8_t sm[];
-    uint8_t* stages = sm;
-    uint8_t* pbuf = stages + C::kStages * C::kStage;
-    uint8_t* qbuf = pbuf + 2 * C::kPBytes;
-    int32_t* slots = reinterpret_cast<int32_t*>(qbuf + 2 * C::kQBytes);   // [kTiles][128]
-    uint32_t* mask = reinterpret_cast<uint32_t*>(slots + C::kTiles * kAttnTile);   // [kMaskDepth][4]
-    float* exch = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(mask) + C::kMaskBytes);
-    float* factor = exch + C::kGroups * 64;                    // [2][NH]: of an item's output
-    float* qscale = factor + 2 * NH;                           // [2][NH]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(qscale + (C::kFp8 ? 2 * NH : 0));
-    uint64_t* kv_full = bars;
+    uint8_t* stages = sm;                                      // k and v of kTiles tiles
+    uint8_t* pbuf = stages + C::kStages * C::kStage;           // [2] weights
+    uint8_t* qbuf = pbuf + 2 * C::kPBytes;                     // [2] queries
+    // [2 warpgroups][4 quadrants][HN] sums of an item, [2][HN] running maxima
+    float* sums = reinterpret_cast<float*>(qbuf + 2 * C::kQBytes);
+    float* maxima = sums + C::kStats / 4;
+    float* qscale = maxima + C::kMax / 4;                      // [2][NH]
+    float* kscale = qscale + C::kQScale / 4;                   // [2 kTiles][128]
+    float* vscale = kscale + (C::kFp8 ? C::kStages * kAttnTile : 0);
+    uint8_t* valid = reinterpret_cast<uint8_t*>(vscale + (C::kFp8 ? C::kStages * kAttnTile : 0));
+    uint64_t* kv_full = reinterpret_cast<uint64_t*>(valid + C::kStages * kAttnTile);
     uint64_t* kv_empty = kv_full + C::kStages;
-    uint64_t* slot_full = kv_empty + C::kStages;
-    uint64_t* slot_empty = slot_full + C::kTiles;
-    uint64_t* q_full = slot_empty + C::kTiles;
+    uint64_t* q_full = kv_empty + C::kStages;
     uint64_t* q_empty = q_full + 2;
     uint64_t* s_full = q_empty + 2;
     uint64_t* s_empty = s_full + 2;
@@ -308,11 +356,11 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
     uint64_t* p_empty = p_full + 2;
     uint64_t* o_full = p_empty + 2;
     uint64_t* o_empty = o_full + 2;
-    uint64_t* f_full = o_empty + 2;
-    uint64_t* f_empty = f_full + 2;
-    uint64_t* drained = f_empty + 2;
+    uint64_t* f_full = o_empty + 2;                            // sums and maxima
+    uint64_t* f_empty = f_full + 1;
+    uint64_t* drained = f_empty + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* ab = reinterpret_cast<volatile int*>(tmem_slot + 1);   // a wait gave up
 
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x / 32), 0);
     const int lane = threadIdx.x & 31;
@@ -321,217 +369,368 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             mbar_init(kv_full + i, 1);
             mbar_init(kv_empty + i, 1);
         }
-        for (int i = 0; i < C::kTiles; ++i) {
-            mbar_init(slot_full + i, 1);
-            mbar_init(slot_empty + i, 2);
-        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, 1);
             mbar_init(q_empty + i, 1);
             mbar_init(s_full + i, 1);
-            mbar_init(s_empty + i, C::kSoftmaxWarps);
-            mbar_init(p_full + i, C::kSoftmaxWarps);
+            mbar_init(s_empty + i, C::kTileWarps);
+            mbar_init(p_full + i, C::kTileWarps);
             mbar_init(p_empty + i, 1);
             mbar_init(o_full + i, 1);
             mbar_init(o_empty + i, 4);
-            mbar_init(f_full + i, C::kSoftmaxWarps);
-            mbar_init(f_empty + i, 4);
         }
+        mbar_init(f_full, 8);
+        mbar_init(f_empty, 4);
         mbar_init(drained, 1);
         // the swizzled tiles need their 1024-byte boundaries
-        *abort_flag = (smem_u32(sm) & 1023u) != 0;
+        *ab = (smem_u32(sm) & 1023u) != 0;
         fence_mbar_init();
     }
-    constexpr int kGatherWarp = C::kSoftmaxWarps + 4;
-    constexpr int kSlotWarp = kGatherWarp + C::kStages, kMmaWarp = kSlotWarp + 1;
-    if (warp == kMmaWarp) {
+    if (warp == C::kMmaWarp) {
         tmem_alloc(tmem_slot, C::kTmem);
         tmem_relinquish();
     }
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    const uint32_t tmem_s = tmem, tmem_o = tmem + 2 * C::kSCols;
+    const uint32_t tmem_s = *tmem_slot, tmem_o = tmem_s + 2 * C::kSCols;
     pdl_wait_then_release();
     // The status word is cleared by the call itself; a wait that gives up sets it a whole
     // wait budget later.
     if (blockIdx.x == 0 && threadIdx.x == 0)
-        *p.status = *abort_flag ? kStatusBadArg : 0u;
+        *p.status = *ab ? kStatusBadArg : 0u;
 
     const int total = p.rows * p.Hkv * p.head_tiles * p.splits;
-    volatile int* ab = abort_flag;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return mbar_try_wait(bar, parity) || wait_on(bar, parity, ab, p.status);
     };
+    // Tiles of an item use the score and weight buffers alternately, from buffer 0 on.
 
-    if (warp < C::kSoftmaxWarps) {
+    if (warp < 8) {
         // ---------------------------------------------------------------- softmax
-        // Thread = one key of the tile (a TMEM lane) x 16 heads.
-        const int wg = warp / 4, quad = warp & 3, key = 32 * quad + lane;
+        // Thread = one key of a tile (a TMEM lane) x HN heads.
+        const int wg = warp / 4, quad = warp & 3, key = 32 * quad + lane, bar_id = 1 + wg;
         const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-        const int bar_id = 1 + wg;
-        float* x4 = exch + wg * 64;                  // [4 quadrants][16 heads]
-        bool bad = false, out_of_here = false;
-        int n = 0, iq = 0;
-        for (int item = blockIdx.x; item < total && !out_of_here; item += gridDim.x) {
+        const int head0 = C::kAlternate ? 0 : HN * wg;
+        float* mx = maxima + wg * HN;
+        // Weights are kept relative to a running maximum that is replaced only where a score
+        // passes it by 2^kSlack: most tiles need no exchange over the keys and no rescaling
+        // of the accumulated output.  (e4m3 weights, times 16, have to stay below 448.)
+        constexpr float kSlack = C::kFp8 ? 4.0f : 8.0f;
+        // the thread's heads in a row of the weights, and the row's part of them as scratch
+        constexpr int kOwn = HN * C::kEb;                // bytes of a term
+        auto scratch = [&](int b, int i) {               // float i of 4 HN
+            constexpr int per = kOwn / 4;
+            return reinterpret_cast<float*>(
+                pbuf + b * C::kPBytes +
+                swizzled<C::kPRow>(i / per * C::kPRow + head0 * C::kEb + i % per * 4));
+        };
+        bool bad = false;
+        int n = 0, iq = 0, use0 = 0, use1 = 0;           // uses of the buffers
+        for (int item = blockIdx.x; item < total; item += gridDim.x) {
             const AttnItem w = attn_item(p, item);
-            float m[16], l[16];
+            const int count = w.tiles - w.tile;
+            if (count == 0)
+                continue;
+            float l[HN];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                m[i] = -3.0e38f;
+            for (int i = 0; i < HN; ++i)
                 l[i] = 0.0f;
-            }
-            for (int j = w.tile; j < w.tiles; ++j, ++n) {
-                const int b = n & 1;
-                bad |= !wait(s_full + b, (n >> 1) & 1);
+            bool first = true, leave = false;
+#pragma unroll 1
+            for (int j = C::kAlternate ? wg : 0; j < count; j += C::kAlternate ? 2 : 1) {
+                const int b = j & 1, u = b ? use1 : use0;
+                bad |= !wait(s_full + b, u & 1);
                 tc_fence_after();
-                float x[16];
-                tmem_ld_32x32b_x16(tmem_s + lanes + b * C::kSCols + 16 * wg, x);
+                float x[HN];
+#pragma unroll
+                for (int c = 0; c < HN; c += 16)
+                    tmem_ld_32x32b_x16(tmem_s + lanes + b * C::kSCols + head0 + c, x + c);
+                if (C::kFp8) {
+#pragma unroll
+                    for (int k = 1; k < C::kQTerms; ++k) {
+#pragma unroll
+                        for (int c = 0; c < HN; c += 16) {
+                            float r[16];
+                            tmem_ld_32x32b_x16(tmem_s + lanes + b * C::kSCols + k * NH + head0 + c, r);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                x[c + i] = fmaf(r[i], k == 1 ? 0.0625f : 0.00390625f, x[c + i]);
+                        }
+                    }
+                }
                 tmem_wait_ld();
                 tc_fence_before();
-                // (the scores' arrival implies the mask's)
-                const uint32_t ok = mask[(n % kMaskDepth) * 4 + quad];
-                __syncwarp();
+                const int ring = (n + j) % C::kStages * kAttnTile + key;
+                const bool ok = valid[ring] != 0;
+                float ks = p.scale_log2, lv = 0.0f, rv = 1.0f;
+                if (C::kFp8) {
+                    const float vs = ok ? vscale[ring] : 1.0f;
+                    ks = ok ? kscale[ring] : 0.0f;
+                    lv = log2f(vs);
+                    rv = 0.0625f / vs;
+                    const float* qs = qscale + (iq & 1) * NH + head0;
+#pragma unroll
+                    for (int i = 0; i < HN; i += 2)
+                        mul2(x[i], x[i + 1], qs[i], qs[i + 1]);
+                }
+                const bool all = __all_sync(0xFFFFFFFFu, ok);
                 if (lane == 0)
                     mbar_arrive(s_empty + b);
+                // Exponents relative to the running maximum (as they are in the first tile).
+                float over = -INFINITY;
+                if (first) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    x[i] *= p.scale_log2;
-                if (ok != 0xFFFFFFFFu) {
-                    const bool mine = (ok >> lane) & 1u;
+                    for (int i = 0; i < HN; ++i)
+                        x[i] = fmaf(x[i], ks, lv);
+                } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        x[i] = mine ? x[i] : -INFINITY;
+                    for (int i = 0; i < HN; i += 2) {
+                        float m0 = mx[i], m1 = mx[i + 1];
+                        if (C::kFp8) {
+                            m0 -= lv;
+                            m1 -= lv;
+                        }
+                        fma2(x[i], x[i + 1], ks, ks, -m0, -m1);
+                    }
                 }
-                float over = x[0] - m[0];
+                if (!all) {
 #pragma unroll
-                for (int i = 1; i < 16; ++i)
-                    over = fmaxf(over, x[i] - m[i]);
-                // The running maximum is replaced only where a score passes it by more than
-                // 2^8: weights then stay below 2^8, and most tiles need no rescaling of the
-                // accumulated output (and no exchange over the keys).
-                const bool first = j == w.tile;
-                if (first || bar_any(over > 8.0f || bad, bar_id, 128)) {
-                    float v[16];
-                    const float mine = reduce16<true>(x);
+                    for (int i = 0; i < HN; ++i)
+                        x[i] = ok ? x[i] : -INFINITY;
+                }
+                if (!first) {
+#pragma unroll
+                    for (int i = 0; i < HN; i += 2)
+                        over = fmaxf(over, fmaxf(x[i], x[i + 1]));
+                }
+                bool waited = false;
+                if (first || bar_any(over > kSlack || bad, bar_id, 128)) {
+                    waited = true;
                     if (first)
-                        bar_all(true, bar_id, 128);  // the last item's sums have been read
-                    if ((lane & 1) == 0)
-                        x4[quad * 16 + lane / 2] = mine;
+                        bad |= !wait(f_empty, (iq & 1) ^ 1);     // the last item's were read
+                    // the products so far are complete, the buffer is free
+                    bad |= !wait(p_empty + b, (u & 1) ^ 1);
+                    if (!C::kAlternate && !first)
+                        bad |= !wait(p_empty + (b ^ 1), ((b ? use0 : use1) - 1) & 1);
+                    if (!first) {
+#pragma unroll
+                        for (int i = 0; i < HN; ++i)
+                            x[i] += mx[i];
+                    }
+#pragma unroll
+                    for (int c = 0; c < HN; c += 16) {
+                        const float r = reduce16<true>(x + c);
+                        if ((lane & 1) == 0)
+                            *scratch(b, quad * HN + c + lane / 2) = r;
+                    }
                     if (!bar_all(!bad, bar_id, 128)) {
-                        out_of_here = true;
+                        leave = true;
                         break;
                     }
-                    float f[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float mn =
-                            fmaxf(fmaxf(fmaxf(m[i], x4[i]), fmaxf(x4[16 + i], x4[32 + i])),
-                                  x4[48 + i]);
-                        f[i] = ex2(m[i] - mn);
-                        m[i] = mn;
-                        l[i] *= f[i];
+                    if (key < HN) {
+                        const float old = first ? -3.0e38f : mx[key];
+                        const float mn = fmaxf(
+                            fmaxf(fmaxf(old, *scratch(b, key)), *scratch(b, HN + key)),
+                            fmaxf(*scratch(b, 2 * HN + key), *scratch(b, 3 * HN + key)));
+                        *scratch(b, key) = ex2(old - mn);
+                        mx[key] = mn;
                     }
-                    if (!first) {
-                        // the products of the tiles before are complete
-                        bad |= !wait(p_empty + ((n - 1) & 1), ((n - 1) >> 1) & 1);
-                        tc_fence_after();
-                        const uint32_t at = tmem_o + lanes + (iq & 1) * C::kOCols + 16 * wg;
-                        tmem_ld_32x32b_x16(at, v);
-                        tmem_wait_ld();
+                    bar_all(true, bar_id, 128);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            v[i] *= f[i];
-                        tmem_st_32x32b_x16(at, v);
+                    for (int i = 0; i < HN; ++i)
+                        x[i] -= mx[i];
+                    if (!first) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int i = 0; i < HN; ++i)
+                            l[i] *= *scratch(b, i);
+#pragma unroll 1
+                        for (int c = 0; c < HN; c += 8) {
+                            const float4 f0 = *reinterpret_cast<const float4*>(scratch(b, c));
+                            const float4 f1 = *reinterpret_cast<const float4*>(scratch(b, c + 4));
+#pragma unroll 1
+                            for (int k = 0; k < C::kPTerms; ++k) {
+                                const uint32_t at =
+                                    tmem_o + lanes +
+                                    ((iq & 1) * C::kAccs + (C::kAlternate ? b : 0)) * C::kOCols +
+                                    k * NH + head0 + c;
+                                float v[8];
+                                tmem_ld_32x32b_x8(at, v);
+                                tmem_wait_ld();
+                                v[0] *= f0.x;
+                                v[1] *= f0.y;
+                                v[2] *= f0.z;
+                                v[3] *= f0.w;
+                                v[4] *= f1.x;
+                                v[5] *= f1.y;
+                                v[6] *= f1.z;
+                                v[7] *= f1.w;
+                                tmem_st_32x32b_x8(at, v);
+                            }
+                        }
                         tmem_wait_st();
                         tc_fence_before();
+                        bar_all(true, bar_id, 128);      // the factors have been read
                     }
+                    first = false;
                 }
+                // e4m3 weights are 16 times the weight
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    x[i] = ex2(x[i] - m[i]);   // a key that is none: 0
-                    l[i] += x[i];
+                for (int i = 0; i < HN; ++i)
+                    x[i] = ex2(C::kFp8 ? x[i] + 4.0f : x[i]);
+#pragma unroll
+                for (int i = 0; i < HN; i += 2) {
+                    if (C::kFp8)
+                        add2_scaled(l[i], l[i + 1], x[i], x[i + 1], rv);
+                    else
+                        add2(l[i], l[i + 1], x[i], x[i + 1]);
                 }
-                bad |= !wait(p_empty + b, ((n >> 1) & 1) ^ 1);
+                if (!waited)
+                    bad |= !wait(p_empty + b, (u & 1) ^ 1);
                 uint8_t* prow = pbuf + b * C::kPBytes;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const uint4 v4 = make_uint4(
-                        pack2<T>(x[8 * c], x[8 * c + 1]), pack2<T>(x[8 * c + 2], x[8 * c + 3]),
-                        pack2<T>(x[8 * c + 4], x[8 * c + 5]), pack2<T>(x[8 * c + 6], x[8 * c + 7]));
-                    *reinterpret_cast<uint4*>(
-                        prow + swizzled<C::kPRow>(key * C::kPRow + 32 * wg + 16 * c)) = v4;
+                for (int c = 0; c < HN; c += 16) {
+                    if (!C::kFp8) {
+#pragma unroll
+                        for (int k = c; k < c + 16; k += 8)
+                            *reinterpret_cast<uint4*>(
+                                prow + swizzled<C::kPRow>(key * C::kPRow + 2 * (head0 + k))) =
+                                make_uint4(pack2<T>(x[k], x[k + 1]), pack2<T>(x[k + 2], x[k + 3]),
+                                           pack2<T>(x[k + 4], x[k + 5]),
+                                           pack2<T>(x[k + 6], x[k + 7]));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {    // the weights, then what is left of them
+                            uint32_t r[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                float* e = x + c + 4 * i;
+                                const uint32_t lo = e4m3_split(e[0], e[1]);
+                                r[i] = lo | e4m3_split(e[2], e[3]) << 16;
+                            }
+                            *reinterpret_cast<uint4*>(
+                                prow +
+                                swizzled<C::kPRow>(key * C::kPRow + k * NH + head0 + c)) =
+                                make_uint4(r[0], r[1], r[2], r[3]);
+                        }
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(p_full + b);
+                if (b)
+                    ++use1;
+                else
+                    ++use0;
             }
-            if (out_of_here)
+            if (leave)
                 break;
-            if (w.tiles == w.tile)
-                continue;
-            // The item's sums; the epilogue's warps get 1 / sum (the output waits for the last
-            // product, the next item's first scores do not).
-            const float mine = reduce16<false>(l);
-            if (!bar_all(!bad, bar_id, 128))             // the last maxima have been read
-                break;
-            if ((lane & 1) == 0)
-                x4[quad * 16 + lane / 2] = mine;
-            bad |= !wait(f_empty + (iq & 1), ((iq >> 1) & 1) ^ 1);
-            if (!bar_all(!bad, bar_id, 128))
-                break;
-            if (quad == 0) {
-                const int i = lane & 15;
-                float mi = 0.0f;
+            if (first) {                                 // no tile of this item
+                bad |= !wait(f_empty, (iq & 1) ^ 1);
+                if (key < HN)
+                    mx[key] = -3.0e38f;
+            }
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    mi = i == k ? m[k] : mi;
-                const float li = (x4[i] + x4[16 + i]) + (x4[32 + i] + x4[48 + i]);
-                if (lane < 16) {
-                    const int h = w.ht * NH + 16 * wg + i;
-                    factor[(iq & 1) * NH + 16 * wg + i] =
-                        p.splits > 1 ? 1.0f : li == 0.0f ? 0.0f : 1.0f / li;
-                    if (p.splits > 1)
-                        reinterpret_cast<float2*>(p.part_ml)[(int64_t)item * NH + 16 * wg + i] =
-                            make_float2(mi, li);
-                    else if (p.lse && h < p.group)
-                        p.lse[(int64_t)w.t * p.Hq + w.g * p.group + h] =
-                            (mi + log2f(li)) * 0.693147180559945309f;
-                }
+            for (int c = 0; c < HN; c += 16) {
+                const float r = reduce16<false>(l + c);
+                if ((lane & 1) == 0)
+                    sums[(wg * 4 + quad) * HN + c + lane / 2] = r;
             }
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(f_full + (iq & 1));
+                mbar_arrive(f_full);
+            n += count;
             ++iq;
         }
-    } else if (warp < kGatherWarp) {
+    } else if (warp < C::kGatherWarp) {
         // --------------------------------------------------------------- epilogue
         // Thread = one element (of D) of NH heads.
         const int quad = warp & 3, dim = 32 * quad + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+        const bool parts = p.splits > 1, write = D == 128 || dim < D;
         int iq = 0;
-        bool ok = true;
-        for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+        for (int item = blockIdx.x; item < total; item += gridDim.x) {
             const AttnItem w = attn_item(p, item);
-            const bool some = w.tiles > w.tile;
-            uint8_t* out = p.out + w.t * p.out_row + (int64_t)(w.g * p.group + w.ht * NH) * p.out_head;
-            const int heads = min(NH, p.group - w.ht * NH);
-            if (some) {
-                ok = wait(f_full + (iq & 1), (iq >> 1) & 1) && wait(o_full + (iq & 1), (iq >> 1) & 1);
+            const int tiles = w.tiles - w.tile, head0 = w.ht * NH;
+            const int heads = parts ? NH : min(NH, p.group - head0);
+            uint8_t* out =
+                p.out + w.t * p.out_row + (int64_t)(w.g * p.group + head0) * p.out_head + 2 * dim;
+            float* part = p.part_o + (int64_t)item * NH * D + dim;
+            // Factors of the accumulators, for head `lane` (+ 32): the weight of its maximum,
+            // over the sum.
+            float fa[(NH + 31) / 32], fb = 0.0f;
+            bool ok = tiles == 0 || wait(f_full, iq & 1);
+#pragma unroll
+            for (int k = 0; k < (NH + 31) / 32; ++k) {
+                const int h = lane + 32 * k, i = C::kAlternate ? h % HN : lane;
+                float m = -3.0e38f, l = 0.0f;
+                fa[k] = 1.0f;
+                if (tiles > 0) {
+                    const float* s = sums + (C::kAlternate ? 0 : k) * 4 * HN + i;
+                    m = maxima[(C::kAlternate ? 0 : k) * HN + i];
+                    l = (s[0] + s[HN]) + (s[2 * HN] + s[3 * HN]);
+                    if (C::kAlternate) {
+                        const float m2 = maxima[HN + i];
+                        const float l2 = (s[4 * HN] + s[5 * HN]) + (s[6 * HN] + s[7 * HN]);
+                        const float mn = fmaxf(m, m2);
+                        fa[k] = ex2(m - mn);
+                        fb = ex2(m2 - mn);
+                        m = mn;
+                        l = l * fa[k] + l2 * fb;
+                    }
+                }
+                if (quad == 0 && h < heads) {
+                    if (parts)
+                        reinterpret_cast<float2*>(p.part_ml)[(int64_t)item * NH + h] =
+                            make_float2(m, l);
+                    else if (p.lse)
+                        p.lse[(int64_t)w.t * p.Hq + w.g * p.group + head0 + h] =
+                            (m + log2f(l)) * 0.693147180559945309f;
+                }
+                const float inv = (C::kFp8 ? 0.0625f : 1.0f) *
+                                  (parts ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l);
+                fa[k] *= inv;
+                fb *= inv;
+            }
+            if (tiles > 0) {
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(f_empty);
+                ok = ok && wait(o_full + (iq & 1), (iq >> 1) & 1);
                 if (!__all_sync(0xFFFFFFFFu, ok))
                     break;
                 tc_fence_after();
             }
-            const bool parts = p.splits > 1, write = D == 128 || dim < D;
-            const int count = parts ? NH : heads;
-            float* part = p.part_o + (int64_t)item * NH * D + dim;
 #pragma unroll 1
-            for (int h0 = 0; h0 < count; h0 += 16) {
-                float o[16] = {};
-                if (some) {
-                    tmem_ld_32x32b_x16(tmem_o + lanes + (iq & 1) * C::kOCols + h0, o);
+            for (int h0 = 0; h0 < heads; h0 += 16) {
+                float o[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[i] = 0.0f;
+                const float f = NH > 32 && h0 >= 32 ? fa[NH / 64] : fa[0];
+#pragma unroll 1
+                for (int a = 0; a < C::kAccs && a < tiles; ++a) {
+                    const uint32_t at =
+                        tmem_o + lanes + ((iq & 1) * C::kAccs + a) * C::kOCols + h0;
+                    const float fac = a == 0 ? f : fb;
+                    float v[16];
+                    tmem_ld_32x32b_x16(at, v);
+                    if (C::kFp8) {
+                        float r[16];
+                        tmem_ld_32x32b_x16(at + NH, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            v[i] = fmaf(r[i], 0.0625f, v[i]);
+                    }
                     tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float s = __shfl_sync(0xFFFFFFFFu, fac, (h0 + i) & 31);
+                        o[i] = s != 0.0f ? fmaf(v[i], s, o[i]) : o[i];
+                    }
                 }
                 if (parts) {
                     float* to = part + h0 * D;
@@ -540,212 +739,239 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                         if (write)
                             to[i * D] = o[i];
                 } else {
-                    const float* f = factor + (iq & 1) * NH + h0;
-                    uint8_t* to = out + h0 * p.out_head + 2 * dim;
+                    uint8_t* to = out + h0 * p.out_head;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float v = f[i] != 0.0f ? o[i] * f[i] : 0.0f;
                         if (write && h0 + i < heads)
-                            *reinterpret_cast<T*>(to) = static_cast<T>(some ? v : 0.0f);
+                            *reinterpret_cast<T*>(to) = static_cast<T>(o[i]);
                         to += p.out_head;
                     }
                 }
             }
-            if (!some) {
-#pragma unroll 1
-                for (int h = dim; h < count; h += kAttnTile) {
-                    if (parts)
-                        reinterpret_cast<float2*>(p.part_ml)[(int64_t)item * NH + h] =
-                            make_float2(-3.0e38f, 0.0f);
-                    else if (p.lse)
-                        p.lse[(int64_t)w.t * p.Hq + w.g * p.group + w.ht * NH + h] = -INFINITY;
-                }
-            }
-            if (some) {
+            if (tiles > 0) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
+                if (lane == 0)
                     mbar_arrive(o_empty + (iq & 1));
-                    mbar_arrive(f_empty + (iq & 1));
-                }
                 ++iq;
             }
         }
-    } else if (warp < kSlotWarp) {
+    } else if (warp < C::kQueryWarp) {
         // ---------------------------------------------------------------- gather
         // Warp i fills stage i of the ring: it waits for the stage, copies the 128 vectors
         // (zeros for keys that are none), waits for its own copies and signals.  The other
-        // stages' warps keep the memory system busy meanwhile.
-        const int pw = warp - kGatherWarp;
+        // stages' warps keep the memory system busy meanwhile.  A warp sees every phase of
+        // the one barrier it waits on.  It reads the list entries of its next tile while its
+        // copies are under way and the pages after them.
+        const int pw = warp - C::kGatherWarp;
+        const bool is_v = pw & 1;
         constexpr int kPerRow = C::kRow / 16;            // copies of 16 bytes a vector takes
-        constexpr int kSpans = 32 / kPerRow;             // vectors copied at a time,
-        constexpr int kSpan = kAttnTile / kSpans;        // kSpan keys apart
+        constexpr int kSpan = 4 * kPerRow;               // keys of a group of kPerRow lanes
         const int chunk = lane % kPerRow, row0 = lane / kPerRow * kSpan;
         const uint32_t stage = smem_u32(stages + pw * C::kStage) + row0 * C::kAtom +
                                (chunk * 16 / C::kAtom) * (kAttnTile * C::kAtom) +
                                (chunk * 16) % C::kAtom;
-        const bool is_v = pw & 1;
         const uint8_t* kv = (is_v ? p.v : p.k) + chunk * 16;
         const int64_t kv_head = is_v ? p.v_head : p.k_head;
         const uint32_t kv_slot = static_cast<uint32_t>(is_v ? p.v_slot : p.k_slot);
-        const int sl = pw / 2;                   // the pair's place in the ring of tiles
-        int n = 0, uses = 0;
-        bool ok = true;
-        for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-            const AttnItem w = attn_item(p, item);
-            const int end = n + max(0, w.tiles - w.tile);
-            const uint8_t* src = kv + w.g * kv_head;
-            // the pair's tiles of the item
-            for (int m = uses * C::kTiles + sl; m < end; m += C::kTiles) {
-                ok = wait(kv_empty + pw, (uses & 1) ^ 1) && wait(slot_full + sl, uses & 1);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok)
-                    break;
-                const int32_t* rows = slots + sl * kAttnTile + row0;
-                const uint4 bits = *reinterpret_cast<const uint4*>(mask + (m % kMaskDepth) * 4);
-                if ((bits.x & bits.y & bits.z & bits.w) == 0xFFFFFFFFu) {
-#pragma unroll 1
-                    for (int i = 0; i < kSpan; i += 8) {
-                        const int4 s0 = *reinterpret_cast<const int4*>(rows + i);
-                        const int4 s1 = *reinterpret_cast<const int4*>(rows + i + 4);
-                        const int32_t s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+        AttnItem w;
+        w.tile = w.tiles = w.n_sel = w.t = w.g = 0;
+        int item = blockIdx.x - gridDim.x, skip = pw / 2;   // tiles to the warp's next one
+        int r = 0, base = 0, len = 0, g = 0;
+        // the lane's keys of a tile: row0 + kPerRow i + chunk, i < 4
+        int32_t entry[4], key[4], page[4];
+        auto advance = [&] {                             // to the warp's next tile; its entries
+            w.tile += skip;
+            bool fresh = false;
+            while (w.tile >= w.tiles) {
+                skip = w.tile - w.tiles;
+                item += gridDim.x;
+                if (item >= total)
+                    return false;
+                w = attn_item(p, item);
+                w.tile += skip;
+                fresh = true;
+            }
+            skip = C::kTiles;
+            if (fresh) {
+                r = request_of(p.row_begin, p.num_requests, w.t);
+                base = p.key_begin[r];
+                len = min(p.clen[w.t], p.key_begin[r + 1] - base);
+            }
+            const int32_t* sel = p.sel + w.t * p.ld_sel;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            cp_async16((stage + i * C::kAtom) ^ swizzle_of<C::kAtom>(k * C::kAtom),
-                                       src + (uint64_t)(uint32_t)s[k] * kv_slot);
+            for (int i = 0; i < 4; ++i) {
+                const int e = (w.tile * kAttnTile + row0 + kPerRow * i + chunk) >> p.block_shift;
+                entry[i] = e < w.n_sel ? sel[e] : -1;
+            }
+            return true;
+        };
+        auto locate = [&] {                              // keys and pages of the entries
+            const int32_t* table = p.table + r * p.ld_table;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int pos = w.tile * kAttnTile + row0 + kPerRow * i + chunk;
+                const int64_t k = ((int64_t)entry[i] << p.block_shift) +
+                                  (pos & ((1 << p.block_shift) - 1));
+                const bool in = entry[i] >= 0 && k < len;
+                key[i] = static_cast<int32_t>(k);
+                page[i] = in ? 0 : -1;
+                if (p.page == 0) {
+                    key[i] += base;
+                } else if (in) {
+                    const int pg = quotient(key[i], p.by_page);
+                    page[i] = table[pg];
+                    key[i] -= pg * p.page;
+                }
+            }
+            g = w.g;
+        };
+        // (one copy of each step, for the instruction cache: the first round only looks up)
+        for (int u = -1;; ++u) {
+            if (u >= 0) {
+                int32_t slot[4];
+                bool whole = true;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t at = (int64_t)page[i] * p.page + key[i];
+                    slot[i] = page[i] >= 0 && at < p.num_slots ? static_cast<int32_t>(at) : -1;
+                    whole = whole && slot[i] >= 0;
+                }
+                whole = __all_sync(0xFFFFFFFFu, whole);
+                if (!__all_sync(0xFFFFFFFFu, wait(kv_empty + pw, (u & 1) ^ 1)))
+                    break;
+                if (!is_v) {
+                    // What the softmax has to know of the keys.  The place was last read for the
+                    // tile 2 kTiles before, whose scores left their buffer before the products of
+                    // the tile kTiles before were begun; those have freed the stage.
+                    const int ring = (u * C::kTiles + pw / 2) % C::kStages * kAttnTile;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = ring + row0 + kPerRow * i + chunk;
+                        valid[k] = slot[i] >= 0;
+                        if (C::kFp8) {
+                            const int64_t at = (int64_t)max(slot[i], 0) * p.Hkv + g;
+                            kscale[k] = slot[i] >= 0 ? p.k_scale[at] : 0.0f;
+                            vscale[k] = slot[i] >= 0 ? p.v_scale[at] : 0.0f;
+                        }
                     }
-                } else {
+                }
+                const uint8_t* src = kv + g * kv_head;
+                constexpr int kStep = kPerRow < 8 ? kPerRow : 8;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int32_t mine = slot[i];
 #pragma unroll 1
-                    for (int i = 0; i < kSpan; ++i) {
-                        const int32_t s = rows[i];
-                        cp_async16((stage + i / 8 * 8 * C::kAtom) ^
-                                       swizzle_of<C::kAtom>(i % 8 * C::kAtom),
-                                   src + (uint64_t)(uint32_t)max(s, 0) * kv_slot, s >= 0);
+                    for (int k = 0; k < kPerRow; k += kStep) {
+                        const int row = i * kPerRow + k;
+                        const uint32_t dst = stage + row / 8 * 8 * C::kAtom;
+                        const int from = (lane & ~(kPerRow - 1)) + k;
+                        if (whole) {
+#pragma unroll
+                            for (int x = 0; x < kStep; ++x) {
+                                const uint32_t s = __shfl_sync(0xFFFFFFFFu, mine, from + x);
+                                cp_async16(dst ^ swizzle_of<C::kAtom>((i * kPerRow % 8 + x) * C::kAtom),
+                                           src + (uint64_t)s * kv_slot);
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int x = 0; x < kStep; ++x) {
+                                const int32_t s = __shfl_sync(0xFFFFFFFFu, mine, from + x);
+                                cp_async16(dst ^ swizzle_of<C::kAtom>((row + x) % 8 * C::kAtom),
+                                           src + (uint64_t)(uint32_t)max(s, 0) * kv_slot, s >= 0);
+                            }
+                        }
                     }
                 }
                 cp_async_commit();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(slot_empty + sl);
+            }
+            const bool more = advance();
+            if (u >= 0) {
                 cp_async_wait<0>();
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(kv_full + pw);
-                ++uses;
             }
-            n = end;
+            if (!more)
+                break;
+            locate();
         }
-    } else if (warp == kSlotWarp) {
-        // ----------------------------------------------------------------- slots
-        // Cache slots of the selected keys, four keys of a tile per lane.  The list entries are
-        // read two tiles ahead and their pages one tile ahead, over the items' ends.
-        struct Tile {
-            int item, t, g, ht, base, r, len, tile;      // item < 0: no tile
-        };
-        Tile d1{-1}, d2{-1};                             // whose pages, whose entries are read
-        int32_t entry[4] = {}, key[4] = {}, page[4] = {};
-        AttnItem w;
-        w.tile = w.tiles = w.n_sel = 0;
-        int next_item = blockIdx.x, r = 0, base = 0, len = 0;
-        int n = 0, iq = 0, last_item = -1, drain = 0;
-        bool ok = true;
-        while (ok && drain < 3) {
-            // tile n: slots from its pages
-            int32_t slot[4];
+    } else if (warp == C::kQueryWarp) {
+        // --------------------------------------------------------------- queries
+        int iq = 0;
+        for (int item = blockIdx.x; item < total; item += gridDim.x) {
+            const AttnItem w = attn_item(p, item);
+            if (w.tiles == w.tile)
+                continue;
+            if (!__all_sync(0xFFFFFFFFu, wait(q_empty + (iq & 1), ((iq >> 1) & 1) ^ 1)))
+                break;
+            const uint8_t* q = p.q + w.t * p.q_row + (int64_t)(w.g * p.group + w.ht * NH) * p.q_head;
+            const int heads = min(NH, p.group - w.ht * NH);
+            uint8_t* dst = qbuf + (iq & 1) * C::kQBytes;
+            if (!C::kFp8) {
+                constexpr int kPerRow = C::kRow / 16;
+#pragma unroll 1
+                for (int i = lane; i < C::kQBytes / 16; i += 32) {
+                    const int h = i / kPerRow, c = i % kPerRow;
+                    const uint32_t off = (c / 8) * (NH * 128) + h * 128 + (c % 8) * 16;
+                    cp_async16(smem_u32(dst) + swizzled<128>(off),
+                               h < heads ? q + h * p.q_head + c * 16 : q, h < heads);
+                }
+                cp_async_commit();
+                cp_async_wait<0>();
+            } else {
+                // A head vector as a sum of e4m3 terms, each 1/16 of the scale of the one before:
+                // two hold the 8 bits of a bf16 element, three the 11 of an fp16 one, down to
+                // 2^-22 of the vector's largest.
+                constexpr int kGroup = D / 16;           // lanes of a vector, 16 elements each
+                const int c = lane % kGroup;
+#pragma unroll 1
+                for (int h = lane / kGroup; h < NH; h += 32 / kGroup) {
+                    float v[16];
+                    float amax = 0.0f;
+                    uint4 in[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+                    if (h < heads) {
+                        const uint4* from = reinterpret_cast<const uint4*>(q + h * p.q_head) + 2 * c;
+                        in[0] = from[0];
+                        in[1] = from[1];
+                    }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t at = (int64_t)page[i] * p.page + key[i];
-                slot[i] = page[i] >= 0 && at < p.num_slots ? static_cast<int32_t>(at) : -1;
-            }
-            const Tile d0 = d1;
-            // tile n + 1: keys and pages from its entries
-            d1 = d2;
-            if (d1.item >= 0) {
-                const int32_t* table = p.table + d1.r * p.ld_table;
+                    for (int i = 0; i < 16; ++i) {
+                        v[i] = value(reinterpret_cast<const T*>(in)[i]);
+                        amax = fmaxf(amax, fabsf(v[i]));
+                    }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int pos = d1.tile * kAttnTile + 32 * i + lane;
-                    const int64_t k = ((int64_t)entry[i] << p.block_shift) +
-                                      (pos & ((1 << p.block_shift) - 1));
-                    const bool in = entry[i] >= 0 && k < d1.len;
-                    key[i] = static_cast<int32_t>(k);
-                    page[i] = in ? 0 : -1;
-                    if (p.page == 0) {
-                        key[i] += d1.base;
-                    } else if (in) {
-                        const int pg = quotient(key[i], p.by_page);
-                        page[i] = table[pg];
-                        key[i] -= pg * p.page;
+                    for (int d = kGroup / 2; d > 0; d >>= 1)
+                        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+                    // a power of two, so that no element is rounded by it
+                    const int ex = static_cast<int>(__float_as_uint(amax) >> 23);
+                    const int up = amax > 0.0f ? min(max(261 - ex, 1), 254) : 127;
+                    const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
+                    if (c == 0)
+                        qscale[(iq & 1) * NH + h] = p.scale_log2 / mul;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        v[i] *= mul;
+#pragma unroll
+                    for (int k = 0; k < C::kQTerms; ++k) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t lo = e4m3_split(v[4 * i], v[4 * i + 1]);
+                            o[i] = lo | e4m3_split(v[4 * i + 2], v[4 * i + 3]) << 16;
+                        }
+                        *reinterpret_cast<uint4*>(
+                            dst + swizzled<C::kAtom>((k * NH + h) * C::kRow + c * 16)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
                     }
                 }
             }
-            // tile n + 2: entries
-            while (w.tile >= w.tiles && next_item < total) {
-                w = attn_item(p, next_item);
-                r = request_of(p.row_begin, p.num_requests, w.t);
-                base = p.key_begin[r];
-                len = min(p.clen[w.t], p.key_begin[r + 1] - base);
-                next_item += gridDim.x;
-            }
-            d2 = Tile{-1};
-            if (w.tile < w.tiles) {
-                d2 = Tile{next_item, w.t, w.g, w.ht, base, r, len, w.tile};
-                const int32_t* sel = p.sel + w.t * p.ld_sel;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int at = (w.tile * kAttnTile + 32 * i + lane) >> p.block_shift;
-                    entry[i] = at < w.n_sel ? sel[at] : -1;
-                }
-                ++w.tile;
-            }
-            drain = d2.item < 0 ? drain + 1 : 0;
-            if (d0.item < 0)
-                continue;
-            const bool new_item = d0.item != last_item;
-            if (new_item) {
-                // the item's queries, before its first tile
-                ok = wait(q_empty + (iq & 1), ((iq >> 1) & 1) ^ 1);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok)
-                    break;
-                constexpr int kPerRow = C::kRow / 16;
-                const uint8_t* q = p.q + d0.t * p.q_row + (int64_t)d0.g * p.group * p.q_head;
-                const uint32_t dst = smem_u32(qbuf + (iq & 1) * C::kQBytes);
-#pragma unroll 1
-                for (int i = lane; i < C::kQBytes / 16; i += 32) {
-                    const int h = i / kPerRow, c16 = i % kPerRow;
-                    const bool in = d0.ht * NH + h < p.group;
-                    const uint32_t off = (c16 / 8) * (NH * 128) + h * 128 + (c16 % 8) * 16;
-                    cp_async16(dst + swizzled<128>(off),
-                               in ? q + (int64_t)(d0.ht * NH + h) * p.q_head + c16 * 16 : q, in);
-                }
-                cp_async_commit();
-            }
-            ok = wait(slot_empty + n % C::kTiles, ((n / C::kTiles) & 1) ^ 1);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok)
-                break;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                slots[(n % C::kTiles) * kAttnTile + 32 * i + lane] = slot[i];
-                const uint32_t bits = __ballot_sync(0xFFFFFFFFu, slot[i] >= 0);
-                if (lane == i)
-                    mask[(n % kMaskDepth) * 4 + i] = bits;
-            }
+            fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(slot_full + n % C::kTiles);
-            if (new_item) {
-                cp_async_wait<0>();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(q_full + (iq & 1));
-                ++iq;
-                last_item = d0.item;
-            }
-            ++n;
+                mbar_arrive(q_full + (iq & 1));
+            ++iq;
         }
     } else {
         // --------------------------------------------------------------------- MMA
@@ -757,58 +983,45 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         // One elected lane waits and issues.
         if (elect_one()) {
             struct Pending {
-                bool any, first, last;
-                int n, iq;
-            } pv{false, false, false, 0, 0};
+                bool any, fresh, last;                  // fresh: the accumulator is empty
+                int j, b, u, iq, n;
+            } pv{false, false, false, 0, 0, 0, 0, 0};
             const uint64_t k_desc = smem_desc(smem_u32(stages), C::kAtom, 16, 8 * C::kAtom);
             // v rows are keys: both operands of the second product are read along their rows.
             // D = 64 takes the same 64 elements for both halves of the 128 output rows.
-            constexpr uint32_t lbo = C::kAtoms > 1 ? kAttnTile * C::kAtom : 0;
+            constexpr uint32_t lbo = D == 64 ? 0 : kAttnTile * C::kAtom;
             const uint64_t v_desc = smem_desc(smem_u32(stages), C::kAtom, lbo, 8 * C::kAtom);
             const uint64_t q_desc = smem_desc(smem_u32(qbuf), C::kAtom, 16, 8 * C::kAtom);
             const uint64_t p_desc = smem_desc(smem_u32(pbuf), C::kPRow, 0, 8 * C::kPRow);
-            int vst = 0;                                // the pending product's stage
-            auto product = [&]() {                      // O += P V of a tile
-                const int b = pv.n & 1;
-                if (!(wait(kv_full + vst, (pv.n / C::kTiles) & 1) &&
-                      (!pv.first || wait(o_empty + (pv.iq & 1), ((pv.iq >> 1) & 1) ^ 1)) &&
-                      wait(p_full + b, (pv.n >> 1) & 1)))
-                    return false;
-                tc_fence_after();
-                const uint64_t a0 = v_desc + vst * (C::kStage / 16);
-                const uint64_t b0 = p_desc + b * (C::kPBytes / 16);
-                const uint32_t d = tmem_o + (pv.iq & 1) * C::kOCols;
-#pragma unroll
-                for (int k = 0; k < kAttnTile / kK; ++k)
-                    mma_f16(d, a0 + k * (kK * C::kAtom / 16), b0 + k * (kK * C::kPRow / 16),
-                            idesc_o, !pv.first || k > 0);
-                mma_commit(kv_empty + vst);
-                mma_commit(p_empty + b);
-                if (pv.last)
-                    mma_commit(o_full + (pv.iq & 1));
-                return true;
+            auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+                if (C::kFp8)
+                    mma_f8f6f4(d, a, b, id, acc);
+                else
+                    mma_f16(d, a, b, id, acc);
             };
-            int n = 0, iq = 0, st = 0;                  // st: the k stage of tile n
-            int item = blockIdx.x, j = 0, first = 0, end = 0;
-            if (item < total) {
-                const AttnItem w = attn_item<true>(p, item);
-                first = j = w.tile;
-                end = w.tiles;
-            }
+            // Scores are issued kAhead tiles before the product of their tile, so that the next
+            // ones are ready when a warpgroup is done with its tile.
+            constexpr int kAhead = C::kTiles > 2 && C::kAlternate ? 2 : 1;
+            Pending queue[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                queue[i] = pv;
+            int use0 = 0, use1 = 0, n = 0, iq = 0, st = 0, vst = 1;   // stages of the next tiles
+            int item = blockIdx.x - gridDim.x, j = 0, count = 0;
             while (true) {
-                while (j >= end && (item += gridDim.x) < total) {
+                while (j >= count && (item += gridDim.x) < total) {
                     const AttnItem w = attn_item<true>(p, item);
-                    first = j = w.tile;
-                    end = w.tiles;
+                    j = 0;
+                    count = w.tiles - w.tile;
                 }
-                const bool more = j < end;
-                const Pending next{more, j == first, j + 1 == end, n, iq};
-                const int next_st = st + 1;
+                const bool more = j < count;
+                const int b = j & 1;
+                const Pending next{more, C::kAlternate ? j < 2 : j == 0, j + 1 == count, j, b,
+                                   b ? use1 : use0, iq, n};
                 if (more) {                             // S = Q K of tile n
-                    const int b = n & 1;
-                    if (!((!next.first || wait(q_full + (iq & 1), (iq >> 1) & 1)) &&
+                    if (!((j > 0 || wait(q_full + (iq & 1), (iq >> 1) & 1)) &&
                           wait(kv_full + st, (n / C::kTiles) & 1) &&
-                          wait(s_empty + b, ((n >> 1) & 1) ^ 1)))
+                          wait(s_empty + b, (next.u & 1) ^ 1)))
                         break;
                     tc_fence_after();
                     const uint64_t a0 = k_desc + st * (C::kStage / 16);
@@ -816,25 +1029,51 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
 #pragma unroll
                     for (int k = 0; k < D / kK; ++k) {
                         const int atom = k * 32 / C::kAtom, in = (k * 32) % C::kAtom;
-                        mma_f16(tmem_s + b * C::kSCols,
-                                a0 + (atom * (kAttnTile * C::kAtom) + in) / 16,
-                                b0 + (atom * (C::kQRows * C::kAtom) + in) / 16, idesc_s, k > 0);
+                        mma(tmem_s + b * C::kSCols, a0 + (atom * (kAttnTile * C::kAtom) + in) / 16,
+                            b0 + (atom * (C::kQRows * C::kAtom) + in) / 16, idesc_s, k > 0);
                     }
                     mma_commit(s_full + b);
                     mma_commit(kv_empty + st);
-                    if (next.last)
+                    if (next.last) {
                         mma_commit(q_empty + (iq & 1));
-                    iq += next.last;
+                        ++iq;
+                    }
+                    use0 += b == 0;
+                    use1 += b;
                     ++j;
                     ++n;
                     st = st + 2 == C::kStages ? 0 : st + 2;
                 }
-                if (pv.any && !product())
+                pv = queue[0];
+                if (pv.any) {                           // O += P V of the tile kAhead before
+                    if (!(wait(kv_full + vst, (pv.n / C::kTiles) & 1) &&
+                          (pv.j > 0 || wait(o_empty + (pv.iq & 1), ((pv.iq >> 1) & 1) ^ 1)) &&
+                          wait(p_full + pv.b, pv.u & 1)))
+                        break;
+                    tc_fence_after();
+                    const uint64_t a0 = v_desc + vst * (C::kStage / 16);
+                    const uint64_t b0 = p_desc + pv.b * (C::kPBytes / 16);
+                    const uint32_t d =
+                        tmem_o + ((pv.iq & 1) * C::kAccs + (C::kAlternate ? pv.b : 0)) * C::kOCols;
+#pragma unroll
+                    for (int k = 0; k < kAttnTile / kK; ++k)
+                        mma(d, a0 + k * (kK * C::kAtom / 16), b0 + k * (kK * C::kPRow / 16),
+                            idesc_o, !pv.fresh || k > 0);
+                    mma_commit(kv_empty + vst);
+                    mma_commit(p_empty + pv.b);
+                    if (pv.last)
+                        mma_commit(o_full + (pv.iq & 1));
+                    vst = vst + 2 >= C::kStages ? 1 : vst + 2;
+                }
+                bool left = more;
+#pragma unroll
+                for (int i = 0; i + 1 < kAhead; ++i) {
+                    queue[i] = queue[i + 1];
+                    left = left || queue[i].any;
+                }
+                queue[kAhead - 1] = next;
+                if (!left)
                     break;
-                if (!more)
-                    break;
-                pv = next;
-                vst = next_st;
             }
             // what was issued, and its arrivals, end before the memory goes
             mma_commit(drained);
@@ -844,9 +1083,9 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         __syncwarp();
     }
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == C::kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::kTmem);
+        tmem_dealloc(tmem_s, C::kTmem);
     }
 }
 
