@@ -25,92 +25,12 @@ __device__ __forceinline__ int request_of(const int32_t* begin, int n, int64_t t
     return lo;
 }
 
-// Cache slot of key position `c` of row t's list (entry c / block), or -1.
-__device__ __forceinline__ int32_t selected_slot(const AttnParams& p, int64_t t, int r, int n_sel,
-                                                 int len, int64_t c)
-{
-    const int64_t e = c >> p.block_shift;
-    if (e >= n_sel)
-        return -1;
-    const int32_t s = p.sel[t * p.ld_sel + e];
-    if (s < 0)
-        return -1;
-    const int64_t j = ((int64_t)s << p.block_shift) + (c & ((1 << p.block_shift) - 1));
-    if (j >= len)
-        return -1;
-    if (p.page == 0) {
-        const int64_t slot = p.key_begin[r] + j;
-        return slot < p.num_slots ? static_cast<int32_t>(slot) : -1;
-    }
-    const int32_t page = static_cast<int32_t>(j) / p.page;
-    const int64_t pg = p.table[r * p.ld_table + page];
-    const int64_t slot = pg * p.page + (j - (int64_t)page * p.page);
-    return pg >= 0 && slot < p.num_slots ? static_cast<int32_t>(slot) : -1;
-}
-
 template <typename T>
 __device__ __forceinline__ float value(T v);
 template <>
 __device__ __forceinline__ float value(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <>
 __device__ __forceinline__ float value(__half v) { return __half2float(v); }
-template <>
-__device__ __forceinline__ float value(__nv_fp8_e4m3 v) { return static_cast<float>(v); }
-
-// One warp per (row, query head): the keys one after another, the running maximum and sum
-// of the softmax, D / 32 elements of the output per lane.
-template <typename T, typename KV, int D>
-__global__ void __launch_bounds__(128)
-attention_kernel(const __grid_constant__ AttnParams p)
-{
-    pdl_wait_then_release();
-    const int64_t item = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
-    if (item >= (int64_t)p.rows * p.Hq)
-        return;
-    const int lane = threadIdx.x & 31;
-    const int64_t t = item / p.Hq;
-    const int h = static_cast<int>(item % p.Hq), g = h / p.group;
-    const int r = request_of(p.row_begin, p.num_requests, t);
-    const int len = min(p.clen[t], p.key_begin[r + 1] - p.key_begin[r]);
-    const int n_sel = p.sel_count ? min(p.num_sel, p.sel_count[t]) : p.num_sel;
-    constexpr int N = D / 32;
-    float q[N], o[N] = {};
-    for (int i = 0; i < N; ++i)
-        q[i] = value(reinterpret_cast<const T*>(p.q + t * p.q_row + h * p.q_head)[lane + 32 * i]);
-    float m = -INFINITY, l = 0.0f;
-    bool any = false;
-    const int64_t total = (int64_t)max(n_sel, 0) << p.block_shift;
-    for (int64_t c0 = 0; c0 < total; c0 += 32) {
-        const int32_t mine = selected_slot(p, t, r, n_sel, len, c0 + lane);
-        for (int i = 0; i < 32; ++i) {
-            const int64_t slot = __shfl_sync(0xFFFFFFFFu, mine, i);
-            if (slot < 0)
-                continue;
-            any = true;
-            const KV* kr = reinterpret_cast<const KV*>(p.k + slot * p.k_slot + g * p.k_head);
-            const KV* vr = reinterpret_cast<const KV*>(p.v + slot * p.v_slot + g * p.v_head);
-            float a = 0.0f;
-            for (int x = 0; x < N; ++x)
-                a = fmaf(q[x], value(kr[lane + 32 * x]), a);
-            for (int d = 16; d > 0; d >>= 1)
-                a += __shfl_xor_sync(0xFFFFFFFFu, a, d);
-            a *= p.scale_log2 * (p.k_scale ? p.k_scale[slot * p.Hkv + g] : 1.0f);
-            const float mn = fmaxf(m, a);
-            const float f = m == mn ? 1.0f : exp2f(m - mn), w = exp2f(a - mn);
-            const float sv = p.v_scale ? p.v_scale[slot * p.Hkv + g] : 1.0f;
-            l = l * f + w;
-            for (int x = 0; x < N; ++x)
-                o[x] = o[x] * f + w * sv * value(vr[lane + 32 * x]);
-            m = mn;
-        }
-    }
-    T* out = reinterpret_cast<T*>(p.out + t * p.out_row + h * p.out_head);
-    for (int x = 0; x < N; ++x)
-        out[lane + 32 * x] = static_cast<T>(any ? o[x] / l : 0.0f);
-    if (p.lse && lane == 0)
-        p.lse[item] = any ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
-}
-
 // ---------------------------------------------------------------- tensor-core kernel
 
 // Modes: k and v of q's type (bf16 or fp16), or e4m3 caches under bf16 or fp16 queries.
@@ -118,6 +38,10 @@ constexpr int kModeBf16 = 0, kModeFp16 = 1, kModeFp8Bf16 = 2, kModeFp8Fp16 = 3;
 
 constexpr long long kWaitCycles = 4000000000LL;   // about two seconds
 constexpr int kSmemLimit = 232448;
+// Items whose query scales are held.  No barrier guards them: the scales of item i + 8 are
+// written after the scores of item i + 6, at least five tiles past the last of item i, were
+// issued, and scores are issued at most three tiles ahead of a tile's weights.
+constexpr int kScaleItems = 8;
 
 template <int D, int NH, int MODE>
 struct AttnCfg {
@@ -148,7 +72,7 @@ struct AttnCfg {
     // Shared memory after the stages, the weights and the queries.
     static constexpr int kStats = 2 * 4 * kHeads * 4;   // sums by warpgroup and quadrant
     static constexpr int kMax = 2 * kHeads * 4;         // maxima by warpgroup
-    static constexpr int kQScale = kFp8 ? 2 * NH * 4 : 0;
+    static constexpr int kQScale = kFp8 ? kScaleItems * NH * 4 : 0;
     static constexpr int kKeyInfo = kAttnTile * (kFp8 ? 9 : 1);   // of a tile, 2 kTiles of them
     static constexpr int kFixed = kStats + kMax + kQScale + 2 * kPBytes + 2 * kQBytes + 8 * 20;
     static constexpr int kFit =
@@ -342,7 +266,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
     // [2 warpgroups][4 quadrants][HN] sums of an item, [2][HN] running maxima
     float* sums = reinterpret_cast<float*>(qbuf + 2 * C::kQBytes);
     float* maxima = sums + C::kStats / 4;
-    float* qscale = maxima + C::kMax / 4;                      // [2][NH]
+    float* qscale = maxima + C::kMax / 4;                      // [kScaleItems][NH]
     float* kscale = qscale + C::kQScale / 4;                   // [2 kTiles][128]
     float* vscale = kscale + (C::kFp8 ? C::kStages * kAttnTile : 0);
     uint8_t* valid = reinterpret_cast<uint8_t*>(vscale + (C::kFp8 ? C::kStages * kAttnTile : 0));
@@ -469,7 +393,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     ks = ok ? kscale[ring] : 0.0f;
                     lv = log2f(vs);
                     rv = 0.0625f / vs;
-                    const float* qs = qscale + (iq & 1) * NH + head0;
+                    const float* qs = qscale + (iq % kScaleItems) * NH + head0;
 #pragma unroll
                     for (int i = 0; i < HN; i += 2)
                         mul2(x[i], x[i + 1], qs[i], qs[i + 1]);
@@ -949,7 +873,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     const int up = amax > 0.0f ? min(max(261 - ex, 1), 254) : 127;
                     const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
                     if (c == 0)
-                        qscale[(iq & 1) * NH + h] = p.scale_log2 / mul;
+                        qscale[(iq % kScaleItems) * NH + h] =      // (infinite elements give NaN, as they do)
+                            amax < INFINITY ? p.scale_log2 / mul : __int_as_float(0x7FFFFFFF);
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         v[i] *= mul;
@@ -1143,12 +1068,17 @@ cudaError_t attention_tc(const AttnParams& p, cudaStream_t st)
 template <int D, int MODE>
 cudaError_t attention_heads(const AttnParams& p, int nh, cudaStream_t st)
 {
-    cudaError_t e = nh == 16   ? attention_tc<D, 16, MODE>(p, st)
-                    : nh == 32 ? attention_tc<D, 32, MODE>(p, st)
-                               : attention_tc<D, 64, MODE>(p, st);
+    cudaError_t e;
+    if (nh == 16)
+        e = attention_tc<D, 16, MODE>(p, st);
+    else if (nh == 32 || MODE == kModeFp8Fp16)
+        e = attention_tc<D, 32, MODE>(p, st);
+    else
+        e = attention_tc<D, MODE == kModeFp8Fp16 ? 32 : 64, MODE>(p, st);
     if (e != cudaSuccess || p.splits == 1)
         return e;
-    using T = typename std::conditional<MODE == kModeBf16, __nv_bfloat16, __half>::type;
+    using T = typename std::conditional<MODE == kModeBf16 || MODE == kModeFp8Bf16, __nv_bfloat16,
+                                        __half>::type;
     count_launch();
     const unsigned blocks = static_cast<unsigned>(((int64_t)p.rows * p.Hq + 3) / 4);
     return launch_pdl(attention_join_kernel<T, D>, dim3(blocks), dim3(128), 0, st, p, nh);
@@ -1184,38 +1114,28 @@ mask_blocks_kernel(const __grid_constant__ MaskBlocksParams p)
         p.count[t] = n;
 }
 
-template <typename T, typename KV>
-cudaError_t attention_of(const AttnParams& p, int D, cudaStream_t st)
-{
-    const unsigned blocks = static_cast<unsigned>(((int64_t)p.rows * p.Hq + 3) / 4);
-    return D == 64 ? launch_pdl(attention_kernel<T, KV, 64>, dim3(blocks), dim3(128), 0, st, p)
-                   : launch_pdl(attention_kernel<T, KV, 128>, dim3(blocks), dim3(128), 0, st, p);
-}
-
 }  // namespace
 
 int attention_heads_per_tile(int group, int dtype, bool fp8)
 {
-    (void)dtype;
-    (void)fp8;
-    return group <= 16 ? 16 : group <= 32 ? 32 : 64;
+    // three terms of 64 fp16 heads do not fit the tensor memory
+    return group <= 16 ? 16 : group <= 32 || (fp8 && dtype == IDX_FP16) ? 32 : 64;
+}
+
+template <int MODE>
+static cudaError_t attention_mode(const AttnParams& p, int D, int nh, cudaStream_t st)
+{
+    return D == 64 ? attention_heads<64, MODE>(p, nh, st) : attention_heads<128, MODE>(p, nh, st);
 }
 
 cudaError_t launch_attention(const AttnParams& p, int D, int dtype, bool fp8, cudaStream_t st)
 {
-    if (!fp8) {
-        const int nh = attention_heads_per_tile(p.group, dtype, fp8);
-        if (dtype == IDX_BF16)
-            return D == 64 ? attention_heads<64, kModeBf16>(p, nh, st)
-                           : attention_heads<128, kModeBf16>(p, nh, st);
-        return D == 64 ? attention_heads<64, kModeFp16>(p, nh, st)
-                       : attention_heads<128, kModeFp16>(p, nh, st);
-    }
+    const int nh = attention_heads_per_tile(p.group, dtype, fp8);
     if (dtype == IDX_BF16)
-        return fp8 ? attention_of<__nv_bfloat16, __nv_fp8_e4m3>(p, D, st)
-                   : attention_of<__nv_bfloat16, __nv_bfloat16>(p, D, st);
-    return fp8 ? attention_of<__half, __nv_fp8_e4m3>(p, D, st)
-               : attention_of<__half, __half>(p, D, st);
+        return fp8 ? attention_mode<kModeFp8Bf16>(p, D, nh, st)
+                   : attention_mode<kModeBf16>(p, D, nh, st);
+    return fp8 ? attention_mode<kModeFp8Fp16>(p, D, nh, st)
+               : attention_mode<kModeFp16>(p, D, nh, st);
 }
 
 cudaError_t launch_mask_blocks(const MaskBlocksParams& p, cudaStream_t st)
