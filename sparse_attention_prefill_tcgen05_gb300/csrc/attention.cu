@@ -77,11 +77,11 @@ struct AttnCfg {
     static constexpr int kFixed = kStats + kMax + kQScale + 2 * kPBytes + 2 * kQBytes + 8 * 20;
     static constexpr int kFit =
         (kSmemLimit - kFixed) / (2 * kStage + 2 * kKeyInfo + 8 * 4);
-    static constexpr int kTiles = kFit < 4 ? kFit : 4;  // tiles in the ring
+    static constexpr int kTiles = kFit < 3 ? kFit : 3;  // tiles in the ring
     static constexpr int kStages = 2 * kTiles;          // and as many warps that fill them
     static constexpr int kSmem = kFixed + kTiles * (2 * kStage + 2 * kKeyInfo + 8 * 4);
-    static constexpr int kGatherWarp = 8 + 4, kQueryWarp = kGatherWarp + kStages;
-    static constexpr int kMmaWarp = kQueryWarp + 1, kThreads = 32 * (kMmaWarp + 1);
+    static constexpr int kGatherWarp = 8 + 4, kMmaWarp = kGatherWarp + kStages;
+    static constexpr int kThreads = 32 * (kMmaWarp + 1);
     static_assert(kCols <= 512 && kTiles >= 2 && kSmem <= kSmemLimit, "tile does not fit");
 };
 
@@ -138,10 +138,15 @@ __device__ __forceinline__ AttnItem attn_item(const AttnParams& p, int item)
     return w;
 }
 
-// 16 values of every lane, combined over the warp: lane i ends with value i / 2.
+// 16 values of every lane, combined over the warp: lane i ends with value i / 2.  Out of line
+// like wait_on: it runs once per row.
 template <bool kMax>
-__device__ __forceinline__ float reduce16(const float* v)
+__device__ __noinline__ float reduce16_of(float v0, float v1, float v2, float v3, float v4,
+                                          float v5, float v6, float v7, float v8, float v9,
+                                          float v10, float v11, float v12, float v13, float v14,
+                                          float v15)
 {
+    const float v[16] = {v0, v1, v2, v3, v4, v5, v6, v7, v8, v9, v10, v11, v12, v13, v14, v15};
     const int lane = threadIdx.x & 31;
     float a[8], b[4], c[2];
     auto op = [](float x, float y) { return kMax ? fmaxf(x, y) : x + y; };
@@ -167,6 +172,13 @@ __device__ __forceinline__ float reduce16(const float* v)
     const float r = __shfl_xor_sync(0xFFFFFFFFu, up ? c[0] : c[1], 2);
     const float d = op(up ? c[1] : c[0], r);
     return op(d, __shfl_xor_sync(0xFFFFFFFFu, d, 1));
+}
+
+template <bool kMax>
+__device__ __forceinline__ float reduce16(const float* v)
+{
+    return reduce16_of<kMax>(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], v[8], v[9], v[10],
+                             v[11], v[12], v[13], v[14], v[15]);
 }
 
 template <typename T>
@@ -226,15 +238,16 @@ __device__ __forceinline__ void add2_scaled(float& a0, float& a1, float b0, floa
     unpair(r, a0, a1);
 }
 
-// Two values as e4m3 (low byte: the first), and what is left of them, 16 times.
-__device__ __forceinline__ uint32_t e4m3_split(float& a, float& b)
+// Two f16 values as e4m3 (low byte: the first); they become 16 times what is left of them.
+__device__ __forceinline__ uint32_t e4m3_split(uint32_t& h)
 {
-    const __nv_fp8x2_storage_t r =
-        __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(r, __NV_E4M3)));
-    a = 16.0f * (a - f.x);
-    b = 16.0f * (b - f.y);
-    return r;
+    const uint16_t code = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&h),
+                                                     __NV_SATFINITE, __NV_E4M3);
+    const __half2 back(__nv_cvt_fp8x2_to_halfraw2(code, __NV_E4M3));
+    const __half2 rest = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&h), back),
+                                 __float2half2_rn(16.0f));
+    h = *reinterpret_cast<const uint32_t*>(&rest);
+    return code;
 }
 
 // The rest of a wait that is not over at once.  Out of line: the roles' loops together have to
@@ -294,7 +307,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             mbar_init(kv_empty + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full + i, 1);
+            mbar_init(q_full + i, 4);
             mbar_init(q_empty + i, 1);
             mbar_init(s_full + i, 1);
             mbar_init(s_empty + i, C::kTileWarps);
@@ -391,8 +404,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 if (C::kFp8) {
                     const float vs = ok ? vscale[ring] : 1.0f;
                     ks = ok ? kscale[ring] : 0.0f;
-                    lv = log2f(vs);
-                    rv = 0.0625f / vs;
+                    lv = __log2f(vs);
+                    rv = __fdividef(0.0625f, vs);
                     const float* qs = qscale + (iq % kScaleItems) * NH + head0;
 #pragma unroll
                     for (int i = 0; i < HN; i += 2)
@@ -524,14 +537,17 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                                            pack2<T>(x[k + 4], x[k + 5]),
                                            pack2<T>(x[k + 6], x[k + 7]));
                     } else {
+                        uint32_t h[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            h[i] = pack2<__half>(x[c + 2 * i], x[c + 2 * i + 1]);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {    // the weights, then what is left of them
                             uint32_t r[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                float* e = x + c + 4 * i;
-                                const uint32_t lo = e4m3_split(e[0], e[1]);
-                                r[i] = lo | e4m3_split(e[2], e[3]) << 16;
+                                const uint32_t lo = e4m3_split(h[2 * i]);
+                                r[i] = lo | e4m3_split(h[2 * i + 1]) << 16;
                             }
                             *reinterpret_cast<uint4*>(
                                 prow +
@@ -574,10 +590,100 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         const int quad = warp & 3, dim = 32 * quad + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
         const bool parts = p.splits > 1, write = D == 128 || dim < D;
+        // The queries of an item, one item ahead: they are converted (e4m3 caches) or copied into
+        // the operand's layout by these warps, which have little else to do.
+        int q_item = blockIdx.x, nq = 0;                 // next item to load, items loaded
+        auto load_queries = [&] {
+            AttnItem w;
+            for (;; q_item += gridDim.x) {
+                if (q_item >= total)
+                    return true;
+                w = attn_item(p, q_item);
+                if (w.tiles > w.tile)
+                    break;
+            }
+            q_item += gridDim.x;
+            if (!__all_sync(0xFFFFFFFFu, wait(q_empty + (nq & 1), ((nq >> 1) & 1) ^ 1)))
+                return false;
+            const uint8_t* q = p.q + w.t * p.q_row + (int64_t)(w.g * p.group + w.ht * NH) * p.q_head;
+            const int heads = min(NH, p.group - w.ht * NH);
+            uint8_t* dst = qbuf + (nq & 1) * C::kQBytes;
+            const int from = threadIdx.x - 32 * 8;       // of the 128 threads
+            if (!C::kFp8) {
+                constexpr int kPerRow = C::kRow / 16;
+#pragma unroll 1
+                for (int i = from; i < C::kQBytes / 16; i += 128) {
+                    const int h = i / kPerRow, c = i % kPerRow;
+                    const uint32_t off = (c / 8) * (NH * 128) + h * 128 + (c % 8) * 16;
+                    cp_async16(smem_u32(dst) + swizzled<128>(off),
+                               h < heads ? q + h * p.q_head + c * 16 : q, h < heads);
+                }
+                cp_async_commit();
+                cp_async_wait<0>();
+            } else {
+                // A head vector as a sum of e4m3 terms, each 1/16 of the scale of the one before:
+                // two hold the 8 bits of a bf16 element, three the 11 of an fp16 one, down to
+                // 2^-22 of the vector's largest.
+                constexpr int kGroup = D / 16;           // lanes of a vector, 16 elements each
+                const int c = lane % kGroup;
+#pragma unroll 1
+                for (int h = from / kGroup; h < NH; h += 128 / kGroup) {
+                    uint4 in[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+                    if (h < heads) {
+                        const uint4* at = reinterpret_cast<const uint4*>(q + h * p.q_head) + 2 * c;
+                        in[0] = at[0];
+                        in[1] = at[1];
+                    }
+                    const T* e = reinterpret_cast<const T*>(in);
+                    float amax = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        amax = fmaxf(amax, fabsf(value(e[i])));
+#pragma unroll
+                    for (int d = kGroup / 2; d > 0; d >>= 1)
+                        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+                    // a power of two that takes amax to 128..256, so that no element is rounded
+                    const int ex = static_cast<int>(__float_as_uint(amax) >> 23);
+                    const int up = amax > 0.0f ? min(max(261 - ex, 1), 254) : 127;
+                    const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
+                    if (c == 0)                          // (infinite elements give NaN, as they do)
+                        qscale[(nq % kScaleItems) * NH + h] =
+                            amax < INFINITY ? p.scale_log2 / mul : __int_as_float(0x7FFFFFFF);
+                    uint32_t v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        v[i] = pack2<__half>(value(e[2 * i]) * mul, value(e[2 * i + 1]) * mul);
+#pragma unroll
+                    for (int k = 0; k < C::kQTerms; ++k) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t lo = e4m3_split(v[2 * i]);
+                            o[i] = lo | e4m3_split(v[2 * i + 1]) << 16;
+                        }
+                        *reinterpret_cast<uint4*>(
+                            dst + swizzled<C::kAtom>((k * NH + h) * C::kRow + c * 16)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(q_full + (nq & 1));
+            ++nq;
+            return true;
+        };
         int iq = 0;
+        bool loaded = load_queries();
         for (int item = blockIdx.x; item < total; item += gridDim.x) {
             const AttnItem w = attn_item(p, item);
             const int tiles = w.tiles - w.tile, head0 = w.ht * NH;
+            // The next item's queries.  Not for items without tiles: the place waited for is
+            // that of the item before this one, which has left it by now; a later one's would
+            // wait for this very warp.
+            if (tiles > 0 && !(loaded = loaded && load_queries()))
+                break;
             const int heads = parts ? NH : min(NH, p.group - head0);
             uint8_t* out =
                 p.out + w.t * p.out_row + (int64_t)(w.g * p.group + head0) * p.out_head + 2 * dim;
@@ -680,7 +786,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 ++iq;
             }
         }
-    } else if (warp < C::kQueryWarp) {
+    } else if (warp < C::kMmaWarp) {
         // ---------------------------------------------------------------- gather
         // Warp i fills stage i of the ring: it waits for the stage, copies the 128 vectors
         // (zeros for keys that are none), waits for its own copies and signals.  The other
@@ -781,30 +887,33 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     }
                 }
                 const uint8_t* src = kv + g * kv_head;
-                constexpr int kStep = kPerRow < 8 ? kPerRow : 8;
+                // (a span's keys are spread over its lanes: slot i of lane k is key kPerRow i + k)
+                const int from = lane & ~(kPerRow - 1);
+                if (whole) {
+                    constexpr int kStep = kPerRow < 8 ? kPerRow : 8;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int32_t mine = slot[i];
+                    for (int i = 0; i < 4; ++i) {
 #pragma unroll 1
-                    for (int k = 0; k < kPerRow; k += kStep) {
-                        const int row = i * kPerRow + k;
-                        const uint32_t dst = stage + row / 8 * 8 * C::kAtom;
-                        const int from = (lane & ~(kPerRow - 1)) + k;
-                        if (whole) {
+                        for (int k = 0; k < kPerRow; k += kStep) {
+                            const uint32_t dst = stage + (i * kPerRow + k) / 8 * 8 * C::kAtom;
 #pragma unroll
                             for (int x = 0; x < kStep; ++x) {
-                                const uint32_t s = __shfl_sync(0xFFFFFFFFu, mine, from + x);
-                                cp_async16(dst ^ swizzle_of<C::kAtom>((i * kPerRow % 8 + x) * C::kAtom),
-                                           src + (uint64_t)s * kv_slot);
-                            }
-                        } else {
-#pragma unroll 1
-                            for (int x = 0; x < kStep; ++x) {
-                                const int32_t s = __shfl_sync(0xFFFFFFFFu, mine, from + x);
-                                cp_async16(dst ^ swizzle_of<C::kAtom>((row + x) % 8 * C::kAtom),
-                                           src + (uint64_t)(uint32_t)max(s, 0) * kv_slot, s >= 0);
+                                const uint32_t s = __shfl_sync(0xFFFFFFFFu, slot[i], from + k + x);
+                                cp_async16(
+                                    dst ^ swizzle_of<C::kAtom>((i * kPerRow % 8 + x) * C::kAtom),
+                                    src + (uint64_t)s * kv_slot);
                             }
                         }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int row = 0; row < kSpan; ++row) {
+                        const int i = row / kPerRow;
+                        const int32_t mine = i < 2 ? (i ? slot[1] : slot[0]) : i == 2 ? slot[2] : slot[3];
+                        const int32_t s = __shfl_sync(0xFFFFFFFFu, mine, from + row % kPerRow);
+                        cp_async16((stage + row / 8 * 8 * C::kAtom) ^
+                                       swizzle_of<C::kAtom>(row % 8 * C::kAtom),
+                                   src + (uint64_t)(uint32_t)max(s, 0) * kv_slot, s >= 0);
                     }
                 }
                 cp_async_commit();
@@ -821,83 +930,6 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 break;
             locate();
         }
-    } else if (warp == C::kQueryWarp) {
-        // --------------------------------------------------------------- queries
-        int iq = 0;
-        for (int item = blockIdx.x; item < total; item += gridDim.x) {
-            const AttnItem w = attn_item(p, item);
-            if (w.tiles == w.tile)
-                continue;
-            if (!__all_sync(0xFFFFFFFFu, wait(q_empty + (iq & 1), ((iq >> 1) & 1) ^ 1)))
-                break;
-            const uint8_t* q = p.q + w.t * p.q_row + (int64_t)(w.g * p.group + w.ht * NH) * p.q_head;
-            const int heads = min(NH, p.group - w.ht * NH);
-            uint8_t* dst = qbuf + (iq & 1) * C::kQBytes;
-            if (!C::kFp8) {
-                constexpr int kPerRow = C::kRow / 16;
-#pragma unroll 1
-                for (int i = lane; i < C::kQBytes / 16; i += 32) {
-                    const int h = i / kPerRow, c = i % kPerRow;
-                    const uint32_t off = (c / 8) * (NH * 128) + h * 128 + (c % 8) * 16;
-                    cp_async16(smem_u32(dst) + swizzled<128>(off),
-                               h < heads ? q + h * p.q_head + c * 16 : q, h < heads);
-                }
-                cp_async_commit();
-                cp_async_wait<0>();
-            } else {
-                // A head vector as a sum of e4m3 terms, each 1/16 of the scale of the one before:
-                // two hold the 8 bits of a bf16 element, three the 11 of an fp16 one, down to
-                // 2^-22 of the vector's largest.
-                constexpr int kGroup = D / 16;           // lanes of a vector, 16 elements each
-                const int c = lane % kGroup;
-#pragma unroll 1
-                for (int h = lane / kGroup; h < NH; h += 32 / kGroup) {
-                    float v[16];
-                    float amax = 0.0f;
-                    uint4 in[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-                    if (h < heads) {
-                        const uint4* from = reinterpret_cast<const uint4*>(q + h * p.q_head) + 2 * c;
-                        in[0] = from[0];
-                        in[1] = from[1];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        v[i] = value(reinterpret_cast<const T*>(in)[i]);
-                        amax = fmaxf(amax, fabsf(v[i]));
-                    }
-#pragma unroll
-                    for (int d = kGroup / 2; d > 0; d >>= 1)
-                        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-                    // a power of two, so that no element is rounded by it
-                    const int ex = static_cast<int>(__float_as_uint(amax) >> 23);
-                    const int up = amax > 0.0f ? min(max(261 - ex, 1), 254) : 127;
-                    const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
-                    if (c == 0)
-                        qscale[(iq % kScaleItems) * NH + h] =      // (infinite elements give NaN, as they do)
-                            amax < INFINITY ? p.scale_log2 / mul : __int_as_float(0x7FFFFFFF);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        v[i] *= mul;
-#pragma unroll
-                    for (int k = 0; k < C::kQTerms; ++k) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t lo = e4m3_split(v[4 * i], v[4 * i + 1]);
-                            o[i] = lo | e4m3_split(v[4 * i + 2], v[4 * i + 3]) << 16;
-                        }
-                        *reinterpret_cast<uint4*>(
-                            dst + swizzled<C::kAtom>((k * NH + h) * C::kRow + c * 16)) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
-                    }
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(q_full + (iq & 1));
-            ++iq;
-        }
     } else {
         // --------------------------------------------------------------------- MMA
         constexpr int kK = 32 / C::kEb;                 // contraction elements of one MMA
@@ -908,9 +940,9 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         // One elected lane waits and issues.
         if (elect_one()) {
             struct Pending {
-                bool any, fresh, last;                  // fresh: the accumulator is empty
+                bool fresh, last;                       // fresh: the accumulator is empty
                 int j, b, u, iq, n;
-            } pv{false, false, false, 0, 0, 0, 0, 0};
+            };
             const uint64_t k_desc = smem_desc(smem_u32(stages), C::kAtom, 16, 8 * C::kAtom);
             // v rows are keys: both operands of the second product are read along their rows.
             // D = 64 takes the same 64 elements for both halves of the 128 output rows.
@@ -924,13 +956,12 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 else
                     mma_f16(d, a, b, id, acc);
             };
-            // Scores are issued kAhead tiles before the product of their tile, so that the next
-            // ones are ready when a warpgroup is done with its tile.
+            // Scores run kAhead tiles ahead of products, so that the next ones are ready when a
+            // warpgroup is done with its tile; but into a next item only one, since its queries
+            // may wait for the output of the item before this one.
             constexpr int kAhead = C::kTiles > 2 && C::kAlternate ? 2 : 1;
-            Pending queue[kAhead];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                queue[i] = pv;
+            Pending queue[kAhead + 1];                  // tiles scored, without their products
+            int pending = 0;
             int use0 = 0, use1 = 0, n = 0, iq = 0, st = 0, vst = 1;   // stages of the next tiles
             int item = blockIdx.x - gridDim.x, j = 0, count = 0;
             while (true) {
@@ -940,13 +971,12 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     count = w.tiles - w.tile;
                 }
                 const bool more = j < count;
-                const int b = j & 1;
-                const Pending next{more, C::kAlternate ? j < 2 : j == 0, j + 1 == count, j, b,
-                                   b ? use1 : use0, iq, n};
-                if (more) {                             // S = Q K of tile n
+                const bool score = more && pending <= (j == 0 ? 1 : kAhead);
+                if (score) {                            // S = Q K of tile n
+                    const int b = j & 1, u = b ? use1 : use0;
                     if (!((j > 0 || wait(q_full + (iq & 1), (iq >> 1) & 1)) &&
                           wait(kv_full + st, (n / C::kTiles) & 1) &&
-                          wait(s_empty + b, (next.u & 1) ^ 1)))
+                          wait(s_empty + b, (u & 1) ^ 1)))
                         break;
                     tc_fence_after();
                     const uint64_t a0 = k_desc + st * (C::kStage / 16);
@@ -959,7 +989,14 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     }
                     mma_commit(s_full + b);
                     mma_commit(kv_empty + st);
-                    if (next.last) {
+                    const bool last = j + 1 == count;
+                    const Pending next{C::kAlternate ? j < 2 : j == 0, last, j, b, u, iq, n};
+#pragma unroll
+                    for (int i = 0; i <= kAhead; ++i)
+                        if (i == pending)
+                            queue[i] = next;
+                    ++pending;
+                    if (last) {
                         mma_commit(q_empty + (iq & 1));
                         ++iq;
                     }
@@ -969,8 +1006,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     ++n;
                     st = st + 2 == C::kStages ? 0 : st + 2;
                 }
-                pv = queue[0];
-                if (pv.any) {                           // O += P V of the tile kAhead before
+                if (pending > (score ? kAhead : 0)) {   // O += P V of the oldest of them
+                    const Pending pv = queue[0];
                     if (!(wait(kv_full + vst, (pv.n / C::kTiles) & 1) &&
                           (pv.j > 0 || wait(o_empty + (pv.iq & 1), ((pv.iq >> 1) & 1) ^ 1)) &&
                           wait(p_full + pv.b, pv.u & 1)))
@@ -989,15 +1026,12 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     if (pv.last)
                         mma_commit(o_full + (pv.iq & 1));
                     vst = vst + 2 >= C::kStages ? 1 : vst + 2;
-                }
-                bool left = more;
 #pragma unroll
-                for (int i = 0; i + 1 < kAhead; ++i) {
-                    queue[i] = queue[i + 1];
-                    left = left || queue[i].any;
+                    for (int i = 0; i < kAhead; ++i)
+                        queue[i] = queue[i + 1];
+                    --pending;
                 }
-                queue[kAhead - 1] = next;
-                if (!left)
+                if (!more && pending == 0)
                     break;
             }
             // what was issued, and its arrivals, end before the memory goes

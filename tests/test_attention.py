@@ -159,6 +159,7 @@ class Batch:
                                    torch.from_numpy(self.lens).cuda(), out, ws, k_scale=c(self.ks),
                                    v_scale=c(self.vs), sel_count=c(self.count),
                                    page_table=c(self.table), lse=lse)
+        assert K.indexer_status(None, ws) == K.IDX_OK
         return out, lse
 
     def check(self, scale=None, **kw):
