@@ -38,10 +38,10 @@ constexpr int kModeBf16 = 0, kModeFp16 = 1, kModeFp8Bf16 = 2, kModeFp8Fp16 = 3;
 
 constexpr long long kWaitCycles = 4000000000LL;   // about two seconds
 constexpr int kSmemLimit = 232448;
-// Items whose query scales are held.  No barrier guards them: the scales of item i + 8 are
-// written after the scores of item i + 6, at least five tiles past the last of item i, were
-// issued, and scores are issued at most three tiles ahead of a tile's weights.
-constexpr int kScaleItems = 8;
+// Items whose query scales are held.  No barrier guards them: the scales of item i + 4 are
+// written after the scores of item i + 2's last tile were issued, and the scores of a tile are
+// issued after those of the tile two before were read.
+constexpr int kScaleItems = 4;
 
 template <int D, int NH, int MODE>
 struct AttnCfg {
@@ -74,14 +74,14 @@ struct AttnCfg {
     static constexpr int kMax = 2 * kHeads * 4;         // maxima by warpgroup
     static constexpr int kQScale = kFp8 ? kScaleItems * NH * 4 : 0;
     static constexpr int kKeyInfo = kAttnTile * (kFp8 ? 9 : 1);   // of a tile, 2 kTiles of them
-    static constexpr int kFixed = kStats + kMax + kQScale + 2 * kPBytes + 2 * kQBytes + 8 * 20;
+    static constexpr int kFixed = kStats + kMax + kQScale + 2 * kPBytes + 2 * kQBytes + 8 * 21;
     static constexpr int kFit =
         (kSmemLimit - kFixed) / (2 * kStage + 2 * kKeyInfo + 8 * 4);
     static constexpr int kTiles = kFit < 3 ? kFit : 3;  // tiles in the ring
     static constexpr int kStages = 2 * kTiles;          // and as many warps that fill them
     static constexpr int kSmem = kFixed + kTiles * (2 * kStage + 2 * kKeyInfo + 8 * 4);
     static constexpr int kGatherWarp = 8 + 4, kMmaWarp = kGatherWarp + kStages;
-    static constexpr int kThreads = 32 * (kMmaWarp + 1);
+    static constexpr int kThreads = 32 * (kMmaWarp + 2);
     static_assert(kCols <= 512 && kTiles >= 2 && kSmem <= kSmemLimit, "tile does not fit");
 };
 
@@ -296,7 +296,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
     uint64_t* f_full = o_empty + 2;                            // sums and maxima
     uint64_t* f_empty = f_full + 1;
     uint64_t* drained = f_empty + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
     volatile int* ab = reinterpret_cast<volatile int*>(tmem_slot + 1);   // a wait gave up
 
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x / 32), 0);
@@ -319,6 +319,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         mbar_init(f_full, 8);
         mbar_init(f_empty, 4);
         mbar_init(drained, 1);
+        mbar_init(drained + 1, 1);
         // the swizzled tiles need their 1024-byte boundaries
         *ab = (smem_u32(sm) & 1023u) != 0;
         fence_mbar_init();
@@ -340,7 +341,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return mbar_try_wait(bar, parity) || wait_on(bar, parity, ab, p.status);
     };
-    // Tiles of an item use the score and weight buffers alternately, from buffer 0 on.
+    // Tiles, numbered over the block's items, use the score and weight buffers alternately.
 
     if (warp < 8) {
         // ---------------------------------------------------------------- softmax
@@ -362,7 +363,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 swizzled<C::kPRow>(i / per * C::kPRow + head0 * C::kEb + i % per * 4));
         };
         bool bad = false;
-        int n = 0, iq = 0, use0 = 0, use1 = 0;           // uses of the buffers
+        int n = 0, iq = 0;                               // tiles and items before this item
         for (int item = blockIdx.x; item < total; item += gridDim.x) {
             const AttnItem w = attn_item(p, item);
             const int count = w.tiles - w.tile;
@@ -374,8 +375,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 l[i] = 0.0f;
             bool first = true, leave = false;
 #pragma unroll 1
-            for (int j = C::kAlternate ? wg : 0; j < count; j += C::kAlternate ? 2 : 1) {
-                const int b = j & 1, u = b ? use1 : use0;
+            for (int j = C::kAlternate ? (wg ^ n) & 1 : 0; j < count; j += C::kAlternate ? 2 : 1) {
+                const int b = (n + j) & 1, u = (n + j) >> 1;
                 bad |= !wait(s_full + b, u & 1);
                 tc_fence_after();
                 float x[HN];
@@ -449,7 +450,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     // the products so far are complete, the buffer is free
                     bad |= !wait(p_empty + b, (u & 1) ^ 1);
                     if (!C::kAlternate && !first)
-                        bad |= !wait(p_empty + (b ^ 1), ((b ? use0 : use1) - 1) & 1);
+                        bad |= !wait(p_empty + (b ^ 1), ((n + j - 1) >> 1) & 1);
                     if (!first) {
 #pragma unroll
                         for (int i = 0; i < HN; ++i)
@@ -560,10 +561,6 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(p_full + b);
-                if (b)
-                    ++use1;
-                else
-                    ++use0;
             }
             if (leave)
                 break;
@@ -674,7 +671,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             ++nq;
             return true;
         };
-        int iq = 0;
+        int n = 0, iq = 0;                               // tiles and items before this item
         bool loaded = load_queries();
         for (int item = blockIdx.x; item < total; item += gridDim.x) {
             const AttnItem w = attn_item(p, item);
@@ -741,7 +738,9 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     o[i] = 0.0f;
                 const float f = NH > 32 && h0 >= 32 ? fa[NH / 64] : fa[0];
 #pragma unroll 1
-                for (int a = 0; a < C::kAccs && a < tiles; ++a) {
+                for (int a = 0; a < C::kAccs && tiles > 0; ++a) {
+                    if (tiles == 1 && C::kAlternate && a != (n & 1))
+                        continue;                        // it was not written
                     const uint32_t at =
                         tmem_o + lanes + ((iq & 1) * C::kAccs + a) * C::kOCols + h0;
                     const float fac = a == 0 ? f : fb;
@@ -783,6 +782,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(o_empty + (iq & 1));
+                n += tiles;
                 ++iq;
             }
         }
@@ -871,9 +871,9 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 if (!__all_sync(0xFFFFFFFFu, wait(kv_empty + pw, (u & 1) ^ 1)))
                     break;
                 if (!is_v) {
-                    // What the softmax has to know of the keys.  The place was last read for the
-                    // tile 2 kTiles before, whose scores left their buffer before the products of
-                    // the tile kTiles before were begun; those have freed the stage.
+                    // What the softmax has to know of the keys.  No barrier guards the place, last
+                    // read for the tile n - 2 kTiles: the scores of tile n - kTiles have freed the
+                    // stage, and were issued after those of tile n - kTiles - 2 were read.
                     const int ring = (u * C::kTiles + pw / 2) % C::kStages * kAttnTile;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -932,112 +932,96 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         }
     } else {
         // --------------------------------------------------------------------- MMA
+        // One elected lane of a warp for the scores, and of another for the products: each waits
+        // and issues.  (One thread for both took 1,400 cycles a tile for its own instructions.)
         constexpr int kK = 32 / C::kEb;                 // contraction elements of one MMA
-        constexpr uint32_t idesc_s =
-            idesc_dense(128, C::kQRows, MODE == kModeBf16 ? 1 : 0, false, false);
-        constexpr uint32_t idesc_o =
-            idesc_dense(128, C::kOCols, MODE == kModeBf16 ? 1 : 0, true, true);
-        // One elected lane waits and issues.
+        const bool scores = warp == C::kMmaWarp;
+        auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+            if (C::kFp8)
+                mma_f8f6f4(d, a, b, id, acc);
+            else
+                mma_f16(d, a, b, id, acc);
+        };
         if (elect_one()) {
-            struct Pending {
-                bool fresh, last;                       // fresh: the accumulator is empty
-                int j, b, u, iq, n;
-            };
-            const uint64_t k_desc = smem_desc(smem_u32(stages), C::kAtom, 16, 8 * C::kAtom);
-            // v rows are keys: both operands of the second product are read along their rows.
-            // D = 64 takes the same 64 elements for both halves of the 128 output rows.
-            constexpr uint32_t lbo = D == 64 ? 0 : kAttnTile * C::kAtom;
-            const uint64_t v_desc = smem_desc(smem_u32(stages), C::kAtom, lbo, 8 * C::kAtom);
-            const uint64_t q_desc = smem_desc(smem_u32(qbuf), C::kAtom, 16, 8 * C::kAtom);
-            const uint64_t p_desc = smem_desc(smem_u32(pbuf), C::kPRow, 0, 8 * C::kPRow);
-            auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-                if (C::kFp8)
-                    mma_f8f6f4(d, a, b, id, acc);
-                else
-                    mma_f16(d, a, b, id, acc);
-            };
-            // Scores run kAhead tiles ahead of products, so that the next ones are ready when a
-            // warpgroup is done with its tile; but into a next item only one, since its queries
-            // may wait for the output of the item before this one.
-            constexpr int kAhead = C::kTiles > 2 && C::kAlternate ? 2 : 1;
-            Pending queue[kAhead + 1];                  // tiles scored, without their products
-            int pending = 0;
-            int use0 = 0, use1 = 0, n = 0, iq = 0, st = 0, vst = 1;   // stages of the next tiles
-            int item = blockIdx.x - gridDim.x, j = 0, count = 0;
-            while (true) {
-                while (j >= count && (item += gridDim.x) < total) {
-                    const AttnItem w = attn_item<true>(p, item);
-                    j = 0;
-                    count = w.tiles - w.tile;
-                }
-                const bool more = j < count;
-                const bool score = more && pending <= (j == 0 ? 1 : kAhead);
-                if (score) {                            // S = Q K of tile n
-                    const int b = j & 1, u = b ? use1 : use0;
-                    if (!((j > 0 || wait(q_full + (iq & 1), (iq >> 1) & 1)) &&
-                          wait(kv_full + st, (n / C::kTiles) & 1) &&
-                          wait(s_empty + b, (u & 1) ^ 1)))
-                        break;
-                    tc_fence_after();
-                    const uint64_t a0 = k_desc + st * (C::kStage / 16);
-                    const uint64_t b0 = q_desc + (iq & 1) * (C::kQBytes / 16);
+            int n = 0, iq = 0, st = 0;                  // tile n's place in the ring
+            uint32_t phase = 0;                         // and the uses of that place
+            bool ok = true;
+            for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+                const AttnItem w = attn_item<true>(p, item);
+                const int count = w.tiles - w.tile;
+                if (count == 0)
+                    continue;
+                if (scores) {                           // S = Q K
+                    constexpr uint32_t idesc =
+                        idesc_dense(128, C::kQRows, MODE == kModeBf16 ? 1 : 0, false, false);
+                    const uint64_t q_desc =
+                        smem_desc(smem_u32(qbuf + (iq & 1) * C::kQBytes), C::kAtom, 16, 8 * C::kAtom);
+                    ok = wait(q_full + (iq & 1), (iq >> 1) & 1);
+                    for (int j = 0; j < count && ok; ++j, ++n) {
+                        ok = wait(kv_full + 2 * st, phase) &&
+                             wait(s_empty + (n & 1), ((n >> 1) & 1) ^ 1);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        const uint64_t k_desc = smem_desc(smem_u32(stages + 2 * st * C::kStage),
+                                                          C::kAtom, 16, 8 * C::kAtom);
 #pragma unroll
-                    for (int k = 0; k < D / kK; ++k) {
-                        const int atom = k * 32 / C::kAtom, in = (k * 32) % C::kAtom;
-                        mma(tmem_s + b * C::kSCols, a0 + (atom * (kAttnTile * C::kAtom) + in) / 16,
-                            b0 + (atom * (C::kQRows * C::kAtom) + in) / 16, idesc_s, k > 0);
+                        for (int k = 0; k < D / kK; ++k) {
+                            const int atom = k * 32 / C::kAtom, in = (k * 32) % C::kAtom;
+                            mma(tmem_s + (n & 1) * C::kSCols,
+                                k_desc + (atom * (kAttnTile * C::kAtom) + in) / 16,
+                                q_desc + (atom * (C::kQRows * C::kAtom) + in) / 16, idesc, k > 0);
+                        }
+                        mma_commit(s_full + (n & 1));
+                        mma_commit(kv_empty + 2 * st);
+                        if (++st == C::kTiles) {
+                            st = 0;
+                            phase ^= 1;
+                        }
                     }
-                    mma_commit(s_full + b);
-                    mma_commit(kv_empty + st);
-                    const bool last = j + 1 == count;
-                    const Pending next{C::kAlternate ? j < 2 : j == 0, last, j, b, u, iq, n};
-#pragma unroll
-                    for (int i = 0; i <= kAhead; ++i)
-                        if (i == pending)
-                            queue[i] = next;
-                    ++pending;
-                    if (last) {
+                    if (ok)
                         mma_commit(q_empty + (iq & 1));
-                        ++iq;
+                } else {                                // O += P V
+                    constexpr uint32_t idesc =
+                        idesc_dense(128, C::kOCols, MODE == kModeBf16 ? 1 : 0, true, true);
+                    // v rows are keys: both operands are read along their rows.  D = 64 takes the
+                    // same 64 elements for both halves of the 128 output rows.
+                    constexpr uint32_t lbo = D == 64 ? 0 : kAttnTile * C::kAtom;
+                    ok = wait(o_empty + (iq & 1), ((iq >> 1) & 1) ^ 1);
+                    for (int j = 0; j < count && ok; ++j, ++n) {
+                        const int b = n & 1;
+                        ok = wait(kv_full + 2 * st + 1, phase) && wait(p_full + b, (n >> 1) & 1);
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        const uint64_t v_desc = smem_desc(
+                            smem_u32(stages + (2 * st + 1) * C::kStage), C::kAtom, lbo, 8 * C::kAtom);
+                        const uint64_t p_desc =
+                            smem_desc(smem_u32(pbuf + b * C::kPBytes), C::kPRow, 0, 8 * C::kPRow);
+                        const uint32_t d =
+                            tmem_o + ((iq & 1) * C::kAccs + (C::kAlternate ? b : 0)) * C::kOCols;
+                        const bool fresh = C::kAlternate ? j < 2 : j == 0;   // an empty accumulator
+#pragma unroll
+                        for (int k = 0; k < kAttnTile / kK; ++k)
+                            mma(d, v_desc + k * (kK * C::kAtom / 16),
+                                p_desc + k * (kK * C::kPRow / 16), idesc, !fresh || k > 0);
+                        mma_commit(p_empty + b);
+                        mma_commit(kv_empty + 2 * st + 1);
+                        if (++st == C::kTiles) {
+                            st = 0;
+                            phase ^= 1;
+                        }
                     }
-                    use0 += b == 0;
-                    use1 += b;
-                    ++j;
-                    ++n;
-                    st = st + 2 == C::kStages ? 0 : st + 2;
+                    if (ok)
+                        mma_commit(o_full + (iq & 1));
                 }
-                if (pending > (score ? kAhead : 0)) {   // O += P V of the oldest of them
-                    const Pending pv = queue[0];
-                    if (!(wait(kv_full + vst, (pv.n / C::kTiles) & 1) &&
-                          (pv.j > 0 || wait(o_empty + (pv.iq & 1), ((pv.iq >> 1) & 1) ^ 1)) &&
-                          wait(p_full + pv.b, pv.u & 1)))
-                        break;
-                    tc_fence_after();
-                    const uint64_t a0 = v_desc + vst * (C::kStage / 16);
-                    const uint64_t b0 = p_desc + pv.b * (C::kPBytes / 16);
-                    const uint32_t d =
-                        tmem_o + ((pv.iq & 1) * C::kAccs + (C::kAlternate ? pv.b : 0)) * C::kOCols;
-#pragma unroll
-                    for (int k = 0; k < kAttnTile / kK; ++k)
-                        mma(d, a0 + k * (kK * C::kAtom / 16), b0 + k * (kK * C::kPRow / 16),
-                            idesc_o, !pv.fresh || k > 0);
-                    mma_commit(kv_empty + vst);
-                    mma_commit(p_empty + pv.b);
-                    if (pv.last)
-                        mma_commit(o_full + (pv.iq & 1));
-                    vst = vst + 2 >= C::kStages ? 1 : vst + 2;
-#pragma unroll
-                    for (int i = 0; i < kAhead; ++i)
-                        queue[i] = queue[i + 1];
-                    --pending;
-                }
-                if (!more && pending == 0)
-                    break;
+                ++iq;
             }
             // what was issued, and its arrivals, end before the memory goes
-            mma_commit(drained);
+            uint64_t* mine = drained + (scores ? 0 : 1);
+            mma_commit(mine);
             volatile int never = 0;
-            mbar_wait(drained, 0, kWaitCycles, &never);
+            mbar_wait(mine, 0, kWaitCycles, &never);
         }
         __syncwarp();
     }
