@@ -351,9 +351,13 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         const int head0 = C::kAlternate ? 0 : HN * wg;
         float* mx = maxima + wg * HN;
         // Weights are kept relative to a running maximum that is replaced only where a score
-        // passes it by 2^kSlack: most tiles need no exchange over the keys and no rescaling
-        // of the accumulated output.  (e4m3 weights, times 16, have to stay below 448.)
-        constexpr float kSlack = C::kFp8 ? 4.0f : 8.0f;
+        // passes it by kSlack: most tiles need no exchange over the keys and no rescaling of
+        // the accumulated output.  bf16 weights and fp32 sums lose nothing at any scale, so
+        // there an item goes by 0 instead of its maxima until a score leaves +-64 (an exchange
+        // for each item's first tile cost a tenth of its time).  fp16 weights have to stay
+        // below 2^16, and e4m3 ones, times 16, below 448.
+        constexpr bool kZeroStart = MODE == kModeBf16;
+        constexpr float kSlack = C::kFp8 ? 4.0f : MODE == kModeFp16 ? 8.0f : 64.0f;
         // the thread's heads in a row of the weights, and the row's part of them as scratch
         constexpr int kOwn = HN * C::kEb;                // bytes of a term
         auto scratch = [&](int b, int i) {               // float i of 4 HN
@@ -373,7 +377,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
 #pragma unroll
             for (int i = 0; i < HN; ++i)
                 l[i] = 0.0f;
-            bool first = true, leave = false;
+            bool first = true, leave = false, based = !kZeroStart;   // based: mx holds the maxima
 #pragma unroll 1
             for (int j = C::kAlternate ? (wg ^ n) & 1 : 0; j < count; j += C::kAlternate ? 2 : 1) {
                 const int b = (n + j) & 1, u = (n + j) >> 1;
@@ -415,12 +419,19 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 const bool all = __all_sync(0xFFFFFFFFu, ok);
                 if (lane == 0)
                     mbar_arrive(s_empty + b);
-                // Exponents relative to the running maximum (as they are in the first tile).
+                // Exponents, relative to the running maximum where there is one.
                 float over = -INFINITY;
-                if (first) {
+                if (kZeroStart ? !based : first) {
 #pragma unroll
-                    for (int i = 0; i < HN; ++i)
-                        x[i] = fmaf(x[i], ks, lv);
+                    for (int i = 0; i < HN; i += 2) {
+                        if (C::kFp8)
+                            fma2(x[i], x[i + 1], ks, ks, lv, lv);
+                        else
+                            mul2(x[i], x[i + 1], ks, ks);
+                        if (kZeroStart)
+                            over = fmaxf(over, fmaxf(fabsf(x[i]), fabsf(x[i + 1])));
+                    }
+                    over = ok ? over : -INFINITY;
                 } else {
 #pragma unroll
                     for (int i = 0; i < HN; i += 2) {
@@ -430,28 +441,26 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                             m1 -= lv;
                         }
                         fma2(x[i], x[i + 1], ks, ks, -m0, -m1);
+                        over = fmaxf(over, fmaxf(x[i], x[i + 1]));
                     }
+                    over = ok ? over : -INFINITY;
                 }
                 if (!all) {
 #pragma unroll
                     for (int i = 0; i < HN; ++i)
                         x[i] = ok ? x[i] : -INFINITY;
                 }
-                if (!first) {
-#pragma unroll
-                    for (int i = 0; i < HN; i += 2)
-                        over = fmaxf(over, fmaxf(x[i], x[i + 1]));
-                }
                 bool waited = false;
-                if (first || bar_any(over > kSlack || bad, bar_id, 128)) {
+                if ((first && !kZeroStart) || bar_any(over > kSlack || bad, bar_id, 128)) {
                     waited = true;
-                    if (first)
-                        bad |= !wait(f_empty, (iq & 1) ^ 1);     // the last item's were read
+                    // (maxima of the item before have been read)
+                    if (first || !based)
+                        bad |= !wait(f_empty, (iq & 1) ^ 1);
                     // the products so far are complete, the buffer is free
                     bad |= !wait(p_empty + b, (u & 1) ^ 1);
                     if (!C::kAlternate && !first)
                         bad |= !wait(p_empty + (b ^ 1), ((n + j - 1) >> 1) & 1);
-                    if (!first) {
+                    if (!first && based) {
 #pragma unroll
                         for (int i = 0; i < HN; ++i)
                             x[i] += mx[i];
@@ -467,7 +476,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                         break;
                     }
                     if (key < HN) {
-                        const float old = first ? -3.0e38f : mx[key];
+                        const float old = first ? -3.0e38f : based ? mx[key] : 0.0f;
                         const float mn = fmaxf(
                             fmaxf(fmaxf(old, *scratch(b, key)), *scratch(b, HN + key)),
                             fmaxf(*scratch(b, 2 * HN + key), *scratch(b, 3 * HN + key)));
@@ -511,8 +520,9 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                         tc_fence_before();
                         bar_all(true, bar_id, 128);      // the factors have been read
                     }
-                    first = false;
+                    based = true;
                 }
+                first = false;
                 // e4m3 weights are 16 times the weight
 #pragma unroll
                 for (int i = 0; i < HN; ++i)
@@ -564,10 +574,10 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             }
             if (leave)
                 break;
-            if (first) {                                 // no tile of this item
+            if (first || !based) {                       // no tile of this item, or no maxima
                 bad |= !wait(f_empty, (iq & 1) ^ 1);
                 if (key < HN)
-                    mx[key] = -3.0e38f;
+                    mx[key] = first ? -3.0e38f : 0.0f;
             }
 #pragma unroll
             for (int c = 0; c < HN; c += 16) {
@@ -672,14 +682,17 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             return true;
         };
         int n = 0, iq = 0;                               // tiles and items before this item
-        bool loaded = load_queries();
         for (int item = blockIdx.x; item < total; item += gridDim.x) {
             const AttnItem w = attn_item(p, item);
             const int tiles = w.tiles - w.tile, head0 = w.ht * NH;
-            // The next item's queries.  Not for items without tiles: the place waited for is
-            // that of the item before this one, which has left it by now; a later one's would
-            // wait for this very warp.
-            if (tiles > 0 && !(loaded = loaded && load_queries()))
+            // The next item's queries (and before the first item its own).  Not for items without
+            // tiles: the place waited for is that of the item before this one, which has left
+            // it by now; a later one's would wait for this very warp.
+            bool loaded = true;
+#pragma unroll 1
+            for (int k = tiles == 0 ? 0 : iq == 0 ? 2 : 1; k > 0; --k)
+                loaded = loaded && load_queries();
+            if (!loaded)
                 break;
             const int heads = parts ? NH : min(NH, p.group - head0);
             uint8_t* out =
@@ -714,10 +727,10 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                             make_float2(m, l);
                     else if (p.lse)
                         p.lse[(int64_t)w.t * p.Hq + w.g * p.group + head0 + h] =
-                            (m + log2f(l)) * 0.693147180559945309f;
+                            (m + __log2f(l)) * 0.693147180559945309f;
                 }
                 const float inv = (C::kFp8 ? 0.0625f : 1.0f) *
-                                  (parts ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l);
+                                  (parts ? 1.0f : l == 0.0f ? 0.0f : __fdividef(1.0f, l));
                 fa[k] *= inv;
                 fb *= inv;
             }
@@ -887,30 +900,33 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     }
                 }
                 const uint8_t* src = kv + g * kv_head;
-                // (a span's keys are spread over its lanes: slot i of lane k is key kPerRow i + k)
+                // A span's keys are spread over its lanes: slot i of lane k is key kPerRow i + k.
+                // (eight rows at a time, for the instruction cache)
                 const int from = lane & ~(kPerRow - 1);
+                auto pick = [&](int i) {
+                    const int32_t lo = i & 1 ? slot[1] : slot[0], hi = i & 1 ? slot[3] : slot[2];
+                    return i & 2 ? hi : lo;
+                };
                 if (whole) {
-                    constexpr int kStep = kPerRow < 8 ? kPerRow : 8;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
 #pragma unroll 1
-                        for (int k = 0; k < kPerRow; k += kStep) {
-                            const uint32_t dst = stage + (i * kPerRow + k) / 8 * 8 * C::kAtom;
+                    for (int row = 0; row < kSpan; row += 8) {
+                        const int32_t a = pick(row / kPerRow);
+                        const int32_t b = kPerRow < 8 ? pick(row / kPerRow + 1) : a;
+                        const uint32_t dst = stage + row * C::kAtom;
+                        const int lane0 = from + row % kPerRow;
 #pragma unroll
-                            for (int x = 0; x < kStep; ++x) {
-                                const uint32_t s = __shfl_sync(0xFFFFFFFFu, slot[i], from + k + x);
-                                cp_async16(
-                                    dst ^ swizzle_of<C::kAtom>((i * kPerRow % 8 + x) * C::kAtom),
-                                    src + (uint64_t)s * kv_slot);
-                            }
+                        for (int x = 0; x < 8; ++x) {
+                            const uint32_t s = __shfl_sync(0xFFFFFFFFu, x < kPerRow ? a : b,
+                                                           lane0 + x % kPerRow);
+                            cp_async16(dst ^ swizzle_of<C::kAtom>(x * C::kAtom),
+                                       src + (uint64_t)s * kv_slot);
                         }
                     }
                 } else {
 #pragma unroll 1
                     for (int row = 0; row < kSpan; ++row) {
-                        const int i = row / kPerRow;
-                        const int32_t mine = i < 2 ? (i ? slot[1] : slot[0]) : i == 2 ? slot[2] : slot[3];
-                        const int32_t s = __shfl_sync(0xFFFFFFFFu, mine, from + row % kPerRow);
+                        const int32_t s =
+                            __shfl_sync(0xFFFFFFFFu, pick(row / kPerRow), from + row % kPerRow);
                         cp_async16((stage + row / 8 * 8 * C::kAtom) ^
                                        swizzle_of<C::kAtom>(row % 8 * C::kAtom),
                                    src + (uint64_t)(uint32_t)max(s, 0) * kv_slot, s >= 0);
