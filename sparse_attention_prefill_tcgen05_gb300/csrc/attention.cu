@@ -72,7 +72,7 @@ struct AttnCfg {
     // Shared memory after the stages, the weights and the queries.
     static constexpr int kStats = 2 * 4 * kHeads * 4;   // sums by warpgroup and quadrant
     static constexpr int kMax = 2 * kHeads * 4;         // maxima by warpgroup
-    static constexpr int kQScale = kFp8 ? kScaleItems * NH * 4 : 0;
+    static constexpr int kQScale = kFp8 ? (kScaleItems + 4) * 4 : 0;
     static constexpr int kKeyInfo = kAttnTile * (kFp8 ? 9 : 1);   // of a tile, 2 kTiles of them
     static constexpr int kFixed = kStats + kMax + kQScale + 2 * kPBytes + 2 * kQBytes + 8 * 21;
     static constexpr int kFit =
@@ -279,7 +279,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
     // [2 warpgroups][4 quadrants][HN] sums of an item, [2][HN] running maxima
     float* sums = reinterpret_cast<float*>(qbuf + 2 * C::kQBytes);
     float* maxima = sums + C::kStats / 4;
-    float* qscale = maxima + C::kMax / 4;                      // [kScaleItems][NH]
+    float* qscale = maxima + C::kMax / 4;                      // [kScaleItems], 4 of scratch
     float* kscale = qscale + C::kQScale / 4;                   // [2 kTiles][128]
     float* vscale = kscale + (C::kFp8 ? C::kStages * kAttnTile : 0);
     uint8_t* valid = reinterpret_cast<uint8_t*>(vscale + (C::kFp8 ? C::kStages * kAttnTile : 0));
@@ -355,9 +355,11 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         // the accumulated output.  bf16 weights and fp32 sums lose nothing at any scale, so
         // there an item goes by 0 instead of its maxima until a score leaves +-64 (an exchange
         // for each item's first tile cost a tenth of its time).  fp16 weights have to stay
-        // below 2^16, and e4m3 ones, times 16, below 448.
+        // below 2^16.  e4m3 ones have to stay below 448, and their terms reach down to 2^-13: they
+        // go by 2^-4 of the maximum, so that it has weight 16.
         constexpr bool kZeroStart = MODE == kModeBf16;
-        constexpr float kSlack = C::kFp8 ? 4.0f : MODE == kModeFp16 ? 8.0f : 64.0f;
+        constexpr float kSlack = MODE == kModeBf16 ? 64.0f : 8.0f;
+        constexpr float kBelow = C::kFp8 ? 4.0f : 0.0f;
         // the thread's heads in a row of the weights, and the row's part of them as scratch
         constexpr int kOwn = HN * C::kEb;                // bytes of a term
         auto scratch = [&](int b, int i) {               // float i of 4 HN
@@ -396,8 +398,9 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                             tmem_ld_32x32b_x16(tmem_s + lanes + b * C::kSCols + k * NH + head0 + c, r);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                x[c + i] = fmaf(r[i], k == 1 ? 0.0625f : 0.00390625f, x[c + i]);
+                            for (int i = 0; i < 16; i += 2)
+                                add2_scaled(x[c + i], x[c + i + 1], r[i], r[i + 1],
+                                            k == 1 ? 0.0625f : 0.00390625f);
                         }
                     }
                 }
@@ -408,13 +411,9 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 float ks = p.scale_log2, lv = 0.0f, rv = 1.0f;
                 if (C::kFp8) {
                     const float vs = ok ? vscale[ring] : 1.0f;
-                    ks = ok ? kscale[ring] : 0.0f;
+                    ks = ok ? kscale[ring] * qscale[iq % kScaleItems] : 0.0f;
                     lv = __log2f(vs);
-                    rv = __fdividef(0.0625f, vs);
-                    const float* qs = qscale + (iq % kScaleItems) * NH + head0;
-#pragma unroll
-                    for (int i = 0; i < HN; i += 2)
-                        mul2(x[i], x[i + 1], qs[i], qs[i + 1]);
+                    rv = __fdividef(1.0f, vs);
                 }
                 const bool all = __all_sync(0xFFFFFFFFu, ok);
                 if (lane == 0)
@@ -478,8 +477,9 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     if (key < HN) {
                         const float old = first ? -3.0e38f : based ? mx[key] : 0.0f;
                         const float mn = fmaxf(
-                            fmaxf(fmaxf(old, *scratch(b, key)), *scratch(b, HN + key)),
-                            fmaxf(*scratch(b, 2 * HN + key), *scratch(b, 3 * HN + key)));
+                            old, fmaxf(fmaxf(*scratch(b, key), *scratch(b, HN + key)),
+                                       fmaxf(*scratch(b, 2 * HN + key), *scratch(b, 3 * HN + key))) -
+                                     kBelow);
                         *scratch(b, key) = ex2(old - mn);
                         mx[key] = mn;
                     }
@@ -523,10 +523,9 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     based = true;
                 }
                 first = false;
-                // e4m3 weights are 16 times the weight
 #pragma unroll
                 for (int i = 0; i < HN; ++i)
-                    x[i] = ex2(C::kFp8 ? x[i] + 4.0f : x[i]);
+                    x[i] = ex2(x[i]);
 #pragma unroll
                 for (int i = 0; i < HN; i += 2) {
                     if (C::kFp8)
@@ -610,7 +609,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     break;
             }
             q_item += gridDim.x;
-            if (!__all_sync(0xFFFFFFFFu, wait(q_empty + (nq & 1), ((nq >> 1) & 1) ^ 1)))
+            // (agreed on by the four warps: they meet below)
+            if (!bar_all(wait(q_empty + (nq & 1), ((nq >> 1) & 1) ^ 1), 3, 128))
                 return false;
             const uint8_t* q = p.q + w.t * p.q_row + (int64_t)(w.g * p.group + w.ht * NH) * p.q_head;
             const int heads = min(NH, p.group - w.ht * NH);
@@ -628,49 +628,63 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 cp_async_commit();
                 cp_async_wait<0>();
             } else {
-                // A head vector as a sum of e4m3 terms, each 1/16 of the scale of the one before:
-                // two hold the 8 bits of a bf16 element, three the 11 of an fp16 one, down to
-                // 2^-22 of the vector's largest.
+                // The queries as sums of e4m3 terms, each 1/16 of the scale of the one before: two
+                // hold the 8 bits of a bf16 element, three the 11 of an fp16 one, down to 2^-22 of
+                // the item's largest.  First its magnitude, then the terms.
                 constexpr int kGroup = D / 16;           // lanes of a vector, 16 elements each
                 const int c = lane % kGroup;
+                float amax = 0.0f, mul = 1.0f;
 #pragma unroll 1
-                for (int h = from / kGroup; h < NH; h += 128 / kGroup) {
-                    uint4 in[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-                    if (h < heads) {
+                for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+                    for (int h = from / kGroup; h < heads; h += 128 / kGroup) {
                         const uint4* at = reinterpret_cast<const uint4*>(q + h * p.q_head) + 2 * c;
-                        in[0] = at[0];
-                        in[1] = at[1];
-                    }
-                    const T* e = reinterpret_cast<const T*>(in);
-                    float amax = 0.0f;
+                        const uint4 in[2] = {at[0], at[1]};
+                        const T* e = reinterpret_cast<const T*>(in);
+                        if (pass == 0) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        amax = fmaxf(amax, fabsf(value(e[i])));
-#pragma unroll
-                    for (int d = kGroup / 2; d > 0; d >>= 1)
-                        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-                    // a power of two that takes amax to 128..256, so that no element is rounded
-                    const int ex = static_cast<int>(__float_as_uint(amax) >> 23);
-                    const int up = amax > 0.0f ? min(max(261 - ex, 1), 254) : 127;
-                    const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
-                    if (c == 0)                          // (infinite elements give NaN, as they do)
-                        qscale[(nq % kScaleItems) * NH + h] =
-                            amax < INFINITY ? p.scale_log2 / mul : __int_as_float(0x7FFFFFFF);
-                    uint32_t v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[i] = pack2<__half>(value(e[2 * i]) * mul, value(e[2 * i + 1]) * mul);
-#pragma unroll
-                    for (int k = 0; k < C::kQTerms; ++k) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t lo = e4m3_split(v[2 * i]);
-                            o[i] = lo | e4m3_split(v[2 * i + 1]) << 16;
+                            for (int i = 0; i < 16; ++i) {
+                                const float m = fabsf(value(e[i]));
+                                amax = fmaxf(amax, m < INFINITY ? m : 0.0f);
+                            }
+                            continue;
                         }
-                        *reinterpret_cast<uint4*>(
-                            dst + swizzled<C::kAtom>((k * NH + h) * C::kRow + c * 16)) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
+                        uint32_t v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            // (+ 0 x: an infinite element makes its head NaN)
+                            const float a = value(e[2 * i]), b = value(e[2 * i + 1]);
+                            v[i] = pack2<__half>(fmaf(a, 0.0f, a * mul), fmaf(b, 0.0f, b * mul));
+                        }
+#pragma unroll
+                        for (int k = 0; k < C::kQTerms; ++k) {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t lo = e4m3_split(v[2 * i]);
+                                o[i] = lo | e4m3_split(v[2 * i + 1]) << 16;
+                            }
+                            *reinterpret_cast<uint4*>(
+                                dst + swizzled<C::kAtom>((k * NH + h) * C::kRow + c * 16)) =
+                                make_uint4(o[0], o[1], o[2], o[3]);
+                        }
+                    }
+                    if (pass == 0) {
+                        float* four = qscale + kScaleItems;
+#pragma unroll
+                        for (int d = 16; d > 0; d >>= 1)
+                            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+                        if (lane == 0)
+                            four[quad] = amax;
+                        bar_all(true, 3, 128);
+                        amax = fmaxf(fmaxf(four[0], four[1]), fmaxf(four[2], four[3]));
+                        bar_all(true, 3, 128);
+                        // a power of two that takes amax to 128..256, so that no element is rounded
+                        const int ex = static_cast<int>(__float_as_uint(amax) >> 23);
+                        const int up = amax > 0.0f ? min(max(261 - ex, 1), 254) : 127;
+                        mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
+                        if (from == 0)
+                            qscale[nq % kScaleItems] = p.scale_log2 / mul;
                     }
                 }
             }
@@ -729,8 +743,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                         p.lse[(int64_t)w.t * p.Hq + w.g * p.group + head0 + h] =
                             (m + __log2f(l)) * 0.693147180559945309f;
                 }
-                const float inv = (C::kFp8 ? 0.0625f : 1.0f) *
-                                  (parts ? 1.0f : l == 0.0f ? 0.0f : __fdividef(1.0f, l));
+                const float inv = parts ? 1.0f : l == 0.0f ? 0.0f : __fdividef(1.0f, l);
                 fa[k] *= inv;
                 fb *= inv;
             }

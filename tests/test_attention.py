@@ -364,6 +364,23 @@ def test_nan_in_a_selected_key_shows():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kv", ["same", "fp8"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_head_that_is_not_finite_leaves_the_others_alone(bad, kv):
+    b = Batch(((3, 300),), 32, 1, 128, 150, 1, "bf16", kv, 0, seed=15)
+    q = b.q.clone()
+    b.q[1, 5, 17] = bad
+    got, lse = b.run()
+    assert bool(torch.isnan(got[1, 5]).all()) and bool(torch.isnan(lse[1, 5]))
+    kf, vf = b.values()
+    keys = selected(b.sel, None, b.lens, b.L, 1)
+    ref = reference(q.double().numpy(), kf, vf, keys, b.slot_of, 1, 128 ** -0.5)
+    got[1, 5] = torch.from_numpy(ref[0][1, 5]).to(got)          # the others are held to the formula
+    lse[1, 5] = float(ref[1][1, 5])
+    check(got, lse, ref, 2.0 ** -8, 2.0 ** -8)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["same", "fp8"])
 def test_strides(kv):
     """q and out inside wider tensors, heads outermost, k and v side by side in one cache."""
     b = Batch(((40, 300),), 32, 4, 128, 60, 1, "bf16", kv, 0, seed=10)
