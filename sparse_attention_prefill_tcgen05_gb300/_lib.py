@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -100,6 +101,9 @@ class _AttentionIo(ctypes.Structure):
         "ld_sel", "ld_page_table")]
 
 
+# the same layout, packed in one go: eleven addresses, ten strides
+_ATTENTION_IO = struct.Struct("11P10q").pack
+
 _lib = None
 
 
@@ -151,7 +155,7 @@ def lib():
                                                ctypes.POINTER(P), ctypes.POINTER(sz)]
         L.indexer_attention_destroy.argtypes = [P]
         L.indexer_attention_destroy.restype = None
-        L.indexer_sparse_attention.argtypes = [P, ctypes.POINTER(_AttentionIo), P, sz, P]
+        L.indexer_sparse_attention.argtypes = [P, P, P, sz, P]
         L.indexer_mask_blocks.argtypes = [P, P, i64, P, i32, P, i32, P, P]
         L.indexer_error_string.argtypes = [i32]
         L.indexer_error_string.restype = ctypes.c_char_p
@@ -174,13 +178,15 @@ def error_string(code: int) -> str:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
+    """The cudaStream_t of a torch stream (default: the current one of the current device)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        # the raw handle: building a torch.cuda.Stream object takes longer than a small kernel
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check(fn: str, rc: int):
@@ -382,25 +388,30 @@ def indexer_chunk_rows(prefix_len: int, budget_token2: float = 2.0e8, chunk_min:
 
 
 # ------------------------------------------------------- operators around the indexer
+# The checks are written out and pointers passed as plain integers: a call of a decode step
+# runs for a few microseconds on the GPU, and as long here.
 
 _DTYPES = {torch.bfloat16: IDX_BF16, torch.float16: IDX_FP16, torch.float32: IDX_FP32}
 
 
-def _dense(name: str, t, dims: int) -> int:
-    """The library's type code of a strided CUDA tensor whose last axis is contiguous."""
+def _dense(name: str, t):
+    """Type code and strides of a 3-d CUDA tensor whose last axis is contiguous."""
     code = _DTYPES.get(t.dtype)
-    if code is None or not t.is_cuda or t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name}: {dims}-d bf16, fp16 or fp32 CUDA tensor with a contiguous "
-                         "last axis expected")
-    return code
+    if code is None or not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{name}: 3-d bf16, fp16 or fp32 CUDA tensor expected")
+    st = t.stride()
+    if st[2] != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: a contiguous last axis expected")
+    return code, st
 
 
 def _i32(name: str, t, shape):
-    """A contiguous int32 CUDA tensor of that shape, or None."""
-    if t is not None and (t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous()
-                          or tuple(t.shape) != tuple(shape)):
+    """Address of a contiguous int32 CUDA tensor of that shape, or None."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or not t.is_cuda or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous int32 CUDA tensor of shape {tuple(shape)} expected")
-    return _ptr(t)
+    return t.data_ptr()
 
 
 class Rope:
@@ -409,6 +420,7 @@ class Rope:
     def __init__(self, handle, spec: _RopeSpec):
         self.handle = handle
         self.spec = spec
+        self.D = spec.D
 
     def __del__(self):
         h, self.handle = getattr(self, "handle", None), None
@@ -433,28 +445,31 @@ def indexer_rope_create(D: int, rot_dim: int, rot_offset: int = 0, layout: int =
 def indexer_rope(rope: Rope, x, positions, out=None, inverse: bool = False, stream=None):
     """Rotate ``x`` [rows, heads, D] at ``positions`` (int32 [rows]) into ``out`` (default: a
     new tensor; may be ``x``) and return it; ``inverse`` turns back."""
+    code, sx = _dense("x", x)
     if out is None:
         out = torch.empty_like(x)
-    code = _dense("x", x, 3)
-    if _dense("out", out, 3) != code or out.shape != x.shape or x.shape[2] != rope.spec.D:
+    rows, heads, D = x.shape
+    ocode, so = _dense("out", out)
+    if ocode != code or out.shape != x.shape or D != rope.D:
         raise ValueError("out: a tensor of x's shape and type, D elements a head, expected")
-    rows, heads, _ = x.shape
-    _check("indexer_rope", lib().indexer_rope(
-        rope.handle, _ptr(x), code, rows, heads, x.stride(0), x.stride(1),
-        _i32("positions", positions, (rows,)), 1 if inverse else 0, _ptr(out), out.stride(0),
-        out.stride(1), _stream(stream)))
+    rc = lib().indexer_rope(rope.handle, x.data_ptr(), code, rows, heads, sx[0], sx[1],
+                            _i32("positions", positions, (rows,)), 1 if inverse else 0,
+                            out.data_ptr(), so[0], so[1], _stream(stream))
+    if rc != IDX_OK:
+        raise IndexerError("indexer_rope", rc)
     return out
 
 
 def _cache_shape(codes, scales, fmt: int):
     """(slots, heads, D) of a cache's codes and scales."""
     slots, heads, n = codes.shape
-    D = 2 * n if fmt == IDX_K_FP4_E2M1_UE8M0 else n
-    want = (slots, heads, D // 32) if fmt == IDX_K_FP4_E2M1_UE8M0 else (slots, heads)
-    kind = torch.uint8 if fmt == IDX_K_FP4_E2M1_UE8M0 else torch.float32
-    if (codes.element_size() != 1 or not codes.is_cuda or not codes.is_contiguous()
-            or scales.dtype != kind or not scales.is_cuda or not scales.is_contiguous()
-            or tuple(scales.shape) != want):
+    if fmt == IDX_K_FP4_E2M1_UE8M0:
+        D, want, kind = 2 * n, (slots, heads, n // 16), torch.uint8
+    else:
+        D, want, kind = n, (slots, heads), torch.float32
+    if (scales.dtype != kind or scales.shape != want or codes.element_size() != 1
+            or not codes.is_cuda or not scales.is_cuda or not codes.is_contiguous()
+            or not scales.is_contiguous()):
         raise ValueError(f"cache: contiguous CUDA codes of one byte and {kind} scales of shape "
                          f"{want} expected")
     return slots, heads, D
@@ -465,14 +480,17 @@ def indexer_cache_write(x, codes, scales, fmt: int = IDX_K_FP8_E4M3, rope: Optio
     """Rotate (``rope``) and quantise ``x`` [rows, heads, D] into rows ``slots`` (int32 [rows];
     default: row i) of a cache: ``codes`` [num_slots, heads, D] (e2m1: D/2) and ``scales``."""
     n, heads, D = _cache_shape(codes, scales, fmt)
-    code = _dense("x", x, 3)
+    code, sx = _dense("x", x)
     rows = x.shape[0]
-    if tuple(x.shape[1:]) != (heads, D):
+    if x.shape[1] != heads or x.shape[2] != D:
         raise ValueError(f"x: [rows, {heads}, {D}] expected")
-    _check("indexer_cache_write", lib().indexer_cache_write(
-        None if rope is None else rope.handle, _ptr(x), code, rows, heads, D, x.stride(0),
-        x.stride(1), _i32("positions", positions, (rows,)), _i32("slots", slots, (rows,)), n,
-        fmt, _ptr(codes), _ptr(scales), _stream(stream)))
+    shape = (rows,)
+    rc = lib().indexer_cache_write(
+        None if rope is None else rope.handle, x.data_ptr(), code, rows, heads, D, sx[0], sx[1],
+        _i32("positions", positions, shape), _i32("slots", slots, shape), n, fmt,
+        codes.data_ptr(), scales.data_ptr(), _stream(stream))
+    if rc != IDX_OK:
+        raise IndexerError("indexer_cache_write", rc)
 
 
 def indexer_cache_read(codes, scales, fmt: int, slots, out, out_scales=None, stream=None):
@@ -485,12 +503,14 @@ def indexer_cache_read(codes, scales, fmt: int, slots, out, out_scales=None, str
         if _cache_shape(out, out_scales, fmt) != (rows, heads, D):
             raise ValueError("out: codes of the cache's heads and size expected")
     else:
-        code = _dense("out", out, 3)
-        if tuple(out.shape[1:]) != (heads, D) or not out.is_contiguous():
+        code, _ = _dense("out", out)
+        if out.shape[1] != heads or out.shape[2] != D or not out.is_contiguous():
             raise ValueError(f"out: contiguous [rows, {heads}, {D}] expected")
-    _check("indexer_cache_read", lib().indexer_cache_read(
-        _ptr(codes), _ptr(scales), fmt, n, heads, D, _i32("slots", slots, (rows,)), rows, code,
-        _ptr(out), _ptr(out_scales), _stream(stream)))
+    rc = lib().indexer_cache_read(
+        codes.data_ptr(), scales.data_ptr(), fmt, n, heads, D, _i32("slots", slots, (rows,)), rows,
+        code, out.data_ptr(), _ptr(out_scales), _stream(stream))
+    if rc != IDX_OK:
+        raise IndexerError("indexer_cache_read", rc)
     return out
 
 
@@ -500,7 +520,7 @@ def indexer_page_slots(plan: Plan, page_table, page_size: int, slots=None, strea
         slots = torch.empty(plan.problem.total_keys, dtype=torch.int32, device=page_table.device)
     table = _i32("page_table", page_table, (plan.problem.num_requests, page_table.shape[-1]))
     _check("indexer_page_slots", lib().indexer_page_slots(
-        plan.handle, table, page_table.stride(0), int(page_size),
+        plan.handle, table, page_table.shape[1], int(page_size),
         _i32("slots", slots, (plan.problem.total_keys,)), _stream(stream)))
     return slots
 
@@ -515,6 +535,15 @@ class Attention:
         self.spec = spec
         self.rows = rows
         self.requests = requests
+        # what the tensors of a call are compared with
+        self.dtype = torch.bfloat16 if spec.dtype == IDX_BF16 else torch.float16
+        self.dense = spec.kv_format == IDX_KV_DENSE
+        self.row_shape = (rows,)
+        self.q_shape = (rows, spec.Hq, spec.D)
+        self.kv_shape = (spec.num_slots, spec.Hkv, spec.D)
+        self.sel_shape = (rows, spec.num_sel)
+        self.scale_shape = (spec.num_slots, spec.Hkv)
+        self.lse_shape = (rows, spec.Hq)
 
     def __del__(self):
         h, self.handle = getattr(self, "handle", None), None
@@ -538,50 +567,58 @@ def indexer_attention_create(plan: Plan, Hq: int, Hkv: int, D: int, num_sel: int
     return Attention(handle, ws.value, spec, plan.problem.total_rows, plan.problem.num_requests)
 
 
+def _heads(name: str, t, shape, dtype):
+    """Strides of a CUDA tensor of that shape and type (None: e4m3 codes of one byte)."""
+    if t.shape != shape or not t.is_cuda or \
+            (t.element_size() != 1 if dtype is None else t.dtype != dtype):
+        raise ValueError(f"{name}: CUDA tensor {shape} of {dtype or 'e4m3 codes'} expected")
+    st = t.stride()
+    if st[2] != 1:
+        raise ValueError(f"{name}: a contiguous last axis expected")
+    return st
+
+
+def _f32(name: str, t, shape):
+    """Address of a contiguous fp32 CUDA tensor of that shape (0: none)."""
+    if t is None:
+        return 0
+    if t.dtype != torch.float32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous fp32 CUDA tensor {shape} expected")
+    return t.data_ptr()
+
+
 def indexer_sparse_attention(attn: Attention, q, k, v, sel, compress_len, out, ws=None,
                              k_scale=None, v_scale=None, sel_count=None, page_table=None,
                              lse=None, stream=None):
     """Attention of ``q`` [rows, Hq, D] over the keys ``sel`` (int32 [rows, num_sel]) of ``k`` and
     ``v`` [num_slots, Hkv, D] into ``out`` (and ``lse`` fp32 [rows, Hq]); see the header."""
-    s = attn.spec
-    dense = s.kv_format == IDX_KV_DENSE
-    for name, t, shape in (("q", q, (attn.rows, s.Hq, s.D)), ("out", out, (attn.rows, s.Hq, s.D)),
-                           ("k", k, (s.num_slots, s.Hkv, s.D)), ("v", v, (s.num_slots, s.Hkv, s.D))):
-        if t.shape != shape or t.stride(2) != 1 or not t.is_cuda:
-            raise ValueError(f"{name}: CUDA tensor {shape} with a contiguous last axis expected")
-        if name in "kv" and not dense:
-            if t.element_size() != 1:
-                raise ValueError(f"{name}: e4m3 codes of one byte expected")
-        elif _DTYPES.get(t.dtype) != s.dtype:
-            raise ValueError(f"{name}: tensor of the attention's type expected")
-    if sel.dtype != torch.int32 or sel.shape != (attn.rows, s.num_sel) or not sel.is_cuda or \
+    kv_type = attn.dtype if attn.dense else None
+    sq = _heads("q", q, attn.q_shape, attn.dtype)
+    so = _heads("out", out, attn.q_shape, attn.dtype)
+    sk = _heads("k", k, attn.kv_shape, kv_type)
+    sv = _heads("v", v, attn.kv_shape, kv_type)
+    if sel.dtype != torch.int32 or sel.shape != attn.sel_shape or not sel.is_cuda or \
             sel.stride(1) != 1:
-        raise ValueError(f"sel: int32 CUDA tensor {(attn.rows, s.num_sel)} expected")
-    for name, t, shape in (("k_scale", k_scale, (s.num_slots, s.Hkv)),
-                           ("v_scale", v_scale, (s.num_slots, s.Hkv)),
-                           ("lse", lse, (attn.rows, s.Hq))):
-        if t is not None and (t.dtype != torch.float32 or t.shape != shape or not t.is_cuda
-                              or not t.is_contiguous()):
-            raise ValueError(f"{name}: contiguous fp32 CUDA tensor {shape} expected")
-    ld_table = 0
+        raise ValueError(f"sel: int32 CUDA tensor {attn.sel_shape} expected")
+    table = ld_table = 0
     if page_table is not None:
         if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_cuda or \
                 page_table.shape[0] != attn.requests or page_table.stride(1) != 1:
             raise ValueError("page_table: int32 CUDA tensor [requests, pages] expected")
+        table = page_table.data_ptr()
         ld_table = page_table.stride(0) if attn.requests > 1 else page_table.shape[1]
-    io = _AttentionIo(
+    io = _ATTENTION_IO(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-        None if k_scale is None else k_scale.data_ptr(),
-        None if v_scale is None else v_scale.data_ptr(), sel.data_ptr(),
-        None if sel_count is None else _i32("sel_count", sel_count, (attn.rows,)).value,
-        _i32("compress_len", compress_len, (attn.rows,)).value,
-        None if page_table is None else page_table.data_ptr(),
-        None if lse is None else lse.data_ptr(), q.stride(0), q.stride(1), k.stride(0),
-        k.stride(1), v.stride(0), v.stride(1), out.stride(0), out.stride(1),
-        sel.stride(0) if attn.rows > 1 else s.num_sel, ld_table)
-    _check("indexer_sparse_attention", lib().indexer_sparse_attention(
-        attn.handle, ctypes.byref(io), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-        _stream(stream)))
+        _f32("k_scale", k_scale, attn.scale_shape), _f32("v_scale", v_scale, attn.scale_shape),
+        sel.data_ptr(), _i32("sel_count", sel_count, attn.row_shape) or 0,
+        _i32("compress_len", compress_len, attn.row_shape) or 0, table,
+        _f32("lse", lse, attn.lse_shape), sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1],
+        sel.stride(0) if attn.rows > 1 else attn.spec.num_sel, ld_table)
+    rc = lib().indexer_sparse_attention(
+        attn.handle, io, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+        _stream(stream))
+    if rc != IDX_OK:
+        raise IndexerError("indexer_sparse_attention", rc)
     return out
 
 
@@ -593,9 +630,12 @@ def indexer_mask_blocks(plan: Plan, cand_mask, compress_len, block: int, blocks,
     if cand_mask.element_size() != 1 or not cand_mask.is_cuda or cand_mask.dim() != 2 or \
             cand_mask.shape[0] != rows or cand_mask.stride(1) != 1:
         raise ValueError("cand_mask: CUDA tensor [rows, blocks] of one byte expected")
-    _check("indexer_mask_blocks", lib().indexer_mask_blocks(
-        plan.handle, _ptr(cand_mask), cand_mask.stride(0) if rows > 1 else cand_mask.shape[1],
-        _i32("compress_len", compress_len, (rows,)), int(block),
-        _i32("blocks", blocks, (rows, blocks.shape[-1])), blocks.shape[-1],
-        _i32("count", count, (rows,)), _stream(stream)))
+    num_sel, shape = blocks.shape[-1], (rows,)
+    rc = lib().indexer_mask_blocks(
+        plan.handle, cand_mask.data_ptr(), cand_mask.stride(0) if rows > 1 else cand_mask.shape[1],
+        _i32("compress_len", compress_len, shape), int(block),
+        _i32("blocks", blocks, (rows, num_sel)), num_sel, _i32("count", count, shape),
+        _stream(stream))
+    if rc != IDX_OK:
+        raise IndexerError("indexer_mask_blocks", rc)
     return blocks

@@ -718,9 +718,28 @@ PlanView plan_view(const indexer_plan_s* p)
 
 void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
-bool device_supported() { return device_info().ok; }
+// The current device's properties, asked for once per device (they do not change).
+static DeviceInfo known_device()
+{
+    static std::atomic<int> known[64];               // 0: not asked; SMs + 1, negative: not supported
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return device_info();
+    DeviceInfo d;
+    int v = known[dev].load(std::memory_order_relaxed);
+    if (v == 0) {
+        d = device_info();
+        v = d.ok ? d.sms + 1 : -d.sms - 1;
+        known[dev].store(v, std::memory_order_relaxed);
+    }
+    d.ok = v > 0;
+    d.sms = (v > 0 ? v : -v) - 1;
+    return d;
+}
 
-int device_sms() { return device_info().sms; }
+bool device_supported() { return known_device().ok; }
+
+int device_sms() { return known_device().sms; }
 
 }  // namespace idx
 
