@@ -381,6 +381,7 @@ cudaError_t launch_page_slots(const PageSlotParams& p, cudaStream_t st);
 // Attention over the selected keys.  A work item is (row, key/value head, tile of query
 // heads, split of the row's key tiles of kAttnTile keys).
 constexpr int kAttnTile = 128;
+constexpr int kMaxSplits = 64;
 // Division of numbers below 2^31 by a constant of the call: n / d = (n * mul) >> shift with
 // mul = ceil(2^shift / d), shift = 31 + ceil(log2 d).
 struct Divisor {
