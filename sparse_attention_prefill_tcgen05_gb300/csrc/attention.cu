@@ -51,7 +51,6 @@ struct AttnCfg {
     static constexpr int kEb = kFp8 ? 1 : 2;            // bytes of an operand element
     static constexpr int kRow = D * kEb;                // bytes of a cached vector
     static constexpr int kAtom = kRow < 128 ? kRow : 128;
-    static constexpr int kAtoms = kRow / kAtom;
     static constexpr int kStage = kAttnTile * kRow;
     static constexpr int kQRows = NH * kQTerms;
     static constexpr int kQBytes = kQRows * kRow;
@@ -77,7 +76,8 @@ struct AttnCfg {
     static constexpr int kFixed = kStats + kMax + kQScale + 2 * kPBytes + 2 * kQBytes + 8 * 21;
     static constexpr int kFit =
         (kSmemLimit - kFixed) / (2 * kStage + 2 * kKeyInfo + 8 * 4);
-    static constexpr int kTiles = kFit < 3 ? kFit : 3;  // tiles in the ring
+    static constexpr int kMostTiles = NH == 16 && kStage <= 16384 ? 4 : 3;
+    static constexpr int kTiles = kFit < kMostTiles ? kFit : kMostTiles;   // tiles in the ring
     static constexpr int kStages = 2 * kTiles;          // and as many warps that fill them
     static constexpr int kSmem = kFixed + kTiles * (2 * kStage + 2 * kKeyInfo + 8 * 4);
     static constexpr int kGatherWarp = 8 + 4, kMmaWarp = kGatherWarp + kStages;
@@ -112,8 +112,16 @@ __device__ __forceinline__ int quotient(int n, const Divisor& d)
     return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * d.mul) >> d.shift);
 }
 
+// The entries of an item's row, read an item ahead of its use: every role walks the items.
+__device__ __forceinline__ int item_entries(const AttnParams& p, int item, int total)
+{
+    if (!p.sel_count || item >= total)
+        return p.num_sel;
+    return p.sel_count[quotient(quotient(quotient(item, p.by_splits), p.by_head_tiles), p.by_hkv)];
+}
+
 template <bool kOneLane = false>
-__device__ __forceinline__ AttnItem attn_item(const AttnParams& p, int item)
+__device__ __forceinline__ AttnItem attn_item(const AttnParams& p, int item, int entries)
 {
     AttnItem w;
     int q = quotient(item, p.by_splits);
@@ -125,13 +133,10 @@ __device__ __forceinline__ AttnItem attn_item(const AttnParams& p, int item)
     q = quotient(item, p.by_hkv);
     w.g = item - q * p.Hkv;
     w.t = q;
-    w.n_sel = p.num_sel;
-    if (p.sel_count) {
-        w.n_sel = max(0, min(p.num_sel, p.sel_count[w.t]));
-        // (the shuffle tells the compiler that the count, and the loops over it, are uniform)
-        if (!kOneLane)
-            w.n_sel = __shfl_sync(0xFFFFFFFFu, w.n_sel, 0);
-    }
+    w.n_sel = max(0, min(p.num_sel, entries));
+    // (the shuffle tells the compiler that the count, and the loops over it, are uniform)
+    if (!kOneLane)
+        w.n_sel = __shfl_sync(0xFFFFFFFFu, w.n_sel, 0);
     const int all = ((w.n_sel << p.block_shift) + kAttnTile - 1) / kAttnTile;
     w.tile = w.split * p.split_tiles;
     w.tiles = max(w.tile, min(all, w.tile + p.split_tiles));
@@ -370,8 +375,10 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         };
         bool bad = false;
         int n = 0, iq = 0;                               // tiles and items before this item
+        int entries = item_entries(p, blockIdx.x, total);
         for (int item = blockIdx.x; item < total; item += gridDim.x) {
-            const AttnItem w = attn_item(p, item);
+            const AttnItem w = attn_item(p, item, entries);
+            entries = item_entries(p, item + gridDim.x, total);
             const int count = w.tiles - w.tile;
             if (count == 0)
                 continue;
@@ -433,14 +440,11 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     over = ok ? over : -INFINITY;
                 } else {
 #pragma unroll
-                    for (int i = 0; i < HN; i += 2) {
-                        float m0 = mx[i], m1 = mx[i + 1];
-                        if (C::kFp8) {
-                            m0 -= lv;
-                            m1 -= lv;
-                        }
-                        fma2(x[i], x[i + 1], ks, ks, -m0, -m1);
-                        over = fmaxf(over, fmaxf(x[i], x[i + 1]));
+                    for (int i = 0; i < HN; i += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(mx + i);
+                        fma2(x[i], x[i + 1], ks, ks, lv - m.x, lv - m.y);
+                        fma2(x[i + 2], x[i + 3], ks, ks, lv - m.z, lv - m.w);
+                        over = fmaxf(over, fmaxf(fmaxf(x[i], x[i + 1]), fmaxf(x[i + 2], x[i + 3])));
                     }
                     over = ok ? over : -INFINITY;
                 }
@@ -461,8 +465,11 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                         bad |= !wait(p_empty + (b ^ 1), ((n + j - 1) >> 1) & 1);
                     if (!first && based) {
 #pragma unroll
-                        for (int i = 0; i < HN; ++i)
-                            x[i] += mx[i];
+                        for (int i = 0; i < HN; i += 4) {
+                            const float4 m = *reinterpret_cast<const float4*>(mx + i);
+                            add2(x[i], x[i + 1], m.x, m.y);
+                            add2(x[i + 2], x[i + 3], m.z, m.w);
+                        }
                     }
 #pragma unroll
                     for (int c = 0; c < HN; c += 16) {
@@ -485,13 +492,19 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     }
                     bar_all(true, bar_id, 128);
 #pragma unroll
-                    for (int i = 0; i < HN; ++i)
-                        x[i] -= mx[i];
+                    for (int i = 0; i < HN; i += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(mx + i);
+                        add2(x[i], x[i + 1], -m.x, -m.y);
+                        add2(x[i + 2], x[i + 3], -m.z, -m.w);
+                    }
                     if (!first) {
                         tc_fence_after();
 #pragma unroll
-                        for (int i = 0; i < HN; ++i)
-                            l[i] *= *scratch(b, i);
+                        for (int i = 0; i < HN; i += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(scratch(b, i));
+                            mul2(l[i], l[i + 1], f.x, f.y);
+                            mul2(l[i + 2], l[i + 3], f.z, f.w);
+                        }
 #pragma unroll 1
                         for (int c = 0; c < HN; c += 8) {
                             const float4 f0 = *reinterpret_cast<const float4*>(scratch(b, c));
@@ -599,12 +612,14 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         // The queries of an item, one item ahead: they are converted (e4m3 caches) or copied into
         // the operand's layout by these warps, which have little else to do.
         int q_item = blockIdx.x, nq = 0;                 // next item to load, items loaded
+        int q_entries = item_entries(p, blockIdx.x, total);
         auto load_queries = [&] {
             AttnItem w;
             for (;; q_item += gridDim.x) {
                 if (q_item >= total)
                     return true;
-                w = attn_item(p, q_item);
+                w = attn_item(p, q_item, q_entries);
+                q_entries = item_entries(p, q_item + gridDim.x, total);
                 if (w.tiles > w.tile)
                     break;
             }
@@ -696,8 +711,10 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             return true;
         };
         int n = 0, iq = 0;                               // tiles and items before this item
+        int entries = item_entries(p, blockIdx.x, total);
         for (int item = blockIdx.x; item < total; item += gridDim.x) {
-            const AttnItem w = attn_item(p, item);
+            const AttnItem w = attn_item(p, item, entries);
+            entries = item_entries(p, item + gridDim.x, total);
             const int tiles = w.tiles - w.tile, head0 = w.ht * NH;
             // The next item's queries (and before the first item its own).  Not for items without
             // tiles: the place waited for is that of the item before this one, which has left
@@ -756,48 +773,57 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     break;
                 tc_fence_after();
             }
+            // 16 heads at a time, 8 of small groups (8 heads of 64: 143 -> 132 us; 32 of 128 in
+            // eights: 238 -> 254)
+            constexpr int kStep = NH == 16 ? 8 : 16;
+            auto load = [](uint32_t at, float* v) {
+                if (kStep == 8)
+                    tmem_ld_32x32b_x8(at, v);
+                else
+                    tmem_ld_32x32b_x16(at, v);
+            };
 #pragma unroll 1
-            for (int h0 = 0; h0 < heads; h0 += 16) {
-                float o[16];
+            for (int h0 = 0; h0 < heads; h0 += kStep) {
+                float o[kStep];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < kStep; ++i)
                     o[i] = 0.0f;
-                const float f = NH > 32 && h0 >= 32 ? fa[NH / 64] : fa[0];
 #pragma unroll 1
                 for (int a = 0; a < C::kAccs && tiles > 0; ++a) {
                     if (tiles == 1 && C::kAlternate && a != (n & 1))
                         continue;                        // it was not written
                     const uint32_t at =
                         tmem_o + lanes + ((iq & 1) * C::kAccs + a) * C::kOCols + h0;
-                    const float fac = a == 0 ? f : fb;
-                    float v[16];
-                    tmem_ld_32x32b_x16(at, v);
+                    const float fac = a > 0 ? fb : NH > 32 && h0 >= 32 ? fa[NH / 64] : fa[0];
+                    float v[kStep];
+                    load(at, v);
                     if (C::kFp8) {
-                        float r[16];
-                        tmem_ld_32x32b_x16(at + NH, r);
+                        float r[kStep];
+                        load(at + NH, r);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
+                        for (int i = 0; i < kStep; ++i)
                             v[i] = fmaf(r[i], 0.0625f, v[i]);
                     }
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < kStep; ++i) {
                         const float s = __shfl_sync(0xFFFFFFFFu, fac, (h0 + i) & 31);
                         o[i] = s != 0.0f ? fmaf(v[i], s, o[i]) : o[i];
                     }
                 }
+                if (!write)
+                    continue;
                 if (parts) {
                     float* to = part + h0 * D;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (write)
-                            to[i * D] = o[i];
+                    for (int i = 0; i < kStep; ++i)
+                        to[i * D] = o[i];
                 } else {
                     uint8_t* to = out + h0 * p.out_head;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (write && h0 + i < heads)
+                    for (int i = 0; i < kStep; ++i) {
+                        if (h0 + i < heads)
                             *reinterpret_cast<T*>(to) = static_cast<T>(o[i]);
                         to += p.out_head;
                     }
@@ -833,7 +859,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         AttnItem w;
         w.tile = w.tiles = w.n_sel = w.t = w.g = 0;
         int item = blockIdx.x - gridDim.x, skip = pw / 2;   // tiles to the warp's next one
-        int r = 0, base = 0, len = 0, g = 0;
+        int entries = item_entries(p, blockIdx.x, total);
+        int r = 0, base = 0, most = 0, len = 0, g = 0;
         // the lane's keys of a tile: row0 + kPerRow i + chunk, i < 4
         int32_t entry[4], key[4], page[4];
         auto advance = [&] {                             // to the warp's next tile; its entries
@@ -844,7 +871,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 item += gridDim.x;
                 if (item >= total)
                     return false;
-                w = attn_item(p, item);
+                w = attn_item(p, item, entries);
+                entries = item_entries(p, item + gridDim.x, total);
                 w.tile += skip;
                 fresh = true;
             }
@@ -852,7 +880,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             if (fresh) {
                 r = request_of(p.row_begin, p.num_requests, w.t);
                 base = p.key_begin[r];
-                len = min(p.clen[w.t], p.key_begin[r + 1] - base);
+                most = p.key_begin[r + 1] - base;
+                len = p.clen[w.t];                       // (used after the copies' wait)
             }
             const int32_t* sel = p.sel + w.t * p.ld_sel;
 #pragma unroll
@@ -869,7 +898,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 const int pos = w.tile * kAttnTile + row0 + kPerRow * i + chunk;
                 const int64_t k = ((int64_t)entry[i] << p.block_shift) +
                                   (pos & ((1 << p.block_shift) - 1));
-                const bool in = entry[i] >= 0 && k < len;
+                const bool in = entry[i] >= 0 && k < min(len, most);
                 key[i] = static_cast<int32_t>(k);
                 page[i] = in ? 0 : -1;
                 if (p.page == 0) {
@@ -975,8 +1004,10 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             int n = 0, iq = 0, st = 0;                  // tile n's place in the ring
             uint32_t phase = 0;                         // and the uses of that place
             bool ok = true;
+            int entries = item_entries(p, blockIdx.x, total);
             for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-                const AttnItem w = attn_item<true>(p, item);
+                const AttnItem w = attn_item<true>(p, item, entries);
+                entries = item_entries(p, item + gridDim.x, total);
                 const int count = w.tiles - w.tile;
                 if (count == 0)
                     continue;
