@@ -409,6 +409,7 @@ int indexer_mask_blocks(indexer_plan_t plan, const uint8_t* cand_mask, int64_t l
     p.block = block;
     p.num_sel = num_sel;
     p.rows = v.T;
+    p.max_blocks = static_cast<int32_t>((v.max_L + (int64_t)block - 1) / block);
     p.num_requests = v.R;
     std::copy(v.row_begin, v.row_begin + v.R + 1, p.row_begin);
     std::copy(v.L, v.L + v.R, p.key_count);

@@ -438,6 +438,7 @@ struct MaskBlocksParams {
     int32_t* blocks;
     int32_t* count;              // nullable
     int32_t block, num_sel, rows, num_requests;
+    int32_t max_blocks;          // of the longest request: bytes of a mask row that exist
     int32_t row_begin[kMaxRequests + 1];
     int32_t key_count[kMaxRequests];
 };
