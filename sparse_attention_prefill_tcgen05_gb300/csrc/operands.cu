@@ -38,20 +38,24 @@ struct Elt<float> {
     static __device__ __forceinline__ float store(float v) { return v; }
 };
 
-// Eight elements at p (16-byte aligned) as fp32, and back with one rounding.
+// Eight elements at p (16-byte aligned), to fp32, and back with one rounding.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8])
-{
-    constexpr int n = sizeof(T) / 2;   // 16-byte words
-    uint4 w[n];
+struct Eight {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p)
+    {
 #pragma unroll
-    for (int i = 0; i < n; ++i)
-        w[i] = reinterpret_cast<const uint4*>(p)[i];
-    const T* e = reinterpret_cast<const T*>(w);
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+            w[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const
+    {
+        const T* e = reinterpret_cast<const T*>(w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = Elt<T>::load(e[i]);
-}
+        for (int i = 0; i < 8; ++i)
+            v[i] = Elt<T>::load(e[i]);
+    }
+};
 
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&v)[8])
@@ -67,29 +71,43 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8])
         reinterpret_cast<uint4*>(p)[i] = w[i];
 }
 
-// Cosine and sine (times the amplitude) of pair i's turn at a position.  position * inc
-// modulo 2^64 is the angle in 2^-64 turns, exactly; its top 32 bits as a signed number
-// are half turns in [-1, 1), rounded once to fp32 (an error below 2e-7 rad at every
-// position, where a 32-bit product of position and frequency would be off by 0.03 rad at
-// position 487,935).
-__device__ __forceinline__ float2 turn(const RopeParams& rp, int32_t pos, int i)
+// Cosine and sine (times the amplitude) of a pair's turn at a position.  position * inc
+// modulo 2^64 is the angle in 2^-64 turns, exactly; its top 32 bits are a quarter turn q and
+// a remainder of at most an eighth of a turn, converted to fp32 with one rounding.  On that
+// range the Taylor series of sine and cosine to the ninth and tenth power leave 2e-9, so the
+// angle's roundings are the error (below 1.5e-7, at every position: a 32-bit product of
+// position and frequency would be off by 0.03 rad at position 487,935).
+__device__ __forceinline__ float2 turn(const RopeParams& rp, int32_t pos, uint64_t inc)
 {
-    const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * rp.inc[i];
-    const float half_turns =
-        static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;   // 2^-31
-    float s, c;
-    sincospif(half_turns, &s, &c);
-    return make_float2(c * rp.amplitude, (rp.inverse ? -s : s) * rp.amplitude);
+    const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * inc;
+    const uint32_t top = static_cast<uint32_t>(phase >> 32);
+    const uint32_t q = (top + 0x20000000u) >> 30;
+    const float z = static_cast<float>(static_cast<int32_t>(top - (q << 30))) *
+                    static_cast<float>(6.283185307179586 / 4294967296.0);
+    const float y = z * z;
+    float s = fmaf(y, 1.0f / 362880.0f, -1.0f / 5040.0f);
+    s = fmaf(y, s, 1.0f / 120.0f);
+    s = fmaf(y, s, -1.0f / 6.0f);
+    s = fmaf(z * y, s, z);
+    float c = fmaf(y, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+    c = fmaf(y, c, -1.0f / 720.0f);
+    c = fmaf(y, c, 1.0f / 24.0f);
+    c = fmaf(y, c, -0.5f);
+    c = fmaf(y, c, 1.0f);
+    const float cq = (q & 1u) ? s : c, sq = (q & 1u) ? c : s;
+    const float ca = ((q + 1u) & 2u) ? -rp.amplitude : rp.amplitude;
+    const float sa = (((q & 2u) != 0u) != (rp.inverse != 0)) ? -rp.amplitude : rp.amplitude;
+    return make_float2(cq * ca, sq * sa);
 }
 
 // A vector's 16 elements of one thread: unit u of the rotated part holds eight pairs, as
 // eight elements at `a` and their partners at `b` (half layout) or as sixteen neighbours
-// (interleaved; b = a + 8); units past the rotated part hold sixteen (or the last eight)
-// other elements.
+// (interleaved; b = a + 8).  The units after those hold the elements left alone, eight from
+// their first half and eight from their second, so that neighbouring threads read
+// neighbouring 16 bytes; the last may have only one eight (b < 0).
 struct Unit {
-    int a, b;       // element offsets of the two groups of eight; b < 0: only one
+    int a, b;       // element offsets of the two groups of eight
     bool rotated;
-    int pair;       // first pair of a rotated unit
 };
 
 __device__ __forceinline__ Unit unit_of(const RopeParams& rp, int u, int D)
@@ -97,80 +115,166 @@ __device__ __forceinline__ Unit unit_of(const RopeParams& rp, int u, int D)
     Unit r;
     const int nrot = rp.rot / 16;
     r.rotated = u < nrot;
-    r.pair = 8 * u;
     if (r.rotated) {
         r.a = rp.offset + (rp.interleaved ? 16 * u : 8 * u);
         r.b = rp.interleaved ? r.a + 8 : r.a + rp.rot / 2;
     } else {
-        const int e = 16 * (u - nrot);          // among the elements left alone
+        const int rest = D - rp.rot;
+        const int e = 8 * (u - nrot), f = e + (rest + 15) / 16 * 8;   // among those left alone
         r.a = e < rp.offset ? e : e + rp.rot;
-        const int f = e + 8;
-        r.b = f >= D - rp.rot ? -1 : f < rp.offset ? f : f + rp.rot;
+        r.b = f >= rest ? -1 : f < rp.offset ? f : f + rp.rot;
     }
     return r;
 }
 
-__device__ __forceinline__ void rotate16(bool interleaved, const float2 (&cs)[8], float (&a)[8],
-                                         float (&b)[8])
+// What a block of the kernels below does: vectors (row, head) of up to `rows` rows and
+// `heads` heads, `lanes` threads each (one unit a thread), as many at once as the block has
+// groups of lanes, and a few per group with their loads in flight together.
+struct Tiling {
+    int32_t rows, heads, lanes, groups;
+    int32_t angle_rows;          // rows whose angles the block's threads take at a time
+    uint32_t by_heads, by_lanes, by_pairs;   // for quotient()
+};
+
+// q / d for q and d up to 2^16 as the high word of q * reciprocal(d); d = 1 has none.
+__device__ __forceinline__ int quotient(uint32_t q, uint32_t reciprocal)
 {
-    if (interleaved) {
+    return reciprocal ? __umulhi(q, reciprocal) : q;
+}
+uint32_t reciprocal(int d)
+{
+    return d == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + d - 1) / d);
+}
+
+constexpr int kAngles = 2048;    // cosines and sines a block keeps
+
+// The angles of a block's rows, once for all heads: those of two neighbouring pairs of row r
+// as one 16-byte word (their cosines, their sines), where the thread of their unit finds its
+// four words without bank conflicts.  A thread takes one pair for every angle_rows-th row.
+__device__ __forceinline__ void block_angles(const RopeParams& rp, const Tiling& t,
+                                             const int32_t* positions, int rows, float* cs)
+{
+    const int pairs = rp.rot / 2, units = rp.rot / 16;
+    int r = quotient(threadIdx.x, t.by_pairs);
+    const int i = threadIdx.x - r * pairs;
+    if (r >= t.angle_rows)
+        return;
+    // a plain load: as an indexed constant, lanes of different pairs would take turns
+    const uint64_t* table = rp.inc;
+    asm volatile("" : "+l"(table));
+    const uint64_t inc = table[i];
+    float* o = cs + ((i % 8) / 2 * units + i / 8) * 4 + (i & 1);
+    for (; r < rows; r += t.angle_rows) {
+        const float2 v = turn(rp, positions[r], inc);
+        o[r * 2 * pairs] = v.x;
+        o[r * 2 * pairs + 2] = v.y;
+    }
+}
+
+// Two fp32 values in a 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t pack(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpack(uint64_t v, float& x, float& y)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// A unit's 16 elements turned by its eight angles (`cs`: the row's, u: the unit).
+__device__ __forceinline__ void rotate16(const RopeParams& rp, const float* cs, int u,
+                                         float (&a)[8], float (&b)[8])
+{
+    const int units = rp.rot / 16;
+    const float4* p = reinterpret_cast<const float4*>(cs) + u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float(&v)[8] = i < 4 ? a : b;
-            const int e = 2 * (i & 3);
-            const float x = v[e], y = v[e + 1];
-            v[e] = fmaf(x, cs[i].x, -y * cs[i].y);
-            v[e + 1] = fmaf(x, cs[i].y, y * cs[i].x);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float x = a[i], y = b[i];
-            a[i] = fmaf(x, cs[i].x, -y * cs[i].y);
-            b[i] = fmaf(x, cs[i].y, y * cs[i].x);
+    for (int k = 0; k < 4; ++k) {
+        const float4 v = p[k * units];
+        const uint64_t c = pack(v.x, v.y), s = pack(v.z, v.w), ns = pack(-v.z, -v.w);
+        if (rp.interleaved) {
+            float(&w)[8] = k < 2 ? a : b;
+            const int e = 4 * (k & 1);
+            const uint64_t x = pack(w[e], w[e + 2]), y = pack(w[e + 1], w[e + 3]);
+            unpack(fma2(x, c, mul2(y, ns)), w[e], w[e + 2]);
+            unpack(fma2(x, s, mul2(y, c)), w[e + 1], w[e + 3]);
+        } else {
+            const uint64_t x = pack(a[2 * k], a[2 * k + 1]), y = pack(b[2 * k], b[2 * k + 1]);
+            unpack(fma2(x, c, mul2(y, ns)), a[2 * k], a[2 * k + 1]);
+            unpack(fma2(x, s, mul2(y, c)), b[2 * k], b[2 * k + 1]);
         }
     }
 }
 
 // ------------------------------------------------------------------------- rotation
 
-// One thread per (row, unit of 16 elements), for `hp` heads: the eight angles are computed
-// once and turn that unit of every head.  Units that are left alone are copied (skipped
-// when the output is the input itself).
+// Each unit is read once, turned in fp32 and written once; HBM bounds it.  The vectors of a
+// thread are loaded together before the angles are computed, and a head's cosines come from
+// shared memory instead of every thread's own.  16,384 x 32 x 128 bf16, all turned: 41 us
+// (6.6 TB/s), 64 rows 2.3 us; four vectors in flight took 42 and 2.9 us, one 44 and 2.1 us,
+// angles per thread (eight heads each) 52 us.
+constexpr int kRopeBatch = 2;
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-rope_kernel(const __grid_constant__ RopeParams rp, const __grid_constant__ RopeCall c, int units,
-            int hp)
+rope_kernel(const __grid_constant__ RopeParams rp, const __grid_constant__ RopeCall c,
+            const __grid_constant__ Tiling t)
 {
+    __shared__ __align__(16) float sm_angles[2 * kAngles];
     pdl_wait_then_release();
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int t = static_cast<int>(i / units);
-    if (t >= c.rows)
-        return;
-    const Unit u = unit_of(rp, static_cast<int>(i % units), c.D);
-    const int h0 = blockIdx.y * hp, h1 = min(c.heads, h0 + hp);
-    const T* x = static_cast<const T*>(c.x) + t * c.x_row;
-    T* out = static_cast<T*>(c.out) + t * c.out_row;
-    float2 cs[8];
-    if (u.rotated) {
-        const int32_t pos = c.positions[t];
+    const int groups = t.groups, g = quotient(threadIdx.x, t.by_lanes);
+    const int l = threadIdx.x - g * t.lanes;
+    const int r0 = blockIdx.x * t.rows, h0 = blockIdx.y * t.heads;
+    const int rows = min(t.rows, c.rows - r0), heads = min(t.heads, c.heads - h0);
+    const Unit u = unit_of(rp, l, c.D);
+    const bool mine = g < groups && (u.rotated || c.x != c.out);
+    const T* x = static_cast<const T*>(c.x) + r0 * c.x_row + h0 * c.x_head;
+    T* out = static_cast<T*>(c.out) + r0 * c.out_row + h0 * c.out_head;
+    constexpr int kB = kRopeBatch;
+    Eight<T> wa[kB], wb[kB];
+    int row[kB], head[kB];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            cs[k] = turn(rp, pos, u.pair + k);
-    } else if (c.x == c.out) {
-        return;
+    for (int j = 0; j < kB; ++j) {
+        const uint32_t q = j * groups + g;
+        row[j] = quotient(q, t.by_heads);
+        head[j] = q - row[j] * t.heads;
+        if (!mine || row[j] >= rows || head[j] >= heads) {
+            row[j] = -1;
+            continue;
+        }
+        const T* p = x + row[j] * c.x_row + head[j] * c.x_head;
+        wa[j].load(p + u.a);
+        if (u.b >= 0)
+            wb[j].load(p + u.b);
     }
-#pragma unroll 4
-    for (int h = h0; h < h1; ++h) {
+    block_angles(rp, t, c.positions + r0, rows, sm_angles);
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kB; ++j) {
+        if (row[j] < 0)
+            continue;
         float a[8], b[8];
-        load8(x + h * c.x_head + u.a, a);
-        if (u.b >= 0)
-            load8(x + h * c.x_head + u.b, b);
+        wa[j].values(a);
+        wb[j].values(b);
         if (u.rotated)
-            rotate16(rp.interleaved, cs, a, b);
-        store8(out + h * c.out_head + u.a, a);
+            rotate16(rp, sm_angles + row[j] * rp.rot, l, a, b);
+        T* p = out + row[j] * c.out_row + head[j] * c.out_head;
+        store8(p + u.a, a);
         if (u.b >= 0)
-            store8(out + h * c.out_head + u.b, b);
+            store8(p + u.b, b);
     }
 }
 
@@ -193,7 +297,7 @@ rope_any_kernel(const __grid_constant__ RopeParams rp, const __grid_constant__ R
         if (e < pairs) {
             const int a = rp.offset + (rp.interleaved ? 2 * e : e);
             const int b = rp.interleaved ? a + 1 : a + pairs;
-            const float2 cs = turn(rp, c.positions[t], e);
+            const float2 cs = turn(rp, c.positions[t], rp.inc[e]);
             const float xa = Elt<T>::load(x[a]), xb = Elt<T>::load(x[b]);
             out[a] = Elt<T>::store(fmaf(xa, cs.x, -xb * cs.y));
             out[b] = Elt<T>::store(fmaf(xa, cs.y, xb * cs.x));
@@ -207,55 +311,65 @@ rope_any_kernel(const __grid_constant__ RopeParams rp, const __grid_constant__ R
 
 // --------------------------------------------------------------------- quantisation
 
-// |x| for the scale: NaN counts as 0 and infinities as the largest finite value, so a
-// scale is always positive and finite.
-__device__ __forceinline__ float magnitude(float x)
+// The largest magnitude of eight values.  NaN becomes 0, since the indexer takes no NaN codes:
+// the maximum that passes a NaN on shows whether there is one, so values without any pay one
+// compare instead of sixteen instructions.
+__device__ __forceinline__ float largest(float (&v)[8])
 {
-    return x == x ? fminf(fabsf(x), 3.402823466e38f) : 0.0f;
+    float m = fabsf(v[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[i])));
+    if (m == m)
+        return m;
+    m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[i] = v[i] == v[i] ? v[i] : 0.0f;
+        m = fmaxf(m, fabsf(v[i]));
+    }
+    return m;
 }
 
-// e4m3 codes of eight values times `inv` (saturating, ties to even; NaN as 0, since the
-// indexer takes no NaN codes).
+// The largest of four groups.
+__device__ __forceinline__ float largest4(const float* groups)
+{
+    const float4 g = *reinterpret_cast<const float4*>(groups);
+    return fmaxf(fmaxf(g.x, g.y), fmaxf(g.z, g.w));
+}
+
+// e4m3 codes of eight values times `inv` (saturating, ties to even).
 __device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float inv)
 {
-    uint32_t w[2];
+    uint32_t two[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t r = 0;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float x = v[4 * i + 2 * j], y = v[4 * i + 2 * j + 1];
-            x = x == x ? x * inv : 0.0f;
-            y = y == y ? y * inv : 0.0f;
-            r |= static_cast<uint32_t>(
-                     __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3))
-                 << (16 * j);
-        }
-        w[i] = r;
+    for (int i = 0; i < 4; ++i) {
+        float2 f;
+        unpack(mul2(pack(v[2 * i], v[2 * i + 1]), pack(inv, inv)), f.x, f.y);
+        two[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
     }
-    return make_uint2(w[0], w[1]);
+    return make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
 }
 
 __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8], float inv)
 {
     uint32_t r = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float x = v[2 * j], y = v[2 * j + 1];
-        x = x == x ? x * inv : 0.0f;
-        y = y == y ? y * inv : 0.0f;
-        r |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(x, y), __NV_E2M1,
-                                                            cudaRoundNearest) &
-                                   0xFFu)
+    for (int j = 0; j < 4; ++j)
+        r |= static_cast<uint32_t>(
+                 __nv_cvt_float2_to_fp4x2(make_float2(v[2 * j] * inv, v[2 * j + 1] * inv),
+                                          __NV_E2M1, cudaRoundNearest) &
+                 0xFFu)
              << (8 * j);
-    }
     return r;
 }
 
-// Scale of an e4m3 row from its largest magnitude: amax / 448, never below the smallest
-// normal number (so its reciprocal is finite), 1 for a zero row.
+// Scale of an e4m3 row from its largest magnitude (an infinite one as the largest finite
+// value): amax / 448, never below the smallest normal number (so its reciprocal is finite), 1
+// for a zero row.
 __device__ __forceinline__ float e4m3_scale(float amax)
 {
+    amax = fminf(amax, 3.402823466e38f);
     return amax > 0.0f ? fmaxf(amax / 448.0f, 1.17549435e-38f) : 1.0f;
 }
 
@@ -265,100 +379,95 @@ __device__ __forceinline__ uint32_t e2m1_exponent(float amax)
 {
     if (!(amax > 0.0f))
         return 127u;
-    const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 2;
+    const int e = min(static_cast<int>(__float_as_uint(amax) >> 23), 254) - 2;
     return static_cast<uint32_t>(max(e, 0));
 }
 
 // 2^(127 - e) for a biased exponent e in 0..252 (the exponents e2m1_exponent returns).
 __device__ __forceinline__ float exp2_neg(uint32_t e) { return __uint_as_float((254u - e) << 23); }
 
-// A group of `lanes` (a power of two, D / 16 rounded up) threads per (row, `hp` heads),
-// one unit of 16 elements each, as in rope_kernel; the largest magnitude of the vector
-// (e4m3) by a shuffle reduction over the group.  For e2m1 the scale covers 32 neighbours:
-// the rotated vector is exchanged through shared memory so that a lane holds 16
-// neighbouring elements and shares its scale with lane ^ 1.
+// The same tiling with one vector per group, `lanes` a power of two: the largest magnitude of a
+// vector (e4m3) by a shuffle reduction over its lanes.  An e2m1 scale covers 32 neighbours,
+// four groups of eight that any lanes may hold: the groups' maxima meet in shared memory, the
+// values stay where they are (exchanging the values took 2.4 times as long).
+//
+// Instructions bound it, not bytes (some 300 per warp and 512 elements: widening, turning,
+// maxima, two divisions, narrowing; without rotation and divisions it runs at 5.9 TB/s), so
+// registers are held down for six blocks per SM (four with fp32, which would spill).  16,384 x 32 x 128 bf16 with 64 turned: e4m3
+// 50 us, e2m1 54 us (4.0 and 3.1 TB/s); two vectors in a group's flight took 58 and 51 us, four
+// 67 and 61 us.
 template <typename T, bool kFp4>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 6 : 4)
 cache_write_kernel(const __grid_constant__ RopeParams rp,
-                   const __grid_constant__ CacheWriteCall c, int lanes, int hp)
+                   const __grid_constant__ CacheWriteCall c, const __grid_constant__ Tiling t)
 {
-    extern __shared__ float sm_rows[];   // kFp4: [threads][16] values
+    __shared__ __align__(16) float sm_angles[2 * kAngles];
+    __shared__ __align__(16) float sm_groups[kFp4 ? kThreads * 2 : 1];   // maxima of eight
     pdl_wait_then_release();
-    const int units = c.D / 16;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t t = i / lanes;
-    const int l = static_cast<int>(i % lanes);
-    const bool row_ok = t < c.rows;
-    const int32_t slot = !row_ok ? -1 : c.slots ? c.slots[t] : static_cast<int32_t>(t);
-    // a skipped row's lanes stay in the shuffles of the warp's other rows
-    const bool keep = slot >= 0 && slot < c.num_slots;
-    const bool on = keep && l < units;
-    Unit u = unit_of(rp, l, c.D);
-    float2 cs[8];
-    if (on && u.rotated) {
-        const int32_t pos = c.positions[t];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            cs[k] = turn(rp, pos, u.pair + k);
-    }
-    const int h0 = blockIdx.y * hp, h1 = min(c.heads, h0 + hp);
-    const T* x = static_cast<const T*>(c.x) + (on ? t * c.x_row : 0);
-    float* mine = kFp4 ? sm_rows + (threadIdx.x - l) * 16 : nullptr;   // the group's vector
-#pragma unroll 2
-    for (int h = h0; h < h1; ++h) {
-        float a[8] = {}, b[8] = {};
-        if (on) {
-            load8(x + h * c.x_head + u.a, a);
-            load8(x + h * c.x_head + u.b, b);
-            if (u.rotated)
-                rotate16(rp.interleaved, cs, a, b);
+    const int g = quotient(threadIdx.x, t.by_lanes);
+    const int l = threadIdx.x - g * t.lanes;
+    const int r0 = blockIdx.x * t.rows, h0 = blockIdx.y * t.heads;
+    const int rows = min(t.rows, c.rows - r0), heads = min(t.heads, c.heads - h0);
+    const int row = quotient(g, t.by_heads), head = g - row * t.heads;
+    const Unit u = unit_of(rp, l, c.D);
+    const bool unit = l < c.D / 16;
+    Eight<T> wa, wb;
+    int slot = -1;
+    if (row < rows && head < heads) {
+        slot = c.slots ? c.slots[r0 + row] : r0 + row;
+        if (unit) {
+            const T* p = static_cast<const T*>(c.x) + (r0 + row) * c.x_row + (h0 + head) * c.x_head;
+            wa.load(p + u.a);
+            wb.load(p + u.b);
         }
-        const int64_t vec = (int64_t)slot * c.heads + h;
-        if (kFp4) {
-            if (on) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    mine[u.a + k] = a[k];
-                    mine[u.b + k] = b[k];
-                }
-            }
-            __syncwarp();
-            float m = 0.0f;
-            if (on) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    a[k] = mine[16 * l + k];
-                    b[k] = mine[16 * l + 8 + k];
-                    m = fmaxf(m, fmaxf(magnitude(a[k]), magnitude(b[k])));
-                }
-            }
-            __syncwarp();
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            if (on) {
-                const uint32_t e = e2m1_exponent(m);
-                const float inv = exp2_neg(e);
-                *reinterpret_cast<uint2*>(c.codes + vec * (c.D / 2) + 8 * l) =
-                    make_uint2(e2m1x8(a, inv), e2m1x8(b, inv));
-                if ((l & 1) == 0)
-                    static_cast<uint8_t*>(c.scales)[vec * (c.D / 32) + l / 2] =
-                        static_cast<uint8_t>(e);
-            }
-        } else {
-            float m = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                m = fmaxf(m, fmaxf(magnitude(a[k]), magnitude(b[k])));
-            for (int d = lanes / 2; d > 0; d >>= 1)
-                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-            if (on) {
-                const float s = e4m3_scale(m);
-                const float inv = 1.0f / s;
-                uint8_t* o = c.codes + vec * c.D;
-                *reinterpret_cast<uint2*>(o + u.a) = e4m3x8(a, inv);
-                *reinterpret_cast<uint2*>(o + u.b) = e4m3x8(b, inv);
-                if (l == 0)
-                    static_cast<float*>(c.scales)[vec] = s;
-            }
+    }
+    if (rp.rot > 0) {
+        block_angles(rp, t, c.positions + r0, rows, sm_angles);
+        __syncthreads();
+    }
+    // a skipped row's lanes stay in the shuffles of the warp's other rows
+    const bool on = unit && slot >= 0 && slot < c.num_slots;
+    float a[8] = {}, b[8] = {}, ma = 0.0f, mb = 0.0f;
+    if (on) {
+        wa.values(a);
+        wb.values(b);
+        if (u.rotated)
+            rotate16(rp, sm_angles + row * rp.rot, l, a, b);
+        ma = largest(a);
+        mb = largest(b);
+    }
+    const int64_t vec = (int64_t)slot * c.heads + h0 + head;
+    if (kFp4) {
+        float* maxima = sm_groups + (threadIdx.x - l) * 2;
+        if (on) {
+            maxima[u.a / 8] = ma;
+            maxima[u.b / 8] = mb;
+        }
+        __syncwarp();
+        if (on) {
+            const uint32_t ea = e2m1_exponent(largest4(maxima + u.a / 32 * 4));
+            const uint32_t eb = e2m1_exponent(largest4(maxima + u.b / 32 * 4));
+            uint8_t* o = c.codes + vec * (c.D / 2);
+            *reinterpret_cast<uint32_t*>(o + u.a / 2) = e2m1x8(a, exp2_neg(ea));
+            *reinterpret_cast<uint32_t*>(o + u.b / 2) = e2m1x8(b, exp2_neg(eb));
+            uint8_t* sc = static_cast<uint8_t*>(c.scales) + vec * (c.D / 32);
+            if (u.a % 32 == 0)
+                sc[u.a / 32] = static_cast<uint8_t>(ea);
+            if (u.b % 32 == 0)
+                sc[u.b / 32] = static_cast<uint8_t>(eb);
+        }
+    } else {
+        float m = fmaxf(ma, mb);
+        for (int d = t.lanes / 2; d > 0; d >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        if (on) {
+            const float s = e4m3_scale(m);
+            const float inv = 1.0f / s;
+            uint8_t* o = c.codes + vec * c.D;
+            *reinterpret_cast<uint2*>(o + u.a) = e4m3x8(a, inv);
+            *reinterpret_cast<uint2*>(o + u.b) = e4m3x8(b, inv);
+            if (l == 0)
+                static_cast<float*>(c.scales)[vec] = s;
         }
     }
 }
@@ -389,11 +498,14 @@ cache_write_any_kernel(const __grid_constant__ RopeParams rp,
         for (int p = l; p < rp.rot / 2; p += 32) {
             const int a = rp.offset + (rp.interleaved ? 2 * p : p);
             const int b = rp.interleaved ? a + 1 : a + rp.rot / 2;
-            const float2 cs = turn(rp, c.positions[t], p);
+            const float2 cs = turn(rp, c.positions[t], rp.inc[p]);
             const float xa = v[a], xb = v[b];
             v[a] = fmaf(xa, cs.x, -xb * cs.y);
             v[b] = fmaf(xa, cs.y, xb * cs.x);
         }
+        __syncwarp();
+        for (int e = l; e < c.D; e += 32)
+            v[e] = v[e] == v[e] ? v[e] : 0.0f;
         __syncwarp();
         const int64_t vec = (int64_t)slot * c.heads + h;
         float m = 0.0f;
@@ -401,7 +513,7 @@ cache_write_any_kernel(const __grid_constant__ RopeParams rp,
             // lane l: the 32 elements of block l
             const int b = l < c.D / 32 ? l : 0;
             for (int e = 0; e < 32; ++e)
-                m = fmaxf(m, magnitude(v[32 * b + e]));
+                m = fmaxf(m, fabsf(v[32 * b + e]));
             const uint32_t ex = e2m1_exponent(m);
             if (l < c.D / 32) {
                 static_cast<uint8_t*>(c.scales)[vec * (c.D / 32) + l] = static_cast<uint8_t>(ex);
@@ -415,7 +527,7 @@ cache_write_any_kernel(const __grid_constant__ RopeParams rp,
             }
         } else {
             for (int e = l; e < c.D; e += 32)
-                m = fmaxf(m, magnitude(v[e]));
+                m = fmaxf(m, fabsf(v[e]));
             for (int d = 16; d > 0; d >>= 1)
                 m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
             const float s = e4m3_scale(m);
@@ -579,14 +691,28 @@ bool whole_units(const RopeParams& rp)
     return rp.rot % 16 == 0 && rp.offset % 8 == 0;
 }
 
-// Heads per thread: as many as leave two blocks per SM and more (angles shared by more
-// heads), one where there are fewer rows than that.
-int heads_per_thread(int64_t threads_per_head, int heads, int sms)
+// The tiling of a call.
+Tiling tiling(const RopeParams& rp, int rows, int heads, int lanes, int batch)
 {
-    int hp = 1;
-    while (hp < 8 && hp * 2 <= heads && threads_per_head * (heads / (2 * hp)) >= (int64_t)sms * 2048)
-        hp *= 2;
-    return hp;
+    Tiling t = {};
+    t.lanes = lanes;
+    t.groups = kThreads / lanes;
+    t.heads = std::min(heads, t.groups * batch);
+    t.rows = std::min(rows, t.groups * batch / t.heads);
+    t.by_lanes = reciprocal(lanes);
+    if (rp.rot > 0) {
+        t.rows = std::min(t.rows, kAngles / (rp.rot / 2));
+        t.angle_rows = kThreads / (rp.rot / 2);
+        t.by_pairs = reciprocal(rp.rot / 2);
+    }
+    t.by_heads = reciprocal(t.heads);
+    return t;
+}
+
+dim3 tiles(const Tiling& t, int rows, int heads)
+{
+    return dim3(static_cast<unsigned>((rows + t.rows - 1) / t.rows),
+                static_cast<unsigned>((heads + t.heads - 1) / t.heads));
 }
 
 template <typename T>
@@ -595,11 +721,9 @@ cudaError_t rope_of(const RopeParams& rp, const RopeCall& c, cudaStream_t st)
     if (whole_units(rp) && c.D % 8 == 0 && vector_rows(c.x, c.x_row, c.x_head, c.dtype) &&
         vector_rows(c.out, c.out_row, c.out_head, c.dtype)) {
         const int units = rp.rot / 16 + (c.D - rp.rot + 15) / 16;
-        const int64_t n = (int64_t)c.rows * units;
-        const int hp = heads_per_thread(n, c.heads, device_sms());
-        const dim3 grid(static_cast<unsigned>((n + kThreads - 1) / kThreads),
-                        static_cast<unsigned>((c.heads + hp - 1) / hp));
-        return launch_pdl(rope_kernel<T>, grid, dim3(kThreads), 0, st, rp, c, units, hp);
+        const Tiling t = tiling(rp, c.rows, c.heads, units, kRopeBatch);
+        return launch_pdl(rope_kernel<T>, tiles(t, c.rows, c.heads), dim3(kThreads), 0, st, rp, c,
+                          t);
     }
     const int64_t n = (int64_t)c.rows * c.heads * (c.D - rp.rot / 2);
     const unsigned blocks =
@@ -614,12 +738,9 @@ cudaError_t cache_write_of(const RopeParams& rp, const CacheWriteCall& c, cudaSt
         int lanes = 2;
         while (lanes * 16 < c.D)
             lanes *= 2;
-        const int64_t n = (int64_t)c.rows * lanes;
-        const int hp = heads_per_thread(n, c.heads, device_sms());
-        const dim3 grid(static_cast<unsigned>((n + kThreads - 1) / kThreads),
-                        static_cast<unsigned>((c.heads + hp - 1) / hp));
-        return launch_pdl(cache_write_kernel<T, kFp4>, grid, dim3(kThreads),
-                          kFp4 ? kThreads * 16 * sizeof(float) : 0, st, rp, c, lanes, hp);
+        const Tiling t = tiling(rp, c.rows, c.heads, lanes, 1);
+        return launch_pdl(cache_write_kernel<T, kFp4>, tiles(t, c.rows, c.heads), dim3(kThreads), 0,
+                          st, rp, c, t);
     }
     const int64_t n = (int64_t)c.rows * c.heads;
     const unsigned blocks = static_cast<unsigned>(
