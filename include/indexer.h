@@ -531,11 +531,11 @@ int indexer_page_slots(indexer_plan_t plan, const int32_t* page_table, int64_t l
  *   block        keys per entry: 1, 2, 4, ... 128
  *   num_sel      entries per row, 1..65,536
  *   num_slots    rows of k and v
- *   scale        finite
+ *   scale        magnitude at most 1e38
  * indexer_attention_create: host only, needs no GPU, once per batch (plan: its requests, rows
- *   and key counts); *workspace_bytes receives what a call needs (0 where rows alone fill
- *   the GPU; else partial results of rows whose keys are split over several blocks).  The plan
- *   may be destroyed afterwards.
+ *   and key counts); *workspace_bytes receives what a call needs: 256 bytes for its status, and
+ *   the partial results where the rows alone do not fill the GPU and their keys are split over
+ *   several blocks.  The plan may be destroyed afterwards.
  */
 #define IDX_KV_DENSE 0
 #define IDX_KV_FP8_E4M3 1
@@ -563,7 +563,8 @@ void indexer_attention_destroy(indexer_attention_t attention);
  * are 16-byte aligned (base and strides), the last axis contiguous, rows of k and v less than
  * 4 GiB apart; out's rows and heads are at least D apart.
  *   q [rows, Hq, D], k and v [num_slots, Hkv, D], out [rows, Hq, D]
- *   k_scale, v_scale  float [num_slots, Hkv] packed (IDX_KV_FP8_E4M3), else NULL
+ *   k_scale, v_scale  float [num_slots, Hkv] packed (IDX_KV_FP8_E4M3), positive and finite (as
+ *                     indexer_cache_write leaves them) on slots that are selected; else NULL
  *   sel               int32 [rows, num_sel], rows ld_sel apart
  *   sel_count         int32 [rows] or NULL (num_sel for every row)
  *   compress_len      int32 [rows]
@@ -590,8 +591,10 @@ typedef struct indexer_attention_io {
     int64_t ld_page_table;
 } indexer_attention_io;
 
-/* ws: 256-byte aligned, at least what indexer_attention_create asked for (may be NULL where
- * that is 0).  Two calls that overlap on the GPU need a workspace each. */
+/* ws: 256-byte aligned, at least what indexer_attention_create asked for (NULL only where the
+ * batch has no rows); its contents need no initialisation.  Two calls that overlap on the GPU
+ * need a workspace each.  A wait that gave up sets the call's status, which
+ * indexer_status(NULL, ws, stream) reads. */
 int indexer_sparse_attention(indexer_attention_t attention, const indexer_attention_io* io,
                              void* ws, size_t ws_bytes, void* stream);
 

@@ -241,7 +241,7 @@ int indexer_attention_create(indexer_plan_t plan, const indexer_attention_spec* 
         (s->block & (s->block - 1)) != 0 || s->num_sel < 1 || s->num_sel > 65536 ||
         (s->dtype != IDX_BF16 && s->dtype != IDX_FP16) ||
         (s->kv_format != IDX_KV_DENSE && s->kv_format != IDX_KV_FP8_E4M3) || s->num_slots < 0 ||
-        s->page_size < 0 || !std::isfinite(s->scale) || s->D < 1)
+        s->page_size < 0 || !(std::fabs(s->scale) <= 1e38f) || s->D < 1)
         return IDX_ERR_INVALID_ARG;
     if (s->D != 64 && s->D != 128)
         return IDX_ERR_UNSUPPORTED;
