@@ -243,6 +243,16 @@ __device__ __forceinline__ void add2_scaled(float& a0, float& a1, float b0, floa
     unpair(r, a0, a1);
 }
 
+// The largest of a warp's values (a NaN gives way): for 32 heads less work than their maxima by
+// shuffles (16,384 rows of 512 e4m3 keys and 64 heads: 4 us of 215), for 16 heads more (170 us
+// against 178).
+__device__ __forceinline__ float warp_max(float v)
+{
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // Two f16 values as e4m3 (low byte: the first); they become 16 times what is left of them.
 __device__ __forceinline__ uint32_t e4m3_split(uint32_t& h)
 {
@@ -471,11 +481,21 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                             add2(x[i + 2], x[i + 3], m.z, m.w);
                         }
                     }
+                    if (HN == 32) {
 #pragma unroll
-                    for (int c = 0; c < HN; c += 16) {
-                        const float r = reduce16<true>(x + c);
+                        for (int c = 0; c < HN; c += 4) {
+                            float4 r;
+                            r.x = warp_max(x[c]);
+                            r.y = warp_max(x[c + 1]);
+                            r.z = warp_max(x[c + 2]);
+                            r.w = warp_max(x[c + 3]);
+                            if (lane == 0)
+                                *reinterpret_cast<float4*>(scratch(b, quad * HN + c)) = r;
+                        }
+                    } else {
+                        const float r = reduce16<true>(x);
                         if ((lane & 1) == 0)
-                            *scratch(b, quad * HN + c + lane / 2) = r;
+                            *scratch(b, quad * HN + lane / 2) = r;
                     }
                     if (!bar_all(!bad, bar_id, 128)) {
                         leave = true;
@@ -645,61 +665,83 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             } else {
                 // The queries as sums of e4m3 terms, each 1/16 of the scale of the one before: two
                 // hold the 8 bits of a bf16 element, three the 11 of an fp16 one, down to 2^-22 of
-                // the item's largest.  First its magnitude, then the terms.
+                // the item's largest.
                 constexpr int kGroup = D / 16;           // lanes of a vector, 16 elements each
                 const int c = lane % kGroup;
-                float amax = 0.0f, mul = 1.0f;
-#pragma unroll 1
-                for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll 1
-                    for (int h = from / kGroup; h < heads; h += 128 / kGroup) {
-                        const uint4* at = reinterpret_cast<const uint4*>(q + h * p.q_head) + 2 * c;
-                        const uint4 in[2] = {at[0], at[1]};
-                        const T* e = reinterpret_cast<const T*>(in);
-                        if (pass == 0) {
+                // the item's largest magnitude, infinities left out, all of its elements asked for
+                // at once (a vector after another: 215 us against 202 for 4,096 rows of 64 heads)
+                using T2 = typename std::conditional<MODE == kModeFp8Bf16, __nv_bfloat162,
+                                                     __half2>::type;
+                constexpr int kIter = (NH * kGroup + 127) / 128;
+                float amax;
+                {
+                    uint4 in[kIter][2];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float m = fabsf(value(e[i]));
-                                amax = fmaxf(amax, m < INFINITY ? m : 0.0f);
-                            }
-                            continue;
-                        }
-                        uint32_t v[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            // (+ 0 x: an infinite element makes its head NaN)
-                            const float a = value(e[2 * i]), b = value(e[2 * i + 1]);
-                            v[i] = pack2<__half>(fmaf(a, 0.0f, a * mul), fmaf(b, 0.0f, b * mul));
-                        }
-#pragma unroll
-                        for (int k = 0; k < C::kQTerms; ++k) {
-                            uint32_t o[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t lo = e4m3_split(v[2 * i]);
-                                o[i] = lo | e4m3_split(v[2 * i + 1]) << 16;
-                            }
-                            *reinterpret_cast<uint4*>(
-                                dst + swizzled<C::kAtom>((k * NH + h) * C::kRow + c * 16)) =
-                                make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int k = 0; k < kIter; ++k) {
+                        const int h = from / kGroup + k * (128 / kGroup);
+                        in[k][0] = in[k][1] = make_uint4(0u, 0u, 0u, 0u);
+                        if (h < heads) {
+                            const uint4* at = reinterpret_cast<const uint4*>(q + h * p.q_head) + 2 * c;
+                            in[k][0] = at[0];
+                            in[k][1] = at[1];
                         }
                     }
-                    if (pass == 0) {
-                        float* four = qscale + kScaleItems;
+                    const T2* two = reinterpret_cast<const T2*>(in);
+                    T2 m = __habs2(two[0]);
 #pragma unroll
-                        for (int d = 16; d > 0; d >>= 1)
-                            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-                        if (lane == 0)
-                            four[quad] = amax;
-                        bar_all(true, 3, 128);
-                        amax = fmaxf(fmaxf(four[0], four[1]), fmaxf(four[2], four[3]));
-                        bar_all(true, 3, 128);
-                        // a power of two that takes amax to 128..256, so that no element is rounded
-                        const int ex = static_cast<int>(__float_as_uint(amax) >> 23);
-                        const int up = amax > 0.0f ? min(max(261 - ex, 1), 254) : 127;
-                        mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
-                        if (from == 0)
-                            qscale[nq % kScaleItems] = p.scale_log2 / mul;
+                    for (int i = 1; i < 8 * kIter; ++i)
+                        m = __hmax2(m, __habs2(two[i]));
+                    amax = fmaxf(value(m.x), value(m.y));
+                    if (!(amax < INFINITY)) {
+                        amax = 0.0f;
+                        const T* e = reinterpret_cast<const T*>(in);
+#pragma unroll
+                        for (int i = 0; i < 16 * kIter; ++i) {
+                            const float a = fabsf(value(e[i]));
+                            amax = fmaxf(amax, a < INFINITY ? a : 0.0f);
+                        }
+                    }
+                }
+                float* four = qscale + kScaleItems;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1)
+                    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+                if (lane == 0)
+                    four[quad] = amax;
+                bar_all(true, 3, 128);
+                amax = fmaxf(fmaxf(four[0], four[1]), fmaxf(four[2], four[3]));
+                bar_all(true, 3, 128);
+                // a power of two that takes amax to 128..256, so that no element is rounded
+                const int ex = static_cast<int>(__float_as_uint(amax) >> 23);
+                const int up = amax > 0.0f ? min(max(261 - ex, 1), 254) : 127;
+                const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
+                if (from == 0)
+                    qscale[nq % kScaleItems] = p.scale_log2 / mul;
+#pragma unroll 1
+                for (int h = from / kGroup; h < heads; h += 128 / kGroup) {
+                    const uint4* at = reinterpret_cast<const uint4*>(q + h * p.q_head) + 2 * c;
+                    const uint4 in[2] = {at[0], at[1]};
+                    const T* e = reinterpret_cast<const T*>(in);
+                    uint32_t v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        // (+ 0 x: an infinite element makes its head NaN)
+                        float a = value(e[2 * i]), b = value(e[2 * i + 1]), a0 = a, b0 = b;
+                        mul2(a, b, mul, mul);
+                        fma2(a0, b0, 0.0f, 0.0f, a, b);
+                        v[i] = pack2<__half>(a0, b0);
+                    }
+#pragma unroll
+                    for (int k = 0; k < C::kQTerms; ++k) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t lo = e4m3_split(v[2 * i]);
+                            o[i] = lo | e4m3_split(v[2 * i + 1]) << 16;
+                        }
+                        *reinterpret_cast<uint4*>(
+                            dst + swizzled<C::kAtom>((k * NH + h) * C::kRow + c * 16)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
                     }
                 }
             }
