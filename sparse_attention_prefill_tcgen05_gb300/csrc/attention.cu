@@ -31,12 +31,41 @@ template <>
 __device__ __forceinline__ float value(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <>
 __device__ __forceinline__ float value(__half v) { return __half2float(v); }
+
 // ---------------------------------------------------------------- tensor-core kernel
+//
+// A work item is a row, a key/value head, a tile of NH query heads and a part of the row's key
+// tiles; a persistent block per SM takes items in turn.  Per tile of 128 selected keys:
+//     S^T [keys x heads] = K Q^T,   P = exp2(S scale log2(e) - reference),   O^T += V^T P
+// in one pass: the reference per head is replaced (and O and the sums rescaled) only when a score
+// leaves its range, the sums are kept per key lane and added up once per item.  Keys are the MMA's
+// 128 rows, so a group of 16 heads fills the tensor cores' rows as well as one of 64, softmax
+// needs no exchange between threads for a key, and V is read transposed where it lies.
+//
+// What it has to do is gather: a row's keys are its own, so T x S x Hkv x 2 x D elements come
+// through L2 whatever the tiling (2,048 rows x 2,048 keys of 128 bf16: 2.1 GB; only the 64 MB
+// behind them come from HBM once).  cp.async of 16 bytes by a warp per stage moved 21 TB/s alone,
+// gathering TMA 9, plain loads 14.  Around it the roles overlap, each a warp or more of its own:
+// gather (a warp per stage, which also looks up its slots), scores, products, two softmax
+// warpgroups, four warps for queries and outputs, one of each ahead of or behind the others by a
+// tile or an item.  All waits are bounded.
+//
+// Measured (GB300; item counts fill the SMs): 32 heads of 128 over 2,048 bf16 keys, 2,048 rows
+// 171 us (12.6 TB/s gathered, 402 TFLOP/s), 64 heads 225 us (612 TFLOP/s), 16 heads 138 us; e4m3
+// caches 172, 290 and 126 us; 512 keys of 16,384 rows, 64 heads, e4m3: 0.80 ms.  What bounds it:
+// shared memory at 32 heads (a tile's 64 KB are written once and read by two MMAs: 1,220 of its
+// 1,600 cycles), the softmax warps' chain of waits, exponentials and conversions at 64, the
+// instruction cache throughout (all roles' loops are some 60 KB; at 100 KB a third of the fetches
+// missed and everything took a third longer).
+
 
 // Modes: k and v of q's type (bf16 or fp16), or e4m3 caches under bf16 or fp16 queries.
 constexpr int kModeBf16 = 0, kModeFp16 = 1, kModeFp8Bf16 = 2, kModeFp8Fp16 = 3;
 
-constexpr long long kWaitCycles = 4000000000LL;   // about two seconds
+// Polls of a wait, each suspended for up to about a microsecond: a tenth of a second at least,
+// several at most.
+constexpr int kWaitTries = 1 << 22;
+constexpr int kGaveUp = 2;   // in the block's abort flag
 constexpr int kSmemLimit = 232448;
 // Items whose query scales are held.  No barrier guards them: the scales of item i + 4 are
 // written after the scores of item i + 2's last tile were issued, and the scores of a tile are
@@ -76,12 +105,25 @@ struct AttnCfg {
     static constexpr int kFixed = kStats + kMax + kQScale + 2 * kPBytes + 2 * kQBytes + 8 * 21;
     static constexpr int kFit =
         (kSmemLimit - kFixed) / (2 * kStage + 2 * kKeyInfo + 8 * 4);
+    // Tiles in the ring: three; four where the stages are small and so few heads leave the
+    // softmax's registers free (16 heads, e4m3 124 us against 149 with three; 8 heads of 64 bf16
+    // 132 against 144; but 32 heads, e4m3 236 against 178: two more warps, fewer registers each).
     static constexpr int kMostTiles = NH == 16 && kStage <= 16384 ? 4 : 3;
     static constexpr int kTiles = kFit < kMostTiles ? kFit : kMostTiles;   // tiles in the ring
     static constexpr int kStages = 2 * kTiles;          // and as many warps that fill them
     static constexpr int kSmem = kFixed + kTiles * (2 * kStage + 2 * kKeyInfo + 8 * 4);
     static constexpr int kGatherWarp = 8 + 4, kMmaWarp = kGatherWarp + kStages;
     static constexpr int kThreads = 32 * (kMmaWarp + 2);
+    // Registers: the softmax warpgroups hold a thread's heads twice over (scores and sums), what
+    // feeds them (gather and MMA warps) needs few, so where the block is whole warpgroups they
+    // trade: at 96 each the 32-head loops spilled (64 heads over 2,048 bf16 keys, 2,048 rows: 244
+    // -> 222 us, e4m3 309 -> 290).  What is traded was launched with: 640 threads of 96.  32 heads
+    // take 136 against 56 (171 us; 128 against 64: 176), 16 heads 128 against 64 (138 us; 136
+    // against 56: 146).
+    static constexpr bool kTrade = kThreads == 640;
+    static constexpr int kSoftmaxRegs = kHeads == 32 ? 136 : 128;
+    static constexpr int kFeedRegs = kHeads == 32 ? 56 : 64;
+    static_assert(256 * kSoftmaxRegs + 128 * 96 + 256 * kFeedRegs <= 640 * 96, "registers");
     static_assert(kCols <= 512 && kTiles >= 2 && kSmem <= kSmemLimit, "tile does not fit");
 };
 
@@ -146,7 +188,7 @@ __device__ __forceinline__ AttnItem attn_item(const AttnParams& p, int item, int
 // 16 values of every lane, combined over the warp: lane i ends with value i / 2.  Out of line
 // like wait_on: it runs once per row.
 template <bool kMax>
-__device__ __noinline__ float reduce16_of(float v0, float v1, float v2, float v3, float v4,
+__device__ __forceinline__ float reduce16_of(float v0, float v1, float v2, float v3, float v4,
                                           float v5, float v6, float v7, float v8, float v9,
                                           float v10, float v11, float v12, float v13, float v14,
                                           float v15)
@@ -265,20 +307,6 @@ __device__ __forceinline__ uint32_t e4m3_split(uint32_t& h)
     return code;
 }
 
-// The rest of a wait that is not over at once.  Out of line: the roles' loops together have to
-// stay in the instruction cache (with every wait inlined a third of the fetches missed it).
-__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* ab,
-                                     uint32_t* status)
-{
-    if (mbar_wait(bar, parity, kWaitCycles, ab))
-        return true;
-    if (!*ab) {
-        *ab = 1;
-        atomicOr(status, kStatusTimeout);
-    }
-    return false;
-}
-
 template <int D, int NH, int MODE>
 __global__ void __launch_bounds__(AttnCfg<D, NH, MODE>::kThreads, 1)
 attention_tc_kernel(const __grid_constant__ AttnParams p)
@@ -353,13 +381,24 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         *p.status = *ab ? kStatusBadArg : 0u;
 
     const int total = p.rows * p.Hkv * p.head_tiles * p.splits;
+    // A short loop in place: the roles' loops together have to stay in the instruction cache, and
+    // a call would keep the compiler from giving the roles different register counts.
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return mbar_try_wait(bar, parity) || wait_on(bar, parity, ab, p.status);
+        if (mbar_try_wait(bar, parity))
+            return true;
+#pragma unroll 1
+        for (int i = 0; i < kWaitTries && *ab == 0; ++i)
+            if (mbar_try_wait_sleep(bar, parity, 1000u))
+                return true;
+        *ab = kGaveUp;
+        return false;
     };
     // Tiles, numbered over the block's items, use the score and weight buffers alternately.
 
     if (warp < 8) {
         // ---------------------------------------------------------------- softmax
+        if (C::kTrade)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         // Thread = one key of a tile (a TMEM lane) x HN heads.
         const int wg = warp / 4, quad = warp & 3, key = 32 * quad + lane, bar_id = 1 + wg;
         const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
@@ -412,7 +451,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
 #pragma unroll
                         for (int c = 0; c < HN; c += 16) {
                             float r[16];
-                            tmem_ld_32x32b_x16(tmem_s + lanes + b * C::kSCols + k * NH + head0 + c, r);
+                            tmem_ld_32x32b_x16(
+                                tmem_s + lanes + b * C::kSCols + k * NH + head0 + c, r);
                             tmem_wait_ld();
 #pragma unroll
                             for (int i = 0; i < 16; i += 2)
@@ -647,7 +687,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             // (agreed on by the four warps: they meet below)
             if (!bar_all(wait(q_empty + (nq & 1), ((nq >> 1) & 1) ^ 1), 3, 128))
                 return false;
-            const uint8_t* q = p.q + w.t * p.q_row + (int64_t)(w.g * p.group + w.ht * NH) * p.q_head;
+            const uint8_t* q =
+                p.q + w.t * p.q_row + (int64_t)(w.g * p.group + w.ht * NH) * p.q_head;
             const int heads = min(NH, p.group - w.ht * NH);
             uint8_t* dst = qbuf + (nq & 1) * C::kQBytes;
             const int from = threadIdx.x - 32 * 8;       // of the 128 threads
@@ -681,7 +722,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                         const int h = from / kGroup + k * (128 / kGroup);
                         in[k][0] = in[k][1] = make_uint4(0u, 0u, 0u, 0u);
                         if (h < heads) {
-                            const uint4* at = reinterpret_cast<const uint4*>(q + h * p.q_head) + 2 * c;
+                            const uint4* at =
+                                reinterpret_cast<const uint4*>(q + h * p.q_head) + 2 * c;
                             in[k][0] = at[0];
                             in[k][1] = at[1];
                         }
@@ -880,254 +922,268 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 ++iq;
             }
         }
-    } else if (warp < C::kMmaWarp) {
-        // ---------------------------------------------------------------- gather
-        // Warp i fills stage i of the ring: it waits for the stage, copies the 128 vectors
-        // (zeros for keys that are none), waits for its own copies and signals.  The other
-        // stages' warps keep the memory system busy meanwhile.  A warp sees every phase of
-        // the one barrier it waits on.  It reads the list entries of its next tile while its
-        // copies are under way and the pages after them.
-        const int pw = warp - C::kGatherWarp;
-        const bool is_v = pw & 1;
-        constexpr int kPerRow = C::kRow / 16;            // copies of 16 bytes a vector takes
-        constexpr int kSpan = 4 * kPerRow;               // keys of a group of kPerRow lanes
-        const int chunk = lane % kPerRow, row0 = lane / kPerRow * kSpan;
-        const uint32_t stage = smem_u32(stages + pw * C::kStage) + row0 * C::kAtom +
-                               (chunk * 16 / C::kAtom) * (kAttnTile * C::kAtom) +
-                               (chunk * 16) % C::kAtom;
-        const uint8_t* kv = (is_v ? p.v : p.k) + chunk * 16;
-        const int64_t kv_head = is_v ? p.v_head : p.k_head;
-        const uint32_t kv_slot = static_cast<uint32_t>(is_v ? p.v_slot : p.k_slot);
-        AttnItem w;
-        w.tile = w.tiles = w.n_sel = w.t = w.g = 0;
-        int item = blockIdx.x - gridDim.x, skip = pw / 2;   // tiles to the warp's next one
-        int entries = item_entries(p, blockIdx.x, total);
-        int r = 0, base = 0, most = 0, len = 0, g = 0;
-        // the lane's keys of a tile: row0 + kPerRow i + chunk, i < 4
-        int32_t entry[4], key[4], page[4];
-        auto advance = [&] {                             // to the warp's next tile; its entries
-            w.tile += skip;
-            bool fresh = false;
-            while (w.tile >= w.tiles) {
-                skip = w.tile - w.tiles;
-                item += gridDim.x;
-                if (item >= total)
-                    return false;
-                w = attn_item(p, item, entries);
-                entries = item_entries(p, item + gridDim.x, total);
+    } else {
+        if (C::kTrade)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kFeedRegs));
+        if (warp < C::kMmaWarp) {
+            // ---------------------------------------------------------------- gather
+            // Warp i fills stage i of the ring: it waits for the stage, copies the 128 vectors
+            // (zeros for keys that are none), waits for its own copies and signals.  The other
+            // stages' warps keep the memory system busy meanwhile.  A warp sees every phase of
+            // the one barrier it waits on.  It reads the list entries of its next tile while its
+            // copies are under way and the pages after them.
+            const int pw = warp - C::kGatherWarp;
+            const bool is_v = pw & 1;
+            constexpr int kPerRow = C::kRow / 16;            // copies of 16 bytes a vector takes
+            constexpr int kSpan = 4 * kPerRow;               // keys of a group of kPerRow lanes
+            const int chunk = lane % kPerRow, row0 = lane / kPerRow * kSpan;
+            const uint32_t stage = smem_u32(stages + pw * C::kStage) + row0 * C::kAtom +
+                                   (chunk * 16 / C::kAtom) * (kAttnTile * C::kAtom) +
+                                   (chunk * 16) % C::kAtom;
+            const uint8_t* kv = (is_v ? p.v : p.k) + chunk * 16;
+            const int64_t kv_head = is_v ? p.v_head : p.k_head;
+            const uint32_t kv_slot = static_cast<uint32_t>(is_v ? p.v_slot : p.k_slot);
+            AttnItem w;
+            w.tile = w.tiles = w.n_sel = w.t = w.g = 0;
+            int item = blockIdx.x - gridDim.x, skip = pw / 2;   // tiles to the warp's next one
+            int entries = item_entries(p, blockIdx.x, total);
+            int r = 0, base = 0, most = 0, len = 0, g = 0;
+            // the lane's keys of a tile: row0 + kPerRow i + chunk, i < 4
+            int32_t entry[4], key[4], page[4];
+            auto advance = [&] {                             // to the warp's next tile; its entries
                 w.tile += skip;
-                fresh = true;
-            }
-            skip = C::kTiles;
-            if (fresh) {
-                r = request_of(p.row_begin, p.num_requests, w.t);
-                base = p.key_begin[r];
-                most = p.key_begin[r + 1] - base;
-                len = p.clen[w.t];                       // (used after the copies' wait)
-            }
-            const int32_t* sel = p.sel + w.t * p.ld_sel;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int e = (w.tile * kAttnTile + row0 + kPerRow * i + chunk) >> p.block_shift;
-                entry[i] = e < w.n_sel ? sel[e] : -1;
-            }
-            return true;
-        };
-        auto locate = [&] {                              // keys and pages of the entries
-            const int32_t* table = p.table + r * p.ld_table;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int pos = w.tile * kAttnTile + row0 + kPerRow * i + chunk;
-                const int64_t k = ((int64_t)entry[i] << p.block_shift) +
-                                  (pos & ((1 << p.block_shift) - 1));
-                const bool in = entry[i] >= 0 && k < min(len, most);
-                key[i] = static_cast<int32_t>(k);
-                page[i] = in ? 0 : -1;
-                if (p.page == 0) {
-                    key[i] += base;
-                } else if (in) {
-                    const int pg = quotient(key[i], p.by_page);
-                    page[i] = table[pg];
-                    key[i] -= pg * p.page;
+                bool fresh = false;
+                while (w.tile >= w.tiles) {
+                    skip = w.tile - w.tiles;
+                    item += gridDim.x;
+                    if (item >= total)
+                        return false;
+                    w = attn_item(p, item, entries);
+                    entries = item_entries(p, item + gridDim.x, total);
+                    w.tile += skip;
+                    fresh = true;
                 }
-            }
-            g = w.g;
-        };
-        // (one copy of each step, for the instruction cache: the first round only looks up)
-        for (int u = -1;; ++u) {
-            if (u >= 0) {
-                int32_t slot[4];
-                bool whole = true;
+                skip = C::kTiles;
+                if (fresh) {
+                    r = request_of(p.row_begin, p.num_requests, w.t);
+                    base = p.key_begin[r];
+                    most = p.key_begin[r + 1] - base;
+                    len = p.clen[w.t];                       // (used after the copies' wait)
+                }
+                const int32_t* sel = p.sel + w.t * p.ld_sel;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int64_t at = (int64_t)page[i] * p.page + key[i];
-                    slot[i] = page[i] >= 0 && at < p.num_slots ? static_cast<int32_t>(at) : -1;
-                    whole = whole && slot[i] >= 0;
+                    const int e =
+                        (w.tile * kAttnTile + row0 + kPerRow * i + chunk) >> p.block_shift;
+                    entry[i] = e < w.n_sel ? sel[e] : -1;
                 }
-                whole = __all_sync(0xFFFFFFFFu, whole);
-                if (!__all_sync(0xFFFFFFFFu, wait(kv_empty + pw, (u & 1) ^ 1)))
-                    break;
-                if (!is_v) {
-                    // What the softmax has to know of the keys.  No barrier guards the place, last
-                    // read for the tile n - 2 kTiles: the scores of tile n - kTiles have freed the
-                    // stage, and were issued after those of tile n - kTiles - 2 were read.
-                    const int ring = (u * C::kTiles + pw / 2) % C::kStages * kAttnTile;
+                return true;
+            };
+            auto locate = [&] {                              // keys and pages of the entries
+                const int32_t* table = p.table + r * p.ld_table;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int pos = w.tile * kAttnTile + row0 + kPerRow * i + chunk;
+                    const int64_t k = ((int64_t)entry[i] << p.block_shift) +
+                                      (pos & ((1 << p.block_shift) - 1));
+                    const bool in = entry[i] >= 0 && k < min(len, most);
+                    key[i] = static_cast<int32_t>(k);
+                    page[i] = in ? 0 : -1;
+                    if (p.page == 0) {
+                        key[i] += base;
+                    } else if (in) {
+                        const int pg = quotient(key[i], p.by_page);
+                        page[i] = table[pg];
+                        key[i] -= pg * p.page;
+                    }
+                }
+                g = w.g;
+            };
+            // (one copy of each step, for the instruction cache: the first round only looks up)
+            for (int u = -1;; ++u) {
+                if (u >= 0) {
+                    int32_t slot[4];
+                    bool whole = true;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int k = ring + row0 + kPerRow * i + chunk;
-                        valid[k] = slot[i] >= 0;
-                        if (C::kFp8) {
-                            const int64_t at = (int64_t)max(slot[i], 0) * p.Hkv + g;
-                            kscale[k] = slot[i] >= 0 ? p.k_scale[at] : 0.0f;
-                            vscale[k] = slot[i] >= 0 ? p.v_scale[at] : 0.0f;
+                        const int64_t at = (int64_t)page[i] * p.page + key[i];
+                        slot[i] = page[i] >= 0 && at < p.num_slots ? static_cast<int32_t>(at) : -1;
+                        whole = whole && slot[i] >= 0;
+                    }
+                    whole = __all_sync(0xFFFFFFFFu, whole);
+                    if (!__all_sync(0xFFFFFFFFu, wait(kv_empty + pw, (u & 1) ^ 1)))
+                        break;
+                    if (!is_v) {
+                        // What the softmax has to know of the keys.  No barrier guards the place,
+                        // last read for the tile n - 2 kTiles: the scores of tile n - kTiles have
+                        // freed the stage, and were issued after those of tile n - kTiles - 2 were
+                        // read.
+                        const int ring = (u * C::kTiles + pw / 2) % C::kStages * kAttnTile;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int k = ring + row0 + kPerRow * i + chunk;
+                            valid[k] = slot[i] >= 0;
+                            if (C::kFp8) {
+                                const int64_t at = (int64_t)max(slot[i], 0) * p.Hkv + g;
+                                kscale[k] = slot[i] >= 0 ? p.k_scale[at] : 0.0f;
+                                vscale[k] = slot[i] >= 0 ? p.v_scale[at] : 0.0f;
+                            }
                         }
                     }
-                }
-                const uint8_t* src = kv + g * kv_head;
-                // A span's keys are spread over its lanes: slot i of lane k is key kPerRow i + k.
-                // (eight rows at a time, for the instruction cache)
-                const int from = lane & ~(kPerRow - 1);
-                auto pick = [&](int i) {
-                    const int32_t lo = i & 1 ? slot[1] : slot[0], hi = i & 1 ? slot[3] : slot[2];
-                    return i & 2 ? hi : lo;
-                };
-                if (whole) {
+                    const uint8_t* src = kv + g * kv_head;
+                    // A span's keys are spread over its lanes: slot i of lane k is key
+                    // kPerRow i + k.  (eight rows at a time, for the instruction cache)
+                    const int from = lane & ~(kPerRow - 1);
+                    auto pick = [&](int i) {
+                        const int32_t lo = i & 1 ? slot[1] : slot[0];
+                        const int32_t hi = i & 1 ? slot[3] : slot[2];
+                        return i & 2 ? hi : lo;
+                    };
+                    if (whole) {
 #pragma unroll 1
-                    for (int row = 0; row < kSpan; row += 8) {
-                        const int32_t a = pick(row / kPerRow);
-                        const int32_t b = kPerRow < 8 ? pick(row / kPerRow + 1) : a;
-                        const uint32_t dst = stage + row * C::kAtom;
-                        const int lane0 = from + row % kPerRow;
+                        for (int row = 0; row < kSpan; row += 8) {
+                            const int32_t a = pick(row / kPerRow);
+                            const int32_t b = kPerRow < 8 ? pick(row / kPerRow + 1) : a;
+                            const uint32_t dst = stage + row * C::kAtom;
+                            const int lane0 = from + row % kPerRow;
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            const uint32_t s = __shfl_sync(0xFFFFFFFFu, x < kPerRow ? a : b,
-                                                           lane0 + x % kPerRow);
-                            cp_async16(dst ^ swizzle_of<C::kAtom>(x * C::kAtom),
-                                       src + (uint64_t)s * kv_slot);
+                            for (int x = 0; x < 8; ++x) {
+                                const uint32_t s = __shfl_sync(0xFFFFFFFFu, x < kPerRow ? a : b,
+                                                               lane0 + x % kPerRow);
+                                cp_async16(dst ^ swizzle_of<C::kAtom>(x * C::kAtom),
+                                           src + (uint64_t)s * kv_slot);
+                            }
                         }
-                    }
-                } else {
+                    } else {
 #pragma unroll 1
-                    for (int row = 0; row < kSpan; ++row) {
-                        const int32_t s =
-                            __shfl_sync(0xFFFFFFFFu, pick(row / kPerRow), from + row % kPerRow);
-                        cp_async16((stage + row / 8 * 8 * C::kAtom) ^
-                                       swizzle_of<C::kAtom>(row % 8 * C::kAtom),
-                                   src + (uint64_t)(uint32_t)max(s, 0) * kv_slot, s >= 0);
+                        for (int row = 0; row < kSpan; ++row) {
+                            const int32_t s =
+                                __shfl_sync(0xFFFFFFFFu, pick(row / kPerRow), from + row % kPerRow);
+                            cp_async16((stage + row / 8 * 8 * C::kAtom) ^
+                                           swizzle_of<C::kAtom>(row % 8 * C::kAtom),
+                                       src + (uint64_t)(uint32_t)max(s, 0) * kv_slot, s >= 0);
+                        }
                     }
+                    cp_async_commit();
                 }
-                cp_async_commit();
-            }
-            const bool more = advance();
-            if (u >= 0) {
-                cp_async_wait<0>();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(kv_full + pw);
-            }
-            if (!more)
-                break;
-            locate();
-        }
-    } else {
-        // --------------------------------------------------------------------- MMA
-        // One elected lane of a warp for the scores, and of another for the products: each waits
-        // and issues.  (One thread for both took 1,400 cycles a tile for its own instructions.)
-        constexpr int kK = 32 / C::kEb;                 // contraction elements of one MMA
-        const bool scores = warp == C::kMmaWarp;
-        auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-            if (C::kFp8)
-                mma_f8f6f4(d, a, b, id, acc);
-            else
-                mma_f16(d, a, b, id, acc);
-        };
-        if (elect_one()) {
-            int n = 0, iq = 0, st = 0;                  // tile n's place in the ring
-            uint32_t phase = 0;                         // and the uses of that place
-            bool ok = true;
-            int entries = item_entries(p, blockIdx.x, total);
-            for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
-                const AttnItem w = attn_item<true>(p, item, entries);
-                entries = item_entries(p, item + gridDim.x, total);
-                const int count = w.tiles - w.tile;
-                if (count == 0)
-                    continue;
-                if (scores) {                           // S = Q K
-                    constexpr uint32_t idesc =
-                        idesc_dense(128, C::kQRows, MODE == kModeBf16 ? 1 : 0, false, false);
-                    const uint64_t q_desc =
-                        smem_desc(smem_u32(qbuf + (iq & 1) * C::kQBytes), C::kAtom, 16, 8 * C::kAtom);
-                    ok = wait(q_full + (iq & 1), (iq >> 1) & 1);
-                    for (int j = 0; j < count && ok; ++j, ++n) {
-                        ok = wait(kv_full + 2 * st, phase) &&
-                             wait(s_empty + (n & 1), ((n >> 1) & 1) ^ 1);
-                        if (!ok)
-                            break;
-                        tc_fence_after();
-                        const uint64_t k_desc = smem_desc(smem_u32(stages + 2 * st * C::kStage),
-                                                          C::kAtom, 16, 8 * C::kAtom);
-#pragma unroll
-                        for (int k = 0; k < D / kK; ++k) {
-                            const int atom = k * 32 / C::kAtom, in = (k * 32) % C::kAtom;
-                            mma(tmem_s + (n & 1) * C::kSCols,
-                                k_desc + (atom * (kAttnTile * C::kAtom) + in) / 16,
-                                q_desc + (atom * (C::kQRows * C::kAtom) + in) / 16, idesc, k > 0);
-                        }
-                        mma_commit(s_full + (n & 1));
-                        mma_commit(kv_empty + 2 * st);
-                        if (++st == C::kTiles) {
-                            st = 0;
-                            phase ^= 1;
-                        }
-                    }
-                    if (ok)
-                        mma_commit(q_empty + (iq & 1));
-                } else {                                // O += P V
-                    constexpr uint32_t idesc =
-                        idesc_dense(128, C::kOCols, MODE == kModeBf16 ? 1 : 0, true, true);
-                    // v rows are keys: both operands are read along their rows.  D = 64 takes the
-                    // same 64 elements for both halves of the 128 output rows.
-                    constexpr uint32_t lbo = D == 64 ? 0 : kAttnTile * C::kAtom;
-                    ok = wait(o_empty + (iq & 1), ((iq >> 1) & 1) ^ 1);
-                    for (int j = 0; j < count && ok; ++j, ++n) {
-                        const int b = n & 1;
-                        ok = wait(kv_full + 2 * st + 1, phase) && wait(p_full + b, (n >> 1) & 1);
-                        if (!ok)
-                            break;
-                        tc_fence_after();
-                        const uint64_t v_desc = smem_desc(
-                            smem_u32(stages + (2 * st + 1) * C::kStage), C::kAtom, lbo, 8 * C::kAtom);
-                        const uint64_t p_desc =
-                            smem_desc(smem_u32(pbuf + b * C::kPBytes), C::kPRow, 0, 8 * C::kPRow);
-                        const uint32_t d =
-                            tmem_o + ((iq & 1) * C::kAccs + (C::kAlternate ? b : 0)) * C::kOCols;
-                        const bool fresh = C::kAlternate ? j < 2 : j == 0;   // an empty accumulator
-#pragma unroll
-                        for (int k = 0; k < kAttnTile / kK; ++k)
-                            mma(d, v_desc + k * (kK * C::kAtom / 16),
-                                p_desc + k * (kK * C::kPRow / 16), idesc, !fresh || k > 0);
-                        mma_commit(p_empty + b);
-                        mma_commit(kv_empty + 2 * st + 1);
-                        if (++st == C::kTiles) {
-                            st = 0;
-                            phase ^= 1;
-                        }
-                    }
-                    if (ok)
-                        mma_commit(o_full + (iq & 1));
+                const bool more = advance();
+                if (u >= 0) {
+                    cp_async_wait<0>();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(kv_full + pw);
                 }
-                ++iq;
+                if (!more)
+                    break;
+                locate();
             }
-            // what was issued, and its arrivals, end before the memory goes
-            uint64_t* mine = drained + (scores ? 0 : 1);
-            mma_commit(mine);
-            volatile int never = 0;
-            mbar_wait(mine, 0, kWaitCycles, &never);
+        } else {
+            // --------------------------------------------------------------------- MMA
+            // One elected lane of a warp for the scores, and of another for the products: each
+            // waits and issues.  (One thread for both took 1,400 cycles a tile for its own instructions.)
+            constexpr int kK = 32 / C::kEb;                 // contraction elements of one MMA
+            const bool scores = warp == C::kMmaWarp;
+            auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+                if (C::kFp8)
+                    mma_f8f6f4(d, a, b, id, acc);
+                else
+                    mma_f16(d, a, b, id, acc);
+            };
+            if (elect_one()) {
+                int n = 0, iq = 0, st = 0;                  // tile n's place in the ring
+                uint32_t phase = 0;                         // and the uses of that place
+                bool ok = true;
+                int entries = item_entries(p, blockIdx.x, total);
+                for (int item = blockIdx.x; item < total && ok; item += gridDim.x) {
+                    const AttnItem w = attn_item<true>(p, item, entries);
+                    entries = item_entries(p, item + gridDim.x, total);
+                    const int count = w.tiles - w.tile;
+                    if (count == 0)
+                        continue;
+                    if (scores) {                           // S = Q K
+                        constexpr uint32_t idesc =
+                            idesc_dense(128, C::kQRows, MODE == kModeBf16 ? 1 : 0, false, false);
+                        const uint64_t q_desc =
+                            smem_desc(smem_u32(qbuf + (iq & 1) * C::kQBytes), C::kAtom, 16,
+                                          8 * C::kAtom);
+                        ok = wait(q_full + (iq & 1), (iq >> 1) & 1);
+                        for (int j = 0; j < count && ok; ++j, ++n) {
+                            ok = wait(kv_full + 2 * st, phase) &&
+                                 wait(s_empty + (n & 1), ((n >> 1) & 1) ^ 1);
+                            if (!ok)
+                                break;
+                            tc_fence_after();
+                            const uint64_t k_desc = smem_desc(smem_u32(stages + 2 * st * C::kStage),
+                                                              C::kAtom, 16, 8 * C::kAtom);
+#pragma unroll
+                            for (int k = 0; k < D / kK; ++k) {
+                                const int atom = k * 32 / C::kAtom, in = (k * 32) % C::kAtom;
+                                mma(tmem_s + (n & 1) * C::kSCols,
+                                    k_desc + (atom * (kAttnTile * C::kAtom) + in) / 16,
+                                    q_desc + (atom * (C::kQRows * C::kAtom) + in) / 16, idesc, k > 0);
+                            }
+                            mma_commit(s_full + (n & 1));
+                            mma_commit(kv_empty + 2 * st);
+                            if (++st == C::kTiles) {
+                                st = 0;
+                                phase ^= 1;
+                            }
+                        }
+                        if (ok)
+                            mma_commit(q_empty + (iq & 1));
+                    } else {                                // O += P V
+                        constexpr uint32_t idesc =
+                            idesc_dense(128, C::kOCols, MODE == kModeBf16 ? 1 : 0, true, true);
+                        // v rows are keys: both operands are read along their rows.  D = 64 takes
+                        // the same 64 elements for both halves of the 128 output rows.
+                        constexpr uint32_t lbo = D == 64 ? 0 : kAttnTile * C::kAtom;
+                        ok = wait(o_empty + (iq & 1), ((iq >> 1) & 1) ^ 1);
+                        for (int j = 0; j < count && ok; ++j, ++n) {
+                            const int b = n & 1;
+                            ok = wait(kv_full + 2 * st + 1, phase) &&
+                                 wait(p_full + b, (n >> 1) & 1);
+                            if (!ok)
+                                break;
+                            tc_fence_after();
+                            const uint64_t v_desc = smem_desc(
+                                smem_u32(stages + (2 * st + 1) * C::kStage), C::kAtom, lbo,
+                                8 * C::kAtom);
+                            const uint64_t p_desc =
+                                smem_desc(smem_u32(pbuf + b * C::kPBytes), C::kPRow, 0,
+                                          8 * C::kPRow);
+                            const uint32_t d =
+                                tmem_o + ((iq & 1) * C::kAccs + (C::kAlternate ? b : 0)) * C::kOCols;
+                            // an empty accumulator
+                            const bool fresh = C::kAlternate ? j < 2 : j == 0;
+#pragma unroll
+                            for (int k = 0; k < kAttnTile / kK; ++k)
+                                mma(d, v_desc + k * (kK * C::kAtom / 16),
+                                    p_desc + k * (kK * C::kPRow / 16), idesc, !fresh || k > 0);
+                            mma_commit(p_empty + b);
+                            mma_commit(kv_empty + 2 * st + 1);
+                            if (++st == C::kTiles) {
+                                st = 0;
+                                phase ^= 1;
+                            }
+                        }
+                        if (ok)
+                            mma_commit(o_full + (iq & 1));
+                    }
+                    ++iq;
+                }
+                // what was issued, and its arrivals, end before the memory goes
+                uint64_t* mine = drained + (scores ? 0 : 1);
+                mma_commit(mine);
+                for (int i = 0; i < kWaitTries && !mbar_try_wait_sleep(mine, 0, 1000u); ++i)
+                    ;
+            }
+            __syncwarp();
         }
-        __syncwarp();
     }
     __syncthreads();
+    if (threadIdx.x == 0 && *ab == kGaveUp)
+        atomicOr(p.status, kStatusTimeout);
     if (warp == C::kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem_s, C::kTmem);
@@ -1205,9 +1261,19 @@ template <int D, int NH, int MODE>
 cudaError_t attention_tc(const AttnParams& p, cudaStream_t st)
 {
     using C = AttnCfg<D, NH, MODE>;
-    static const cudaError_t attr =
-        cudaFuncSetAttribute(attention_tc_kernel<D, NH, MODE>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static const cudaError_t attr = [] {
+        // the warpgroups' trade has to add up against what a block is launched with
+        cudaFuncAttributes a;
+        cudaError_t e = cudaFuncGetAttributes(&a, attention_tc_kernel<D, NH, MODE>);
+        if (e == cudaSuccess && C::kTrade &&
+            a.numRegs * C::kThreads <
+                256 * C::kSoftmaxRegs + 128 * a.numRegs + 256 * C::kFeedRegs)
+            e = cudaErrorLaunchOutOfResources;
+        return e != cudaSuccess
+                   ? e
+                   : cudaFuncSetAttribute(attention_tc_kernel<D, NH, MODE>,
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    }();
     if (attr != cudaSuccess)
         return attr;
     const int items = p.rows * p.Hkv * p.head_tiles * p.splits;
@@ -1309,7 +1375,10 @@ mask_blocks_kernel(const __grid_constant__ MaskBlocksParams p)
 
 int attention_heads_per_tile(int group, int dtype, bool fp8)
 {
-    // three terms of 64 fp16 heads do not fit the tensor memory
+    // The smallest tile that holds the group: a wider one computes heads that are none (16 heads in
+    // tiles of 16 138 us, of 32 165; 32 heads of 32 171, of 64 235: 2,048 rows, 2,048 keys of
+    // 128 bf16), a narrower one gathers the keys again for each (32 heads in two of 16 295 us, 64
+    // in two of 32 331 against 225).  Three terms of 64 fp16 heads do not fit the tensor memory.
     return group <= 16 ? 16 : group <= 32 || (fp8 && dtype == IDX_FP16) ? 32 : 64;
 }
 

@@ -393,9 +393,9 @@ __device__ __forceinline__ float exp2_neg(uint32_t e) { return __uint_as_float((
 //
 // Instructions bound it, not bytes (some 300 per warp and 512 elements: widening, turning,
 // maxima, two divisions, narrowing; without rotation and divisions it runs at 5.9 TB/s), so
-// registers are held down for six blocks per SM (four with fp32, which would spill).  16,384 x 32 x 128 bf16 with 64 turned: e4m3
-// 50 us, e2m1 54 us (4.0 and 3.1 TB/s); two vectors in a group's flight took 58 and 51 us, four
-// 67 and 61 us.
+// registers are held down for six blocks per SM (four with fp32, which would spill).  16,384 x
+// 32 x 128 bf16 with 64 turned: e4m3 50 us, e2m1 54 us (4.0 and 3.1 TB/s); two vectors of a
+// group in flight took 58 and 51 us, four 67 and 61 us.
 template <typename T, bool kFp4>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 6 : 4)
 cache_write_kernel(const __grid_constant__ RopeParams rp,
