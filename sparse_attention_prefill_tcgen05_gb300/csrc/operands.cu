@@ -132,6 +132,7 @@ __device__ __forceinline__ Unit unit_of(const RopeParams& rp, int u, int D)
 // groups of lanes, and a few per group with their loads in flight together.
 struct Tiling {
     int32_t rows, heads, lanes, groups;
+    int32_t batch;               // vectors a group takes
     int32_t angle_rows;          // rows whose angles the block's threads take at a time
     uint32_t by_heads, by_lanes, by_pairs;   // for quotient()
 };
@@ -318,8 +319,9 @@ __device__ __forceinline__ float largest(float (&v)[8])
 {
     float m = fabsf(v[0]);
 #pragma unroll
-    for (int i = 1; i < 8; ++i)
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[i])));
+    for (int i = 1; i < 7; i += 2)
+        asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(v[i])), "f"(fabsf(v[i + 1])));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[7])));
     if (m == m)
         return m;
     m = 0.0f;
@@ -386,18 +388,19 @@ __device__ __forceinline__ uint32_t e2m1_exponent(float amax)
 // 2^(127 - e) for a biased exponent e in 0..252 (the exponents e2m1_exponent returns).
 __device__ __forceinline__ float exp2_neg(uint32_t e) { return __uint_as_float((254u - e) << 23); }
 
-// The same tiling with one vector per group, `lanes` a power of two: the largest magnitude of a
-// vector (e4m3) by a shuffle reduction over its lanes.  An e2m1 scale covers 32 neighbours,
-// four groups of eight that any lanes may hold: the groups' maxima meet in shared memory, the
-// values stay where they are (exchanging the values took 2.4 times as long).
+// The same tiling, `lanes` a power of two; a group takes its vectors one after another, the next
+// one's loads under way.  The largest magnitude of a vector (e4m3) by a shuffle reduction over
+// its lanes.  An e2m1 scale covers 32 neighbours, four groups of eight that any lanes may hold:
+// the groups' maxima meet in shared memory, the values stay where they are (exchanging the values
+// took 2.4 times as long).
 //
-// Instructions bound it, not bytes (some 300 per warp and 512 elements: widening, turning,
-// maxima, two divisions, narrowing; without rotation and divisions it runs at 5.9 TB/s), so
-// registers are held down for six blocks per SM (four with fp32, which would spill).  16,384 x
-// 32 x 128 bf16 with 64 turned: e4m3 50 us, e2m1 54 us (4.0 and 3.1 TB/s); two vectors of a
-// group in flight took 58 and 51 us, four 67 and 61 us.
+// Instructions bound it, not bytes (some 300 per warp and 512 elements: widening, turning, maxima,
+// two divisions, narrowing; without rotation and divisions it runs at 5.9 TB/s).  16,384 x 32 x
+// 128 bf16 with 64 turned: e4m3 42 us, e2m1 42 us (4.8 and 4.0 TB/s).  Blocks of 64 registers,
+// four an SM: at 40 and six the loop took 52 and 58 us, and without it, a vector a group, whose
+// set-up is a third of its instructions, it was 50 and 53 us at best.
 template <typename T, bool kFp4>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 6 : 4)
+__global__ void __launch_bounds__(kThreads, 4)
 cache_write_kernel(const __grid_constant__ RopeParams rp,
                    const __grid_constant__ CacheWriteCall c, const __grid_constant__ Tiling t)
 {
@@ -408,67 +411,90 @@ cache_write_kernel(const __grid_constant__ RopeParams rp,
     const int l = threadIdx.x - g * t.lanes;
     const int r0 = blockIdx.x * t.rows, h0 = blockIdx.y * t.heads;
     const int rows = min(t.rows, c.rows - r0), heads = min(t.heads, c.heads - h0);
-    const int row = quotient(g, t.by_heads), head = g - row * t.heads;
     const Unit u = unit_of(rp, l, c.D);
     const bool unit = l < c.D / 16;
+    const T* x = static_cast<const T*>(c.x) + r0 * c.x_row + h0 * c.x_head;
     Eight<T> wa, wb;
-    int slot = -1;
-    if (row < rows && head < heads) {
-        slot = c.slots ? c.slots[r0 + row] : r0 + row;
-        if (unit) {
-            const T* p = static_cast<const T*>(c.x) + (r0 + row) * c.x_row + (h0 + head) * c.x_head;
-            wa.load(p + u.a);
-            wb.load(p + u.b);
+    int row = quotient(g, t.by_heads), head = g - row * t.heads, slot = -1;
+    auto load = [&] {
+        slot = -1;
+        if (row < rows && head < heads) {
+            slot = c.slots ? c.slots[r0 + row] : r0 + row;
+            if (unit) {
+                const T* p = x + row * c.x_row + head * c.x_head;
+                wa.load(p + u.a);
+                wb.load(p + u.b);
+            }
         }
-    }
+    };
+    load();
     if (rp.rot > 0) {
         block_angles(rp, t, c.positions + r0, rows, sm_angles);
         __syncthreads();
     }
-    // a skipped row's lanes stay in the shuffles of the warp's other rows
-    const bool on = unit && slot >= 0 && slot < c.num_slots;
-    float a[8] = {}, b[8] = {}, ma = 0.0f, mb = 0.0f;
-    if (on) {
-        wa.values(a);
-        wb.values(b);
-        if (u.rotated)
-            rotate16(rp, sm_angles + row * rp.rot, l, a, b);
-        ma = largest(a);
-        mb = largest(b);
-    }
-    const int64_t vec = (int64_t)slot * c.heads + h0 + head;
-    if (kFp4) {
-        float* maxima = sm_groups + (threadIdx.x - l) * 2;
+    float* maxima = sm_groups + (kFp4 ? (threadIdx.x - l) * 2 : 0);
+    const int row_step = quotient(t.groups, t.by_heads), head_step = t.groups - row_step * t.heads;
+#pragma unroll 1
+    for (int j = 0;;) {
+        // a skipped row's lanes stay in the shuffles of the warp's other rows
+        const bool on = unit && slot >= 0 && slot < c.num_slots;
+        const int64_t vec = (int64_t)slot * c.heads + h0 + head;
+        const int angles = row * rp.rot;
+        float a[8] = {}, b[8] = {}, ma = 0.0f, mb = 0.0f;
         if (on) {
-            maxima[u.a / 8] = ma;
-            maxima[u.b / 8] = mb;
+            wa.values(a);
+            wb.values(b);
         }
-        __syncwarp();
+        if (++j < t.batch) {
+            row += row_step;
+            head += head_step;
+            if (head >= t.heads) {
+                head -= t.heads;
+                ++row;
+            }
+            load();
+        }
         if (on) {
-            const uint32_t ea = e2m1_exponent(largest4(maxima + u.a / 32 * 4));
-            const uint32_t eb = e2m1_exponent(largest4(maxima + u.b / 32 * 4));
-            uint8_t* o = c.codes + vec * (c.D / 2);
-            *reinterpret_cast<uint32_t*>(o + u.a / 2) = e2m1x8(a, exp2_neg(ea));
-            *reinterpret_cast<uint32_t*>(o + u.b / 2) = e2m1x8(b, exp2_neg(eb));
-            uint8_t* sc = static_cast<uint8_t*>(c.scales) + vec * (c.D / 32);
-            if (u.a % 32 == 0)
-                sc[u.a / 32] = static_cast<uint8_t>(ea);
-            if (u.b % 32 == 0)
-                sc[u.b / 32] = static_cast<uint8_t>(eb);
+            if (u.rotated)
+                rotate16(rp, sm_angles + angles, l, a, b);
+            ma = largest(a);
+            mb = largest(b);
         }
-    } else {
-        float m = fmaxf(ma, mb);
-        for (int d = t.lanes / 2; d > 0; d >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-        if (on) {
-            const float s = e4m3_scale(m);
-            const float inv = 1.0f / s;
-            uint8_t* o = c.codes + vec * c.D;
-            *reinterpret_cast<uint2*>(o + u.a) = e4m3x8(a, inv);
-            *reinterpret_cast<uint2*>(o + u.b) = e4m3x8(b, inv);
-            if (l == 0)
-                static_cast<float*>(c.scales)[vec] = s;
+        if (kFp4) {
+            if (on) {
+                maxima[u.a / 8] = ma;
+                maxima[u.b / 8] = mb;
+            }
+            __syncwarp();
+            if (on) {
+                const uint32_t ea = e2m1_exponent(largest4(maxima + u.a / 32 * 4));
+                const uint32_t eb = e2m1_exponent(largest4(maxima + u.b / 32 * 4));
+                uint8_t* o = c.codes + vec * (c.D / 2);
+                *reinterpret_cast<uint32_t*>(o + u.a / 2) = e2m1x8(a, exp2_neg(ea));
+                *reinterpret_cast<uint32_t*>(o + u.b / 2) = e2m1x8(b, exp2_neg(eb));
+                uint8_t* sc = static_cast<uint8_t*>(c.scales) + vec * (c.D / 32);
+                if (u.a % 32 == 0)
+                    sc[u.a / 32] = static_cast<uint8_t>(ea);
+                if (u.b % 32 == 0)
+                    sc[u.b / 32] = static_cast<uint8_t>(eb);
+            }
+            __syncwarp();
+        } else {
+            float m = fmaxf(ma, mb);
+            for (int d = t.lanes / 2; d > 0; d >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            if (on) {
+                const float s = e4m3_scale(m);
+                const float inv = 1.0f / s;
+                uint8_t* o = c.codes + vec * c.D;
+                *reinterpret_cast<uint2*>(o + u.a) = e4m3x8(a, inv);
+                *reinterpret_cast<uint2*>(o + u.b) = e4m3x8(b, inv);
+                if (l == 0)
+                    static_cast<float*>(c.scales)[vec] = s;
+            }
         }
+        if (j >= t.batch)
+            break;
     }
 }
 
@@ -705,6 +731,7 @@ Tiling tiling(const RopeParams& rp, int rows, int heads, int lanes, int batch)
         t.angle_rows = kThreads / (rp.rot / 2);
         t.by_pairs = reciprocal(rp.rot / 2);
     }
+    t.batch = (t.rows * t.heads + t.groups - 1) / t.groups;
     t.by_heads = reciprocal(t.heads);
     return t;
 }
@@ -738,7 +765,13 @@ cudaError_t cache_write_of(const RopeParams& rp, const CacheWriteCall& c, cudaSt
         int lanes = 2;
         while (lanes * 16 < c.D)
             lanes *= 2;
-        const Tiling t = tiling(rp, c.rows, c.heads, lanes, 1);
+        // Several vectors a group, up to eight, where that leaves six blocks an SM (rows of 32
+        // heads to e4m3: 16,384 rows 42 us in eights, 61 one by one; 4,096 rows 12.6 in fours,
+        // 13.6 in eights, 15.7 one by one; 1,024 rows 5.0 one by one, 6.3 in threes).
+        const int64_t blocks = ((int64_t)c.rows * c.heads * lanes + kThreads - 1) / kThreads;
+        const int batch = static_cast<int>(
+            std::max<int64_t>(1, std::min<int64_t>(8, blocks / (6 * device_sms()))));
+        const Tiling t = tiling(rp, c.rows, c.heads, lanes, batch);
         return launch_pdl(cache_write_kernel<T, kFp4>, tiles(t, c.rows, c.heads), dim3(kThreads), 0,
                           st, rp, c, t);
     }
