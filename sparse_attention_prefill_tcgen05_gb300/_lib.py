@@ -105,6 +105,7 @@ class _AttentionIo(ctypes.Structure):
 _ATTENTION_IO = struct.Struct("11P10q").pack
 
 _lib = None
+_C = torch._C
 
 
 def lib():
@@ -185,7 +186,8 @@ def _stream(stream=None):
     """The cudaStream_t of a torch stream (default: the current one of the current device)."""
     if stream is None:
         # the raw handle: building a torch.cuda.Stream object takes longer than a small kernel
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # (no lazy initialisation either: there are CUDA tensors)
+        return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -391,15 +393,16 @@ def indexer_chunk_rows(prefix_len: int, budget_token2: float = 2.0e8, chunk_min:
 # The checks are written out and pointers passed as plain integers: a call of a decode step
 # runs for a few microseconds on the GPU, and as long here.
 
+_INT32 = torch.int32
 _DTYPES = {torch.bfloat16: IDX_BF16, torch.float16: IDX_FP16, torch.float32: IDX_FP32}
 
 
 def _dense(name: str, t):
     """Type code and strides of a 3-d CUDA tensor whose last axis is contiguous."""
     code = _DTYPES.get(t.dtype)
-    if code is None or not t.is_cuda or t.dim() != 3:
-        raise ValueError(f"{name}: 3-d bf16, fp16 or fp32 CUDA tensor expected")
     st = t.stride()
+    if code is None or len(st) != 3 or not t.is_cuda:
+        raise ValueError(f"{name}: 3-d bf16, fp16 or fp32 CUDA tensor expected")
     if st[2] != 1 and t.shape[2] > 1:
         raise ValueError(f"{name}: a contiguous last axis expected")
     return code, st
@@ -409,7 +412,7 @@ def _i32(name: str, t, shape):
     """Address of a contiguous int32 CUDA tensor of that shape, or None."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not _INT32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous int32 CUDA tensor of shape {tuple(shape)} expected")
     return t.data_ptr()
 
@@ -448,11 +451,12 @@ def indexer_rope(rope: Rope, x, positions, out=None, inverse: bool = False, stre
     code, sx = _dense("x", x)
     if out is None:
         out = torch.empty_like(x)
-    rows, heads, D = x.shape
-    ocode, so = _dense("out", out)
-    if ocode != code or out.shape != x.shape or D != rope.D:
+    shape = x.shape
+    rows, heads, D = shape
+    ocode, so = (code, sx) if out is x else _dense("out", out)
+    if ocode != code or out.shape != shape or D != rope.D:
         raise ValueError("out: a tensor of x's shape and type, D elements a head, expected")
-    rc = lib().indexer_rope(rope.handle, x.data_ptr(), code, rows, heads, sx[0], sx[1],
+    rc = (_lib or lib()).indexer_rope(rope.handle, x.data_ptr(), code, rows, heads, sx[0], sx[1],
                             _i32("positions", positions, (rows,)), 1 if inverse else 0,
                             out.data_ptr(), so[0], so[1], _stream(stream))
     if rc != IDX_OK:
@@ -481,11 +485,11 @@ def indexer_cache_write(x, codes, scales, fmt: int = IDX_K_FP8_E4M3, rope: Optio
     default: row i) of a cache: ``codes`` [num_slots, heads, D] (e2m1: D/2) and ``scales``."""
     n, heads, D = _cache_shape(codes, scales, fmt)
     code, sx = _dense("x", x)
-    rows = x.shape[0]
-    if x.shape[1] != heads or x.shape[2] != D:
+    rows, x_heads, x_D = x.shape
+    if x_heads != heads or x_D != D:
         raise ValueError(f"x: [rows, {heads}, {D}] expected")
     shape = (rows,)
-    rc = lib().indexer_cache_write(
+    rc = (_lib or lib()).indexer_cache_write(
         None if rope is None else rope.handle, x.data_ptr(), code, rows, heads, D, sx[0], sx[1],
         _i32("positions", positions, shape), _i32("slots", slots, shape), n, fmt,
         codes.data_ptr(), scales.data_ptr(), _stream(stream))
@@ -504,9 +508,9 @@ def indexer_cache_read(codes, scales, fmt: int, slots, out, out_scales=None, str
             raise ValueError("out: codes of the cache's heads and size expected")
     else:
         code, _ = _dense("out", out)
-        if out.shape[1] != heads or out.shape[2] != D or not out.is_contiguous():
+        if out.shape != (rows, heads, D) or not out.is_contiguous():
             raise ValueError(f"out: contiguous [rows, {heads}, {D}] expected")
-    rc = lib().indexer_cache_read(
+    rc = (_lib or lib()).indexer_cache_read(
         codes.data_ptr(), scales.data_ptr(), fmt, n, heads, D, _i32("slots", slots, (rows,)), rows,
         code, out.data_ptr(), _ptr(out_scales), _stream(stream))
     if rc != IDX_OK:
@@ -614,7 +618,7 @@ def indexer_sparse_attention(attn: Attention, q, k, v, sel, compress_len, out, w
         _i32("compress_len", compress_len, attn.row_shape) or 0, table,
         _f32("lse", lse, attn.lse_shape), sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1],
         sel.stride(0) if attn.rows > 1 else attn.spec.num_sel, ld_table)
-    rc = lib().indexer_sparse_attention(
+    rc = (_lib or lib()).indexer_sparse_attention(
         attn.handle, io, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
         _stream(stream))
     if rc != IDX_OK:
@@ -631,7 +635,7 @@ def indexer_mask_blocks(plan: Plan, cand_mask, compress_len, block: int, blocks,
             cand_mask.shape[0] != rows or cand_mask.stride(1) != 1:
         raise ValueError("cand_mask: CUDA tensor [rows, blocks] of one byte expected")
     num_sel, shape = blocks.shape[-1], (rows,)
-    rc = lib().indexer_mask_blocks(
+    rc = (_lib or lib()).indexer_mask_blocks(
         plan.handle, cand_mask.data_ptr(), cand_mask.stride(0) if rows > 1 else cand_mask.shape[1],
         _i32("compress_len", compress_len, shape), int(block),
         _i32("blocks", blocks, (rows, num_sel)), num_sel, _i32("count", count, shape),
