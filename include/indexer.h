@@ -534,8 +534,8 @@ int indexer_page_slots(indexer_plan_t plan, const int32_t* page_table, int64_t l
  *   scale        magnitude at most 1e38
  * indexer_attention_create: host only, needs no GPU, once per batch (plan: its requests, rows
  *   and key counts); *workspace_bytes receives what a call needs: 256 bytes for its status, and
- *   the partial results where the rows alone do not fill the GPU and their keys are split over
- *   several blocks.  The plan may be destroyed afterwards.
+ *   partial results where the rows alone do not fill the GPU and their keys are split over many
+ *   blocks.  The plan may be destroyed afterwards.
  */
 #define IDX_KV_DENSE 0
 #define IDX_KV_FP8_E4M3 1

@@ -123,7 +123,11 @@ struct AttnCfg {
     static constexpr bool kTrade = kThreads == 640;
     static constexpr int kSoftmaxRegs = kHeads == 32 ? 136 : 128;
     static constexpr int kFeedRegs = kHeads == 32 ? 56 : 64;
-    static_assert(256 * kSoftmaxRegs + 128 * 96 + 256 * kFeedRegs <= 640 * 96, "registers");
+    static constexpr int kLaunchRegs = 96;
+    static_assert(256 * kSoftmaxRegs + 128 * kLaunchRegs + 256 * kFeedRegs <= 640 * kLaunchRegs,
+                  "registers");
+    static_assert(NH * D * 4 <= kStages * kStage && NH * 8 <= kStages * kAttnTile,
+                  "a split's part in shared memory");
     static_assert(kCols <= 512 && kTiles >= 2 && kSmem <= kSmemLimit, "tile does not fit");
 };
 
@@ -663,6 +667,9 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             n += count;
             ++iq;
         }
+        __syncwarp();
+        if (C::kTrade)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLaunchRegs));
     } else if (warp < C::kGatherWarp) {
         // --------------------------------------------------------------- epilogue
         // Thread = one element (of D) of NH heads.
@@ -812,7 +819,13 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             const int heads = parts ? NH : min(NH, p.group - head0);
             uint8_t* out =
                 p.out + w.t * p.out_row + (int64_t)(w.g * p.group + head0) * p.out_head + 2 * dim;
-            float* part = p.part_o + (int64_t)item * NH * D + dim;
+            // (A cluster's parts stay in shared memory, for a block's one item: the sums and maxima
+            // where softmax, which is done with the keys by then, read what it had to know of
+            // them; the output in the stages once the last product is complete.)
+            float* part = (p.cluster ? reinterpret_cast<float*>(stages)
+                                     : p.part_o + (int64_t)item * NH * D) + dim;
+            float2* part_ml = p.cluster ? reinterpret_cast<float2*>(valid)
+                                        : reinterpret_cast<float2*>(p.part_ml) + (int64_t)item * NH;
             // Factors of the accumulators, for head `lane` (+ 32): the weight of its maximum,
             // over the sum.
             float fa[(NH + 31) / 32], fb = 0.0f;
@@ -838,8 +851,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 }
                 if (quad == 0 && h < heads) {
                     if (parts)
-                        reinterpret_cast<float2*>(p.part_ml)[(int64_t)item * NH + h] =
-                            make_float2(m, l);
+                        part_ml[h] = make_float2(m, l);
                     else if (p.lse)
                         p.lse[(int64_t)w.t * p.Hq + w.g * p.group + head0 + h] =
                             (m + __log2f(l)) * 0.693147180559945309f;
@@ -1178,21 +1190,73 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 for (int i = 0; i < kWaitTries && !mbar_try_wait_sleep(mine, 0, 1000u); ++i)
                     ;
             }
-            __syncwarp();
         }
+        __syncwarp();
+        if (C::kTrade)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kLaunchRegs));
     }
     __syncthreads();
     if (threadIdx.x == 0 && *ab == kGaveUp)
         atomicOr(p.status, kStatusTimeout);
+    if (p.cluster) {
+        // The blocks of a row's splits are a cluster and have an item each: every block joins its
+        // share of the heads from all blocks' parts.
+        cluster_sync();
+        const AttnItem w = attn_item(p, blockIdx.x, p.num_sel);
+        const int heads = min(NH, p.group - w.ht * NH), head0 = w.g * p.group + w.ht * NH;
+        constexpr int kPer = D / 4;                      // threads of a head, four elements each
+        const int d = threadIdx.x % kPer * 4;
+        const uint32_t parts = smem_u32(stages), ml = smem_u32(valid);
+        for (int h = w.split + threadIdx.x / kPer * p.splits; h < heads;
+             h += C::kThreads / kPer * p.splits) {
+            float2 stat[kMaxCluster];                    // maximum and sum
+            float4 v[kMaxCluster];
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) {
+                stat[r] = make_float2(-3.0e38f, 0.0f);
+                if (r < p.splits) {
+                    stat[r] = ld_cluster2(cluster_address(ml + 8 * h, r));
+                    v[r] = ld_cluster4(cluster_address(parts + (h * D + d) * 4, r));
+                }
+            }
+            float m = stat[0].x, l = 0.0f;
+#pragma unroll
+            for (int r = 1; r < kMaxCluster; ++r)
+                m = fmaxf(m, stat[r].x);
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) {
+                const float f = ex2(stat[r].x - m);
+                l = fmaf(stat[r].y, f, l);
+                if (r < p.splits && f != 0.0f) {
+                    o.x = fmaf(v[r].x, f, o.x);
+                    o.y = fmaf(v[r].y, f, o.y);
+                    o.z = fmaf(v[r].z, f, o.z);
+                    o.w = fmaf(v[r].w, f, o.w);
+                }
+            }
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            T* out = reinterpret_cast<T*>(p.out + w.t * p.out_row +
+                                          (int64_t)(head0 + h) * p.out_head) + d;
+            out[0] = static_cast<T>(o.x * inv);
+            out[1] = static_cast<T>(o.y * inv);
+            out[2] = static_cast<T>(o.z * inv);
+            out[3] = static_cast<T>(o.w * inv);
+            if (p.lse && d == 0)
+                p.lse[(int64_t)w.t * p.Hq + head0 + h] =
+                    (m + log2f(l)) * 0.693147180559945309f;
+        }
+        cluster_sync();                                  // no block leaves while it is read
+    }
     if (warp == C::kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem_s, C::kTmem);
     }
 }
 
-// Split rows: the partial outputs of a row and head, weighted by their maxima.  One warp per
-// (row, query head): the maxima and sums of all splits in one read, the parts four at a time
-// (read one after another, 16 parts took 8 us).
+// Rows split over more blocks than a cluster joins: the partial outputs of a row and head, weighted
+// by their maxima.  One warp per (row, query head): the maxima and sums of all splits in one read,
+// the parts four at a time (read one after another, 16 parts took 8 us).
 template <typename T, int D>
 __global__ void __launch_bounds__(128)
 attention_join_kernel(const __grid_constant__ AttnParams p, int nh)
@@ -1265,9 +1329,7 @@ cudaError_t attention_tc(const AttnParams& p, cudaStream_t st)
         // the warpgroups' trade has to add up against what a block is launched with
         cudaFuncAttributes a;
         cudaError_t e = cudaFuncGetAttributes(&a, attention_tc_kernel<D, NH, MODE>);
-        if (e == cudaSuccess && C::kTrade &&
-            a.numRegs * C::kThreads <
-                256 * C::kSoftmaxRegs + 128 * a.numRegs + 256 * C::kFeedRegs)
+        if (e == cudaSuccess && C::kTrade && a.numRegs != C::kLaunchRegs)
             e = cudaErrorLaunchOutOfResources;
         return e != cudaSuccess
                    ? e
@@ -1277,8 +1339,9 @@ cudaError_t attention_tc(const AttnParams& p, cudaStream_t st)
     if (attr != cudaSuccess)
         return attr;
     const int items = p.rows * p.Hkv * p.head_tiles * p.splits;
-    return launch_pdl(attention_tc_kernel<D, NH, MODE>, dim3(std::min(items, device_sms())),
-                      dim3(C::kThreads), C::kSmem, st, p);
+    const unsigned blocks = p.cluster ? items : std::min(items, device_sms());
+    return launch_pdl_cluster(attention_tc_kernel<D, NH, MODE>, dim3(blocks), dim3(C::kThreads),
+                              C::kSmem, st, p.cluster ? p.splits : 1, p);
 }
 
 template <int D, int MODE>
@@ -1291,7 +1354,7 @@ cudaError_t attention_heads(const AttnParams& p, int nh, cudaStream_t st)
         e = attention_tc<D, 32, MODE>(p, st);
     else
         e = attention_tc<D, MODE == kModeFp8Fp16 ? 32 : 64, MODE>(p, st);
-    if (e != cudaSuccess || p.splits == 1)
+    if (e != cudaSuccess || p.splits == 1 || p.cluster)
         return e;
     using T = typename std::conditional<MODE == kModeBf16 || MODE == kModeFp8Bf16, __nv_bfloat16,
                                         __half>::type;

@@ -27,6 +27,7 @@ struct indexer_attention_s {
 namespace {
 
 constexpr int kPlanSms = 152;    // SMs the splits are planned for
+constexpr int kClusterBlocks = 144;   // blocks in clusters of 4 that run at once
 
 bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -269,11 +270,14 @@ int indexer_attention_create(indexer_plan_t plan, const indexer_attention_spec* 
     std::copy(v.row_begin, v.row_begin + v.R + 1, p.row_begin);
     std::copy(v.key_begin, v.key_begin + v.R + 1, p.key_begin);
     // Work items: rows x key/value heads x tiles of query heads, each over the row's key
-    // tiles.  Where they do not fill the SMs, the tiles of a row are split: the number of
-    // splits that ends first by measured times (one row of 16 tiles: 16.6 us whole, 10.9 in
-    // 4 splits, 9.6 in 8; 64 rows of 16: 18.1 whole, 17.4 in 2, 19.9 in 4; 64 rows of 4: 8.8
-    // whole, 12.0 in 2): 0.65 us a tile, 1.2 an item, 2.2 for the kernel that joins the parts
-    // and their bytes at 1.5 TB/s.
+    // tiles.  Where they do not fill the SMs, the tiles of a row are split.  Two or four splits
+    // that all run at once are a cluster, which joins them through its shared memory; more are
+    // joined from the workspace by a kernel of its own.  The number that ends first by measured
+    // times (32 heads of 128, 16 tiles a row: 64 rows 16.7 us whole, 14.1 in a cluster of 2, 16.3
+    // in 2 with the kernel; 32 rows in 4: 11.5 and 12.6; one row 16.1 whole, 10.2 and 10.5 in 4,
+    // 9.9 in 8; 64 rows of 8 tiles 11.0 whole, 11.3 in a cluster of 2; a cluster of 8 does not run
+    // on all SMs at once: 16 rows 17.5): 0.65 us a tile, 1.2 an item, 2.9 for a cluster's join, 3
+    // for the kernel's and the parts' bytes at 1.5 TB/s.
     const int nh = attention_heads_per_tile(p.group, s->dtype, s->kv_format != IDX_KV_DENSE);
     p.head_tiles = (p.group + nh - 1) / nh;
     const int64_t tiles = (((int64_t)s->num_sel << p.block_shift) + kAttnTile - 1) / kAttnTile;
@@ -288,10 +292,13 @@ int indexer_attention_create(indexer_plan_t plan, const indexer_attention_spec* 
         if ((tiles + per - 1) / per != n)
             continue;
         const double waves = static_cast<double>((items * n + kPlanSms - 1) / kPlanSms);
-        const double cost = waves * (0.65 * per + 1.2) +
-                            (n > 1 ? 2.2 + 1e-6 / 1.5 * (items * n) * nh * s->D * 4.0 : 0.0);
+        const bool cluster = (n == 2 || n == kMaxCluster) && items * n <= kClusterBlocks;
+        const double join =
+            n == 1 ? 0.0 : cluster ? 2.9 : 3.0 + 1e-6 / 1.5 * (items * n) * nh * s->D * 4.0;
+        const double cost = waves * (0.65 * per + 1.2) + join;
         if (cost < best) {
             best = cost;
+            p.cluster = cluster;
             p.splits = static_cast<int32_t>(n);
             p.split_tiles = static_cast<int32_t>(per);
         }
@@ -300,7 +307,7 @@ int indexer_attention_create(indexer_plan_t plan, const indexer_attention_spec* 
     p.by_head_tiles = divisor(p.head_tiles);
     p.by_hkv = divisor(p.Hkv);
     // status word, then the parts of split rows
-    a->part_floats = p.splits > 1 ? (size_t)(items * p.splits) * nh : 0;
+    a->part_floats = p.splits > 1 && !p.cluster ? (size_t)(items * p.splits) * nh : 0;
     a->ws_bytes = 256 + a->part_floats * (s->D + 2) * sizeof(float);
     *out = a;
     if (ws_bytes)

@@ -14,20 +14,29 @@ namespace idx {
 // previous kernel in the stream has finished; it calls pdl_wait_then_release() before
 // any global memory access.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                       cudaStream_t st, Args&&... args)
+cudaError_t launch_pdl_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                               cudaStream_t st, int cluster, Args&&... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                       cudaStream_t st, Args&&... args)
+{
+    return launch_pdl_cluster(kern, grid, block, smem, st, 1, static_cast<Args&&>(args)...);
 }
 
 constexpr int kTileKeys = 128;   // MMA M: keys per tile (one TMEM lane each)
@@ -381,6 +390,7 @@ cudaError_t launch_page_slots(const PageSlotParams& p, cudaStream_t st);
 // Attention over the selected keys.  A work item is (row, key/value head, tile of query
 // heads, split of the row's key tiles of kAttnTile keys).
 constexpr int kAttnTile = 128;
+constexpr int kMaxCluster = 4;      // splits that a cluster joins
 constexpr int kMaxSplits = 64;
 // Division of numbers below 2^31 by a constant of the call: n / d = (n * mul) >> shift with
 // mul = ceil(2^shift / d), shift = 31 + ceil(log2 d).
@@ -421,6 +431,7 @@ struct AttnParams {
     int32_t num_slots;
     int32_t page;                // 0: packed keys
     int32_t splits;              // splits per row
+    int32_t cluster;             // a row's splits are a cluster's blocks, which join them
     Divisor by_page, by_splits, by_head_tiles, by_hkv;
     int32_t split_tiles;         // key tiles per split
     int32_t num_requests;

@@ -299,6 +299,30 @@ def test_a_maximum_that_moves_through_the_list(order, kv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,G,Hkv,D,kv,dt,kernel", [
+    (40, 8, 1, 64, "same", "bf16", True), (33, 5, 2, 64, "fp8", "bf16", False),
+    (64, 32, 1, 128, "fp8", "bf16", False), (48, 40, 1, 128, "same", "fp16", False),
+    (16, 16, 1, 64, "fp8", "fp16", True),
+    (30, 16, 1, 64, "fp8", "fp16", False), (5, 70, 1, 128, "same", "bf16", False),
+    (9, 9, 3, 128, "same", "bf16", False), (1, 64, 1, 128, "fp8", "bf16", True),
+    (2, 3, 2, 64, "same", "fp16", True),
+])
+def test_split_rows(rows, G, Hkv, D, kv, dt, kernel):
+    """Rows too few for the SMs, over 2,048 keys each: joined within a cluster or, in three parts or
+    more than four, by a kernel, which shows in the workspace; lists that leave splits empty."""
+    b = Batch(((rows, 2100),), G * Hkv, Hkv, D, 2048, 1, dt, kv, 16, seed=rows + G)
+    for t, n in enumerate((2048, 0, 1, 128, 129, 700, 1024, 1025, 1920)):
+        if t + 1 < rows:
+            b.sel[t, n:] = -1
+    attn = b.attention()
+    assert (attn.workspace_bytes > 256) == kernel
+    b.check(attn=attn)
+    b.count = torch.tensor([(0, 3, 2048, 1100, 257)[t % 5] for t in range(rows)], dtype=torch.int32)
+    b.check(attn=attn)
+    b.check(attn=attn, with_lse=False)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kv", ["same", "fp8"])
 @pytest.mark.parametrize("block", [1, 8])
 def test_rows_that_select_nothing_and_lists_with_holes(block, kv):
