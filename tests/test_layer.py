@@ -130,3 +130,58 @@ def test_chunks_and_steps_select_and_attend_as_one_call(blocks, e4m3):
         res.append(run(layer, x, table, chunks))
         check(layer, x, *res[-1], 8 if blocks else 1, e4m3)
     assert torch.equal(res[0][1].sort(-1).values, res[1][1].sort(-1).values)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,e4m3", [(1, False), (24, True), (60, False)])
+def test_a_captured_decode_step_replays(rows, e4m3):
+    """The operators in a CUDA graph (rows split over a kernel's, four and two blocks), replayed on
+    new inputs, give what the calls give."""
+    g = torch.Generator().manual_seed(rows)
+    L, Hq, Hkv, nsel, page = 2100, 8, 1, 2048, 4
+    plan = K.indexer_plan(np.arange(rows + 1), np.arange(rows + 1) * L,
+                          np.full(rows, L), 32, 128, 8)
+    table = torch.randperm(rows * -(-L // page), generator=g).int().view(rows, -1).cuda()
+    n = table.numel() * page
+    attn = K.indexer_attention_create(
+        plan, Hq, Hkv, 128, nsel, num_slots=n, page_size=page,
+        kv_format=K.IDX_KV_FP8_E4M3 if e4m3 else K.IDX_KV_DENSE)
+    ws = torch.empty(max(256, attn.workspace_bytes), dtype=torch.uint8, device="cuda")
+    rope = K.indexer_rope_create(128, 64)
+    x = torch.zeros(rows, Hkv, 128, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(rows, Hq, 128, dtype=torch.bfloat16, device="cuda")
+    pos = torch.full((rows,), L - 1, dtype=torch.int32, device="cuda")
+    slots = (table[:, (L - 1) // page] * page + (L - 1) % page).contiguous()
+    lens = torch.full((rows,), L, dtype=torch.int32, device="cuda")
+    codes = torch.randint(0, 120, (n, Hkv, 128), generator=g, dtype=torch.uint8).cuda()
+    scales = torch.full((n, Hkv), 2.0 ** -7, device="cuda")
+    kv = codes if e4m3 else torch.randn(n, Hkv, 128, generator=g).bfloat16().cuda()
+    sel = torch.stack([torch.randperm(L, generator=g)[:nsel] for _ in range(rows)]).int().cuda()
+    turned_q, read, out = torch.empty_like(q), torch.empty_like(x), torch.empty_like(q)
+
+    def step():
+        K.indexer_rope(rope, q, pos, out=turned_q)
+        K.indexer_cache_write(x, codes, scales, rope=rope, positions=pos, slots=slots)
+        K.indexer_cache_read(codes, scales, K.IDX_K_FP8_E4M3, slots, read)
+        K.indexer_sparse_attention(attn, turned_q, kv, kv, sel, lens, out, ws, page_table=table,
+                                   k_scale=scales if e4m3 else None,
+                                   v_scale=scales if e4m3 else None)
+
+    step()                                               # loads the kernels
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        x.copy_(torch.randn(x.shape, generator=g).bfloat16())
+        q.copy_(torch.randn(q.shape, generator=g).bfloat16())
+        step()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (turned_q, read, out)]
+        for t in (turned_q, read, out):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert K.indexer_status(None, ws) == K.IDX_OK
+        assert all(torch.equal(a, b) for a, b in zip(want, (turned_q, read, out)))
+        assert torch.isfinite(out.float()).all() and out.float().abs().max() > 0
