@@ -523,7 +523,8 @@ int indexer_page_slots(indexer_plan_t plan, const int32_t* page_table, int64_t l
  * Formats: q and out are dtype (IDX_BF16, IDX_FP16); k and v are of that type
  * (IDX_KV_DENSE) or caches of format IDX_K_FP8_E4M3 with their scales [num_slots, Hkv]
  * (IDX_KV_FP8_E4M3).  Scores, softmax and sums are fp32; the softmax weights enter the product with
- * v with 8 bits of mantissa or more, relative to the row's largest.
+ * v with 8 bits of mantissa or more (11 where q is fp16), relative to the
+ * row's largest.
  *
  * indexer_attention_spec:
  *   Hq, Hkv      query and key/value heads, Hkv divides Hq, Hq <= IDX_MAX_HEADS

@@ -77,14 +77,17 @@ template <int D, int NH, int MODE>
 struct AttnCfg {
     static constexpr bool kFp8 = MODE >= kModeFp8Bf16;
     static constexpr int kQTerms = MODE == kModeFp8Bf16 ? 2 : MODE == kModeFp8Fp16 ? 3 : 1;
-    static constexpr int kPTerms = kFp8 ? 2 : 1;
+    // Weights over e4m3 caches: two terms hold the 8 bits of a bf16 output, three the 11 of an fp16
+    // one (a fourth, zero, for rows of a swizzle's width; with two, fp16 outputs were off twice
+    // as far as their own rounding).
+    static constexpr int kPTerms = MODE == kModeFp8Bf16 ? 2 : MODE == kModeFp8Fp16 ? 4 : 1;
     static constexpr int kEb = kFp8 ? 1 : 2;            // bytes of an operand element
     static constexpr int kRow = D * kEb;                // bytes of a cached vector
     static constexpr int kAtom = kRow < 128 ? kRow : 128;
     static constexpr int kStage = kAttnTile * kRow;
     static constexpr int kQRows = NH * kQTerms;
     static constexpr int kQBytes = kQRows * kRow;
-    static constexpr int kPRow = NH * kPTerms * kEb;    // 2 NH
+    static constexpr int kPRow = NH * kPTerms * kEb;
     static constexpr int kPBytes = kAttnTile * kPRow;
     // Two softmax warpgroups.  Up to 32 heads they take alternate tiles of an item, each with
     // an output accumulator, running maximum and sum of its own (joined by the epilogue): a
@@ -630,7 +633,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                         for (int i = 0; i < 8; ++i)
                             h[i] = pack2<__half>(x[c + 2 * i], x[c + 2 * i + 1]);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {    // the weights, then what is left of them
+                        for (int k = 0; k < C::kPTerms; ++k) {   // and what is left of them
                             uint32_t r[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
@@ -895,12 +898,15 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     float v[kStep];
                     load(at, v);
                     if (C::kFp8) {
-                        float r[kStep];
-                        load(at + NH, r);
-                        tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < kStep; ++i)
-                            v[i] = fmaf(r[i], 0.0625f, v[i]);
+                        for (int k = 1; k < (C::kPTerms == 4 ? 3 : 2); ++k) {
+                            float r[kStep];
+                            load(at + k * NH, r);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < kStep; ++i)
+                                v[i] = fmaf(r[i], k == 1 ? 0.0625f : 0.00390625f, v[i]);
+                        }
                     }
                     tmem_wait_ld();
 #pragma unroll
@@ -1349,12 +1355,14 @@ template <int D, int MODE>
 cudaError_t attention_heads(const AttnParams& p, int nh, cudaStream_t st)
 {
     cudaError_t e;
-    if (nh == 16)
+    if constexpr (MODE == kModeFp8Fp16)
         e = attention_tc<D, 16, MODE>(p, st);
-    else if (nh == 32 || MODE == kModeFp8Fp16)
+    else if (nh == 16)
+        e = attention_tc<D, 16, MODE>(p, st);
+    else if (nh == 32)
         e = attention_tc<D, 32, MODE>(p, st);
     else
-        e = attention_tc<D, MODE == kModeFp8Fp16 ? 32 : 64, MODE>(p, st);
+        e = attention_tc<D, 64, MODE>(p, st);
     if (e != cudaSuccess || p.splits == 1 || p.cluster)
         return e;
     using T = typename std::conditional<MODE == kModeBf16 || MODE == kModeFp8Bf16, __nv_bfloat16,
@@ -1442,8 +1450,12 @@ int attention_heads_per_tile(int group, int dtype, bool fp8)
     // The smallest tile that holds the group: a wider one computes heads that are none (16 heads in
     // tiles of 16 138 us, of 32 165; 32 heads of 32 171, of 64 235: 2,048 rows, 2,048 keys of
     // 128 bf16), a narrower one gathers the keys again for each (32 heads in two of 16 295 us, 64
-    // in two of 32 331 against 225).  Three terms of 64 fp16 heads do not fit the tensor memory.
-    return group <= 16 ? 16 : group <= 32 || (fp8 && dtype == IDX_FP16) ? 32 : 64;
+    // in two of 32 331 against 225).  Under fp16 queries over
+    // e4m3 caches the terms of more than 16 heads do not fit the tensor memory (32 heads in two of
+    // 16 with three terms 262 us, in one of 32 with two 175).
+    if (fp8 && dtype == IDX_FP16)
+        return 16;
+    return group <= 16 ? 16 : group <= 32 ? 32 : 64;
 }
 
 template <int MODE>
