@@ -430,6 +430,10 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 pbuf + b * C::kPBytes +
                 swizzled<C::kPRow>(i / per * C::kPRow + head0 * C::kEb + i % per * 4));
         };
+        // A reference this far below zero is taken anew from the next tile's scores as they are:
+        // subtracted from a score near zero and added back it would round it away (to 2^-12 at
+        // the limit, to nothing at a reference of -3e38).
+        constexpr float kFar = -4096.0f;
         bool bad = false;
         int n = 0, iq = 0;                               // tiles and items before this item
         int entries = item_entries(p, blockIdx.x, total);
@@ -443,7 +447,9 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
 #pragma unroll
             for (int i = 0; i < HN; ++i)
                 l[i] = 0.0f;
-            bool first = true, leave = false, based = !kZeroStart;   // based: mx holds the maxima
+            // first: no key yet, so no maximum (and weights and sums of nothing but zeros); based: mx
+            // holds the maxima; far: one of them is below kFar
+            bool first = true, leave = false, based = !kZeroStart, far = false;
 #pragma unroll 1
             for (int j = C::kAlternate ? (wg ^ n) & 1 : 0; j < count; j += C::kAlternate ? 2 : 1) {
                 const int b = (n + j) & 1, u = (n + j) >> 1;
@@ -473,6 +479,11 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 tc_fence_before();
                 const int ring = (n + j) % C::kStages * kAttnTile + key;
                 const bool ok = valid[ring] != 0;
+                // a tile without a key leaves everything as it is
+                const bool some =
+                    !first ||
+                    __any_sync(0xFFFFFFFFu,
+                               reinterpret_cast<const uint32_t*>(valid + (ring - key))[lane] != 0u);
                 float ks = p.scale_log2, lv = 0.0f, rv = 1.0f;
                 if (C::kFp8) {
                     const float vs = ok ? vscale[ring] : 1.0f;
@@ -485,7 +496,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     mbar_arrive(s_empty + b);
                 // Exponents, relative to the running maximum where there is one.
                 float over = -INFINITY;
-                if (kZeroStart ? !based : first) {
+                const bool raw = first || !based || far;
+                if (raw) {
 #pragma unroll
                     for (int i = 0; i < HN; i += 2) {
                         if (C::kFp8)
@@ -512,7 +524,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                         x[i] = ok ? x[i] : -INFINITY;
                 }
                 bool waited = false;
-                if ((first && !kZeroStart) || bar_any(over > kSlack || bad, bar_id, 128)) {
+                if ((raw && based && some) || bar_any(over > kSlack || bad, bar_id, 128)) {
                     waited = true;
                     // (maxima of the item before have been read)
                     if (first || !based)
@@ -521,7 +533,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     bad |= !wait(p_empty + b, (u & 1) ^ 1);
                     if (!C::kAlternate && !first)
                         bad |= !wait(p_empty + (b ^ 1), ((n + j - 1) >> 1) & 1);
-                    if (!first && based) {
+                    if (!raw) {
 #pragma unroll
                         for (int i = 0; i < HN; i += 4) {
                             const float4 m = *reinterpret_cast<const float4*>(mx + i);
@@ -549,16 +561,17 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                         leave = true;
                         break;
                     }
+                    float mn = 0.0f;
                     if (key < HN) {
                         const float old = first ? -3.0e38f : based ? mx[key] : 0.0f;
-                        const float mn = fmaxf(
+                        mn = fmaxf(
                             old, fmaxf(fmaxf(*scratch(b, key), *scratch(b, HN + key)),
                                        fmaxf(*scratch(b, 2 * HN + key), *scratch(b, 3 * HN + key))) -
                                      kBelow);
                         *scratch(b, key) = ex2(old - mn);
                         mx[key] = mn;
                     }
-                    bar_all(true, bar_id, 128);
+                    far = bar_any(mn < kFar, bar_id, 128);
 #pragma unroll
                     for (int i = 0; i < HN; i += 4) {
                         const float4 m = *reinterpret_cast<const float4*>(mx + i);
@@ -603,7 +616,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     }
                     based = true;
                 }
-                first = false;
+                first = !some;
 #pragma unroll
                 for (int i = 0; i < HN; ++i)
                     x[i] = ex2(x[i]);
@@ -654,7 +667,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             }
             if (leave)
                 break;
-            if (first || !based) {                       // no tile of this item, or no maxima
+            if (first || !based) {                       // no key of this item, or no maxima
                 bad |= !wait(f_empty, (iq & 1) ^ 1);
                 if (key < HN)
                     mx[key] = first ? -3.0e38f : 0.0f;
