@@ -77,18 +77,25 @@ template <int D, int NH, int MODE>
 struct AttnCfg {
     static constexpr bool kFp8 = MODE >= kModeFp8Bf16;
     static constexpr int kQTerms = MODE == kModeFp8Bf16 ? 2 : MODE == kModeFp8Fp16 ? 3 : 1;
-    // Weights over e4m3 caches: two terms hold the 8 bits of a bf16 output, three the 11 of an fp16
-    // one (a fourth, zero, for rows of a swizzle's width; with two, fp16 outputs were off twice
-    // as far as their own rounding).
-    static constexpr int kPTerms = MODE == kModeFp8Bf16 ? 2 : MODE == kModeFp8Fp16 ? 4 : 1;
-    static constexpr int kEb = kFp8 ? 1 : 2;            // bytes of an operand element
+    // Keys meet the queries as they are cached.  Values of e4m3 caches become bf16 in shared memory
+    // (exactly), so that a weight, times its value's scale, keeps a bf16 number's range and its 8
+    // bits whatever the sizes of the list's other weights and scales.  As e4m3 terms relative to the
+    // largest product, which saved the conversion, weights ended at 2^-18 of it: a value of zeros
+    // (scale 1) or a long list took the others' place.  fp16 outputs have 11 bits: a second bf16
+    // term holds what is left of a weight, into the same accumulator.
+    static constexpr int kPTerms = MODE == kModeFp8Fp16 ? 2 : 1;
+    static constexpr bool kWide = MODE != kModeFp16;    // weights have an fp32 number's range
+    static constexpr int kEb = kFp8 ? 1 : 2;            // bytes of a cached element
     static constexpr int kRow = D * kEb;                // bytes of a cached vector
     static constexpr int kAtom = kRow < 128 ? kRow : 128;
-    static constexpr int kStage = kAttnTile * kRow;
+    static constexpr int kKStage = kAttnTile * kRow;
+    static constexpr int kVStage = kAttnTile * D * 2;
+    static constexpr int kTileBytes = kKStage + kVStage;
     static constexpr int kQRows = NH * kQTerms;
     static constexpr int kQBytes = kQRows * kRow;
-    static constexpr int kPRow = NH * kPTerms * kEb;
-    static constexpr int kPBytes = kAttnTile * kPRow;
+    static constexpr int kPRow = NH * 2;
+    static constexpr int kPTile = kAttnTile * kPRow;    // of a term
+    static constexpr int kPBytes = kPTerms * kPTile;
     // Two softmax warpgroups.  Up to 32 heads they take alternate tiles of an item, each with
     // an output accumulator, running maximum and sum of its own (joined by the epilogue): a
     // tile's chain of waits, exponentials and stores then overlaps the next tile's.  64 heads
@@ -98,7 +105,7 @@ struct AttnCfg {
     static constexpr int kTileWarps = kAlternate ? 4 : 8;   // softmax warps that take a tile
     static constexpr int kAccs = kAlternate ? 2 : 1;    // accumulators of an item
     static constexpr int kSCols = kQRows;               // TMEM columns of a score tile
-    static constexpr int kOCols = NH * kPTerms;         // of an accumulator
+    static constexpr int kOCols = NH;                   // of an accumulator
     static constexpr int kCols = 2 * kSCols + 2 * kAccs * kOCols;
     static constexpr int kTmem = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     // Shared memory after the stages, the weights and the queries.
@@ -108,14 +115,14 @@ struct AttnCfg {
     static constexpr int kKeyInfo = kAttnTile * (kFp8 ? 9 : 1);   // of a tile, 2 kTiles of them
     static constexpr int kFixed = kStats + kMax + kQScale + 2 * kPBytes + 2 * kQBytes + 8 * 21;
     static constexpr int kFit =
-        (kSmemLimit - kFixed) / (2 * kStage + 2 * kKeyInfo + 8 * 4);
+        (kSmemLimit - kFixed) / (kTileBytes + 2 * kKeyInfo + 8 * 4);
     // Tiles in the ring: three; four where the stages are small and so few heads leave the
     // softmax's registers free (16 heads, e4m3 124 us against 149 with three; 8 heads of 64 bf16
     // 132 against 144; but 32 heads, e4m3 236 against 178: two more warps, fewer registers each).
-    static constexpr int kMostTiles = NH == 16 && kStage <= 16384 ? 4 : 3;
+    static constexpr int kMostTiles = NH == 16 && kTileBytes <= 49152 ? 4 : 3;
     static constexpr int kTiles = kFit < kMostTiles ? kFit : kMostTiles;   // tiles in the ring
     static constexpr int kStages = 2 * kTiles;          // and as many warps that fill them
-    static constexpr int kSmem = kFixed + kTiles * (2 * kStage + 2 * kKeyInfo + 8 * 4);
+    static constexpr int kSmem = kFixed + kTiles * (kTileBytes + 2 * kKeyInfo + 8 * 4);
     static constexpr int kGatherWarp = 8 + 4, kMmaWarp = kGatherWarp + kStages;
     static constexpr int kThreads = 32 * (kMmaWarp + 2);
     // Registers: the softmax warpgroups hold a thread's heads twice over (scores and sums), what
@@ -130,7 +137,7 @@ struct AttnCfg {
     static constexpr int kLaunchRegs = 96;
     static_assert(256 * kSoftmaxRegs + 128 * kLaunchRegs + 256 * kFeedRegs <= 640 * kLaunchRegs,
                   "registers");
-    static_assert(NH * D * 4 <= kStages * kStage && NH * 8 <= kStages * kAttnTile,
+    static_assert(NH * D * 4 <= kTiles * kTileBytes && NH * 8 <= kStages * kAttnTile,
                   "a split's part in shared memory");
     static_assert(kCols <= 512 && kTiles >= 2 && kSmem <= kSmemLimit, "tile does not fit");
 };
@@ -315,6 +322,20 @@ __device__ __forceinline__ uint32_t e4m3_split(uint32_t& h)
     return code;
 }
 
+// Eight e4m3 codes (low byte first) as bf16, which holds every one of them.
+__device__ __forceinline__ uint4 bf16_of_e4m3x8(uint32_t lo, uint32_t hi)
+{
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h(__nv_cvt_fp8x2_to_halfraw2(
+            static_cast<__nv_fp8x2_storage_t>((i < 2 ? lo : hi) >> (16 * (i & 1))), __NV_E4M3));
+        const float2 f = __half22float2(h);
+        r[i] = pack2<__nv_bfloat16>(f.x, f.y);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
 template <int D, int NH, int MODE>
 __global__ void __launch_bounds__(AttnCfg<D, NH, MODE>::kThreads, 1)
 attention_tc_kernel(const __grid_constant__ AttnParams p)
@@ -325,7 +346,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
     constexpr int HN = C::kHeads;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint8_t* stages = sm;                                      // k and v of kTiles tiles
-    uint8_t* pbuf = stages + C::kStages * C::kStage;           // [2] weights
+    uint8_t* pbuf = stages + C::kTiles * C::kTileBytes;        // [2] weights
     uint8_t* qbuf = pbuf + 2 * C::kPBytes;                     // [2] queries
     // [2 warpgroups][4 quadrants][HN] sums of an item, [2][HN] running maxima
     float* sums = reinterpret_cast<float*>(qbuf + 2 * C::kQBytes);
@@ -354,7 +375,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(kv_full + i, 1);
+            mbar_init(kv_full + i, C::kFp8 ? 2 : 1);
             mbar_init(kv_empty + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -417,18 +438,16 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         // the accumulated output.  bf16 weights and fp32 sums lose nothing at any scale, so
         // there an item goes by 0 instead of its maxima until a score leaves +-64 (an exchange
         // for each item's first tile cost a tenth of its time).  fp16 weights have to stay
-        // below 2^16.  e4m3 ones have to stay below 448, and their terms reach down to 2^-13: they
-        // go by 2^-4 of the maximum, so that it has weight 16.
-        constexpr bool kZeroStart = MODE == kModeBf16;
-        constexpr float kSlack = MODE == kModeBf16 ? 64.0f : 8.0f;
-        constexpr float kBelow = C::kFp8 ? 4.0f : 0.0f;
+        // below 2^16.
+        constexpr bool kZeroStart = C::kWide;
+        constexpr float kSlack = C::kWide ? 64.0f : 8.0f;
         // the thread's heads in a row of the weights, and the row's part of them as scratch
-        constexpr int kOwn = HN * C::kEb;                // bytes of a term
+        constexpr int kOwn = HN * 2;                     // bytes of a term
         auto scratch = [&](int b, int i) {               // float i of 4 HN
             constexpr int per = kOwn / 4;
             return reinterpret_cast<float*>(
                 pbuf + b * C::kPBytes +
-                swizzled<C::kPRow>(i / per * C::kPRow + head0 * C::kEb + i % per * 4));
+                swizzled<C::kPRow>(i / per * C::kPRow + head0 * 2 + i % per * 4));
         };
         // A reference this far below zero is taken anew from the next tile's scores as they are:
         // subtracted from a score near zero and added back it would round it away (to 2^-12 at
@@ -484,12 +503,10 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     !first ||
                     __any_sync(0xFFFFFFFFu,
                                reinterpret_cast<const uint32_t*>(valid + (ring - key))[lane] != 0u);
-                float ks = p.scale_log2, lv = 0.0f, rv = 1.0f;
+                float ks = p.scale_log2, vs = 1.0f;
                 if (C::kFp8) {
-                    const float vs = ok ? vscale[ring] : 1.0f;
                     ks = ok ? kscale[ring] * qscale[iq % kScaleItems] : 0.0f;
-                    lv = __log2f(vs);
-                    rv = __fdividef(1.0f, vs);
+                    vs = vscale[ring];
                 }
                 const bool all = __all_sync(0xFFFFFFFFu, ok);
                 if (lane == 0)
@@ -500,10 +517,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 if (raw) {
 #pragma unroll
                     for (int i = 0; i < HN; i += 2) {
-                        if (C::kFp8)
-                            fma2(x[i], x[i + 1], ks, ks, lv, lv);
-                        else
-                            mul2(x[i], x[i + 1], ks, ks);
+                        mul2(x[i], x[i + 1], ks, ks);
                         if (kZeroStart)
                             over = fmaxf(over, fmaxf(fabsf(x[i]), fabsf(x[i + 1])));
                     }
@@ -512,8 +526,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
 #pragma unroll
                     for (int i = 0; i < HN; i += 4) {
                         const float4 m = *reinterpret_cast<const float4*>(mx + i);
-                        fma2(x[i], x[i + 1], ks, ks, lv - m.x, lv - m.y);
-                        fma2(x[i + 2], x[i + 3], ks, ks, lv - m.z, lv - m.w);
+                        fma2(x[i], x[i + 1], ks, ks, -m.x, -m.y);
+                        fma2(x[i + 2], x[i + 3], ks, ks, -m.z, -m.w);
                         over = fmaxf(over, fmaxf(fmaxf(x[i], x[i + 1]), fmaxf(x[i + 2], x[i + 3])));
                     }
                     over = ok ? over : -INFINITY;
@@ -566,8 +580,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                         const float old = first ? -3.0e38f : based ? mx[key] : 0.0f;
                         mn = fmaxf(
                             old, fmaxf(fmaxf(*scratch(b, key), *scratch(b, HN + key)),
-                                       fmaxf(*scratch(b, 2 * HN + key), *scratch(b, 3 * HN + key))) -
-                                     kBelow);
+                                       fmaxf(*scratch(b, 2 * HN + key), *scratch(b, 3 * HN + key))));
                         *scratch(b, key) = ex2(old - mn);
                         mx[key] = mn;
                     }
@@ -590,25 +603,22 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                         for (int c = 0; c < HN; c += 8) {
                             const float4 f0 = *reinterpret_cast<const float4*>(scratch(b, c));
                             const float4 f1 = *reinterpret_cast<const float4*>(scratch(b, c + 4));
-#pragma unroll 1
-                            for (int k = 0; k < C::kPTerms; ++k) {
-                                const uint32_t at =
-                                    tmem_o + lanes +
-                                    ((iq & 1) * C::kAccs + (C::kAlternate ? b : 0)) * C::kOCols +
-                                    k * NH + head0 + c;
-                                float v[8];
-                                tmem_ld_32x32b_x8(at, v);
-                                tmem_wait_ld();
-                                v[0] *= f0.x;
-                                v[1] *= f0.y;
-                                v[2] *= f0.z;
-                                v[3] *= f0.w;
-                                v[4] *= f1.x;
-                                v[5] *= f1.y;
-                                v[6] *= f1.z;
-                                v[7] *= f1.w;
-                                tmem_st_32x32b_x8(at, v);
-                            }
+                            const uint32_t at =
+                                tmem_o + lanes +
+                                ((iq & 1) * C::kAccs + (C::kAlternate ? b : 0)) * C::kOCols + head0 +
+                                c;
+                            float v[8];
+                            tmem_ld_32x32b_x8(at, v);
+                            tmem_wait_ld();
+                            v[0] *= f0.x;
+                            v[1] *= f0.y;
+                            v[2] *= f0.z;
+                            v[3] *= f0.w;
+                            v[4] *= f1.x;
+                            v[5] *= f1.y;
+                            v[6] *= f1.z;
+                            v[7] *= f1.w;
+                            tmem_st_32x32b_x8(at, v);
                         }
                         tmem_wait_st();
                         tc_fence_before();
@@ -621,43 +631,34 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 for (int i = 0; i < HN; ++i)
                     x[i] = ex2(x[i]);
 #pragma unroll
-                for (int i = 0; i < HN; i += 2) {
-                    if (C::kFp8)
-                        add2_scaled(l[i], l[i + 1], x[i], x[i + 1], rv);
-                    else
-                        add2(l[i], l[i + 1], x[i], x[i + 1]);
+                for (int i = 0; i < HN; i += 2)
+                    add2(l[i], l[i + 1], x[i], x[i + 1]);
+                if (C::kFp8) {
+#pragma unroll
+                    for (int i = 0; i < HN; i += 2)
+                        mul2(x[i], x[i + 1], vs, vs);
                 }
                 if (!waited)
                     bad |= !wait(p_empty + b, (u & 1) ^ 1);
+                using W = typename std::conditional<C::kWide, __nv_bfloat16, __half>::type;
                 uint8_t* prow = pbuf + b * C::kPBytes;
 #pragma unroll
-                for (int c = 0; c < HN; c += 16) {
-                    if (!C::kFp8) {
+                for (int k = 0; k < C::kPTerms; ++k) {
 #pragma unroll
-                        for (int k = c; k < c + 16; k += 8)
-                            *reinterpret_cast<uint4*>(
-                                prow + swizzled<C::kPRow>(key * C::kPRow + 2 * (head0 + k))) =
-                                make_uint4(pack2<T>(x[k], x[k + 1]), pack2<T>(x[k + 2], x[k + 3]),
-                                           pack2<T>(x[k + 4], x[k + 5]),
-                                           pack2<T>(x[k + 6], x[k + 7]));
-                    } else {
-                        uint32_t h[8];
+                    for (int c = 0; c < HN; c += 8) {
+                        uint32_t h[4];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            h[i] = pack2<__half>(x[c + 2 * i], x[c + 2 * i + 1]);
-#pragma unroll
-                        for (int k = 0; k < C::kPTerms; ++k) {   // and what is left of them
-                            uint32_t r[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t lo = e4m3_split(h[2 * i]);
-                                r[i] = lo | e4m3_split(h[2 * i + 1]) << 16;
-                            }
-                            *reinterpret_cast<uint4*>(
-                                prow +
-                                swizzled<C::kPRow>(key * C::kPRow + k * NH + head0 + c)) =
-                                make_uint4(r[0], r[1], r[2], r[3]);
+                        for (int i = 0; i < 4; ++i) {
+                            float &lo = x[c + 2 * i], &hi = x[c + 2 * i + 1];
+                            h[i] = pack2<W>(lo, hi);
+                            if (k + 1 < C::kPTerms)          // what is left of them
+                                add2(lo, hi, -__uint_as_float(h[i] << 16),
+                                     -__uint_as_float(h[i] & 0xFFFF0000u));
                         }
+                        *reinterpret_cast<uint4*>(
+                            prow + k * C::kPTile +
+                            swizzled<C::kPRow>(key * C::kPRow + 2 * (head0 + c))) =
+                            make_uint4(h[0], h[1], h[2], h[3]);
                     }
                 }
                 fence_proxy_async_smem();
@@ -910,17 +911,6 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     const float fac = a > 0 ? fb : NH > 32 && h0 >= 32 ? fa[NH / 64] : fa[0];
                     float v[kStep];
                     load(at, v);
-                    if (C::kFp8) {
-#pragma unroll
-                        for (int k = 1; k < (C::kPTerms == 4 ? 3 : 2); ++k) {
-                            float r[kStep];
-                            load(at + k * NH, r);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < kStep; ++i)
-                                v[i] = fmaf(r[i], k == 1 ? 0.0625f : 0.00390625f, v[i]);
-                        }
-                    }
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < kStep; ++i) {
@@ -959,29 +949,46 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kFeedRegs));
         if (warp < C::kMmaWarp) {
             // ---------------------------------------------------------------- gather
-            // Warp i fills stage i of the ring: it waits for the stage, copies the 128 vectors
-            // (zeros for keys that are none), waits for its own copies and signals.  The other
-            // stages' warps keep the memory system busy meanwhile.  A warp sees every phase of
-            // the one barrier it waits on.  It reads the list entries of its next tile while its
-            // copies are under way and the pages after them.
-            const int pw = warp - C::kGatherWarp;
-            const bool is_v = pw & 1;
+            // Two warps fill a place of the ring: one its keys and one its values, or (e4m3 caches,
+            // whose values are converted by the warp that copied them) each both of 64 keys.  A
+            // warp looks up its keys' slots, waits for the place, copies the vectors (zeros for
+            // keys that are none), waits for its own copies and signals.  The other places'
+            // warps keep the memory system busy meanwhile.  A warp sees every phase of the
+            // barriers it waits on.  It reads the list entries of its next tile while its copies are
+            // under way and the pages after them.  (2,048 rows x 2,048 e4m3 keys: 16, 32 and 64 heads
+            // 188, 209 and 278 us; a warp for all of a tile's values 233, 265 and 313.  16-bit keys
+            // both ways round: 160, 183 and 265 against 151, 184 and 234.)
+            constexpr bool kBoth = C::kFp8;
+            const int pw = warp - C::kGatherWarp, place = pw / 2;
+            const bool is_v = !kBoth && (pw & 1);
+            const int first_key = kBoth ? (pw & 1) * 64 : 0;
+            constexpr int kOwnKeys = kBoth ? 2 : 4;          // of a lane
             constexpr int kPerRow = C::kRow / 16;            // copies of 16 bytes a vector takes
-            constexpr int kSpan = 4 * kPerRow;               // keys of a group of kPerRow lanes
-            const int chunk = lane % kPerRow, row0 = lane / kPerRow * kSpan;
-            const uint32_t stage = smem_u32(stages + pw * C::kStage) + row0 * C::kAtom +
-                                   (chunk * 16 / C::kAtom) * (kAttnTile * C::kAtom) +
-                                   (chunk * 16) % C::kAtom;
-            const uint8_t* kv = (is_v ? p.v : p.k) + chunk * 16;
-            const int64_t kv_head = is_v ? p.v_head : p.k_head;
-            const uint32_t kv_slot = static_cast<uint32_t>(is_v ? p.v_slot : p.k_slot);
+            constexpr int kSpan = kOwnKeys * kPerRow;        // keys of a group of kPerRow lanes
+            const int chunk = lane % kPerRow, row0 = first_key + lane / kPerRow * kSpan;
+            // a vector's 16 bytes in its row (of kAtom bytes, further ones in a next tile of rows)
+            constexpr int kNext = kAttnTile * C::kAtom;
+            const uint32_t place_at = smem_u32(stages + place * C::kTileBytes);
+            const uint32_t copy_at =
+                place_at + (is_v ? C::kKStage : 0) + row0 * C::kAtom + (chunk * 16 / C::kAtom) * kNext + (chunk * 16) % C::kAtom;
+            // Values of e4m3 caches are copied to where the second half of their own bf16 row goes
+            // (rows of 64: one half or the other), read back by the lane that copied them and
+            // written as bf16 over the row.  Four lanes of every eight are a row of the pair ahead
+            // or behind, which spreads the eight over the banks: they read and write 16 bytes of
+            // even chunks in a row of an even and one of an odd swizzle.
+            const int flip = C::kFp8 ? (lane >> 2) & 1 : 0;
+            const uint32_t v_row =
+                (place_at + C::kKStage + row0 * 128) ^ swizzle_of<128>(flip * 128);
+            const uint32_t v_codes = (v_row + (D == 128 ? kAttnTile * 128 : 0)) ^
+                                     ((D == 128 ? 0 : flip * 64) + chunk * 16);
+            const uint32_t v_values = (v_row + chunk / 4 * (kAttnTile * 128)) ^ chunk % 4 * 32;
             AttnItem w;
             w.tile = w.tiles = w.n_sel = w.t = w.g = 0;
-            int item = blockIdx.x - gridDim.x, skip = pw / 2;   // tiles to the warp's next one
+            int item = blockIdx.x - gridDim.x, skip = place;    // tiles to the warp's next one
             int entries = item_entries(p, blockIdx.x, total);
             int r = 0, base = 0, most = 0, len = 0, g = 0;
-            // the lane's keys of a tile: row0 + kPerRow i + chunk, i < 4
-            int32_t entry[4], key[4], page[4];
+            // the lane's keys of a tile: row0 + kPerRow i + chunk
+            int32_t entry[kOwnKeys], key[kOwnKeys], page[kOwnKeys];
             auto advance = [&] {                             // to the warp's next tile; its entries
                 w.tile += skip;
                 bool fresh = false;
@@ -1004,7 +1011,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 }
                 const int32_t* sel = p.sel + w.t * p.ld_sel;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < kOwnKeys; ++i) {
                     const int e =
                         (w.tile * kAttnTile + row0 + kPerRow * i + chunk) >> p.block_shift;
                     entry[i] = e < w.n_sel ? sel[e] : -1;
@@ -1014,7 +1021,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             auto locate = [&] {                              // keys and pages of the entries
                 const int32_t* table = p.table + r * p.ld_table;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < kOwnKeys; ++i) {
                     const int pos = w.tile * kAttnTile + row0 + kPerRow * i + chunk;
                     const int64_t k = ((int64_t)entry[i] << p.block_shift) +
                                       (pos & ((1 << p.block_shift) - 1));
@@ -1034,94 +1041,126 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             // (one copy of each step, for the instruction cache: the first round only looks up)
             for (int u = -1;; ++u) {
                 if (u >= 0) {
-                    int32_t slot[4];
+                    int32_t slot[kOwnKeys];
                     bool whole = true;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < kOwnKeys; ++i) {
                         const int64_t at = (int64_t)page[i] * p.page + key[i];
                         slot[i] = page[i] >= 0 && at < p.num_slots ? static_cast<int32_t>(at) : -1;
                         whole = whole && slot[i] >= 0;
                     }
                     whole = __all_sync(0xFFFFFFFFu, whole);
-                    if (!__all_sync(0xFFFFFFFFu, wait(kv_empty + pw, (u & 1) ^ 1)))
+                    if (!__all_sync(0xFFFFFFFFu, wait(kv_empty + 2 * place + is_v, (u & 1) ^ 1)))
                         break;
                     if (!is_v) {
-                        // What the softmax has to know of the keys.  No barrier guards the place,
-                        // last read for the tile n - 2 kTiles: the scores of tile n - kTiles have
-                        // freed the stage, and were issued after those of tile n - kTiles - 2 were
-                        // read.
-                        const int ring = (u * C::kTiles + pw / 2) % C::kStages * kAttnTile;
+                        // What the softmax has to know of the keys.  No barrier guards the place, last
+                        // read for the tile n - 2 kTiles: the scores of tile n - kTiles have freed the
+                        // stage, and were issued after those of tile n - kTiles - 2 were read.
+                        const int ring = (u * C::kTiles + place) % C::kStages * kAttnTile;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < kOwnKeys; ++i) {
                             const int k = ring + row0 + kPerRow * i + chunk;
                             valid[k] = slot[i] >= 0;
                             if (C::kFp8) {
                                 const int64_t at = (int64_t)max(slot[i], 0) * p.Hkv + g;
-                                kscale[k] = slot[i] >= 0 ? p.k_scale[at] : 0.0f;
-                                vscale[k] = slot[i] >= 0 ? p.v_scale[at] : 0.0f;
+                                cp_async4(smem_u32(kscale + k), p.k_scale + at, slot[i] >= 0);
+                                cp_async4(smem_u32(vscale + k), p.v_scale + at, slot[i] >= 0);
                             }
                         }
                     }
-                    const uint8_t* src = kv + g * kv_head;
                     // A span's keys are spread over its lanes: slot i of lane k is key
                     // kPerRow i + k.  (eight rows at a time, for the instruction cache)
-                    const int from = lane & ~(kPerRow - 1);
-                    auto pick = [&](int i) {
-                        const int32_t lo = i & 1 ? slot[1] : slot[0];
-                        const int32_t hi = i & 1 ? slot[3] : slot[2];
-                        return i & 2 ? hi : lo;
-                    };
-                    if (whole) {
+                    auto copy = [&](const uint8_t* src, uint32_t stride, uint32_t to, int turn,
+                                    auto width) {
+                        constexpr int kW = decltype(width)::value;
+                        const int from = (lane & ~(kPerRow - 1)) ^ turn;
+                        auto pick = [&](int i) {
+                            const int32_t lo = i & 1 ? slot[1] : slot[0];
+                            const int32_t hi = i & 1 ? slot[kOwnKeys - 1] : slot[kOwnKeys - 2];
+                            return kOwnKeys > 2 && (i & 2) ? hi : lo;
+                        };
+                        if (whole) {
 #pragma unroll 1
-                        for (int row = 0; row < kSpan; row += 8) {
-                            const int32_t a = pick(row / kPerRow);
-                            const int32_t b = kPerRow < 8 ? pick(row / kPerRow + 1) : a;
-                            const uint32_t dst = stage + row * C::kAtom;
-                            const int lane0 = from + row % kPerRow;
+                            for (int row = 0; row < kSpan; row += 8) {
+                                const int32_t a = pick(row / kPerRow);
+                                const int32_t b = kPerRow < 8 ? pick(row / kPerRow + 1) : a;
+                                const uint32_t dst = to + row * kW;
+                                const int lane0 = from ^ row % kPerRow;
 #pragma unroll
-                            for (int x = 0; x < 8; ++x) {
-                                const uint32_t s = __shfl_sync(0xFFFFFFFFu, x < kPerRow ? a : b,
-                                                               lane0 + x % kPerRow);
-                                cp_async16(dst ^ swizzle_of<C::kAtom>(x * C::kAtom),
-                                           src + (uint64_t)s * kv_slot);
+                                for (int x = 0; x < 8; ++x) {
+                                    const uint32_t s = __shfl_sync(
+                                        0xFFFFFFFFu, x < kPerRow ? a : b, lane0 ^ x % kPerRow);
+                                    cp_async16(dst ^ swizzle_of<kW>(x * kW),
+                                               src + (uint64_t)s * stride);
+                                }
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int row = 0; row < kSpan; ++row) {
+                                const int32_t s = __shfl_sync(0xFFFFFFFFu, pick(row / kPerRow),
+                                                              from ^ row % kPerRow);
+                                cp_async16((to + row / 8 * 8 * kW) ^ swizzle_of<kW>(row % 8 * kW),
+                                           src + (uint64_t)(uint32_t)max(s, 0) * stride, s >= 0);
                             }
                         }
-                    } else {
-#pragma unroll 1
-                        for (int row = 0; row < kSpan; ++row) {
-                            const int32_t s =
-                                __shfl_sync(0xFFFFFFFFu, pick(row / kPerRow), from + row % kPerRow);
-                            cp_async16((stage + row / 8 * 8 * C::kAtom) ^
-                                           swizzle_of<C::kAtom>(row % 8 * C::kAtom),
-                                       src + (uint64_t)(uint32_t)max(s, 0) * kv_slot, s >= 0);
-                        }
+                        cp_async_commit();
+                    };
+                    copy((is_v ? p.v : p.k) + chunk * 16 + g * (is_v ? p.v_head : p.k_head),
+                         static_cast<uint32_t>(is_v ? p.v_slot : p.k_slot), copy_at, 0,
+                         std::integral_constant<int, C::kAtom>());
+                    if (kBoth) {
+                        if (!__all_sync(0xFFFFFFFFu, wait(kv_empty + 2 * place + 1, (u & 1) ^ 1)))
+                            break;
+                        copy(p.v + chunk * 16 + g * p.v_head, static_cast<uint32_t>(p.v_slot),
+                             v_codes, flip, std::integral_constant<int, 128>());
                     }
-                    cp_async_commit();
                 }
                 const bool more = advance();
                 if (u >= 0) {
+                    if (kBoth) {
+                        cp_async_wait<1>();
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(kv_full + 2 * place);
+                    }
                     cp_async_wait<0>();
+                    if (C::kFp8) {
+#pragma unroll 1
+                        for (int row = 0; row < kSpan; row += 4) {
+                            const uint32_t at = row / 8 * 1024;
+                            const uint32_t four = swizzle_of<128>((row & 4) * 128);
+                            uint4 codes[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                codes[x] =
+                                    lds128((v_codes + at) ^ four ^ swizzle_of<128>(x * 128));
+                            __syncwarp();                    // (the rows have been read)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const uint32_t to =
+                                    (v_values + at) ^ four ^ swizzle_of<128>(x * 128);
+                                sts128(to, bf16_of_e4m3x8(codes[x].x, codes[x].y));
+                                sts128(to ^ 16, bf16_of_e4m3x8(codes[x].z, codes[x].w));
+                            }
+                        }
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(kv_full + pw);
+                        mbar_arrive(kv_full + 2 * place + (kBoth || is_v));
                 }
                 if (!more)
                     break;
                 locate();
             }
+            cp_async_wait<0>();                              // (of a wait that gave up)
         } else {
             // --------------------------------------------------------------------- MMA
             // One elected lane of a warp for the scores, and of another for the products: each
             // waits and issues.  (One thread for both took 1,400 cycles a tile for its own instructions.)
-            constexpr int kK = 32 / C::kEb;                 // contraction elements of one MMA
+            constexpr int kK = 32 / C::kEb;                 // contraction elements of a score MMA
             const bool scores = warp == C::kMmaWarp;
-            auto mma = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-                if (C::kFp8)
-                    mma_f8f6f4(d, a, b, id, acc);
-                else
-                    mma_f16(d, a, b, id, acc);
-            };
             if (elect_one()) {
                 int n = 0, iq = 0, st = 0;                  // tile n's place in the ring
                 uint32_t phase = 0;                         // and the uses of that place
@@ -1146,12 +1185,13 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                             if (!ok)
                                 break;
                             tc_fence_after();
-                            const uint64_t k_desc = smem_desc(smem_u32(stages + 2 * st * C::kStage),
+                            const uint64_t k_desc = smem_desc(smem_u32(stages + st * C::kTileBytes),
                                                               C::kAtom, 16, 8 * C::kAtom);
 #pragma unroll
                             for (int k = 0; k < D / kK; ++k) {
                                 const int atom = k * 32 / C::kAtom, in = (k * 32) % C::kAtom;
-                                mma(tmem_s + (n & 1) * C::kSCols,
+                                (C::kFp8 ? mma_f8f6f4 : mma_f16)(
+                                    tmem_s + (n & 1) * C::kSCols,
                                     k_desc + (atom * (kAttnTile * C::kAtom) + in) / 16,
                                     q_desc + (atom * (C::kQRows * C::kAtom) + in) / 16, idesc, k > 0);
                             }
@@ -1166,10 +1206,10 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                             mma_commit(q_empty + (iq & 1));
                     } else {                                // O += P V
                         constexpr uint32_t idesc =
-                            idesc_dense(128, C::kOCols, MODE == kModeBf16 ? 1 : 0, true, true);
+                            idesc_dense(128, C::kOCols, C::kWide ? 1 : 0, true, true);
                         // v rows are keys: both operands are read along their rows.  D = 64 takes
                         // the same 64 elements for both halves of the 128 output rows.
-                        constexpr uint32_t lbo = D == 64 ? 0 : kAttnTile * C::kAtom;
+                        constexpr uint32_t lbo = D == 64 ? 0 : kAttnTile * 128;
                         ok = wait(o_empty + (iq & 1), ((iq >> 1) & 1) ^ 1);
                         for (int j = 0; j < count && ok; ++j, ++n) {
                             const int b = n & 1;
@@ -1179,8 +1219,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                                 break;
                             tc_fence_after();
                             const uint64_t v_desc = smem_desc(
-                                smem_u32(stages + (2 * st + 1) * C::kStage), C::kAtom, lbo,
-                                8 * C::kAtom);
+                                smem_u32(stages + st * C::kTileBytes + C::kKStage), 128, lbo, 1024);
                             const uint64_t p_desc =
                                 smem_desc(smem_u32(pbuf + b * C::kPBytes), C::kPRow, 0,
                                           8 * C::kPRow);
@@ -1189,9 +1228,9 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                             // an empty accumulator
                             const bool fresh = C::kAlternate ? j < 2 : j == 0;
 #pragma unroll
-                            for (int k = 0; k < kAttnTile / kK; ++k)
-                                mma(d, v_desc + k * (kK * C::kAtom / 16),
-                                    p_desc + k * (kK * C::kPRow / 16), idesc, !fresh || k > 0);
+                            for (int k = 0; k < C::kPTerms * kAttnTile / 16; ++k)
+                                mma_f16(d, v_desc + k % (kAttnTile / 16) * 128,
+                                        p_desc + k * C::kPRow, idesc, !fresh || k > 0);
                             mma_commit(p_empty + b);
                             mma_commit(kv_empty + 2 * st + 1);
                             if (++st == C::kTiles) {
@@ -1368,13 +1407,11 @@ template <int D, int MODE>
 cudaError_t attention_heads(const AttnParams& p, int nh, cudaStream_t st)
 {
     cudaError_t e;
-    if constexpr (MODE == kModeFp8Fp16)
+    if (nh == 16)
         e = attention_tc<D, 16, MODE>(p, st);
-    else if (nh == 16)
-        e = attention_tc<D, 16, MODE>(p, st);
-    else if (nh == 32)
+    else if (MODE == kModeFp8Fp16 || nh == 32)
         e = attention_tc<D, 32, MODE>(p, st);
-    else
+    else if constexpr (MODE != kModeFp8Fp16)
         e = attention_tc<D, 64, MODE>(p, st);
     if (e != cudaSuccess || p.splits == 1 || p.cluster)
         return e;
@@ -1463,11 +1500,10 @@ int attention_heads_per_tile(int group, int dtype, bool fp8)
     // The smallest tile that holds the group: a wider one computes heads that are none (16 heads in
     // tiles of 16 138 us, of 32 165; 32 heads of 32 171, of 64 235: 2,048 rows, 2,048 keys of
     // 128 bf16), a narrower one gathers the keys again for each (32 heads in two of 16 295 us, 64
-    // in two of 32 331 against 225).  Under fp16 queries over
-    // e4m3 caches the terms of more than 16 heads do not fit the tensor memory (32 heads in two of
-    // 16 with three terms 262 us, in one of 32 with two 175).
+    // in two of 32 331 against 225).  fp16 queries over e4m3 caches: two of 32, the terms of 64
+    // leave room for two tiles and too few registers (541 us against 459).
     if (fp8 && dtype == IDX_FP16)
-        return 16;
+        return group <= 16 ? 16 : 32;
     return group <= 16 ? 16 : group <= 32 ? 32 : 64;
 }
 

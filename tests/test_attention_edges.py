@@ -20,7 +20,7 @@ from tests.test_attention import Batch, reference, selected
 
 pytestmark = pytest.mark.gpu
 
-MODES = [("bf16", "same"), ("fp16", "same")]
+MODES = [("bf16", "same"), ("fp16", "same"), ("bf16", "fp8"), ("fp16", "fp8")]
 TILE = 128
 
 
@@ -97,7 +97,7 @@ def test_unmapped_pages_before_mapped_ones(dt, kv):
 
 @pytest.mark.parametrize("rows", [11, 170])
 @pytest.mark.parametrize("group", [8, 32, 64])
-@pytest.mark.parametrize("dt,kv", MODES + [("bf16", "fp8"), ("fp16", "fp8")])
+@pytest.mark.parametrize("dt,kv", MODES)
 def test_scores_far_below_zero_next_to_tiles_without_a_key(dt, kv, group, rows):
     """A tile without a key has no maximum: not 0 either, beside which exp(-150) is nothing."""
     b = Batch(((rows, 1024),), group, 1, 64, 1024, 1, dt, kv, 0, seed=group, lens=[1024] * rows)
@@ -137,3 +137,68 @@ def test_keys_of_no_weight_before_others(dt, rows):
     for a, c in zip(want, some):
         a[:, ::2] = c[:, ::2]
     hold(b, got, lse, want)
+
+# ---------------------------------------------------- weights over e4m3 caches
+
+
+@pytest.mark.parametrize("rows", [3, 160])
+@pytest.mark.parametrize("nats", [5.0, 8.0, 12.0])
+@pytest.mark.parametrize("size", [1.0, 1e-4])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_a_value_of_zeros_far_above_the_rest(dt, size, nats, rows):
+    """The key of the largest score has a value of zeros, whose scale is 1 as the cache's writer
+    leaves it: the output is what the rest weighs."""
+    b = Batch(((rows, 600),), 8, 1, 128, 512, 1, dt, "fp8", 0, seed=24, lens=[600] * rows)
+    b.q[:, :, 0] = 8.0
+    b.k[:, :, 0] = 0
+    b.vs *= size
+    for t in range(rows):
+        b.sel[t, 77] = 599                                 # (rows have it once)
+        b.sel[t][torch.arange(512) != 77] = torch.randperm(599, generator=b.g)[:511].to(torch.int32)
+    top = torch.zeros(128)
+    top[0] = 448.0
+    b.k[599, 0] = top.to(torch.float8_e4m3fn).view(torch.uint8)
+    b.ks[599] = nats * 128 ** 0.5 / 8 / 448
+    b.v[599], b.vs[599] = 0, 1.0
+    check(b)
+
+
+@pytest.mark.parametrize("n", [2048, 16384, 65536])
+@pytest.mark.parametrize("dt,kv,nats", [("bf16", "fp8", 13.0), ("fp16", "fp8", 13.0), ("bf16", "same", 13.0)])
+def test_one_key_far_above_a_long_list(dt, kv, nats, n):
+    """Every weight but one is e^-nats of the largest; together they weigh as much as it does or more."""
+    one_far_above(dt, kv, nats, n)
+
+
+def one_far_above(dt, kv, nats, n):
+    b = Batch(((2, n),), 16, 1, 64, n, 1, dt, kv, 0, seed=25, lens=[n, n])
+    b.sel = torch.stack([torch.arange(n), torch.arange(n - 1, -1, -1)]).to(torch.int32)
+    g = torch.Generator().manual_seed(26)
+    b.q = torch.zeros((2, 16, 64))
+    b.q[:, :, 0] = 8.0
+    b.q = b.q.to(b.dt)
+    k = torch.zeros((n, 1, 64))
+    k[n // 3, 0, 0] = 448.0 if kv == "fp8" else nats
+    v = 100 + 300 * torch.rand((n, 1, 64), generator=g)
+    v[n // 3] = 1.0
+    if kv == "fp8":
+        b.k, b.v = (x.to(torch.float8_e4m3fn).view(torch.uint8) for x in (k, v))
+        b.ks, b.vs = torch.full((n, 1), nats / 448), torch.full((n, 1), 0.01)
+    else:
+        b.k, b.v = k.to(b.dt), v.to(b.dt)
+    check(b)
+
+
+@pytest.mark.parametrize("D,group,Hkv,nsel,block", [(128, 32, 1, 300, 1), (64, 5, 2, 20, 8), (64, 64, 1, 7, 64),
+                                                    (128, 20, 2, 129, 1), (128, 16, 1, 1, 1)])
+def test_fp16_queries_over_e4m3_keep_their_eleven_bits(D, group, Hkv, nsel, block):
+    check(Batch(((9, 700),), group * Hkv, Hkv, D, nsel, block, "fp16", "fp8", 16, seed=27, spread=2.0))
+
+
+def test_value_scales_far_apart():
+    """Scales from 2^-100 to 2^60 in one list: each value counts with its own."""
+    b = Batch(((5, 512),), 16, 1, 64, 512, 1, "bf16", "fp8", 0, seed=28, lens=[512] * 5)
+    b.vs = torch.exp2(torch.randint(-100, 60, (512, 1), generator=b.g).float())
+    check(b)
+    b.vs = torch.exp2(torch.randint(-100, -60, (512, 1), generator=b.g).float())
+    check(b)
