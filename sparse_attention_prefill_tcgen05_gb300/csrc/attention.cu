@@ -784,10 +784,15 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
                 if (from == 0)
                     qscale[nq % kScaleItems] = p.scale_log2 / mul;
+                // (heads that are none are zeros: the tile's scores are those of all its heads)
 #pragma unroll 1
-                for (int h = from / kGroup; h < heads; h += 128 / kGroup) {
-                    const uint4* at = reinterpret_cast<const uint4*>(q + h * p.q_head) + 2 * c;
-                    const uint4 in[2] = {at[0], at[1]};
+                for (int h = from / kGroup; h < NH; h += 128 / kGroup) {
+                    uint4 in[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+                    if (h < heads) {
+                        const uint4* at = reinterpret_cast<const uint4*>(q + h * p.q_head) + 2 * c;
+                        in[0] = at[0];
+                        in[1] = at[1];
+                    }
                     const T* e = reinterpret_cast<const T*>(in);
                     uint32_t v[8];
 #pragma unroll

@@ -202,3 +202,18 @@ def test_value_scales_far_apart():
     check(b)
     b.vs = torch.exp2(torch.randint(-100, -60, (512, 1), generator=b.g).float())
     check(b)
+
+
+@pytest.mark.parametrize("rows", [2, 200])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("group", [1, 5, 8, 20, 40])
+def test_places_of_a_tile_without_a_head_hold_nothing_of_the_last_call(group, dt, rows):
+    """The same bits after a call that has filled the shared memory with other queries, keys and
+    weights, in wider groups."""
+    b = Batch(((rows, 600),), group, 1, 128, 500, 1, dt, "fp8", 16, seed=30 + group)
+    first, lse = check(b)
+    for wide in (group, 64):
+        other = Batch(((200, 600),), wide, 1, 128, 500, 1, dt, "fp8", 16, seed=31, spread=400.0)
+        other.run()
+        again, lse2 = b.run()
+        assert torch.equal(first, again) and torch.equal(lse, lse2)
