@@ -438,9 +438,12 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         // the accumulated output.  bf16 weights and fp32 sums lose nothing at any scale, so
         // there an item goes by 0 instead of its maxima until a score leaves +-64 (an exchange
         // for each item's first tile cost a tenth of its time).  fp16 weights have to stay
-        // below 2^16.
+        // below 2^16 and end at 2^-24: they go by 2^-7 of the maximum, so that it has weight 2^7 to
+        // 2^15 and the others their 11 bits down to 2^-21 of it, some to 2^-31 (by the maximum
+        // itself a list's small weights were lost from 2^-25 of it on).
         constexpr bool kZeroStart = C::kWide;
-        constexpr float kSlack = C::kWide ? 64.0f : 8.0f;
+        constexpr float kSlack = C::kWide ? 64.0f : 15.0f;
+        constexpr float kBelow = C::kWide ? 0.0f : 7.0f;
         // the thread's heads in a row of the weights, and the row's part of them as scratch
         constexpr int kOwn = HN * 2;                     // bytes of a term
         auto scratch = [&](int b, int i) {               // float i of 4 HN
@@ -580,7 +583,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                         const float old = first ? -3.0e38f : based ? mx[key] : 0.0f;
                         mn = fmaxf(
                             old, fmaxf(fmaxf(*scratch(b, key), *scratch(b, HN + key)),
-                                       fmaxf(*scratch(b, 2 * HN + key), *scratch(b, 3 * HN + key))));
+                                       fmaxf(*scratch(b, 2 * HN + key), *scratch(b, 3 * HN + key))) -
+                                     kBelow);
                         *scratch(b, key) = ex2(old - mn);
                         mx[key] = mn;
                     }

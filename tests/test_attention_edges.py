@@ -170,11 +170,11 @@ def test_one_key_far_above_a_long_list(dt, kv, nats, n):
     one_far_above(dt, kv, nats, n)
 
 
-def one_far_above(dt, kv, nats, n):
-    b = Batch(((2, n),), 16, 1, 64, n, 1, dt, kv, 0, seed=25, lens=[n, n])
-    b.sel = torch.stack([torch.arange(n), torch.arange(n - 1, -1, -1)]).to(torch.int32)
+def one_far_above(dt, kv, nats, n, rows=2):
+    b = Batch(((rows, n),), 16, 1, 64, n, 1, dt, kv, 0, seed=25, lens=[n] * rows)
+    b.sel = torch.stack([torch.arange(n), torch.arange(n - 1, -1, -1)] * (rows // 2)).to(torch.int32)
     g = torch.Generator().manual_seed(26)
-    b.q = torch.zeros((2, 16, 64))
+    b.q = torch.zeros((rows, 16, 64))
     b.q[:, :, 0] = 8.0
     b.q = b.q.to(b.dt)
     k = torch.zeros((n, 1, 64))
@@ -217,3 +217,9 @@ def test_places_of_a_tile_without_a_head_hold_nothing_of_the_last_call(group, dt
         other.run()
         again, lse2 = b.run()
         assert torch.equal(first, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("rows", [2, 170])
+def test_fp16_weights_far_below_the_largest(rows):
+    """Weights of 2^-25.5 of the largest, which keep some bits in fp16 relative to 2^7 of it."""
+    one_far_above("fp16", "same", 17.7, 2048, rows)
