@@ -111,7 +111,7 @@ struct AttnCfg {
     // Shared memory after the stages, the weights and the queries.
     static constexpr int kStats = 2 * 4 * kHeads * 4;   // sums by warpgroup and quadrant
     static constexpr int kMax = 2 * kHeads * 4;         // maxima by warpgroup
-    static constexpr int kQScale = kFp8 ? (kScaleItems + 4) * 4 : 0;
+    static constexpr int kQScale = kFp8 ? (kScaleItems + 1) * NH * 4 : 0;
     static constexpr int kKeyInfo = kAttnTile * (kFp8 ? 9 : 1);   // of a tile, 2 kTiles of them
     static constexpr int kFixed = kStats + kMax + kQScale + 2 * kPBytes + 2 * kQBytes + 8 * 21;
     static constexpr int kFit =
@@ -351,7 +351,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
     // [2 warpgroups][4 quadrants][HN] sums of an item, [2][HN] running maxima
     float* sums = reinterpret_cast<float*>(qbuf + 2 * C::kQBytes);
     float* maxima = sums + C::kStats / 4;
-    float* qscale = maxima + C::kMax / 4;                      // [kScaleItems], 4 of scratch
+    float* qscale = maxima + C::kMax / 4;                      // [kScaleItems][NH], [NH] of scratch
     float* kscale = qscale + C::kQScale / 4;                   // [2 kTiles][128]
     float* vscale = kscale + (C::kFp8 ? C::kStages * kAttnTile : 0);
     uint8_t* valid = reinterpret_cast<uint8_t*>(vscale + (C::kFp8 ? C::kStages * kAttnTile : 0));
@@ -499,6 +499,15 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 }
                 tmem_wait_ld();
                 tc_fence_before();
+                if (C::kFp8) {
+                    const float* qs = qscale + iq % kScaleItems * NH + head0;
+#pragma unroll
+                    for (int i = 0; i < HN; i += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(qs + i);
+                        mul2(x[i], x[i + 1], f.x, f.y);
+                        mul2(x[i + 2], x[i + 3], f.z, f.w);
+                    }
+                }
                 const int ring = (n + j) % C::kStages * kAttnTile + key;
                 const bool ok = valid[ring] != 0;
                 // a tile without a key leaves everything as it is
@@ -508,7 +517,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                                reinterpret_cast<const uint32_t*>(valid + (ring - key))[lane] != 0u);
                 float ks = p.scale_log2, vs = 1.0f;
                 if (C::kFp8) {
-                    ks = ok ? kscale[ring] * qscale[iq % kScaleItems] : 0.0f;
+                    ks = ok ? kscale[ring] : 0.0f;
                     vs = vscale[ring];
                 }
                 const bool all = __all_sync(0xFFFFFFFFu, ok);
@@ -735,16 +744,18 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
             } else {
                 // The queries as sums of e4m3 terms, each 1/16 of the scale of the one before: two
                 // hold the 8 bits of a bf16 element, three the 11 of an fp16 one, down to 2^-22 of
-                // the item's largest.
+                // its head's largest.  One scale for all heads, which would leave nothing of a head
+                // 2^-22 of its neighbour's size, spared the softmax a product (64 heads over 2,048 x
+                // 2,048 keys: 280 us against 302); a flag for heads of one size took as long.
                 constexpr int kGroup = D / 16;           // lanes of a vector, 16 elements each
                 const int c = lane % kGroup;
-                // the item's largest magnitude, infinities left out, all of its elements asked for
-                // at once (a vector after another: 215 us against 202 for 4,096 rows of 64 heads)
-                using T2 = typename std::conditional<MODE == kModeFp8Bf16, __nv_bfloat162,
-                                                     __half2>::type;
-                constexpr int kIter = (NH * kGroup + 127) / 128;
-                float amax;
+                float* mul = qscale + kScaleItems * NH;  // of a head, by the lanes that read it
                 {
+                    // the heads' largest magnitudes, all of their elements asked for at once (a
+                    // vector after another: 215 us against 202 for 4,096 rows of 64 heads)
+                    using T2 = typename std::conditional<MODE == kModeFp8Bf16, __nv_bfloat162,
+                                                         __half2>::type;
+                    constexpr int kIter = (NH * kGroup + 127) / 128;
                     uint4 in[kIter][2];
 #pragma unroll
                     for (int k = 0; k < kIter; ++k) {
@@ -757,37 +768,30 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                             in[k][1] = at[1];
                         }
                     }
-                    const T2* two = reinterpret_cast<const T2*>(in);
-                    T2 m = __habs2(two[0]);
 #pragma unroll
-                    for (int i = 1; i < 8 * kIter; ++i)
-                        m = __hmax2(m, __habs2(two[i]));
-                    amax = fmaxf(value(m.x), value(m.y));
-                    if (!(amax < INFINITY)) {
-                        amax = 0.0f;
-                        const T* e = reinterpret_cast<const T*>(in);
+                    for (int k = 0; k < kIter; ++k) {
+                        const int h = from / kGroup + k * (128 / kGroup);
+                        const T2* two = reinterpret_cast<const T2*>(in[k]);
+                        T2 m = __habs2(two[0]);
 #pragma unroll
-                        for (int i = 0; i < 16 * kIter; ++i) {
-                            const float a = fabsf(value(e[i]));
-                            amax = fmaxf(amax, a < INFINITY ? a : 0.0f);
+                        for (int i = 1; i < 8; ++i)
+                            m = __hmax2(m, __habs2(two[i]));
+                        float amax = fmaxf(value(m.x), value(m.y));
+#pragma unroll
+                        for (int d = kGroup / 2; d > 0; d >>= 1)
+                            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+                        // a power of two that takes amax to 128..256, so that no element is
+                        // rounded (any of an infinite one, whose head is NaN whatever it is)
+                        const int ex = static_cast<int>(__float_as_uint(amax) >> 23);
+                        const int up = amax > 0.0f ? min(max(261 - ex, 1), 254) : 127;
+                        const float f = __uint_as_float(static_cast<uint32_t>(up) << 23);
+                        if (c == 0 && h < NH) {
+                            mul[h] = f;
+                            qscale[nq % kScaleItems * NH + h] = p.scale_log2 / f;
                         }
                     }
+                    __syncwarp();
                 }
-                float* four = qscale + kScaleItems;
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1)
-                    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-                if (lane == 0)
-                    four[quad] = amax;
-                bar_all(true, 3, 128);
-                amax = fmaxf(fmaxf(four[0], four[1]), fmaxf(four[2], four[3]));
-                bar_all(true, 3, 128);
-                // a power of two that takes amax to 128..256, so that no element is rounded
-                const int ex = static_cast<int>(__float_as_uint(amax) >> 23);
-                const int up = amax > 0.0f ? min(max(261 - ex, 1), 254) : 127;
-                const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
-                if (from == 0)
-                    qscale[nq % kScaleItems] = p.scale_log2 / mul;
                 // (heads that are none are zeros: the tile's scores are those of all its heads)
 #pragma unroll 1
                 for (int h = from / kGroup; h < NH; h += 128 / kGroup) {
@@ -798,12 +802,13 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                         in[1] = at[1];
                     }
                     const T* e = reinterpret_cast<const T*>(in);
+                    const float f = mul[h];
                     uint32_t v[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         // (+ 0 x: an infinite element makes its head NaN)
                         float a = value(e[2 * i]), b = value(e[2 * i + 1]), a0 = a, b0 = b;
-                        mul2(a, b, mul, mul);
+                        mul2(a, b, f, f);
                         fma2(a0, b0, 0.0f, 0.0f, a, b);
                         v[i] = pack2<__half>(a0, b0);
                     }

@@ -223,3 +223,14 @@ def test_places_of_a_tile_without_a_head_hold_nothing_of_the_last_call(group, dt
 def test_fp16_weights_far_below_the_largest(rows):
     """Weights of 2^-25.5 of the largest, which keep some bits in fp16 relative to 2^7 of it."""
     one_far_above("fp16", "same", 17.7, 2048, rows)
+
+
+@pytest.mark.parametrize("dt,far", [("bf16", 1e30), ("bf16", 1e-30), ("fp16", 2.0 ** 14), ("fp16", 2.0 ** -12)])
+def test_heads_of_very_different_sizes(dt, far):
+    """A head's queries are held relative to its own largest element, not to its neighbours'."""
+    b = Batch(((6, 400),), 20, 1, 128, 300, 1, dt, "fp8", 16, seed=29)
+    b.q[:, 3] *= far
+    b.q[:, 11] /= far if dt == "bf16" else 1.0
+    if dt == "fp16" and far > 1:
+        b.q[:, 4:] *= 2.0 ** -12
+    check(b, scale=1.0)
