@@ -435,14 +435,17 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
         float* mx = maxima + wg * HN;
         // Weights are kept relative to a running maximum that is replaced only where a score
         // passes it by kSlack: most tiles need no exchange over the keys and no rescaling of
-        // the accumulated output.  bf16 weights and fp32 sums lose nothing at any scale, so
-        // there an item goes by 0 instead of its maxima until a score leaves +-64 (an exchange
-        // for each item's first tile cost a tenth of its time).  fp16 weights have to stay
+        // the accumulated output.  bf16 weights and fp32 sums have room, so there an item goes by 0
+        // instead of its maxima until a score leaves +-32 (an exchange for each item's first tile
+        // cost a tenth of its time): weights of 2^32 at most over values below 2^80 leave a list of
+        // 65,536 keys finite, and values above 2^-84 keep their bits.  (+-64 left them 2^-52 to
+        // 2^48 and took as long where scores have a deviation of 4, 177 us, 188 for 199 at 16; +-16
+        // took 188 and 230.)  fp16 weights have to stay
         // below 2^16 and end at 2^-24: they go by 2^-7 of the maximum, so that it has weight 2^7 to
         // 2^15 and the others their 11 bits down to 2^-21 of it, some to 2^-31 (by the maximum
         // itself a list's small weights were lost from 2^-25 of it on).
         constexpr bool kZeroStart = C::kWide;
-        constexpr float kSlack = C::kWide ? 64.0f : 15.0f;
+        constexpr float kSlack = C::kWide ? 32.0f : 15.0f;
         constexpr float kBelow = C::kWide ? 0.0f : 7.0f;
         // the thread's heads in a row of the weights, and the row's part of them as scratch
         constexpr int kOwn = HN * 2;                     // bytes of a term

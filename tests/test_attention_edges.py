@@ -234,3 +234,21 @@ def test_heads_of_very_different_sizes(dt, far):
     if dt == "fp16" and far > 1:
         b.q[:, 4:] *= 2.0 ** -12
     check(b, scale=1.0)
+
+
+@pytest.mark.parametrize("kv", ["same", "fp8"])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_large_and_small_values_under_large_scores(sign, kv):
+    """Scores of +-60 in base 2 over values of 1e25 or 1e-30: the output is as large as the values."""
+    b = Batch(((4, 600),), 16, 1, 64, 400, 1, "bf16", kv, 0, seed=30, lens=[600] * 4)
+    b.q = torch.full((4, 16, 64), sign * 1.0).to(b.dt)
+    one = 60 * np.log(2) / 8                              # the score, over sqrt(64) and 64 products
+    rnd = torch.rand((600, 1, 64), generator=b.g)
+    if kv == "fp8":
+        b.k = (200 - 16 * rnd).to(torch.float8_e4m3fn).view(torch.uint8)
+        b.ks = torch.full((600, 1), one / 200)
+        b.vs = torch.full((600, 1), 1e23 if sign > 0 else 1e-32)
+    else:
+        b.k = (one - 0.1 * rnd).to(b.dt)
+        b.v = ((1e25 if sign > 0 else 1e-30) * (1 + rnd)).to(b.dt)
+    check(b)
