@@ -1,5 +1,6 @@
 // Attention over the selected keys, and the block lists of candidate masks.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -1401,19 +1402,24 @@ template <int D, int NH, int MODE>
 cudaError_t attention_tc(const AttnParams& p, cudaStream_t st)
 {
     using C = AttnCfg<D, NH, MODE>;
-    static const cudaError_t attr = [] {
-        // the warpgroups' trade has to add up against what a block is launched with
-        cudaFuncAttributes a;
-        cudaError_t e = cudaFuncGetAttributes(&a, attention_tc_kernel<D, NH, MODE>);
-        if (e == cudaSuccess && C::kTrade && a.numRegs != C::kLaunchRegs)
-            e = cudaErrorLaunchOutOfResources;
-        return e != cudaSuccess
-                   ? e
-                   : cudaFuncSetAttribute(attention_tc_kernel<D, NH, MODE>,
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    }();
-    if (attr != cudaSuccess)
-        return attr;
+    static std::atomic<uint64_t> ready;
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess)
+        e = once_per_device(ready, device, [] {
+            // the warpgroups' trade has to add up against what a block is launched with
+            cudaFuncAttributes a;
+            cudaError_t r = cudaFuncGetAttributes(&a, attention_tc_kernel<D, NH, MODE>);
+            if (r == cudaSuccess && C::kTrade && a.numRegs != C::kLaunchRegs)
+                r = cudaErrorLaunchOutOfResources;
+            return r != cudaSuccess
+                       ? r
+                       : cudaFuncSetAttribute(attention_tc_kernel<D, NH, MODE>,
+                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              C::kSmem);
+        });
+    if (e != cudaSuccess)
+        return e;
     const int items = p.rows * p.Hkv * p.head_tiles * p.splits;
     const unsigned blocks = p.cluster ? items : std::min(items, device_sms());
     return launch_pdl_cluster(attention_tc_kernel<D, NH, MODE>, dim3(blocks), dim3(C::kThreads),

@@ -1,6 +1,7 @@
 // Internal interfaces between the host library and the kernels.  Nothing in
 // here crosses the C ABI.
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -323,6 +324,20 @@ PlanView plan_view(const struct ::indexer_plan_s* p);
 void count_launch();             // adds one to indexer_launch_count
 bool device_supported();         // the current device is one the kernels are built for
 int device_sms();                // its SMs
+
+// A kernel's attributes belong to a device: `set` runs in a device's first call, and again in the
+// next one if it failed.  `done` has a bit per device (the 65th and later are set every time).
+template <typename Set>
+cudaError_t once_per_device(std::atomic<uint64_t>& done, int device, Set set)
+{
+    const uint64_t bit = device >= 0 && device < 64 ? 1ull << device : 0;
+    if (done.load(std::memory_order_acquire) & bit)
+        return cudaSuccess;
+    const cudaError_t e = set();
+    if (e == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 constexpr int kMaxRotPairs = 128;
 constexpr int kMaxHeadDim = 256;
