@@ -204,6 +204,8 @@ class Plan:
         self.workspace_bytes = workspace_bytes
         self.problem = problem
         self._keep = keepalive
+        keys = keepalive[1]
+        self.max_keys = int((keys[1:] - keys[:-1]).max()) if keys.numel() > 1 else 0
 
     def info(self):
         kb, rc, ns, st = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
@@ -533,12 +535,13 @@ class Attention:
     """Owns an ``indexer_attention_t``; destroyed with the object."""
 
     def __init__(self, handle, workspace_bytes: int, spec: _AttentionSpec, rows: int,
-                 requests: int):
+                 requests: int, max_keys: int):
         self.handle = handle
         self.workspace_bytes = workspace_bytes
         self.spec = spec
         self.rows = rows
         self.requests = requests
+        self.pages = -(-max_keys // spec.page_size) if spec.page_size > 0 else 0
         # what the tensors of a call are compared with
         self.dtype = torch.bfloat16 if spec.dtype == IDX_BF16 else torch.float16
         self.dense = spec.kv_format == IDX_KV_DENSE
@@ -568,7 +571,8 @@ def indexer_attention_create(plan: Plan, Hq: int, Hkv: int, D: int, num_sel: int
     handle, ws = ctypes.c_void_p(), ctypes.c_size_t()
     _check("indexer_attention_create", lib().indexer_attention_create(
         plan.handle, ctypes.byref(spec), ctypes.byref(handle), ctypes.byref(ws)))
-    return Attention(handle, ws.value, spec, plan.problem.total_rows, plan.problem.num_requests)
+    return Attention(handle, ws.value, spec, plan.problem.total_rows, plan.problem.num_requests,
+                     plan.max_keys)
 
 
 def _heads(name: str, t, shape, dtype):
@@ -607,8 +611,10 @@ def indexer_sparse_attention(attn: Attention, q, k, v, sel, compress_len, out, w
     table = ld_table = 0
     if page_table is not None:
         if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_cuda or \
-                page_table.shape[0] != attn.requests or page_table.stride(1) != 1:
-            raise ValueError("page_table: int32 CUDA tensor [requests, pages] expected")
+                page_table.shape[0] != attn.requests or page_table.shape[1] < attn.pages or \
+                page_table.stride(1) != 1:
+            raise ValueError(f"page_table: int32 CUDA tensor [requests, {attn.pages} pages or more] "
+                             "expected")
         table = page_table.data_ptr()
         ld_table = page_table.stride(0) if attn.requests > 1 else page_table.shape[1]
     io = _ATTENTION_IO(
@@ -631,9 +637,10 @@ def indexer_mask_blocks(plan: Plan, cand_mask, compress_len, block: int, blocks,
     """The candidate blocks of every mask row as a list: ``blocks`` int32 [rows, num_sel]
     (ascending, then -1) and ``count`` int32 [rows]."""
     rows = plan.problem.total_rows
+    need = -(-plan.max_keys // block) if block > 0 else 0
     if cand_mask.element_size() != 1 or not cand_mask.is_cuda or cand_mask.dim() != 2 or \
-            cand_mask.shape[0] != rows or cand_mask.stride(1) != 1:
-        raise ValueError("cand_mask: CUDA tensor [rows, blocks] of one byte expected")
+            cand_mask.shape[0] != rows or cand_mask.shape[1] < need or cand_mask.stride(1) != 1:
+        raise ValueError(f"cand_mask: CUDA tensor [rows, {need} blocks or more] of one byte expected")
     num_sel, shape = blocks.shape[-1], (rows,)
     rc = (_lib or lib()).indexer_mask_blocks(
         plan.handle, cand_mask.data_ptr(), cand_mask.stride(0) if rows > 1 else cand_mask.shape[1],
