@@ -397,6 +397,14 @@ def indexer_chunk_rows(prefix_len: int, budget_token2: float = 2.0e8, chunk_min:
 
 _INT32 = torch.int32
 _DTYPES = {torch.bfloat16: IDX_BF16, torch.float16: IDX_FP16, torch.float32: IDX_FP32}
+# what codes and masks come in: bytes, or the type itself
+_E4M3 = frozenset((torch.uint8, torch.int8, torch.float8_e4m3fn))
+_E2M1 = frozenset((torch.uint8, torch.int8)
+                  + ((torch.float4_e2m1fn_x2,) if hasattr(torch, "float4_e2m1fn_x2") else ()))
+_E8M0 = frozenset((torch.uint8, torch.int8)
+                  + ((torch.float8_e8m0fnu,) if hasattr(torch, "float8_e8m0fnu") else ()))
+_FLOAT = frozenset((torch.float32,))
+_MASK = frozenset((torch.uint8, torch.int8, torch.bool))
 
 
 def _dense(name: str, t):
@@ -470,14 +478,16 @@ def _cache_shape(codes, scales, fmt: int):
     """(slots, heads, D) of a cache's codes and scales."""
     slots, heads, n = codes.shape
     if fmt == IDX_K_FP4_E2M1_UE8M0:
-        D, want, kind = 2 * n, (slots, heads, n // 16), torch.uint8
+        D, want, kind, name = 2 * n, (slots, heads, n // 16), _E2M1, "e2m1 codes and ue8m0"
+        scale_kind = _E8M0
     else:
-        D, want, kind = n, (slots, heads), torch.float32
-    if (scales.dtype != kind or scales.shape != want or codes.element_size() != 1
+        D, want, kind, name = n, (slots, heads), _E4M3, "e4m3 codes and fp32"
+        scale_kind = _FLOAT
+    if (codes.dtype not in kind or scales.dtype not in scale_kind or scales.shape != want
             or not codes.is_cuda or not scales.is_cuda or not codes.is_contiguous()
             or not scales.is_contiguous()):
-        raise ValueError(f"cache: contiguous CUDA codes of one byte and {kind} scales of shape "
-                         f"{want} expected")
+        raise ValueError(f"cache: contiguous CUDA {name} scales (or their bytes) of shape {want} "
+                         "expected")
     return slots, heads, D
 
 
@@ -576,9 +586,9 @@ def indexer_attention_create(plan: Plan, Hq: int, Hkv: int, D: int, num_sel: int
 
 
 def _heads(name: str, t, shape, dtype):
-    """Strides of a CUDA tensor of that shape and type (None: e4m3 codes of one byte)."""
+    """Strides of a CUDA tensor of that shape and type (None: e4m3 codes or their bytes)."""
     if t.shape != shape or not t.is_cuda or \
-            (t.element_size() != 1 if dtype is None else t.dtype != dtype):
+            (t.dtype not in _E4M3 if dtype is None else t.dtype != dtype):
         raise ValueError(f"{name}: CUDA tensor {shape} of {dtype or 'e4m3 codes'} expected")
     st = t.stride()
     if st[2] != 1:
@@ -638,9 +648,10 @@ def indexer_mask_blocks(plan: Plan, cand_mask, compress_len, block: int, blocks,
     (ascending, then -1) and ``count`` int32 [rows]."""
     rows = plan.problem.total_rows
     need = -(-plan.max_keys // block) if block > 0 else 0
-    if cand_mask.element_size() != 1 or not cand_mask.is_cuda or cand_mask.dim() != 2 or \
+    if cand_mask.dtype not in _MASK or not cand_mask.is_cuda or cand_mask.dim() != 2 or \
             cand_mask.shape[0] != rows or cand_mask.shape[1] < need or cand_mask.stride(1) != 1:
-        raise ValueError(f"cand_mask: CUDA tensor [rows, {need} blocks or more] of one byte expected")
+        raise ValueError(f"cand_mask: CUDA tensor [rows, {need} blocks or more] of bytes or truth values "
+                         "expected")
     num_sel, shape = blocks.shape[-1], (rows,)
     rc = (_lib or lib()).indexer_mask_blocks(
         plan.handle, cand_mask.data_ptr(), cand_mask.stride(0) if rows > 1 else cand_mask.shape[1],

@@ -50,3 +50,48 @@ def test_a_mask_too_narrow_for_the_longest_request():
             K.indexer_mask_blocks(plan, mask, lens, 8, blocks)
     with pytest.raises(K.IndexerError):                        # no block at all: the library's refusal
         K.indexer_mask_blocks(plan, whole, lens, 0, blocks)
+
+
+OTHERS = [torch.float8_e5m2, torch.float8_e4m3fnuz, torch.bool]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", OTHERS)
+def test_codes_of_another_type(kind):
+    plan = _plan()
+    table = torch.zeros((2, 7), dtype=torch.int32, device="cuda")
+    codes = torch.zeros((160, 1, 128), dtype=torch.uint8, device="cuda")
+    for good in (codes, codes.view(torch.float8_e4m3fn), codes.view(torch.int8)):
+        _attention_call(plan, table, fmt=K.IDX_KV_FP8_E4M3, k=good, v=good)
+    for bad in (dict(k=codes.view(kind), v=codes), dict(k=codes, v=codes.view(kind))):
+        with pytest.raises(ValueError):
+            _attention_call(plan, table, fmt=K.IDX_KV_FP8_E4M3, **bad)
+    x = torch.ones((160, 1, 128), dtype=torch.bfloat16, device="cuda")
+    s = torch.empty((160, 1), device="cuda")
+    e4, e8 = codes[:, :, :64].contiguous(), torch.empty((160, 1, 4), dtype=torch.uint8, device="cuda")
+    K.indexer_cache_write(x, codes.view(torch.float8_e4m3fn), s)
+    K.indexer_cache_write(x, e4, e8, K.IDX_K_FP4_E2M1_UE8M0)
+    for call in (lambda: K.indexer_cache_write(x, codes.view(kind), s),
+                 lambda: K.indexer_cache_write(x, e4.view(kind), e8, K.IDX_K_FP4_E2M1_UE8M0),
+                 lambda: K.indexer_cache_write(x, e4, e8.view(kind), K.IDX_K_FP4_E2M1_UE8M0),
+                 lambda: K.indexer_cache_write(x, e4.view(torch.float8_e4m3fn), e8,
+                                               K.IDX_K_FP4_E2M1_UE8M0),
+                 lambda: K.indexer_cache_read(codes.view(kind), s, K.IDX_K_FP8_E4M3, None, x)):
+        with pytest.raises(ValueError, match="cache"):
+            call()
+    torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_masks_of_truth_values_and_of_another_type():
+    plan = _plan()
+    lens = torch.tensor([100, 100, 37, 37], dtype=torch.int32, device="cuda")
+    mask = torch.arange(52, device="cuda").view(4, 13) % 3 == 0
+    a, b = (torch.empty((4, 8), dtype=torch.int32, device="cuda") for _ in "ab")
+    K.indexer_mask_blocks(plan, mask, lens, 8, a)
+    K.indexer_mask_blocks(plan, mask.to(torch.uint8), lens, 8, b)
+    assert torch.equal(a, b)
+    # -0.0 is a byte that is not zero
+    for kind in (torch.float8_e4m3fn, torch.float8_e5m2):
+        with pytest.raises(ValueError, match="cand_mask"):
+            K.indexer_mask_blocks(plan, mask.to(torch.uint8).view(kind), lens, 8, a)
