@@ -37,13 +37,17 @@ size_t type_bytes(int dtype) { return dtype == IDX_FP32 ? 4 : 2; }
 
 int finish(cudaError_t e) { return e == cudaSuccess ? IDX_OK : IDX_ERR_CUDA; }
 
-// 2^64 turns per 2 pi radians: a frequency in radians per position as the phase a
-// position adds, modulo one turn.
+// A frequency in radians per position as the phase a position adds, in 2^-64 turns, modulo one
+// turn.  1 / 2 pi is two doubles and their product with the frequency too, so that the phase of
+// position 2^31 has the frequency's own rounding (2^-53 of it, 1.2e-7 rad at one radian a position)
+// and no other.
 uint64_t phase_increment(double radians)
 {
-    double turns = radians / 6.283185307179586476925286766559;
-    turns -= std::floor(turns);
-    return static_cast<uint64_t>(std::ldexp(turns, 53)) << 11;
+    constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+    const double turns = radians * kHi;
+    const double rest = std::fma(radians, kHi, -turns) + radians * kLo;
+    return static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64)) +
+           static_cast<uint64_t>(static_cast<int64_t>(std::nearbyint(std::ldexp(rest, 64))));
 }
 
 }  // namespace
