@@ -345,19 +345,31 @@ __device__ __forceinline__ float largest4(const float* groups)
     return fmaxf(fmaxf(g.x, g.y), fmaxf(g.z, g.w));
 }
 
-// e4m3 codes of eight values times `inv` (saturating, ties to even).  A product with the rounded
-// reciprocal is a unit in the last place of fp32 off the quotient, as the turned values
-// themselves are; correcting it took 42 -> 45 us for 16,384 rows and changed no code of 300,000.
-__device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float inv)
+// e4m3 codes of eight values over `scale` (saturating, ties to even).  The quotient is the fp32 one:
+// x inv, inv the rounded reciprocal, less what that is too much (Markstein's theorem: a faithful
+// quotient and a correctly rounded reciprocal give the correctly rounded quotient; the signs keep
+// that of a zero).  x inv alone took 42 us instead of 45 for 16,384 rows, but values half way between
+// two codes, such as three quarters of their vector's largest, went to either.
+__device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float scale, float inv)
 {
     uint32_t two[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        const uint64_t q = mul2(pack(v[2 * i], v[2 * i + 1]), pack(inv, inv));
+        const uint64_t over = fma2(q, pack(scale, scale), pack(-v[2 * i], -v[2 * i + 1]));
         float2 f;
-        unpack(mul2(pack(v[2 * i], v[2 * i + 1]), pack(inv, inv)), f.x, f.y);
+        unpack(fma2(over, pack(-inv, -inv), q), f.x, f.y);
         two[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
     }
     return make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
+}
+
+// Infinite values as the largest finite one (they would leave a NaN of a quotient).
+__device__ __forceinline__ void finite8(float (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = fminf(fmaxf(v[i], -3.402823466e38f), 3.402823466e38f);
 }
 
 __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8], float inv)
@@ -375,11 +387,13 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8], float inv)
 
 // Scale of an e4m3 row from its largest magnitude (an infinite one as the largest finite
 // value): amax / 448, never below the smallest normal number (so its reciprocal is finite), 1
-// for a zero row.
+// for a zero row.  The division as above: 1 / 448 is a constant.
 __device__ __forceinline__ float e4m3_scale(float amax)
 {
     amax = fminf(amax, 3.402823466e38f);
-    return amax > 0.0f ? fmaxf(amax / 448.0f, 1.17549435e-38f) : 1.0f;
+    constexpr float kInv = 1.0f / 448.0f;
+    const float q = amax * kInv;
+    return amax > 0.0f ? fmaxf(fmaf(fmaf(q, -448.0f, amax), kInv, q), 1.17549435e-38f) : 1.0f;
 }
 
 // Biased exponent floor(log2(amax)) - 2 of an e2m1 block, clamped to ue8m0's 0..254; 127
@@ -401,9 +415,9 @@ __device__ __forceinline__ float exp2_neg(uint32_t e) { return __uint_as_float((
 // the groups' maxima meet in shared memory, the values stay where they are (exchanging the values
 // took 2.4 times as long).
 //
-// Instructions bound it, not bytes (some 300 per warp and 512 elements: widening, turning, maxima,
-// two divisions, narrowing; without rotation and divisions it runs at 5.9 TB/s).  16,384 x 32 x
-// 128 bf16 with 64 turned: e4m3 42 us, e2m1 42 us (4.8 and 4.0 TB/s).  Blocks of 64 registers,
+// Instructions bound it, not bytes (some 310 per warp and 512 elements: widening, turning, maxima,
+// quotients, narrowing; without rotation and quotients it runs at 5.9 TB/s).  16,384 x 32 x
+// 128 bf16 with 64 turned: e4m3 45 us, e2m1 42 us (4.5 and 4.0 TB/s).  Blocks of 64 registers,
 // four an SM: at 40 and six the loop took 52 and 58 us, and without it, a vector a group, whose
 // set-up is a third of its instructions, it was 50 and 53 us at best.
 template <typename T, bool kFp4>
@@ -494,8 +508,12 @@ cache_write_kernel(const __grid_constant__ RopeParams rp,
                 const float s = e4m3_scale(m);
                 const float inv = 1.0f / s;
                 uint8_t* o = c.codes + vec * c.D;
-                *reinterpret_cast<uint2*>(o + u.a) = e4m3x8(a, inv);
-                *reinterpret_cast<uint2*>(o + u.b) = e4m3x8(b, inv);
+                if (m == INFINITY) {
+                    finite8(a);
+                    finite8(b);
+                }
+                *reinterpret_cast<uint2*>(o + u.a) = e4m3x8(a, s, inv);
+                *reinterpret_cast<uint2*>(o + u.b) = e4m3x8(b, s, inv);
                 if (l == 0)
                     static_cast<float*>(c.scales)[vec] = s;
             }
@@ -571,7 +589,8 @@ cache_write_any_kernel(const __grid_constant__ RopeParams rp,
                 float w[8];
                 for (int k = 0; k < 8; ++k)
                     w[k] = v[8 * l + k];
-                *reinterpret_cast<uint2*>(c.codes + vec * c.D + 8 * l) = e4m3x8(w, inv);
+                finite8(w);
+                *reinterpret_cast<uint2*>(c.codes + vec * c.D + 8 * l) = e4m3x8(w, s, inv);
             }
         }
         __syncwarp();
@@ -792,7 +811,7 @@ cudaError_t cache_write_of(const RopeParams& rp, const CacheWriteCall& c, cudaSt
         while (lanes * 16 < c.D)
             lanes *= 2;
         // Several vectors a group, up to eight, where that leaves six blocks an SM (rows of 32
-        // heads to e4m3: 16,384 rows 42 us in eights, 61 one by one; 4,096 rows 12.6 in fours,
+        // heads to e4m3, a product for the quotient: 16,384 rows 42 us in eights, 61 one by one; 4,096 rows 12.6 in fours,
         // 13.6 in eights, 15.7 one by one; 1,024 rows 5.0 one by one, 6.3 in threes).
         const int64_t blocks = ((int64_t)c.rows * c.heads * lanes + kThreads - 1) / kThreads;
         const int batch = static_cast<int>(
