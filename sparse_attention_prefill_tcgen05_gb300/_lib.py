@@ -191,6 +191,15 @@ def _stream(stream=None):
     return stream.cuda_stream
 
 
+def _new(stream, make, *args, **kw):
+    """A tensor that a call on ``stream`` writes, from that stream's memory: the current stream's may
+    still be in use by work queued there."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def _check(fn: str, rc: int):
     if rc != IDX_OK:
         raise IndexerError(fn, rc)
@@ -370,7 +379,7 @@ def indexer_page_indices(plan: Plan, raw_idx, page_table, page_size: int, page_i
     int32 [rows, topk] and ``page_table`` int32 [requests, ld] on the device; writes into
     ``page_idx`` (default: a new tensor; may be ``raw_idx``) and returns it."""
     if page_idx is None:
-        page_idx = torch.empty_like(raw_idx)
+        page_idx = _new(stream, torch.empty_like, raw_idx)
     for name, t in (("raw_idx", raw_idx), ("page_table", page_table), ("page_idx", page_idx)):
         if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
             raise ValueError(f"{name}: contiguous int32 CUDA tensor expected")
@@ -460,7 +469,7 @@ def indexer_rope(rope: Rope, x, positions, out=None, inverse: bool = False, stre
     new tensor; may be ``x``) and return it; ``inverse`` turns back."""
     code, sx = _dense("x", x)
     if out is None:
-        out = torch.empty_like(x)
+        out = _new(stream, torch.empty_like, x)
     shape = x.shape
     rows, heads, D = shape
     ocode, so = (code, sx) if out is x else _dense("out", out)
@@ -533,7 +542,8 @@ def indexer_cache_read(codes, scales, fmt: int, slots, out, out_scales=None, str
 def indexer_page_slots(plan: Plan, page_table, page_size: int, slots=None, stream=None):
     """Cache slots of the batch's packed keys (int32 [total_keys]) from a page table."""
     if slots is None:
-        slots = torch.empty(plan.problem.total_keys, dtype=torch.int32, device=page_table.device)
+        slots = _new(stream, torch.empty, plan.problem.total_keys, dtype=torch.int32,
+                     device=page_table.device)
     table = _i32("page_table", page_table, (plan.problem.num_requests, page_table.shape[-1]))
     _check("indexer_page_slots", lib().indexer_page_slots(
         plan.handle, table, page_table.shape[1], int(page_size),
