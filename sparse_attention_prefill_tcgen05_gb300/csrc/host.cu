@@ -721,19 +721,17 @@ void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 // The current device's properties, asked for once per device (they do not change).
 static DeviceInfo known_device()
 {
-    static std::atomic<int> known[64];               // 0: not asked; SMs + 1, negative: not supported
+    static std::atomic<int> known[64];               // its SMs, negative: not supported
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
         return device_info();
+    const int v = remembered(known[dev], [] {
+        const DeviceInfo d = device_info();
+        return d.ok ? d.sms : -d.sms;                // (0 SMs: it could not be asked)
+    });
     DeviceInfo d;
-    int v = known[dev].load(std::memory_order_relaxed);
-    if (v == 0) {
-        d = device_info();
-        v = d.ok ? d.sms + 1 : -d.sms - 1;
-        known[dev].store(v, std::memory_order_relaxed);
-    }
     d.ok = v > 0;
-    d.sms = (v > 0 ? v : -v) - 1;
+    d.sms = v > 0 ? v : -v;
     return d;
 }
 

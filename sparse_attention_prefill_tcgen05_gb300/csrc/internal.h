@@ -339,6 +339,19 @@ cudaError_t once_per_device(std::atomic<uint64_t>& done, int device, Set set)
     return e;
 }
 
+// An answer that does not change, kept once there is one (0: none).
+template <typename Ask>
+int remembered(std::atomic<int>& known, Ask ask)
+{
+    int v = known.load(std::memory_order_relaxed);
+    if (v == 0) {
+        v = ask();
+        if (v != 0)
+            known.store(v, std::memory_order_relaxed);
+    }
+    return v;
+}
+
 constexpr int kMaxRotPairs = 128;
 constexpr int kMaxHeadDim = 256;
 

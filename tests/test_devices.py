@@ -1,4 +1,4 @@
-"""Kernel attributes are set once per device (a host-only program over csrc/internal.h)."""
+"""What is asked of or set on a device once (host-only programs over csrc/internal.h)."""
 import os
 import shutil
 import subprocess
@@ -37,14 +37,40 @@ int main()
 """
 
 
-def test_a_device_that_comes_later_is_set_up_too(tmp_path):
+ANSWERS = r"""
+#include "internal.h"
+int main()
+{
+    std::atomic<int> known{0};
+    int calls = 0, answer = 0;
+    auto ask = [&] { ++calls; return answer; };
+    if (idx::remembered(known, ask) != 0 || idx::remembered(known, ask) != 0 || calls != 2)
+        return 1;                                        // no answer is not one
+    answer = -152;
+    if (idx::remembered(known, ask) != -152 || calls != 3)
+        return 2;
+    answer = 7;
+    return idx::remembered(known, ask) == -152 && calls == 3 ? 0 : 3;
+}
+"""
+
+
+def run(program, tmp_path):
     include = "/usr/local/cuda/include"
     if shutil.which("g++") is None or not os.path.exists(os.path.join(include, "cuda_runtime.h")):
         pytest.skip("no host compiler or CUDA headers")
     src, exe = tmp_path / "once.cpp", tmp_path / "once"
-    src.write_text(PROGRAM)
+    src.write_text(program)
     subprocess.run(["g++", "-std=c++17", "-I" + CSRC, "-I" + include, str(src), "-o", str(exe)], check=True)
     assert subprocess.run([str(exe)]).returncode == 0
+
+
+def test_a_device_that_comes_later_is_set_up_too(tmp_path):
+    run(PROGRAM, tmp_path)
+
+
+def test_a_device_that_could_not_be_asked_is_asked_again(tmp_path):
+    run(ANSWERS, tmp_path)
 
 
 def test_no_launch_keeps_a_device_attribute_for_the_process():
