@@ -595,6 +595,11 @@ def indexer_attention_create(plan: Plan, Hq: int, Hkv: int, D: int, num_sel: int
                      plan.max_keys)
 
 
+def _packed(t):
+    """Whether a row's elements are neighbours (a single one has any stride)."""
+    return t.stride(1) == 1 or t.shape[1] <= 1
+
+
 def _heads(name: str, t, shape, dtype):
     """Strides of a CUDA tensor of that shape and type (None: e4m3 codes or their bytes)."""
     if t.shape != shape or not t.is_cuda or \
@@ -626,13 +631,13 @@ def indexer_sparse_attention(attn: Attention, q, k, v, sel, compress_len, out, w
     sk = _heads("k", k, attn.kv_shape, kv_type)
     sv = _heads("v", v, attn.kv_shape, kv_type)
     if sel.dtype != torch.int32 or sel.shape != attn.sel_shape or not sel.is_cuda or \
-            sel.stride(1) != 1:
+            not _packed(sel):
         raise ValueError(f"sel: int32 CUDA tensor {attn.sel_shape} expected")
     table = ld_table = 0
     if page_table is not None:
         if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_cuda or \
                 page_table.shape[0] != attn.requests or page_table.shape[1] < attn.pages or \
-                page_table.stride(1) != 1:
+                not _packed(page_table):
             raise ValueError(f"page_table: int32 CUDA tensor [requests, {attn.pages} pages or more] "
                              "expected")
         table = page_table.data_ptr()
@@ -659,7 +664,7 @@ def indexer_mask_blocks(plan: Plan, cand_mask, compress_len, block: int, blocks,
     rows = plan.problem.total_rows
     need = -(-plan.max_keys // block) if block > 0 else 0
     if cand_mask.dtype not in _MASK or not cand_mask.is_cuda or cand_mask.dim() != 2 or \
-            cand_mask.shape[0] != rows or cand_mask.shape[1] < need or cand_mask.stride(1) != 1:
+            cand_mask.shape[0] != rows or cand_mask.shape[1] < need or not _packed(cand_mask):
         raise ValueError(f"cand_mask: CUDA tensor [rows, {need} blocks or more] of bytes or truth values "
                          "expected")
     num_sel, shape = blocks.shape[-1], (rows,)

@@ -95,3 +95,31 @@ def test_masks_of_truth_values_and_of_another_type():
     for kind in (torch.float8_e4m3fn, torch.float8_e5m2):
         with pytest.raises(ValueError, match="cand_mask"):
             K.indexer_mask_blocks(plan, mask.to(torch.uint8).view(kind), lens, 8, a)
+
+
+@pytest.mark.gpu
+def test_a_single_column_of_any_stride():
+    """Lists of one entry, tables of one page and masks of one block taken out of wider tensors."""
+    cu = np.array([0, 1, 2, 3], np.int32)
+    plan = K.indexer_plan(cu, cu * 8, np.full(3, 8, np.int32), 32, 128, 8)
+    a = K.indexer_attention_create(plan, 4, 1, 64, 1, block=8, page_size=8, num_slots=24)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn((3, 4, 64), generator=g, device="cuda").bfloat16()
+    k, v = (torch.randn((24, 1, 64), generator=g, device="cuda").bfloat16() for _ in "kv")
+    lens = torch.full((3,), 8, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(max(a.workspace_bytes, 256), dtype=torch.uint8, device="cuda")
+    table = torch.tensor([[2], [0], [1]], dtype=torch.int32, device="cuda")
+    sel = torch.zeros((3, 1), dtype=torch.int32, device="cuda")
+    want, got = torch.empty_like(q), torch.empty_like(q)
+    K.indexer_sparse_attention(a, q, k, v, sel, lens, want, ws, page_table=table)
+    blocks = torch.empty((3, 1), dtype=torch.int32, device="cuda")
+    wide = torch.ones((3, 4), dtype=torch.uint8, device="cuda")
+    K.indexer_mask_blocks(plan, wide[:, ::2][:, :1], lens, 8, blocks)
+    assert torch.equal(blocks, sel)
+    wide_sel = torch.zeros((3, 6), dtype=torch.int32, device="cuda")
+    wide_sel[:, 1::2] = 99
+    wide_table = torch.full((3, 6), 77, dtype=torch.int32, device="cuda")
+    wide_table[:, :1] = table
+    K.indexer_sparse_attention(a, q, k, v, wide_sel[:, ::2][:, :1], lens, got, ws,
+                               page_table=wide_table[:, ::3][:, :1])
+    assert torch.equal(got, want)
