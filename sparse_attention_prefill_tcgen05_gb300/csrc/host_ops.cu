@@ -277,11 +277,14 @@ int indexer_attention_create(indexer_plan_t plan, const indexer_attention_spec* 
     // tiles.  Where they do not fill the SMs, the tiles of a row are split.  Two or four splits
     // that all run at once are a cluster, which joins them through its shared memory; more are
     // joined from the workspace by a kernel of its own.  The number that ends first by measured
-    // times (32 heads of 128, 16 tiles a row: 64 rows 16.7 us whole, 14.1 in a cluster of 2, 16.3
-    // in 2 with the kernel; 32 rows in 4: 11.5 and 12.6; one row 16.1 whole, 10.2 and 10.5 in 4,
-    // 9.9 in 8; 64 rows of 8 tiles 11.0 whole, 11.3 in a cluster of 2; a cluster of 8 does not run
-    // on all SMs at once: 16 rows 17.5): 0.65 us a tile, 1.2 an item, 2.9 for a cluster's join, 3
-    // for the kernel's and the parts' bytes at 1.5 TB/s.
+    // times: 0.65 us a tile, 2 an item, 1.4 for a cluster's join, 1.1 for the kernel's, 0.15 for each
+    // part of a row and the parts' bytes at 4 TB/s.  Fitted to 231 calls (16, 32 and 64 heads of 128, 8
+    // and 32 of 64, one or four to a cached head, 16-bit and e4m3 caches, both query types; 1 to 200
+    // rows of 4 to 64 tiles), each timed whole, in 2 to 64 parts and in clusters of 2 and 4: the chosen
+    // number takes 0.5 % longer than the best on average, 12 % at most.  (One row of 64 tiles, 32 heads
+    // of 128: 47 us whole, 17.5 in 4, 12.3 in 16, which are chosen, 16.9 in 64.  64 rows of 16 tiles of
+    // e4m3: 13.9 in a cluster of 2, 18.8 whole.)  A cluster of 8 does not run on all SMs at once
+    // (16 rows 17.5 us against 10.4 in four).
     const int nh = attention_heads_per_tile(p.group, s->dtype, s->kv_format != IDX_KV_DENSE);
     p.head_tiles = (p.group + nh - 1) / nh;
     const int64_t tiles = (((int64_t)s->num_sel << p.block_shift) + kAttnTile - 1) / kAttnTile;
@@ -297,9 +300,9 @@ int indexer_attention_create(indexer_plan_t plan, const indexer_attention_spec* 
             continue;
         const double waves = static_cast<double>((items * n + kPlanSms - 1) / kPlanSms);
         const bool cluster = (n == 2 || n == kMaxCluster) && items * n <= kClusterBlocks;
-        const double join =
-            n == 1 ? 0.0 : cluster ? 2.9 : 3.0 + 1e-6 / 1.5 * (items * n) * nh * s->D * 4.0;
-        const double cost = waves * (0.65 * per + 1.2) + join;
+        const double bytes = 4.0 * s->D * nh * (items * n);
+        const double join = n == 1 ? 0.0 : cluster ? 1.4 : 1.1 + 0.15 * n + 1e-6 / 4 * bytes;
+        const double cost = waves * (0.65 * per + 2.0) + join;
         if (cost < best) {
             best = cost;
             p.cluster = cluster;
