@@ -471,7 +471,8 @@ int indexer_rope(indexer_rope_t rope, const void* x, int32_t dtype, int32_t rows
  * one of the key formats:
  *   IDX_K_FP8_E4M3         codes e4m3 [num_slots, heads, D], scales float [num_slots, heads]:
  *                          scale = largest magnitude / 448 (at least 2^-126; 1 for a zero
- *                          vector), code = e4m3(x / scale), ties to even, saturating
+ *                          vector), code = e4m3(x / scale), both quotients in fp32, ties
+ *                          to even, saturating
  *   IDX_K_FP4_E2M1_UE8M0   codes [num_slots, heads, D/2] (element 2i in the low nibble),
  *                          scales ue8m0 [num_slots, heads, D/32]: 2^e with e =
  *                          floor(log2(largest magnitude)) - 2 of the 32 elements (1 for a
@@ -522,9 +523,10 @@ int indexer_page_slots(indexer_plan_t plan, const int32_t* page_table, int64_t l
  *   slot is not below num_slots, are left out.
  * Formats: q and out are dtype (IDX_BF16, IDX_FP16); k and v are of that type
  * (IDX_KV_DENSE) or caches of format IDX_K_FP8_E4M3 with their scales [num_slots, Hkv]
- * (IDX_KV_FP8_E4M3).  Scores, softmax and sums are fp32; the softmax weights enter the product with
- * v with 8 bits of mantissa or more (11 where q is fp16), relative to the
- * row's largest.
+ * (IDX_KV_FP8_E4M3).  Scores, softmax and sums are fp32; the softmax weights (times v's scale) enter
+ * the product with v with 8 significant bits, 11 where q is fp16 (over fp16 keys those below 2^-21 of
+ * the row's largest with fewer, down to 2^-31 of it).  Under bf16 queries values from 2^-84 to 2^80
+ * in size keep those bits in every list.
  *
  * indexer_attention_spec:
  *   Hq, Hkv      query and key/value heads, Hkv divides Hq, Hq <= IDX_MAX_HEADS

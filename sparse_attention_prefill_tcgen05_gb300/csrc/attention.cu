@@ -47,19 +47,26 @@ __device__ __forceinline__ float value(__half v) { return __half2float(v); }
 // through L2 whatever the tiling (2,048 rows x 2,048 keys of 128 bf16: 2.1 GB; only the 64 MB
 // behind them come from HBM once).  cp.async of 16 bytes by a warp per stage moved 21 TB/s alone,
 // gathering TMA 9, plain loads 14.  Around it the roles overlap, each a warp or more of its own:
-// gather (a warp per stage, which also looks up its slots), scores, products, two softmax
-// warpgroups, four warps for queries and outputs, one of each ahead of or behind the others by a
-// tile or an item.  All waits are bounded.  Rows that do not fill the SMs are split over blocks,
-// two or four of them a cluster that joins its parts in shared memory (64 rows over 2,048 e4m3
-// keys, 32 heads: 14.1 us, 8 of them the latency of a single tile).
+// gather (two warps per tile of the ring, which also look up its slots and convert e4m3 values),
+// scores, products, two softmax warpgroups, four warps for queries and outputs, one of each ahead
+// of or behind the others by a tile or an item.  All waits are bounded.  Rows that do not fill the
+// SMs are split over blocks, two or four of them a cluster that joins its parts in shared memory (64
+// rows over 2,048 e4m3 keys, 32 heads: 14.0 us, 8 of them the latency of a single tile).
 //
-// Measured (GB300; item counts fill the SMs): 32 heads of 128 over 2,048 bf16 keys, 2,048 rows
-// 171 us (12.6 TB/s gathered, 402 TFLOP/s), 64 heads 225 us (612 TFLOP/s), 16 heads 138 us; e4m3
-// caches 172, 290 and 126 us; 512 keys of 16,384 rows, 64 heads, e4m3: 0.80 ms.  What bounds it:
-// shared memory at 32 heads (a tile's 64 KB are written once and read by two MMAs: 1,220 of its
-// 1,600 cycles), the softmax warps' chain of waits, exponentials and conversions at 64, the
-// instruction cache throughout (all roles' loops are some 60 KB; at 100 KB a third of the fetches
-// missed and everything took a third longer).
+// Roundings: scores, maxima, sums and outputs are fp32; weights are rounded to bf16 (fp16 under fp16
+// keys, two bf16 terms under fp16 queries over e4m3 caches) because the tensor cores take 16-bit
+// operands at twice tf32's rate and half its bytes in shared memory, which bounds the kernel, and
+// roundings of 2^-8 of a weight at most, of either sign, add up to less than the output's own: over
+// 2,048 x 2,048 bf16 keys it is off by 0.0024 of its size where fp32 weights leave 0.0017, the
+// output's rounding alone.
+//
+// Measured (GB300; items fill the SMs): 32 heads of 128 over 2,048 bf16 keys, 2,048 rows 176 us
+// (12.2 TB/s gathered, 390 TFLOP/s), 64 heads 234 us (587 TFLOP/s), 16 heads 152 us; e4m3 caches 219,
+// 302 and 190 us; 512 keys of 16,384 rows, 64 heads, e4m3: 0.76 ms.  What bounds it: shared memory at
+// 32 heads (a tile's 64 KB are written once and read by two MMAs: 1,220 of its 1,600 cycles; e4m3
+// tiles too, whose values are written twice), the softmax warps' chain of waits, exponentials and
+// conversions at 64, the instruction cache throughout (all roles' loops are some 60 KB; at 100 KB
+// a third of the fetches missed and everything took a third longer).
 
 // Modes: k and v of q's type (bf16 or fp16), or e4m3 caches under bf16 or fp16 queries.
 constexpr int kModeBf16 = 0, kModeFp16 = 1, kModeFp8Bf16 = 2, kModeFp8Fp16 = 3;
@@ -118,8 +125,9 @@ struct AttnCfg {
     static constexpr int kFit =
         (kSmemLimit - kFixed) / (kTileBytes + 2 * kKeyInfo + 8 * 4);
     // Tiles in the ring: three; four where the stages are small and so few heads leave the
-    // softmax's registers free (16 heads, e4m3 124 us against 149 with three; 8 heads of 64 bf16
-    // 132 against 144; but 32 heads, e4m3 236 against 178: two more warps, fewer registers each).
+    // softmax's registers free (16 heads of 128, e4m3 190 us against 193 with three; 8 heads of 64
+    // 103 against 109, e4m3 143 against 155; but 32 heads of 64 143 against 134, e4m3 250 against 187:
+    // two more warps, fewer registers each).
     static constexpr int kMostTiles = NH == 16 && kTileBytes <= 49152 ? 4 : 3;
     static constexpr int kTiles = kFit < kMostTiles ? kFit : kMostTiles;   // tiles in the ring
     static constexpr int kStages = 2 * kTiles;          // and as many warps that fill them
@@ -128,10 +136,9 @@ struct AttnCfg {
     static constexpr int kThreads = 32 * (kMmaWarp + 2);
     // Registers: the softmax warpgroups hold a thread's heads twice over (scores and sums), what
     // feeds them (gather and MMA warps) needs few, so where the block is whole warpgroups they
-    // trade: at 96 each the 32-head loops spilled (64 heads over 2,048 bf16 keys, 2,048 rows: 244
-    // -> 222 us, e4m3 309 -> 290).  What is traded was launched with: 640 threads of 96.  32 heads
-    // take 136 against 56 (171 us; 128 against 64: 176), 16 heads 128 against 64 (138 us; 136
-    // against 56: 146).
+    // trade: at 96 each the 32-head loops spill (e4m3, 32 heads 219 -> 272 us, 64 heads 302 -> 339).
+    // What is traded was launched with: 640 threads of 96.  32 heads take 136 against 56 (176 us; 128
+    // against 64: 180), 16 heads 128 against 64 (152 us; 136 against 56 the same, without 157).
     static constexpr bool kTrade = kThreads == 640;
     static constexpr int kSoftmaxRegs = kHeads == 32 ? 136 : 128;
     static constexpr int kFeedRegs = kHeads == 32 ? 56 : 64;
@@ -201,8 +208,7 @@ __device__ __forceinline__ AttnItem attn_item(const AttnParams& p, int item, int
     return w;
 }
 
-// 16 values of every lane, combined over the warp: lane i ends with value i / 2.  Out of line
-// like wait_on: it runs once per row.
+// 16 values of every lane, combined over the warp: lane i ends with value i / 2.
 template <bool kMax>
 __device__ __forceinline__ float reduce16_of(float v0, float v1, float v2, float v3, float v4,
                                           float v5, float v6, float v7, float v8, float v9,
@@ -302,8 +308,8 @@ __device__ __forceinline__ void add2_scaled(float& a0, float& a1, float b0, floa
 }
 
 // The largest of a warp's values (a NaN gives way): for 32 heads less work than their maxima by
-// shuffles (16,384 rows of 512 e4m3 keys and 64 heads: 4 us of 215), for 16 heads more (170 us
-// against 178).
+// shuffles (64 heads over 2,048 x 2,048 fp16 keys 242 us against 246, 32 over bf16 keys with scores of
+// deviation 16 199 against 207), for 16 as much.
 __device__ __forceinline__ float warp_max(float v)
 {
     float r;
@@ -756,7 +762,7 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                 float* mul = qscale + kScaleItems * NH;  // of a head, by the lanes that read it
                 {
                     // the heads' largest magnitudes, all of their elements asked for at once (a
-                    // vector after another: 215 us against 202 for 4,096 rows of 64 heads)
+                    // vector after another 6 % more: 4,096 rows of 64 heads, 512 keys each)
                     using T2 = typename std::conditional<MODE == kModeFp8Bf16, __nv_bfloat162,
                                                          __half2>::type;
                     constexpr int kIter = (NH * kGroup + 127) / 128;
@@ -905,8 +911,8 @@ attention_tc_kernel(const __grid_constant__ AttnParams p)
                     break;
                 tc_fence_after();
             }
-            // 16 heads at a time, 8 of small groups (8 heads of 64: 143 -> 132 us; 32 of 128 in
-            // eights: 238 -> 254)
+            // 16 heads at a time, 8 of small groups (8 heads of 64: 8 % less; 32 of 128 in
+            // eights 7 % more)
             constexpr int kStep = NH == 16 ? 8 : 16;
             auto load = [](uint32_t at, float* v) {
                 if (kStep == 8)
@@ -1454,7 +1460,8 @@ __device__ __forceinline__ uint32_t nonzero_bytes(uint32_t w)
 
 // One warp per row.  A lane reads 16 mask bytes of each of four runs of 512 at once and counts
 // them; its first set byte's place is the row's count so far plus the lanes' before it.  (A byte
-// a lane with a ballot per 32 bytes waited for memory at every step.)
+// a lane with a ballot per 32 bytes waited for memory at every step.)  16,384 rows of 18,750 blocks:
+// 3.5 TB/s, the walk over set bits between the reads.
 __global__ void __launch_bounds__(128)
 mask_blocks_kernel(const __grid_constant__ MaskBlocksParams p)
 {
@@ -1521,10 +1528,11 @@ mask_blocks_kernel(const __grid_constant__ MaskBlocksParams p)
 int attention_heads_per_tile(int group, int dtype, bool fp8)
 {
     // The smallest tile that holds the group: a wider one computes heads that are none (16 heads in
-    // tiles of 16 138 us, of 32 165; 32 heads of 32 171, of 64 235: 2,048 rows, 2,048 keys of
-    // 128 bf16), a narrower one gathers the keys again for each (32 heads in two of 16 295 us, 64
-    // in two of 32 331 against 225).  fp16 queries over e4m3 caches: two of 32, the terms of 64
-    // leave room for two tiles and too few registers (541 us against 459).
+    // tiles of 16 153 us, of 32 168; 32 heads of 32 176, of 64 226: 2,048 rows, 2,048 keys of
+    // 128 bf16; e4m3 190, 217, 219, 298), a narrower one gathers the keys again for each (32 heads in two
+    // of 16 298 us, 64 in two of 32 337 against 236; e4m3 361 and 419 against 302).  fp16 queries over
+    // e4m3 caches: two of 32, the terms of 64 leave room for two tiles and too few registers (541
+    // us against 476).
     if (fp8 && dtype == IDX_FP16)
         return group <= 16 ? 16 : 32;
     return group <= 16 ? 16 : group <= 32 ? 32 : 64;
