@@ -609,6 +609,122 @@ int indexer_mask_blocks(indexer_plan_t plan, const uint8_t* cand_mask, int64_t l
                         const int32_t* compress_len, int32_t block, int32_t* blocks,
                         int32_t num_sel, int32_t* count, void* stream);
 
+/* --------------------------------------------------------------- cache append
+ * New keys and values of a batch into their caches, the keys rotated on the way, in one launch:
+ * for row t with position p = positions[t]
+ *     k_cache[slot] = k[t] turned by rope to position p (rope NULL: as it is),  v_cache[slot] = v[t]
+ * rounded once to the cache's type, or (cache_dtype IDX_CODES) as codes and scales of format
+ * IDX_K_FP8_E4M3, exactly as indexer_cache_write stores them.
+ *   slot = slots[t] where slots is given (the plan may then be NULL, positions too without rope);
+ *   else that of key p of the row's request: page_table[r, p / page_size] * page_size +
+ *   p % page_size with page_size > 0, the packed key cu_seqlens_k[r] + p without.
+ * Rows whose position is not a key of the request (0 <= p < its key count), whose page is unmapped
+ * (a negative entry) or whose slot is not in [0, num_slots) are skipped: the caches stay as they
+ * are.  No two rows of a call may name the same slot.
+ *   k, v              [rows, heads, D] of dtype IDX_BF16, IDX_FP16 or IDX_FP32, strides in elements
+ *                     (last axis contiguous, none negative); rows: the plan's, where there is one
+ *   k_cache, v_cache  [num_slots, heads, D] of cache_dtype: dtype itself (any of the two 16-bit types
+ *                     for IDX_FP32), or IDX_CODES: e4m3 codes (D a multiple of 32, 8-byte aligned
+ *                     rows and heads) with k_scale, v_scale float [num_slots, heads] packed.  Strides
+ *                     in elements, slots and heads at least D apart: two halves of one tensor will do
+ *   D                 1..256 (with rope: rope's)
+ */
+typedef struct indexer_append_io {
+    const void* k;
+    const void* v;
+    void* k_cache;
+    void* v_cache;
+    float* k_scale;
+    float* v_scale;
+    const int32_t* positions;
+    const int32_t* slots;
+    const int32_t* page_table;
+    int64_t k_row, k_head;
+    int64_t v_row, v_head;
+    int64_t kc_slot, kc_head;
+    int64_t vc_slot, vc_head;
+    int64_t ld_page_table;
+    int32_t rows;
+    int32_t heads;
+    int32_t D;
+    int32_t dtype;
+    int32_t cache_dtype;
+    int32_t num_slots;
+    int32_t page_size;
+} indexer_append_io;
+
+int indexer_cache_append(indexer_plan_t plan, indexer_rope_t rope, const indexer_append_io* io,
+                         void* stream);
+
+/* ------------------------------------------------------ attention parts joined
+ * Attention over disjoint sets of keys as one: of `parts` outputs and log-sum-exps of the same rows
+ * (indexer_sparse_attention's and indexer_causal_attention's, say)
+ *     lse[t,h] = log(sum_p exp(lse_p[t,h]) + exp(sink[h])),
+ *     out[t,h,:] = sum_p exp(lse_p[t,h] - lse[t,h]) out_p[t,h,:]
+ * in fp32 with one rounding.  sink float [heads]: a learned logit of attending to nothing (NULL: none).
+ * A part whose lse is -inf takes no part, whatever its output holds; where all are, and there is no
+ * sink, out = 0 and lse = -inf.
+ *   part[p]      [rows, heads, D] of part_dtype, strides in elements (last axis contiguous);
+ *   part_lse[p]  float [rows, heads] packed
+ *   out          [rows, heads, D] of out_dtype: part_dtype, or any type over IDX_FP32 parts; may be
+ *                one of the parts with its strides, else it overlaps none
+ *   lse          float [rows, heads] packed, or NULL; may be one of the parts'
+ *   D            1..256; rows * heads below 2^31
+ */
+#define IDX_MAX_PARTS 8
+
+typedef struct indexer_join_io {
+    const void* part[IDX_MAX_PARTS];
+    const float* part_lse[IDX_MAX_PARTS];
+    int64_t part_row[IDX_MAX_PARTS];
+    int64_t part_head[IDX_MAX_PARTS];
+    void* out;
+    float* lse;
+    const float* sink;
+    int64_t out_row, out_head;
+    int32_t parts;
+    int32_t rows;
+    int32_t heads;
+    int32_t D;
+    int32_t part_dtype;
+    int32_t out_dtype;
+} indexer_join_io;
+
+int indexer_attention_join(const indexer_join_io* io, void* stream);
+
+/* ------------------------------------------------------------------- RMS norm
+ *     h = x + residual,   y = h / sqrt(mean(h^2) + eps) * weight
+ * per row of n elements (1..65,536), in fp32 (so the squares of a row have to be within its range);
+ * h is rounded where it is stored (total), y where it is (out), and its codes are those of the
+ * unrounded y: e4m3, a scale for every `group` elements, as format IDX_K_FP8_E4M3 has them (largest
+ * magnitude / 448; NaN as 0, an infinity as the largest code).
+ *   x, residual, total, out  [rows, n] of dtype IDX_BF16, IDX_FP16 or IDX_FP32, rows `_row` elements
+ *                 apart (outputs at least n); residual may be NULL (h = x), total and out too.  total
+ *                 may be residual or x, out may be x (with the same strides); no other overlap
+ *   weight        [n] of weight_dtype: dtype or IDX_FP32 (NULL: ones)
+ *   codes         [rows, n] packed, or NULL; scales float [rows, n / group] packed
+ *   group         32, 64, 128 or 256, a divisor of n, or n itself (one scale a row)
+ *   eps           >= 0
+ */
+typedef struct indexer_norm_io {
+    const void* x;
+    const void* residual;
+    const void* weight;
+    void* total;
+    void* out;
+    uint8_t* codes;
+    float* scales;
+    int64_t x_row, residual_row, total_row, out_row;
+    int32_t rows;
+    int32_t n;
+    int32_t group;
+    int32_t dtype;
+    int32_t weight_dtype;
+    float eps;
+} indexer_norm_io;
+
+int indexer_rms_norm(const indexer_norm_io* io, void* stream);
+
 const char* indexer_error_string(int status);
 int indexer_version(void);
 

@@ -41,6 +41,7 @@ IDX_ROPE_HALF = 0
 IDX_ROPE_INTERLEAVED = 1
 IDX_KV_DENSE = 0
 IDX_KV_FP8_E4M3 = 1
+IDX_MAX_PARTS = 8
 
 EXPORTED = ("indexer_plan", "indexer_plan_destroy", "indexer_plan_info", "indexer_logits",
             "indexer_topk", "indexer_fused_topk", "indexer_candidate_blocks",
@@ -52,7 +53,8 @@ EXPORTED = ("indexer_plan", "indexer_plan_destroy", "indexer_plan_info", "indexe
             "indexer_noalloc_status", "indexer_rope_create", "indexer_rope_destroy",
             "indexer_rope", "indexer_cache_write", "indexer_cache_read", "indexer_page_slots",
             "indexer_attention_create", "indexer_attention_destroy", "indexer_sparse_attention",
-            "indexer_mask_blocks")
+            "indexer_mask_blocks", "indexer_cache_append", "indexer_attention_join",
+            "indexer_rms_norm")
 IDX_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -103,6 +105,10 @@ class _AttentionIo(ctypes.Structure):
 
 # the same layout, packed in one go: eleven addresses, ten strides
 _ATTENTION_IO = struct.Struct("11P10q").pack
+# indexer_append_io, indexer_join_io and indexer_norm_io
+_APPEND_IO = struct.Struct("9P9q7i").pack
+_JOIN_IO = struct.Struct("16P16q3P2q6i").pack
+_NORM_IO = struct.Struct("7P4q5if").pack
 
 _lib = None
 _C = torch._C
@@ -158,6 +164,9 @@ def lib():
         L.indexer_attention_destroy.restype = None
         L.indexer_sparse_attention.argtypes = [P, P, P, sz, P]
         L.indexer_mask_blocks.argtypes = [P, P, i64, P, i32, P, i32, P, P]
+        L.indexer_cache_append.argtypes = [P, P, P, P]
+        L.indexer_attention_join.argtypes = [P, P]
+        L.indexer_rms_norm.argtypes = [P, P]
         L.indexer_error_string.argtypes = [i32]
         L.indexer_error_string.restype = ctypes.c_char_p
         for name in EXPORTED:
@@ -676,3 +685,162 @@ def indexer_mask_blocks(plan: Plan, cand_mask, compress_len, block: int, blocks,
     if rc != IDX_OK:
         raise IndexerError("indexer_mask_blocks", rc)
     return blocks
+
+
+def _cache_rows(name: str, t, shape, dtype):
+    """Strides of a cache of [num_slots, heads, D] elements (dtype None: e4m3 codes or bytes)."""
+    if t.dim() != 3 or t.shape[1:] != shape or not t.is_cuda or \
+            (t.dtype not in _E4M3 if dtype is None else t.dtype != dtype):
+        raise ValueError(f"{name}: CUDA tensor [num_slots, {shape[0]}, {shape[1]}] of "
+                         f"{dtype or 'e4m3 codes'} expected")
+    st = t.stride()
+    if st[2] != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: a contiguous last axis expected")
+    # a single slot's or head's stride says nothing
+    return st[0] if t.shape[0] > 1 else shape[0] * shape[1], st[1] if shape[0] > 1 else shape[1]
+
+
+def indexer_cache_append(plan: Optional[Plan], k, v, k_cache, v_cache, positions,
+                         rope: Optional[Rope] = None, page_table=None, page_size: int = 0,
+                         slots=None, k_scale=None, v_scale=None, stream=None):
+    """Write the batch's new ``k`` (turned by ``rope``) and ``v`` [rows, heads, D] into their caches
+    [num_slots, heads, D]: of a 16-bit type, or e4m3 codes with ``k_scale`` and ``v_scale``
+    [num_slots, heads].  Row t goes to its request's key ``positions[t]`` (int32 [rows]), through
+    ``page_table`` [requests, pages] with ``page_size`` > 0, or to ``slots[t]``."""
+    code, sk = _dense("k", k)
+    vcode, sv = _dense("v", v)
+    shape = k.shape
+    rows, heads, D = shape
+    if vcode != code or v.shape != shape:
+        raise ValueError("v: a tensor of k's shape and type expected")
+    if k_scale is None and v_scale is None:
+        kind = k_cache.dtype
+        cache_code = _DTYPES.get(kind, -1)
+    else:
+        kind, cache_code = None, IDX_CODES
+    num_slots = k_cache.shape[0]
+    kc, vc = _cache_rows("k_cache", k_cache, shape[1:], kind), \
+        _cache_rows("v_cache", v_cache, shape[1:], kind)
+    if v_cache.shape[0] != num_slots:
+        raise ValueError("v_cache: as many slots as k_cache expected")
+    if cache_code == IDX_CODES and (k_scale is None or v_scale is None):
+        raise ValueError("k_scale and v_scale: both or none expected")
+    scales = (num_slots, heads)
+    table = ld_table = 0
+    if page_size > 0 and slots is None:
+        if plan is None or page_table is None:
+            raise ValueError("page_size: a plan and its page_table expected")
+        requests, pages = plan.problem.num_requests, -(-plan.max_keys // page_size)
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_cuda or \
+                page_table.shape[0] != requests or page_table.shape[1] < pages or \
+                not _packed(page_table):
+            raise ValueError(f"page_table: int32 CUDA tensor [requests, {pages} pages or more] "
+                             "expected")
+        table = page_table.data_ptr()
+        ld_table = page_table.stride(0) if requests > 1 else page_table.shape[1]
+    elif page_table is not None and slots is None:
+        raise ValueError("page_table: a page_size expected")
+    io = _APPEND_IO(
+        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        _f32("k_scale", k_scale, scales), _f32("v_scale", v_scale, scales),
+        _i32("positions", positions, (rows,)) or 0, _i32("slots", slots, (rows,)) or 0, table,
+        sk[0], sk[1], sv[0], sv[1], kc[0], kc[1], vc[0], vc[1], ld_table, rows, heads, D, code,
+        cache_code, num_slots, page_size)
+    rc = (_lib or lib()).indexer_cache_append(
+        None if plan is None else plan.handle, None if rope is None else rope.handle, io,
+        _stream(stream))
+    if rc != IDX_OK:
+        raise IndexerError("indexer_cache_append", rc)
+
+
+_NO_PARTS = (0,) * IDX_MAX_PARTS
+
+
+def indexer_attention_join(outs, lses, out=None, lse=None, sink=None, stream=None):
+    """Join attention outputs ``outs`` [rows, heads, D] over disjoint keys by their log-sum-exps
+    ``lses`` (fp32 [rows, heads]) into ``out`` (default: a new tensor of their type; may be one of
+    them) and ``lse``; ``sink`` fp32 [heads]: the logit of attending to nothing."""
+    n = len(outs)
+    if n < 1 or n > IDX_MAX_PARTS or len(lses) != n:
+        raise ValueError(f"outs, lses: 1 to {IDX_MAX_PARTS} parts each expected")
+    first = outs[0]
+    shape, dtype = first.shape, first.dtype
+    code, _ = _dense("outs", first)
+    rows, heads, D = shape
+    if out is None:
+        out = _new(stream, torch.empty, shape, dtype=dtype, device=first.device)
+    ocode, so = _dense("out", out)
+    if out.shape != shape:
+        raise ValueError(f"out: [{rows}, {heads}, {D}] expected")
+    parts, part_lses, row, head = [], [], [], []
+    for o, l in zip(outs, lses):
+        st = _dense("outs", o)[1]
+        if o.shape != shape or o.dtype != dtype:
+            raise ValueError("outs: tensors of one shape and type expected")
+        parts.append(o.data_ptr())
+        if l is None:
+            raise ValueError("lses: a log-sum-exp for every part expected")
+        part_lses.append(_f32("lses", l, shape[:2]))
+        row.append(st[0])
+        head.append(st[1])
+    pad = _NO_PARTS[n:]
+    io = _JOIN_IO(*parts, *pad, *part_lses, *pad, *row, *pad, *head, *pad, out.data_ptr(),
+                  _f32("lse", lse, shape[:2]), _f32("sink", sink, (heads,)),
+                  so[0] if rows > 1 else max(so[0], D), so[1] if heads > 1 else max(so[1], D),
+                  n, rows, heads, D, code, ocode)
+    rc = (_lib or lib()).indexer_attention_join(io, _stream(stream))
+    if rc != IDX_OK:
+        raise IndexerError("indexer_attention_join", rc)
+    return out
+
+
+def _matrix(name: str, t, shape, dtype):
+    """Address and row stride of a CUDA matrix with neighbouring elements (0, 0: none)."""
+    if t is None:
+        return 0, 0
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
+        raise ValueError(f"{name}: CUDA tensor {tuple(shape)} of {dtype} expected")
+    if not _packed(t):
+        raise ValueError(f"{name}: a contiguous last axis expected")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+
+
+def indexer_rms_norm(x, weight=None, eps: float = 1e-6, residual=None, total=None, out=None,
+                     codes=None, scales=None, stream=None):
+    """Norm of ``x`` [rows, n] (plus ``residual``, the sum into ``total``) times ``weight`` [n] into
+    ``out`` (default: a new tensor, unless ``codes`` are asked for) and, as e4m3, into ``codes``
+    [rows, n] with ``scales`` fp32 [rows, n / group].  Returns ``out``."""
+    shape, dtype = x.shape, x.dtype
+    code = _DTYPES.get(dtype)
+    if code is None or len(shape) != 2:
+        raise ValueError("x: 2-d bf16, fp16 or fp32 CUDA tensor expected")
+    rows, n = shape
+    px, sx = _matrix("x", x, shape, dtype)
+    pr, sr = _matrix("residual", residual, shape, dtype)
+    pt, st = _matrix("total", total, shape, dtype)
+    if out is None and codes is None:
+        out = _new(stream, torch.empty, shape, dtype=dtype, device=x.device)
+    po, so = _matrix("out", out, shape, dtype)
+    pw, wcode = 0, code
+    if weight is not None:
+        wcode = _DTYPES.get(weight.dtype, -1)
+        if weight.shape != shape[1:] or not weight.is_cuda or not weight.is_contiguous():
+            raise ValueError(f"weight: contiguous CUDA tensor ({n},) expected")
+        pw = weight.data_ptr()
+    pc = ps = group = 0
+    if codes is not None:
+        if codes.dtype not in _E4M3 or codes.shape != shape or not codes.is_cuda or \
+                not codes.is_contiguous():
+            raise ValueError(f"codes: contiguous CUDA tensor {tuple(shape)} of e4m3 codes expected")
+        if scales is None or scales.dim() != 2 or scales.shape[1] < 1 or n % scales.shape[1] != 0:
+            raise ValueError("scales: fp32 CUDA tensor [rows, n / group] expected")
+        group = n // scales.shape[1]
+        pc, ps = codes.data_ptr(), _f32("scales", scales, (rows, n // group))
+    elif scales is not None:
+        raise ValueError("scales: codes expected")
+    rc = (_lib or lib()).indexer_rms_norm(
+        _NORM_IO(px, pr, pw, pt, po, pc, ps, sx, sr, st, so, rows, n, group, code, wcode, eps),
+        _stream(stream))
+    if rc != IDX_OK:
+        raise IndexerError("indexer_rms_norm", rc)
+    return out

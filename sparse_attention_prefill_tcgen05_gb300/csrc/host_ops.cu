@@ -431,4 +431,176 @@ int indexer_mask_blocks(indexer_plan_t plan, const uint8_t* cand_mask, int64_t l
     return finish(launch_mask_blocks(p, static_cast<cudaStream_t>(stream)));
 }
 
+int indexer_cache_append(indexer_plan_t plan, indexer_rope_t rope, const indexer_append_io* io,
+                         void* stream)
+{
+    if (!io || !dense_type(io->dtype) || io->rows < 0 || io->heads < 1 ||
+        io->heads > IDX_MAX_HEADS || io->D < 1 || io->D > kMaxHeadDim || io->num_slots < 0 ||
+        io->page_size < 0 || (rope && rope->D != io->D) ||
+        (io->cache_dtype != IDX_BF16 && io->cache_dtype != IDX_FP16 &&
+         io->cache_dtype != IDX_CODES) ||
+        (io->dtype != IDX_FP32 && io->cache_dtype != IDX_CODES && io->cache_dtype != io->dtype) ||
+        (io->cache_dtype == IDX_CODES && io->D % 32 != 0) || io->k_row < 0 || io->k_head < 0 ||
+        io->v_row < 0 || io->v_head < 0 || io->kc_slot < 0 || io->kc_head < 0 ||
+        io->vc_slot < 0 || io->vc_head < 0 || (!plan && !io->slots))
+        return IDX_ERR_INVALID_ARG;
+    const bool fp8 = io->cache_dtype == IDX_CODES;
+    const size_t eb = type_bytes(io->dtype);
+    if (io->rows > 0 &&
+        (!io->k || !io->v || ((rope || !io->slots) && !io->positions) || !is_aligned(io->k, eb) ||
+         !is_aligned(io->v, eb) || !is_aligned(io->positions, 4) || !is_aligned(io->slots, 4) ||
+         !is_aligned(io->page_table, 4) || !is_aligned(io->k_scale, 4) ||
+         !is_aligned(io->v_scale, 4)))
+        return IDX_ERR_INVALID_ARG;
+    if (io->rows > 0 && io->num_slots > 0 &&
+        (!io->k_cache || !io->v_cache || !is_aligned(io->k_cache, fp8 ? 8 : 2) ||
+         !is_aligned(io->v_cache, fp8 ? 8 : 2) || (fp8 && (!io->k_scale || !io->v_scale)) ||
+         (io->heads > 1 && (io->kc_head < io->D || io->vc_head < io->D)) ||
+         (io->num_slots > 1 && (io->kc_slot < io->D || io->vc_slot < io->D)) ||
+         (fp8 && (io->kc_slot % 8 != 0 || io->kc_head % 8 != 0 || io->vc_slot % 8 != 0 ||
+                  io->vc_head % 8 != 0))))
+        return IDX_ERR_INVALID_ARG;
+    AppendCall c;
+    std::memset(&c, 0, sizeof(c));
+    if (plan) {
+        const PlanView v = plan_view(plan);
+        if (io->rows != v.T)
+            return IDX_ERR_INVALID_ARG;
+        if (!io->slots && io->page_size > 0 && io->rows > 0 &&
+            (!io->page_table ||
+             io->ld_page_table < (v.max_L + (int64_t)io->page_size - 1) / io->page_size))
+            return IDX_ERR_INVALID_ARG;
+        c.num_requests = v.R;
+        std::copy(v.row_begin, v.row_begin + v.R + 1, c.row_begin);
+        std::copy(v.key_begin, v.key_begin + v.R + 1, c.key_begin);
+    }
+    if (!device_supported())
+        return IDX_ERR_UNSUPPORTED;
+    if (io->rows == 0 || io->num_slots == 0)
+        return IDX_OK;
+    RopeParams rp;
+    if (rope)
+        rp = rope->p;
+    else
+        std::memset(&rp, 0, sizeof(rp));
+    c.k = io->k;
+    c.v = io->v;
+    c.k_cache = io->k_cache;
+    c.v_cache = io->v_cache;
+    c.k_scale = io->k_scale;
+    c.v_scale = io->v_scale;
+    c.positions = io->positions;
+    c.slots = io->slots;
+    c.table = io->page_table;
+    c.k_row = io->k_row;
+    c.k_head = io->k_head;
+    c.v_row = io->v_row;
+    c.v_head = io->v_head;
+    c.kc_slot = io->kc_slot;
+    c.kc_head = io->kc_head;
+    c.vc_slot = io->vc_slot;
+    c.vc_head = io->vc_head;
+    c.ld_table = io->ld_page_table;
+    c.rows = io->rows;
+    c.heads = io->heads;
+    c.D = io->D;
+    c.dtype = io->dtype;
+    c.cache_dtype = io->cache_dtype;
+    c.num_slots = io->num_slots;
+    c.page = io->page_size;
+    count_launch();
+    return finish(launch_append(rp, c, static_cast<cudaStream_t>(stream)));
+}
+
+int indexer_attention_join(const indexer_join_io* io, void* stream)
+{
+    if (!io || io->parts < 1 || io->parts > IDX_MAX_PARTS || io->rows < 0 || io->heads < 1 ||
+        io->heads > IDX_MAX_HEADS || io->D < 1 || io->D > kMaxHeadDim ||
+        !dense_type(io->part_dtype) || !dense_type(io->out_dtype) ||
+        (io->part_dtype != IDX_FP32 && io->out_dtype != io->part_dtype) || io->out_row < 0 ||
+        io->out_head < 0 || (int64_t)io->rows * io->heads > INT32_MAX)
+        return IDX_ERR_INVALID_ARG;
+    JoinCall c;
+    std::memset(&c, 0, sizeof(c));
+    for (int p = 0; p < io->parts; ++p) {
+        if (io->part_row[p] < 0 || io->part_head[p] < 0 ||
+            (io->rows > 0 && (!io->part[p] || !io->part_lse[p] ||
+                              !is_aligned(io->part[p], type_bytes(io->part_dtype)) ||
+                              !is_aligned(io->part_lse[p], 4))))
+            return IDX_ERR_INVALID_ARG;
+        c.part[p] = io->part[p];
+        c.part_lse[p] = io->part_lse[p];
+        c.part_row[p] = io->part_row[p];
+        c.part_head[p] = io->part_head[p];
+    }
+    if (io->rows > 0 &&
+        (!io->out || !is_aligned(io->out, type_bytes(io->out_dtype)) || !is_aligned(io->lse, 4) ||
+         !is_aligned(io->sink, 4) || (io->heads > 1 && io->out_head < io->D) ||
+         (io->rows > 1 && io->out_row < io->D)))
+        return IDX_ERR_INVALID_ARG;
+    if (!device_supported())
+        return IDX_ERR_UNSUPPORTED;
+    if (io->rows == 0)
+        return IDX_OK;
+    c.out = io->out;
+    c.lse = io->lse;
+    c.sink = io->sink;
+    c.out_row = io->out_row;
+    c.out_head = io->out_head;
+    c.parts = io->parts;
+    c.rows = io->rows;
+    c.heads = io->heads;
+    c.D = io->D;
+    c.part_dtype = io->part_dtype;
+    c.out_dtype = io->out_dtype;
+    count_launch();
+    return finish(launch_join(c, static_cast<cudaStream_t>(stream)));
+}
+
+int indexer_rms_norm(const indexer_norm_io* io, void* stream)
+{
+    if (!io || !dense_type(io->dtype) || io->rows < 0 || io->n < 1 || io->n > kMaxNorm ||
+        !(io->eps >= 0.0f) || !std::isfinite(io->eps) ||
+        (io->weight && io->weight_dtype != io->dtype && io->weight_dtype != IDX_FP32) ||
+        io->x_row < 0 || io->residual_row < 0 || io->total_row < 0 || io->out_row < 0)
+        return IDX_ERR_INVALID_ARG;
+    if (io->codes && io->group != io->n &&
+        ((io->group != 32 && io->group != 64 && io->group != 128 && io->group != 256) ||
+         io->n % io->group != 0))
+        return IDX_ERR_INVALID_ARG;
+    const size_t eb = type_bytes(io->dtype);
+    if (io->rows > 0 &&
+        (!io->x || (!io->residual && io->total) || (!io->out && !io->codes && !io->total) ||
+         !is_aligned(io->x, eb) || !is_aligned(io->residual, eb) ||
+         !is_aligned(io->total, eb) || !is_aligned(io->out, eb) ||
+         !is_aligned(io->weight, type_bytes(io->weight_dtype)) ||
+         (io->codes && (!io->scales || !is_aligned(io->scales, 4))) ||
+         (io->rows > 1 && ((io->total && io->total_row < io->n) ||
+                           (io->out && io->out_row < io->n)))))
+        return IDX_ERR_INVALID_ARG;
+    if (!device_supported())
+        return IDX_ERR_UNSUPPORTED;
+    if (io->rows == 0)
+        return IDX_OK;
+    const NormCall c{io->x,
+                     io->residual,
+                     io->weight,
+                     io->total,
+                     io->out,
+                     io->codes,
+                     io->scales,
+                     io->x_row,
+                     io->residual_row,
+                     io->total_row,
+                     io->out_row,
+                     io->rows,
+                     io->n,
+                     io->group,
+                     io->dtype,
+                     io->dtype == IDX_FP32 || io->weight_dtype == IDX_FP32,
+                     io->eps};
+    count_launch();
+    return finish(launch_norm(c, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -390,6 +390,30 @@ struct CacheWriteCall {
 };
 cudaError_t launch_cache_write(const RopeParams& rp, const CacheWriteCall& c, cudaStream_t st);
 
+// k and v [rows, heads, D], k rotated (rp.rot > 0), into slots of their caches: slots[i], or (nullptr)
+// that of key positions[i] of row i's request through its page table (page > 0) or among the packed
+// keys.  Keys outside the request, unmapped pages and slots outside [0, num_slots) are skipped.
+struct AppendCall {
+    const void* k;
+    const void* v;
+    void* k_cache;
+    void* v_cache;
+    float* k_scale;              // [num_slots, heads] (e4m3)
+    float* v_scale;
+    const int32_t* positions;
+    const int32_t* slots;
+    const int32_t* table;
+    int64_t k_row, k_head, v_row, v_head;           // strides in elements
+    int64_t kc_slot, kc_head, vc_slot, vc_head;
+    int64_t ld_table;
+    int32_t rows, heads, D, dtype;
+    int32_t cache_dtype;         // IDX_BF16, IDX_FP16, or IDX_CODES: e4m3
+    int32_t num_slots, page, num_requests;
+    int32_t row_begin[kMaxRequests + 1];
+    int32_t key_begin[kMaxRequests + 1];
+};
+cudaError_t launch_append(const RopeParams& rp, const AppendCall& c, cudaStream_t st);
+
 // Cache rows slots[i] (nullptr: i), i < rows: as values of out_dtype, or (out_dtype
 // IDX_CODES) as codes and scales.  Rows of slots outside the cache read as zeros.
 struct CacheReadCall {
@@ -469,6 +493,37 @@ struct AttnParams {
 // Query heads of one key/value head that a work item takes together.
 int attention_heads_per_tile(int group, int dtype, bool fp8);
 cudaError_t launch_attention(const AttnParams& p, int D, int dtype, bool fp8, cudaStream_t st);
+
+// Attention over disjoint sets of keys, joined by their log-sum-exps.
+constexpr int kMaxParts = 8;
+struct JoinCall {
+    const void* part[kMaxParts];
+    const float* part_lse[kMaxParts];               // [rows, heads]
+    int64_t part_row[kMaxParts], part_head[kMaxParts];   // strides in elements
+    void* out;
+    float* lse;                  // nullable
+    const float* sink;           // [heads], nullable
+    int64_t out_row, out_head;
+    int32_t parts, rows, heads, D;
+    int32_t part_dtype, out_dtype;
+};
+cudaError_t launch_join(const JoinCall& c, cudaStream_t st);
+
+// Rows divided by their root mean square, times a weight.
+constexpr int kMaxNorm = 65536;     // elements of a row
+struct NormCall {
+    const void* x;
+    const void* residual;        // nullable
+    const void* weight;          // nullable: ones
+    void* total;                 // x + residual, nullable
+    void* out;                   // nullable
+    uint8_t* codes;              // [rows, n] e4m3, nullable
+    float* scales;               // [rows, n / group]
+    int64_t x_row, residual_row, total_row, out_row;     // strides in elements
+    int32_t rows, n, group, dtype, weight_fp32;
+    float eps;
+};
+cudaError_t launch_norm(const NormCall& c, cudaStream_t st);
 
 struct MaskBlocksParams {
     const uint8_t* mask;

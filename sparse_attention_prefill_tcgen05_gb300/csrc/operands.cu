@@ -11,6 +11,7 @@
 #include <cuda_fp8.h>
 
 #include "indexer.h"
+#include "elements.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -18,59 +19,7 @@ namespace idx {
 namespace {
 
 constexpr int kThreads = 256;
-
-// ------------------------------------------------------------------ element types
-
-template <typename T>
-struct Elt;
-template <>
-struct Elt<__nv_bfloat16> {
-    static __device__ __forceinline__ float load(__nv_bfloat16 v) { return __bfloat162float(v); }
-    static __device__ __forceinline__ __nv_bfloat16 store(float v) { return __float2bfloat16(v); }
-};
-template <>
-struct Elt<__half> {
-    static __device__ __forceinline__ float load(__half v) { return __half2float(v); }
-    static __device__ __forceinline__ __half store(float v) { return __float2half(v); }
-};
-template <>
-struct Elt<float> {
-    static __device__ __forceinline__ float load(float v) { return v; }
-    static __device__ __forceinline__ float store(float v) { return v; }
-};
-
-// Eight elements at p (16-byte aligned), to fp32, and back with one rounding.
-template <typename T>
-struct Eight {
-    uint4 w[sizeof(T) / 2];
-    __device__ __forceinline__ void load(const T* p)
-    {
-#pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
-            w[i] = reinterpret_cast<const uint4*>(p)[i];
-    }
-    __device__ __forceinline__ void values(float (&v)[8]) const
-    {
-        const T* e = reinterpret_cast<const T*>(w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = Elt<T>::load(e[i]);
-    }
-};
-
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&v)[8])
-{
-    constexpr int n = sizeof(T) / 2;
-    uint4 w[n];
-    T* e = reinterpret_cast<T*>(w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        e[i] = Elt<T>::store(v[i]);
-#pragma unroll
-    for (int i = 0; i < n; ++i)
-        reinterpret_cast<uint4*>(p)[i] = w[i];
-}
+constexpr int kAppendRows = 1024;   // rows of a block: kThreads / 2 groups of eight vectors at most
 
 // Cosine and sine (times the amplitude) of a pair's turn at a position.  position * inc
 // modulo 2^64 is the angle in 2^-64 turns, exactly; its top 32 bits are a quarter turn q and
@@ -115,21 +64,25 @@ struct Unit {
     bool rotated;
 };
 
-__device__ __forceinline__ Unit unit_of(const RopeParams& rp, int u, int D)
+__device__ __forceinline__ Unit unit_of(int rot, int offset, int interleaved, int u, int D)
 {
     Unit r;
-    const int nrot = rp.rot / 16;
+    const int nrot = rot / 16;
     r.rotated = u < nrot;
     if (r.rotated) {
-        r.a = rp.offset + (rp.interleaved ? 16 * u : 8 * u);
-        r.b = rp.interleaved ? r.a + 8 : r.a + rp.rot / 2;
+        r.a = offset + (interleaved ? 16 * u : 8 * u);
+        r.b = interleaved ? r.a + 8 : r.a + rot / 2;
     } else {
-        const int rest = D - rp.rot;
+        const int rest = D - rot;
         const int e = 8 * (u - nrot), f = e + (rest + 15) / 16 * 8;   // among those left alone
-        r.a = e < rp.offset ? e : e + rp.rot;
-        r.b = f >= rest ? -1 : f < rp.offset ? f : f + rp.rot;
+        r.a = e < offset ? e : e + rot;
+        r.b = f >= rest ? -1 : f < offset ? f : f + rot;
     }
     return r;
+}
+__device__ __forceinline__ Unit unit_of(const RopeParams& rp, int u, int D)
+{
+    return unit_of(rp.rot, rp.offset, rp.interleaved, u, D);
 }
 
 // What a block of the kernels below does: vectors (row, head) of up to `rows` rows and
@@ -175,30 +128,6 @@ __device__ __forceinline__ void block_angles(const RopeParams& rp, const Tiling&
         o[r * 2 * pairs] = v.x;
         o[r * 2 * pairs + 2] = v.y;
     }
-}
-
-// Two fp32 values in a 64-bit register: one instruction for both.
-__device__ __forceinline__ uint64_t pack(float x, float y)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ void unpack(uint64_t v, float& x, float& y)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
 }
 
 // A unit's 16 elements turned by its eight angles (`cs`: the row's, u: the unit).
@@ -317,59 +246,11 @@ rope_any_kernel(const __grid_constant__ RopeParams rp, const __grid_constant__ R
 
 // --------------------------------------------------------------------- quantisation
 
-// The largest magnitude of eight values.  NaN becomes 0, since the indexer takes no NaN codes:
-// the maximum that passes a NaN on shows whether there is one, so values without any pay one
-// compare instead of sixteen instructions.
-__device__ __forceinline__ float largest(float (&v)[8])
-{
-    float m = fabsf(v[0]);
-#pragma unroll
-    for (int i = 1; i < 7; i += 2)
-        asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(v[i])), "f"(fabsf(v[i + 1])));
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[7])));
-    if (m == m)
-        return m;
-    m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[i] = v[i] == v[i] ? v[i] : 0.0f;
-        m = fmaxf(m, fabsf(v[i]));
-    }
-    return m;
-}
-
 // The largest of four groups.
 __device__ __forceinline__ float largest4(const float* groups)
 {
     const float4 g = *reinterpret_cast<const float4*>(groups);
     return fmaxf(fmaxf(g.x, g.y), fmaxf(g.z, g.w));
-}
-
-// e4m3 codes of eight values over `scale` (saturating, ties to even).  The quotient is the fp32 one:
-// x inv, inv the rounded reciprocal, less what that is too much (Markstein's theorem: a faithful
-// quotient and a correctly rounded reciprocal give the correctly rounded quotient; the signs keep
-// that of a zero).  x inv alone took 42 us instead of 45 for 16,384 rows, but values half way between
-// two codes, such as three quarters of their vector's largest, went to either.
-__device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float scale, float inv)
-{
-    uint32_t two[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint64_t q = mul2(pack(v[2 * i], v[2 * i + 1]), pack(inv, inv));
-        const uint64_t over = fma2(q, pack(scale, scale), pack(-v[2 * i], -v[2 * i + 1]));
-        float2 f;
-        unpack(fma2(over, pack(-inv, -inv), q), f.x, f.y);
-        two[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-    }
-    return make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
-}
-
-// Infinite values as the largest finite one (they would leave a NaN of a quotient).
-__device__ __forceinline__ void finite8(float (&v)[8])
-{
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = fminf(fmaxf(v[i], -3.402823466e38f), 3.402823466e38f);
 }
 
 __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8], float inv)
@@ -383,17 +264,6 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8], float inv)
                  0xFFu)
              << (8 * j);
     return r;
-}
-
-// Scale of an e4m3 row from its largest magnitude (an infinite one as the largest finite
-// value): amax / 448, never below the smallest normal number (so its reciprocal is finite), 1
-// for a zero row.  The division as above: 1 / 448 is a constant.
-__device__ __forceinline__ float e4m3_scale(float amax)
-{
-    amax = fminf(amax, 3.402823466e38f);
-    constexpr float kInv = 1.0f / 448.0f;
-    const float q = amax * kInv;
-    return amax > 0.0f ? fmaxf(fmaf(fmaf(q, -448.0f, amax), kInv, q), 1.17549435e-38f) : 1.0f;
 }
 
 // Biased exponent floor(log2(amax)) - 2 of an e2m1 block, clamped to ue8m0's 0..254; 127
@@ -592,6 +462,197 @@ cache_write_any_kernel(const __grid_constant__ RopeParams rp,
                 finite8(w);
                 *reinterpret_cast<uint2*>(c.codes + vec * c.D + 8 * l) = e4m3x8(w, s, inv);
             }
+        }
+        __syncwarp();
+    }
+}
+
+// ---------------------------------------------------------------------- cache append
+
+// Slot of a row's new key: through the request's page table, at its place among the packed keys,
+// or as given.  -1 where there is none.
+__device__ __forceinline__ int32_t append_slot(const AppendCall& c, int t)
+{
+    int64_t slot;
+    if (c.slots) {
+        slot = c.slots[t];
+    } else {
+        int lo = 0, hi = c.num_requests - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (c.row_begin[mid] <= t)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const int32_t j = c.positions[t], base = c.key_begin[lo];
+        if (j < 0 || j >= c.key_begin[lo + 1] - base)
+            return -1;
+        if (c.page > 0) {
+            const int32_t pg = c.table[lo * c.ld_table + j / c.page];
+            slot = pg < 0 ? -1 : (int64_t)pg * c.page + j % c.page;
+        } else {
+            slot = base + j;
+        }
+    }
+    return slot >= 0 && slot < c.num_slots ? static_cast<int32_t>(slot) : -1;
+}
+
+// Keys (blocks of z = 0, turned) and values (z = 1, as they are) of the same rows, in one launch:
+// the rotation's tiling, or for e4m3 the cache writes'.  The first vectors' loads are under way
+// while the block's threads look up its rows' slots (position, page, slot: two reads one after the
+// other) and compute its angles; a group then takes a few vectors, the next one's loads under
+// way.
+template <typename T, typename C>
+__global__ void __launch_bounds__(kThreads, 4)
+append_kernel(const __grid_constant__ RopeParams rp, const __grid_constant__ AppendCall c,
+              const __grid_constant__ Tiling t)
+{
+    constexpr bool kFp8 = sizeof(C) == 1;
+    __shared__ __align__(16) float sm_angles[2 * kAngles];
+    __shared__ int32_t sm_slots[kAppendRows];
+    pdl_wait_then_release();
+    const bool is_v = blockIdx.z != 0;
+    const int rot = is_v ? 0 : rp.rot;
+    const int g = quotient(threadIdx.x, t.by_lanes);
+    const int l = threadIdx.x - g * t.lanes;
+    const int r0 = blockIdx.x * t.rows, h0 = blockIdx.y * t.heads;
+    const int rows = min(t.rows, c.rows - r0), heads = min(t.heads, c.heads - h0);
+    const Unit u = unit_of(rot, is_v ? 0 : rp.offset, rp.interleaved, l, c.D);
+    const bool unit = g < t.groups && l < rot / 16 + (c.D - rot + 15) / 16;
+    const int64_t x_row = is_v ? c.v_row : c.k_row, x_head = is_v ? c.v_head : c.k_head;
+    const T* x = static_cast<const T*>(is_v ? c.v : c.k) + r0 * x_row + h0 * x_head;
+    C* cache = static_cast<C*>(is_v ? c.v_cache : c.k_cache);
+    float* scales = is_v ? c.v_scale : c.k_scale;
+    const int64_t to_slot = is_v ? c.vc_slot : c.kc_slot, to_head = is_v ? c.vc_head : c.kc_head;
+    Eight<T> wa, wb;
+    int row = quotient(g, t.by_heads), head = g - row * t.heads;
+    bool here = false;
+    auto load = [&] {
+        here = unit && row < rows && head < heads;
+        if (here) {
+            const T* p = x + row * x_row + head * x_head;
+            wa.load(p + u.a);
+            if (u.b >= 0)
+                wb.load(p + u.b);
+        }
+    };
+    load();
+    for (int i = threadIdx.x; i < rows; i += kThreads)
+        sm_slots[i] = append_slot(c, r0 + i);
+    if (rot > 0)
+        block_angles(rp, t, c.positions + r0, rows, sm_angles);
+    __syncthreads();
+    const int row_step = quotient(t.groups, t.by_heads), head_step = t.groups - row_step * t.heads;
+#pragma unroll 1
+    for (int j = 0;;) {
+        const int32_t slot = here ? sm_slots[row] : -1;
+        const bool on = slot >= 0;
+        const int h = h0 + head, angles = row * rot;
+        float a[8] = {}, b[8] = {};
+        if (on) {
+            wa.values(a);
+            if (u.b >= 0)
+                wb.values(b);
+        }
+        if (++j < t.batch) {
+            row += row_step;
+            head += head_step;
+            if (head >= t.heads) {
+                head -= t.heads;
+                ++row;
+            }
+            load();
+        }
+        if (on && u.rotated)
+            rotate16(rp, sm_angles + angles, l, a, b);
+        if constexpr (kFp8) {
+            // (a skipped row's lanes stay in the shuffles of the warp's other rows)
+            float m = 0.0f;
+            if (on)
+                m = fmaxf(largest(a), largest(b));
+            for (int d = t.lanes / 2; d > 0; d >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            if (on) {
+                const float s = e4m3_scale(m);
+                const float inv = 1.0f / s;
+                if (m == INFINITY) {
+                    finite8(a);
+                    finite8(b);
+                }
+                uint8_t* o = reinterpret_cast<uint8_t*>(cache) + slot * to_slot + h * to_head;
+                *reinterpret_cast<uint2*>(o + u.a) = e4m3x8(a, s, inv);
+                *reinterpret_cast<uint2*>(o + u.b) = e4m3x8(b, s, inv);
+                if (l == 0)
+                    scales[(int64_t)slot * c.heads + h] = s;
+            }
+        } else if (on) {
+            C* o = cache + slot * to_slot + h * to_head;
+            store8(o + u.a, a);
+            if (u.b >= 0)
+                store8(o + u.b, b);
+        }
+        if (j >= t.batch)
+            break;
+    }
+}
+
+// Any rotation, size and alignment: one warp per (row, head, keys or values).
+template <typename T, typename C>
+__global__ void __launch_bounds__(kThreads)
+append_any_kernel(const __grid_constant__ RopeParams rp, const __grid_constant__ AppendCall c)
+{
+    __shared__ float sm[kThreads / 32][kMaxHeadDim];
+    pdl_wait_then_release();
+    float* v = sm[threadIdx.x / 32];
+    const int l = threadIdx.x & 31;
+    const int64_t n = 2 * (int64_t)c.rows * c.heads;
+    for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; i < n;
+         i += (int64_t)gridDim.x * (kThreads / 32)) {
+        const bool is_v = i & 1;
+        const int t = static_cast<int>((i >> 1) / c.heads), h = static_cast<int>((i >> 1) % c.heads);
+        const int32_t slot = append_slot(c, t);
+        if (slot < 0)
+            continue;
+        const T* x = is_v ? static_cast<const T*>(c.v) + t * c.v_row + h * c.v_head
+                          : static_cast<const T*>(c.k) + t * c.k_row + h * c.k_head;
+        for (int e = l; e < c.D; e += 32)
+            v[e] = Elt<T>::load(x[e]);
+        __syncwarp();
+        for (int p = l; p < (is_v ? 0 : rp.rot / 2); p += 32) {
+            const int a = rp.offset + (rp.interleaved ? 2 * p : p);
+            const int b = rp.interleaved ? a + 1 : a + rp.rot / 2;
+            const float2 cs = turn(rp, c.positions[t], rp.inc[p]);
+            const float xa = v[a], xb = v[b];
+            v[a] = fmaf(xa, cs.x, -xb * cs.y);
+            v[b] = fmaf(xa, cs.y, xb * cs.x);
+        }
+        __syncwarp();
+        C* o = is_v ? static_cast<C*>(c.v_cache) + slot * c.vc_slot + h * c.vc_head
+                    : static_cast<C*>(c.k_cache) + slot * c.kc_slot + h * c.kc_head;
+        if constexpr (sizeof(C) == 1) {
+            float m = 0.0f;
+            for (int e = l; e < c.D; e += 32) {
+                v[e] = v[e] == v[e] ? v[e] : 0.0f;
+                m = fmaxf(m, fabsf(v[e]));
+            }
+            for (int d = 16; d > 0; d >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            __syncwarp();
+            const float s = e4m3_scale(m);
+            const float inv = 1.0f / s;
+            if (l == 0)
+                (is_v ? c.v_scale : c.k_scale)[(int64_t)slot * c.heads + h] = s;
+            if (l < c.D / 8) {
+                float w[8];
+                for (int k = 0; k < 8; ++k)
+                    w[k] = v[8 * l + k];
+                finite8(w);
+                *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(o) + 8 * l) = e4m3x8(w, s, inv);
+            }
+        } else {
+            for (int e = l; e < c.D; e += 32)
+                o[e] = Elt<C>::store(v[e]);
         }
         __syncwarp();
     }
@@ -831,6 +892,35 @@ cudaError_t cache_write_of(const RopeParams& rp, const CacheWriteCall& c, cudaSt
     return launch_pdl(cache_write_any_kernel<T, kFp4>, dim3(blocks), dim3(kThreads), 0, st, rp, c);
 }
 
+template <typename T, typename C>
+cudaError_t append_of(const RopeParams& rp, const AppendCall& c, cudaStream_t st)
+{
+    constexpr bool kFp8 = sizeof(C) == 1;
+    const bool whole =
+        whole_units(rp) && c.D % 8 == 0 && vector_rows(c.k, c.k_row, c.k_head, c.dtype) &&
+        vector_rows(c.v, c.v_row, c.v_head, c.dtype) &&
+        (kFp8 || (vector_rows(c.k_cache, c.kc_slot, c.kc_head, IDX_BF16) &&
+                  vector_rows(c.v_cache, c.vc_slot, c.vc_head, IDX_BF16)));
+    if (whole) {
+        // threads of a vector: for the maximum over it (e4m3) a power of two (rot_dim is a multiple
+        // of 16, so turned keys take as many units as values)
+        int lanes = kFp8 ? 2 : std::max(2, (c.D + 15) / 16);
+        while (kFp8 && lanes * 16 < c.D)
+            lanes *= 2;
+        const int64_t blocks = (2 * (int64_t)c.rows * c.heads * lanes + kThreads - 1) / kThreads;
+        const int batch = static_cast<int>(
+            std::max<int64_t>(1, std::min<int64_t>(8, blocks / (6 * device_sms()))));
+        const Tiling t = tiling(rp, c.rows, c.heads, lanes, batch);
+        dim3 grid = tiles(t, c.rows, c.heads);
+        grid.z = 2;
+        return launch_pdl(append_kernel<T, C>, grid, dim3(kThreads), 0, st, rp, c, t);
+    }
+    const int64_t n = 2 * (int64_t)c.rows * c.heads;
+    const unsigned blocks = static_cast<unsigned>(
+        std::min<int64_t>((n + kThreads / 32 - 1) / (kThreads / 32), 152 * 16));
+    return launch_pdl(append_any_kernel<T, C>, dim3(blocks), dim3(kThreads), 0, st, rp, c);
+}
+
 unsigned stride_blocks(int64_t items)
 {
     return static_cast<unsigned>(std::min<int64_t>((items + kThreads - 1) / kThreads, 152 * 64));
@@ -858,6 +948,21 @@ cudaError_t launch_cache_write(const RopeParams& rp, const CacheWriteCall& c, cu
     return c.dtype == IDX_BF16   ? cache_write_of<__nv_bfloat16, false>(rp, c, st)
            : c.dtype == IDX_FP16 ? cache_write_of<__half, false>(rp, c, st)
                                  : cache_write_of<float, false>(rp, c, st);
+}
+
+cudaError_t launch_append(const RopeParams& rp, const AppendCall& c, cudaStream_t st)
+{
+    if (c.rows <= 0)
+        return cudaSuccess;
+    if (c.cache_dtype == IDX_CODES)
+        return c.dtype == IDX_BF16   ? append_of<__nv_bfloat16, uint8_t>(rp, c, st)
+               : c.dtype == IDX_FP16 ? append_of<__half, uint8_t>(rp, c, st)
+                                     : append_of<float, uint8_t>(rp, c, st);
+    if (c.dtype == IDX_FP32)
+        return c.cache_dtype == IDX_BF16 ? append_of<float, __nv_bfloat16>(rp, c, st)
+                                         : append_of<float, __half>(rp, c, st);
+    return c.dtype == IDX_BF16 ? append_of<__nv_bfloat16, __nv_bfloat16>(rp, c, st)
+                               : append_of<__half, __half>(rp, c, st);
 }
 
 cudaError_t launch_cache_read(const CacheReadCall& c, cudaStream_t st)
