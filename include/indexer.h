@@ -609,6 +609,73 @@ int indexer_mask_blocks(indexer_plan_t plan, const uint8_t* cand_mask, int64_t l
                         const int32_t* compress_len, int32_t block, int32_t* blocks,
                         int32_t num_sel, int32_t* count, void* stream);
 
+/* ------------------------------------------------------------ causal attention
+ * Attention of a batch's new tokens over the cached keys of their requests.  For row t of request r,
+ * query head h and its key/value head g = h / (Hq / Hkv), with n = compress_len[t] (at most the
+ * request's key count):
+ *     a_j = scale * <q[t,h,:], k[slot(j),g,:]>,   lse[t,h] = log sum_j exp(a_j),
+ *     out[t,h,:] = sum_j exp(a_j - lse[t,h]) v[slot(j),g,:]
+ * over the keys j < n, with window > 0 only those with j >= n - window or j < sinks (a key that is
+ * both counts once).  Lengths may be any in any order: a row of length 0 (padding) sees nothing.  A
+ * row that sees no key gives out = 0 and lse = -inf.
+ *   slot(j), formats, strides, rounding of weights: as indexer_sparse_attention has them (weights of
+ *   8 significant bits, 11 under fp16 queries, those below 2^-21 of the row's largest with fewer over
+ *   fp16 keys).  Keys on negative table entries, or whose slot is not below num_slots, are left out.
+ *   Keys that no row of the call sees are not read, or have no effect, whatever they hold.
+ *
+ * indexer_causal_spec:
+ *   Hq, Hkv      query and key/value heads, Hkv divides Hq, Hq <= IDX_MAX_HEADS
+ *   D            64 or 128 (others IDX_ERR_UNSUPPORTED)
+ *   window       keys a row sees up to its own, 0: all of them
+ *   sinks        first keys that stay visible under a window
+ *   num_slots    rows of k and v
+ *   page_size    0: packed keys
+ *   scale        magnitude at most 1e38
+ * indexer_causal_attention_create: host only, needs no GPU, once per batch (plan: its requests, rows
+ *   and key counts); *workspace_bytes receives what a call needs: 256 bytes for its status, and
+ *   partial results where the rows alone do not fill the GPU.  The plan may be destroyed afterwards.
+ */
+typedef struct indexer_causal_spec {
+    int32_t Hq;
+    int32_t Hkv;
+    int32_t D;
+    int32_t window;
+    int32_t sinks;
+    int32_t dtype;
+    int32_t kv_format;
+    int32_t num_slots;
+    int32_t page_size;
+    float scale;
+} indexer_causal_spec;
+
+typedef struct indexer_causal_s* indexer_causal_t;
+
+int indexer_causal_attention_create(indexer_plan_t plan, const indexer_causal_spec* spec,
+                                    indexer_causal_t* out_attention, size_t* workspace_bytes);
+void indexer_causal_attention_destroy(indexer_causal_t attention);
+
+/* Operands of one call, as those of indexer_sparse_attention (rows of k and v any distance apart). */
+typedef struct indexer_causal_io {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* out;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* compress_len;
+    const int32_t* page_table;
+    float* lse;
+    int64_t q_row, q_head;
+    int64_t k_slot, k_head;
+    int64_t v_slot, v_head;
+    int64_t out_row, out_head;
+    int64_t ld_page_table;
+} indexer_causal_io;
+
+/* ws and status: as indexer_sparse_attention's. */
+int indexer_causal_attention(indexer_causal_t attention, const indexer_causal_io* io, void* ws,
+                             size_t ws_bytes, void* stream);
+
 /* --------------------------------------------------------------- cache append
  * New keys and values of a batch into their caches, the keys rotated on the way, in one launch:
  * for row t with position p = positions[t]

@@ -15,6 +15,7 @@ from ._lib import (  # noqa: F401
     indexer_cache_read, indexer_cache_write, indexer_page_slots, indexer_rope,
     indexer_rope_create, Attention, IDX_KV_DENSE, IDX_KV_FP8_E4M3, indexer_attention_create,
     indexer_mask_blocks, indexer_sparse_attention, IDX_MAX_PARTS, indexer_attention_join,
-    indexer_cache_append, indexer_rms_norm,
+    indexer_cache_append, indexer_rms_norm, CausalAttention, indexer_causal_attention,
+    indexer_causal_attention_create,
     lib,
 )

@@ -54,7 +54,8 @@ EXPORTED = ("indexer_plan", "indexer_plan_destroy", "indexer_plan_info", "indexe
             "indexer_rope", "indexer_cache_write", "indexer_cache_read", "indexer_page_slots",
             "indexer_attention_create", "indexer_attention_destroy", "indexer_sparse_attention",
             "indexer_mask_blocks", "indexer_cache_append", "indexer_attention_join",
-            "indexer_rms_norm")
+            "indexer_rms_norm", "indexer_causal_attention_create",
+            "indexer_causal_attention_destroy", "indexer_causal_attention")
 IDX_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -94,6 +95,12 @@ class _AttentionSpec(ctypes.Structure):
     _fields_ += [("scale", ctypes.c_float)]
 
 
+class _CausalSpec(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "Hq", "Hkv", "D", "window", "sinks", "dtype", "kv_format", "num_slots", "page_size")]
+    _fields_ += [("scale", ctypes.c_float)]
+
+
 class _AttentionIo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "q", "k", "v", "out", "k_scale", "v_scale", "sel", "sel_count", "compress_len",
@@ -105,7 +112,8 @@ class _AttentionIo(ctypes.Structure):
 
 # the same layout, packed in one go: eleven addresses, ten strides
 _ATTENTION_IO = struct.Struct("11P10q").pack
-# indexer_append_io, indexer_join_io and indexer_norm_io
+# indexer_causal_io, indexer_append_io, indexer_join_io and indexer_norm_io
+_CAUSAL_IO = struct.Struct("9P9q").pack
 _APPEND_IO = struct.Struct("9P9q7i").pack
 _JOIN_IO = struct.Struct("16P16q3P2q6i").pack
 _NORM_IO = struct.Struct("7P4q5if").pack
@@ -164,6 +172,11 @@ def lib():
         L.indexer_attention_destroy.restype = None
         L.indexer_sparse_attention.argtypes = [P, P, P, sz, P]
         L.indexer_mask_blocks.argtypes = [P, P, i64, P, i32, P, i32, P, P]
+        L.indexer_causal_attention_create.argtypes = [P, ctypes.POINTER(_CausalSpec),
+                                                      ctypes.POINTER(P), ctypes.POINTER(sz)]
+        L.indexer_causal_attention_destroy.argtypes = [P]
+        L.indexer_causal_attention_destroy.restype = None
+        L.indexer_causal_attention.argtypes = [P, P, P, sz, P]
         L.indexer_cache_append.argtypes = [P, P, P, P]
         L.indexer_attention_join.argtypes = [P, P]
         L.indexer_rms_norm.argtypes = [P, P]
@@ -171,7 +184,8 @@ def lib():
         L.indexer_error_string.restype = ctypes.c_char_p
         for name in EXPORTED:
             if name not in ("indexer_plan_destroy", "indexer_error_string",
-                            "indexer_rope_destroy", "indexer_attention_destroy"):
+                            "indexer_rope_destroy", "indexer_attention_destroy",
+                            "indexer_causal_attention_destroy"):
                 getattr(L, name).restype = ctypes.c_int
         L.indexer_launch_count.restype = ctypes.c_longlong
         L.indexer_fallback_rows.argtypes = [P, P, P]
@@ -685,6 +699,80 @@ def indexer_mask_blocks(plan: Plan, cand_mask, compress_len, block: int, blocks,
     if rc != IDX_OK:
         raise IndexerError("indexer_mask_blocks", rc)
     return blocks
+
+
+class CausalAttention:
+    """Owns an ``indexer_causal_t``; destroyed with the object."""
+
+    def __init__(self, handle, workspace_bytes: int, spec: _CausalSpec, rows: int, requests: int,
+                 max_keys: int):
+        self.handle = handle
+        self.workspace_bytes = workspace_bytes
+        self.spec = spec
+        self.rows = rows
+        self.requests = requests
+        self.pages = -(-max_keys // spec.page_size) if spec.page_size > 0 else 0
+        # what the tensors of a call are compared with
+        self.dtype = torch.bfloat16 if spec.dtype == IDX_BF16 else torch.float16
+        self.kv_type = self.dtype if spec.kv_format == IDX_KV_DENSE else None
+        self.row_shape = (rows,)
+        self.q_shape = (rows, spec.Hq, spec.D)
+        self.kv_shape = (spec.num_slots, spec.Hkv, spec.D)
+        self.scale_shape = (spec.num_slots, spec.Hkv)
+        self.lse_shape = (rows, spec.Hq)
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h is not None and _lib is not None:
+            _lib.indexer_causal_attention_destroy(h)
+
+
+def indexer_causal_attention_create(plan: Plan, Hq: int, Hkv: int, D: int, window: int = 0,
+                                    sinks: int = 0, dtype: int = IDX_BF16,
+                                    kv_format: int = IDX_KV_DENSE,
+                                    num_slots: Optional[int] = None, page_size: int = 0,
+                                    scale: Optional[float] = None) -> CausalAttention:
+    """Causal attention of the plan's rows over their requests' cached keys (host only): all of
+    them, or with ``window`` > 0 the last ``window`` and the first ``sinks``."""
+    spec = _CausalSpec(Hq, Hkv, D, window, sinks, dtype, kv_format,
+                       plan.problem.total_keys if num_slots is None else num_slots, page_size,
+                       max(D, 1) ** -0.5 if scale is None else scale)
+    handle, ws = ctypes.c_void_p(), ctypes.c_size_t()
+    _check("indexer_causal_attention_create", lib().indexer_causal_attention_create(
+        plan.handle, ctypes.byref(spec), ctypes.byref(handle), ctypes.byref(ws)))
+    return CausalAttention(handle, ws.value, spec, plan.problem.total_rows,
+                           plan.problem.num_requests, plan.max_keys)
+
+
+def indexer_causal_attention(attn: CausalAttention, q, k, v, compress_len, out, ws=None,
+                             k_scale=None, v_scale=None, page_table=None, lse=None, stream=None):
+    """Attention of ``q`` [rows, Hq, D] over the keys below ``compress_len`` (int32 [rows]) of ``k``
+    and ``v`` [num_slots, Hkv, D] into ``out`` (and ``lse`` fp32 [rows, Hq]); see the header."""
+    sq = _heads("q", q, attn.q_shape, attn.dtype)
+    so = _heads("out", out, attn.q_shape, attn.dtype)
+    sk = _heads("k", k, attn.kv_shape, attn.kv_type)
+    sv = _heads("v", v, attn.kv_shape, attn.kv_type)
+    table = ld_table = 0
+    if page_table is not None:
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_cuda or \
+                page_table.shape[0] != attn.requests or page_table.shape[1] < attn.pages or \
+                not _packed(page_table):
+            raise ValueError(f"page_table: int32 CUDA tensor [requests, {attn.pages} pages or more] "
+                             "expected")
+        table = page_table.data_ptr()
+        ld_table = page_table.stride(0) if attn.requests > 1 else page_table.shape[1]
+    io = _CAUSAL_IO(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+        _f32("k_scale", k_scale, attn.scale_shape), _f32("v_scale", v_scale, attn.scale_shape),
+        _i32("compress_len", compress_len, attn.row_shape) or 0, table,
+        _f32("lse", lse, attn.lse_shape), sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], so[0], so[1],
+        ld_table)
+    rc = (_lib or lib()).indexer_causal_attention(
+        attn.handle, io, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+        _stream(stream))
+    if rc != IDX_OK:
+        raise IndexerError("indexer_causal_attention", rc)
+    return out
 
 
 def _cache_rows(name: str, t, shape, dtype):

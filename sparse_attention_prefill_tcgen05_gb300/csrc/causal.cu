@@ -1,0 +1,941 @@
+// Causal attention of new tokens over the cached keys of their requests: all of them, or a sliding
+// window and the first few.
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "indexer.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace idx {
+namespace {
+
+// A work item is a key/value head, 256 rows of a request and a part of the keys they see.  Rows are
+// (token, query head of the group) pairs in that order, so that a group of any size fills the tensor
+// cores' 128 rows and its heads read each key once.  Per tile of 128 keys and each of the item's two
+// tiles of 128 rows
+//     S [rows x keys] = Q K^T,   P = exp2(S scale log2(e) - reference),   O += P V
+// with S, P and O in TMEM: a softmax thread owns a row, so its maximum and sum are its own, P goes back
+// over S as the product's first operand, and one row tile's softmax runs under the other's products.
+// The reference follows the row's maximum only when that has grown by kSlack, so that O is seldom
+// rescaled.
+//
+// Which keys: row by row those of [len - window, len) and [0, sinks).  An item walks a list of
+// consecutive places: the sinks, then from the first key that any of its rows sees to the last.
+// Roles: a warp lists items, four load keys and values (converting e4m3), two load queries, one issues
+// the products, two warpgroups do softmax and outputs.  All waits are bounded.
+
+constexpr int kModeBf16 = 0, kModeFp16 = 1, kModeFp8Bf16 = 2, kModeFp8Fp16 = 3;
+constexpr int kWaitTries = 1 << 22;     // of about a microsecond at most
+constexpr int kGaveUp = 2;
+constexpr int kSmemLimit = 232448;
+constexpr int kRows = kCausalRows;      // of an item
+constexpr int kInfos = 4;               // items listed ahead
+constexpr int kKeyRing = 8;             // tiles whose keys' validity and scales are kept
+
+template <int D, int MODE>
+struct Cfg {
+    static constexpr bool kFp8 = MODE >= kModeFp8Bf16;
+    // Operands: scores in the queries' type, whose 8 or 11 bits hold every e4m3 value; products over
+    // e4m3 caches in bf16, because a weight times its value's scale needs an fp32 number's range, of
+    // two terms under fp16 queries, whose outputs have 11 bits.
+    static constexpr bool kHalfS = MODE == kModeFp16 || MODE == kModeFp8Fp16;
+    static constexpr bool kHalfP = MODE == kModeFp16;
+    static constexpr int kPTerms = MODE == kModeFp8Fp16 ? 2 : 1;
+    static constexpr int kAtom = 128 * 128;             // 128 rows of 64 elements
+    static constexpr int kStage = 128 * D * 2;          // keys or values of a tile
+    static constexpr int kQ = 2 * kStage;
+    static constexpr int kRaw = kFp8 ? 128 * D : 0;     // codes of a tile
+    static constexpr int kRaws = kFp8 ? (D == 64 ? 6 : 3) : 0;
+    static constexpr int kStages = kFp8 ? (D == 64 ? 4 : 3) : (D == 64 ? 8 : 5);
+    // loads under way before one is waited for
+    static constexpr int kLag = kFp8 ? kRaws - 1 : 2;
+    static constexpr int kKeyInfo = kKeyRing * (16 + (kFp8 ? 2 * 128 * 4 : 0));
+    static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 * kInfos + 1;
+    static constexpr int kSmem = kQ + kStages * kStage + kRaws * kRaw + kKeyInfo + kInfos * 48 +
+                                 8 * kBars + 16;
+    static_assert(kSmem <= kSmemLimit, "tiles do not fit");
+    static_assert(kFp8 || kLag <= kStages - 3, "a load is signalled before its place is waited for");
+    static_assert(kKeyRing >= kStages / 2 + 2, "key ring");
+    static constexpr int kThreads = 512, kLaunchRegs = 128;
+    static constexpr int kSoftmaxRegs = kFp8 ? 184 : 200;
+    static constexpr int kFeedRegs = kFp8 ? 48 : 56, kLoadRegs = kFp8 ? 96 : 56;
+    static_assert(2 * kSoftmaxRegs + kFeedRegs + kLoadRegs <= 4 * kLaunchRegs, "registers");
+    static constexpr int kTmemO = 256;                  // columns: scores (and weights), then outputs
+};
+
+struct Item {
+    int r, g, i0, rows;      // request, key/value head, first (token, head) row and how many
+    int sinks, off, n;       // places of the list below sinks are keys; others are off keys on; places
+    int tile, tiles;         // tiles [tile, tiles) of the list; tile < 0: no more items
+    int split, base, keys;   // the request's first packed key and its keys
+};
+static_assert(sizeof(Item) == 48, "item");
+
+__device__ __forceinline__ int quotient(int n, const Divisor& d)
+{
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * d.mul) >> d.shift);
+}
+
+__device__ __forceinline__ constexpr uint32_t swizzled(uint32_t off)
+{
+    return off ^ (((off >> 7) & 7u) << 4);
+}
+
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ void fma2(float& a, float& b, uint64_t s, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair(a, b)), "l"(s), "l"(c));
+    unpair(r, a, b);
+}
+__device__ __forceinline__ void mul2(float& a, float& b, uint64_t s)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a, b)), "l"(s));
+    unpair(r, a, b);
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+template <bool kHalf>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    uint32_t r;
+    if (kHalf)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two e4m3 codes (low half) as two fp16 or bf16 numbers, exactly.
+template <bool kHalf>
+__device__ __forceinline__ uint32_t of_e4m3x2(uint32_t codes)
+{
+    const __half2 h(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3));
+    if (kHalf)
+        return *reinterpret_cast<const uint32_t*>(&h);
+    const float2 f = __half22float2(h);
+    return pack2<false>(f.x, f.y);
+}
+
+template <bool kHalf>
+__device__ __forceinline__ uint4 of_e4m3x8(uint32_t lo, uint32_t hi)
+{
+    return make_uint4(of_e4m3x2<kHalf>(lo & 0xFFFFu), of_e4m3x2<kHalf>(lo >> 16),
+                      of_e4m3x2<kHalf>(hi & 0xFFFFu), of_e4m3x2<kHalf>(hi >> 16));
+}
+
+// The low n bits (none below 0, all above 31).
+__device__ __forceinline__ uint32_t below(int n)
+{
+    return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+}
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(512, 1)
+causal_kernel(const __grid_constant__ CausalParams p)
+{
+    using C = Cfg<D, MODE>;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    uint8_t* qbuf = sm;                                      // [2 row tiles]
+    uint8_t* stages = qbuf + C::kQ;
+    uint8_t* raws = stages + C::kStages * C::kStage;
+    uint4* valid = reinterpret_cast<uint4*>(raws + C::kRaws * C::kRaw);     // [kKeyRing] bits
+    float* kscale = reinterpret_cast<float*>(valid + kKeyRing);             // [kKeyRing][128]
+    float* vscale = kscale + (C::kFp8 ? kKeyRing * 128 : 0);
+    Item* infos = reinterpret_cast<Item*>(vscale + (C::kFp8 ? kKeyRing * 128 : 0));
+    uint64_t* kv_full = reinterpret_cast<uint64_t*>(infos + kInfos);
+    uint64_t* kv_empty = kv_full + C::kStages;
+    uint64_t* q_full = kv_empty + C::kStages;
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* s_full = q_empty + 1;
+    uint64_t* p_full = s_full + 2;
+    uint64_t* o_full = p_full + 2;
+    uint64_t* info_full = o_full + 2;
+    uint64_t* info_empty = info_full + kInfos;
+    uint64_t* drained = info_empty + kInfos;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+    volatile int* ab = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x / 32), 0);
+    const int lane = threadIdx.x & 31;
+    constexpr int kMmaWarp = 8, kListWarp = 9, kQWarp = 10, kLoadWarp = 12;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(kv_full + i, 4);
+            mbar_init(kv_empty + i, 1);
+        }
+        mbar_init(q_full, 2);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, 4);
+            mbar_init(o_full + i, 1);
+        }
+        for (int i = 0; i < kInfos; ++i) {
+            mbar_init(info_full + i, 1);
+            mbar_init(info_empty + i, 8 + 1 + 2 + 4);
+        }
+        mbar_init(drained, 1);
+        *ab = (smem_u32(sm) & 1023u) != 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait_then_release();
+    // (a wait that gives up sets the status a whole wait budget after this)
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        *p.status = *ab ? kStatusBadArg : 0u;
+
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity))
+            return true;
+#pragma unroll 1
+        for (int i = 0; i < kWaitTries && *ab == 0; ++i)
+            if (mbar_try_wait_sleep(bar, parity, 1000u))
+                return true;
+        *ab = kGaveUp;
+        return false;
+    };
+    // The block's it-th item; false at the end of the list or where a wait gave up.
+    auto item_of = [&](int it, Item& w) {
+        if (!wait(info_full + it % kInfos, (it / kInfos) & 1))
+            return false;
+        w = infos[it % kInfos];
+        return w.tile >= 0;
+    };
+
+    if (warp < 8) {
+        // ---------------------------------------------------------------- softmax
+        // Thread = one row of one of the two row tiles.
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
+        const int wg = warp / 4, quad = warp & 3;
+        const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+        const uint32_t s_at = tmem + lanes + 128 * wg;
+        const uint32_t o_at = tmem + lanes + C::kTmemO + D * wg;
+        // Weights go by a reference that is replaced once a score passes it by kSlack.  fp16 weights
+        // end at 2^-24: theirs is 2^-7 of the maximum, so that they keep their 11 bits down to
+        // 2^-21 of it and the largest stays below 2^16.
+        constexpr float kSlack = C::kHalfP ? 15.0f : 8.0f;
+        constexpr float kBelow = C::kHalfP ? 7.0f : 0.0f;
+        uint32_t su = 0, ou = 0;                             // score tiles, items so far
+        int n = 0;                                           // tiles before this item
+        for (int it = 0;; ++it) {
+            Item w;
+            const bool more = __all_sync(0xFFFFFFFFu, item_of(it, w));
+            if (!more)
+                break;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(info_empty + it % kInfos);
+            const int count = w.tiles - w.tile;
+            if (128 * wg >= w.rows) {
+                n += max(count, 0);
+                continue;
+            }
+            const int i = 128 * wg + 32 * quad + lane;
+            const bool mine = i < w.rows;
+            const int token = quotient(w.i0 + i, p.by_group);
+            const int head = w.i0 + i - token * p.group + w.g * p.group;
+            const int t = p.row_begin[w.r] + token;
+            // places of the list that the row sees: below a, and from c to b
+            const int len = mine ? max(0, min(p.clen[t], w.keys)) : 0;
+            const int a = min(len, p.sinks), b = len - w.off;
+            const int c = p.window > 0 ? max(0, len - p.window) - w.off : 0;
+            float m = -INFINITY, l = 0.0f;                   // reference and sum
+            bool ok = true;
+            for (int j = 0; j < count; ++j, ++su) {
+                ok = wait(s_full + wg, su & 1);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int e0 = (w.tile + j) * 128, ring = (n + j) % kKeyRing;
+                float x[128];
+#pragma unroll
+                for (int k = 0; k < 128; k += 32)
+                    tmem_ld_32x32b_x32(s_at + k, x + k);
+                const uint4 keys = valid[ring];
+                tmem_wait_ld();
+                if (C::kFp8) {
+                    const float4* ks = reinterpret_cast<const float4*>(kscale + ring * 128);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float4 f = ks[k];
+                        mul2(x[4 * k], x[4 * k + 1], pair(f.x, f.y));
+                        mul2(x[4 * k + 2], x[4 * k + 3], pair(f.z, f.w));
+                    }
+                } else if (p.negate) {
+#pragma unroll
+                    for (int k = 0; k < 128; ++k)
+                        x[k] = -x[k];
+                }
+                const bool whole = (e0 + 128 <= a || (e0 >= c && e0 + 128 <= b)) &&
+                                   (keys.x & keys.y & keys.z & keys.w) == 0xFFFFFFFFu;
+                if (!__all_sync(0xFFFFFFFFu, whole)) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int e = e0 + 32 * k;
+                        const uint32_t in = k == 0 ? keys.x : k == 1 ? keys.y : k == 2 ? keys.z : keys.w;
+                        const uint32_t see =
+                            (below(a - e) | (below(b - e) & ~below(c - e))) & in;
+#pragma unroll
+                        for (int q = 0; q < 32; ++q)
+                            x[32 * k + q] = (see >> q) & 1u ? x[32 * k + q] : -INFINITY;
+                    }
+                }
+                float top = max3(x[0], x[1], x[2]);
+#pragma unroll
+                for (int k = 3; k < 127; k += 2)
+                    top = max3(top, x[k], x[k + 1]);
+                top = fmaxf(top, x[127]);
+                if (!C::kFp8)
+                    top *= p.scale_log2;
+                const bool raise = top > m + kSlack || (m == -INFINITY && top > -INFINITY);
+                if (__any_sync(0xFFFFFFFFu, raise)) {
+                    const float to = raise ? top - kBelow : m;
+                    const float f = m == -INFINITY ? 0.0f : ex2(m - to);
+                    if (__any_sync(0xFFFFFFFFu, raise && m > -INFINITY)) {
+                        // (the products so far were issued before these scores)
+                        const float g = m == -INFINITY ? 1.0f : f;
+#pragma unroll 1
+                        for (int k = 0; k < D; k += 32) {
+                            float v[32];
+                            tmem_ld_32x32b_x32(o_at + k, v);
+                            tmem_wait_ld();
+                            uint32_t r[32];
+#pragma unroll
+                            for (int q = 0; q < 32; ++q)
+                                r[q] = __float_as_uint(v[q] * g);
+                            tmem_st_32x32b_x32(o_at + k, r);
+                        }
+                    }
+                    l *= f;
+                    m = to;
+                }
+                const float ref = m == -INFINITY ? 0.0f : m;
+                const uint64_t mul = pair(p.scale_log2, p.scale_log2), sub = pair(-ref, -ref);
+                uint64_t sum = pair(0.0f, 0.0f);
+#pragma unroll
+                for (int k = 0; k < 128; k += 64) {
+                    uint32_t r[32];
+#pragma unroll
+                    for (int q = 0; q < 64; q += 2) {
+                        float &lo = x[k + q], &hi = x[k + q + 1];
+                        if (C::kFp8)
+                            unpair(add2(pair(lo, hi), sub), lo, hi);
+                        else
+                            fma2(lo, hi, mul, sub);
+                        lo = ex2(lo);
+                        hi = ex2(hi);
+                        sum = add2(sum, pair(lo, hi));
+                        if (!C::kFp8)
+                            r[q / 2] = pack2<C::kHalfP>(lo, hi);
+                    }
+                    if (!C::kFp8)
+                        tmem_st_32x32b_x32(s_at + k / 2, r);
+                }
+                if (C::kFp8) {
+                    const float4* vs = reinterpret_cast<const float4*>(vscale + ring * 128);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float4 f = vs[k];
+                        mul2(x[4 * k], x[4 * k + 1], pair(f.x, f.y));
+                        mul2(x[4 * k + 2], x[4 * k + 3], pair(f.z, f.w));
+                    }
+#pragma unroll
+                    for (int term = 0; term < C::kPTerms; ++term) {
+#pragma unroll
+                        for (int k = 0; k < 128; k += 64) {
+                            uint32_t r[32];
+#pragma unroll
+                            for (int q = 0; q < 64; q += 2) {
+                                float &lo = x[k + q], &hi = x[k + q + 1];
+                                const uint32_t h = pack2<false>(lo, hi);
+                                r[q / 2] = h;
+                                if (term + 1 < C::kPTerms) {     // what is left of them
+                                    lo -= __uint_as_float(h << 16);
+                                    hi -= __uint_as_float(h & 0xFFFF0000u);
+                                }
+                            }
+                            tmem_st_32x32b_x32(s_at + 64 * term + k / 2, r);
+                        }
+                    }
+                }
+                float s0, s1;
+                unpair(sum, s0, s1);
+                l += s0 + s1;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(p_full + wg);
+            }
+            if (!ok)
+                break;
+            n += max(count, 0);
+            // ---- output
+            if (count > 0) {
+                ok = wait(o_full + wg, ou & 1);
+                ++ou;
+                if (!__all_sync(0xFFFFFFFFu, ok))
+                    break;
+                tc_fence_after();
+            }
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float lse = (m + log2f(l)) * 0.693147180559945309f;
+            if (p.splits > 1) {
+                const int64_t at = ((int64_t)w.split * p.rows + t) * p.Hq + head;
+                if (mine)
+                    p.part_lse[at] = l == 0.0f ? -INFINITY : lse;
+#pragma unroll 1
+                for (int k = 0; k < D && count > 0; k += 32) {
+                    float v[32];
+                    tmem_ld_32x32b_x32(o_at + k, v);
+                    tmem_wait_ld();
+                    if (!mine || l == 0.0f)
+                        continue;
+                    float4* to = reinterpret_cast<float4*>(p.part_o + at * D + k);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        to[q] = make_float4(v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv,
+                                            v[4 * q + 3] * inv);
+                }
+            } else {
+                uint8_t* out = p.out + t * p.out_row + head * p.out_head;
+                if (mine && p.lse)
+                    p.lse[(int64_t)t * p.Hq + head] = l == 0.0f ? -INFINITY : lse;
+#pragma unroll 1
+                for (int k = 0; k < D; k += 32) {
+                    float v[32];
+                    if (count > 0) {
+                        tmem_ld_32x32b_x32(o_at + k, v);
+                        tmem_wait_ld();
+                    }
+                    uint32_t r[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        r[q] = l == 0.0f ? 0u : pack2<C::kHalfS>(v[2 * q] * inv, v[2 * q + 1] * inv);
+                    if (!mine)
+                        continue;
+                    if (p.out_vec) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            reinterpret_cast<uint4*>(out + 2 * k)[q] =
+                                make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            reinterpret_cast<uint16_t*>(out + 2 * k)[2 * q] = r[q] & 0xFFFFu;
+                            reinterpret_cast<uint16_t*>(out + 2 * k)[2 * q + 1] = r[q] >> 16;
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+        }
+        __syncwarp();
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLaunchRegs));
+    } else if (warp >= kLoadWarp) {
+        // ------------------------------------------------------- keys and values
+        // A warp takes 32 keys of every tile, a lane looks one of them up.  Copies are signalled
+        // kLag loads later, once they have landed; e4m3 codes land in a ring of their own and are
+        // converted by the lane that copied them.
+        if (C::kLoadRegs < C::kLaunchRegs)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLoadRegs));
+        constexpr int kEb = C::kFp8 ? 1 : 2;
+        constexpr int kPer = D * kEb / 16;                   // copies of a vector
+        constexpr int kAtOnce = 32 / kPer;                   // vectors of a warp's instruction
+        const int row0 = 32 * (warp - kLoadWarp), chunk = lane % kPer, sub = lane / kPer;
+        int st = 0, phase = 1, raw = 0;                      // next place, its empty parity
+        int done_st = 0, done_raw = 0;                       // next place to signal
+        int n = 0;                                           // tiles so far
+        bool ok = true;
+        // Signal the oldest load (its copies have landed).
+        auto signal = [&](bool is_v) {
+            if (C::kFp8) {
+                // into the place, once its last reader has left it
+                ok = __all_sync(0xFFFFFFFFu, ok && wait(kv_empty + st, phase));
+                if (!ok)
+                    return;
+                const uint32_t from = smem_u32(raws + done_raw * C::kRaw) + row0 * D + lane * 16;
+                const uint32_t to = smem_u32(stages + st * C::kStage);
+                auto convert = [&](auto half) {
+                    constexpr bool kHalf = decltype(half)::value;
+#pragma unroll
+                    for (int k = 0; k < kPer; k += 4) {
+                        uint4 w[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            w[q] = lds128(from + (k + q) * 512);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int row = row0 + (k + q) * kAtOnce + sub;
+                            const uint32_t off = (chunk / 4) * C::kAtom + row * 128 + (chunk % 4) * 32;
+                            sts128(to + swizzled(off), of_e4m3x8<kHalf>(w[q].x, w[q].y));
+                            sts128(to + swizzled(off + 16), of_e4m3x8<kHalf>(w[q].z, w[q].w));
+                        }
+                    }
+                };
+                if (is_v || !C::kHalfS)
+                    convert(std::false_type());
+                else
+                    convert(std::true_type());
+                if (++st == C::kStages) {
+                    st = 0;
+                    phase ^= 1;
+                }
+                done_raw = done_raw + 1 == C::kRaws ? 0 : done_raw + 1;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(kv_full + done_st);
+            done_st = done_st + 1 == C::kStages ? 0 : done_st + 1;
+        };
+        for (int it = 0; ok; ++it) {
+            Item w;
+            if (!__all_sync(0xFFFFFFFFu, item_of(it, w)))
+                break;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(info_empty + it % kInfos);
+            const int32_t* table = p.table + w.r * p.ld_table;
+            const uint8_t* kh = p.k + w.g * p.k_head + chunk * 16;
+            const uint8_t* vh = p.v + w.g * p.v_head + chunk * 16;
+            // the lane's key of a tile: its page and place there
+            int page = -1, rest = 0;
+            auto look = [&](int tile) {
+                const int e = tile * 128 + row0 + lane;
+                page = -1;
+                rest = e < w.sinks ? e : e + w.off;
+                if (e < w.n) {
+                    page = 0;
+                    if (p.page > 0) {
+                        const int pg = quotient(rest, p.by_page);
+                        page = table[pg];
+                        rest -= pg * p.page;
+                    } else {
+                        rest += w.base;
+                    }
+                }
+            };
+            int loads = 0, signalled = 0;                    // of this item
+            if (w.tile < w.tiles)
+                look(w.tile);
+            for (int tile = w.tile; tile < w.tiles && ok; ++tile, ++n) {
+                const int64_t at = (int64_t)page * p.page + rest;
+                const int32_t slot = page >= 0 && at < p.num_slots ? static_cast<int32_t>(at) : -1;
+                const uint32_t bits = __ballot_sync(0xFFFFFFFFu, slot >= 0);
+                float ks = 0.0f, vs = 0.0f;
+                if (C::kFp8 && slot >= 0) {
+                    ks = p.k_scale[(int64_t)slot * p.Hkv + w.g] * p.scale_log2;
+                    vs = p.v_scale[(int64_t)slot * p.Hkv + w.g];
+                }
+                if (tile + 1 < w.tiles)
+                    look(tile + 1);
+#pragma unroll 1
+                for (int is_v = 0; is_v < 2; ++is_v) {
+                    uint32_t to;
+                    if (!C::kFp8) {
+                        ok = __all_sync(0xFFFFFFFFu, wait(kv_empty + st, phase));
+                        if (!ok)
+                            break;
+                        to = smem_u32(stages + st * C::kStage);
+                        if (++st == C::kStages) {
+                            st = 0;
+                            phase ^= 1;
+                        }
+                    } else {
+                        to = smem_u32(raws + raw * C::kRaw) + row0 * D + lane * 16;
+                        raw = raw + 1 == C::kRaws ? 0 : raw + 1;
+                    }
+                    const uint8_t* src = is_v ? vh : kh;
+                    const int64_t stride = is_v ? p.v_slot : p.k_slot;
+#pragma unroll
+                    for (int k = 0; k < kPer; ++k) {
+                        const int row = k * kAtOnce + sub;
+                        const int32_t s = __shfl_sync(0xFFFFFFFFu, slot, row);
+                        const uint32_t off = C::kFp8 ? k * 512
+                                                     : swizzled((chunk / 8) * C::kAtom +
+                                                                (row0 + row) * 128 + (chunk % 8) * 16);
+                        cp_async16(to + off, src + max(s, 0) * stride, s >= 0);
+                    }
+                    cp_async_commit();
+                    ++loads;
+                    if (loads - signalled > C::kLag) {
+                        cp_async_wait<C::kLag>();
+                        signal(signalled & 1);
+                        ++signalled;
+                    }
+                    if (is_v == 0) {
+                        // (the ring's place was last read for a tile whose keys have left their stage)
+                        const int ring = n % kKeyRing;
+                        if (lane == 0)
+                            reinterpret_cast<uint32_t*>(valid + ring)[warp - kLoadWarp] = bits;
+                        if (C::kFp8) {
+                            kscale[ring * 128 + row0 + lane] = ks;
+                            vscale[ring * 128 + row0 + lane] = vs;
+                        }
+                    }
+                }
+            }
+            // The item's last loads: the next item may be a long wait away.
+            if (ok) {
+                cp_async_wait<0>();
+                for (; signalled < loads && ok; ++signalled)
+                    signal(signalled & 1);
+            }
+        }
+        cp_async_wait<0>();                                  // (of a wait that gave up)
+        __syncwarp();
+        if (C::kLoadRegs < C::kLaunchRegs)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kLaunchRegs));
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kFeedRegs));
+        if (warp == kListWarp) {
+            // ------------------------------------------------------------ items
+            // Longest first (a request's last rows see the most keys), every second round backwards.
+            for (int it = 0, round = 0;; ++it, ++round) {
+                const int64_t first = (int64_t)round * gridDim.x;
+                const int64_t pos =
+                    first + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                Item w = {};
+                w.tile = -1;
+                const bool last = first >= p.items;
+                if (!last && pos >= p.items) {               // none in this round
+                    --it;
+                    continue;
+                }
+                if (!__all_sync(0xFFFFFFFFu,
+                                wait(info_empty + it % kInfos, ((it / kInfos) & 1) ^ 1)))
+                    break;
+                if (!last) {
+                    int q = p.items - 1 - static_cast<int>(pos);
+                    int d = quotient(q, p.by_splits);
+                    w.split = q - d * p.splits;
+                    q = d;
+                    d = quotient(q, p.by_hkv);
+                    w.g = q - d * p.Hkv;
+                    int lo = 0, hi = p.num_requests - 1;     // the request of tile d
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) >> 1;
+                        if (p.tile_begin[mid] <= d)
+                            lo = mid;
+                        else
+                            hi = mid - 1;
+                    }
+                    w.r = lo;
+                    w.i0 = (d - p.tile_begin[lo]) * kRows;
+                    const int row0 = p.row_begin[lo];
+                    w.rows = min(kRows, (p.row_begin[lo + 1] - row0) * p.group - w.i0);
+                    w.base = p.key_begin[lo];
+                    w.keys = p.key_begin[lo + 1] - w.base;
+                    const int t0 = quotient(w.i0, p.by_group);
+                    const int t1 = quotient(w.i0 + w.rows - 1, p.by_group);
+                    int most = 0, least = 0x7FFFFFFF;        // keys of the rows, first key in a window
+                    for (int t = t0 + lane; t <= t1; t += 32) {
+                        const int len = max(0, min(p.clen[row0 + t], w.keys));
+                        most = max(most, len);
+                        if (len > 0)
+                            least = min(least, p.window > 0 ? max(0, len - p.window) : 0);
+                    }
+                    most = __reduce_max_sync(0xFFFFFFFFu, most);
+                    least = min(__reduce_min_sync(0xFFFFFFFFu, least), most);
+                    if (least > p.sinks) {
+                        w.sinks = p.sinks;
+                        w.off = least - p.sinks;
+                    }
+                    w.n = most - w.off;
+                    const int tiles = (w.n + 127) / 128;
+                    const int per = quotient(tiles + p.splits - 1, p.by_splits);
+                    w.tile = min(tiles, w.split * per);
+                    w.tiles = min(tiles, w.tile + per);
+                }
+                if (lane == 0) {
+                    infos[it % kInfos] = w;
+                    mbar_arrive(info_full + it % kInfos);
+                }
+                if (last)
+                    break;
+            }
+        } else if (warp == kQWarp || warp == kQWarp + 1) {
+            // ---------------------------------------------------------- queries
+            constexpr int kPer = D / 8;                      // copies of a vector
+            const int from = threadIdx.x - 32 * kQWarp;      // of 64 threads
+            uint32_t u = 0;
+            for (int it = 0;; ++it) {
+                Item w;
+                if (!__all_sync(0xFFFFFFFFu, item_of(it, w)))
+                    break;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(info_empty + it % kInfos);
+                if (w.tile >= w.tiles)
+                    continue;
+                if (!__all_sync(0xFFFFFFFFu, wait(q_empty, (u & 1) ^ 1)))
+                    break;
+                ++u;
+                const int rows = w.rows > 128 ? 256 : 128, t0 = p.row_begin[w.r];
+#pragma unroll 4
+                for (int x = from; x < rows * kPer; x += 64) {
+                    const int i = x / kPer, c = x % kPer;
+                    const int token = quotient(w.i0 + i, p.by_group);
+                    const int head = w.i0 + i - token * p.group + w.g * p.group;
+                    const bool in = i < w.rows;
+                    const uint32_t off = (i / 128) * C::kStage + (c / 8) * C::kAtom +
+                                         swizzled((i % 128) * 128 + (c % 8) * 16);
+                    cp_async16(smem_u32(qbuf) + off,
+                               in ? p.q + (t0 + token) * p.q_row + head * p.q_head + c * 16 : p.q, in);
+                }
+                cp_async_commit();
+                cp_async_wait<0>();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(q_full);
+            }
+        } else if (warp == kMmaWarp) {
+            // --------------------------------------------------------- products
+            // One elected lane issues everything, in this order: the next scores of a row tile go
+            // over the weights whose product was issued just before.
+            if (elect_one()) {
+                constexpr uint32_t s_desc = idesc_dense(128, 128, C::kHalfS ? 0 : 1, false, false);
+                constexpr uint32_t o_desc = idesc_dense(128, D, C::kHalfP ? 0 : 1, false, true);
+                uint32_t u = 0, pu0 = 0, pu1 = 0;            // items, weight tiles so far
+                int st = 0, phase = 0;
+                bool ok = true;
+                auto next = [&](int& s) {                    // a place of the ring and the next one
+                    s = st;
+                    const bool r = wait(kv_full + st, phase);
+                    if (++st == C::kStages) {
+                        st = 0;
+                        phase ^= 1;
+                    }
+                    return r;
+                };
+                auto scores = [&](int half, int place) {
+                    const uint64_t q = smem_desc(smem_u32(qbuf + half * C::kStage), 128, 16, 1024);
+                    const uint64_t k = smem_desc(smem_u32(stages + place * C::kStage), 128, 16, 1024);
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const int at = ((i / 4) * C::kAtom + (i % 4) * 32) / 16;
+                        mma_f16(tmem + 128 * half, q + at, k + at, s_desc, i > 0);
+                    }
+                    mma_commit(s_full + half);
+                };
+                auto products = [&](int half, int place, bool more) {
+                    const uint64_t v =
+                        smem_desc(smem_u32(stages + place * C::kStage), 128, C::kAtom, 1024);
+#pragma unroll
+                    for (int i = 0; i < 8 * C::kPTerms; ++i)
+                        mma_f16_tmem(tmem + C::kTmemO + D * half, tmem + 128 * half + 8 * i,
+                                     v + (i % 8) * 128, o_desc, more || i > 0);
+                };
+                for (int it = 0; ok; ++it) {
+                    Item w;
+                    if (!item_of(it, w))
+                        break;
+                    mbar_arrive(info_empty + it % kInfos);
+                    const int count = w.tiles - w.tile;
+                    if (count <= 0)
+                        continue;
+                    const bool two = w.rows > 128;
+                    int ks, vs;
+                    ok = wait(q_full, u & 1) && next(ks);
+                    if (!ok)
+                        break;
+                    ++u;
+                    tc_fence_after();
+                    scores(0, ks);
+                    if (two)
+                        scores(1, ks);
+                    mma_commit(kv_empty + ks);
+                    if (count == 1)
+                        mma_commit(q_empty);
+                    for (int j = 0; j < count; ++j) {
+                        const bool last = j + 1 == count;
+                        ok = next(vs) && wait(p_full, pu0 & 1);
+                        if (!ok)
+                            break;
+                        ++pu0;
+                        tc_fence_after();
+                        products(0, vs, j > 0);
+                        if (last) {
+                            mma_commit(o_full);
+                        } else {
+                            ok = next(ks);
+                            if (!ok)
+                                break;
+                            tc_fence_after();
+                            scores(0, ks);
+                        }
+                        if (two) {
+                            ok = wait(p_full + 1, pu1 & 1);
+                            if (!ok)
+                                break;
+                            ++pu1;
+                            tc_fence_after();
+                            products(1, vs, j > 0);
+                            if (last)
+                                mma_commit(o_full + 1);
+                        }
+                        mma_commit(kv_empty + vs);
+                        if (!last) {
+                            if (two)
+                                scores(1, ks);
+                            mma_commit(kv_empty + ks);
+                            if (j + 2 == count)
+                                mma_commit(q_empty);
+                        }
+                    }
+                }
+                // what was issued, and its arrivals, end before the memory goes
+                mma_commit(drained);
+                for (int i = 0; i < kWaitTries && !mbar_try_wait_sleep(drained, 0, 1000u); ++i)
+                    ;
+            }
+        }
+        __syncwarp();
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kLaunchRegs));
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && *ab == kGaveUp)
+        atomicOr(p.status, kStatusTimeout);
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Parts of rows whose keys were split over blocks: a warp per (row, query head), the parts' weights
+// from one read of their log-sum-exps.  Parts without a key were not written and are not read.
+template <typename T, int D>
+__global__ void __launch_bounds__(128)
+causal_join_kernel(const __grid_constant__ CausalParams p)
+{
+    pdl_wait_then_release();
+    const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / 32, n = (int64_t)p.rows * p.Hq;
+    if (i >= n)
+        return;
+    const int lane = threadIdx.x & 31;
+    const float lse = lane < p.splits ? p.part_lse[lane * n + i] : -INFINITY;
+    float m = lse;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    const float ref = m == -INFINITY ? 0.0f : m;
+    const float f = exp2f((lse - ref) * 1.4426950408889634f);
+    float sum = f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    constexpr int N = D / 32;
+    float o[N] = {};
+    for (int s0 = 0; s0 < p.splits; s0 += 4) {
+        float in[4][N], w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int s = s0 + k;
+            w[k] = __shfl_sync(0xFFFFFFFFu, f, s & 31);
+            if (s >= p.splits || w[k] == 0.0f) {
+                w[k] = 0.0f;
+                continue;
+            }
+            const float* at = p.part_o + (s * n + i) * D + N * lane;
+            if (N == 4)
+                *reinterpret_cast<float4*>(in[k]) = *reinterpret_cast<const float4*>(at);
+            else
+                *reinterpret_cast<float2*>(in[k]) = *reinterpret_cast<const float2*>(at);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                o[e] = w[k] != 0.0f ? fmaf(in[k][e], w[k], o[e]) : o[e];
+    }
+    const int64_t t = i / p.Hq;
+    const int h = static_cast<int>(i - t * p.Hq);
+    T* out = reinterpret_cast<T*>(p.out + t * p.out_row + h * p.out_head) + N * lane;
+    const float inv = sum > 0.0f ? 1.0f / sum : sum;
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        out[e] = static_cast<T>(o[e] * inv);
+    if (p.lse && lane == 0)
+        p.lse[i] = m == -INFINITY ? m : ref + log2f(sum) * 0.693147180559945309f;
+}
+
+template <int D, int MODE>
+cudaError_t causal(const CausalParams& p, cudaStream_t st)
+{
+    using C = Cfg<D, MODE>;
+    static std::atomic<uint64_t> ready;
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess)
+        e = once_per_device(ready, device, [] {
+            // the warpgroups' trade has to add up against what a block is launched with
+            cudaFuncAttributes a;
+            cudaError_t r = cudaFuncGetAttributes(&a, causal_kernel<D, MODE>);
+            if (r == cudaSuccess && a.numRegs != C::kLaunchRegs)
+                r = cudaErrorLaunchOutOfResources;
+            return r != cudaSuccess
+                       ? r
+                       : cudaFuncSetAttribute(causal_kernel<D, MODE>,
+                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              C::kSmem);
+        });
+    if (e != cudaSuccess)
+        return e;
+    const unsigned blocks = static_cast<unsigned>(std::min(p.items, device_sms()));
+    e = launch_pdl(causal_kernel<D, MODE>, dim3(blocks), dim3(C::kThreads), C::kSmem, st, p);
+    if (e != cudaSuccess || p.splits == 1)
+        return e;
+    using T = typename std::conditional<C::kHalfS, __half, __nv_bfloat16>::type;
+    count_launch();
+    const unsigned join = static_cast<unsigned>(((int64_t)p.rows * p.Hq + 3) / 4);
+    return launch_pdl(causal_join_kernel<T, D>, dim3(join), dim3(128), 0, st, p);
+}
+
+template <int MODE>
+cudaError_t causal_mode(const CausalParams& p, int D, cudaStream_t st)
+{
+    return D == 64 ? causal<64, MODE>(p, st) : causal<128, MODE>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_causal(const CausalParams& p, int D, int dtype, bool fp8, cudaStream_t st)
+{
+    if (dtype == IDX_BF16)
+        return fp8 ? causal_mode<kModeFp8Bf16>(p, D, st) : causal_mode<kModeBf16>(p, D, st);
+    return fp8 ? causal_mode<kModeFp8Fp16>(p, D, st) : causal_mode<kModeFp16>(p, D, st);
+}
+
+}  // namespace idx

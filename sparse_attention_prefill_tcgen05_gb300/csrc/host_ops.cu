@@ -24,6 +24,14 @@ struct indexer_attention_s {
     size_t ws_bytes = 0;
 };
 
+struct indexer_causal_s {
+    indexer_causal_spec spec;
+    CausalParams p;              // everything but the operands of a call
+    int64_t max_pages = 0;       // of the longest request
+    size_t part_rows = 0;        // (row, head, part) triples of split rows
+    size_t ws_bytes = 0;
+};
+
 namespace {
 
 constexpr int kPlanSms = 152;    // SMs the splits are planned for
@@ -429,6 +437,162 @@ int indexer_mask_blocks(indexer_plan_t plan, const uint8_t* cand_mask, int64_t l
     std::copy(v.L, v.L + v.R, p.key_count);
     count_launch();
     return finish(launch_mask_blocks(p, static_cast<cudaStream_t>(stream)));
+}
+
+int indexer_causal_attention_create(indexer_plan_t plan, const indexer_causal_spec* s,
+                                    indexer_causal_t* out, size_t* ws_bytes)
+{
+    if (!out)
+        return IDX_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (!plan || !s || s->Hkv < 1 || s->Hq < 1 || s->Hq > IDX_MAX_HEADS ||
+        s->Hq % s->Hkv != 0 || s->window < 0 || s->sinks < 0 ||
+        (s->dtype != IDX_BF16 && s->dtype != IDX_FP16) ||
+        (s->kv_format != IDX_KV_DENSE && s->kv_format != IDX_KV_FP8_E4M3) || s->num_slots < 0 ||
+        s->page_size < 0 || !(std::fabs(s->scale) <= 1e38f) || s->D < 1)
+        return IDX_ERR_INVALID_ARG;
+    if (s->D != 64 && s->D != 128)
+        return IDX_ERR_UNSUPPORTED;
+    const PlanView v = plan_view(plan);
+    if ((int64_t)v.T * s->Hq > INT32_MAX)
+        return IDX_ERR_INVALID_ARG;
+    indexer_causal_s* a = new (std::nothrow) indexer_causal_s();
+    if (!a)
+        return IDX_ERR_INVALID_ARG;
+    a->spec = *s;
+    CausalParams& p = a->p;
+    std::memset(&p, 0, sizeof(p));
+    const bool fp8 = s->kv_format == IDX_KV_FP8_E4M3;
+    const double scale = s->scale * 1.4426950408889634;
+    p.negate = !fp8 && scale < 0.0;
+    p.scale_log2 = static_cast<float>(p.negate ? -scale : scale);
+    // (a masked score is -inf, which 0 would make NaN; 2^-100 leaves all weights alike as 0 does)
+    if (p.scale_log2 == 0.0f)
+        p.scale_log2 = 0x1p-100f;
+    p.rows = v.T;
+    p.Hq = s->Hq;
+    p.Hkv = s->Hkv;
+    p.group = s->Hq / s->Hkv;
+    p.window = s->window;
+    p.sinks = s->window > 0 ? s->sinks : 0;
+    p.num_slots = s->num_slots;
+    p.page = s->page_size;
+    p.num_requests = v.R;
+    std::copy(v.row_begin, v.row_begin + v.R + 1, p.row_begin);
+    std::copy(v.key_begin, v.key_begin + v.R + 1, p.key_begin);
+    if (s->page_size > 0)
+        a->max_pages = (v.max_L + (int64_t)s->page_size - 1) / s->page_size;
+    int64_t all = 0, longest = 0, work = 0;
+    for (int r = 0; r < v.R; ++r) {
+        const int64_t rows = (int64_t)(v.row_begin[r + 1] - v.row_begin[r]) * p.group;
+        const int64_t tiles = (rows + kCausalRows - 1) / kCausalRows;
+        int64_t seen = v.L[r];
+        if (p.window > 0)
+            seen = std::min<int64_t>(seen, (int64_t)p.window + p.sinks +
+                                               std::min<int64_t>(rows, kCausalRows) / p.group);
+        const int64_t keys = (seen + 127) / 128;
+        p.tile_begin[r] = static_cast<int32_t>(all);
+        all += tiles;
+        work += tiles * keys;
+        if (tiles > 0)
+            longest = std::max(longest, keys);
+    }
+    p.tile_begin[v.R] = static_cast<int32_t>(all);
+    const int64_t items = all * s->Hkv;
+    work *= s->Hkv;
+    if (items > (1 << 26)) {
+        delete a;
+        return IDX_ERR_INVALID_ARG;
+    }
+    // Items that do not fill the SMs are split.
+    p.splits = 1;
+    double best = INFINITY;
+    for (int64_t n = 1; n <= std::min<int64_t>(kCausalSplits, std::max<int64_t>(1, longest)); ++n) {
+        const double waves = static_cast<double>((items * n + kPlanSms - 1) / kPlanSms);
+        const double tiles = std::max(static_cast<double>(work) / kPlanSms,
+                                      std::ceil(static_cast<double>(longest) / n));
+        const double bytes = 8.0 * n * v.T * s->Hq * s->D;
+        const double cost = 1.1 * tiles + 2.5 * waves + (n == 1 ? 0.0 : 3.0 + 1e-6 / 4 * bytes);
+        if (cost < best) {
+            best = cost;
+            p.splits = static_cast<int32_t>(n);
+        }
+    }
+    p.items = static_cast<int32_t>(items * p.splits);
+    p.by_page = divisor(std::max(1, s->page_size));
+    p.by_group = divisor(p.group);
+    p.by_splits = divisor(p.splits);
+    p.by_hkv = divisor(p.Hkv);
+    // status word, then the parts of split rows
+    a->part_rows = p.splits > 1 ? (size_t)p.splits * v.T * s->Hq : 0;
+    a->ws_bytes = 256 + a->part_rows * (s->D + 1) * sizeof(float);
+    *out = a;
+    if (ws_bytes)
+        *ws_bytes = a->ws_bytes;
+    return IDX_OK;
+}
+
+void indexer_causal_attention_destroy(indexer_causal_t a) { delete a; }
+
+int indexer_causal_attention(indexer_causal_t a, const indexer_causal_io* io, void* ws,
+                             size_t ws_bytes, void* stream)
+{
+    if (!a || !io)
+        return IDX_ERR_INVALID_ARG;
+    const indexer_causal_spec& s = a->spec;
+    const bool fp8 = s.kv_format == IDX_KV_FP8_E4M3;
+    const int64_t kb = fp8 ? 1 : 2;       // bytes of a cached element
+    if (a->p.rows > 0) {
+        const bool strides_ok =
+            io->q_row >= 0 && io->q_head >= 0 && io->k_slot >= 0 && io->k_head >= 0 &&
+            io->v_slot >= 0 && io->v_head >= 0 && io->out_row >= 0 && io->out_head >= 0 &&
+            (io->q_row * 2) % 16 == 0 && (io->q_head * 2) % 16 == 0 &&
+            (io->k_slot * kb) % 16 == 0 && (io->k_head * kb) % 16 == 0 &&
+            (io->v_slot * kb) % 16 == 0 && (io->v_head * kb) % 16 == 0 &&
+            (s.Hq == 1 || io->out_head >= s.D) && (a->p.rows == 1 || io->out_row >= s.D);
+        if (!strides_ok || !io->q || !io->out || !io->compress_len ||
+            (s.num_slots > 0 && (!io->k || !io->v)) || !is_aligned(io->q, 16) ||
+            !is_aligned(io->k, 16) || !is_aligned(io->v, 16) || !is_aligned(io->out, 2) ||
+            !is_aligned(io->compress_len, 4) || !is_aligned(io->page_table, 4) ||
+            !is_aligned(io->lse, 4) || !is_aligned(io->k_scale, 4) || !is_aligned(io->v_scale, 4) ||
+            (fp8 && s.num_slots > 0 && (!io->k_scale || !io->v_scale)) ||
+            (s.page_size > 0 && a->max_pages > 0 &&
+             (!io->page_table || io->ld_page_table < a->max_pages)))
+            return IDX_ERR_INVALID_ARG;
+        if (!ws || !is_aligned(ws, 256))
+            return IDX_ERR_INVALID_ARG;
+        if (ws_bytes < a->ws_bytes)
+            return IDX_ERR_WORKSPACE;
+    }
+    if (!device_supported())
+        return IDX_ERR_UNSUPPORTED;
+    if (a->p.rows == 0)
+        return IDX_OK;
+    CausalParams p = a->p;
+    p.q = static_cast<const uint8_t*>(io->q);
+    p.k = static_cast<const uint8_t*>(io->k);
+    p.v = static_cast<const uint8_t*>(io->v);
+    p.out = static_cast<uint8_t*>(io->out);
+    p.k_scale = io->k_scale;
+    p.v_scale = io->v_scale;
+    p.clen = io->compress_len;
+    p.table = io->page_table;
+    p.lse = io->lse;
+    p.q_row = 2 * io->q_row;
+    p.q_head = 2 * io->q_head;
+    p.k_slot = kb * io->k_slot;
+    p.k_head = kb * io->k_head;
+    p.v_slot = kb * io->v_slot;
+    p.v_head = kb * io->v_head;
+    p.out_row = 2 * io->out_row;
+    p.out_head = 2 * io->out_head;
+    p.out_vec = is_aligned(io->out, 16) && p.out_row % 16 == 0 && p.out_head % 16 == 0;
+    p.ld_table = io->ld_page_table;
+    p.status = static_cast<uint32_t*>(ws);
+    p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
+    p.part_lse = p.part_o + a->part_rows * s.D;
+    count_launch();
+    return finish(launch_causal(p, s.D, s.dtype, fp8, static_cast<cudaStream_t>(stream)));
 }
 
 int indexer_cache_append(indexer_plan_t plan, indexer_rope_t rope, const indexer_append_io* io,

@@ -494,6 +494,40 @@ struct AttnParams {
 int attention_heads_per_tile(int group, int dtype, bool fp8);
 cudaError_t launch_attention(const AttnParams& p, int D, int dtype, bool fp8, cudaStream_t st);
 
+// Causal attention of a batch's rows over the cached keys of their requests.  A work item is
+// (256 (token, query head) rows of a request, key/value head, part of their keys).
+constexpr int kCausalRows = 256;
+constexpr int kCausalSplits = 32;
+struct CausalParams {
+    const uint8_t* q;            // byte strides
+    const uint8_t* k;
+    const uint8_t* v;
+    uint8_t* out;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* clen;
+    const int32_t* table;
+    float* lse;
+    int64_t q_row, q_head, k_slot, k_head, v_slot, v_head, out_row, out_head;
+    int64_t ld_table;
+    float* part_o;               // [splits, rows, Hq, D] of split rows
+    float* part_lse;             // [splits, rows, Hq]
+    uint32_t* status;
+    float scale_log2;            // scale * log2(e), its magnitude over 16-bit caches
+    int32_t negate;              // ... whose scores are then turned over
+    int32_t out_vec;             // out takes 16-byte stores
+    int32_t rows, Hq, Hkv, group;
+    int32_t window, sinks;       // window 0: every key below a row's length
+    int32_t num_slots, page;
+    int32_t splits, items;
+    Divisor by_page, by_group, by_splits, by_hkv;
+    int32_t num_requests;
+    int32_t row_begin[kMaxRequests + 1];
+    int32_t key_begin[kMaxRequests + 1];
+    int32_t tile_begin[kMaxRequests + 1];   // tiles of kCausalRows rows before a request's
+};
+cudaError_t launch_causal(const CausalParams& p, int D, int dtype, bool fp8, cudaStream_t st);
+
 // Attention over disjoint sets of keys, joined by their log-sum-exps.
 constexpr int kMaxParts = 8;
 struct JoinCall {
