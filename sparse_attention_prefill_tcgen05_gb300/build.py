@@ -19,8 +19,9 @@ ROOT = os.path.dirname(HERE)
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libindexer.so")
 SOURCES = ["logits_tc.cu", "select.cu", "rowtopk.cu", "misc.cu", "host.cu",
-           "operands.cu", "attention.cu", "causal.cu", "layer.cu", "host_ops.cu"]
-HEADERS = ["internal.h", "ptx.cuh", "groupsel.cuh", "elements.cuh"]
+           "operands.cu", "attention.cu", "attention_range.cu", "causal.cu", "layer.cu", "host_ops.cu"]
+HEADERS = ["internal.h", "ptx.cuh", "groupsel.cuh", "elements.cuh",
+           "attention_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]

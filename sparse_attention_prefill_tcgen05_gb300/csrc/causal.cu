@@ -14,7 +14,7 @@
 namespace idx {
 namespace {
 
-// A work item is a key/value head, 256 rows of a request and a part of the keys they see.  Rows are
+// A work item is a key/value head and 256 rows of a request.  Rows are
 // (token, query head of the group) pairs in that order, so that a group of any size fills the tensor
 // cores' 128 rows and its heads read each key once.  Per tile of 128 keys and each of the item's two
 // tiles of 128 rows
@@ -72,7 +72,8 @@ struct Item {
     int r, g, i0, rows;      // request, key/value head, first (token, head) row and how many
     int sinks, off, n;       // places of the list below sinks are keys; others are off keys on; places
     int tile, tiles;         // tiles [tile, tiles) of the list; tile < 0: no more items
-    int split, base, keys;   // the request's first packed key and its keys
+    int part;                // where a part of an item goes, -1: the whole item
+    int base, keys;          // the request's first packed key and its keys
 };
 static_assert(sizeof(Item) == 48, "item");
 
@@ -410,8 +411,8 @@ causal_kernel(const __grid_constant__ CausalParams p)
             }
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             const float lse = (m + log2f(l)) * 0.693147180559945309f;
-            if (p.splits > 1) {
-                const int64_t at = ((int64_t)w.split * p.rows + t) * p.Hq + head;
+            if (w.part >= 0) {
+                const int64_t at = (int64_t)w.part * kRows + i;
                 if (mine)
                     p.part_lse[at] = l == 0.0f ? -INFINITY : lse;
 #pragma unroll 1
@@ -621,29 +622,20 @@ causal_kernel(const __grid_constant__ CausalParams p)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kFeedRegs));
         if (warp == kListWarp) {
             // ------------------------------------------------------------ items
-            // Longest first (a request's last rows see the most keys), every second round backwards.
-            for (int it = 0, round = 0;; ++it, ++round) {
-                const int64_t first = (int64_t)round * gridDim.x;
-                const int64_t pos =
-                    first + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            // The block's share of all items' key tiles, as it was planned: from the first's on.
+            int item = p.cut_item[blockIdx.x], from = p.cut_tile[blockIdx.x];
+            const int last_item = p.cut_item[blockIdx.x + 1], end = p.cut_tile[blockIdx.x + 1];
+            for (int it = 0;; ++it, ++item, from = 0) {
                 Item w = {};
                 w.tile = -1;
-                const bool last = first >= p.items;
-                if (!last && pos >= p.items) {               // none in this round
-                    --it;
-                    continue;
-                }
+                const bool more = item < last_item || (item == last_item && from < end);
                 if (!__all_sync(0xFFFFFFFFu,
                                 wait(info_empty + it % kInfos, ((it / kInfos) & 1) ^ 1)))
                     break;
-                if (!last) {
-                    int q = p.items - 1 - static_cast<int>(pos);
-                    int d = quotient(q, p.by_splits);
-                    w.split = q - d * p.splits;
-                    q = d;
-                    d = quotient(q, p.by_hkv);
-                    w.g = q - d * p.Hkv;
-                    int lo = 0, hi = p.num_requests - 1;     // the request of tile d
+                if (more) {
+                    const int d = quotient(item, p.by_hkv);
+                    w.g = item - d * p.Hkv;
+                    int lo = 0, hi = p.num_requests - 1;     // the request of row tile d
                     while (lo < hi) {
                         const int mid = (lo + hi + 1) >> 1;
                         if (p.tile_begin[mid] <= d)
@@ -653,8 +645,8 @@ causal_kernel(const __grid_constant__ CausalParams p)
                     }
                     w.r = lo;
                     w.i0 = (d - p.tile_begin[lo]) * kRows;
-                    const int row0 = p.row_begin[lo];
-                    w.rows = min(kRows, (p.row_begin[lo + 1] - row0) * p.group - w.i0);
+                    const int row0 = p.row_begin[lo], tokens = p.row_begin[lo + 1] - row0;
+                    w.rows = min(kRows, tokens * p.group - w.i0);
                     w.base = p.key_begin[lo];
                     w.keys = p.key_begin[lo + 1] - w.base;
                     const int t0 = quotient(w.i0, p.by_group);
@@ -674,15 +666,19 @@ causal_kernel(const __grid_constant__ CausalParams p)
                     }
                     w.n = most - w.off;
                     const int tiles = (w.n + 127) / 128;
-                    const int per = quotient(tiles + p.splits - 1, p.by_splits);
-                    w.tile = min(tiles, w.split * per);
-                    w.tiles = min(tiles, w.tile + per);
+                    const int planned =
+                        causal_tiles(w.keys, tokens, t0, t1, p.window, p.sinks);
+                    const int to = item == last_item ? end : planned;
+                    // the part's share of the tiles that there are
+                    w.tile = static_cast<int>((int64_t)from * tiles / planned);
+                    w.tiles = static_cast<int>((int64_t)to * tiles / planned);
+                    w.part = from > 0 ? 2 * blockIdx.x : to < planned ? 2 * blockIdx.x + 1 : -1;
                 }
                 if (lane == 0) {
                     infos[it % kInfos] = w;
                     mbar_arrive(info_full + it % kInfos);
                 }
-                if (last)
+                if (!more)
                     break;
             }
         } else if (warp == kQWarp || warp == kQWarp + 1) {
@@ -834,61 +830,90 @@ causal_kernel(const __grid_constant__ CausalParams p)
     }
 }
 
-// Parts of rows whose keys were split over blocks: a warp per (row, query head), the parts' weights
-// from one read of their log-sum-exps.  Parts without a key were not written and are not read.
+// Items that end in another block than they began: their parts, weighted by their log-sum-exps.  A
+// block of the grid's x for every cut (the first of an item does it all), a warp a row.  Parts
+// without a key were not written and are not read.
 template <typename T, int D>
 __global__ void __launch_bounds__(128)
 causal_join_kernel(const __grid_constant__ CausalParams p)
 {
     pdl_wait_then_release();
-    const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / 32, n = (int64_t)p.rows * p.Hq;
-    if (i >= n)
+    const int cut = blockIdx.x + 1, item = p.cut_item[cut];
+    if (p.cut_tile[cut] == 0 || (p.cut_item[cut - 1] == item && p.cut_tile[cut - 1] > 0))
         return;
-    const int lane = threadIdx.x & 31;
-    const float lse = lane < p.splits ? p.part_lse[lane * n + i] : -INFINITY;
-    float m = lse;
+    int end = cut + 1;                                       // the blocks [cut - 1, end) share it
+    while (end < p.blocks && p.cut_item[end] == item && p.cut_tile[end] > 0)
+        ++end;
+    const int d = quotient(item, p.by_hkv), g = item - d * p.Hkv;
+    int r = 0, hi = p.num_requests - 1;
+    while (r < hi) {
+        const int mid = (r + hi + 1) >> 1;
+        if (p.tile_begin[mid] <= d)
+            r = mid;
+        else
+            hi = mid - 1;
+    }
+    const int i0 = (d - p.tile_begin[r]) * kRows, row0 = p.row_begin[r];
+    const int i = blockIdx.y * 4 + threadIdx.x / 32, lane = threadIdx.x & 31;
+    if (i >= min(kRows, (p.row_begin[r + 1] - row0) * p.group - i0))
+        return;
+    const int token = quotient(i0 + i, p.by_group);
+    const int64_t t = row0 + token;
+    const int head = i0 + i - token * p.group + g * p.group;
+    const int parts = end - cut + 1;
+    // (the first part is its block's last item, the others are their blocks' first)
+    auto place = [&](int s) { return (int64_t)(2 * (cut - 1 + s) + (s == 0)) * kRows + i; };
+    constexpr int kEach = kCausalBlocks / 32 + 1;
+    float f[kEach], m = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    for (int k = 0; k < kEach; ++k) {
+        const int s = lane + 32 * k;
+        f[k] = s < parts ? p.part_lse[place(s)] : -INFINITY;
+        m = fmaxf(m, f[k]);
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1)
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
     const float ref = m == -INFINITY ? 0.0f : m;
-    const float f = exp2f((lse - ref) * 1.4426950408889634f);
-    float sum = f;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    for (int k = 0; k < kEach; ++k) {
+        f[k] = exp2f((f[k] - ref) * 1.4426950408889634f);
+        sum += f[k];
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1)
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
     constexpr int N = D / 32;
     float o[N] = {};
-    for (int s0 = 0; s0 < p.splits; s0 += 4) {
-        float in[4][N], w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int s = s0 + k;
-            w[k] = __shfl_sync(0xFFFFFFFFu, f, s & 31);
-            if (s >= p.splits || w[k] == 0.0f) {
-                w[k] = 0.0f;
-                continue;
+    for (int k = 0; k < kEach; ++k) {
+        for (int s0 = 32 * k; s0 < min(parts, 32 * k + 32); s0 += 4) {
+            float in[4][N], w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                w[q] = __shfl_sync(0xFFFFFFFFu, f[k], (s0 + q) & 31);    // 0 past the parts
+                if (w[q] == 0.0f)
+                    continue;
+                const float* at = p.part_o + place(s0 + q) * D + N * lane;
+                if (N == 4)
+                    *reinterpret_cast<float4*>(in[q]) = *reinterpret_cast<const float4*>(at);
+                else
+                    *reinterpret_cast<float2*>(in[q]) = *reinterpret_cast<const float2*>(at);
             }
-            const float* at = p.part_o + (s * n + i) * D + N * lane;
-            if (N == 4)
-                *reinterpret_cast<float4*>(in[k]) = *reinterpret_cast<const float4*>(at);
-            else
-                *reinterpret_cast<float2*>(in[k]) = *reinterpret_cast<const float2*>(at);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    o[e] = w[q] != 0.0f ? fmaf(in[q][e], w[q], o[e]) : o[e];
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int e = 0; e < N; ++e)
-                o[e] = w[k] != 0.0f ? fmaf(in[k][e], w[k], o[e]) : o[e];
     }
-    const int64_t t = i / p.Hq;
-    const int h = static_cast<int>(i - t * p.Hq);
-    T* out = reinterpret_cast<T*>(p.out + t * p.out_row + h * p.out_head) + N * lane;
+    T* out = reinterpret_cast<T*>(p.out + t * p.out_row + head * p.out_head) + N * lane;
     const float inv = sum > 0.0f ? 1.0f / sum : sum;
 #pragma unroll
     for (int e = 0; e < N; ++e)
         out[e] = static_cast<T>(o[e] * inv);
     if (p.lse && lane == 0)
-        p.lse[i] = m == -INFINITY ? m : ref + log2f(sum) * 0.693147180559945309f;
+        p.lse[t * p.Hq + head] = m == -INFINITY ? m : ref + log2f(sum) * 0.693147180559945309f;
 }
 
 template <int D, int MODE>
@@ -913,14 +938,12 @@ cudaError_t causal(const CausalParams& p, cudaStream_t st)
         });
     if (e != cudaSuccess)
         return e;
-    const unsigned blocks = static_cast<unsigned>(std::min(p.items, device_sms()));
-    e = launch_pdl(causal_kernel<D, MODE>, dim3(blocks), dim3(C::kThreads), C::kSmem, st, p);
-    if (e != cudaSuccess || p.splits == 1)
+    e = launch_pdl(causal_kernel<D, MODE>, dim3(p.blocks), dim3(C::kThreads), C::kSmem, st, p);
+    if (e != cudaSuccess || !p.joined)
         return e;
     using T = typename std::conditional<C::kHalfS, __half, __nv_bfloat16>::type;
     count_launch();
-    const unsigned join = static_cast<unsigned>(((int64_t)p.rows * p.Hq + 3) / 4);
-    return launch_pdl(causal_join_kernel<T, D>, dim3(join), dim3(128), 0, st, p);
+    return launch_pdl(causal_join_kernel<T, D>, dim3(p.blocks - 1, kRows / 4), dim3(128), 0, st, p);
 }
 
 template <int MODE>

@@ -27,8 +27,10 @@ struct indexer_attention_s {
 struct indexer_causal_s {
     indexer_causal_spec spec;
     CausalParams p;              // everything but the operands of a call
+    AttnParams rows;             // the same for rows one by one
+    bool by_rows = false;        // which of the two
     int64_t max_pages = 0;       // of the longest request
-    size_t part_rows = 0;        // (row, head, part) triples of split rows
+    size_t part_floats = 0;      // partial vectors
     size_t ws_bytes = 0;
 };
 
@@ -56,6 +58,159 @@ uint64_t phase_increment(double radians)
     const double rest = std::fma(radians, kHi, -turns) + radians * kLo;
     return static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64)) +
            static_cast<uint64_t>(static_cast<int64_t>(std::nearbyint(std::ldexp(rest, 64))));
+}
+
+// Where a call's items do not fill the SMs, the tiles of a row are split.  Two or four splits
+// that all run at once are a cluster, which joins them through its shared memory; more are
+// joined from the workspace by a kernel of its own.  The number that ends first by measured
+// times: 0.65 us a tile, 2 an item, 1.4 for a cluster's join, 1.1 for the kernel's, 0.15 for each
+// part of a row and the parts' bytes at 4 TB/s.  Fitted to 231 calls (16, 32 and 64 heads of 128, 8
+// and 32 of 64, one or four to a cached head, 16-bit and e4m3 caches, both query types; 1 to 200
+// rows of 4 to 64 tiles), each timed whole, in 2 to 64 parts and in clusters of 2 and 4: the chosen
+// number takes 0.5 % longer than the best on average, 12 % at most.  (One row of 64 tiles, 32 heads
+// of 128: 47 us whole, 17.5 in 4, 12.3 in 16, which are chosen, 16.9 in 64.  64 rows of 16 tiles of
+// e4m3: 13.9 in a cluster of 2, 18.8 whole.)  A cluster of 8 does not run on all SMs at once
+// (16 rows 17.5 us against 10.4 in four).
+double row_splits(AttnParams& p, int64_t items, int64_t tiles, int D, int nh)
+{
+    double best = INFINITY;
+    for (int64_t n = 1; n <= std::min<int64_t>(tiles, kMaxSplits) && items * n <= (1 << 30); ++n) {
+        const int64_t per = (tiles + n - 1) / n;
+        if ((tiles + per - 1) / per != n)
+            continue;
+        const double waves = static_cast<double>((items * n + kPlanSms - 1) / kPlanSms);
+        const bool cluster = (n == 2 || n == kMaxCluster) && items * n <= kClusterBlocks;
+        const double bytes = 4.0 * D * nh * (items * n);
+        const double join = n == 1 ? 0.0 : cluster ? 1.4 : 1.1 + 0.15 * n + 1e-6 / 4 * bytes;
+        const double cost = waves * (0.65 * per + 2.0) + join;
+        if (cost < best) {
+            best = cost;
+            p.cluster = cluster;
+            p.splits = static_cast<int32_t>(n);
+            p.split_tiles = static_cast<int32_t>(per);
+        }
+    }
+    return best;
+}
+
+// The tiled form of causal attention: what each block takes, and its time in microseconds.  An item
+// costs its key tiles and as much as kItemTiles of them for its queries and outputs; every block gets
+// an equal run of that, cut where it ends inside an item, or else at the nearest item's end.
+double causal_cuts(CausalParams& p)
+{
+    constexpr double kItemTiles = 2.0, kTileUs = 1.7, kJoinUs = 6.0;
+    int64_t row_tiles = 0;
+    for (int r = 0; r < p.num_requests; ++r) {
+        p.tile_begin[r] = static_cast<int32_t>(row_tiles);
+        const int64_t rows = (int64_t)(p.row_begin[r + 1] - p.row_begin[r]) * p.group;
+        row_tiles += (rows + kCausalRows - 1) / kCausalRows;
+    }
+    p.tile_begin[p.num_requests] = static_cast<int32_t>(row_tiles);
+    const int64_t items = row_tiles * p.Hkv;
+    if (items > (1 << 26))
+        return INFINITY;
+    // Every item's tiles: the same for all heads of a row tile.
+    const auto walk = [&](auto visit) {
+        for (int r = 0; r < p.num_requests; ++r) {
+            const int tokens = p.row_begin[r + 1] - p.row_begin[r];
+            const int keys = p.key_begin[r + 1] - p.key_begin[r];
+            for (int d = p.tile_begin[r]; d < p.tile_begin[r + 1]; ++d) {
+                const int i0 = (d - p.tile_begin[r]) * kCausalRows;
+                const int i1 = std::min(i0 + kCausalRows, tokens * p.group) - 1;
+                visit(d, causal_tiles(keys, tokens, i0 / p.group, i1 / p.group, p.window, p.sinks));
+            }
+        }
+    };
+    double total = 0.0;
+    int64_t tiles = 0;
+    walk([&](int, int n) {
+        total += p.Hkv * (n + kItemTiles);
+        tiles += (int64_t)p.Hkv * n;
+    });
+    double best = INFINITY;
+    for (int cut = 0; cut < 2; ++cut) {
+        CausalParams c = p;
+        c.blocks = static_cast<int32_t>(std::min<int64_t>(
+            kCausalBlocks, cut ? std::max<int64_t>(1, tiles / 4) : std::max<int64_t>(1, items)));
+        const double share = total / c.blocks;
+        c.joined = 0;
+        c.cut_item[0] = c.cut_tile[0] = 0;
+        int b = 1;
+        double done = 0.0, longest = 0.0, begun = 0.0;
+        walk([&](int d, int n) {
+            for (int g = 0; g < p.Hkv; ++g) {
+                const int item = d * p.Hkv + g;
+                const double cost = n + kItemTiles;
+                while (b < c.blocks && b * share < done + cost) {
+                    const double in = b * share - done - kItemTiles;
+                    int at = cut ? static_cast<int>(in + 0.5) : 0;
+                    if (!cut && b * share - done >= cost / 2)
+                        break;                               // (after it)
+                    at = std::min(std::max(at, 0), n);
+                    if (cut && c.cut_item[b - 1] == item)
+                        at = std::max(at, c.cut_tile[b - 1] + 1);   // (no part is empty)
+                    if (at >= n)
+                        break;
+                    c.cut_item[b] = item;
+                    c.cut_tile[b] = at;
+                    c.joined |= at > 0;
+                    const double here = done + (at > 0 ? at + kItemTiles : 0.0);
+                    longest = std::max(longest, here - begun);
+                    begun = done + (at > 0 ? at : 0.0);
+                    ++b;
+                }
+                done += cost;
+            }
+        });
+        longest = std::max(longest, done - begun);
+        for (; b <= c.blocks; ++b) {
+            c.cut_item[b] = static_cast<int32_t>(items);
+            c.cut_tile[b] = 0;
+        }
+        const double time = longest * kTileUs + (c.joined ? kJoinUs : 0.0);
+        if (time < best) {
+            best = time;
+            p = c;
+        }
+    }
+    return best;
+}
+
+// The form for rows one by one, and its time.
+double causal_rows(AttnParams& q, const CausalParams& p, const indexer_causal_spec& s, bool fp8)
+{
+    std::memset(&q, 0, sizeof(q));
+    q.scale_log2 = static_cast<float>(s.scale * 1.4426950408889634);
+    q.rows = p.rows;
+    q.Hq = p.Hq;
+    q.Hkv = p.Hkv;
+    q.group = p.group;
+    q.num_slots = p.num_slots;
+    q.page = p.page;
+    q.by_page = p.by_page;
+    q.window = p.window;
+    q.sinks = p.sinks;
+    q.num_requests = p.num_requests;
+    std::copy(p.row_begin, p.row_begin + p.num_requests + 1, q.row_begin);
+    std::copy(p.key_begin, p.key_begin + p.num_requests + 1, q.key_begin);
+    const int nh = attention_heads_per_tile(p.group, s.dtype, fp8);
+    q.head_tiles = (p.group + nh - 1) / nh;
+    const int64_t items = (int64_t)p.rows * p.Hkv * q.head_tiles;
+    int64_t most = 1;
+    for (int r = 0; r < p.num_requests; ++r) {
+        int64_t keys = p.key_begin[r + 1] - p.key_begin[r];
+        if (p.window > 0)
+            keys = std::min<int64_t>(keys, (int64_t)p.window + p.sinks);
+        if (p.row_begin[r + 1] > p.row_begin[r])
+            most = std::max(most, (keys + kAttnTile - 1) / kAttnTile);
+    }
+    if (items > (1 << 30))
+        return INFINITY;
+    const double cost = row_splits(q, items, most, s.D, nh);
+    q.by_splits = divisor(q.splits);
+    q.by_head_tiles = divisor(q.head_tiles);
+    q.by_hkv = divisor(q.Hkv);
+    return cost;
 }
 
 }  // namespace
@@ -281,18 +436,7 @@ int indexer_attention_create(indexer_plan_t plan, const indexer_attention_spec* 
     p.num_requests = v.R;
     std::copy(v.row_begin, v.row_begin + v.R + 1, p.row_begin);
     std::copy(v.key_begin, v.key_begin + v.R + 1, p.key_begin);
-    // Work items: rows x key/value heads x tiles of query heads, each over the row's key
-    // tiles.  Where they do not fill the SMs, the tiles of a row are split.  Two or four splits
-    // that all run at once are a cluster, which joins them through its shared memory; more are
-    // joined from the workspace by a kernel of its own.  The number that ends first by measured
-    // times: 0.65 us a tile, 2 an item, 1.4 for a cluster's join, 1.1 for the kernel's, 0.15 for each
-    // part of a row and the parts' bytes at 4 TB/s.  Fitted to 231 calls (16, 32 and 64 heads of 128, 8
-    // and 32 of 64, one or four to a cached head, 16-bit and e4m3 caches, both query types; 1 to 200
-    // rows of 4 to 64 tiles), each timed whole, in 2 to 64 parts and in clusters of 2 and 4: the chosen
-    // number takes 0.5 % longer than the best on average, 12 % at most.  (One row of 64 tiles, 32 heads
-    // of 128: 47 us whole, 17.5 in 4, 12.3 in 16, which are chosen, 16.9 in 64.  64 rows of 16 tiles of
-    // e4m3: 13.9 in a cluster of 2, 18.8 whole.)  A cluster of 8 does not run on all SMs at once
-    // (16 rows 17.5 us against 10.4 in four).
+    // Work items: rows x key/value heads x tiles of query heads, each over the row's key tiles.
     const int nh = attention_heads_per_tile(p.group, s->dtype, s->kv_format != IDX_KV_DENSE);
     p.head_tiles = (p.group + nh - 1) / nh;
     const int64_t tiles = (((int64_t)s->num_sel << p.block_shift) + kAttnTile - 1) / kAttnTile;
@@ -301,23 +445,7 @@ int indexer_attention_create(indexer_plan_t plan, const indexer_attention_spec* 
         delete a;
         return IDX_ERR_INVALID_ARG;
     }
-    double best = INFINITY;
-    for (int64_t n = 1; n <= std::min<int64_t>(tiles, kMaxSplits) && items * n <= (1 << 30); ++n) {
-        const int64_t per = (tiles + n - 1) / n;
-        if ((tiles + per - 1) / per != n)
-            continue;
-        const double waves = static_cast<double>((items * n + kPlanSms - 1) / kPlanSms);
-        const bool cluster = (n == 2 || n == kMaxCluster) && items * n <= kClusterBlocks;
-        const double bytes = 4.0 * s->D * nh * (items * n);
-        const double join = n == 1 ? 0.0 : cluster ? 1.4 : 1.1 + 0.15 * n + 1e-6 / 4 * bytes;
-        const double cost = waves * (0.65 * per + 2.0) + join;
-        if (cost < best) {
-            best = cost;
-            p.cluster = cluster;
-            p.splits = static_cast<int32_t>(n);
-            p.split_tiles = static_cast<int32_t>(per);
-        }
-    }
+    row_splits(p, items, tiles, s->D, nh);
     p.by_splits = divisor(p.splits);
     p.by_head_tiles = divisor(p.head_tiles);
     p.by_hkv = divisor(p.Hkv);
@@ -482,50 +610,27 @@ int indexer_causal_attention_create(indexer_plan_t plan, const indexer_causal_sp
     std::copy(v.key_begin, v.key_begin + v.R + 1, p.key_begin);
     if (s->page_size > 0)
         a->max_pages = (v.max_L + (int64_t)s->page_size - 1) / s->page_size;
-    int64_t all = 0, longest = 0, work = 0;
-    for (int r = 0; r < v.R; ++r) {
-        const int64_t rows = (int64_t)(v.row_begin[r + 1] - v.row_begin[r]) * p.group;
-        const int64_t tiles = (rows + kCausalRows - 1) / kCausalRows;
-        int64_t seen = v.L[r];
-        if (p.window > 0)
-            seen = std::min<int64_t>(seen, (int64_t)p.window + p.sinks +
-                                               std::min<int64_t>(rows, kCausalRows) / p.group);
-        const int64_t keys = (seen + 127) / 128;
-        p.tile_begin[r] = static_cast<int32_t>(all);
-        all += tiles;
-        work += tiles * keys;
-        if (tiles > 0)
-            longest = std::max(longest, keys);
-    }
-    p.tile_begin[v.R] = static_cast<int32_t>(all);
-    const int64_t items = all * s->Hkv;
-    work *= s->Hkv;
-    if (items > (1 << 26)) {
+    p.by_page = divisor(std::max(1, s->page_size));
+    p.by_group = divisor(p.group);
+    p.by_hkv = divisor(p.Hkv);
+    const double tiled = causal_cuts(p);
+    const double by_rows = causal_rows(a->rows, p, *s, fp8);
+    if (tiled == INFINITY && by_rows == INFINITY) {
         delete a;
         return IDX_ERR_INVALID_ARG;
     }
-    // Items that do not fill the SMs are split.
-    p.splits = 1;
-    double best = INFINITY;
-    for (int64_t n = 1; n <= std::min<int64_t>(kCausalSplits, std::max<int64_t>(1, longest)); ++n) {
-        const double waves = static_cast<double>((items * n + kPlanSms - 1) / kPlanSms);
-        const double tiles = std::max(static_cast<double>(work) / kPlanSms,
-                                      std::ceil(static_cast<double>(longest) / n));
-        const double bytes = 8.0 * n * v.T * s->Hq * s->D;
-        const double cost = 1.1 * tiles + 2.5 * waves + (n == 1 ? 0.0 : 3.0 + 1e-6 / 4 * bytes);
-        if (cost < best) {
-            best = cost;
-            p.splits = static_cast<int32_t>(n);
-        }
+    a->by_rows = by_rows < tiled;
+    // status word, then the parts of what is cut
+    if (a->by_rows) {
+        const AttnParams& q = a->rows;
+        const int nh = attention_heads_per_tile(q.group, s->dtype, fp8);
+        a->part_floats = q.splits > 1 && !q.cluster
+                             ? (size_t)q.rows * q.Hkv * q.head_tiles * q.splits * nh * (s->D + 2)
+                             : 0;
+    } else {
+        a->part_floats = p.joined ? (size_t)2 * p.blocks * kCausalRows * (s->D + 1) : 0;
     }
-    p.items = static_cast<int32_t>(items * p.splits);
-    p.by_page = divisor(std::max(1, s->page_size));
-    p.by_group = divisor(p.group);
-    p.by_splits = divisor(p.splits);
-    p.by_hkv = divisor(p.Hkv);
-    // status word, then the parts of split rows
-    a->part_rows = p.splits > 1 ? (size_t)p.splits * v.T * s->Hq : 0;
-    a->ws_bytes = 256 + a->part_rows * (s->D + 1) * sizeof(float);
+    a->ws_bytes = 256 + a->part_floats * sizeof(float);
     *out = a;
     if (ws_bytes)
         *ws_bytes = a->ws_bytes;
@@ -568,6 +673,32 @@ int indexer_causal_attention(indexer_causal_t a, const indexer_causal_io* io, vo
         return IDX_ERR_UNSUPPORTED;
     if (a->p.rows == 0)
         return IDX_OK;
+    count_launch();
+    if (a->by_rows) {
+        AttnParams p = a->rows;
+        p.q = static_cast<const uint8_t*>(io->q);
+        p.k = static_cast<const uint8_t*>(io->k);
+        p.v = static_cast<const uint8_t*>(io->v);
+        p.out = static_cast<uint8_t*>(io->out);
+        p.k_scale = io->k_scale;
+        p.v_scale = io->v_scale;
+        p.clen = io->compress_len;
+        p.table = io->page_table;
+        p.lse = io->lse;
+        p.q_row = 2 * io->q_row;
+        p.q_head = 2 * io->q_head;
+        p.k_slot = kb * io->k_slot;
+        p.k_head = kb * io->k_head;
+        p.v_slot = kb * io->v_slot;
+        p.v_head = kb * io->v_head;
+        p.out_row = 2 * io->out_row;
+        p.out_head = 2 * io->out_head;
+        p.ld_table = io->ld_page_table;
+        p.status = static_cast<uint32_t*>(ws);
+        p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
+        p.part_o = p.part_ml + a->part_floats / (s.D + 2) * 2;
+        return finish(launch_attention_range(p, s.D, s.dtype, fp8, static_cast<cudaStream_t>(stream)));
+    }
     CausalParams p = a->p;
     p.q = static_cast<const uint8_t*>(io->q);
     p.k = static_cast<const uint8_t*>(io->k);
@@ -590,8 +721,7 @@ int indexer_causal_attention(indexer_causal_t a, const indexer_causal_io* io, vo
     p.ld_table = io->ld_page_table;
     p.status = static_cast<uint32_t*>(ws);
     p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
-    p.part_lse = p.part_o + a->part_rows * s.D;
-    count_launch();
+    p.part_lse = p.part_o + a->part_floats / (s.D + 1) * s.D;
     return finish(launch_causal(p, s.D, s.dtype, fp8, static_cast<cudaStream_t>(stream)));
 }
 

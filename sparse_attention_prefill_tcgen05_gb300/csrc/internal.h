@@ -486,6 +486,7 @@ struct AttnParams {
     int32_t cluster;             // a row's splits are a cluster's blocks, which join them
     Divisor by_page, by_splits, by_head_tiles, by_hkv;
     int32_t split_tiles;         // key tiles per split
+    int32_t window, sinks;       // ranges: as CausalParams has them
     int32_t num_requests;
     int32_t row_begin[kMaxRequests + 1];
     int32_t key_begin[kMaxRequests + 1];
@@ -493,11 +494,26 @@ struct AttnParams {
 // Query heads of one key/value head that a work item takes together.
 int attention_heads_per_tile(int group, int dtype, bool fp8);
 cudaError_t launch_attention(const AttnParams& p, int D, int dtype, bool fp8, cudaStream_t st);
+// The same over the keys below clen (sel and sel_count unused): all of them, or under a window.
+cudaError_t launch_attention_range(const AttnParams& p, int D, int dtype, bool fp8, cudaStream_t st);
 
 // Causal attention of a batch's rows over the cached keys of their requests.  A work item is
-// (256 (token, query head) rows of a request, key/value head, part of their keys).
+// (256 (token, query head) rows of a request, key/value head); a block takes a run of items' key
+// tiles, which may begin and end inside an item.
 constexpr int kCausalRows = 256;
-constexpr int kCausalSplits = 32;
+constexpr int kCausalBlocks = 152;
+// Tiles of 128 keys that tokens t0..t1 of a request of `tokens` new tokens see where its last token
+// sees all its keys (which is what a plan goes by; their lengths are known on the device).
+__host__ __device__ inline int causal_tiles(int keys, int tokens, int t0, int t1, int window,
+                                            int sinks)
+{
+    const int before = keys - tokens + 1;
+    const int most = before + t1 > 0 ? before + t1 : 0;
+    int n = most;
+    if (window > 0 && before + t0 - window > sinks)
+        n = most - (before + t0 - window) + sinks;
+    return n > 128 ? (n + 127) / 128 : 1;
+}
 struct CausalParams {
     const uint8_t* q;            // byte strides
     const uint8_t* k;
@@ -510,8 +526,8 @@ struct CausalParams {
     float* lse;
     int64_t q_row, q_head, k_slot, k_head, v_slot, v_head, out_row, out_head;
     int64_t ld_table;
-    float* part_o;               // [splits, rows, Hq, D] of split rows
-    float* part_lse;             // [splits, rows, Hq]
+    float* part_o;               // [2 blocks, kCausalRows, D]: parts of a block's first and last item
+    float* part_lse;             // [2 blocks, kCausalRows]
     uint32_t* status;
     float scale_log2;            // scale * log2(e), its magnitude over 16-bit caches
     int32_t negate;              // ... whose scores are then turned over
@@ -519,8 +535,11 @@ struct CausalParams {
     int32_t rows, Hq, Hkv, group;
     int32_t window, sinks;       // window 0: every key below a row's length
     int32_t num_slots, page;
-    int32_t splits, items;
-    Divisor by_page, by_group, by_splits, by_hkv;
+    int32_t blocks;
+    int32_t joined;              // whether an item is cut
+    Divisor by_page, by_group, by_hkv;
+    int32_t cut_item[kCausalBlocks + 1];    // where a block begins: in item, before tile
+    int32_t cut_tile[kCausalBlocks + 1];
     int32_t num_requests;
     int32_t row_begin[kMaxRequests + 1];
     int32_t key_begin[kMaxRequests + 1];
