@@ -26,8 +26,8 @@ namespace {
 //
 // Which keys: row by row those of [len - window, len) and [0, sinks).  An item walks a list of
 // consecutive places: the sinks, then from the first key that any of its rows sees to the last.
-// Roles: a warp lists items, four load keys and values (converting e4m3), two load queries, one issues
-// the products, two warpgroups do softmax and outputs.  All waits are bounded.
+// Roles: four warps load keys and values (converting e4m3), two load queries (one of them lists the
+// items), two issue the products, two warpgroups do softmax and outputs.  All waits are bounded.
 
 constexpr int kModeBf16 = 0, kModeFp16 = 1, kModeFp8Bf16 = 2, kModeFp8Fp16 = 3;
 constexpr int kWaitTries = 1 << 22;     // of about a microsecond at most
@@ -55,15 +55,14 @@ struct Cfg {
     // loads under way before one is waited for
     static constexpr int kLag = kFp8 ? kRaws - 1 : 2;
     static constexpr int kKeyInfo = kKeyRing * (16 + (kFp8 ? 2 * 128 * 4 : 0));
-    static constexpr int kBars = 2 * kStages + 2 + 2 + 2 + 2 + 2 * kInfos + 1;
+    static constexpr int kBars = 2 * kStages + 2 + 4 + 4 + 4 + 2 * kInfos + 2;
     static constexpr int kSmem = kQ + kStages * kStage + kRaws * kRaw + kKeyInfo + kInfos * 48 +
                                  8 * kBars + 16;
     static_assert(kSmem <= kSmemLimit, "tiles do not fit");
     static_assert(kFp8 || kLag <= kStages - 3, "a load is signalled before its place is waited for");
     static_assert(kKeyRing >= kStages / 2 + 2, "key ring");
     static constexpr int kThreads = 512, kLaunchRegs = 128;
-    static constexpr int kSoftmaxRegs = kFp8 ? 184 : 200;
-    static constexpr int kFeedRegs = kFp8 ? 48 : 56, kLoadRegs = kFp8 ? 96 : 56;
+    static constexpr int kSoftmaxRegs = 160, kFeedRegs = 80, kLoadRegs = 112;
     static_assert(2 * kSoftmaxRegs + kFeedRegs + kLoadRegs <= 4 * kLaunchRegs, "registers");
     static constexpr int kTmemO = 256;                  // columns: scores (and weights), then outputs
 };
@@ -160,43 +159,44 @@ causal_kernel(const __grid_constant__ CausalParams p)
     uint8_t* qbuf = sm;                                      // [2 row tiles]
     uint8_t* stages = qbuf + C::kQ;
     uint8_t* raws = stages + C::kStages * C::kStage;
-    uint4* valid = reinterpret_cast<uint4*>(raws + C::kRaws * C::kRaw);     // [kKeyRing] bits
-    float* kscale = reinterpret_cast<float*>(valid + kKeyRing);             // [kKeyRing][128]
+    uint2* valid = reinterpret_cast<uint2*>(raws + C::kRaws * C::kRaw);     // [kKeyRing][2] bits
+    float* kscale = reinterpret_cast<float*>(valid + 2 * kKeyRing);         // [kKeyRing][128]
     float* vscale = kscale + (C::kFp8 ? kKeyRing * 128 : 0);
     Item* infos = reinterpret_cast<Item*>(vscale + (C::kFp8 ? kKeyRing * 128 : 0));
     uint64_t* kv_full = reinterpret_cast<uint64_t*>(infos + kInfos);
     uint64_t* kv_empty = kv_full + C::kStages;
     uint64_t* q_full = kv_empty + C::kStages;
     uint64_t* q_empty = q_full + 1;
-    uint64_t* s_full = q_empty + 1;
-    uint64_t* p_full = s_full + 2;
-    uint64_t* o_full = p_full + 2;
-    uint64_t* info_full = o_full + 2;
+    uint64_t* s_full = q_empty + 1;                          // [2 halves of the keys][2 row tiles]
+    uint64_t* p_full = s_full + 4;
+    uint64_t* pv_done = p_full + 4;
+    uint64_t* info_full = pv_done + 4;
     uint64_t* info_empty = info_full + kInfos;
     uint64_t* drained = info_empty + kInfos;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 2);
     volatile int* ab = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x / 32), 0);
     const int lane = threadIdx.x & 31;
-    constexpr int kMmaWarp = 8, kListWarp = 9, kQWarp = 10, kLoadWarp = 12;
+    constexpr int kMmaWarp = 8, kQWarp = 10, kLoadWarp = 12;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(kv_full + i, 4);
-            mbar_init(kv_empty + i, 1);
+            mbar_init(kv_empty + i, 2);
         }
         mbar_init(q_full, 2);
-        mbar_init(q_empty, 1);
-        for (int i = 0; i < 2; ++i) {
+        mbar_init(q_empty, 2);
+        for (int i = 0; i < 4; ++i) {
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, 4);
-            mbar_init(o_full + i, 1);
+            mbar_init(pv_done + i, 1);
         }
         for (int i = 0; i < kInfos; ++i) {
             mbar_init(info_full + i, 1);
-            mbar_init(info_empty + i, 8 + 1 + 2 + 4);
+            mbar_init(info_empty + i, 8 + 2 + 2 + 4);
         }
         mbar_init(drained, 1);
+        mbar_init(drained + 1, 1);
         *ab = (smem_u32(sm) & 1023u) != 0;
         fence_mbar_init();
     }
@@ -237,14 +237,14 @@ causal_kernel(const __grid_constant__ CausalParams p)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
         const int wg = warp / 4, quad = warp & 3;
         const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-        const uint32_t s_at = tmem + lanes + 128 * wg;
+        const uint32_t s_row = tmem + lanes + 128 * wg;
         const uint32_t o_at = tmem + lanes + C::kTmemO + D * wg;
         // Weights go by a reference that is replaced once a score passes it by kSlack.  fp16 weights
         // end at 2^-24: theirs is 2^-7 of the maximum, so that they keep their 11 bits down to
         // 2^-21 of it and the largest stays below 2^16.
         constexpr float kSlack = C::kHalfP ? 15.0f : 8.0f;
         constexpr float kBelow = C::kHalfP ? 7.0f : 0.0f;
-        uint32_t su = 0, ou = 0;                             // score tiles, items so far
+        uint32_t su = 0;                                     // half tiles so far
         int n = 0;                                           // tiles before this item
         for (int it = 0;; ++it) {
             Item w;
@@ -254,9 +254,9 @@ causal_kernel(const __grid_constant__ CausalParams p)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(info_empty + it % kInfos);
-            const int count = w.tiles - w.tile;
+            const int count = max(w.tiles - w.tile, 0);
             if (128 * wg >= w.rows) {
-                n += max(count, 0);
+                n += count;
                 continue;
             }
             const int i = 128 * wg + 32 * quad + lane;
@@ -270,71 +270,79 @@ causal_kernel(const __grid_constant__ CausalParams p)
             const int c = p.window > 0 ? max(0, len - p.window) - w.off : 0;
             float m = -INFINITY, l = 0.0f;                   // reference and sum
             bool ok = true;
-            for (int j = 0; j < count; ++j, ++su) {
-                ok = wait(s_full + wg, su & 1);
+#pragma unroll 1
+            for (int h = 0; h < 2 * count; ++h, ++su) {
+                const int half = su & 1, ring = (n + h / 2) % kKeyRing;
+                const uint32_t s_at = s_row + 64 * half;
+                ok = wait(s_full + 2 * half + wg, (su >> 1) & 1);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const int e0 = (w.tile + j) * 128, ring = (n + j) % kKeyRing;
-                float x[128];
-#pragma unroll
-                for (int k = 0; k < 128; k += 32)
-                    tmem_ld_32x32b_x32(s_at + k, x + k);
-                const uint4 keys = valid[ring];
+                const int e0 = w.tile * 128 + 64 * h;
+                float x[64];
+                tmem_ld_32x32b_x32(s_at, x);
+                tmem_ld_32x32b_x32(s_at + 32, x + 32);
+                const uint2 keys = valid[2 * ring + half];
+                const bool whole = (e0 + 64 <= a || (e0 >= c && e0 + 64 <= b)) &&
+                                   (keys.x & keys.y) == 0xFFFFFFFFu;
+                const bool all = __all_sync(0xFFFFFFFFu, whole);
                 tmem_wait_ld();
-                if (C::kFp8) {
-                    const float4* ks = reinterpret_cast<const float4*>(kscale + ring * 128);
+                if (C::kFp8) {                               // scores times their key's scale
+                    const float4* ks =
+                        reinterpret_cast<const float4*>(kscale + ring * 128 + 64 * half);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
+                    for (int k = 0; k < 16; ++k) {
                         const float4 f = ks[k];
                         mul2(x[4 * k], x[4 * k + 1], pair(f.x, f.y));
                         mul2(x[4 * k + 2], x[4 * k + 3], pair(f.z, f.w));
                     }
-                } else if (p.negate) {
-#pragma unroll
-                    for (int k = 0; k < 128; ++k)
-                        x[k] = -x[k];
                 }
-                const bool whole = (e0 + 128 <= a || (e0 >= c && e0 + 128 <= b)) &&
-                                   (keys.x & keys.y & keys.z & keys.w) == 0xFFFFFFFFu;
-                if (!__all_sync(0xFFFFFFFFu, whole)) {
+                if (!all) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 2; ++k) {
                         const int e = e0 + 32 * k;
-                        const uint32_t in = k == 0 ? keys.x : k == 1 ? keys.y : k == 2 ? keys.z : keys.w;
-                        const uint32_t see =
-                            (below(a - e) | (below(b - e) & ~below(c - e))) & in;
+                        const uint32_t see = (below(a - e) | (below(b - e) & ~below(c - e))) &
+                                             (k == 0 ? keys.x : keys.y);
 #pragma unroll
                         for (int q = 0; q < 32; ++q)
                             x[32 * k + q] = (see >> q) & 1u ? x[32 * k + q] : -INFINITY;
                     }
                 }
-                float top = max3(x[0], x[1], x[2]);
+                float t4[4];
 #pragma unroll
-                for (int k = 3; k < 127; k += 2)
-                    top = max3(top, x[k], x[k + 1]);
-                top = fmaxf(top, x[127]);
+                for (int k = 0; k < 4; ++k) {
+                    t4[k] = max3(x[16 * k], x[16 * k + 1], x[16 * k + 2]);
+#pragma unroll
+                    for (int q = 3; q < 15; q += 2)
+                        t4[k] = max3(t4[k], x[16 * k + q], x[16 * k + q + 1]);
+                    t4[k] = fmaxf(t4[k], x[16 * k + 15]);
+                }
+                float top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
                 if (!C::kFp8)
                     top *= p.scale_log2;
+                // A new reference for rows whose scores have passed the old one.
                 const bool raise = top > m + kSlack || (m == -INFINITY && top > -INFINITY);
                 if (__any_sync(0xFFFFFFFFu, raise)) {
                     const float to = raise ? top - kBelow : m;
                     const float f = m == -INFINITY ? 0.0f : ex2(m - to);
                     if (__any_sync(0xFFFFFFFFu, raise && m > -INFINITY)) {
-                        // (the products so far were issued before these scores)
+                        // the products so far are complete (these scores told of all but the last)
+                        ok = __all_sync(0xFFFFFFFFu, wait(pv_done + 2 * (half ^ 1) + wg,
+                                                          ((su - 1) >> 1) & 1));
+                        tc_fence_after();
                         const float g = m == -INFINITY ? 1.0f : f;
 #pragma unroll 1
-                        for (int k = 0; k < D; k += 32) {
-                            float v[32];
-                            tmem_ld_32x32b_x32(o_at + k, v);
+                        for (int k = 0; k < D; k += 16) {
+                            float v[16];
+                            tmem_ld_32x32b_x16(o_at + k, v);
                             tmem_wait_ld();
-                            uint32_t r[32];
 #pragma unroll
-                            for (int q = 0; q < 32; ++q)
-                                r[q] = __float_as_uint(v[q] * g);
-                            tmem_st_32x32b_x32(o_at + k, r);
+                            for (int q = 0; q < 16; ++q)
+                                v[q] *= g;
+                            tmem_st_32x32b_x8(o_at + k, v);
+                            tmem_st_32x32b_x8(o_at + k + 8, v + 8);
                         }
                     }
                     l *= f;
@@ -342,69 +350,48 @@ causal_kernel(const __grid_constant__ CausalParams p)
                 }
                 const float ref = m == -INFINITY ? 0.0f : m;
                 const uint64_t mul = pair(p.scale_log2, p.scale_log2), sub = pair(-ref, -ref);
-                uint64_t sum = pair(0.0f, 0.0f);
+                const float2* vs = reinterpret_cast<const float2*>(vscale + ring * 128 + 64 * half);
+                uint32_t r[32], rest[C::kPTerms > 1 ? 32 : 1];
+                uint64_t sum[4] = {};
 #pragma unroll
-                for (int k = 0; k < 128; k += 64) {
-                    uint32_t r[32];
-#pragma unroll
-                    for (int q = 0; q < 64; q += 2) {
-                        float &lo = x[k + q], &hi = x[k + q + 1];
-                        if (C::kFp8)
-                            unpair(add2(pair(lo, hi), sub), lo, hi);
-                        else
-                            fma2(lo, hi, mul, sub);
-                        lo = ex2(lo);
-                        hi = ex2(hi);
-                        sum = add2(sum, pair(lo, hi));
-                        if (!C::kFp8)
-                            r[q / 2] = pack2<C::kHalfP>(lo, hi);
+                for (int q = 0; q < 64; q += 2) {
+                    float lo = x[q], hi = x[q + 1];
+                    if (C::kFp8)
+                        unpair(add2(pair(lo, hi), sub), lo, hi);
+                    else
+                        fma2(lo, hi, mul, sub);
+                    lo = ex2(lo);
+                    hi = ex2(hi);
+                    sum[q / 2 % 4] = add2(sum[q / 2 % 4], pair(lo, hi));
+                    if (C::kFp8) {
+                        const float2 f = vs[q / 2];
+                        mul2(lo, hi, pair(f.x, f.y));
                     }
-                    if (!C::kFp8)
-                        tmem_st_32x32b_x32(s_at + k / 2, r);
+                    r[q / 2] = pack2<C::kHalfP>(lo, hi);
+                    if constexpr (C::kPTerms > 1)            // what is left of them
+                        rest[q / 2] = pack2<false>(lo - __uint_as_float(r[q / 2] << 16),
+                                                   hi - __uint_as_float(r[q / 2] & 0xFFFF0000u));
                 }
-                if (C::kFp8) {
-                    const float4* vs = reinterpret_cast<const float4*>(vscale + ring * 128);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const float4 f = vs[k];
-                        mul2(x[4 * k], x[4 * k + 1], pair(f.x, f.y));
-                        mul2(x[4 * k + 2], x[4 * k + 3], pair(f.z, f.w));
-                    }
-#pragma unroll
-                    for (int term = 0; term < C::kPTerms; ++term) {
-#pragma unroll
-                        for (int k = 0; k < 128; k += 64) {
-                            uint32_t r[32];
-#pragma unroll
-                            for (int q = 0; q < 64; q += 2) {
-                                float &lo = x[k + q], &hi = x[k + q + 1];
-                                const uint32_t h = pack2<false>(lo, hi);
-                                r[q / 2] = h;
-                                if (term + 1 < C::kPTerms) {     // what is left of them
-                                    lo -= __uint_as_float(h << 16);
-                                    hi -= __uint_as_float(h & 0xFFFF0000u);
-                                }
-                            }
-                            tmem_st_32x32b_x32(s_at + 64 * term + k / 2, r);
-                        }
-                    }
-                }
-                float s0, s1;
-                unpair(sum, s0, s1);
-                l += s0 + s1;
+                tmem_st_32x32b_x32(s_at, r);
+                if constexpr (C::kPTerms > 1)
+                    tmem_st_32x32b_x32(s_at + 32, rest);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(p_full + wg);
+                    mbar_arrive(p_full + 2 * half + wg);
+                float s0, s1;
+                unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+                l += s0 + s1;
             }
             if (!ok)
                 break;
-            n += max(count, 0);
+            n += count;
             // ---- output
             if (count > 0) {
-                ok = wait(o_full + wg, ou & 1);
-                ++ou;
+                // (the last scores told of all products but the last two)
+                const uint32_t parity = ((su - 1) >> 1) & 1;
+                ok = wait(pv_done + wg, parity) && wait(pv_done + 2 + wg, parity);
                 if (!__all_sync(0xFFFFFFFFu, ok))
                     break;
                 tc_fence_after();
@@ -565,9 +552,16 @@ causal_kernel(const __grid_constant__ CausalParams p)
                 for (int is_v = 0; is_v < 2; ++is_v) {
                     uint32_t to;
                     if (!C::kFp8) {
-                        ok = __all_sync(0xFFFFFFFFu, wait(kv_empty + st, phase));
-                        if (!ok)
-                            break;
+                        // no place yet: what has been asked for is signalled before the wait
+                        if (!__all_sync(0xFFFFFFFFu, mbar_test_wait(kv_empty + st, phase))) {
+                            if (signalled < loads)
+                                cp_async_wait<0>();
+                            for (; signalled < loads; ++signalled)
+                                signal(signalled & 1);
+                            ok = __all_sync(0xFFFFFFFFu, wait(kv_empty + st, phase));
+                            if (!ok)
+                                break;
+                        }
                         to = smem_u32(stages + st * C::kStage);
                         if (++st == C::kStages) {
                             st = 0;
@@ -579,14 +573,16 @@ causal_kernel(const __grid_constant__ CausalParams p)
                     }
                     const uint8_t* src = is_v ? vh : kh;
                     const int64_t stride = is_v ? p.v_slot : p.k_slot;
+                    // (16-bit vectors: chunk x of row y of eight is at x ^ y)
+                    if (!C::kFp8)
+                        to += (chunk / 8) * C::kAtom + (row0 + sub) * 128 + ((chunk ^ sub) % 8) * 16;
 #pragma unroll
                     for (int k = 0; k < kPer; ++k) {
-                        const int row = k * kAtOnce + sub;
-                        const int32_t s = __shfl_sync(0xFFFFFFFFu, slot, row);
-                        const uint32_t off = C::kFp8 ? k * 512
-                                                     : swizzled((chunk / 8) * C::kAtom +
-                                                                (row0 + row) * 128 + (chunk % 8) * 16);
-                        cp_async16(to + off, src + max(s, 0) * stride, s >= 0);
+                        const int32_t s = __shfl_sync(0xFFFFFFFFu, slot, k * kAtOnce + sub);
+                        const uint32_t at = C::kFp8 ? to + k * 512
+                                                    : (to ^ (k * kAtOnce % 8 * 16)) +
+                                                          k * kAtOnce * 128;
+                        cp_async16(at, src + max(s, 0) * stride, s >= 0);
                     }
                     cp_async_commit();
                     ++loads;
@@ -599,7 +595,7 @@ causal_kernel(const __grid_constant__ CausalParams p)
                         // (the ring's place was last read for a tile whose keys have left their stage)
                         const int ring = n % kKeyRing;
                         if (lane == 0)
-                            reinterpret_cast<uint32_t*>(valid + ring)[warp - kLoadWarp] = bits;
+                            reinterpret_cast<uint32_t*>(valid + 2 * ring)[warp - kLoadWarp] = bits;
                         if (C::kFp8) {
                             kscale[ring * 128 + row0 + lane] = ks;
                             vscale[ring * 128 + row0 + lane] = vs;
@@ -620,18 +616,24 @@ causal_kernel(const __grid_constant__ CausalParams p)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kLaunchRegs));
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kFeedRegs));
-        if (warp == kListWarp) {
-            // ------------------------------------------------------------ items
+        if (warp >= kQWarp) {
+            // ------------------------------------------------- items and queries
+            // Both warps load queries; the first lists the items, two ahead of those it loads for.
             // The block's share of all items' key tiles, as it was planned: from the first's on.
-            int item = p.cut_item[blockIdx.x], from = p.cut_tile[blockIdx.x];
+            int item = p.cut_item[blockIdx.x], begin = p.cut_tile[blockIdx.x];
             const int last_item = p.cut_item[blockIdx.x + 1], end = p.cut_tile[blockIdx.x + 1];
-            for (int it = 0;; ++it, ++item, from = 0) {
+            int listed = 0;
+            bool more = true;
+            auto list = [&] {
+                const int it = listed++;
                 Item w = {};
                 w.tile = -1;
-                const bool more = item < last_item || (item == last_item && from < end);
+                more = item < last_item || (item == last_item && begin < end);
                 if (!__all_sync(0xFFFFFFFFu,
-                                wait(info_empty + it % kInfos, ((it / kInfos) & 1) ^ 1)))
-                    break;
+                                wait(info_empty + it % kInfos, ((it / kInfos) & 1) ^ 1))) {
+                    more = false;
+                    return;
+                }
                 if (more) {
                     const int d = quotient(item, p.by_hkv);
                     w.g = item - d * p.Hkv;
@@ -670,23 +672,29 @@ causal_kernel(const __grid_constant__ CausalParams p)
                         causal_tiles(w.keys, tokens, t0, t1, p.window, p.sinks);
                     const int to = item == last_item ? end : planned;
                     // the part's share of the tiles that there are
-                    w.tile = static_cast<int>((int64_t)from * tiles / planned);
+                    w.tile = static_cast<int>((int64_t)begin * tiles / planned);
                     w.tiles = static_cast<int>((int64_t)to * tiles / planned);
-                    w.part = from > 0 ? 2 * blockIdx.x : to < planned ? 2 * blockIdx.x + 1 : -1;
+                    const int place = 2 * static_cast<int>(blockIdx.x);
+                    w.part = begin > 0 ? place : to < planned ? place + 1 : -1;
                 }
                 if (lane == 0) {
                     infos[it % kInfos] = w;
                     mbar_arrive(info_full + it % kInfos);
                 }
-                if (!more)
-                    break;
-            }
-        } else if (warp == kQWarp || warp == kQWarp + 1) {
-            // ---------------------------------------------------------- queries
+                ++item;
+                begin = 0;
+            };
             constexpr int kPer = D / 8;                      // copies of a vector
             const int from = threadIdx.x - 32 * kQWarp;      // of 64 threads
+            // kStep rows on are some tokens and some heads on, or one token more and a group's heads less
+            const int step_tokens = quotient(64 / kPer, p.by_group);
+            const int step_heads = 64 / kPer - step_tokens * p.group;
+            const int64_t step_bytes = step_tokens * p.q_row + step_heads * p.q_head;
+            const int64_t wrap_bytes = p.q_row - p.group * p.q_head;
             uint32_t u = 0;
             for (int it = 0;; ++it) {
+                while (warp == kQWarp && more && listed < it + 3)
+                    list();
                 Item w;
                 if (!__all_sync(0xFFFFFFFFu, item_of(it, w)))
                     break;
@@ -698,17 +706,29 @@ causal_kernel(const __grid_constant__ CausalParams p)
                 if (!__all_sync(0xFFFFFFFFu, wait(q_empty, (u & 1) ^ 1)))
                     break;
                 ++u;
-                const int rows = w.rows > 128 ? 256 : 128, t0 = p.row_begin[w.r];
+                const int rows = w.rows > 128 ? 256 : 128;
+                // the thread's rows, kStep apart: (token, head of the group)
+                constexpr int kStep = 64 / kPer;
+                const int chunk = from % kPer, first = from / kPer;
+                int token = quotient(w.i0 + first, p.by_group);
+                int head = w.i0 + first - token * p.group;
+                const uint8_t* src = p.q + (int64_t)(p.row_begin[w.r] + token) * p.q_row +
+                                     (int64_t)(w.g * p.group + head) * p.q_head + chunk * 16;
+                uint32_t to = smem_u32(qbuf) + (chunk / 8) * C::kAtom + first * 128;
+                uint32_t in = chunk % 8 * 16;
 #pragma unroll 4
-                for (int x = from; x < rows * kPer; x += 64) {
-                    const int i = x / kPer, c = x % kPer;
-                    const int token = quotient(w.i0 + i, p.by_group);
-                    const int head = w.i0 + i - token * p.group + w.g * p.group;
-                    const bool in = i < w.rows;
-                    const uint32_t off = (i / 128) * C::kStage + (c / 8) * C::kAtom +
-                                         swizzled((i % 128) * 128 + (c % 8) * 16);
-                    cp_async16(smem_u32(qbuf) + off,
-                               in ? p.q + (t0 + token) * p.q_row + head * p.q_head + c * 16 : p.q, in);
+                for (int x = first; x < rows; x += kStep) {
+                    // (row tiles of more than an atom are kStage apart)
+                    const uint32_t at = to + (x / 128) * (C::kStage - 128 * 128) +
+                                        (in ^ ((x & 7) * 16));
+                    cp_async16(at, x < w.rows ? src : p.q, x < w.rows);
+                    to += kStep * 128;
+                    head += step_heads;
+                    src += step_bytes;
+                    if (head >= p.group) {
+                        head -= p.group;
+                        src += wrap_bytes;
+                    }
                 }
                 cp_async_commit();
                 cp_async_wait<0>();
@@ -717,14 +737,19 @@ causal_kernel(const __grid_constant__ CausalParams p)
                 if (lane == 0)
                     mbar_arrive(q_full);
             }
-        } else if (warp == kMmaWarp) {
+        } else {
             // --------------------------------------------------------- products
-            // One elected lane issues everything, in this order: the next scores of a row tile go
-            // over the weights whose product was issued just before.
+            // A warp for each row tile, an elected lane issues everything, in this order: the next
+            // scores of a half go over the weights whose product was issued just before.
             if (elect_one()) {
-                constexpr uint32_t s_desc = idesc_dense(128, 128, C::kHalfS ? 0 : 1, false, false);
+                constexpr uint32_t s_desc = idesc_dense(128, 64, C::kHalfS ? 0 : 1, false, false);
                 constexpr uint32_t o_desc = idesc_dense(128, D, C::kHalfP ? 0 : 1, false, true);
-                uint32_t u = 0, pu0 = 0, pu1 = 0;            // items, weight tiles so far
+                const int rt = warp - kMmaWarp;
+                const uint32_t s_at = tmem + 128 * rt, o_at = tmem + C::kTmemO + D * rt;
+                const uint64_t q = smem_desc(smem_u32(qbuf + rt * C::kStage), 128, 16, 1024);
+                const uint64_t kd = smem_desc(smem_u32(stages), 128, 16, 1024);
+                const uint64_t vd = smem_desc(smem_u32(stages), 128, C::kAtom, 1024);
+                uint32_t u = 0, pu = 0;                      // items, weight tiles so far
                 int st = 0, phase = 0;
                 bool ok = true;
                 auto next = [&](int& s) {                    // a place of the ring and the next one
@@ -737,22 +762,25 @@ causal_kernel(const __grid_constant__ CausalParams p)
                     return r;
                 };
                 auto scores = [&](int half, int place) {
-                    const uint64_t q = smem_desc(smem_u32(qbuf + half * C::kStage), 128, 16, 1024);
-                    const uint64_t k = smem_desc(smem_u32(stages + place * C::kStage), 128, 16, 1024);
+                    const uint64_t k = kd + (place * C::kStage + half * 8192) / 16;
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
                         const int at = ((i / 4) * C::kAtom + (i % 4) * 32) / 16;
-                        mma_f16(tmem + 128 * half, q + at, k + at, s_desc, i > 0);
+                        mma_f16(s_at + 64 * half, q + at, k + at, s_desc, i > 0);
                     }
-                    mma_commit(s_full + half);
+                    mma_commit(s_full + 2 * half + rt);
                 };
                 auto products = [&](int half, int place, bool more) {
-                    const uint64_t v =
-                        smem_desc(smem_u32(stages + place * C::kStage), 128, C::kAtom, 1024);
+                    if (!wait(p_full + 2 * half + rt, pu & 1))
+                        return false;
+                    tc_fence_after();
+                    const uint64_t v = vd + (place * C::kStage + half * 8192) / 16;
 #pragma unroll
-                    for (int i = 0; i < 8 * C::kPTerms; ++i)
-                        mma_f16_tmem(tmem + C::kTmemO + D * half, tmem + 128 * half + 8 * i,
-                                     v + (i % 8) * 128, o_desc, more || i > 0);
+                    for (int i = 0; i < 4 * C::kPTerms; ++i)
+                        mma_f16_tmem(o_at, s_at + 64 * half + 32 * (i / 4) + 8 * (i % 4),
+                                     v + i % 4 * 128, o_desc, more || i > 0);
+                    mma_commit(pv_done + 2 * half + rt);
+                    return true;
                 };
                 for (int it = 0; ok; ++it) {
                     Item w;
@@ -762,50 +790,41 @@ causal_kernel(const __grid_constant__ CausalParams p)
                     const int count = w.tiles - w.tile;
                     if (count <= 0)
                         continue;
-                    const bool two = w.rows > 128;
                     int ks, vs;
-                    ok = wait(q_full, u & 1) && next(ks);
+                    ok = wait(q_full, u & 1);
+                    ++u;
+                    if (128 * rt >= w.rows) {                // no such rows: hand everything on
+                        mbar_arrive(q_empty);
+                        for (int j = 0; j < 2 * count && ok; ++j) {
+                            ok = next(ks);
+                            mbar_arrive(kv_empty + ks);
+                        }
+                        continue;
+                    }
+                    ok = ok && next(ks);
                     if (!ok)
                         break;
-                    ++u;
                     tc_fence_after();
                     scores(0, ks);
-                    if (two)
-                        scores(1, ks);
+                    scores(1, ks);
                     mma_commit(kv_empty + ks);
                     if (count == 1)
                         mma_commit(q_empty);
-                    for (int j = 0; j < count; ++j) {
+                    for (int j = 0; j < count; ++j, ++pu) {
                         const bool last = j + 1 == count;
-                        ok = next(vs) && wait(p_full, pu0 & 1);
+                        ok = next(vs) && products(0, vs, j > 0);
+                        if (ok && !last) {
+                            ok = next(ks);
+                            tc_fence_after();
+                            if (ok)
+                                scores(0, ks);
+                        }
+                        ok = ok && products(1, vs, true);
                         if (!ok)
                             break;
-                        ++pu0;
-                        tc_fence_after();
-                        products(0, vs, j > 0);
-                        if (last) {
-                            mma_commit(o_full);
-                        } else {
-                            ok = next(ks);
-                            if (!ok)
-                                break;
-                            tc_fence_after();
-                            scores(0, ks);
-                        }
-                        if (two) {
-                            ok = wait(p_full + 1, pu1 & 1);
-                            if (!ok)
-                                break;
-                            ++pu1;
-                            tc_fence_after();
-                            products(1, vs, j > 0);
-                            if (last)
-                                mma_commit(o_full + 1);
-                        }
                         mma_commit(kv_empty + vs);
                         if (!last) {
-                            if (two)
-                                scores(1, ks);
+                            scores(1, ks);
                             mma_commit(kv_empty + ks);
                             if (j + 2 == count)
                                 mma_commit(q_empty);
@@ -813,8 +832,8 @@ causal_kernel(const __grid_constant__ CausalParams p)
                     }
                 }
                 // what was issued, and its arrivals, end before the memory goes
-                mma_commit(drained);
-                for (int i = 0; i < kWaitTries && !mbar_try_wait_sleep(drained, 0, 1000u); ++i)
+                mma_commit(drained + rt);
+                for (int i = 0; i < kWaitTries && !mbar_try_wait_sleep(drained + rt, 0, 1000u); ++i)
                     ;
             }
         }

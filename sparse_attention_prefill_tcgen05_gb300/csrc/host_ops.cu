@@ -591,9 +591,7 @@ int indexer_causal_attention_create(indexer_plan_t plan, const indexer_causal_sp
     CausalParams& p = a->p;
     std::memset(&p, 0, sizeof(p));
     const bool fp8 = s->kv_format == IDX_KV_FP8_E4M3;
-    const double scale = s->scale * 1.4426950408889634;
-    p.negate = !fp8 && scale < 0.0;
-    p.scale_log2 = static_cast<float>(p.negate ? -scale : scale);
+    p.scale_log2 = static_cast<float>(s->scale * 1.4426950408889634);
     // (a masked score is -inf, which 0 would make NaN; 2^-100 leaves all weights alike as 0 does)
     if (p.scale_log2 == 0.0f)
         p.scale_log2 = 0x1p-100f;
@@ -613,7 +611,8 @@ int indexer_causal_attention_create(indexer_plan_t plan, const indexer_causal_sp
     p.by_page = divisor(std::max(1, s->page_size));
     p.by_group = divisor(p.group);
     p.by_hkv = divisor(p.Hkv);
-    const double tiled = causal_cuts(p);
+    // (over 16-bit caches the tiled form takes the largest score before the scale)
+    const double tiled = s->scale < 0.0f && !fp8 ? INFINITY : causal_cuts(p);
     const double by_rows = causal_rows(a->rows, p, *s, fp8);
     if (tiled == INFINITY && by_rows == INFINITY) {
         delete a;
