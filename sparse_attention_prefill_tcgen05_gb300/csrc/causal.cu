@@ -54,9 +54,9 @@ struct Cfg {
     static constexpr int kStages = kFp8 ? (D == 64 ? 4 : 3) : (D == 64 ? 8 : 5);
     // loads under way before one is waited for
     static constexpr int kLag = kFp8 ? kRaws - 1 : 2;
-    static constexpr int kKeyInfo = kKeyRing * (16 + (kFp8 ? 2 * 128 * 4 : 0));
+    static constexpr int kKeyInfo = kKeyRing * (32 + (kFp8 ? 2 * 128 * 4 : 0));
     static constexpr int kBars = 2 * kStages + 2 + 4 + 4 + 4 + 2 * kInfos + 2;
-    static constexpr int kSmem = kQ + kStages * kStage + kRaws * kRaw + kKeyInfo + kInfos * 48 +
+    static constexpr int kSmem = kQ + kStages * kStage + kRaws * kRaw + kKeyInfo + kInfos * 64 +
                                  8 * kBars + 16;
     static_assert(kSmem <= kSmemLimit, "tiles do not fit");
     static_assert(kFp8 || kLag <= kStages - 3, "a load is signalled before its place is waited for");
@@ -73,8 +73,12 @@ struct Item {
     int tile, tiles;         // tiles [tile, tiles) of the list; tile < 0: no more items
     int part;                // where a part of an item goes, -1: the whole item
     int base, keys;          // the request's first packed key and its keys
+    int inner, outer;        // places that every row sees: [inner, outer)
+    int pad[2];
+    // Whether a row may be blind to a key of the tile that others see.
+    __device__ __forceinline__ bool edge(int t) const { return t * 128 < inner || t * 128 + 128 > outer; }
 };
-static_assert(sizeof(Item) == 48, "item");
+static_assert(sizeof(Item) == 64, "item");
 
 __device__ __forceinline__ int quotient(int n, const Divisor& d)
 {
@@ -160,7 +164,8 @@ causal_kernel(const __grid_constant__ CausalParams p)
     uint8_t* stages = qbuf + C::kQ;
     uint8_t* raws = stages + C::kStages * C::kStage;
     uint2* valid = reinterpret_cast<uint2*>(raws + C::kRaws * C::kRaw);     // [kKeyRing][2] bits
-    float* kscale = reinterpret_cast<float*>(valid + 2 * kKeyRing);         // [kKeyRing][128]
+    uint2* bad = valid + 2 * kKeyRing;                                      // of values, edge tiles
+    float* kscale = reinterpret_cast<float*>(bad + 2 * kKeyRing);           // [kKeyRing][128]
     float* vscale = kscale + (C::kFp8 ? kKeyRing * 128 : 0);
     Item* infos = reinterpret_cast<Item*>(vscale + (C::kFp8 ? kKeyRing * 128 : 0));
     uint64_t* kv_full = reinterpret_cast<uint64_t*>(infos + kInfos);
@@ -265,11 +270,12 @@ causal_kernel(const __grid_constant__ CausalParams p)
             const int head = w.i0 + i - token * p.group + w.g * p.group;
             const int t = p.row_begin[w.r] + token;
             // places of the list that the row sees: below a, and from c to b
+            // (rows that are none see everything, so that nothing is masked for them)
             const int len = mine ? max(0, min(p.clen[t], w.keys)) : 0;
-            const int a = min(len, p.sinks), b = len - w.off;
+            const int a = min(len, p.sinks), b = mine ? len - w.off : 0x7FFFFFFF;
             const int c = p.window > 0 ? max(0, len - p.window) - w.off : 0;
             float m = -INFINITY, l = 0.0f;                   // reference and sum
-            bool ok = true;
+            bool ok = true, lost = false;
 #pragma unroll 1
             for (int h = 0; h < 2 * count; ++h, ++su) {
                 const int half = su & 1, ring = (n + h / 2) % kKeyRing;
@@ -281,13 +287,42 @@ causal_kernel(const __grid_constant__ CausalParams p)
                 }
                 tc_fence_after();
                 const int e0 = w.tile * 128 + 64 * h;
-                float x[64];
-                tmem_ld_32x32b_x32(s_at, x);
-                tmem_ld_32x32b_x32(s_at + 32, x + 32);
                 const uint2 keys = valid[2 * ring + half];
                 const bool whole = (e0 + 64 <= a || (e0 >= c && e0 + 64 <= b)) &&
                                    (keys.x & keys.y) == 0xFFFFFFFFu;
-                const bool all = __all_sync(0xFFFFFFFFu, whole);
+                if (w.edge(w.tile + h / 2) || !__all_sync(0xFFFFFFFFu, whole)) {
+                    // Masked where they lie: with it in the registers of all tiles, the few that have
+                    // a mask cost the others a sixth of their time.
+                    uint64_t blind = 0;                      // values that are not finite
+                    if (w.edge(w.tile + h / 2)) {
+                        const int load = 2 * (n + h / 2) + 1;
+                        ok = __all_sync(0xFFFFFFFFu, wait(kv_full + load % C::kStages,
+                                                          (load / C::kStages) & 1));
+                        const uint2 v = bad[2 * ring + half];
+                        blind = v.x | static_cast<uint64_t>(v.y) << 32;
+                    }
+#pragma unroll 1
+                    for (int k = 0; k < 64; k += 16) {
+                        const int e = e0 + k;
+                        const uint32_t see = (below(a - e) | (below(b - e) & ~below(c - e))) &
+                                             ((k < 32 ? keys.x : keys.y) >> (k & 16));
+                        // (taken out of the tile; whoever sees one has no number for an output)
+                        if ((see & 0xFFFFu & static_cast<uint32_t>(blind >> k)) != 0u)
+                            lost = true;
+                        float v[16];
+                        tmem_ld_32x32b_x16(s_at + k, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            v[q] = (see >> q) & 1u ? v[q] : -INFINITY;
+                        tmem_st_32x32b_x8(s_at + k, v);
+                        tmem_st_32x32b_x8(s_at + k + 8, v + 8);
+                    }
+                    tmem_wait_st();
+                }
+                float x[64];
+                tmem_ld_32x32b_x32(s_at, x);
+                tmem_ld_32x32b_x32(s_at + 32, x + 32);
                 tmem_wait_ld();
                 if (C::kFp8) {                               // scores times their key's scale
                     const float4* ks =
@@ -297,17 +332,6 @@ causal_kernel(const __grid_constant__ CausalParams p)
                         const float4 f = ks[k];
                         mul2(x[4 * k], x[4 * k + 1], pair(f.x, f.y));
                         mul2(x[4 * k + 2], x[4 * k + 3], pair(f.z, f.w));
-                    }
-                }
-                if (!all) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int e = e0 + 32 * k;
-                        const uint32_t see = (below(a - e) | (below(b - e) & ~below(c - e))) &
-                                             (k == 0 ? keys.x : keys.y);
-#pragma unroll
-                        for (int q = 0; q < 32; ++q)
-                            x[32 * k + q] = (see >> q) & 1u ? x[32 * k + q] : -INFINITY;
                     }
                 }
                 float t4[4];
@@ -396,7 +420,7 @@ causal_kernel(const __grid_constant__ CausalParams p)
                     break;
                 tc_fence_after();
             }
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float inv = lost ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
             const float lse = (m + log2f(l)) * 0.693147180559945309f;
             if (w.part >= 0) {
                 const int64_t at = (int64_t)w.part * kRows + i;
@@ -409,11 +433,13 @@ causal_kernel(const __grid_constant__ CausalParams p)
                     tmem_wait_ld();
                     if (!mine || l == 0.0f)
                         continue;
-                    float4* to = reinterpret_cast<float4*>(p.part_o + at * D + k);
+                    uint32_t r[32];
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        to[q] = make_float4(v[4 * q] * inv, v[4 * q + 1] * inv, v[4 * q + 2] * inv,
-                                            v[4 * q + 3] * inv);
+                    for (int q = 0; q < 32; ++q)
+                        r[q] = __float_as_uint(v[q] * inv);
+#pragma unroll
+                    for (int q = 0; q < 32; q += 8)
+                        stg256(p.part_o + at * D + k + q, r + q);
                 }
             } else {
                 uint8_t* out = p.out + t * p.out_row + head * p.out_head;
@@ -433,10 +459,8 @@ causal_kernel(const __grid_constant__ CausalParams p)
                     if (!mine)
                         continue;
                     if (p.out_vec) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            reinterpret_cast<uint4*>(out + 2 * k)[q] =
-                                make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+                        stg256(out + 2 * k, r);
+                        stg256(out + 2 * k + 32, r + 8);
                     } else {
 #pragma unroll
                         for (int q = 0; q < 16; ++q) {
@@ -466,7 +490,7 @@ causal_kernel(const __grid_constant__ CausalParams p)
         int n = 0;                                           // tiles so far
         bool ok = true;
         // Signal the oldest load (its copies have landed).
-        auto signal = [&](bool is_v) {
+        auto signal = [&](bool is_v, bool edge, int ring) {
             if (C::kFp8) {
                 // into the place, once its last reader has left it
                 ok = __all_sync(0xFFFFFFFFu, ok && wait(kv_empty + st, phase));
@@ -500,6 +524,34 @@ causal_kernel(const __grid_constant__ CausalParams p)
                     phase ^= 1;
                 }
                 done_raw = done_raw + 1 == C::kRaws ? 0 : done_raw + 1;
+            }
+            if (is_v && edge) {
+                // A weight of 0 times a value that is not finite would be NaN in rows that do not see
+                // the key: such vectors become zeros, and rows that see one are told.
+                __syncwarp();
+                uint8_t* v = stages + done_st * C::kStage + (row0 + lane) * 128;
+                using T2 = typename std::conditional<C::kHalfP, __half2, __nv_bfloat162>::type;
+                const T2 none = {0.0f, 0.0f};
+                T2 sum = none;
+#pragma unroll 4
+                for (int x = 0; x < D / 8; ++x) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(
+                        v + (x / 8) * C::kAtom + (((x ^ lane) & 7) << 4));
+                    const T2* two = reinterpret_cast<const T2*>(&w);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        sum = __hfma2(two[k], none, sum);
+                }
+                const float2 f = {static_cast<float>(sum.x), static_cast<float>(sum.y)};
+                const bool not_finite = !(f.x == 0.0f && f.y == 0.0f);
+                const uint32_t bits = __ballot_sync(0xFFFFFFFFu, not_finite);
+                if (not_finite)
+#pragma unroll 1
+                    for (int x = 0; x < D / 8; ++x)
+                        *reinterpret_cast<uint4*>(v + (x / 8) * C::kAtom + (x & 7) * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                if (lane == 0)
+                    reinterpret_cast<uint32_t*>(bad + 2 * ring)[warp - kLoadWarp] = bits;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -535,17 +587,28 @@ causal_kernel(const __grid_constant__ CausalParams p)
                 }
             };
             int loads = 0, signalled = 0;                    // of this item
+            const int n0 = n;
+            auto signal_next = [&] {
+                signal(signalled & 1, w.edge(w.tile + signalled / 2),
+                       (n0 + signalled / 2) % kKeyRing);
+                ++signalled;
+            };
             if (w.tile < w.tiles)
                 look(w.tile);
             for (int tile = w.tile; tile < w.tiles && ok; ++tile, ++n) {
                 const int64_t at = (int64_t)page * p.page + rest;
                 const int32_t slot = page >= 0 && at < p.num_slots ? static_cast<int32_t>(at) : -1;
                 const uint32_t bits = __ballot_sync(0xFFFFFFFFu, slot >= 0);
-                float ks = 0.0f, vs = 0.0f;
+                // (scales of keys that a row sees are positive and finite; others leave -inf and 0 as
+                // they are)
+                float ks = 1.0f, vs = 1.0f;
                 if (C::kFp8 && slot >= 0) {
-                    ks = p.k_scale[(int64_t)slot * p.Hkv + w.g] * p.scale_log2;
+                    ks = p.k_scale[(int64_t)slot * p.Hkv + w.g];
                     vs = p.v_scale[(int64_t)slot * p.Hkv + w.g];
+                    ks = ks > 0.0f && ks < INFINITY ? ks : 1.0f;
+                    vs = vs > 0.0f && vs < INFINITY ? vs : 1.0f;
                 }
+                ks *= p.scale_log2;
                 if (tile + 1 < w.tiles)
                     look(tile + 1);
 #pragma unroll 1
@@ -556,8 +619,8 @@ causal_kernel(const __grid_constant__ CausalParams p)
                         if (!__all_sync(0xFFFFFFFFu, mbar_test_wait(kv_empty + st, phase))) {
                             if (signalled < loads)
                                 cp_async_wait<0>();
-                            for (; signalled < loads; ++signalled)
-                                signal(signalled & 1);
+                            while (signalled < loads)
+                                signal_next();
                             ok = __all_sync(0xFFFFFFFFu, wait(kv_empty + st, phase));
                             if (!ok)
                                 break;
@@ -588,8 +651,7 @@ causal_kernel(const __grid_constant__ CausalParams p)
                     ++loads;
                     if (loads - signalled > C::kLag) {
                         cp_async_wait<C::kLag>();
-                        signal(signalled & 1);
-                        ++signalled;
+                        signal_next();
                     }
                     if (is_v == 0) {
                         // (the ring's place was last read for a tile whose keys have left their stage)
@@ -606,8 +668,8 @@ causal_kernel(const __grid_constant__ CausalParams p)
             // The item's last loads: the next item may be a long wait away.
             if (ok) {
                 cp_async_wait<0>();
-                for (; signalled < loads && ok; ++signalled)
-                    signal(signalled & 1);
+                while (signalled < loads && ok)
+                    signal_next();
             }
         }
         cp_async_wait<0>();                                  // (of a wait that gave up)
@@ -653,20 +715,28 @@ causal_kernel(const __grid_constant__ CausalParams p)
                     w.keys = p.key_begin[lo + 1] - w.base;
                     const int t0 = quotient(w.i0, p.by_group);
                     const int t1 = quotient(w.i0 + w.rows - 1, p.by_group);
-                    int most = 0, least = 0x7FFFFFFF;        // keys of the rows, first key in a window
+                    // the rows' longest and shortest length, their windows' first and last beginning
+                    int most = 0, fewest = 0x7FFFFFFF, least = 0x7FFFFFFF, latest = 0;
                     for (int t = t0 + lane; t <= t1; t += 32) {
                         const int len = max(0, min(p.clen[row0 + t], w.keys));
+                        const int lo = p.window > 0 ? max(0, len - p.window) : 0;
                         most = max(most, len);
+                        fewest = min(fewest, len);
+                        latest = max(latest, lo);
                         if (len > 0)
-                            least = min(least, p.window > 0 ? max(0, len - p.window) : 0);
+                            least = min(least, lo);
                     }
                     most = __reduce_max_sync(0xFFFFFFFFu, most);
+                    fewest = __reduce_min_sync(0xFFFFFFFFu, fewest);
+                    latest = __reduce_max_sync(0xFFFFFFFFu, latest);
                     least = min(__reduce_min_sync(0xFFFFFFFFu, least), most);
                     if (least > p.sinks) {
                         w.sinks = p.sinks;
                         w.off = least - p.sinks;
                     }
                     w.n = most - w.off;
+                    w.inner = latest - w.off;
+                    w.outer = fewest - w.off;
                     const int tiles = (w.n + 127) / 128;
                     const int planned =
                         causal_tiles(w.keys, tokens, t0, t1, p.window, p.sinks);
@@ -686,11 +756,8 @@ causal_kernel(const __grid_constant__ CausalParams p)
             };
             constexpr int kPer = D / 8;                      // copies of a vector
             const int from = threadIdx.x - 32 * kQWarp;      // of 64 threads
-            // kStep rows on are some tokens and some heads on, or one token more and a group's heads less
-            const int step_tokens = quotient(64 / kPer, p.by_group);
-            const int step_heads = 64 / kPer - step_tokens * p.group;
-            const int64_t step_bytes = step_tokens * p.q_row + step_heads * p.q_head;
-            const int64_t wrap_bytes = p.q_row - p.group * p.q_head;
+            // x / group as the high word of a product, exact for x group < 2^32
+            const uint32_t group_inv = p.group > 1 ? 0xFFFFFFFFu / p.group + 1 : 0u;
             uint32_t u = 0;
             for (int it = 0;; ++it) {
                 while (warp == kQWarp && more && listed < it + 3)
@@ -707,28 +774,21 @@ causal_kernel(const __grid_constant__ CausalParams p)
                     break;
                 ++u;
                 const int rows = w.rows > 128 ? 256 : 128;
-                // the thread's rows, kStep apart: (token, head of the group)
+                // row x of the item: (token, head of the group), counted from the first row's token
                 constexpr int kStep = 64 / kPer;
                 const int chunk = from % kPer, first = from / kPer;
-                int token = quotient(w.i0 + first, p.by_group);
-                int head = w.i0 + first - token * p.group;
-                const uint8_t* src = p.q + (int64_t)(p.row_begin[w.r] + token) * p.q_row +
-                                     (int64_t)(w.g * p.group + head) * p.q_head + chunk * 16;
-                uint32_t to = smem_u32(qbuf) + (chunk / 8) * C::kAtom + first * 128;
-                uint32_t in = chunk % 8 * 16;
-#pragma unroll 4
+                const int t0 = quotient(w.i0, p.by_group), h0 = w.i0 - t0 * p.group;
+                const uint8_t* src = p.q + (int64_t)(p.row_begin[w.r] + t0) * p.q_row +
+                                     (int64_t)(w.g * p.group) * p.q_head + chunk * 16;
+                const uint32_t to = smem_u32(qbuf) + (chunk / 8) * C::kAtom;
+#pragma unroll 8
                 for (int x = first; x < rows; x += kStep) {
-                    // (row tiles of more than an atom are kStage apart)
-                    const uint32_t at = to + (x / 128) * (C::kStage - 128 * 128) +
-                                        (in ^ ((x & 7) * 16));
-                    cp_async16(at, x < w.rows ? src : p.q, x < w.rows);
-                    to += kStep * 128;
-                    head += step_heads;
-                    src += step_bytes;
-                    if (head >= p.group) {
-                        head -= p.group;
-                        src += wrap_bytes;
-                    }
+                    const uint32_t token = group_inv ? __umulhi(h0 + x, group_inv) : h0 + x;
+                    const uint32_t head = h0 + x - token * p.group;
+                    const uint8_t* at = src + token * p.q_row + head * p.q_head;
+                    // (row tiles are kStage apart)
+                    const uint32_t off = (x / 128) * C::kStage + x % 128 * 128 + (((chunk ^ x) & 7) << 4);
+                    cp_async16(to + off, x < w.rows ? at : p.q, x < w.rows);
                 }
                 cp_async_commit();
                 cp_async_wait<0>();

@@ -611,8 +611,8 @@ int indexer_causal_attention_create(indexer_plan_t plan, const indexer_causal_sp
     p.by_page = divisor(std::max(1, s->page_size));
     p.by_group = divisor(p.group);
     p.by_hkv = divisor(p.Hkv);
-    // (over 16-bit caches the tiled form takes the largest score before the scale)
-    const double tiled = s->scale < 0.0f && !fp8 ? INFINITY : causal_cuts(p);
+    // (the tiled form masks and takes the largest score before the scale)
+    const double tiled = s->scale < 0.0f ? INFINITY : causal_cuts(p);
     const double by_rows = causal_rows(a->rows, p, *s, fp8);
     if (tiled == INFINITY && by_rows == INFINITY) {
         delete a;
@@ -716,7 +716,7 @@ int indexer_causal_attention(indexer_causal_t a, const indexer_causal_io* io, vo
     p.v_head = kb * io->v_head;
     p.out_row = 2 * io->out_row;
     p.out_head = 2 * io->out_head;
-    p.out_vec = is_aligned(io->out, 16) && p.out_row % 16 == 0 && p.out_head % 16 == 0;
+    p.out_vec = is_aligned(io->out, 32) && p.out_row % 32 == 0 && p.out_head % 32 == 0;
     p.ld_table = io->ld_page_table;
     p.status = static_cast<uint32_t*>(ws);
     p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);

@@ -529,8 +529,8 @@ struct CausalParams {
     float* part_o;               // [2 blocks, kCausalRows, D]: parts of a block's first and last item
     float* part_lse;             // [2 blocks, kCausalRows]
     uint32_t* status;
-    float scale_log2;            // scale * log2(e), not negative over 16-bit caches
-    int32_t out_vec;             // out takes 16-byte stores
+    float scale_log2;            // scale * log2(e), positive
+    int32_t out_vec;             // out takes 32-byte stores
     int32_t rows, Hq, Hkv, group;
     int32_t window, sinks;       // window 0: every key below a row's length
     int32_t num_slots, page;

@@ -234,6 +234,52 @@ def test_what_no_row_sees_has_no_effect(kv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["same", "fp8"])
+@pytest.mark.parametrize("rows,window", [(300, 0), (300, 70), (2, 0)])
+def test_what_some_rows_do_not_see(kv, rows, window):
+    """Values (16-bit) and keys that are not finite change nothing in rows that do not see them, and
+    give none that see them a number where the formula has none."""
+    b = Batch([(rows, 500), (40, 90)], 4, 2, 64, window, 3, kv=kv, page=16, seed=12)
+    want = b.run()
+    first = 500 - rows // 2                                       # keys of the second half's rows
+    at = torch.from_numpy(b.slot_of(0, np.arange(first, 500)))
+    bad = at[::3]
+    sees = np.array([r == 0 and n > first for r, n in zip(b.req, b.lens)])
+
+    def edit(k, v):
+        if kv == "fp8":
+            k[bad[::2].cuda()] = 0x7F
+            v[bad[1::2].cuda()] = 0xFF
+        else:
+            k[bad[::2].cuda(), :, 5] = math.nan
+            v[bad[1::2].cuda(), :, 7] = math.inf
+            v[bad[1::4].cuda(), :, 9] = math.nan
+        return k, v
+    got = b.run(edit=edit)
+    assert torch.equal(got[0][~sees], want[0][~sees]) and torch.equal(got[1][~sees], want[1][~sees])
+    last = [t for t in range(b.T) if sees[t]][-1]
+    assert torch.isnan(got[0][last]).any(-1).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv", ["same", "fp8"])
+def test_gaps_between_windows(kv):
+    """Keys between two rows' windows that neither sees."""
+    lens = [100] * 20 + [950] * 20
+    b = Batch([(40, 1000)], 4, 2, 128, 60, 4, kv=kv, page=16, lens=lens, seed=13)
+    want = b.run()
+    gap = torch.from_numpy(b.slot_of(0, np.arange(100, 890))).cuda()
+
+    def edit(k, v):
+        k[gap], v[gap] = (0x7F, 0x7F) if kv == "fp8" else (math.nan, math.inf)
+        return k, v
+    if kv == "fp8":
+        b.ks[gap.cpu()], b.vs[gap.cpu()] = math.inf, math.nan
+    got = b.run(edit=edit)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
 def test_strides():
     """q, k, v and out as parts of wider tensors; no log-sum-exp asked for; the rest stays."""
     b = Batch([(50, 300)], 4, 2, 64, 40, 2, page=16, seed=8)
