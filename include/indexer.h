@@ -654,7 +654,8 @@ int indexer_causal_attention_create(indexer_plan_t plan, const indexer_causal_sp
                                     indexer_causal_t* out_attention, size_t* workspace_bytes);
 void indexer_causal_attention_destroy(indexer_causal_t attention);
 
-/* Operands of one call, as those of indexer_sparse_attention (rows of k and v any distance apart). */
+/* Operands of one call, as those of indexer_sparse_attention (rows and heads of q, and rows of k and v,
+ * less than 4 GiB apart). */
 typedef struct indexer_causal_io {
     const void* q;
     const void* k;

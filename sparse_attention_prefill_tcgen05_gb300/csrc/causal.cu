@@ -276,54 +276,10 @@ causal_kernel(const __grid_constant__ CausalParams p)
             const int c = p.window > 0 ? max(0, len - p.window) - w.off : 0;
             float m = -INFINITY, l = 0.0f;                   // reference and sum
             bool ok = true, lost = false;
-#pragma unroll 1
-            for (int h = 0; h < 2 * count; ++h, ++su) {
-                const int half = su & 1, ring = (n + h / 2) % kKeyRing;
+            // A half's weights from its scores in x.  Once for tiles that all rows see and once for the
+            // others, whose masks in the same code would cost all tiles a sixth of their time.
+            const auto weigh = [&](float(&x)[64], int ring, int half) {
                 const uint32_t s_at = s_row + 64 * half;
-                ok = wait(s_full + 2 * half + wg, (su >> 1) & 1);
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const int e0 = w.tile * 128 + 64 * h;
-                const uint2 keys = valid[2 * ring + half];
-                const bool whole = (e0 + 64 <= a || (e0 >= c && e0 + 64 <= b)) &&
-                                   (keys.x & keys.y) == 0xFFFFFFFFu;
-                if (w.edge(w.tile + h / 2) || !__all_sync(0xFFFFFFFFu, whole)) {
-                    // Masked where they lie: with it in the registers of all tiles, the few that have
-                    // a mask cost the others a sixth of their time.
-                    uint64_t blind = 0;                      // values that are not finite
-                    if (w.edge(w.tile + h / 2)) {
-                        const int load = 2 * (n + h / 2) + 1;
-                        ok = __all_sync(0xFFFFFFFFu, wait(kv_full + load % C::kStages,
-                                                          (load / C::kStages) & 1));
-                        const uint2 v = bad[2 * ring + half];
-                        blind = v.x | static_cast<uint64_t>(v.y) << 32;
-                    }
-#pragma unroll 1
-                    for (int k = 0; k < 64; k += 16) {
-                        const int e = e0 + k;
-                        const uint32_t see = (below(a - e) | (below(b - e) & ~below(c - e))) &
-                                             ((k < 32 ? keys.x : keys.y) >> (k & 16));
-                        // (taken out of the tile; whoever sees one has no number for an output)
-                        if ((see & 0xFFFFu & static_cast<uint32_t>(blind >> k)) != 0u)
-                            lost = true;
-                        float v[16];
-                        tmem_ld_32x32b_x16(s_at + k, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int q = 0; q < 16; ++q)
-                            v[q] = (see >> q) & 1u ? v[q] : -INFINITY;
-                        tmem_st_32x32b_x8(s_at + k, v);
-                        tmem_st_32x32b_x8(s_at + k + 8, v + 8);
-                    }
-                    tmem_wait_st();
-                }
-                float x[64];
-                tmem_ld_32x32b_x32(s_at, x);
-                tmem_ld_32x32b_x32(s_at + 32, x + 32);
-                tmem_wait_ld();
                 if (C::kFp8) {                               // scores times their key's scale
                     const float4* ks =
                         reinterpret_cast<const float4*>(kscale + ring * 128 + 64 * half);
@@ -407,6 +363,63 @@ causal_kernel(const __grid_constant__ CausalParams p)
                 float s0, s1;
                 unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
                 l += s0 + s1;
+            };
+#pragma unroll 1
+            for (int h = 0; h < 2 * count; ++h, ++su) {
+                const int half = su & 1, ring = (n + h / 2) % kKeyRing;
+                const uint32_t s_at = s_row + 64 * half;
+                ok = wait(s_full + 2 * half + wg, (su >> 1) & 1);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int e0 = w.tile * 128 + 64 * h;
+                float x[64];
+                tmem_ld_32x32b_x32(s_at, x);
+                tmem_ld_32x32b_x32(s_at + 32, x + 32);
+                const uint2 keys = valid[2 * ring + half];
+                const bool edge = w.edge(w.tile + h / 2);
+                tmem_wait_ld();
+                if (edge || (keys.x & keys.y) != 0xFFFFFFFFu) {
+                    uint64_t blind = 0;                      // values that are not finite
+                    if (edge) {
+                        const int load = 2 * (n + h / 2) + 1;
+                        ok = __all_sync(0xFFFFFFFFu, wait(kv_full + load % C::kStages,
+                                                          (load / C::kStages) & 1));
+                        const uint2 v = bad[2 * ring + half];
+                        blind = v.x | static_cast<uint64_t>(v.y) << 32;
+                    }
+                    const bool whole = (e0 + 64 <= a || (e0 >= c && e0 + 64 <= b)) && blind == 0 &&
+                                       (keys.x & keys.y) == 0xFFFFFFFFu;
+                    if (!__all_sync(0xFFFFFFFFu, whole)) {
+                        // masked where they lie, and read again
+#pragma unroll 1
+                        for (int k = 0; k < 64; k += 16) {
+                            const int e = e0 + k;
+                            const uint32_t see = (below(a - e) | (below(b - e) & ~below(c - e))) &
+                                                 ((k < 32 ? keys.x : keys.y) >> (k & 16));
+                            // (taken out of the tile; whoever sees one has no number for an output)
+                            if ((see & 0xFFFFu & static_cast<uint32_t>(blind >> k)) != 0u)
+                                lost = true;
+                            float v[16];
+                            tmem_ld_32x32b_x16(s_at + k, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int q = 0; q < 16; ++q)
+                                v[q] = (see >> q) & 1u ? v[q] : -INFINITY;
+                            tmem_st_32x32b_x8(s_at + k, v);
+                            tmem_st_32x32b_x8(s_at + k + 8, v + 8);
+                        }
+                        tmem_wait_st();
+                        tmem_ld_32x32b_x32(s_at, x);
+                        tmem_ld_32x32b_x32(s_at + 32, x + 32);
+                        tmem_wait_ld();
+                    }
+                    weigh(x, ring, half);
+                } else {
+                    weigh(x, ring, half);
+                }
             }
             if (!ok)
                 break;
@@ -635,7 +648,7 @@ causal_kernel(const __grid_constant__ CausalParams p)
                         raw = raw + 1 == C::kRaws ? 0 : raw + 1;
                     }
                     const uint8_t* src = is_v ? vh : kh;
-                    const int64_t stride = is_v ? p.v_slot : p.k_slot;
+                    const uint32_t stride = static_cast<uint32_t>(is_v ? p.v_slot : p.k_slot);
                     // (16-bit vectors: chunk x of row y of eight is at x ^ y)
                     if (!C::kFp8)
                         to += (chunk / 8) * C::kAtom + (row0 + sub) * 128 + ((chunk ^ sub) % 8) * 16;
@@ -645,7 +658,8 @@ causal_kernel(const __grid_constant__ CausalParams p)
                         const uint32_t at = C::kFp8 ? to + k * 512
                                                     : (to ^ (k * kAtOnce % 8 * 16)) +
                                                           k * kAtOnce * 128;
-                        cp_async16(at, src + max(s, 0) * stride, s >= 0);
+                        cp_async16(at, src + static_cast<uint64_t>(static_cast<uint32_t>(max(s, 0))) * stride,
+                                   s >= 0);
                     }
                     cp_async_commit();
                     ++loads;
@@ -757,6 +771,8 @@ causal_kernel(const __grid_constant__ CausalParams p)
             constexpr int kPer = D / 8;                      // copies of a vector
             const int from = threadIdx.x - 32 * kQWarp;      // of 64 threads
             // x / group as the high word of a product, exact for x group < 2^32
+            const uint32_t q_row = static_cast<uint32_t>(p.q_row);
+            const uint32_t q_head = static_cast<uint32_t>(p.q_head);
             const uint32_t group_inv = p.group > 1 ? 0xFFFFFFFFu / p.group + 1 : 0u;
             uint32_t u = 0;
             for (int it = 0;; ++it) {
@@ -785,7 +801,8 @@ causal_kernel(const __grid_constant__ CausalParams p)
                 for (int x = first; x < rows; x += kStep) {
                     const uint32_t token = group_inv ? __umulhi(h0 + x, group_inv) : h0 + x;
                     const uint32_t head = h0 + x - token * p.group;
-                    const uint8_t* at = src + token * p.q_row + head * p.q_head;
+                    const uint8_t* at = src + static_cast<uint64_t>(token) * q_row +
+                                        static_cast<uint64_t>(head) * q_head;
                     // (row tiles are kStage apart)
                     const uint32_t off = (x / 128) * C::kStage + x % 128 * 128 + (((chunk ^ x) & 7) << 4);
                     cp_async16(to + off, x < w.rows ? at : p.q, x < w.rows);
