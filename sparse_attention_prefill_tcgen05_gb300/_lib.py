@@ -853,30 +853,35 @@ def indexer_attention_join(outs, lses, out=None, lse=None, sink=None, stream=Non
         raise ValueError(f"outs, lses: 1 to {IDX_MAX_PARTS} parts each expected")
     first = outs[0]
     shape, dtype = first.shape, first.dtype
-    code, _ = _dense("outs", first)
+    if len(shape) != 3 or dtype not in _DTYPES:
+        raise ValueError("outs: 3-d bf16, fp16 or fp32 CUDA tensors expected")
     rows, heads, D = shape
+    ml = (rows, heads)
+    parts, part_lses, row, head = [], [], [], []
+    for o, l in zip(outs, lses):
+        if o.shape != shape or o.dtype != dtype or not o.is_cuda:
+            raise ValueError("outs: CUDA tensors of one shape and type expected")
+        if l is None or l.dtype != torch.float32 or l.shape != ml or not l.is_cuda or \
+                not l.is_contiguous():
+            raise ValueError(f"lses: contiguous fp32 CUDA tensors {ml} expected")
+        st = o.stride()
+        if st[2] != 1 and D > 1:
+            raise ValueError("outs: a contiguous last axis expected")
+        parts.append(o.data_ptr())
+        part_lses.append(l.data_ptr())
+        row.append(st[0])
+        head.append(st[1])
     if out is None:
         out = _new(stream, torch.empty, shape, dtype=dtype, device=first.device)
     ocode, so = _dense("out", out)
     if out.shape != shape:
         raise ValueError(f"out: [{rows}, {heads}, {D}] expected")
-    parts, part_lses, row, head = [], [], [], []
-    for o, l in zip(outs, lses):
-        st = _dense("outs", o)[1]
-        if o.shape != shape or o.dtype != dtype:
-            raise ValueError("outs: tensors of one shape and type expected")
-        parts.append(o.data_ptr())
-        if l is None:
-            raise ValueError("lses: a log-sum-exp for every part expected")
-        part_lses.append(_f32("lses", l, shape[:2]))
-        row.append(st[0])
-        head.append(st[1])
     pad = _NO_PARTS[n:]
-    io = _JOIN_IO(*parts, *pad, *part_lses, *pad, *row, *pad, *head, *pad, out.data_ptr(),
-                  _f32("lse", lse, shape[:2]), _f32("sink", sink, (heads,)),
-                  so[0] if rows > 1 else max(so[0], D), so[1] if heads > 1 else max(so[1], D),
-                  n, rows, heads, D, code, ocode)
-    rc = (_lib or lib()).indexer_attention_join(io, _stream(stream))
+    rc = (_lib or lib()).indexer_attention_join(
+        _JOIN_IO(*parts, *pad, *part_lses, *pad, *row, *pad, *head, *pad, out.data_ptr(),
+                 _f32("lse", lse, ml), _f32("sink", sink, (heads,)),
+                 so[0] if rows > 1 else D, so[1] if heads > 1 else D,
+                 n, rows, heads, D, _DTYPES[dtype], ocode), _stream(stream))
     if rc != IDX_OK:
         raise IndexerError("indexer_attention_join", rc)
     return out
@@ -888,9 +893,10 @@ def _matrix(name: str, t, shape, dtype):
         return 0, 0
     if t.shape != shape or t.dtype != dtype or not t.is_cuda:
         raise ValueError(f"{name}: CUDA tensor {tuple(shape)} of {dtype} expected")
-    if not _packed(t):
+    st = t.stride()
+    if st[1] != 1 and shape[1] > 1:
         raise ValueError(f"{name}: a contiguous last axis expected")
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+    return t.data_ptr(), st[0] if shape[0] > 1 else shape[1]
 
 
 def indexer_rms_norm(x, weight=None, eps: float = 1e-6, residual=None, total=None, out=None,
@@ -903,11 +909,11 @@ def indexer_rms_norm(x, weight=None, eps: float = 1e-6, residual=None, total=Non
     if code is None or len(shape) != 2:
         raise ValueError("x: 2-d bf16, fp16 or fp32 CUDA tensor expected")
     rows, n = shape
+    if out is None and codes is None:
+        out = _new(stream, torch.empty, shape, dtype=dtype, device=x.device)
     px, sx = _matrix("x", x, shape, dtype)
     pr, sr = _matrix("residual", residual, shape, dtype)
     pt, st = _matrix("total", total, shape, dtype)
-    if out is None and codes is None:
-        out = _new(stream, torch.empty, shape, dtype=dtype, device=x.device)
     po, so = _matrix("out", out, shape, dtype)
     pw, wcode = 0, code
     if weight is not None:
@@ -920,10 +926,11 @@ def indexer_rms_norm(x, weight=None, eps: float = 1e-6, residual=None, total=Non
         if codes.dtype not in _E4M3 or codes.shape != shape or not codes.is_cuda or \
                 not codes.is_contiguous():
             raise ValueError(f"codes: contiguous CUDA tensor {tuple(shape)} of e4m3 codes expected")
-        if scales is None or scales.dim() != 2 or scales.shape[1] < 1 or n % scales.shape[1] != 0:
+        groups = 0 if scales is None or scales.dim() != 2 else scales.shape[1]
+        if groups < 1 or n % groups != 0:
             raise ValueError("scales: fp32 CUDA tensor [rows, n / group] expected")
-        group = n // scales.shape[1]
-        pc, ps = codes.data_ptr(), _f32("scales", scales, (rows, n // group))
+        group = n // groups
+        pc, ps = codes.data_ptr(), _f32("scales", scales, (rows, groups))
     elif scales is not None:
         raise ValueError("scales: codes expected")
     rc = (_lib or lib()).indexer_rms_norm(
