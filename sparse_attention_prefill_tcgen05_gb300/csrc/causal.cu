@@ -62,7 +62,7 @@ struct Cfg {
     static_assert(kFp8 || kLag <= kStages - 3, "a load is signalled before its place is waited for");
     static_assert(kKeyRing >= kStages / 2 + 2, "key ring");
     static constexpr int kThreads = 512, kLaunchRegs = 128;
-    static constexpr int kSoftmaxRegs = 160, kFeedRegs = 80, kLoadRegs = 112;
+    static constexpr int kSoftmaxRegs = 184, kFeedRegs = 56, kLoadRegs = 88;
     static_assert(2 * kSoftmaxRegs + kFeedRegs + kLoadRegs <= 4 * kLaunchRegs, "registers");
     static constexpr int kTmemO = 256;                  // columns: scores (and weights), then outputs
 };
@@ -251,27 +251,37 @@ causal_kernel(const __grid_constant__ CausalParams p)
         constexpr float kBelow = C::kHalfP ? 7.0f : 0.0f;
         uint32_t su = 0;                                     // half tiles so far
         int n = 0;                                           // tiles before this item
-        for (int it = 0;; ++it) {
-            Item w;
+        const int i = 128 * wg + 32 * quad + lane;           // row of an item
+        // The next item and the thread's row of it, one item ahead: its length is on its way while the
+        // item before is written.
+        Item w;
+        int t = 0, head = 0, row_len = 0, it = 0;
+        auto fetch = [&] {
             const bool more = __all_sync(0xFFFFFFFFu, item_of(it, w));
             if (!more)
-                break;
+                return false;
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(info_empty + it % kInfos);
+            ++it;
+            const int token = quotient(w.i0 + i, p.by_group);
+            head = w.i0 + i - token * p.group + w.g * p.group;
+            t = p.row_begin[w.r] + token;
+            row_len = i < w.rows ? p.clen[t] : 0;
+            return true;
+        };
+        bool more = fetch();
+        while (more) {
             const int count = max(w.tiles - w.tile, 0);
             if (128 * wg >= w.rows) {
                 n += count;
+                more = fetch();
                 continue;
             }
-            const int i = 128 * wg + 32 * quad + lane;
             const bool mine = i < w.rows;
-            const int token = quotient(w.i0 + i, p.by_group);
-            const int head = w.i0 + i - token * p.group + w.g * p.group;
-            const int t = p.row_begin[w.r] + token;
             // places of the list that the row sees: below a, and from c to b
             // (rows that are none see everything, so that nothing is masked for them)
-            const int len = mine ? max(0, min(p.clen[t], w.keys)) : 0;
+            const int len = max(0, min(row_len, w.keys));
             const int a = min(len, p.sinks), b = mine ? len - w.off : 0x7FFFFFFF;
             const int c = p.window > 0 ? max(0, len - p.window) - w.off : 0;
             float m = -INFINITY, l = 0.0f;                   // reference and sum
@@ -425,8 +435,9 @@ causal_kernel(const __grid_constant__ CausalParams p)
                 break;
             n += count;
             // ---- output
+            const int part = w.part, out_t = t, out_head = head;
+            more = fetch();
             if (count > 0) {
-                // (the last scores told of all products but the last two)
                 const uint32_t parity = ((su - 1) >> 1) & 1;
                 ok = wait(pv_done + wg, parity) && wait(pv_done + 2 + wg, parity);
                 if (!__all_sync(0xFFFFFFFFu, ok))
@@ -434,43 +445,41 @@ causal_kernel(const __grid_constant__ CausalParams p)
                 tc_fence_after();
             }
             const float inv = lost ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
-            const float lse = (m + log2f(l)) * 0.693147180559945309f;
-            if (w.part >= 0) {
-                const int64_t at = (int64_t)w.part * kRows + i;
-                if (mine)
-                    p.part_lse[at] = l == 0.0f ? -INFINITY : lse;
-#pragma unroll 1
-                for (int k = 0; k < D && count > 0; k += 32) {
-                    float v[32];
-                    tmem_ld_32x32b_x32(o_at + k, v);
+            const float lse = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+            const int64_t at = (int64_t)part * kRows + i;
+            uint8_t* out = p.out + out_t * p.out_row + out_head * p.out_head;
+            if (mine && part >= 0)
+                p.part_lse[at] = lse;
+            else if (mine && p.lse)
+                p.lse[(int64_t)out_t * p.Hq + out_head] = lse;
+            // (the next columns are read while these are written)
+            float v[2][32];
+            if (count > 0)
+                tmem_ld_32x32b_x32(o_at, v[0]);
+#pragma unroll
+            for (int k = 0; k < D; k += 32) {
+                float(&o)[32] = v[(k / 32) & 1];
+                if (count > 0) {
                     tmem_wait_ld();
-                    if (!mine || l == 0.0f)
-                        continue;
-                    uint32_t r[32];
-#pragma unroll
-                    for (int q = 0; q < 32; ++q)
-                        r[q] = __float_as_uint(v[q] * inv);
-#pragma unroll
-                    for (int q = 0; q < 32; q += 8)
-                        stg256(p.part_o + at * D + k + q, r + q);
+                    if (k + 32 < D)
+                        tmem_ld_32x32b_x32(o_at + k + 32, v[(k / 32 + 1) & 1]);
                 }
-            } else {
-                uint8_t* out = p.out + t * p.out_row + head * p.out_head;
-                if (mine && p.lse)
-                    p.lse[(int64_t)t * p.Hq + head] = l == 0.0f ? -INFINITY : lse;
-#pragma unroll 1
-                for (int k = 0; k < D; k += 32) {
-                    float v[32];
-                    if (count > 0) {
-                        tmem_ld_32x32b_x32(o_at + k, v);
-                        tmem_wait_ld();
+                if (part >= 0) {
+                    if (mine && l != 0.0f) {
+#pragma unroll
+                        for (int q = 0; q < 32; q += 8) {
+                            uint32_t r[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                r[e] = __float_as_uint(o[q + e] * inv);
+                            stg256(p.part_o + at * D + k + q, r);
+                        }
                     }
+                } else if (mine) {
                     uint32_t r[16];
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
-                        r[q] = l == 0.0f ? 0u : pack2<C::kHalfS>(v[2 * q] * inv, v[2 * q + 1] * inv);
-                    if (!mine)
-                        continue;
+                        r[q] = l == 0.0f ? 0u : pack2<C::kHalfS>(o[2 * q] * inv, o[2 * q + 1] * inv);
                     if (p.out_vec) {
                         stg256(out + 2 * k, r);
                         stg256(out + 2 * k + 32, r + 8);
@@ -482,6 +491,7 @@ causal_kernel(const __grid_constant__ CausalParams p)
                         }
                     }
                 }
+                __syncwarp();
             }
             tc_fence_before();
         }

@@ -613,7 +613,13 @@ int indexer_causal_attention_create(indexer_plan_t plan, const indexer_causal_sp
     p.by_hkv = divisor(p.Hkv);
     // (the tiled form masks and takes the largest score before the scale)
     const double tiled = s->scale < 0.0f ? INFINITY : causal_cuts(p);
-    const double by_rows = causal_rows(a->rows, p, *s, fp8);
+    // The form that ends first.  Over 1,350 calls (1 to 32 requests of 1 to 256 rows and 256 to 32,768
+    // keys; 8, 32 and 64 heads, 1 to 16 to a cached one, of 64 and 128, 16-bit and e4m3 caches), each
+    // timed both ways, the chosen one takes 0.2 % longer than the other on average where it loses, 28 %
+    // at most (8.9 us against 11.4): rows one by one for a token or two a request (64 over 16,384 keys, 4
+    // heads of 128: 315 us against 444 in tiles), tiles from about eight (2,048 rows: 0.72 ms against
+    // 8.0).  Tiles of 64 KB take the rows' form 1.3 times as long as what its splits are chosen by.
+    const double by_rows = causal_rows(a->rows, p, *s, fp8) * (s->D == 128 && !fp8 ? 1.3 : 1.0);
     if (tiled == INFINITY && by_rows == INFINITY) {
         delete a;
         return IDX_ERR_INVALID_ARG;
@@ -848,6 +854,7 @@ int indexer_attention_join(const indexer_join_io* io, void* stream)
     c.D = io->D;
     c.part_dtype = io->part_dtype;
     c.out_dtype = io->out_dtype;
+    c.by_heads = divisor(c.heads);
     count_launch();
     return finish(launch_join(c, static_cast<cudaStream_t>(stream)));
 }

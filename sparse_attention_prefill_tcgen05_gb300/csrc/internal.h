@@ -558,6 +558,7 @@ struct JoinCall {
     int64_t out_row, out_head;
     int32_t parts, rows, heads, D;
     int32_t part_dtype, out_dtype;
+    Divisor by_heads;
 };
 cudaError_t launch_join(const JoinCall& c, cudaStream_t st);
 

@@ -251,7 +251,12 @@ cudaError_t norm_of(const NormCall& c, cudaStream_t st)
 //
 // A part whose lse is -inf has no key and is not read.
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;
+
+__device__ __forceinline__ int quotient(int n, const Divisor& d)
+{
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * d.mul) >> d.shift);
+}
 
 // The weights of a vector's parts, relative to their sum (and the sink's part of it), and its lse.
 template <int P>
@@ -291,8 +296,8 @@ join_kernel(const __grid_constant__ JoinCall c)
     const bool on = g < groups && vec < n;
     float lse = 0.0f;
     if (on) {
-        const int64_t t = vec / c.heads;
-        const int h = static_cast<int>(vec - t * c.heads);
+        const int t = quotient(static_cast<int>(vec), c.by_heads);
+        const int h = static_cast<int>(vec) - t * c.heads;
         Eight<T> v[P];
 #pragma unroll
         for (int p = 0; p < P; ++p)
@@ -330,8 +335,8 @@ join_any_kernel(const __grid_constant__ JoinCall c)
     if (vec >= (int64_t)c.rows * c.heads)
         return;
     const int lane = threadIdx.x & 31;
-    const int64_t t = vec / c.heads;
-    const int h = static_cast<int>(vec - t * c.heads);
+    const int t = quotient(static_cast<int>(vec), c.by_heads);
+    const int h = static_cast<int>(vec) - t * c.heads;
     float w[kMaxParts];
     const float lse = join_weights<kMaxParts>(c, vec, h, w);
     for (int e = lane; e < c.D; e += 32) {
