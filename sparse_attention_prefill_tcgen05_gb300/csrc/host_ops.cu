@@ -599,8 +599,9 @@ int indexer_causal_attention_create(indexer_plan_t plan, const indexer_causal_sp
     p.Hq = s->Hq;
     p.Hkv = s->Hkv;
     p.group = s->Hq / s->Hkv;
-    p.window = s->window;
-    p.sinks = s->window > 0 ? s->sinks : 0;
+    // (a window as long as the longest request hides nothing)
+    p.window = s->window < v.max_L ? s->window : 0;
+    p.sinks = p.window > 0 ? std::min(s->sinks, v.max_L) : 0;
     p.num_slots = s->num_slots;
     p.page = s->page_size;
     p.num_requests = v.R;

@@ -171,6 +171,15 @@ def test_lengths_in_any_order(window, sinks, kv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 2 ** 31 - 1), (300, 2 ** 31 - 1), (2, 0), (900, 5), (901, 5)])
+@pytest.mark.parametrize("requests", [[(70, 20), (200, 900)], [(1, 900), (1, 5)]])
+def test_windows_at_their_limits(window, sinks, requests):
+    """Windows and sinks longer than any request, requests with fewer keys than rows."""
+    b = Batch(requests, 4, 2, 64, window, sinks, page=16, seed=14)
+    b.check(*b.run())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kv", ["same", "fp8"])
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 def test_large_scores(dt, kv):
