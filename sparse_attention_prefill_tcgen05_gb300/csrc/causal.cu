@@ -209,6 +209,8 @@ causal_kernel(const __grid_constant__ CausalParams p)
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
+    if (threadIdx.x == 32 * kQWarp && p.q_boxes)
+        tma_prefetch_desc(&p.q_map);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -799,6 +801,24 @@ causal_kernel(const __grid_constant__ CausalParams p)
                 if (!__all_sync(0xFFFFFFFFu, wait(q_empty, (u & 1) ^ 1)))
                     break;
                 ++u;
+                if (p.q_boxes) {
+                    // A box is a row tile's 128 (token, head) pairs, in the tile's own order.  Tokens past
+                    // the request's are another's or zeros, rows that are none.  (By cp.async, 256 rows of
+                    // 128 took 10,000 cycles beside the softmax, most of an item's beginning.)
+                    const int x = warp - kQWarp;
+                    if (lane == 0 && 128 * x < w.rows) {
+                        const int token = p.row_begin[w.r] + quotient(w.i0 + 128 * x, p.by_group);
+                        mbar_arrive_expect_tx(q_full, C::kStage);
+#pragma unroll
+                        for (int k = 0; k < D / 64; ++k)
+                            tma_load_3d(qbuf + x * C::kStage + k * C::kAtom, &p.q_map, q_full, 64 * k,
+                                        w.g * p.group, token);
+                    } else if (lane == 0) {
+                        mbar_arrive(q_full);
+                    }
+                    __syncwarp();
+                    continue;
+                }
                 const int rows = w.rows > 128 ? 256 : 128;
                 // row x of the item: (token, head of the group), counted from the first row's token
                 constexpr int kStep = 64 / kPer;

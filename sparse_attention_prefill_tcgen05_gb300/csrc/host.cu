@@ -710,6 +710,28 @@ int prepare(Ctx& c, const void* q, const float* s_q, const float* w, const void*
 
 namespace idx {
 
+// Boxes of 64 16-bit elements x `box_heads` heads x `box_rows` rows of [rows, heads, D], 128-byte
+// swizzled.  False where the strides (bytes) are none that a map takes.
+bool map_rows(CUtensorMap* m, const void* base, int D, int heads, int rows, int64_t head, int64_t row,
+              int box_heads, int box_rows)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (heads == 1)
+        head = 2 * D;
+    if (rows == 1)
+        row = head * heads;
+    if (!enc || head < 2 * D || row < 2 * D || head >= (1ll << 40) || row >= (1ll << 40))
+        return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)head, (cuuint64_t)row};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
 PlanView plan_view(const indexer_plan_s* p)
 {
     return PlanView{p->R, p->T, p->Lk, p->max_L, p->row_begin.data(), p->key_begin.data(),

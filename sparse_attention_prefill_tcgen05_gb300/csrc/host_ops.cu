@@ -726,6 +726,9 @@ int indexer_causal_attention(indexer_causal_t a, const indexer_causal_io* io, vo
     p.out_row = 2 * io->out_row;
     p.out_head = 2 * io->out_head;
     p.out_vec = is_aligned(io->out, 32) && p.out_row % 32 == 0 && p.out_head % 32 == 0;
+    p.q_boxes = p.group <= 128 && 128 % p.group == 0 &&
+                map_rows(&p.q_map, io->q, s.D, s.Hq, p.rows, p.q_head, p.q_row, p.group,
+                         128 / p.group);
     p.ld_table = io->ld_page_table;
     p.status = static_cast<uint32_t*>(ws);
     p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);

@@ -515,6 +515,8 @@ __host__ __device__ inline int causal_tiles(int keys, int tokens, int t0, int t1
     return n > 128 ? (n + 127) / 128 : 1;
 }
 struct CausalParams {
+    CUtensorMap q_map;           // boxes of 128 rows of queries, 64 elements wide
+    int32_t q_boxes;             // whether it holds: the group divides 128
     const uint8_t* q;            // byte strides
     const uint8_t* k;
     const uint8_t* v;
@@ -544,6 +546,9 @@ struct CausalParams {
     int32_t key_begin[kMaxRequests + 1];
     int32_t tile_begin[kMaxRequests + 1];   // tiles of kCausalRows rows before a request's
 };
+// A map of 16-bit rows [rows, heads, D] (byte strides) for boxes of 64 elements; false: none takes them.
+bool map_rows(CUtensorMap* m, const void* base, int D, int heads, int rows, int64_t head, int64_t row,
+              int box_heads, int box_rows);
 cudaError_t launch_causal(const CausalParams& p, int D, int dtype, bool fp8, cudaStream_t st);
 
 // Attention over disjoint sets of keys, joined by their log-sum-exps.
