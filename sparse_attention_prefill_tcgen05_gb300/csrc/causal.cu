@@ -405,28 +405,18 @@ causal_kernel(const __grid_constant__ CausalParams p)
                     const bool whole = (e0 + 64 <= a || (e0 >= c && e0 + 64 <= b)) && blind == 0 &&
                                        (keys.x & keys.y) == 0xFFFFFFFFu;
                     if (!__all_sync(0xFFFFFFFFu, whole)) {
-                        // masked where they lie, and read again
-#pragma unroll 1
-                        for (int k = 0; k < 64; k += 16) {
-                            const int e = e0 + k;
-                            const uint32_t see = (below(a - e) | (below(b - e) & ~below(c - e))) &
-                                                 ((k < 32 ? keys.x : keys.y) >> (k & 16));
-                            // (taken out of the tile; whoever sees one has no number for an output)
-                            if ((see & 0xFFFFu & static_cast<uint32_t>(blind >> k)) != 0u)
-                                lost = true;
-                            float v[16];
-                            tmem_ld_32x32b_x16(s_at + k, v);
-                            tmem_wait_ld();
 #pragma unroll
-                            for (int q = 0; q < 16; ++q)
-                                v[q] = (see >> q) & 1u ? v[q] : -INFINITY;
-                            tmem_st_32x32b_x8(s_at + k, v);
-                            tmem_st_32x32b_x8(s_at + k + 8, v + 8);
+                        for (int k = 0; k < 2; ++k) {
+                            const int e = e0 + 32 * k;
+                            const uint32_t see = (below(a - e) | (below(b - e) & ~below(c - e))) &
+                                                 (k == 0 ? keys.x : keys.y);
+                            // (taken out of the tile; whoever sees one has no number for an output)
+                            if ((see & static_cast<uint32_t>(blind >> (32 * k))) != 0u)
+                                lost = true;
+#pragma unroll
+                            for (int q = 0; q < 32; ++q)
+                                x[32 * k + q] = (see >> q) & 1u ? x[32 * k + q] : -INFINITY;
                         }
-                        tmem_wait_st();
-                        tmem_ld_32x32b_x32(s_at, x);
-                        tmem_ld_32x32b_x32(s_at + 32, x + 32);
-                        tmem_wait_ld();
                     }
                     weigh(x, ring, half);
                 } else {
