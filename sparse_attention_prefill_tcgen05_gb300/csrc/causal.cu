@@ -14,20 +14,38 @@
 namespace idx {
 namespace {
 
-// A work item is a key/value head and 256 rows of a request.  Rows are
-// (token, query head of the group) pairs in that order, so that a group of any size fills the tensor
-// cores' 128 rows and its heads read each key once.  Per tile of 128 keys and each of the item's two
-// tiles of 128 rows
+// A work item is a key/value head and 256 rows of a request.  Rows are (token, query head of the
+// group) pairs in that order, so that a group of any size fills the tensor cores' 128 rows and its heads
+// read each key once.  Per tile of 128 keys and each of the item's two tiles of 128 rows
 //     S [rows x keys] = Q K^T,   P = exp2(S scale log2(e) - reference),   O += P V
-// with S, P and O in TMEM: a softmax thread owns a row, so its maximum and sum are its own, P goes back
-// over S as the product's first operand, and one row tile's softmax runs under the other's products.
-// The reference follows the row's maximum only when that has grown by kSlack, so that O is seldom
-// rescaled.
+// with S, P and O in TMEM: a softmax thread owns a row, so its maximum and sum are its own, and P goes
+// back over S as the product's first operand.  A tile's keys are two halves of 64, each with scores of
+// its own: while one half is weighed, the product and the next scores of the other run.  The reference
+// follows the row's maximum only when that has grown by kSlack, so that O is seldom rescaled.
 //
 // Which keys: row by row those of [len - window, len) and [0, sinks).  An item walks a list of
-// consecutive places: the sinks, then from the first key that any of its rows sees to the last.
+// consecutive places: the sinks, then from the first key that any of its rows sees to the last.  Every
+// block gets an equal run of all items' key tiles, which may begin and end inside an item (256 items
+// on 152 SMs: 824 us where whole ones took 880); cut items are joined by a kernel of their own.
+//
 // Roles: four warps load keys and values (converting e4m3), two load queries (one of them lists the
 // items), two issue the products, two warpgroups do softmax and outputs.  All waits are bounded.
+//
+// Roundings: scores, maxima, sums and outputs are fp32.  Weights are rounded to the values' type, which
+// the tensor cores take at twice tf32's rate and half its bytes: roundings of 2^-8 of a weight at most, of
+// either sign, so that a bf16 output is off by 0.0024 of its size where fp32 weights leave 0.0017, the
+// output's own rounding.
+//
+// Measured (GB300): 2,048 tokens behind 29,951, 4 x 8 heads of 128, bf16: 708 us (1.47 PFLOP/s, 78 % of the
+// measured matrix rate); three prompts of 2,389 to 7,167 tokens, 8 x 4 heads of 64, fp16: 412 us (0.8
+// PFLOP/s); 16,384 tokens under a window of 1,024, 8 x 8 heads of 128, e4m3: 631 us (0.87 PFLOP/s).  What
+// bounds it: a half's chain in its softmax warp (wait, read, maximum, 64 exponentials, store: about 1,000
+// cycles, of which the exponentials alone are 256), under which the MMAs run (60 % of the tensor pipe at
+// heads of 128); over e4m3 caches also the scales, which every thread reads from shared memory for
+// every key; an item's end and beginning, some 6,000 cycles.  Tried without gain: four softmax
+// warpgroups of a half each (their registers leave room for reading the scores twice only: 515 us for
+// the prompts where two took 465), the next half's scores read ahead (they are seldom there yet, 554),
+// turns between the two warps of an SM's quarter (507).
 
 constexpr int kModeBf16 = 0, kModeFp16 = 1, kModeFp8Bf16 = 2, kModeFp8Fp16 = 3;
 constexpr int kWaitTries = 1 << 22;     // of about a microsecond at most
