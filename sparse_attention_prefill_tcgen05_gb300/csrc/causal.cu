@@ -964,17 +964,16 @@ causal_kernel(const __grid_constant__ CausalParams p)
     }
 }
 
-// Items that end in another block than they began: their parts, weighted by their log-sum-exps.  A
-// block of the grid's x for every cut (the first of an item does it all), a warp a row.  Parts
-// without a key were not written and are not read.
-template <typename T, int D>
+// Items that end in another block than they began: their parts, weighted by their log-sum-exps.  The
+// grid's x is such an item, a warp takes a row, or (W = 4, items of many parts) a block, whose warps take
+// every fourth part: 38 parts of 128 rows one after another took a warp 12 us.  Parts without a key
+// were not written and are not read.
+template <typename T, int D, int W>
 __global__ void __launch_bounds__(128)
 causal_join_kernel(const __grid_constant__ CausalParams p)
 {
     pdl_wait_then_release();
-    const int cut = blockIdx.x + 1, item = p.cut_item[cut];
-    if (p.cut_tile[cut] == 0 || (p.cut_item[cut - 1] == item && p.cut_tile[cut - 1] > 0))
-        return;
+    const int cut = p.first_cut[blockIdx.x], item = p.cut_item[cut];
     int end = cut + 1;                                       // the blocks [cut - 1, end) share it
     while (end < p.blocks && p.cut_item[end] == item && p.cut_tile[end] > 0)
         ++end;
@@ -988,9 +987,10 @@ causal_join_kernel(const __grid_constant__ CausalParams p)
             hi = mid - 1;
     }
     const int i0 = (d - p.tile_begin[r]) * kRows, row0 = p.row_begin[r];
-    const int i = blockIdx.y * 4 + threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int i = blockIdx.y * (4 / W) + warp / W;
     if (i >= min(kRows, (p.row_begin[r + 1] - row0) * p.group - i0))
-        return;
+        return;                                              // (with W = 4 the whole block)
     const int token = quotient(i0 + i, p.by_group);
     const int64_t t = row0 + token;
     const int head = i0 + i - token * p.group + g * p.group;
@@ -1021,14 +1021,17 @@ causal_join_kernel(const __grid_constant__ CausalParams p)
     float o[N] = {};
 #pragma unroll
     for (int k = 0; k < kEach; ++k) {
-        for (int s0 = 32 * k; s0 < min(parts, 32 * k + 32); s0 += 4) {
+        for (int s0 = 32 * k + warp % W; s0 < min(parts, 32 * k + 32); s0 += 4 * W) {
             float in[4][N], w[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                w[q] = __shfl_sync(0xFFFFFFFFu, f[k], (s0 + q) & 31);    // 0 past the parts
+                // (0 past the parts, and past this 32)
+                const int s = s0 + W * q;
+                w[q] = __shfl_sync(0xFFFFFFFFu, f[k], s & 31);
+                w[q] = s < 32 * k + 32 ? w[q] : 0.0f;
                 if (w[q] == 0.0f)
                     continue;
-                const float* at = p.part_o + place(s0 + q) * D + N * lane;
+                const float* at = p.part_o + place(s) * D + N * lane;
                 if (N == 4)
                     *reinterpret_cast<float4*>(in[q]) = *reinterpret_cast<const float4*>(at);
                 else
@@ -1040,6 +1043,19 @@ causal_join_kernel(const __grid_constant__ CausalParams p)
                 for (int e = 0; e < N; ++e)
                     o[e] = w[q] != 0.0f ? fmaf(in[q][e], w[q], o[e]) : o[e];
         }
+    }
+    if constexpr (W > 1) {
+        __shared__ float both[W][D];
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            both[warp][N * lane + e] = o[e];
+        __syncthreads();
+        if (warp > 0)
+            return;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            for (int q = 1; q < W; ++q)
+                o[e] += both[q][N * lane + e];
     }
     T* out = reinterpret_cast<T*>(p.out + t * p.out_row + head * p.out_head) + N * lane;
     const float inv = sum > 0.0f ? 1.0f / sum : sum;
@@ -1077,7 +1093,10 @@ cudaError_t causal(const CausalParams& p, cudaStream_t st)
         return e;
     using T = typename std::conditional<C::kHalfS, __half, __nv_bfloat16>::type;
     count_launch();
-    return launch_pdl(causal_join_kernel<T, D>, dim3(p.blocks - 1, kRows / 4), dim3(128), 0, st, p);
+    if (p.blocks > 4 * p.joined)
+        return launch_pdl(causal_join_kernel<T, D, 4>, dim3(p.joined, p.most_rows), dim3(128), 0, st, p);
+    return launch_pdl(causal_join_kernel<T, D, 1>, dim3(p.joined, (p.most_rows + 3) / 4), dim3(128), 0,
+                      st, p);
 }
 
 template <int MODE>

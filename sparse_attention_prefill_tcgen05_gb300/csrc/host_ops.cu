@@ -95,14 +95,17 @@ double row_splits(AttnParams& p, int64_t items, int64_t tiles, int D, int nh)
 
 // The tiled form of causal attention: what each block takes, and its time in microseconds.  An item
 // costs its key tiles and as much as kItemTiles of them for its queries and outputs; every block gets
-// an equal run of that, cut where it ends inside an item, or else at the nearest item's end.
+// an equal run of that, cut where it ends inside an item, or else at the nearest item's end.  (16 rows over
+// 32,768 keys, 4 x 8 heads of 128: 25 us on 152 blocks, 84 row by row; 2,048 keys 12.9 on 64 blocks.)
 double causal_cuts(CausalParams& p)
 {
-    constexpr double kItemTiles = 2.0, kTileUs = 1.7, kJoinUs = 6.0;
+    constexpr double kItemTiles = 2.0, kTileUs = 2.0, kJoinUs = 5.0, kPartUs = 0.04;
     int64_t row_tiles = 0;
     for (int r = 0; r < p.num_requests; ++r) {
         p.tile_begin[r] = static_cast<int32_t>(row_tiles);
         const int64_t rows = (int64_t)(p.row_begin[r + 1] - p.row_begin[r]) * p.group;
+        p.most_rows = static_cast<int32_t>(
+            std::max<int64_t>(p.most_rows, std::min<int64_t>(rows, kCausalRows)));
         row_tiles += (rows + kCausalRows - 1) / kCausalRows;
     }
     p.tile_begin[p.num_requests] = static_cast<int32_t>(row_tiles);
@@ -128,10 +131,12 @@ double causal_cuts(CausalParams& p)
         tiles += (int64_t)p.Hkv * n;
     });
     double best = INFINITY;
-    for (int cut = 0; cut < 2; ++cut) {
+    // Whole items, or at least four tiles a block, two or one.
+    for (int cut = 0; cut < 8; cut = cut ? 2 * cut : 1) {
         CausalParams c = p;
         c.blocks = static_cast<int32_t>(std::min<int64_t>(
-            kCausalBlocks, cut ? std::max<int64_t>(1, tiles / 4) : std::max<int64_t>(1, items)));
+            kCausalBlocks,
+            cut ? std::max<int64_t>(1, cut * tiles / 4) : std::max<int64_t>(1, items)));
         const double share = total / c.blocks;
         c.joined = 0;
         c.cut_item[0] = c.cut_tile[0] = 0;
@@ -153,7 +158,8 @@ double causal_cuts(CausalParams& p)
                         break;
                     c.cut_item[b] = item;
                     c.cut_tile[b] = at;
-                    c.joined |= at > 0;
+                    if (at > 0 && (c.joined == 0 || c.cut_item[c.first_cut[c.joined - 1]] != item))
+                        c.first_cut[c.joined++] = b;
                     const double here = done + (at > 0 ? at + kItemTiles : 0.0);
                     longest = std::max(longest, here - begun);
                     begun = done + (at > 0 ? at : 0.0);
@@ -167,7 +173,8 @@ double causal_cuts(CausalParams& p)
             c.cut_item[b] = static_cast<int32_t>(items);
             c.cut_tile[b] = 0;
         }
-        const double time = longest * kTileUs + (c.joined ? kJoinUs : 0.0);
+        const double parts = c.joined ? static_cast<double>(c.blocks) / c.joined : 0.0;
+        const double time = longest * kTileUs + (c.joined ? kJoinUs + kPartUs * parts : 0.0);
         if (time < best) {
             best = time;
             p = c;
@@ -616,8 +623,8 @@ int indexer_causal_attention_create(indexer_plan_t plan, const indexer_causal_sp
     const double tiled = s->scale < 0.0f ? INFINITY : causal_cuts(p);
     // The form that ends first.  Over 1,350 calls (1 to 32 requests of 1 to 256 rows and 256 to 32,768
     // keys; 8, 32 and 64 heads, 1 to 16 to a cached one, of 64 and 128, 16-bit and e4m3 caches), each
-    // timed both ways, the chosen one takes 0.2 % longer than the other on average where it loses, 28 %
-    // at most (8.9 us against 11.4): rows one by one for a token or two a request (64 over 16,384 keys, 4
+    // timed both ways, the chosen one takes 0.3 % longer than the better one on average, 21 % at most
+    // (18.6 us against 15.4): rows one by one for a token or two a request (64 over 16,384 keys, 4
     // heads of 128: 315 us against 444 in tiles), tiles from about eight (2,048 rows: 0.72 ms against
     // 8.0).  Tiles of 64 KB take the rows' form 1.3 times as long as what its splits are chosen by.
     const double by_rows = causal_rows(a->rows, p, *s, fp8) * (s->D == 128 && !fp8 ? 1.3 : 1.0);

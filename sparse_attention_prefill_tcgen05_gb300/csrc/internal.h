@@ -537,10 +537,12 @@ struct CausalParams {
     int32_t window, sinks;       // window 0: every key below a row's length
     int32_t num_slots, page;
     int32_t blocks;
-    int32_t joined;              // whether an item is cut
+    int32_t joined;              // items that are cut,
+    int32_t most_rows;           // the most rows that an item has
     Divisor by_page, by_group, by_hkv;
     int32_t cut_item[kCausalBlocks + 1];    // where a block begins: in item, before tile
     int32_t cut_tile[kCausalBlocks + 1];
+    int32_t first_cut[kCausalBlocks];       // of each item that is cut: the first block that begins in it
     int32_t num_requests;
     int32_t row_begin[kMaxRequests + 1];
     int32_t key_begin[kMaxRequests + 1];
