@@ -641,7 +641,7 @@ causal_kernel(const __grid_constant__ CausalParams p)
                     ks = ks > 0.0f && ks < INFINITY ? ks : 1.0f;
                     vs = vs > 0.0f && vs < INFINITY ? vs : 1.0f;
                 }
-                ks *= p.scale_log2;
+                ks = fmaxf(ks * p.scale_log2, 1.17549435e-38f);      // (0 times -inf is none)
                 if (tile + 1 < w.tiles)
                     look(tile + 1);
 #pragma unroll 1

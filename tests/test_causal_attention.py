@@ -208,6 +208,14 @@ def test_scales(scale, kv):
 
 
 @pytest.mark.gpu
+def test_smallest_scales():
+    """Keys of the smallest scale under a small factor, masked and not."""
+    b = Batch([(70, 300)], 4, 2, 64, 60, 3, kv="fp8", scale=2.0 ** -90, seed=15)
+    b.ks[::3] = 2.0 ** -126
+    b.check(*b.run())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kv", ["same", "fp8"])
 @pytest.mark.parametrize("window", [0, 90])
 def test_unmapped_pages(kv, window):
