@@ -735,7 +735,8 @@ int indexer_cache_append(indexer_plan_t plan, indexer_rope_t rope, const indexer
  *   part[p]      [rows, heads, D] of part_dtype, strides in elements (last axis contiguous);
  *   part_lse[p]  float [rows, heads] packed
  *   out          [rows, heads, D] of out_dtype: part_dtype, or any type over IDX_FP32 parts; may be
- *                one of the parts with its strides, else it overlaps none
+ *                one of the parts with its type and strides (others at its address are refused), else it
+ *                overlaps none
  *   lse          float [rows, heads] packed, or NULL; may be one of the parts'
  *   D            1..256; rows * heads below 2^31
  */

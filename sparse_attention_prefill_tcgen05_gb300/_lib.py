@@ -847,7 +847,7 @@ _NO_PARTS = (0,) * IDX_MAX_PARTS
 def indexer_attention_join(outs, lses, out=None, lse=None, sink=None, stream=None):
     """Join attention outputs ``outs`` [rows, heads, D] over disjoint keys by their log-sum-exps
     ``lses`` (fp32 [rows, heads]) into ``out`` (default: a new tensor of their type; may be one of
-    them) and ``lse``; ``sink`` fp32 [heads]: the logit of attending to nothing."""
+    them, as it is) and ``lse``; ``sink`` fp32 [heads]: the logit of attending to nothing."""
     n = len(outs)
     if n < 1 or n > IDX_MAX_PARTS or len(lses) != n:
         raise ValueError(f"outs, lses: 1 to {IDX_MAX_PARTS} parts each expected")

@@ -840,6 +840,12 @@ int indexer_attention_join(const indexer_join_io* io, void* stream)
                               !is_aligned(io->part[p], type_bytes(io->part_dtype)) ||
                               !is_aligned(io->part_lse[p], 4))))
             return IDX_ERR_INVALID_ARG;
+        // (in place a thread overwrites what it alone has read; with another type or stride, what others
+        // are yet to read)
+        if (io->rows > 0 && io->part[p] == io->out &&
+            (io->part_dtype != io->out_dtype || (io->rows > 1 && io->part_row[p] != io->out_row) ||
+             (io->heads > 1 && io->part_head[p] != io->out_head)))
+            return IDX_ERR_INVALID_ARG;
         c.part[p] = io->part[p];
         c.part_lse[p] = io->part_lse[p];
         c.part_row[p] = io->part_row[p];
