@@ -600,16 +600,6 @@ __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_
         : "memory");
 }
 
-// The same for 8 columns of the warp's values as they are.
-__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* v)
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
-                     taddr),
-                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
-                 "r"(v[7])
-                 : "memory");
-}
-
 // D[tmem] (+)= A[tmem] * B[smem]^T, kind::f16: A's rows are lanes, its 16-bit elements two to a
 // column.
 __device__ __forceinline__ void mma_f16_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
