@@ -654,6 +654,11 @@ int indexer_causal_attention_create(indexer_plan_t plan, const indexer_causal_sp
                                     indexer_causal_t* out_attention, size_t* workspace_bytes);
 void indexer_causal_attention_destroy(indexer_causal_t attention);
 
+/* What was chosen: *tiles 1 for tiles of rows, 0 for rows one by one; of the tiles, the blocks that share
+ * them and how many (row tile, key/value head) items are cut between blocks and joined (else 0). */
+int indexer_causal_attention_info(indexer_causal_t attention, int32_t* tiles, int32_t* blocks,
+                                  int32_t* joined);
+
 /* Operands of one call, as those of indexer_sparse_attention (rows and heads of q, and rows of k and v,
  * less than 4 GiB apart). */
 typedef struct indexer_causal_io {

@@ -55,7 +55,8 @@ EXPORTED = ("indexer_plan", "indexer_plan_destroy", "indexer_plan_info", "indexe
             "indexer_attention_create", "indexer_attention_destroy", "indexer_sparse_attention",
             "indexer_mask_blocks", "indexer_cache_append", "indexer_attention_join",
             "indexer_rms_norm", "indexer_causal_attention_create",
-            "indexer_causal_attention_destroy", "indexer_causal_attention")
+            "indexer_causal_attention_destroy", "indexer_causal_attention",
+            "indexer_causal_attention_info")
 IDX_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -177,6 +178,7 @@ def lib():
         L.indexer_causal_attention_destroy.argtypes = [P]
         L.indexer_causal_attention_destroy.restype = None
         L.indexer_causal_attention.argtypes = [P, P, P, sz, P]
+        L.indexer_causal_attention_info.argtypes = [P] + [ctypes.POINTER(ctypes.c_int32)] * 3
         L.indexer_cache_append.argtypes = [P, P, P, P]
         L.indexer_attention_join.argtypes = [P, P]
         L.indexer_rms_norm.argtypes = [P, P]
@@ -720,6 +722,12 @@ class CausalAttention:
         self.kv_shape = (spec.num_slots, spec.Hkv, spec.D)
         self.scale_shape = (spec.num_slots, spec.Hkv)
         self.lse_shape = (rows, spec.Hq)
+
+    def info(self):
+        n = [ctypes.c_int32() for _ in range(3)]
+        _check("indexer_causal_attention_info",
+               lib().indexer_causal_attention_info(self.handle, *map(ctypes.byref, n)))
+        return dict(zip(("tiles", "blocks", "joined"), (x.value for x in n)))
 
     def __del__(self):
         h, self.handle = getattr(self, "handle", None), None

@@ -652,6 +652,20 @@ int indexer_causal_attention_create(indexer_plan_t plan, const indexer_causal_sp
 
 void indexer_causal_attention_destroy(indexer_causal_t a) { delete a; }
 
+int indexer_causal_attention_info(indexer_causal_t a, int32_t* tiles, int32_t* blocks,
+                                  int32_t* joined)
+{
+    if (!a)
+        return IDX_ERR_INVALID_ARG;
+    if (tiles)
+        *tiles = !a->by_rows;
+    if (blocks)
+        *blocks = a->by_rows ? 0 : a->p.blocks;
+    if (joined)
+        *joined = a->by_rows ? 0 : a->p.joined;
+    return IDX_OK;
+}
+
 int indexer_causal_attention(indexer_causal_t a, const indexer_causal_io* io, void* ws,
                              size_t ws_bytes, void* stream)
 {
