@@ -622,6 +622,8 @@ int indexer_mask_blocks(indexer_plan_t plan, const uint8_t* cand_mask, int64_t l
  *   8 significant bits, 11 under fp16 queries, those below 2^-21 of the row's largest with fewer over
  *   fp16 keys).  Keys on negative table entries, or whose slot is not below num_slots, are left out.
  *   Keys that no row of the call sees are not read, or have no effect, whatever they hold.
+ *   A value that is not finite makes its column of the rows that see its key infinite or NaN, and changes
+ *   neither other columns nor other rows (but a score that is not a number leaves its row none).
  *
  * indexer_causal_spec:
  *   Hq, Hkv      query and key/value heads, Hkv divides Hq, Hq <= IDX_MAX_HEADS

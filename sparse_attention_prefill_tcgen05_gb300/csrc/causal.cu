@@ -52,7 +52,7 @@ constexpr int kWaitTries = 1 << 22;     // of about a microsecond at most
 constexpr int kGaveUp = 2;
 constexpr int kSmemLimit = 232448;
 constexpr int kRows = kCausalRows;      // of an item
-constexpr int kInfos = 4;               // items listed ahead
+constexpr int kInfos = 4;               // items listed: the one that is weighed, and ahead
 constexpr int kKeyRing = 8;             // tiles whose keys' validity and scales are kept
 
 template <int D, int MODE>
@@ -170,6 +170,40 @@ __device__ __forceinline__ uint4 of_e4m3x8(uint32_t lo, uint32_t hi)
                       of_e4m3x2<kHalf>(hi & 0xFFFFu), of_e4m3x2<kHalf>(hi >> 16));
 }
 
+// Two fp16 or bf16 numbers, zeros for those that are not finite.
+template <bool kHalf>
+__device__ __forceinline__ uint32_t finite2(uint32_t two)
+{
+    constexpr uint32_t kExponent = kHalf ? 0x7C00u : 0x7F80u;
+    return two & (((two & kExponent) != kExponent ? 0xFFFFu : 0u) |
+                  ((two >> 16 & kExponent) != kExponent ? 0xFFFF0000u : 0u));
+}
+
+// o += those of a cached vector's elements [d, d + 16) that are not finite.  Whether any o is a number.
+template <int MODE>
+__device__ __forceinline__ bool add_not_finite(float (&o)[16], const uint8_t* v, int d)
+{
+    using T = typename std::conditional<MODE == kModeFp16, __half, __nv_bfloat16>::type;
+    constexpr bool kFp8 = MODE >= kModeFp8Bf16;
+    uint4 w[kFp8 ? 1 : 2];
+#pragma unroll
+    for (int k = 0; k < (kFp8 ? 1 : 2); ++k)
+        w[k] = reinterpret_cast<const uint4*>(v)[kFp8 ? d / 16 : d / 8 + k];
+    bool some = false;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+        if (kFp8) {
+            if ((reinterpret_cast<const uint8_t*>(w)[q] & 0x7Fu) == 0x7Fu)
+                o[q] = NAN;
+        } else {
+            const float f = static_cast<float>(reinterpret_cast<const T*>(w)[q]);
+            o[q] += isfinite(f) ? 0.0f : f;
+        }
+        some = some || o[q] == o[q];
+    }
+    return some;
+}
+
 // The low n bits (none below 0, all above 31).
 __device__ __forceinline__ uint32_t below(int n)
 {
@@ -281,12 +315,12 @@ causal_kernel(const __grid_constant__ CausalParams p)
         Item w;
         int t = 0, head = 0, row_len = 0, it = 0;
         auto fetch = [&] {
+            if (it > 0 && lane == 0)
+                mbar_arrive(info_empty + (it - 1) % kInfos);
             const bool more = __all_sync(0xFFFFFFFFu, item_of(it, w));
             if (!more)
                 return false;
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(info_empty + it % kInfos);
             ++it;
             const int token = quotient(w.i0 + i, p.by_group);
             head = w.i0 + i - token * p.group + w.g * p.group;
@@ -309,7 +343,15 @@ causal_kernel(const __grid_constant__ CausalParams p)
             const int a = min(len, p.sinks), b = mine ? len - w.off : 0x7FFFFFFF;
             const int c = p.window > 0 ? max(0, len - p.window) - w.off : 0;
             float m = -INFINITY, l = 0.0f;                   // reference and sum
-            bool ok = true, lost = false;
+            bool ok = true;
+            // halves of which the row lost a value, a bit for as many neighbours as 32 bits need
+            uint32_t lost = 0;
+            const auto bit_of = [&](int h) {
+                return 1u << (h >> max(0, 27 - __clz(2 * count - 1)));
+            };
+            const auto seen = [&](int e) {                   // of 32 places from e on
+                return below(a - e) | (below(b - e) & ~below(c - e));
+            };
             // A half's weights from its scores in x.  Once for tiles that all rows see and once for the
             // others, whose masks in the same code would cost all tiles a sixth of their time.
             const auto weigh = [&](float(&x)[64], int ring, int half) {
@@ -430,11 +472,9 @@ causal_kernel(const __grid_constant__ CausalParams p)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const int e = e0 + 32 * k;
-                            const uint32_t see = (below(a - e) | (below(b - e) & ~below(c - e))) &
-                                                 (k == 0 ? keys.x : keys.y);
-                            // (taken out of the tile; whoever sees one has no number for an output)
+                            const uint32_t see = seen(e) & (k == 0 ? keys.x : keys.y);
                             if ((see & static_cast<uint32_t>(blind >> (32 * k))) != 0u)
-                                lost = true;
+                                lost |= bit_of(h);
 #pragma unroll
                             for (int q = 0; q < 32; ++q)
                                 x[32 * k + q] = (see >> q) & 1u ? x[32 * k + q] : -INFINITY;
@@ -448,6 +488,52 @@ causal_kernel(const __grid_constant__ CausalParams p)
             if (!ok)
                 break;
             n += count;
+            lost = mine ? lost : 0u;
+            if (__any_sync(0xFFFFFFFFu, lost != 0u)) {
+                // Values that are not finite, of keys that some rows do not see, were taken out of their
+                // tiles: rows that see one get it in its column here, from the cache.
+                const uint32_t parity = ((su - 1) >> 1) & 1;
+                ok = wait(pv_done + wg, parity) && wait(pv_done + 2 + wg, parity);
+                if (!__all_sync(0xFFFFFFFFu, ok))
+                    break;
+                tc_fence_after();
+                const Item& s = infos[(it - 1) % kInfos];
+                const uint8_t* vh = p.v + s.g * p.v_head;
+                const int32_t* table = p.table + s.r * p.ld_table;
+#pragma unroll 1
+                for (int d = 0; d < D; d += 16) {
+                    float o[16];
+                    tmem_ld_32x32b_x16(o_at + d, o);
+                    tmem_wait_ld();
+#pragma unroll 1
+                    bool left = lost != 0u;                  // until no column is a number
+#pragma unroll 1
+                    for (int h = 0; left && h < 2 * count; ++h) {
+                        if (!(lost & bit_of(h)) || !s.edge(s.tile + h / 2))
+                            continue;
+#pragma unroll 1
+                        for (int e = s.tile * 128 + 64 * h, end = e + 64; left && e < end; ++e) {
+                            if (!(e < a || (e >= c && e < b)))
+                                continue;
+                            int64_t slot = e < s.sinks ? e : e + s.off;
+                            if (p.page > 0) {
+                                const int pg = quotient(static_cast<int>(slot), p.by_page);
+                                const int page = table[pg];
+                                slot = page < 0 ? -1 : slot + ((int64_t)page - pg) * p.page;
+                            } else {
+                                slot += s.base;
+                            }
+                            if (slot < 0 || slot >= p.num_slots)
+                                continue;
+                            left = add_not_finite<MODE>(o, vh + slot * p.v_slot, d);
+                        }
+                    }
+                    __syncwarp();
+                    tmem_st_32x32b_x8(o_at + d, o);
+                    tmem_st_32x32b_x8(o_at + d + 8, o + 8);
+                }
+                tmem_wait_st();
+            }
             // ---- output
             const int part = w.part, out_t = t, out_head = head;
             more = fetch();
@@ -458,7 +544,7 @@ causal_kernel(const __grid_constant__ CausalParams p)
                     break;
                 tc_fence_after();
             }
-            const float inv = lost ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             const float lse = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
             const int64_t at = (int64_t)part * kRows + i;
             uint8_t* out = p.out + out_t * p.out_row + out_head * p.out_head;
@@ -564,7 +650,7 @@ causal_kernel(const __grid_constant__ CausalParams p)
             }
             if (is_v && edge) {
                 // A weight of 0 times a value that is not finite would be NaN in rows that do not see
-                // the key: such vectors become zeros, and rows that see one are told.
+                // the key: such values become zeros, and rows that see the key are told.
                 __syncwarp();
                 uint8_t* v = stages + done_st * C::kStage + (row0 + lane) * 128;
                 using T2 = typename std::conditional<C::kHalfP, __half2, __nv_bfloat162>::type;
@@ -584,9 +670,11 @@ causal_kernel(const __grid_constant__ CausalParams p)
                 const uint32_t bits = __ballot_sync(0xFFFFFFFFu, not_finite);
                 if (not_finite)
 #pragma unroll 1
-                    for (int x = 0; x < D / 8; ++x)
-                        *reinterpret_cast<uint4*>(v + (x / 8) * C::kAtom + (x & 7) * 16) =
-                            make_uint4(0u, 0u, 0u, 0u);
+                    for (int x = 0; x < D / 4; ++x) {
+                        uint2* two =
+                            reinterpret_cast<uint2*>(v + (x / 16) * C::kAtom + (x & 15) * 8);
+                        *two = make_uint2(finite2<C::kHalfP>(two->x), finite2<C::kHalfP>(two->y));
+                    }
                 if (lane == 0)
                     reinterpret_cast<uint32_t*>(bad + 2 * ring)[warp - kLoadWarp] = bits;
             }
