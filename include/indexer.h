@@ -622,8 +622,9 @@ int indexer_mask_blocks(indexer_plan_t plan, const uint8_t* cand_mask, int64_t l
  *   8 significant bits, 11 under fp16 queries, those below 2^-21 of the row's largest with fewer over
  *   fp16 keys).  Keys on negative table entries, or whose slot is not below num_slots, are left out.
  *   Keys that no row of the call sees are not read, or have no effect, whatever they hold.
- *   A value that is not finite makes its column of the rows that see its key infinite or NaN, and changes
- *   neither other columns nor other rows (but a score that is not a number leaves its row none).
+ *   A value that is not finite makes its column of the rows that see its key infinite or NaN (where the
+ *   key's weight is above 0 in fp32), and changes neither other columns nor other rows.  A score that is
+ *   NaN or +inf leaves its row no number.
  *
  * indexer_causal_spec:
  *   Hq, Hkv      query and key/value heads, Hkv divides Hq, Hq <= IDX_MAX_HEADS
@@ -635,7 +636,8 @@ int indexer_mask_blocks(indexer_plan_t plan, const uint8_t* cand_mask, int64_t l
  *   scale        magnitude at most 1e38
  * indexer_causal_attention_create: host only, needs no GPU, once per batch (plan: its requests, rows
  *   and key counts); *workspace_bytes receives what a call needs: 256 bytes for its status, and
- *   partial results where the rows alone do not fill the GPU.  The plan may be destroyed afterwards.
+ *   partial results where work is cut so that all SMs get an equal share: up to 40 MB at D = 128, 20 at
+ *   64, in tiles.  The plan may be destroyed afterwards.
  */
 typedef struct indexer_causal_spec {
     int32_t Hq;
@@ -737,8 +739,8 @@ int indexer_cache_append(indexer_plan_t plan, indexer_rope_t rope, const indexer
  *     lse[t,h] = log(sum_p exp(lse_p[t,h]) + exp(sink[h])),
  *     out[t,h,:] = sum_p exp(lse_p[t,h] - lse[t,h]) out_p[t,h,:]
  * in fp32 with one rounding.  sink float [heads]: a learned logit of attending to nothing (NULL: none).
- * A part whose lse is -inf takes no part, whatever its output holds; where all are, and there is no
- * sink, out = 0 and lse = -inf.
+ * A part whose lse is -inf, or whose weight is 0 in fp32, takes no part, whatever its output holds; where
+ * all are -inf, and there is no sink, out = 0 and lse = -inf.
  *   part[p]      [rows, heads, D] of part_dtype, strides in elements (last axis contiguous);
  *   part_lse[p]  float [rows, heads] packed
  *   out          [rows, heads, D] of out_dtype: part_dtype, or any type over IDX_FP32 parts; may be

@@ -36,13 +36,15 @@ namespace {
 // either sign, so that a bf16 output is off by 0.0024 of its size where fp32 weights leave 0.0017, the
 // output's own rounding.
 //
-// Measured (GB300): 2,048 tokens behind 29,951, 4 x 8 heads of 128, bf16: 705 us (1.47 PFLOP/s, 78 % of the
-// measured matrix rate); three prompts of 2,389 to 7,167 tokens, 8 x 4 heads of 64, fp16: 409 us (0.8
-// PFLOP/s); 16,384 tokens under a window of 1,024, 8 x 8 heads of 128, e4m3: 629 us (0.88 PFLOP/s).  What
+// Measured (GB300): 2,048 tokens behind 29,951, 4 x 8 heads of 128, bf16: 710 us (1.46 PFLOP/s, 78 % of the
+// measured matrix rate); three prompts of 2,389 to 7,167 tokens, 8 x 4 heads of 64, fp16: 412 us (0.8
+// PFLOP/s); 16,384 tokens under a window of 1,024, 8 x 8 heads of 128, e4m3: 632 us (0.87 PFLOP/s).  What
 // bounds it: a half's chain in its softmax warp (wait, read, maximum, 64 exponentials, store: about 1,000
 // cycles, of which the exponentials alone are 256), under which the MMAs run (60 % of the tensor pipe at
-// heads of 128); over e4m3 caches also the scales, which every thread reads from shared memory for
-// every key; an item's end and beginning, some 6,000 cycles.  Tried without gain: four softmax
+// heads of 128); an item's end and beginning, some 6,000 cycles.  Over e4m3 caches a tile of heads of 128
+// takes 2.9 us with both row tiles and 2.4 with one (16-bit ones 2.3 and 1.8): not the scales that every
+// softmax thread reads alone, which would halve; how much the loading warps' conversions cost is not
+// measured.  Tried without gain: four softmax
 // warpgroups of a half each (their registers leave room for reading the scores twice only: 515 us for
 // the prompts where two took 465), the next half's scores read ahead (they are seldom there yet, 554),
 // turns between the two warps of an SM's quarter (507).
@@ -82,7 +84,8 @@ struct Cfg {
     // Registers: what is traded was launched with, 512 threads of 128.  The softmax holds a half's scores
     // and weights, and two outputs' columns at an item's end; loading warps convert four e4m3 vectors at a
     // time.  (176, 64 and 96 the same over 16-bit caches, 676 us against 657 under a window of e4m3 keys;
-    // 200, 56 and 56 838.)
+    // 200, 56 and 56 838.)  fp16 over e4m3, whose weights have two terms, spills 100 bytes a thread at heads
+    // of 128 and 52 at 64; the split was not tried for it.
     static constexpr int kThreads = 512, kLaunchRegs = 128;
     static constexpr int kSoftmaxRegs = 184, kFeedRegs = 56, kLoadRegs = 88;
     static_assert(2 * kSoftmaxRegs + kFeedRegs + kLoadRegs <= 4 * kLaunchRegs, "registers");

@@ -623,10 +623,12 @@ int indexer_causal_attention_create(indexer_plan_t plan, const indexer_causal_sp
     const double tiled = s->scale < 0.0f ? INFINITY : causal_cuts(p);
     // The form that ends first.  Over 1,350 calls (1 to 32 requests of 1 to 256 rows and 256 to 32,768
     // keys; 8, 32 and 64 heads, 1 to 16 to a cached one, of 64 and 128, 16-bit and e4m3 caches), each
-    // timed both ways, the chosen one takes 0.3 % longer than the better one on average, 21 % at most
-    // (18.6 us against 15.4): rows one by one for a token or two a request (64 over 16,384 keys, 4
-    // heads of 128: 315 us against 444 in tiles), tiles from about eight (2,048 rows: 0.72 ms against
-    // 8.0).  Tiles of 64 KB take the rows' form 1.3 times as long as what its splits are chosen by.
+    // timed both ways, the chosen one takes 0.6 % longer than the better one on average, six calls more
+    // than 20 %, 38 % at most (four requests of two tokens over 32,768 bf16 keys, 8 heads of 128: 122
+    // us against 89 in tiles, which take 1.6 us each there, not kTileUs): rows one by one for a token
+    // or two a request (64 over 16,384 keys, 4 heads of 128: 322 us against 444 in tiles), tiles from
+    // about eight (2,048 rows: 0.71 ms against 8.0).  Tiles of 64 KB take the rows' form 1.3 times as
+    // long as what its splits are chosen by.
     const double by_rows = causal_rows(a->rows, p, *s, fp8) * (s->D == 128 && !fp8 ? 1.3 : 1.0);
     if (tiled == INFINITY && by_rows == INFINITY) {
         delete a;

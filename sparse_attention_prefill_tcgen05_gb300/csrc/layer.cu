@@ -47,7 +47,8 @@ __device__ __forceinline__ float block_reduce(float v, float* part)
 // A block per row, which stays in registers (one read of it, one write of each output): eights of
 // neighbours, V a thread, a warp's side by side, so that a group's eights are neighbouring lanes.  16,384
 // rows of 7,168 bf16 with residual and e4m3 codes: 170 us (6.2 TB/s of the 6.8 a copy reaches), HBM
-// bounds it; 64 rows 12 us, the call on the host.
+// bounds it; 64 rows 12 us, the call on the host.  Rows above 32,768 elements (V = 8) do not fit: some 5 KB
+// a thread go through local memory, and 256 rows of 65,536 take 176 us, of 32,768 16.
 template <typename T, typename W, int V>
 __global__ void __launch_bounds__(1024)
 norm_kernel(const __grid_constant__ NormCall c)

@@ -502,9 +502,10 @@ __device__ __forceinline__ int32_t append_slot(const AppendCall& c, int t)
 // the rotation's tiling, or for e4m3 the cache writes'.  The first vectors' loads are under way
 // while the block's threads look up its rows' slots (position, page, slot: two reads one after the
 // other) and compute its angles; a group then takes a few vectors, the next one's loads under
-// way.  16,384 rows of 4 heads of 128 to e4m3: 16 us, instructions as for the cache writes (0.7 of the
-// issue slots); batches that leave two to twelve blocks an SM take as long, 24 took 20.  64 rows of 8
-// heads: 8.8 us, the call on the host.
+// way.  16,384 rows of 4 heads of 128 to e4m3: 16 us over one cache after another (14 over the same one, which
+// the L2 holds; 10 to bf16), instructions as for the cache writes (0.7 of the issue slots); batches that
+// leave two to twelve blocks an SM take as long, 24 took 20.  64 rows of 8 heads: 9 us, the call on the
+// host.
 template <typename T, typename C>
 __global__ void __launch_bounds__(kThreads, 4)
 append_kernel(const __grid_constant__ RopeParams rp, const __grid_constant__ AppendCall c,
